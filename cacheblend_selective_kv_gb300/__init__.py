@@ -6,7 +6,8 @@ no fallback: if ``libcacheblend.so`` is missing or cannot be loaded, every call 
 
 Entry points (same names as the C ABI): ``cb_model_create``, ``cb_model_destroy``,
 ``cb_rerope``, ``cb_blend``, ``cb_blend_gradual``, ``cb_selected_count``, ``cb_last_error``;
-``BlendModel`` bundles a handle with the device tensors it borrows.
+``BlendModel`` bundles a handle with the device tensors it borrows, ``KV8Cache`` an 8-bit paged K/V cache
+with the operators on it (write, read, attention, evict).
 """
 from __future__ import annotations
 
@@ -28,7 +29,8 @@ EXPORTED = ("cb_model_create", "cb_model_destroy", "cb_rerope", "cb_blend", "cb_
             "cb_blend_paged", "cb_kv_gather_pages", "cb_kv_scatter_pages", "cb_pages_create", "cb_pages_destroy",
             "cb_pages_alloc", "cb_pages_retain", "cb_pages_release", "cb_pages_plan_write", "cb_pages_count",
             "cb_pages_free", "cb_index_create", "cb_index_destroy", "cb_index_size", "cb_index_match",
-            "cb_select_hkvd", "cb_blend_hkvd", "cb_gradual_layout")
+            "cb_select_hkvd", "cb_blend_hkvd", "cb_gradual_layout", "cb_kv8_create", "cb_kv8_destroy", "cb_kv8_status",
+            "cb_kv8_write", "cb_kv8_read", "cb_kv8_attention", "cb_kv8_evict", "cb_blend_kv8")
 CB_STATIC_MAX_CHUNKS = 256
 CB_STATUS_BAD_TOKEN, CB_STATUS_WAIT_TIMEOUT, CB_STATUS_BAD_ROW = 1, 2, 4
 
@@ -69,6 +71,17 @@ class CbLayerIO(ctypes.Structure):
 class CbPagedKV(ctypes.Structure):
     _fields_ = [("pool", ctypes.c_void_p), ("n_pages", ctypes.c_int64), ("page_size", ctypes.c_int32),
                 ("src_table", ctypes.c_void_p), ("dst_table", ctypes.c_void_p)]
+
+
+class CbKV8Config(ctypes.Structure):
+    _fields_ = [("n_layers", ctypes.c_int32), ("n_heads", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("dtype", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("n_pages", ctypes.c_int64), ("weight_cells", ctypes.c_int64)]
+
+
+class CbKV8Seqs(ctypes.Structure):
+    _fields_ = [("n_seqs", ctypes.c_int32), ("table", ctypes.c_void_p), ("table_ld", ctypes.c_int32),
+                ("lens", ctypes.c_void_p), ("max_len", ctypes.c_int32)]
 
 
 class CbKernelProfile(ctypes.Structure):
@@ -161,6 +174,23 @@ def lib() -> ctypes.CDLL:
         L.cb_blend_hkvd.restype = ctypes.c_int
         L.cb_blend_hkvd.argtypes = [vp, vp, i32, vp, ctypes.POINTER(CbChunk), i32, vp, i32, vp, vp,
                                     ctypes.POINTER(CbStats), vp]
+        sq = ctypes.POINTER(CbKV8Seqs)
+        L.cb_kv8_create.restype = ctypes.c_int
+        L.cb_kv8_create.argtypes = [ctypes.POINTER(CbKV8Config), vp, vp, ctypes.POINTER(vp)]
+        L.cb_kv8_destroy.restype = ctypes.c_int
+        L.cb_kv8_destroy.argtypes = [vp]
+        L.cb_kv8_status.restype = ctypes.c_int
+        L.cb_kv8_status.argtypes = [vp, ctypes.POINTER(ctypes.c_uint32), i32]
+        for f in (L.cb_kv8_write, L.cb_kv8_read):
+            f.restype = ctypes.c_int
+            f.argtypes = [vp, sq, i32, i32, vp, vp, i64, i64, vp, i32, vp]
+        L.cb_kv8_attention.restype = ctypes.c_int
+        L.cb_kv8_attention.argtypes = [vp, sq, i32, vp, i64, vp, i32, ctypes.c_float, vp, i64, vp, i32, i32, vp]
+        L.cb_kv8_evict.restype = ctypes.c_int
+        L.cb_kv8_evict.argtypes = [vp, sq, vp, i32, i32, i32, vp, i32, i32, i32, i32, vp, vp, vp, vp]
+        L.cb_blend_kv8.restype = ctypes.c_int
+        L.cb_blend_kv8.argtypes = [vp, vp, i32, vp, vp, vp, ctypes.POINTER(CbChunk), i32, ctypes.POINTER(ctypes.c_double),
+                                   i32, vp, vp, vp, vp, ctypes.POINTER(CbStats), vp]
         L.cb_profile_enable.restype = ctypes.c_int
         L.cb_profile_enable.argtypes = [vp, i32, i32]
         L.cb_profile_read.restype = i32
@@ -388,6 +418,201 @@ class Pages:
         if self.h:
             lib().cb_pages_destroy(self.h)
             self.h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def cb_blend_kv8(handle: int, tokens, n_tokens: int, cache: "KV8Cache", src_table, dst_table, chunks, ratios, work_kv,
+                 out_logits, out_selected=None, out_dev=None, stream=None, stats: bool = False):
+    """Blend over an 8-bit paged pool: chunk caches read through src_table, blended K/V written through dst_table
+    (device int32 tables); work_kv is the caller's contiguous working copy."""
+    st = CbStats()
+    r = (ctypes.c_double * max(1, len(ratios)))(*[float(x) for x in ratios])
+    _check(lib().cb_blend_kv8(handle, _ptr(tokens), int(n_tokens), cache.handle, _ptr(src_table), _ptr(dst_table),
+                              _chunks(chunks), len(chunks), r, len(ratios), _ptr(work_kv), _ptr(out_logits),
+                              _ptr(out_selected), _ptr(out_dev), ctypes.byref(st) if stats else None, _stream(stream)))
+    if stats:
+        return {f: getattr(st, f) for f, _ in CbStats._fields_}
+    return None
+
+
+class KV8Cache:
+    """An 8-bit paged K/V cache (cb_kv8_*): the caller's pool and the operators on it.
+
+    codes: device uint8 (or float8_e4m3fn) [n_layers][2][n_pages][n_kv_heads][page_size][head_dim]; scales: device
+    float32 [n_layers][2][n_pages][n_kv_heads].  ``KV8Cache.empty`` allocates both.  dtype ('bf16' | 'f32') is that of
+    the K/V rows, queries and outputs.  weight_cells: scratch of attention calls that return weights (``cells``).
+
+    Every call takes the batch as ``table`` (device int32 [n_seqs][pages]) and ``lens`` (device int32 [n_seqs], or None:
+    max_len each); ``max_len`` bounds the lengths (default: all the table can hold).  Calls are asynchronous on `stream`
+    (default: the current one) and allocate nothing, so they can be captured into a graph.  A tensor of another shape,
+    type or device raises ValueError before anything is enqueued."""
+
+    def __init__(self, codes, scales, n_heads: int, dtype: str = "bf16", weight_cells: int = 0):
+        import torch
+        self.handle = None
+        if codes.dim() != 6 or codes.shape[1] != 2 or codes.element_size() != 1 or not codes.is_contiguous() or not codes.is_cuda:
+            raise ValueError("codes must be a contiguous device tensor of bytes [n_layers][2][n_pages][n_kv_heads][page_size][head_dim]")
+        if scales.dtype != torch.float32 or scales.shape != codes.shape[:4] or not scales.is_contiguous() or scales.device != codes.device:
+            raise ValueError("scales must be contiguous float32 [n_layers][2][n_pages][n_kv_heads] on the codes' device")
+        if dtype not in ("bf16", "f32"):
+            raise ValueError("dtype must be 'bf16' or 'f32'")
+        self.codes, self.scales = codes, scales               # borrowed by the handle
+        self.n_layers, _, self.n_pages, self.n_kv_heads, self.page_size, self.head_dim = codes.shape
+        self.n_heads, self.device = int(n_heads), codes.device
+        self.dtype = torch.bfloat16 if dtype == "bf16" else torch.float32
+        self._i32, self._f32 = torch.int32, torch.float32
+        self._lib = lib()
+        cfg = CbKV8Config(self.n_layers, self.n_heads, self.n_kv_heads, self.head_dim, CB_BF16 if dtype == "bf16" else CB_F32,
+                          self.page_size, self.n_pages, int(weight_cells))
+        h = ctypes.c_void_p()
+        with torch.cuda.device(self.device):
+            _check(self._lib.cb_kv8_create(ctypes.byref(cfg), codes.data_ptr(), scales.data_ptr(), ctypes.byref(h)))
+        self.handle = h.value
+
+    @classmethod
+    def empty(cls, n_layers: int, n_pages: int, n_kv_heads: int, page_size: int, head_dim: int, n_heads: int,
+              dtype: str = "bf16", weight_cells: int = 0, device="cuda"):
+        """A cache over a new pool (all blocks zero)."""
+        import torch
+        codes = torch.zeros((n_layers, 2, n_pages, n_kv_heads, page_size, head_dim), dtype=torch.uint8, device=device)
+        scales = torch.zeros((n_layers, 2, n_pages, n_kv_heads), dtype=torch.float32, device=device)
+        return cls(codes, scales, n_heads, dtype, weight_cells)
+
+    @staticmethod
+    def cells(n_q: int, n_heads: int, max_len: int) -> int:
+        """weight_cells that an attention call of n_q query rows over at most max_len keys needs to return weights."""
+        return n_q * n_heads * (-(-max_len // 128) * 128 + 1)
+
+    def _int(self, t, name, *shape):
+        if t.dtype != self._i32 or t.device != self.device or not t.is_contiguous() or t.dim() != len(shape) or \
+                any(w is not None and w != n for n, w in zip(t.shape, shape)):
+            raise ValueError(f"{name} must be a contiguous int32 tensor {list(shape)} on {self.device}")
+        return t.data_ptr()
+
+    def _seqs(self, table, lens, max_len):
+        tp = self._int(table, "table", None, None)
+        n, ld = table.shape
+        lp = None if lens is None else self._int(lens, "lens", n)
+        return CbKV8Seqs(n, tp, ld, lp, ld * self.page_size if max_len is None else int(max_len))
+
+    def _call(self, f, *args, stream=None):
+        """The library call with the cache's device current."""
+        import torch
+        if torch.cuda.current_device() == self.device.index:
+            _check(f(self.handle, *args, _stream(stream)))
+        else:
+            with torch.cuda.device(self.device):
+                _check(f(self.handle, *args, _stream(stream)))
+
+    def _rows(self, t, name, n_layers, n_rows=None):
+        """(pointer, layer stride, row stride) of K/V rows [n_layers][n_rows][n_kv_heads][head_dim] (or without the
+        layers when there is one)."""
+        if t.dim() == 3 and n_layers == 1:
+            t = t.unsqueeze(0)
+        if t.dtype != self.dtype or t.device != self.device or t.dim() != 4 or t.shape[0] != n_layers or \
+                t.shape[2:] != (self.n_kv_heads, self.head_dim) or (n_rows is not None and t.shape[1] != n_rows):
+            raise ValueError(f"{name} must be {self.dtype} [{n_layers}][rows][{self.n_kv_heads}][{self.head_dim}] on {self.device}")
+        sl, sr, sh, sd = t.stride()
+        if sd != 1 or (sh != self.head_dim and self.n_kv_heads > 1):
+            raise ValueError(f"{name}: the heads of a row must be contiguous")
+        rows = t.shape[1]
+        w = self.n_kv_heads * self.head_dim
+        return t.data_ptr(), sl if n_layers > 1 else 0, sr if rows > 1 else w, rows
+
+    def _io(self, f, table, lens, k, v, layer, n_layers, row_start, max_len, stream):
+        kp, kl, kr, rows = self._rows(k, "k", n_layers)
+        vp, vl, vr, _ = self._rows(v, "v", n_layers, rows)
+        if kl != vl or kr != vr:
+            raise ValueError("k and v must have the same strides")
+        sq = self._seqs(table, lens, max_len)
+        rs = None if row_start is None else self._int(row_start, "row_start", sq.n_seqs + 1)
+        self._call(f, sq, layer, n_layers, kp, vp, kl, kr, rs, rows, stream=stream)
+
+    def write(self, table, lens, k, v, layer: int = 0, n_layers: int = 1, row_start=None, max_len=None, stream=None):
+        """k and v ([n_layers][n_rows][n_kv_heads][head_dim]) become the last rows of their sequences (lens counts them
+        already), quantised into their blocks.  row_start (device int32 [n_seqs + 1]) gives each sequence its rows; None
+        shares them evenly."""
+        self._io(self._lib.cb_kv8_write, table, lens, k, v, layer, n_layers, row_start, max_len, stream)
+
+    def read(self, table, lens, k, v, layer: int = 0, n_layers: int = 1, row_start=None, max_len=None, stream=None):
+        """The last rows of each sequence as values, into k and v (as for write)."""
+        self._io(self._lib.cb_kv8_read, table, lens, k, v, layer, n_layers, row_start, max_len, stream)
+
+    def attention(self, table, lens, q, out=None, layer: int = 0, q_start=None, scale=None, weights=None, add: bool = False,
+                  max_len=None, stream=None):
+        """softmax(q k * scale) v of the query rows q [n_q][n_heads][head_dim], each sequence's last rows, over its cache
+        (causal); returns out.  weights (device float32 [n_seqs][n_kv_heads][ld >= max_len]) receives, or with add
+        accumulates, the weight of every key.  q_start as row_start of write; scale defaults to head_dim ** -0.5."""
+        if out is None:
+            import torch
+            out = torch.empty(q.shape, dtype=self.dtype, device=self.device)
+            if q_start is not None:
+                out.zero_()                                   # rows that belong to no sequence
+        row = (self.n_heads, self.head_dim)
+        strides = []
+        for t, name in ((q, "q"), (out, "out")):
+            if t.dtype != self.dtype or t.device != self.device or t.dim() != 3 or t.shape[1:] != row or t.shape[0] != q.shape[0]:
+                raise ValueError(f"{name} must be {self.dtype} [n_q][{self.n_heads}][{self.head_dim}] on {self.device}")
+            sr, sh, sd = t.stride()
+            if sd != 1 or (sh != self.head_dim and self.n_heads > 1):
+                raise ValueError(f"{name}: the heads of a row must be contiguous")
+            strides.append(sr if t.shape[0] > 1 else self.n_heads * self.head_dim)
+        sq = self._seqs(table, lens, max_len)
+        qs = None if q_start is None else self._int(q_start, "q_start", sq.n_seqs + 1)
+        wp, ld = None, 0
+        if weights is not None:
+            if weights.dtype != self._f32 or weights.device != self.device or not weights.is_contiguous() or \
+                    weights.dim() != 3 or weights.shape[:2] != (sq.n_seqs, self.n_kv_heads):
+                raise ValueError(f"weights must be contiguous float32 [{sq.n_seqs}][{self.n_kv_heads}][keys] on {self.device}")
+            wp, ld = weights.data_ptr(), weights.shape[2]
+        self._call(self._lib.cb_kv8_attention, sq, layer, q.data_ptr(), strides[0], qs, q.shape[0],
+                   self.head_dim ** -0.5 if scale is None else scale, out.data_ptr(), strides[1], wp, ld, 1 if add else 0,
+                   stream=stream)
+        return out
+
+    def evict(self, table, lens, dst_table, weights, n_keep: int, n_sink: int = 0, n_recent: int = 0, out_rows=None,
+              out_lens=None, out_weights=None, layer: int = 0, n_layers: int = 1, max_len=None, stream=None):
+        """Every KV head keeps n_keep rows of each sequence: the first n_sink, the last n_recent and of the others those of
+        largest weight (weights: device float32 [n_layers][n_seqs][n_kv_heads][ld]).  The kept rows move to dst_table
+        (table itself: in place; else pages that table does not name).  Returns dict(rows, lens, weights); out_weights
+        defaults to weights itself, out_lens may be lens."""
+        import torch
+        sq = self._seqs(table, lens, max_len)
+        n = sq.n_seqs
+        dp = self._int(dst_table, "dst_table", n, None)
+        if out_weights is None:
+            out_weights = weights
+        if out_lens is None:
+            out_lens = torch.empty(n, dtype=torch.int32, device=self.device)
+        if out_rows is None:
+            out_rows = torch.empty((n_layers, n, self.n_kv_heads, max(int(n_keep), 0)), dtype=torch.int32, device=self.device)
+        for t, name in ((weights, "weights"), (out_weights, "out_weights")):
+            if t.dtype != self._f32 or t.device != self.device or not t.is_contiguous() or t.dim() != 4 or \
+                    t.shape[:3] != (n_layers, n, self.n_kv_heads) or t.shape[3] != weights.shape[3]:
+                raise ValueError(f"{name} must be contiguous float32 [{n_layers}][{n}][{self.n_kv_heads}][rows] on {self.device}")
+        rp = self._int(out_rows, "out_rows", n_layers, n, self.n_kv_heads, int(n_keep))
+        lp = self._int(out_lens, "out_lens", n)
+        self._call(self._lib.cb_kv8_evict, sq, dp, dst_table.shape[1], layer, n_layers, weights.data_ptr(), weights.shape[3],
+                   n_keep, n_sink, n_recent, out_weights.data_ptr(), rp, lp, stream=stream)
+        return dict(rows=out_rows, lens=out_lens, weights=out_weights)
+
+    def status(self, clear: bool = False) -> int:
+        """Device status bits (CB_STATUS_*) recorded by the kernels; synchronises."""
+        import torch
+        v = ctypes.c_uint32()
+        with torch.cuda.device(self.device):
+            _check(self._lib.cb_kv8_status(self.handle, ctypes.byref(v), 1 if clear else 0))
+        return v.value
+
+    def close(self):
+        if self.handle:
+            self._lib.cb_kv8_destroy(self.handle)
+            self.handle = None
 
     def __del__(self):
         try:

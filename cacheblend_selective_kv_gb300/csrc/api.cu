@@ -12,6 +12,7 @@
 #include <new>
 
 #include "cb_common.cuh"
+#include "cb_kv8.cuh"
 
 using namespace cb;
 
@@ -852,6 +853,57 @@ cb_status cb_blend_paged(cb_model* mp, const int32_t* tokens, int32_t n_tokens, 
     ks[0] = ks[1];
     return blend_impl(m, tokens, n_tokens, nullptr, t, n_chunks, n_ctx, ks, work_kv, out_logits, out_selected, out_dev,
                       stats, (cudaStream_t)stream, nullptr, pg, shift);
+}
+
+cb_status cb_blend_kv8(cb_model* mp, const int32_t* tokens, int32_t n_tokens, cb_kv8* cache, const int32_t* src_table,
+                       const int32_t* dst_table, const cb_chunk* chunks, int32_t n_chunks, const double* ratios,
+                       int32_t n_ratios, void* work_kv, float* out_logits, int32_t* out_selected, float* out_dev,
+                       cb_stats* stats, void* stream) {
+    g_err[0] = 0;
+    if (!mp || !cache) return fail(CB_ERR_INVALID_ARG, "cb_blend_kv8: null model or cache");
+    Model& m = *mp;
+    const cb_config& c = m.cfg;
+    const int L = c.n_layers;
+    if (cache->cfg.n_layers != L || cache->cfg.n_kv_heads != c.n_kv_heads || cache->cfg.head_dim != c.head_dim ||
+        cache->cfg.dtype != c.dtype || cache->device != m.device)
+        return fail(CB_ERR_INVALID_ARG, "cb_blend_kv8: the cache's layers, KV heads, head_dim, dtype or device are not the model's");
+    if (!dst_table || (n_chunks > 0 && !src_table)) return fail(CB_ERR_INVALID_ARG, "cb_blend_kv8: missing block table");
+    if ((uintptr_t)work_kv % 16) return fail(CB_ERR_INVALID_ARG, "cb_blend_kv8: work_kv not 16-byte aligned");
+    if (!ratios || n_ratios != L - 1)
+        return fail(CB_ERR_INVALID_ARG, "cb_blend_kv8: need n_layers - 1 = %d ratios (got %d)", L - 1, n_ratios);
+    for (int i = 0; i < n_ratios; ++i)
+        if (!(ratios[i] >= 0.0 && ratios[i] <= 1.0)) return fail(CB_ERR_INVALID_ARG, "ratio of layer %d outside [0, 1]", i + 1);
+    ChunkTable t;
+    int n_ctx = 0;
+    cb_status st = check_blend(m, tokens, n_tokens, work_kv, chunks, n_chunks, work_kv, out_logits, t, n_ctx);
+    if (st != CB_OK) return st;
+    std::vector<int> ks(L, 0);
+    for (int l = 1; l < L; ++l) {
+        ks[l] = cb_selected_count(n_ctx, ratios[l - 1]);
+        if (l >= 2 && ks[l] > ks[l - 1])
+            return fail(CB_ERR_INVALID_ARG, "layer %d keeps %d rows, more than layer %d's %d: the sets must be nested",
+                        l, ks[l], l - 1, ks[l - 1]);
+    }
+    ks[0] = ks[1];
+    // the context rows out of the pool, into rows 0 .. n_ctx - 1 of every (layer, K|V) block of the working copy
+    const int P = cache->cfg.page_size;
+    const int64_t nkv = (int64_t)c.n_kv_heads * c.head_dim, block = (int64_t)n_tokens * nkv;
+    char* v0 = (char*)work_kv + block * (int64_t)act_size(m);
+    if (n_ctx > 0) {
+        const cb_kv8_seqs src = {1, src_table, (n_ctx + P - 1) / P, nullptr, n_ctx};
+        st = cb_kv8_read(cache, &src, 0, L, work_kv, v0, 2 * block, nkv, nullptr, n_ctx, stream);
+        if (st != CB_OK) return st;
+    }
+    st = blend_impl(m, tokens, n_tokens, work_kv, t, n_chunks, n_ctx, ks, work_kv, out_logits, out_selected, out_dev, stats,
+                    (cudaStream_t)stream);
+    if (st != CB_OK) return st;
+    const cb_kv8_seqs dst = {1, dst_table, (n_tokens + P - 1) / P, nullptr, n_tokens};
+    st = cb_kv8_write(cache, &dst, 0, L, work_kv, v0, 2 * block, nkv, nullptr, n_tokens, stream);
+    if (st == CB_OK && stats) {
+        stats->kernel_launches += n_ctx > 0 ? 2 : 1;
+        stats->kv_bytes_moved += 2.0 * L * ((double)n_ctx + n_tokens) * (double)nkv * (1.0 + (double)act_size(m));
+    }
+    return st;
 }
 
 cb_status cb_kv_gather_pages(cb_model* mp, const cb_paged_kv* pg, int32_t n_rows, void* out_kv, void* stream) {

@@ -1,0 +1,147 @@
+// 8-bit paged K/V cache: the parts its kernels share (block addressing, scales, e4m3 conversions).
+//
+// Pool: codes [L][2][n_pages][Hkv][P][hd] e4m3 bytes, scales [L][2][n_pages][Hkv] float.  A block (one page's rows
+// of one KV head in one layer's K or V) is P * hd consecutive bytes, so a tile of an attention head is a few
+// contiguous pieces whatever the number of heads.  A scale is a power of two (or 0 for a block of zeros): dividing
+// by it and multiplying by it are exact in fp32, so the only rounding a value meets is the one to e4m3, and a
+// code's value is exact in bf16.
+#pragma once
+#include <cuda_fp8.h>
+
+#include "cb_common.cuh"
+
+namespace cb {
+
+// the cache handle (cb_kv8): the caller's buffers and the scratch of its calls
+struct Kv8 {
+    cb_kv8_config cfg;
+    int device;
+    int num_sms;
+    int shift;               // log2(page_size)
+    uint8_t* codes;
+    float* scales;
+    unsigned* status;        // ST_* bits
+    float* scores;           // weight_cells floats: attention calls that return weights
+};
+
+// A batch of sequences as the kernels see it.
+struct Kv8Seqs {
+    int n;
+    const int* table;        // [n][table_ld] page ids
+    int table_ld;
+    const int* lens;         // [n] rows in the cache, or NULL: max_len each
+    int max_len;
+    int64_t n_pages;
+    int shift;
+    unsigned* status;
+};
+
+// Rows that belong to the batch: sequence s owns rows start(s) .. start(s+1)-1 of an array of n_rows, and they are
+// its last rows in the cache.
+struct Kv8Rows {
+    const int* start;        // [n + 1], or NULL: `each` rows per sequence
+    int each;
+    int n_rows;
+};
+
+__device__ __forceinline__ int kv8_len(const Kv8Seqs& q, int s) { return q.lens ? q.lens[s] : q.max_len; }
+
+// rows [r0, r1) of sequence s; false (and a status bit) when the offsets or the length are out of range
+__device__ __forceinline__ bool kv8_rows(const Kv8Seqs& q, const Kv8Rows& r, int s, int& r0, int& r1, int& len) {
+    r0 = r.start ? r.start[s] : s * r.each;
+    r1 = r.start ? r.start[s + 1] : r0 + r.each;
+    len = kv8_len(q, s);
+    if (r0 < 0 || r1 < r0 || r1 > r.n_rows || len < 0 || len > q.max_len) {
+        atomicOr(q.status, ST_BAD_ROW);
+        return false;
+    }
+    return true;
+}
+
+// page of block `blk` of sequence s, or -1 (and a status bit) for an id outside the pool
+__device__ __forceinline__ int kv8_page(const Kv8Seqs& q, int s, int blk) {
+    const int p = q.table[(int64_t)s * q.table_ld + blk];
+    if (p < 0 || p >= q.n_pages) {
+        atomicOr(q.status, ST_BAD_ROW);
+        return -1;
+    }
+    return p;
+}
+
+// The smallest power of two sc with top <= 448 sc (0 for 0): 448 = 1.75 * 2^8.  Never below 2^-126, so that the
+// scale and its reciprocal are normal numbers.
+__device__ __forceinline__ float kv8_scale(float top) {
+    if (!(top > 0.f)) return 0.f;
+    const unsigned b = __float_as_uint(top);
+    int e = (int)(b >> 23) - 8 + ((b & 0x7fffffu) > 0x600000u ? 1 : 0);
+    if (e < 1) e = 1;
+    return __uint_as_float((unsigned)e << 23);
+}
+// 1 / sc of a scale above (exact), 0 for 0
+__device__ __forceinline__ float kv8_inverse(float sc) {
+    return sc > 0.f ? __uint_as_float((254u << 23) - __float_as_uint(sc)) : 0.f;
+}
+// |x| for the block's largest value: infinities and NaN do not count
+__device__ __forceinline__ float kv8_mag(float x) {
+    const float a = fabsf(x);
+    return a <= 3.402823466e38f ? a : 0.f;
+}
+// an infinity has no e4m3 code and is kept as NaN rather than as a large finite value
+__device__ __forceinline__ float kv8_nan_inf(float x) { return fabsf(x) <= 3.402823466e38f ? x : __int_as_float(0x7fc00000); }
+
+__device__ __forceinline__ uint32_t kv8_code2(float a, float b) {           // codes of a (low byte) and b
+    return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+}
+__device__ __forceinline__ float2 kv8_value2(uint32_t c2) {
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(c2 & 0xffffu), __NV_E4M3);
+    return __half22float2(__half2(h));
+}
+// four codes whose values are multiplied by the power of two f and rounded to e4m3 again
+__device__ __forceinline__ uint32_t kv8_rescale4(uint32_t c4, float f) {
+    const float2 a = kv8_value2(c4), b = kv8_value2(c4 >> 16);
+    return kv8_code2(a.x * f, a.y * f) | (kv8_code2(b.x * f, b.y * f) << 16);
+}
+
+// ------------------------------------------------------------------------------------------------
+// launchers
+// ------------------------------------------------------------------------------------------------
+struct Kv8Io {                // contiguous K/V rows beside the cache
+    void* k;
+    void* v;
+    int64_t layer_stride;     // elements between layers
+    int64_t row_stride;       // elements between rows ([Hkv][hd] inside a row is contiguous)
+    bool bf16;
+};
+cudaError_t launch_kv8_write(const Kv8& c, const Kv8Seqs& q, const Kv8Rows& r, const Kv8Io& io, int layer, int n_layers,
+                             cudaStream_t s);
+cudaError_t launch_kv8_read(const Kv8& c, const Kv8Seqs& q, const Kv8Rows& r, const Kv8Io& io, int layer, int n_layers,
+                            cudaStream_t s);
+
+struct Kv8Attn {
+    const void* q;            // [n_q][Hq][hd]
+    int64_t q_stride;         // elements between rows
+    void* out;
+    int64_t out_stride;
+    float scale;
+    float* weights;           // [n_seqs][Hkv][weights_ld] or NULL
+    int weights_ld;
+    bool add;                 // add to the weights instead of writing them
+};
+cudaError_t launch_kv8_attention(const Kv8& c, const Kv8Seqs& q, const Kv8Rows& r, const Kv8Attn& a, int layer,
+                                 cudaStream_t s);
+
+struct Kv8Evict {
+    const int* dst_table;
+    int dst_ld;
+    const float* weights;     // [n_layers][n_seqs][Hkv][weights_ld]
+    float* out_weights;
+    int weights_ld;
+    int keep, sink, recent;
+    int* out_rows;            // [n_layers][n_seqs][Hkv][keep]
+    int* out_lens;            // [n_seqs]
+};
+cudaError_t launch_kv8_evict(const Kv8& c, const Kv8Seqs& q, const Kv8Evict& e, int layer, int n_layers, cudaStream_t s);
+
+}  // namespace cb
+
+struct cb_kv8 : public cb::Kv8 {};

@@ -1,0 +1,293 @@
+// 8-bit paged K/V cache: writing rows into it and reading them back.
+//
+// write: a block's scale is the smallest power of two s with max|x| <= 448 s, a row's code e4m3(x / s).  A block that
+// already holds earlier rows of the sequence keeps max(old scale, new rows' scale); its old codes are rounded to
+// the larger one when it grew.
+// read: code * s, exact in bf16 and fp32.
+//
+// Both are bound by HBM: 2 or 4 bytes a value on one side, 1 on the other.  Work is split by block: TPB threads
+// (32..256) hold one block's rows in registers as NP 16-byte vectors each, find the block's largest value with one
+// reduction and store the codes, so every row is read once and a code block is written as one contiguous piece.
+#include "cb_kv8.cuh"
+
+namespace cb {
+
+namespace {
+
+constexpr int THREADS = 256;
+
+// Which block a slot stands for.  With `each` rows per sequence, they touch at most per_seq blocks of it and the
+// slots are s * per_seq ..; with ragged rows, n rows touch at most n / P + 2 blocks, so that start(s) / P + 2 s is a
+// base that leaves every sequence room for its blocks.
+struct Slots {
+    int per_seq;              // > 0: equal rows
+    int total;
+};
+Slots kv8_slots(const Kv8Seqs& q, const Kv8Rows& r) {
+    const int P = 1 << q.shift;
+    if (!r.start) {
+        const int per = r.each > 0 ? (int)(((int64_t)r.each + P - 2) / P) + 1 : 0;
+        return {per, per * q.n};
+    }
+    return {0, (r.n_rows >> q.shift) + 2 * q.n};
+}
+
+struct Block {
+    int src_row;              // source row of logical row `first` of the sequence's new rows
+    int lo, hi;               // rows of the block that belong to the call
+    int page;
+};
+
+// the block of slot u; false when the slot has none
+__device__ __forceinline__ bool kv8_block(const Kv8Seqs& q, const Kv8Rows& r, int per_seq, int u, Block& b) {
+    int s, local;
+    if (per_seq > 0) {
+        s = u / per_seq;
+        local = u - s * per_seq;
+    } else {
+        int a = 0, z = q.n - 1;                        // the last sequence whose base is at most u
+        while (a < z) {
+            const int m = (a + z + 1) >> 1;
+            if ((r.start[m] >> q.shift) + 2 * m <= u) a = m; else z = m - 1;
+        }
+        s = a;
+        local = u - ((r.start[s] >> q.shift) + 2 * s);
+    }
+    if (s >= q.n || local < 0) return false;
+    int r0, r1, len;
+    if (!kv8_rows(q, r, s, r0, r1, len)) return false;
+    const int n = r1 - r0;
+    if (n == 0) return false;
+    if (n > len) {
+        atomicOr(q.status, ST_BAD_ROW);
+        return false;
+    }
+    const int P = 1 << q.shift, first = len - n;
+    const int blk = (first >> q.shift) + local;
+    if (blk > (len - 1) >> q.shift) return false;
+    b.lo = max(first - blk * P, 0);
+    b.hi = min(len - blk * P, P);
+    b.src_row = r0 + blk * P + b.lo - first;           // source row of block row lo
+    b.page = kv8_page(q, s, blk);
+    return b.page >= 0;
+}
+
+// maximum over the TPB threads of a group (TPB a power of two from 32 to 256)
+__device__ __forceinline__ float group_max(float v, int tpb, float* sm) {
+    v = warp_max(v);
+    if (tpb == 32) return v;
+    const int warp = threadIdx.x >> 5, per = tpb >> 5, g0 = warp / per * per;
+    if ((threadIdx.x & 31) == 0) sm[warp] = v;
+    __syncthreads();
+    v = sm[g0];
+    for (int i = 1; i < per; ++i) v = fmaxf(v, sm[g0 + i]);
+    return v;
+}
+
+template <typename T> struct Vec;                      // 16 bytes of a row
+template <> struct Vec<bf16> {
+    static constexpr int N = 8;
+    __device__ static void get(const uint4& u, float* f) {
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f[2 * i] = __uint_as_float(w[i] << 16);
+            f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
+    }
+};
+template <> struct Vec<float> {
+    static constexpr int N = 4;
+    __device__ static void get(const uint4& u, float* f) {
+        f[0] = __uint_as_float(u.x);
+        f[1] = __uint_as_float(u.y);
+        f[2] = __uint_as_float(u.z);
+        f[3] = __uint_as_float(u.w);
+    }
+};
+
+struct CacheArgs {
+    Kv8Seqs q;
+    Kv8Rows r;
+    const void* src[2];
+    int64_t layer_stride, row_stride;
+    uint8_t* codes;
+    float* scales;
+    int per_seq, units;       // units = slots * Hkv
+    int Hkv, hd, layer;
+    int tpb;                  // threads of a block's group
+};
+
+template <typename T, int NP>
+__global__ void __launch_bounds__(THREADS) kv8_write_kernel(const CacheArgs a) {
+    constexpr int VN = Vec<T>::N;
+    __shared__ float sm[2][THREADS / 32];
+    const int groups = THREADS / a.tpb, group = threadIdx.x / a.tpb, t = threadIdx.x - group * a.tpb;
+    const int unit = blockIdx.x * groups + group;
+    const int lk = blockIdx.y, kv = lk & 1, l = lk >> 1;
+    const int P = 1 << a.q.shift, vpr = a.hd / VN;     // vectors per row
+    Block b{};
+    const int slot = unit / a.Hkv, head = unit - slot * a.Hkv;
+    const bool live = unit < a.units && kv8_block(a.q, a.r, a.per_seq, slot, b);
+    uint4 x[NP];
+    float top = 0.f;
+    const T* src = (const T*)a.src[kv] + l * a.layer_stride + (int64_t)head * a.hd;
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+        const int v = t + i * a.tpb, row = v / vpr, e = v - row * vpr;
+        x[i] = make_uint4(0, 0, 0, 0);
+        if (live && row >= b.lo && row < b.hi)
+            x[i] = *reinterpret_cast<const uint4*>(src + (int64_t)(b.src_row + row - b.lo) * a.row_stride + e * VN);
+    }
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+        float f[VN];
+        Vec<T>::get(x[i], f);
+#pragma unroll
+        for (int k = 0; k < VN; ++k) top = fmaxf(top, kv8_mag(f[k]));
+    }
+    top = group_max(top, a.tpb, sm[0]);
+    if (!live) return;                                 // no barrier below
+    const int64_t blk = ((int64_t)((a.layer + l) * 2 + kv) * a.q.n_pages + b.page) * a.Hkv + head;
+    uint8_t* dst = a.codes + blk * P * a.hd;
+    float sc = kv8_scale(top);
+    if (b.lo > 0) {                                    // earlier rows of the sequence stay in the block
+        const float was = a.scales[blk];
+        if (was >= sc) {
+            sc = was;
+        } else if (was > 0.f) {                        // (codes of a block of zeros stay as they are)
+            const float f = was * kv8_inverse(sc);
+            for (int i = t; i < b.lo * a.hd / 16; i += a.tpb) {
+                uint4 c = reinterpret_cast<uint4*>(dst)[i];
+                c.x = kv8_rescale4(c.x, f);
+                c.y = kv8_rescale4(c.y, f);
+                c.z = kv8_rescale4(c.z, f);
+                c.w = kv8_rescale4(c.w, f);
+                reinterpret_cast<uint4*>(dst)[i] = c;
+            }
+        }
+    }
+    const float inv = kv8_inverse(sc);
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+        const int v = t + i * a.tpb, row = v / vpr, e = v - row * vpr;
+        if (row < b.lo || row >= b.hi) continue;
+        float f[VN];
+        Vec<T>::get(x[i], f);
+        uint32_t w[VN / 4];
+#pragma unroll
+        for (int k = 0; k < VN / 4; ++k) {
+            const float* g = f + 4 * k;
+            w[k] = kv8_code2(kv8_nan_inf(g[0]) * inv, kv8_nan_inf(g[1]) * inv) |
+                   (kv8_code2(kv8_nan_inf(g[2]) * inv, kv8_nan_inf(g[3]) * inv) << 16);
+        }
+        uint8_t* d = dst + row * a.hd + e * VN;
+        if (VN == 8) *reinterpret_cast<uint2*>(d) = make_uint2(w[0], w[VN / 4 - 1]);
+        else *reinterpret_cast<uint32_t*>(d) = w[0];
+    }
+    // every thread of the group has read the old scale before one of them replaces it
+    if (a.tpb > 32) asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(a.tpb) : "memory");
+    else __syncwarp();
+    if (t == 0) a.scales[blk] = sc;
+}
+
+template <typename T> __device__ __forceinline__ uint4 pack_values(const float* f);
+template <> __device__ __forceinline__ uint4 pack_values<bf16>(const float* f) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 p = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t*>(&p);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+template <> __device__ __forceinline__ uint4 pack_values<float>(const float* f) {
+    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+}
+
+template <typename T>
+__global__ void __launch_bounds__(THREADS) kv8_read_kernel(const CacheArgs a) {
+    constexpr int VN = Vec<T>::N;
+    const int groups = THREADS / a.tpb, group = threadIdx.x / a.tpb, t = threadIdx.x - group * a.tpb;
+    const int unit = blockIdx.x * groups + group;
+    const int lk = blockIdx.y, kv = lk & 1, l = lk >> 1;
+    const int P = 1 << a.q.shift, vpr = a.hd / VN;
+    Block b{};
+    const int slot = unit / a.Hkv, head = unit - slot * a.Hkv;
+    if (unit >= a.units || !kv8_block(a.q, a.r, a.per_seq, slot, b)) return;
+    const int64_t blk = ((int64_t)((a.layer + l) * 2 + kv) * a.q.n_pages + b.page) * a.Hkv + head;
+    const uint8_t* src = a.codes + blk * P * a.hd;
+    const float sc = a.scales[blk];
+    T* dst = (T*)a.src[kv] + l * a.layer_stride + (int64_t)head * a.hd;
+    for (int v = b.lo * vpr + t; v < b.hi * vpr; v += a.tpb) {
+        const int row = v / vpr, e = v - row * vpr;
+        float f[VN];
+#pragma unroll
+        for (int k = 0; k < VN / 4; ++k) {
+            const uint32_t c = reinterpret_cast<const uint32_t*>(src)[v * (VN / 4) + k];
+            const float2 p = kv8_value2(c), z = kv8_value2(c >> 16);
+            f[4 * k] = p.x * sc;
+            f[4 * k + 1] = p.y * sc;
+            f[4 * k + 2] = z.x * sc;
+            f[4 * k + 3] = z.y * sc;
+        }
+        *reinterpret_cast<uint4*>(dst + (int64_t)(b.src_row + row - b.lo) * a.row_stride + e * VN) = pack_values<T>(f);
+    }
+}
+
+CacheArgs cache_args(const Kv8& c, const Kv8Seqs& q, const Kv8Rows& r, const Kv8Io& io, int layer, int es) {
+    CacheArgs a{};
+    const Slots sl = kv8_slots(q, r);
+    a.q = q;
+    a.r = r;
+    a.src[0] = io.k;
+    a.src[1] = io.v;
+    a.layer_stride = io.layer_stride;
+    a.row_stride = io.row_stride;
+    a.codes = c.codes;
+    a.scales = c.scales;
+    a.per_seq = sl.per_seq;
+    a.Hkv = c.cfg.n_kv_heads;
+    a.units = sl.total * a.Hkv;
+    a.hd = c.cfg.head_dim;
+    a.layer = layer;
+    // four 16-byte vectors per thread where the block is small enough for that
+    const int want = (1 << q.shift) * a.hd * es / 64;
+    a.tpb = want < 32 ? 32 : (want > THREADS ? THREADS : want);
+    return a;
+}
+
+template <typename T>
+cudaError_t write_typed(const CacheArgs& a, int n_layers, int np, cudaStream_t s) {
+    const dim3 grid((a.units + THREADS / a.tpb - 1) / (THREADS / a.tpb), 2 * n_layers);
+    switch (np) {
+        case 4: kv8_write_kernel<T, 4><<<grid, THREADS, 0, s>>>(a); break;
+        case 8: kv8_write_kernel<T, 8><<<grid, THREADS, 0, s>>>(a); break;
+        case 16: kv8_write_kernel<T, 16><<<grid, THREADS, 0, s>>>(a); break;
+        default: kv8_write_kernel<T, 32><<<grid, THREADS, 0, s>>>(a); break;
+    }
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_kv8_write(const Kv8& c, const Kv8Seqs& q, const Kv8Rows& r, const Kv8Io& io, int layer, int n_layers,
+                             cudaStream_t s) {
+    const int es = io.bf16 ? 2 : 4;
+    const CacheArgs a = cache_args(c, q, r, io, layer, es);
+    if (a.units == 0 || n_layers == 0) return cudaSuccess;
+    const int np = (1 << q.shift) * a.hd * es / 16 / a.tpb;
+    return io.bf16 ? write_typed<bf16>(a, n_layers, np, s) : write_typed<float>(a, n_layers, np, s);
+}
+
+cudaError_t launch_kv8_read(const Kv8& c, const Kv8Seqs& q, const Kv8Rows& r, const Kv8Io& io, int layer, int n_layers,
+                            cudaStream_t s) {
+    const CacheArgs a = cache_args(c, q, r, io, layer, io.bf16 ? 2 : 4);
+    if (a.units == 0 || n_layers == 0) return cudaSuccess;
+    const dim3 grid((a.units + THREADS / a.tpb - 1) / (THREADS / a.tpb), 2 * n_layers);
+    if (io.bf16) kv8_read_kernel<bf16><<<grid, THREADS, 0, s>>>(a);
+    else kv8_read_kernel<float><<<grid, THREADS, 0, s>>>(a);
+    return cudaGetLastError();
+}
+
+}  // namespace cb

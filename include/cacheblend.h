@@ -283,6 +283,113 @@ int32_t cb_pages_plan_write(cb_pages* pages, const int32_t* table, int32_t n, in
 int32_t cb_pages_count(const cb_pages* pages, int32_t id);
 int64_t cb_pages_free(const cb_pages* pages);
 
+/* 8-bit paged K/V cache (section "把账算细": the stored caches are what fills the memory).  A pool of pages like
+ * cb_paged_kv's that holds each value as one e4m3 byte and one scale per block (the rows of one page, of one KV
+ * head, in one layer's K or V): half the bytes of a bf16 pool for chunk caches and for every later pass over them.
+ *   codes   device [n_layers][2][n_pages][n_kv_heads][page_size][head_dim] e4m3 bytes (2 = K, V), 128-byte aligned
+ *   scales  device float32 [n_layers][2][n_pages][n_kv_heads]; a value is code * scale
+ * A scale is a power of two, or 0 for a block of zeros: the smallest s with max|x| <= 448 s over the block's finite
+ * values, not below 2^-126, and a code is x / s rounded to nearest even.  Values read back are exact in bf16 and
+ * fp32.  A NaN or an infinity is kept as NaN and does not count for the scale.
+ * Both buffers are the caller's.  A handle borrows them, knows their geometry and owns the scratch of its calls; it
+ * lives on the device that was current at creation, and its calls are made with that device current.  Calls on one
+ * handle must not overlap on the GPU (they share its scratch and its pages); two handles may share one pool as long
+ * as no page is written while another call reads it. */
+typedef struct cb_kv8 cb_kv8;
+typedef struct {
+    int32_t n_layers;
+    int32_t n_heads;         /* query heads (a multiple of n_kv_heads, at most 8 per KV head) */
+    int32_t n_kv_heads;
+    int32_t head_dim;        /* 64 or 128 */
+    int32_t dtype;           /* cb_dtype of the K/V rows, queries and outputs of the calls */
+    int32_t page_size;       /* rows per page: 16, 32, 64, 128 or 256 */
+    int64_t n_pages;         /* n_pages * page_size * n_kv_heads < 2^31 */
+    int64_t weight_cells;    /* floats of scratch for attention calls that return weights (0: none): such a call needs
+                                n_q * n_heads * (max_len rounded up to 128, plus 1) */
+} cb_kv8_config;
+
+/* A batch of sequences: row j of sequence s is row j % page_size of page table[s * table_ld + j / page_size].  All
+ * arrays are device int32 and are read when the call's kernels run, so a captured graph follows their contents.
+ * A page id outside the pool, a length outside [0, max_len] or row offsets out of range are recorded as
+ * CB_STATUS_BAD_ROW (read with cb_kv8_status) and their rows are skipped (attention: such keys are not seen). */
+typedef struct {
+    int32_t n_seqs;          /* <= 65535 */
+    const int32_t* table;    /* [n_seqs][table_ld] */
+    int32_t table_ld;        /* table_ld * page_size >= max_len */
+    const int32_t* lens;     /* [n_seqs] rows of each sequence in the cache, or NULL: max_len each */
+    int32_t max_len;         /* upper bound of the lengths; sizes the launches */
+} cb_kv8_seqs;
+
+/* Create and destroy a handle (create allocates the scratch, destroy synchronises the device; NULL is accepted).
+ * cb_kv8_status: as cb_model_status.  Errors: CB_ERR_INVALID_ARG, CB_ERR_UNSUPPORTED, CB_ERR_OOM, CB_ERR_CUDA. */
+cb_status cb_kv8_create(const cb_kv8_config* cfg, void* codes, float* scales, cb_kv8** out);
+cb_status cb_kv8_destroy(cb_kv8* cache);
+cb_status cb_kv8_status(cb_kv8* cache, uint32_t* bits, int32_t clear);
+
+/* Rows into the cache and back, for layers layer .. layer + n_layers - 1.
+ *   k, v         device [n_layers][n_rows][n_kv_heads][head_dim] in cfg.dtype, with layer_stride and row_stride
+ *                elements between layers and rows (16-byte aligned, strides multiples of 16 bytes): the K and V halves of
+ *                cb_blend's out_kv, or slices of a fused projection's rows.
+ *   row_start    device int32 [n_seqs + 1] or NULL: sequence s owns rows row_start[s] .. row_start[s + 1] - 1; NULL: the
+ *                n_rows rows are shared evenly, in order (n_rows a multiple of n_seqs).
+ * A sequence's n rows are its LAST n rows in the cache, lens already counting them.  Rows behind a sequence's last
+ * one, in the cache and in k and v, are left as they were.
+ *   write  quantises the rows into their blocks.  A block that also holds earlier rows of its sequence keeps the larger
+ *          of its old scale and the new rows' own, and its old codes are rounded to it if it grew.  The pages written
+ *          must belong to one sequence (cb_pages_plan_write gives a shared block a page of its own).
+ *   read   writes code * scale.
+ * Async on `stream`; no allocation. */
+cb_status cb_kv8_write(cb_kv8* cache, const cb_kv8_seqs* seqs, int32_t layer, int32_t n_layers, const void* k,
+                       const void* v, int64_t layer_stride, int64_t row_stride, const int32_t* row_start,
+                       int32_t n_rows, void* stream);
+cb_status cb_kv8_read(cb_kv8* cache, const cb_kv8_seqs* seqs, int32_t layer, int32_t n_layers, void* k, void* v,
+                      int64_t layer_stride, int64_t row_stride, const int32_t* row_start, int32_t n_rows, void* stream);
+
+/* Attention of new query rows over the cache of one layer (decoding steps, speculated tokens, a query's rows over a
+ * blended context).  The n query rows of a sequence belong to its last n cache rows: row i sees keys
+ * 0 .. len - n + i and gives softmax(q k * scale) v over them, query head h reading KV head h / (n_heads /
+ * n_kv_heads); a row that sees nothing gives 0.  Query and output rows: q_start shares n_q rows among the sequences
+ * as row_start does above; rows that belong to no sequence are neither read nor written.
+ *   q, out       device [n_q][n_heads][head_dim] in cfg.dtype, q_stride and out_stride elements between rows
+ *                (16-byte aligned, strides multiples of 16 bytes); they must not overlap
+ *   scale        usually 1 / sqrt(head_dim)
+ *   weights      device float32 [n_seqs][n_kv_heads][weights_ld >= max_len] or NULL: the weight every key received, the
+ *                sum of its softmax weights over the call's rows of its sequence and the heads of its group, at entries
+ *                0 .. len - 1 (others are left as they were); add != 0 adds to what stands there.  What cb_kv8_evict
+ *                ranks by: written once for a query window, or added up over decoding steps.
+ * NaN behind what a row sees (in a later row's K or V, or behind the sequence) does not reach it.
+ * Every sum runs in a fixed order: the same call gives the same bits.  Async on `stream`; no allocation. */
+cb_status cb_kv8_attention(cb_kv8* cache, const cb_kv8_seqs* seqs, int32_t layer, const void* q, int64_t q_stride,
+                           const int32_t* q_start, int32_t n_q, float scale, void* out, int64_t out_stride,
+                           float* weights, int32_t weights_ld, int32_t add, void* stream);
+
+/* Eviction by accumulated weight: each KV head of each layer layer .. layer + n_layers - 1 keeps its first n_sink rows,
+ * its last n_recent rows and, of the rows between, those of largest weight (ties to the lower row; a weight that is
+ * not positive, or NaN, ranks as 0): n_keep rows, or all of a sequence with no more than that.  The kept rows, in
+ * order, become rows 0, 1, .. of the destination pages, quantised as cb_kv8_write would quantise their values.  Heads
+ * keep different rows; K was rotated at its own position when it was stored, so attention needs no positions.
+ *   dst_table    device int32 [n_seqs][dst_ld]: seqs->table itself (with its table_ld) evicts in place; any other table
+ *                must name pages that seqs->table does not.
+ *   weights      device float32 [n_layers][n_seqs][n_kv_heads][weights_ld]
+ *   out_weights  the same shape, or weights itself: the kept rows' weights at entries 0 .. kept - 1, 0 at kept .. len - 1
+ *   out_rows     device int32 [n_layers][n_seqs][n_kv_heads][n_keep]: the kept rows, ascending, -1 behind the last
+ *   out_lens     device int32 [n_seqs]: min(len, n_keep); may be seqs->lens
+ * Async on `stream`; no allocation. */
+cb_status cb_kv8_evict(cb_kv8* cache, const cb_kv8_seqs* seqs, const int32_t* dst_table, int32_t dst_ld, int32_t layer,
+                       int32_t n_layers, const float* weights, int32_t weights_ld, int32_t n_keep, int32_t n_sink,
+                       int32_t n_recent, float* out_weights, int32_t* out_rows, int32_t* out_lens, void* stream);
+
+/* A blend whose chunk caches and blended K/V live in an 8-bit pool: cb_blend_paged with cb_kv8_read and cb_kv8_write
+ * at its two ends.  The n_ctx context rows (K still rotated at each chunk's src_pos) are read through src_table into
+ * work_kv, the blend runs there, and all n_tokens rows are written through dst_table (device int32, one entry per
+ * page_size rows; copy-on-write as for cb_blend_paged).  The cache and the model must agree in n_layers, n_kv_heads,
+ * head_dim and dtype.  All other arguments are those of cb_blend_paged; logits and work_kv come from the unrounded
+ * blend, the pool holds it in 8 bits. */
+cb_status cb_blend_kv8(cb_model* model, const int32_t* tokens, int32_t n_tokens, cb_kv8* cache,
+                       const int32_t* src_table, const int32_t* dst_table, const cb_chunk* chunks, int32_t n_chunks,
+                       const double* ratios, int32_t n_ratios, void* work_kv, float* out_logits, int32_t* out_selected,
+                       float* out_dev, cb_stats* stats, void* stream);
+
 /* Fragment lookup on the GPU (LMCache coordinator blend-index page, sections "四、数据结构与召回" and
  * "六、HTTP 接口"): which indexed chunks a request's tokens contain and where, i.e. the (src_pos, dst_pos)
  * chunk layout of a blend.
