@@ -22,6 +22,10 @@ struct Kv8 {
     float* scales;
     unsigned* status;        // ST_* bits
     float* scores;           // weight_cells floats: attention calls that return weights
+    float2* stats;           // their rows' (max, 1 / sum)
+    float* part;             // attention: pieces of items that span CTAs
+    unsigned* arrived;       // attention: pieces finished, one count per CTA (0 between calls)
+    alignas(64) unsigned char map[128];   // tensor map of the codes
 };
 
 // A batch of sequences as the kernels see it.
@@ -129,6 +133,10 @@ struct Kv8Attn {
 };
 cudaError_t launch_kv8_attention(const Kv8& c, const Kv8Seqs& q, const Kv8Rows& r, const Kv8Attn& a, int layer,
                                  cudaStream_t s);
+
+size_t kv8_part_floats(int num_sms);
+int kv8_most_ctas(int num_sms);
+bool kv8_make_map(const Kv8& c, void* out);
 
 struct Kv8Evict {
     const int* dst_table;

@@ -91,6 +91,12 @@ cb_status check_io(const cb_kv8& c, const void* k, const void* v, int64_t layer_
     return CB_OK;
 }
 
+void free_scratch(cb_kv8* c) {
+    void* ptrs[] = {c->status, c->scores, c->stats, c->part, c->arrived};
+    for (void* x : ptrs)
+        if (x) cudaFree(x);
+}
+
 }  // namespace
 
 extern "C" {
@@ -122,8 +128,9 @@ cb_status cb_kv8_create(const cb_kv8_config* cfg, void* codes, float* scales, cb
     h->cfg = c;
     h->codes = (uint8_t*)codes;
     h->scales = scales;
-    h->status = nullptr;
-    h->scores = nullptr;
+    h->status = h->arrived = nullptr;
+    h->scores = h->part = nullptr;
+    h->stats = nullptr;
     h->shift = 0;
     while ((1 << h->shift) < c.page_size) ++h->shift;
     if (cudaGetDevice(&h->device) != cudaSuccess ||
@@ -132,12 +139,23 @@ cb_status cb_kv8_create(const cb_kv8_config* cfg, void* codes, float* scales, cb
         delete h;
         return fail(CB_ERR_CUDA, "cb_kv8_create: no CUDA device");
     }
+    const size_t ctas = (size_t)kv8_most_ctas(h->num_sms);
     if (cudaMalloc(&h->status, 64) != cudaSuccess || cudaMemset(h->status, 0, 64) != cudaSuccess ||
-        (c.weight_cells > 0 && cudaMalloc(&h->scores, (size_t)c.weight_cells * 4) != cudaSuccess)) {
+        cudaMalloc(&h->part, kv8_part_floats(h->num_sms) * 4) != cudaSuccess ||
+        cudaMalloc(&h->arrived, ctas * 4) != cudaSuccess || cudaMemset(h->arrived, 0, ctas * 4) != cudaSuccess ||
+        (c.weight_cells > 0 && (cudaMalloc(&h->scores, (size_t)c.weight_cells * 4) != cudaSuccess ||
+                                // a row of at least one key takes 129 cells
+                                cudaMalloc(&h->stats, ((size_t)c.weight_cells / 129 + 1) * sizeof(float2)) != cudaSuccess))) {
         cudaGetLastError();
-        if (h->status) cudaFree(h->status);
+        free_scratch(h);
         delete h;
         return fail(CB_ERR_OOM, "cb_kv8_create: workspace allocation failed");
+    }
+    if (!kv8_make_map(*h, h->map) || cudaDeviceSynchronize() != cudaSuccess) {
+        cudaGetLastError();
+        free_scratch(h);
+        delete h;
+        return fail(CB_ERR_CUDA, "cb_kv8_create: no tensor map of the codes, or a device error");
     }
     *out = h;
     return CB_OK;
@@ -147,8 +165,7 @@ cb_status cb_kv8_destroy(cb_kv8* c) {
     set_last_error("");
     if (!c) return CB_OK;
     cudaDeviceSynchronize();
-    cudaFree(c->status);
-    if (c->scores) cudaFree(c->scores);
+    free_scratch(c);
     delete c;
     return CB_OK;
 }

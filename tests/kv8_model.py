@@ -94,13 +94,18 @@ class Model:
         return out
 
     def attention(self, table, lens, q, starts, layer, scale):
-        """out [n_q][Hq][hd], weights list of [H][len] per sequence, spread sum p|v| [n_q][Hq][hd] and the largest
-        sum |q k| scale of any row and key (for error bounds)."""
+        """out [n_q][Hq][hd], weights list of [H][len] per sequence, and for error bounds: spread, sum p|v|
+        [n_q][Hq][hd]; the largest sum |q k| scale of any row and key; self.floor [n_q][Hq][hd], the sum over tiles of
+        128 keys of (largest p * scale of V in the tile) * (sum of |codes of V|)."""
         out, spread = np.zeros(q.shape), np.zeros(q.shape)
+        self.floor = np.zeros(q.shape)
         ws, big = [], 0.0
         G = q.shape[1] // self.H
         for s, n in enumerate(lens):
             k, v = self.rows(table[s], n, layer)
+            sv = np.zeros((n, self.H))
+            for b in range(-(-n // self.P)):
+                sv[b * self.P:(b + 1) * self.P] = self.scales[layer, 1, table[s][b]]
             w = np.zeros((self.H, n))
             r0, r1 = starts[s], starts[s + 1]
             for i in range(r0, r1):
@@ -117,6 +122,10 @@ class Model:
                     out[i, h] = p @ vv
                     spread[i, h] = p @ np.abs(vv)
                     w[h // G, :seen] += p
+                    ss = sv[:seen, h // G]
+                    code = np.abs(vv) / np.where(ss > 0, ss, 1.0)[:, None]
+                    for t in range(0, seen, 128):
+                        self.floor[i, h] += (p * ss)[t:t + 128].max() * code[t:t + 128].sum(axis=0)
             ws.append(w)
         return out, ws, spread, big
 

@@ -7,7 +7,14 @@ score's error is at most ds = (head_dim + 8) u max sum|q k| scale (products and 
 softmax weight is then off by a factor e^(2 ds), about 2 ds, plus at most 16 u of its own evaluation.  out adds a sum
 over keys in fp32 (at most (128 + len / 128) u of sum p|v|: 128 keys at a time, then the steps' partial sums), the
 representation of p by the matrix unit's operands (2^-11 of it in bf16 calls, 2^-23 in fp32 ones) and one rounding of
-the result (half a step: 2^-8 |out| in bf16, 2^-24 in fp32)."""
+the result (half a step: 2^-8 |out| in bf16, 2^-24 in fp32).
+
+That representation has a floor too.  p times V's block scale stands as T e4m3 terms, term t in units of 16^-t, of numbers
+scaled so that the largest of a tile of 128 keys lies between 128 and 256.  A term's last place is 2^-9, so a number
+below the terms' range is off by at most half of it in the last term, 2^-10 16^-(T-1): relative to the tile's largest
+p * scale, Y >= 128 in those units, at most 2^-17 16^-(T-1), that is 2^-25 for T = 3 (bf16) and 2^-37 for T = 6 (fp32).
+An output element meets it once per key, times the key's code: 2^-25 or 2^-37 of the sum over tiles of
+Y sum|code| (the model's `floor`).  It shows only where keys of one tile differ by 2^14 and more in p * scale."""
 import numpy as np
 import pytest
 
@@ -206,12 +213,12 @@ def check_attention(c, q, q64, starts, out, w=None, layer=0, w_before=0.0, scale
     ref, ws, spread, big = c.model.attention(c.table_np, c.lens, q64, starts, layer, scale)
     ds = (c.hd + 8) * U * big
     steps = 128 + max(c.lens) / 128
-    p_rep, rnd = (2.0 ** -11, 2.0 ** -8) if c.dtype == "bf16" else (2.0 ** -23, 2.0 ** -24)
+    p_rep, rnd, last = (2.0 ** -11, 2.0 ** -8, 2.0 ** -25) if c.dtype == "bf16" else (2.0 ** -23, 2.0 ** -24, 2.0 ** -37)
     got = f64(out)
     owned = np.zeros(len(q64), bool)
     for s in range(len(c.lens)):
         owned[starts[s]:starts[s + 1]] = True
-    tol = rnd * np.abs(ref) + (2 * ds + (16 + steps) * U + p_rep) * spread
+    tol = rnd * np.abs(ref) + (2 * ds + (16 + steps) * U + p_rep) * spread + last * c.model.floor
     err = np.abs(got - ref)[owned]
     assert np.all(err <= tol[owned] + 1e-30), (err.max(), float((err / (tol[owned] + 1e-30)).max()))
     if w is not None:
