@@ -465,7 +465,11 @@ class KV8Cache:
         self.n_layers, _, self.n_pages, self.n_kv_heads, self.page_size, self.head_dim = codes.shape
         self.n_heads, self.device = int(n_heads), codes.device
         self.dtype = torch.bfloat16 if dtype == "bf16" else torch.float32
-        self._i32, self._f32 = torch.int32, torch.float32
+        self._i32, self._f32, self._dev = torch.int32, torch.float32, codes.get_device()
+        self._kv_row, self._kv_width = (self.n_kv_heads, self.head_dim), self.n_kv_heads * self.head_dim
+        self._q_row, self._q_width = (self.n_heads, self.head_dim), self.n_heads * self.head_dim
+        self._scale = self.head_dim ** -0.5
+        self._raw_stream = torch._C._cuda_getCurrentRawStream
         self._lib = lib()
         cfg = CbKV8Config(self.n_layers, self.n_heads, self.n_kv_heads, self.head_dim, CB_BF16 if dtype == "bf16" else CB_F32,
                           self.page_size, self.n_pages, int(weight_cells))
@@ -488,50 +492,47 @@ class KV8Cache:
         """weight_cells that an attention call of n_q query rows over at most max_len keys needs to return weights."""
         return n_q * n_heads * (-(-max_len // 128) * 128 + 1)
 
+    # A decoding step calls write and attention once per layer, so the checks below stay within a few microseconds.
     def _int(self, t, name, *shape):
-        if t.dtype != self._i32 or t.device != self.device or not t.is_contiguous() or t.dim() != len(shape) or \
-                any(w is not None and w != n for n, w in zip(t.shape, shape)):
+        if t.dtype is not self._i32 or t.get_device() != self._dev or not t.is_contiguous() or t.shape != shape:
             raise ValueError(f"{name} must be a contiguous int32 tensor {list(shape)} on {self.device}")
         return t.data_ptr()
 
     def _seqs(self, table, lens, max_len):
-        tp = self._int(table, "table", None, None)
+        if table.dim() != 2:
+            raise ValueError("table must be int32 [n_seqs][pages]")
         n, ld = table.shape
-        lp = None if lens is None else self._int(lens, "lens", n)
-        return CbKV8Seqs(n, tp, ld, lp, ld * self.page_size if max_len is None else int(max_len))
+        return CbKV8Seqs(n, self._int(table, "table", n, ld), ld, None if lens is None else self._int(lens, "lens", n),
+                         ld * self.page_size if max_len is None else max_len)
 
-    def _call(self, f, *args, stream=None):
-        """The library call with the cache's device current."""
-        import torch
-        if torch.cuda.current_device() == self.device.index:
-            _check(f(self.handle, *args, _stream(stream)))
-        else:
-            with torch.cuda.device(self.device):
-                _check(f(self.handle, *args, _stream(stream)))
+    def _stream(self, stream):
+        if stream is None:
+            return self._raw_stream(self._dev)
+        return stream if isinstance(stream, int) else stream.cuda_stream
 
-    def _rows(self, t, name, n_layers, n_rows=None):
-        """(pointer, layer stride, row stride) of K/V rows [n_layers][n_rows][n_kv_heads][head_dim] (or without the
+    def _kv(self, t, name, n_layers):
+        """(pointer, layer stride, row stride, rows) of K/V rows [n_layers][rows][n_kv_heads][head_dim] (or without the
         layers when there is one)."""
-        if t.dim() == 3 and n_layers == 1:
-            t = t.unsqueeze(0)
-        if t.dtype != self.dtype or t.device != self.device or t.dim() != 4 or t.shape[0] != n_layers or \
-                t.shape[2:] != (self.n_kv_heads, self.head_dim) or (n_rows is not None and t.shape[1] != n_rows):
+        shape, stride = t.shape, t.stride()
+        if len(shape) == 3 and n_layers == 1:
+            shape, stride = (1, *shape), (0, *stride)
+        if t.dtype is not self.dtype or t.get_device() != self._dev or len(shape) != 4 or shape[0] != n_layers or \
+                shape[2:] != self._kv_row:
             raise ValueError(f"{name} must be {self.dtype} [{n_layers}][rows][{self.n_kv_heads}][{self.head_dim}] on {self.device}")
-        sl, sr, sh, sd = t.stride()
-        if sd != 1 or (sh != self.head_dim and self.n_kv_heads > 1):
+        if stride[3] != 1 or (stride[2] != self.head_dim and self.n_kv_heads > 1):
             raise ValueError(f"{name}: the heads of a row must be contiguous")
-        rows = t.shape[1]
-        w = self.n_kv_heads * self.head_dim
-        return t.data_ptr(), sl if n_layers > 1 else 0, sr if rows > 1 else w, rows
+        return t.data_ptr(), stride[0] if n_layers > 1 else 0, stride[1] if shape[1] > 1 else self._kv_width, shape[1]
 
     def _io(self, f, table, lens, k, v, layer, n_layers, row_start, max_len, stream):
-        kp, kl, kr, rows = self._rows(k, "k", n_layers)
-        vp, vl, vr, _ = self._rows(v, "v", n_layers, rows)
-        if kl != vl or kr != vr:
-            raise ValueError("k and v must have the same strides")
+        kp, *lay = self._kv(k, "k", n_layers)
+        vp, *lay_v = self._kv(v, "v", n_layers)
+        if lay != lay_v:
+            raise ValueError("k and v must have the same number of rows and the same strides")
         sq = self._seqs(table, lens, max_len)
-        rs = None if row_start is None else self._int(row_start, "row_start", sq.n_seqs + 1)
-        self._call(f, sq, layer, n_layers, kp, vp, kl, kr, rs, rows, stream=stream)
+        code = f(self.handle, sq, layer, n_layers, kp, vp, lay[0], lay[1],
+                 None if row_start is None else self._int(row_start, "row_start", sq.n_seqs + 1), lay[2], self._stream(stream))
+        if code:
+            _check(code)
 
     def write(self, table, lens, k, v, layer: int = 0, n_layers: int = 1, row_start=None, max_len=None, stream=None):
         """k and v ([n_layers][n_rows][n_kv_heads][head_dim]) become the last rows of their sequences (lens counts them
@@ -543,36 +544,39 @@ class KV8Cache:
         """The last rows of each sequence as values, into k and v (as for write)."""
         self._io(self._lib.cb_kv8_read, table, lens, k, v, layer, n_layers, row_start, max_len, stream)
 
+    def _q(self, t, name):
+        shape, stride = t.shape, t.stride()
+        if t.dtype is not self.dtype or t.get_device() != self._dev or len(shape) != 3 or shape[1:] != self._q_row:
+            raise ValueError(f"{name} must be {self.dtype} [n_q][{self.n_heads}][{self.head_dim}] on {self.device}")
+        if stride[2] != 1 or (stride[1] != self.head_dim and self.n_heads > 1):
+            raise ValueError(f"{name}: the heads of a row must be contiguous")
+        return t.data_ptr(), stride[0] if shape[0] > 1 else self._q_width, shape[0]
+
     def attention(self, table, lens, q, out=None, layer: int = 0, q_start=None, scale=None, weights=None, add: bool = False,
                   max_len=None, stream=None):
         """softmax(q k * scale) v of the query rows q [n_q][n_heads][head_dim], each sequence's last rows, over its cache
         (causal); returns out.  weights (device float32 [n_seqs][n_kv_heads][ld >= max_len]) receives, or with add
         accumulates, the weight of every key.  q_start as row_start of write; scale defaults to head_dim ** -0.5."""
         if out is None:
-            import torch
-            out = torch.empty(q.shape, dtype=self.dtype, device=self.device)
-            if q_start is not None:
-                out.zero_()                                   # rows that belong to no sequence
-        row = (self.n_heads, self.head_dim)
-        strides = []
-        for t, name in ((q, "q"), (out, "out")):
-            if t.dtype != self.dtype or t.device != self.device or t.dim() != 3 or t.shape[1:] != row or t.shape[0] != q.shape[0]:
-                raise ValueError(f"{name} must be {self.dtype} [n_q][{self.n_heads}][{self.head_dim}] on {self.device}")
-            sr, sh, sd = t.stride()
-            if sd != 1 or (sh != self.head_dim and self.n_heads > 1):
-                raise ValueError(f"{name}: the heads of a row must be contiguous")
-            strides.append(sr if t.shape[0] > 1 else self.n_heads * self.head_dim)
+            # rows that belong to no sequence are not written: zeros there
+            out = q.new_empty(q.shape) if q_start is None else q.new_zeros(q.shape)
+        qp, qs, n = self._q(q, "q")
+        op, os_, n_out = self._q(out, "out")
+        if n_out != n:
+            raise ValueError(f"out must have q's {n} rows")
         sq = self._seqs(table, lens, max_len)
-        qs = None if q_start is None else self._int(q_start, "q_start", sq.n_seqs + 1)
         wp, ld = None, 0
         if weights is not None:
-            if weights.dtype != self._f32 or weights.device != self.device or not weights.is_contiguous() or \
-                    weights.dim() != 3 or weights.shape[:2] != (sq.n_seqs, self.n_kv_heads):
+            ld = weights.shape[-1]
+            if weights.dtype is not self._f32 or weights.get_device() != self._dev or not weights.is_contiguous() or \
+                    weights.shape != (sq.n_seqs, self.n_kv_heads, ld):
                 raise ValueError(f"weights must be contiguous float32 [{sq.n_seqs}][{self.n_kv_heads}][keys] on {self.device}")
-            wp, ld = weights.data_ptr(), weights.shape[2]
-        self._call(self._lib.cb_kv8_attention, sq, layer, q.data_ptr(), strides[0], qs, q.shape[0],
-                   self.head_dim ** -0.5 if scale is None else scale, out.data_ptr(), strides[1], wp, ld, 1 if add else 0,
-                   stream=stream)
+            wp = weights.data_ptr()
+        code = self._lib.cb_kv8_attention(self.handle, sq, layer, qp, qs,
+                                          None if q_start is None else self._int(q_start, "q_start", sq.n_seqs + 1), n,
+                                          self._scale if scale is None else scale, op, os_, wp, ld, add, self._stream(stream))
+        if code:
+            _check(code)
         return out
 
     def evict(self, table, lens, dst_table, weights, n_keep: int, n_sink: int = 0, n_recent: int = 0, out_rows=None,
@@ -581,32 +585,35 @@ class KV8Cache:
         largest weight (weights: device float32 [n_layers][n_seqs][n_kv_heads][ld]).  The kept rows move to dst_table
         (table itself: in place; else pages that table does not name).  Returns dict(rows, lens, weights); out_weights
         defaults to weights itself, out_lens may be lens."""
-        import torch
         sq = self._seqs(table, lens, max_len)
         n = sq.n_seqs
-        dp = self._int(dst_table, "dst_table", n, None)
+        if dst_table.dim() != 2:
+            raise ValueError("dst_table must be int32 [n_seqs][pages]")
+        dst_ld = dst_table.shape[1]
+        dp = self._int(dst_table, "dst_table", n, dst_ld)
         if out_weights is None:
             out_weights = weights
         if out_lens is None:
-            out_lens = torch.empty(n, dtype=torch.int32, device=self.device)
+            out_lens = table.new_empty(n)
         if out_rows is None:
-            out_rows = torch.empty((n_layers, n, self.n_kv_heads, max(int(n_keep), 0)), dtype=torch.int32, device=self.device)
+            out_rows = table.new_empty((n_layers, n, self.n_kv_heads, max(int(n_keep), 0)))
+        ld = weights.shape[-1]
         for t, name in ((weights, "weights"), (out_weights, "out_weights")):
-            if t.dtype != self._f32 or t.device != self.device or not t.is_contiguous() or t.dim() != 4 or \
-                    t.shape[:3] != (n_layers, n, self.n_kv_heads) or t.shape[3] != weights.shape[3]:
+            if t.dtype is not self._f32 or t.get_device() != self._dev or not t.is_contiguous() or \
+                    t.shape != (n_layers, n, self.n_kv_heads, ld):
                 raise ValueError(f"{name} must be contiguous float32 [{n_layers}][{n}][{self.n_kv_heads}][rows] on {self.device}")
-        rp = self._int(out_rows, "out_rows", n_layers, n, self.n_kv_heads, int(n_keep))
-        lp = self._int(out_lens, "out_lens", n)
-        self._call(self._lib.cb_kv8_evict, sq, dp, dst_table.shape[1], layer, n_layers, weights.data_ptr(), weights.shape[3],
-                   n_keep, n_sink, n_recent, out_weights.data_ptr(), rp, lp, stream=stream)
+        code = self._lib.cb_kv8_evict(self.handle, sq, dp, dst_ld, layer, n_layers, weights.data_ptr(), ld, n_keep, n_sink,
+                                      n_recent, out_weights.data_ptr(),
+                                      self._int(out_rows, "out_rows", n_layers, n, self.n_kv_heads, n_keep),
+                                      self._int(out_lens, "out_lens", n), self._stream(stream))
+        if code:
+            _check(code)
         return dict(rows=out_rows, lens=out_lens, weights=out_weights)
 
     def status(self, clear: bool = False) -> int:
         """Device status bits (CB_STATUS_*) recorded by the kernels; synchronises."""
-        import torch
         v = ctypes.c_uint32()
-        with torch.cuda.device(self.device):
-            _check(self._lib.cb_kv8_status(self.handle, ctypes.byref(v), 1 if clear else 0))
+        _check(self._lib.cb_kv8_status(self.handle, ctypes.byref(v), 1 if clear else 0))
         return v.value
 
     def close(self):

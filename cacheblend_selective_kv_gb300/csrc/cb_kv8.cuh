@@ -25,6 +25,7 @@ struct Kv8 {
     float2* stats;           // their rows' (max, 1 / sum)
     float* part;             // attention: pieces of items that span CTAs
     unsigned* arrived;       // attention: pieces finished, one count per CTA (0 between calls)
+    void* scratch;           // the allocation that holds the five above
     alignas(64) unsigned char map[128];   // tensor map of the codes
 };
 

@@ -32,14 +32,22 @@ cb_status check_handle(const cb_kv8* c, const char* who) {
     return c ? CB_OK : fail(CB_ERR_INVALID_ARG, "%s: null cache", who);
 }
 
-// the device the handle lives on has to be the current one (the last check before a launch)
-cb_status check_device(const cb_kv8* c, const char* who) {
-    int dev = -1;
-    if (cudaGetDevice(&dev) != cudaSuccess) return fail(CB_ERR_CUDA, "%s: no CUDA device", who);
-    if (dev != c->device)
-        return fail(CB_ERR_INVALID_ARG, "%s: the cache is on device %d, the current one is %d", who, c->device, dev);
-    return CB_OK;
-}
+// The handle's device is made current for a call and the caller's put back (the last step before a launch).
+struct OnDevice {
+    int was = -1;
+    bool moved = false;
+    cb_status to(const cb_kv8* c, const char* who) {
+        if (cudaGetDevice(&was) != cudaSuccess || (was != c->device && cudaSetDevice(c->device) != cudaSuccess)) {
+            cudaGetLastError();
+            return fail(CB_ERR_CUDA, "%s: the cache's CUDA device %d is not available", who, c->device);
+        }
+        moved = was != c->device;
+        return CB_OK;
+    }
+    ~OnDevice() {
+        if (moved) cudaSetDevice(was);
+    }
+};
 
 cb_status check_layers(const cb_kv8& c, int32_t layer, int32_t n_layers, const char* who) {
     if (layer < 0 || n_layers < 0 || layer > c.cfg.n_layers - n_layers)
@@ -91,12 +99,6 @@ cb_status check_io(const cb_kv8& c, const void* k, const void* v, int64_t layer_
     return CB_OK;
 }
 
-void free_scratch(cb_kv8* c) {
-    void* ptrs[] = {c->status, c->scores, c->stats, c->part, c->arrived};
-    for (void* x : ptrs)
-        if (x) cudaFree(x);
-}
-
 }  // namespace
 
 extern "C" {
@@ -128,9 +130,6 @@ cb_status cb_kv8_create(const cb_kv8_config* cfg, void* codes, float* scales, cb
     h->cfg = c;
     h->codes = (uint8_t*)codes;
     h->scales = scales;
-    h->status = h->arrived = nullptr;
-    h->scores = h->part = nullptr;
-    h->stats = nullptr;
     h->shift = 0;
     while ((1 << h->shift) < c.page_size) ++h->shift;
     if (cudaGetDevice(&h->device) != cudaSuccess ||
@@ -139,21 +138,27 @@ cb_status cb_kv8_create(const cb_kv8_config* cfg, void* codes, float* scales, cb
         delete h;
         return fail(CB_ERR_CUDA, "cb_kv8_create: no CUDA device");
     }
-    const size_t ctas = (size_t)kv8_most_ctas(h->num_sms);
-    if (cudaMalloc(&h->status, 64) != cudaSuccess || cudaMemset(h->status, 0, 64) != cudaSuccess ||
-        cudaMalloc(&h->part, kv8_part_floats(h->num_sms) * 4) != cudaSuccess ||
-        cudaMalloc(&h->arrived, ctas * 4) != cudaSuccess || cudaMemset(h->arrived, 0, ctas * 4) != cudaSuccess ||
-        (c.weight_cells > 0 && (cudaMalloc(&h->scores, (size_t)c.weight_cells * 4) != cudaSuccess ||
-                                // a row of at least one key takes 129 cells
-                                cudaMalloc(&h->stats, ((size_t)c.weight_cells / 129 + 1) * sizeof(float2)) != cudaSuccess))) {
+    // one allocation: status, arrival counts (both zero between calls), pieces, statistics, scores
+    const size_t head = 256 + ((size_t)kv8_most_ctas(h->num_sms) * 4 + 255) / 256 * 256;
+    const size_t part = (kv8_part_floats(h->num_sms) * 4 + 255) / 256 * 256;
+    // a row of a call that returns weights takes at least 129 cells
+    const size_t stats = c.weight_cells > 0 ? (((size_t)c.weight_cells / 129 + 1) * sizeof(float2) + 255) / 256 * 256 : 0;
+    if (cudaMalloc(&h->scratch, head + part + stats + (size_t)c.weight_cells * 4) != cudaSuccess) {
         cudaGetLastError();
-        free_scratch(h);
         delete h;
         return fail(CB_ERR_OOM, "cb_kv8_create: workspace allocation failed");
     }
-    if (!kv8_make_map(*h, h->map) || cudaDeviceSynchronize() != cudaSuccess) {
+    char* at = (char*)h->scratch;
+    h->status = (unsigned*)at;
+    h->arrived = (unsigned*)(at + 256);
+    h->part = (float*)(at + head);
+    h->stats = (float2*)(at + head + part);
+    h->scores = (float*)(at + head + part + stats);
+    // cleared before the handle is given out, whatever stream its first call uses
+    if (!kv8_make_map(*h, h->map) || cudaMemset(h->scratch, 0, head) != cudaSuccess ||
+        cudaStreamSynchronize(cudaStreamLegacy) != cudaSuccess) {
         cudaGetLastError();
-        free_scratch(h);
+        cudaFree(h->scratch);
         delete h;
         return fail(CB_ERR_CUDA, "cb_kv8_create: no tensor map of the codes, or a device error");
     }
@@ -164,8 +169,10 @@ cb_status cb_kv8_create(const cb_kv8_config* cfg, void* codes, float* scales, cb
 cb_status cb_kv8_destroy(cb_kv8* c) {
     set_last_error("");
     if (!c) return CB_OK;
+    OnDevice on;
+    if (on.to(c, "cb_kv8_destroy") != CB_OK) return CB_ERR_CUDA;
     cudaDeviceSynchronize();
-    free_scratch(c);
+    cudaFree(c->scratch);
     delete c;
     return CB_OK;
 }
@@ -174,7 +181,8 @@ cb_status cb_kv8_status(cb_kv8* c, uint32_t* bits, int32_t clear) {
     cb_status st = check_handle(c, "cb_kv8_status");
     if (st != CB_OK) return st;
     if (!bits) return fail(CB_ERR_INVALID_ARG, "cb_kv8_status: null bits");
-    st = check_device(c, "cb_kv8_status");
+    OnDevice on;
+    st = on.to(c, "cb_kv8_status");
     if (st != CB_OK) return st;
     if (cudaDeviceSynchronize() != cudaSuccess || cudaMemcpy(bits, c->status, 4, cudaMemcpyDeviceToHost) != cudaSuccess ||
         (clear && cudaMemset(c->status, 0, 64) != cudaSuccess))
@@ -195,7 +203,8 @@ cb_status cb_kv8_write(cb_kv8* c, const cb_kv8_seqs* seqs, int32_t layer, int32_
     if (st != CB_OK) return st;
     if (n_rows == 0 || n_layers == 0 || q.n == 0) return CB_OK;
     st = check_io(*c, k, v, layer_stride, row_stride, n_layers, n_rows, who, io);
-    if (st == CB_OK) st = check_device(c, who);
+    OnDevice on;
+    if (st == CB_OK) st = on.to(c, who);
     if (st != CB_OK) return st;
     return cuda_result(launch_kv8_write(*c, q, r, io, layer, n_layers, (cudaStream_t)stream), who);
 }
@@ -213,7 +222,8 @@ cb_status cb_kv8_read(cb_kv8* c, const cb_kv8_seqs* seqs, int32_t layer, int32_t
     if (st != CB_OK) return st;
     if (n_rows == 0 || n_layers == 0 || q.n == 0) return CB_OK;
     st = check_io(*c, k, v, layer_stride, row_stride, n_layers, n_rows, who, io);
-    if (st == CB_OK) st = check_device(c, who);
+    OnDevice on;
+    if (st == CB_OK) st = on.to(c, who);
     if (st != CB_OK) return st;
     return cuda_result(launch_kv8_read(*c, q, r, io, layer, n_layers, (cudaStream_t)stream), who);
 }
@@ -248,7 +258,8 @@ cb_status cb_kv8_attention(cb_kv8* c, const cb_kv8_seqs* seqs, int32_t layer, co
                         (long long)cells, (long long)c->cfg.weight_cells);
     }
     if (sq.n == 0 || (n_q == 0 && !weights)) return CB_OK;
-    st = check_device(c, who);
+    OnDevice on;
+    st = on.to(c, who);
     if (st != CB_OK) return st;
     const Kv8Attn a{q, q_stride, out, out_stride, scale, weights, weights_ld, add != 0};
     return cuda_result(launch_kv8_attention(*c, sq, r, a, layer, (cudaStream_t)stream), who);
@@ -276,7 +287,8 @@ cb_status cb_kv8_evict(cb_kv8* c, const cb_kv8_seqs* seqs, const int32_t* dst_ta
     const int64_t cells = (int64_t)n_layers * q.n * c->cfg.n_kv_heads * weights_ld * 4;
     if (weights != out_weights && overlap(weights, cells, out_weights, cells))
         return fail(CB_ERR_INVALID_ARG, "%s: weights and out_weights overlap without being the same", who);
-    st = check_device(c, who);
+    OnDevice on;
+    st = on.to(c, who);
     if (st != CB_OK) return st;
     const Kv8Evict e{dst_table, dst_ld, weights, out_weights, weights_ld, n_keep, n_sink, n_recent, out_rows, out_lens};
     return cuda_result(launch_kv8_evict(*c, q, e, layer, n_layers, (cudaStream_t)stream), who);

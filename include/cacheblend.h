@@ -291,10 +291,10 @@ int64_t cb_pages_free(const cb_pages* pages);
  * A scale is a power of two, or 0 for a block of zeros: the smallest s with max|x| <= 448 s over the block's finite
  * values, not below 2^-126, and a code is x / s rounded to nearest even.  Values read back are exact in bf16 and
  * fp32.  A NaN or an infinity is kept as NaN and does not count for the scale.
- * Both buffers are the caller's.  A handle borrows them, knows their geometry and owns the scratch of its calls; it
- * lives on the device that was current at creation, and its calls are made with that device current.  Calls on one
- * handle must not overlap on the GPU (they share its scratch and its pages); two handles may share one pool as long
- * as no page is written while another call reads it. */
+ * Both buffers are the caller's.  A handle borrows them, knows their geometry and owns the scratch of its calls.  It
+ * lives on the device that was current at creation; its calls run there whichever device is current, on a stream of
+ * that device.  Calls on one handle must not overlap on the GPU (they share its scratch and its pages); two handles
+ * may share one pool as long as no page is written while another call reads it. */
 typedef struct cb_kv8 cb_kv8;
 typedef struct {
     int32_t n_layers;
