@@ -20,14 +20,19 @@
 // spans several CTAs is joined by the CTA that finishes last, in the order of the pieces (the result does not depend on
 // which one that is).  Which items a CTA has follows from the lengths on the device, so a captured graph stays valid.
 //
-// Roles: warps 0-3 softmax and output (thread = key, then thread = dim), warp 4 TMA (page by page through the block
-// table), warp 5 MMA.  S of the next tile is computed while P of this one is formed; O of a tile is read back from
+// Roles: softmax and output warps in groups of four (thread = key, then thread = dim; a group owns NC / GR of the columns,
+// so that many columns get more warps and not more registers per thread), one TMA warp (page by page through the block
+// table), one MMA warp.  S of the next tile is computed while P of this one is formed; O of a tile is read back from
 // tensor memory and added in registers while the next tile's P is formed, which rescales it exactly and makes every
-// tile's sum its own.
+// tile's sum its own.  P is stored [key][column], the B operand MN-major, so that a thread's terms are a few vector
+// stores instead of a byte store for each; what belongs to a column (its maximum, its factors) is computed by one lane
+// per warp and read back from shared memory.
 #include <cudaTypedefs.h>
 
+#include <algorithm>
 #include <climits>
 #include <cstring>
+#include <iterator>
 
 #include "cb_kv8.cuh"
 #include "cb_ptx.cuh"
@@ -37,9 +42,6 @@ namespace cb {
 namespace {
 
 constexpr int TK = 128;                  // keys per tile
-constexpr int SOFT = 128;                // softmax threads
-constexpr int THREADS = SOFT + 64;
-constexpr int STAGES = 2;                // K and V tiles in flight
 
 struct AttnArgs {
     Kv8Seqs q;
@@ -88,8 +90,38 @@ template <int ROW> __device__ __forceinline__ uint64_t f8_desc(uint32_t saddr, u
     return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(lbo >> 4) << 16) | ((uint64_t)((8 * ROW) >> 4) << 32) |
            ((uint64_t)1 << 46) | ((uint64_t)(ROW == 128 ? 2 : 4) << 61);
 }
-__host__ __device__ constexpr uint32_t f8_idesc(int N, bool a_mn) {
-    return (1u << 4) | ((uint32_t)(N >> 3) << 17) | (8u << 24) | (a_mn ? 1u << 15 : 0u);   // M = 128
+// B operand MN-major: rows (keys) of PITCH bytes = columns in the PITCH-byte swizzle; more than 128 columns are further
+// blocks of 128 rows
+template <int PITCH> __device__ __forceinline__ uint64_t p_desc(uint32_t saddr) {
+    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)((TK * PITCH) >> 4) << 16) | ((uint64_t)((8 * PITCH) >> 4) << 32) |
+           ((uint64_t)1 << 46) | ((uint64_t)(PITCH == 128 ? 2 : PITCH == 64 ? 4 : 6) << 61);
+}
+template <int PITCH> __device__ __forceinline__ uint32_t p_at(uint32_t key, uint32_t col) {
+    const uint32_t c = col % PITCH, ch = c >> 4;
+    const uint32_t x = PITCH == 128 ? (ch ^ key) & 7 : PITCH == 64 ? (ch ^ (key >> 1)) & 3 : (ch ^ (key >> 2)) & 1;
+    return col / PITCH * (TK * PITCH) + key * PITCH + x * 16 + (c & 15);
+}
+__host__ __device__ constexpr uint32_t f8_idesc(int N, bool mn) {       // M = 128; mn: both operands MN-major
+    return (1u << 4) | ((uint32_t)(N >> 3) << 17) | (8u << 24) | (mn ? 3u << 15 : 0u);
+}
+// N consecutive columns of this thread's lane, without the wait
+template <int N> __device__ __forceinline__ void tmem_ld_cols(uint32_t addr, uint32_t* r) {
+    if constexpr (N == 4) {
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
+    } else if constexpr (N == 8) {
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                     : "r"(addr));
+    } else {
+        ptx::tmem_ld16_issue(addr, r);
+    }
+}
+// ... and the wait, through which the registers pass so that no use of them moves above it
+template <int N> __device__ __forceinline__ void tmem_ld_done(uint32_t* r) {
+#pragma unroll
+    for (int k = 0; k < N; k += 4)
+        asm volatile("tcgen05.wait::ld.sync.aligned;" : "+r"(r[k]), "+r"(r[k + 1]), "+r"(r[k + 2]), "+r"(r[k + 3])::"memory");
 }
 // byte `b` of row `row` in that swizzled layout
 template <int ROW> __device__ __forceinline__ uint32_t f8_at(uint32_t row, uint32_t b) {
@@ -146,46 +178,51 @@ struct Cursor {
     }
 };
 
+constexpr int MAX_STAGES = 3;
 struct Shared {
-    uint64_t k_full[STAGES], v_full[STAGES], empty[STAGES];
+    uint64_t k_full[MAX_STAGES], v_full[MAX_STAGES], empty[MAX_STAGES];
     uint64_t s_full[2], s_free[2];
     uint64_t p_full, o_full, q_full, drain;
     uint32_t tmem;
     int abort;
-    long long total;                     // tiles of all items
     int s0, qt0, g0, tile0;              // where this CTA begins
+    Seq seq0;
     int last;                            // this CTA joins the item
-    int prefix[THREADS / 32];
-    long long sums[THREADS / 32];
+    long long sums[32];
 };
 
 // ------------------------------------------------------------------------------------------------
-// HD: head_dim; NC: query columns; TQ, TP: terms of q and P
+// HD: head_dim; NC: query columns; GR: softmax groups; TQ, TP: terms of q and P; CTAS per SM; STAGES: K and V tiles in flight
 // ------------------------------------------------------------------------------------------------
-template <int HD, int NC, int TQ, int TP> struct Shape {
+template <int HD_, int NC_, int GR_, int TQ_, int TP_, int CTAS_, int STAGES_> struct Shape {
+    static constexpr int HD = HD_, NC = NC_, GR = GR_, TQ = TQ_, TP = TP_, CTAS = CTAS_, STAGES = STAGES_;
+    static constexpr int NW = NC / GR;                                     // columns of a group
+    static constexpr int SOFT = 128 * GR, THREADS = SOFT + 64;
     static constexpr int NQ = round16(TQ * NC), NP = round16(TP * NC);     // MMA columns
-    static constexpr int KV_BYTES = TK * HD;
-    static constexpr int Q_BYTES = NQ * HD, P_BYTES = NP * TK;
+    static constexpr int KV_BYTES = TK * HD, Q_BYTES = NQ * HD;
+    static constexpr int PITCH = NP <= 32 ? 32 : NP <= 64 ? 64 : 128;
+    static constexpr int P_BYTES = (NP + 127) / 128 * TK * PITCH;
     static constexpr int O_COL = 2 * NQ;
     static constexpr int TMEM = pow2_cols(2 * NQ + NP);
     // K/V stages, Q, P (all 1024-byte aligned), then the softmax exchange and the control block
     static constexpr int OFF_Q = 2 * STAGES * KV_BYTES;
     static constexpr int OFF_P = (OFF_Q + Q_BYTES + 1023) / 1024 * 1024;
     static constexpr int OFF_X = (OFF_P + P_BYTES + 1023) / 1024 * 1024;
-    // floats: wmax [2][4][NC], ymax [2][4][NC], qscale [NC], wsum [4][NC], nan_from [HD]
-    static constexpr int X_FLOATS = 8 * NC + 8 * NC + NC + 4 * NC + HD;
+    // floats: wmax, ymax [2][GR][4][NW]; cols [2][4 GR][4][NW]; qscale [NC]; wsum, colm [4][NC]; nan_from [HD]
+    static constexpr int X_FLOATS = 2 * 8 * NC + 2 * 4 * GR * 4 * NW + NC + 8 * NC + HD;
     static constexpr int OFF_C = (OFF_X + X_FLOATS * 4 + 63) / 64 * 64;
     static constexpr int BYTES = OFF_C + (int)sizeof(Shared) + 1024;       // + alignment of the base
-    // CTAs per SM: what registers and tensor memory allow
-    static constexpr int CTAS = NC <= 8 && TMEM <= 128 ? 3 : 2;
+    static constexpr int PIECE = NC * (HD + 2);                            // floats of an unfinished item
     static_assert(TMEM * CTAS <= 512 && 2 * NQ + NP <= 512, "tensor memory");
+    static_assert((BYTES + 1024) * CTAS <= 228 * 1024 && STAGES <= MAX_STAGES, "shared memory");
+    static_assert(NW == 4 || NW == 8 || NW == 16, "columns of a group");
 };
 
-template <typename T, int HD, int NC, int TQ, int TP>
-__global__ void __launch_bounds__(THREADS, Shape<HD, NC, TQ, TP>::CTAS)
+template <typename T, typename S>
+__global__ void __launch_bounds__(S::THREADS, S::CTAS)
     kv8_attn_kernel(const __grid_constant__ CUtensorMap map, const AttnArgs p) {
-    using S = Shape<HD, NC, TQ, TP>;
-    constexpr int NQ = S::NQ, NP = S::NP;
+    constexpr int HD = S::HD, NC = S::NC, NW = S::NW, GR = S::GR, TQ = S::TQ, TP = S::TP, NQ = S::NQ, NP = S::NP;
+    constexpr int STAGES = S::STAGES, SOFT = S::SOFT, THREADS = S::THREADS, TMA_WARP = SOFT / 32, MMA_WARP = TMA_WARP + 1;
     extern __shared__ uint8_t raw[];
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
     uint8_t* sK = sm;                                   // [STAGES][TK][HD]
@@ -194,9 +231,11 @@ __global__ void __launch_bounds__(THREADS, Shape<HD, NC, TQ, TP>::CTAS)
     uint8_t* sP = sm + S::OFF_P;
     float* wmax = reinterpret_cast<float*>(sm + S::OFF_X);
     float* ymax = wmax + 8 * NC;
-    float* qscale = ymax + 8 * NC;
+    float* cols_of = ymax + 8 * NC;
+    float* qscale = cols_of + 2 * 4 * GR * 4 * NW;
     float* wsum = qscale + NC;
-    int* nan_from = reinterpret_cast<int*>(wsum + 4 * NC);
+    float* colm = wsum + 4 * NC;
+    int* nan_from = reinterpret_cast<int*>(colm + 4 * NC);
     Shared& c = *reinterpret_cast<Shared*>(sm + S::OFF_C);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     unsigned* status = p.q.status;
@@ -210,25 +249,27 @@ __global__ void __launch_bounds__(THREADS, Shape<HD, NC, TQ, TP>::CTAS)
         }
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(ptx::smem_u32(&c.s_full[i]), 1);
-            ptx::mbar_init(ptx::smem_u32(&c.s_free[i]), 4);
+            ptx::mbar_init(ptx::smem_u32(&c.s_free[i]), SOFT / 32);
         }
-        ptx::mbar_init(ptx::smem_u32(&c.p_full), 4);
+        ptx::mbar_init(ptx::smem_u32(&c.p_full), SOFT / 32);
         ptx::mbar_init(ptx::smem_u32(&c.o_full), 1);
-        ptx::mbar_init(ptx::smem_u32(&c.q_full), 4);
+        ptx::mbar_init(ptx::smem_u32(&c.q_full), SOFT / 32);
         ptx::mbar_init(ptx::smem_u32(&c.drain), 1);
         c.abort = 0;
         ptx::fence_barrier_init();
         ptx::prefetch_tmap(&map);
     }
-    if (warp == 5) {
+    if (warp == MMA_WARP) {
         ptx::tmem_alloc(ptx::smem_u32(&c.tmem), S::TMEM);
         ptx::tmem_relinquish();
     }
 
-    // ---- this CTA's piece of the list: two passes over the sequences, THREADS at a time
+    // ---- this CTA's piece of the list, THREADS sequences at a time (the first step's are kept)
+    const Seq q_own = tid < p.q.n ? seq_at(p, tid) : Seq{0, 0, 0};
+    const long long t_own = seq_tiles(p, q_own);
     {
-        long long mine = 0;
-        for (int s = tid; s < p.q.n; s += THREADS) mine += seq_tiles(p, seq_at(p, s));
+        long long mine = t_own;
+        for (int s = tid + THREADS; s < p.q.n; s += THREADS) mine += seq_tiles(p, seq_at(p, s));
         for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
         if (lane == 0) c.sums[warp] = mine;
     }
@@ -244,8 +285,8 @@ __global__ void __launch_bounds__(THREADS, Shape<HD, NC, TQ, TP>::CTAS)
         long long base = 0;                                      // tiles of the sequences before this step's
         for (int s0 = 0; s0 < p.q.n; s0 += THREADS) {
             const int s = s0 + tid;
-            const Seq q = s < p.q.n ? seq_at(p, s) : Seq{0, 0, 0};
-            const long long mine = seq_tiles(p, q);
+            const Seq q = s0 == 0 ? q_own : (s < p.q.n ? seq_at(p, s) : Seq{0, 0, 0});
+            const long long mine = s0 == 0 ? t_own : seq_tiles(p, q);
             long long x = mine;
             for (int o = 1; o < 32; o <<= 1) {
                 const long long y = __shfl_up_sync(0xffffffffu, x, o);
@@ -271,6 +312,7 @@ __global__ void __launch_bounds__(THREADS, Shape<HD, NC, TQ, TP>::CTAS)
                 c.qt0 = qt;
                 c.g0 = (int)(left / nt);
                 c.tile0 = (int)(left % nt);
+                c.seq0 = q;
             }
             if (all > t0) break;
             base = all;
@@ -284,11 +326,11 @@ __global__ void __launch_bounds__(THREADS, Shape<HD, NC, TQ, TP>::CTAS)
         cur.qt = c.qt0;
         cur.g = c.g0;
         cur.t = c.tile0;
-        cur.q = seq_at(p, cur.s);
+        cur.q = c.seq0;
         cur.settle(p);
     }
 
-    if (warp == 4) {
+    if (warp == TMA_WARP) {
         // ------------------------------------------------------------------------------------ TMA
         const int boxes = TK / p.box, rows = p.box;              // boxes per tile, one lane each
         const int per_page = 1 << p.q.shift;
@@ -329,11 +371,11 @@ __global__ void __launch_bounds__(THREADS, Shape<HD, NC, TQ, TP>::CTAS)
             ptx::mbar_wait(ptx::smem_u32(&c.k_full[st]), par, &never, status);
             ptx::mbar_wait(ptx::smem_u32(&c.v_full[st]), par, &never, status);
         }
-    } else if (warp == 5) {
+    } else if (warp == MMA_WARP) {
         // ------------------------------------------------------------------------------------ MMA
         if (lane == 0) {
             constexpr uint32_t id_s = f8_idesc(NQ, false), id_o = f8_idesc(NP, true);
-            const uint64_t qd = f8_desc<HD>(ptx::smem_u32(sQ), 16), pd = f8_desc<128>(ptx::smem_u32(sP), 16);
+            const uint64_t qd = f8_desc<HD>(ptx::smem_u32(sQ), 16), pd = p_desc<S::PITCH>(ptx::smem_u32(sP));
             int left = 0, item = 0;
             bool ok = true;
             auto values = [&](int i) {                           // O^T = V^T P^T of tile i
@@ -345,7 +387,7 @@ __global__ void __launch_bounds__(THREADS, Shape<HD, NC, TQ, TP>::CTAS)
                 const uint64_t vd = f8_desc<HD>(ptx::smem_u32(sV + st * S::KV_BYTES), 0);
 #pragma unroll
                 for (int k = 0; k < TK / 32; ++k)
-                    mma_e4m3(tmem + S::O_COL, vd + (uint64_t)(k * 32 * HD >> 4), pd + (uint64_t)(k * 32 >> 4), id_o, k > 0);
+                    mma_e4m3(tmem + S::O_COL, vd + (uint64_t)(k * 32 * HD >> 4), pd + (uint64_t)(k * 32 * S::PITCH >> 4), id_o, k > 0);
                 ptx::mma_commit(ptx::smem_u32(&c.empty[st]));
                 ptx::mma_commit(ptx::smem_u32(&c.o_full));
                 return true;
@@ -382,7 +424,8 @@ __global__ void __launch_bounds__(THREADS, Shape<HD, NC, TQ, TP>::CTAS)
         // ------------------------------------------------------------------------------------ softmax, output
         // A wait that gives up raises `abort`, after which every wait returns at once: these warps then run on to
         // their last tile (their barriers stay in step, the counters stay whole) with results that are not valid.
-        const uint32_t my_lanes = tmem + ((uint32_t)(warp * 32) << 16);
+        const int gr = warp >> 2, quarter = warp & 3, key = tid & 127, c0 = gr * NW;     // this group's first column
+        const uint32_t my_lanes = tmem + ((uint32_t)(quarter * 32) << 16);
         const float to_exp2 = p.a.scale * 1.4426950408889634f;
         int item = 0;
         for (int i = 0; i < count; ++item) {
@@ -393,14 +436,14 @@ __global__ void __launch_bounds__(THREADS, Shape<HD, NC, TQ, TP>::CTAS)
             const T* qbase = (const T*)p.a.q + (int64_t)(q.r0 + q0) * p.a.q_stride + (int64_t)g * p.G * HD;
 
             auto page_of = [&](int t) -> int {                   // page of this thread's key in tile t of the item
-                const int j = t * TK + tid;
+                const int j = t * TK + key;
                 return t < first + n_here && j < q.len ? kv8_page(p.q, s, j >> p.q.shift) : -1;
             };
             int page = page_of(first), page_next = page_of(first + 1);
             float ksc = page >= 0 ? p.ks[(int64_t)page * p.Hkv + g] : 0.f, vsc = page >= 0 ? p.vs[(int64_t)page * p.Hkv + g] : 0.f;
 
             // Q as terms: column r = (query row, head of the group), lane = HD / 32 of its dims
-            for (int r = warp; r < NC; r += 4) {
+            for (int r = warp; r < NC; r += SOFT / 32) {
                 constexpr int E = HD / 32;
                 float x[E];
                 float top = 0.f;
@@ -435,35 +478,39 @@ __global__ void __launch_bounds__(THREADS, Shape<HD, NC, TQ, TP>::CTAS)
             ptx::named_bar_sync(1, SOFT);
             if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&c.q_full));
 
-            float acc[NC], lsum[NC], mrun[NC], alpha[NC], oscale[NC];
+            float acc[NW], lsum[NW];
+            float mrun = -INFINITY;                              // running maximum of column c0 + lane
 #pragma unroll
-            for (int k = 0; k < NC; ++k) {
-                acc[k] = 0.f;
-                lsum[k] = 0.f;
-                mrun[k] = -INFINITY;
-                alpha[k] = 1.f;
-                oscale[k] = 0.f;
-            }
-            // acc = acc * alpha + O of the tile before
-            auto add_tile = [&](int done) {
+            for (int k = 0; k < NW; ++k) acc[k] = lsum[k] = 0.f;
+            // factors of this warp's columns in a tile: [0] running maximum, [1] scale of P, [2] factor of what was summed
+            // before, [3] scale of O
+            auto col = [&](int i_, int what) { return cols_of + (((i_ & 1) * 4 * GR + warp) * 4 + what) * NW; };
+            auto add_tile = [&](int done) {                      // acc = acc * factor + O of a finished tile
                 ptx::mbar_wait(ptx::smem_u32(&c.o_full), done & 1, abort, status);
                 ptx::tc_fence_after();
-                uint32_t o[NP];
+                uint32_t o[TP][NW];
 #pragma unroll
-                for (int k = 0; k < NP; k += 16) ptx::tmem_ld16_issue(my_lanes + S::O_COL + k, o + k);
+                for (int t = 0; t < TP; ++t) tmem_ld_cols<NW>(my_lanes + S::O_COL + t * NC + c0, o[t]);
 #pragma unroll
-                for (int k = 0; k < NP; k += 16) ptx::tmem_ld_wait16(o + k);
+                for (int t = 0; t < TP; ++t) tmem_ld_done<NW>(o[t]);
+                const float4* al = reinterpret_cast<const float4*>(col(done, 2));
+                const float4* os = reinterpret_cast<const float4*>(col(done, 3));
 #pragma unroll
-                for (int k = 0; k < NC; ++k) {
-                    float v = __uint_as_float(o[(TP - 1) * NC + k]);
+                for (int k = 0; k < NW; k += 4) {
+                    const float4 a4 = al[k / 4], o4 = os[k / 4];
+                    const float av[4] = {a4.x, a4.y, a4.z, a4.w}, ov[4] = {o4.x, o4.y, o4.z, o4.w};
 #pragma unroll
-                    for (int t = TP - 2; t >= 0; --t) v = fmaf(v, 0.0625f, __uint_as_float(o[t * NC + k]));
-                    acc[k] = fmaf(v, oscale[k], acc[k] * alpha[k]);
+                    for (int n = 0; n < 4; ++n) {
+                        float v = __uint_as_float(o[TP - 1][k + n]);
+#pragma unroll
+                        for (int t = TP - 2; t >= 0; --t) v = fmaf(v, 0.0625f, __uint_as_float(o[t][k + n]));
+                        acc[k + n] = fmaf(v, ov[n], acc[k + n] * av[n]);
+                    }
                 }
             };
 
             for (int t = first; t < first + n_here; ++t, ++i) {
-                const int b = i & 1, j = t * TK + tid;
+                const int b = i & 1, j = t * TK + key;
                 const bool have = page >= 0;
                 const float ks_now = ksc, vs_now = vsc;
                 // the next tile's scales and the page after it, while this one is worked on
@@ -474,104 +521,111 @@ __global__ void __launch_bounds__(THREADS, Shape<HD, NC, TQ, TP>::CTAS)
 
                 ptx::mbar_wait(ptx::smem_u32(&c.s_full[b]), (i >> 1) & 1, abort, status);
                 ptx::tc_fence_after();
-                float x[NC];
+                float x[NW];
                 {
-                    uint32_t w[NQ];
+                    uint32_t w[TQ][NW];
 #pragma unroll
-                    for (int k = 0; k < NQ; k += 16) ptx::tmem_ld16_issue(my_lanes + b * NQ + k, w + k);
+                    for (int n = 0; n < TQ; ++n) tmem_ld_cols<NW>(my_lanes + b * NQ + n * NC + c0, w[n]);
 #pragma unroll
-                    for (int k = 0; k < NQ; k += 16) ptx::tmem_ld_wait16(w + k);
+                    for (int n = 0; n < TQ; ++n) tmem_ld_done<NW>(w[n]);
                     ptx::tc_fence_before();
                     __syncwarp();
                     if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&c.s_free[b]));
 #pragma unroll
-                    for (int k = 0; k < NC; ++k) {
-                        float v = __uint_as_float(w[(TQ - 1) * NC + k]);
+                    for (int k = 0; k < NW; ++k) {
+                        float v = __uint_as_float(w[TQ - 1][k]);
 #pragma unroll
-                        for (int n = TQ - 2; n >= 0; --n) v = fmaf(v, 0.0625f, __uint_as_float(w[n * NC + k]));
-                        x[k] = v * (ks_now * qscale[k]);
+                        for (int n = TQ - 2; n >= 0; --n) v = fmaf(v, 0.0625f, __uint_as_float(w[n][k]));
+                        x[k] = v * (ks_now * qscale[c0 + k]);
                     }
                 }
                 // column k (query row k / G) sees key j from its own position on: k >= (j - pos0) G
-                const int hidden = have ? min(max(j - pos0, 0), NC) * p.G : NC;
+                const int hidden = have ? min(max(j - pos0, 0), NC) * p.G - c0 : NC;
                 if (hidden > 0) {
 #pragma unroll
-                    for (int k = 0; k < NC; ++k)
+                    for (int k = 0; k < NW; ++k)
                         if (k < hidden) x[k] = -INFINITY;
                 }
                 if (p.scores) {
 #pragma unroll
-                    for (int k = 0; k < NC; ++k)
-                        if (k < cols)
-                            p.scores[((int64_t)(q.r0 + q0 + k / p.G) * p.Hq + g * p.G + k % p.G) * p.score_ld + j] = x[k];
+                    for (int k = 0; k < NW; ++k)
+                        if (c0 + k < cols)
+                            p.scores[((int64_t)(q.r0 + q0 + (c0 + k) / p.G) * p.Hq + g * p.G + (c0 + k) % p.G) * p.score_ld + j] = x[k];
                 }
                 // maxima over the tile's keys of the scores, and of scores with V's scale: y = x + log2(scale), which says
                 // how far a column's P can be scaled up.  A warp's keys lie in one block unless pages have 16 rows.
-                float* wm = wmax + b * 4 * NC;
-                float* wy = ymax + b * 4 * NC;
+                float* wm = wmax + ((b * GR + gr) * 4) * NW;
+                float* wy = ymax + ((b * GR + gr) * 4) * NW;
                 const float ev = have && vs_now > 0.f ? (float)((int)(__float_as_uint(vs_now) >> 23) - 127) : -INFINITY;
-                if (p.box >= 32) {
-                    const float ew = redux_max(ev);
+                const float ew = redux_max(ev);
 #pragma unroll
-                    for (int k = 0; k < NC; ++k) {
-                        const float m = redux_max(x[k]);
-                        if (lane == 0) {
-                            wm[warp * NC + k] = m;
-                            wy[warp * NC + k] = m + ew;
-                        }
+                for (int k = 0; k < NW; k += 4) {
+                    float m[4], y[4];
+#pragma unroll
+                    for (int n = 0; n < 4; ++n) {
+                        m[n] = redux_max(x[k + n]);
+                        y[n] = p.box >= 32 ? m[n] + ew : redux_max(x[k + n] + ev);
                     }
-                } else {
-#pragma unroll
-                    for (int k = 0; k < NC; ++k) {
-                        const float m = redux_max(x[k]), y = redux_max(x[k] + ev);
-                        if (lane == 0) {
-                            wm[warp * NC + k] = m;
-                            wy[warp * NC + k] = y;
-                        }
+                    if (lane == 0) {
+                        *reinterpret_cast<float4*>(wm + quarter * NW + k) = make_float4(m[0], m[1], m[2], m[3]);
+                        *reinterpret_cast<float4*>(wy + quarter * NW + k) = make_float4(y[0], y[1], y[2], y[3]);
                     }
                 }
-                ptx::named_bar_sync(1, SOFT);
-                float a_now[NC], os_now[NC];
-#pragma unroll
-                for (int k = 0; k < NC; ++k) {
-                    const float mt = fmaxf(fmaxf(wm[k], wm[NC + k]), fmaxf(wm[2 * NC + k], wm[3 * NC + k]));
-                    const float yt = fmaxf(fmaxf(wy[k], wy[NC + k]), fmaxf(wy[2 * NC + k], wy[3 * NC + k]));
-                    const float mn = fmaxf(mrun[k], mt), ref = mn == -INFINITY ? 0.f : mn;
-                    a_now[k] = mn == mrun[k] ? 1.f : exp2_fast(mrun[k] - ref);
-                    mrun[k] = mn;
-                    const float e = exp2_fast(x[k] - ref);
-                    lsum[k] = fmaf(lsum[k], a_now[k], e);
+                ptx::named_bar_sync(2 + gr, 128);
+                if (lane < NW) {
+                    const float mt = fmaxf(fmaxf(wm[lane], wm[NW + lane]), fmaxf(wm[2 * NW + lane], wm[3 * NW + lane]));
+                    const float yt = fmaxf(fmaxf(wy[lane], wy[NW + lane]), fmaxf(wy[2 * NW + lane], wy[3 * NW + lane]));
+                    const float mn = fmaxf(mrun, mt), ref = mn == -INFINITY ? 0.f : mn;
                     // P of the column times V's scale, scaled by the power of two that brings its largest value to 128 .. 256
                     const int up = 8 + (yt == -INFINITY ? 0 : (int)floorf(fminf(fmaxf(ref - yt, -118.f), 118.f)));
-                    x[k] = e * (have ? vs_now * __uint_as_float((unsigned)(127 + up) << 23) : 0.f);
-                    os_now[k] = __uint_as_float((unsigned)(127 - up) << 23);
+                    col(i, 0)[lane] = ref;
+                    col(i, 1)[lane] = __uint_as_float((unsigned)(127 + up) << 23);
+                    col(i, 2)[lane] = mn == mrun ? 1.f : exp2_fast(mrun - ref);
+                    col(i, 3)[lane] = __uint_as_float((unsigned)(127 - up) << 23);
+                    mrun = mn;
+                }
+                __syncwarp();
+                const float v_mul = have ? vs_now : 0.f;
+#pragma unroll
+                for (int k = 0; k < NW; k += 4) {
+                    const float4 r4 = *reinterpret_cast<const float4*>(col(i, 0) + k), p4 = *reinterpret_cast<const float4*>(col(i, 1) + k),
+                                 a4 = *reinterpret_cast<const float4*>(col(i, 2) + k);
+                    const float rv[4] = {r4.x, r4.y, r4.z, r4.w}, pv[4] = {p4.x, p4.y, p4.z, p4.w}, av[4] = {a4.x, a4.y, a4.z, a4.w};
+#pragma unroll
+                    for (int n = 0; n < 4; ++n) {
+                        const float e = exp2_fast(x[k + n] - rv[n]);
+                        lsum[k + n] = fmaf(lsum[k + n], av[n], e);
+                        x[k + n] = e * (v_mul * pv[n]);
+                    }
                 }
                 if (t > first) add_tile(i - 1);
-                // P as terms, one byte per column and term (sP is free: O of the tile before is complete)
+                // P as terms (sP is free: O of the tile before is complete)
 #pragma unroll
-                for (int k = 0; k < NC; k += 2) {
-                    alpha[k] = a_now[k];
-                    alpha[k + 1] = a_now[k + 1];
-                    oscale[k] = os_now[k];
-                    oscale[k + 1] = os_now[k + 1];
+                for (int n = 0; n < TP; ++n) {
+                    uint32_t w[NW / 4];
 #pragma unroll
-                    for (int n = 0; n < TP; ++n) {
-                        const uint32_t c2 = kv8_code2(x[k], x[k + 1]);
-                        const float2 v = kv8_value2(c2);
-                        x[k] = (x[k] - v.x) * 16.f;
-                        x[k + 1] = (x[k + 1] - v.y) * 16.f;
-                        sP[f8_at<TK>(n * NC + k, tid)] = (uint8_t)c2;
-                        sP[f8_at<TK>(n * NC + k + 1, tid)] = (uint8_t)(c2 >> 8);
+                    for (int k = 0; k < NW; k += 4) {
+                        const uint32_t lo = kv8_code2(x[k], x[k + 1]), hi = kv8_code2(x[k + 2], x[k + 3]);
+                        w[k / 4] = lo | (hi << 16);
+                        const float2 u = kv8_value2(lo), v = kv8_value2(hi);
+                        x[k] = (x[k] - u.x) * 16.f;
+                        x[k + 1] = (x[k + 1] - u.y) * 16.f;
+                        x[k + 2] = (x[k + 2] - v.x) * 16.f;
+                        x[k + 3] = (x[k + 3] - v.y) * 16.f;
                     }
+                    uint8_t* d = sP + p_at<S::PITCH>(key, n * NC + c0);
+                    if constexpr (NW == 4) *reinterpret_cast<uint32_t*>(d) = w[0];
+                    else if constexpr (NW == 8) *reinterpret_cast<uint2*>(d) = make_uint2(w[0], w[1]);
+                    else *reinterpret_cast<uint4*>(d) = make_uint4(w[0], w[1], w[2], w[3]);
                 }
                 // V rows that no weight may meet: one that was not loaded or lies behind the sequence is zeroed (0 times
                 // NaN would be NaN); in one that only later query rows see, NaN codes are taken out and remembered
-                if (!have || (j > pos0 && q.n > 1)) {
+                if (gr == 0 && (!have || (j > pos0 && q.n > 1))) {
                     const int st = i % STAGES;
                     ptx::mbar_wait(ptx::smem_u32(&c.v_full[st]), (i / STAGES) & 1, abort, status);
                     uint8_t* row = sV + st * S::KV_BYTES;
                     for (int d = 0; d < HD; d += 16) {
-                        uint4* v = reinterpret_cast<uint4*>(row + f8_at<HD>(tid, d));
+                        uint4* v = reinterpret_cast<uint4*>(row + f8_at<HD>(key, d));
                         if (!have) {
                             *v = make_uint4(0, 0, 0, 0);
                         } else {
@@ -594,81 +648,110 @@ __global__ void __launch_bounds__(THREADS, Shape<HD, NC, TQ, TP>::CTAS)
             add_tile(i - 1);
             ptx::tc_fence_before();
 #pragma unroll
-            for (int k = 0; k < NC; ++k) {
+            for (int k = 0; k < NW; ++k) {
                 const float v = warp_sum(lsum[k]);
-                if (lane == 0) wsum[warp * NC + k] = v;
+                if (lane == 0) wsum[quarter * NC + c0 + k] = v;
             }
-            ptx::named_bar_sync(1, SOFT);
+            if (quarter == 0 && lane < NW) colm[c0 + lane] = mrun;
+            ptx::named_bar_sync(1, SOFT);                        // sums, maxima and nan_from of all groups
 #pragma unroll
-            for (int k = 0; k < NC; ++k) lsum[k] = (wsum[k] + wsum[NC + k]) + (wsum[2 * NC + k] + wsum[3 * NC + k]);
-            if (tid < HD && nan_from[tid] != INT_MAX) {
-                const int k0 = (nan_from[tid] - pos0) * p.G;     // columns from the row that sees the NaN on
+            for (int k = 0; k < NW; ++k) {
+                const float* w = wsum + c0 + k;
+                lsum[k] = (w[0] + w[NC]) + (w[2 * NC] + w[3 * NC]);
+            }
+            if (key < HD && nan_from[key] != INT_MAX) {
+                const int k0 = (nan_from[key] - pos0) * p.G - c0;        // columns from the row that sees the NaN on
 #pragma unroll
-                for (int k = 0; k < NC; ++k)
+                for (int k = 0; k < NW; ++k)
                     if (k >= k0) acc[k] = __int_as_float(0x7fc00000);
             }
-            bool mine = true;                                    // this CTA writes the item's result
-            if (first > 0 || first + n_here < cur.nt) {
-                constexpr int PIECE = NC * (HD + 2);
-                const long long begin = t0 + (i - n_here) - first;           // the item's first tile in the list
-                const int c_first = (int)(begin / per), c_last = (int)((begin + cur.nt - 1) / per);
-                float* piece = p.part + (int64_t)(blockIdx.x * 2 + (first > 0 ? 0 : 1)) * PIECE;
-                if (tid < HD) {
+            const auto out_at = [&](int k) {                     // output row of column k
+                return (T*)p.a.out + (int64_t)(q.r0 + q0 + k / p.G) * p.a.out_stride + (int64_t)(g * p.G + k % p.G) * HD;
+            };
+            const auto stat_at = [&](int k) { return p.stats + (int64_t)(q.r0 + q0 + k / p.G) * p.Hq + g * p.G + k % p.G; };
+            if (first == 0 && n_here == cur.nt) {
 #pragma unroll
-                    for (int k = 0; k < NC; ++k) piece[k * HD + tid] = acc[k];
+                for (int k = 0; k < NW; ++k) {
+                    if (c0 + k >= cols) continue;
+                    const float inv = 1.f / lsum[k];
+                    if (key < HD) out_at(c0 + k)[key] = from_f<T>(pos0 + (c0 + k) / p.G >= 0 ? acc[k] * inv : 0.f);
+                    if (p.scores && key == 0) *stat_at(c0 + k) = make_float2(colm[c0 + k], inv);
                 }
-                if (tid == 0) {
+            } else {
+                const long long begin = t0 + (i - n_here) - first;           // the item's first tile in the list
+                const int u0 = (int)(begin / per), n_pieces = (int)((begin + cur.nt - 1) / per) - u0 + 1;
+                const auto piece_at = [&](int u) { return p.part + (int64_t)((u0 + u) * 2 + (u == 0 ? 1 : 0)) * S::PIECE; };
+                float* piece = piece_at(blockIdx.x - u0);
+                if (key < HD) {
 #pragma unroll
-                    for (int k = 0; k < NC; ++k) {
-                        piece[NC * HD + 2 * k] = mrun[k];
-                        piece[NC * HD + 2 * k + 1] = lsum[k];
-                    }
+                    for (int k = 0; k < NW; ++k) piece[(c0 + k) * HD + key] = acc[k];
+                }
+                if (key == 0) {
+#pragma unroll
+                    for (int k = 0; k < NW; ++k)
+                        *reinterpret_cast<float2*>(piece + NC * HD + 2 * (c0 + k)) = make_float2(colm[c0 + k], lsum[k]);
                 }
                 __threadfence();
                 ptx::named_bar_sync(1, SOFT);
                 if (tid == 0) {
-                    const unsigned n = (unsigned)(c_last - c_first + 1);
-                    c.last = atomicAdd(p.arrived + c_first, 1u) == n - 1;
-                    if (c.last) atomicExch(p.arrived + c_first, 0u);
+                    c.last = atomicAdd(p.arrived + u0, 1u) == (unsigned)n_pieces - 1;
+                    if (c.last) atomicExch(p.arrived + u0, 0u);
                     __threadfence();
                 }
                 ptx::named_bar_sync(1, SOFT);
-                mine = c.last != 0;
-                if (mine) {                                      // join the pieces in their order
+                if (c.last) {                                    // join the pieces in their order, a warp per column
+                    constexpr int LANES = HD / 4, SIDE = 32 / LANES;         // lanes of a row; rows side by side
+                    const int side = lane / LANES, d = (lane % LANES) * 4;
+                    for (int k = warp; k < cols; k += SOFT / 32) {
+                        float m = -INFINITY;
+                        for (int u = lane; u < n_pieces; u += 32) m = fmaxf(m, __ldcg(piece_at(u) + NC * HD + 2 * k));
+                        m = warp_max(m);
+                        float l = 0.f;
+                        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+                        for (int ub = 0; ub < n_pieces; ub += 32) {
+                            float f = 0.f;
+                            if (ub + lane < n_pieces) {
+                                const float2 ml = __ldcg(reinterpret_cast<const float2*>(piece_at(ub + lane) + NC * HD + 2 * k));
+                                f = ml.x == -INFINITY ? 0.f : exp2_fast(ml.x - m);
+                                l = fmaf(ml.y, f, l);
+                            }
+                            const int n = min(32, n_pieces - ub);
+                            for (int v0 = 0; v0 < n; v0 += 8 * SIDE) {
+                                float4 o[8];
 #pragma unroll
-                    for (int k = 0; k < NC; ++k) {
-                        acc[k] = 0.f;
-                        lsum[k] = 0.f;
-                        mrun[k] = -INFINITY;
-                    }
-                    for (int u = c_first; u <= c_last; ++u) {
-                        const float* o = p.part + (int64_t)(u * 2 + (u == c_first ? 1 : 0)) * PIECE;
+                                for (int v = 0; v < 8; ++v) {
+                                    const int u = v0 + v * SIDE + side;
+                                    o[v] = u < n ? __ldcg(reinterpret_cast<const float4*>(piece_at(ub + u) + k * HD + d))
+                                                 : make_float4(0.f, 0.f, 0.f, 0.f);
+                                }
 #pragma unroll
-                        for (int k = 0; k < NC; ++k) mrun[k] = fmaxf(mrun[k], __ldcg(o + NC * HD + 2 * k));
-                    }
-                    for (int u = c_first; u <= c_last; ++u) {
-                        const float* o = p.part + (int64_t)(u * 2 + (u == c_first ? 1 : 0)) * PIECE;
-#pragma unroll
-                        for (int k = 0; k < NC; ++k) {
-                            const float2 ml = __ldcg(reinterpret_cast<const float2*>(o + NC * HD + 2 * k));
-                            const float f = ml.x == -INFINITY ? 0.f : exp2_fast(ml.x - mrun[k]);
-                            lsum[k] = fmaf(ml.y, f, lsum[k]);
-                            if (tid < HD) acc[k] = fmaf(__ldcg(o + k * HD + tid), f, acc[k]);
+                                for (int v = 0; v < 8; ++v) {
+                                    const float w = __shfl_sync(0xffffffffu, f, (v0 + v * SIDE + side) & 31);
+                                    a.x = fmaf(o[v].x, w, a.x);
+                                    a.y = fmaf(o[v].y, w, a.y);
+                                    a.z = fmaf(o[v].z, w, a.z);
+                                    a.w = fmaf(o[v].w, w, a.w);
+                                }
+                            }
                         }
+                        l = warp_sum(l);
+                        if (SIDE == 2) {
+                            a.x += __shfl_xor_sync(0xffffffffu, a.x, 16);
+                            a.y += __shfl_xor_sync(0xffffffffu, a.y, 16);
+                            a.z += __shfl_xor_sync(0xffffffffu, a.z, 16);
+                            a.w += __shfl_xor_sync(0xffffffffu, a.w, 16);
+                        }
+                        const float inv = 1.f / l;
+                        const bool sees = pos0 + k / p.G >= 0;
+                        if (side == 0) {
+                            T* o = out_at(k) + d;
+                            o[0] = from_f<T>(sees ? a.x * inv : 0.f);
+                            o[1] = from_f<T>(sees ? a.y * inv : 0.f);
+                            o[2] = from_f<T>(sees ? a.z * inv : 0.f);
+                            o[3] = from_f<T>(sees ? a.w * inv : 0.f);
+                        }
+                        if (p.scores && lane == 0) *stat_at(k) = make_float2(m, inv);
                     }
-                }
-            }
-            if (mine) {
-#pragma unroll
-                for (int k = 0; k < NC; ++k) {
-                    if (k >= cols) continue;
-                    const int row = k / p.G, h = k % p.G;
-                    const float inv = 1.f / lsum[k];
-                    if (tid < HD)
-                        ((T*)p.a.out)[(int64_t)(q.r0 + q0 + row) * p.a.out_stride + (int64_t)(g * p.G + h) * HD + tid] =
-                            from_f<T>(pos0 + row >= 0 ? acc[k] * inv : 0.f);
-                    if (p.scores && tid == 0)
-                        p.stats[(int64_t)(q.r0 + q0 + row) * p.Hq + g * p.G + h] = make_float2(mrun[k], inv);
                 }
             }
             if (i < count) cur.next_item(p);
@@ -676,7 +759,7 @@ __global__ void __launch_bounds__(THREADS, Shape<HD, NC, TQ, TP>::CTAS)
     }
     ptx::tc_fence_before();
     __syncthreads();
-    if (warp == 5) {
+    if (warp == MMA_WARP) {
         ptx::tc_fence_after();
         ptx::tmem_dealloc(tmem, S::TMEM);
     }
@@ -700,41 +783,51 @@ __global__ void __launch_bounds__(128) kv8_weights_kernel(const AttnArgs p) {
     *dst = p.a.add ? *dst + w : w;
 }
 
-template <typename T, int HD, int NC, int TQ, int TP>
+template <typename T, typename S>
 cudaError_t launch_shape(const Kv8& c, AttnArgs& p, cudaStream_t s) {
-    using S = Shape<HD, NC, TQ, TP>;
     static std::atomic<uint64_t> done{0};
-    const cudaError_t e = smem_limit_once(kv8_attn_kernel<T, HD, NC, TQ, TP>, S::BYTES, done);
+    const cudaError_t e = smem_limit_once(kv8_attn_kernel<T, S>, S::BYTES, done);
     if (e != cudaSuccess) return e;
-    p.QT = NC / p.G;
+    p.QT = S::NC / p.G;
     const int64_t items = ((int64_t)p.r.n_rows / p.QT + p.q.n) * p.Hkv;
     const int64_t tiles = items * ((p.q.max_len + TK - 1) / TK + 1);
     const int64_t most = (int64_t)c.num_sms * S::CTAS;
     CUtensorMap map;
     memcpy(&map, c.map, sizeof map);
-    kv8_attn_kernel<T, HD, NC, TQ, TP><<<(int)(tiles < most ? tiles : most), THREADS, S::BYTES, s>>>(map, p);
+    kv8_attn_kernel<T, S><<<(int)(tiles < most ? tiles : most), S::THREADS, S::BYTES, s>>>(map, p);
     return cudaGetLastError();
 }
+
+//                           columns, groups, terms of q and P, CTAs per SM, stages
+template <int HD> using C4 = Shape<HD, 4, 1, 2, 3, 3, 2>;
+template <int HD> using C8 = Shape<HD, 8, 1, 2, 3, 3, 2>;
+template <int HD> using C16 = Shape<HD, 16, 2, 2, 3, 2, 2>;
+template <int HD> using C32 = Shape<HD, 32, 4, 2, 3, 1, 3>;
+template <int HD> using C64 = Shape<HD, 64, 4, 2, 3, 1, 3>;
+template <int HD> using F4 = Shape<HD, 4, 1, 6, 6, 3, 2>;
+template <int HD> using F8 = Shape<HD, 8, 1, 6, 6, 2, 2>;
 
 template <int HD> cudaError_t launch_dim(const Kv8& c, AttnArgs& p, cudaStream_t s) {
     // query columns per item: what a sequence's rows need on average, within what tensor memory holds
     const int rows = (p.r.n_rows + p.q.n - 1) / p.q.n, need = rows * p.G;
     if (c.cfg.dtype == CB_BF16) {
-        if (need <= 4) return launch_shape<bf16, HD, 4, 2, 3>(c, p, s);
-        if (need <= 8) return launch_shape<bf16, HD, 8, 2, 3>(c, p, s);
-        if (need <= 16) return launch_shape<bf16, HD, 16, 2, 3>(c, p, s);
-        return launch_shape<bf16, HD, 32, 2, 3>(c, p, s);
+        if (need <= 4) return launch_shape<bf16, C4<HD>>(c, p, s);
+        if (need <= 8) return launch_shape<bf16, C8<HD>>(c, p, s);
+        if (need <= 16) return launch_shape<bf16, C16<HD>>(c, p, s);
+        if (need <= 32) return launch_shape<bf16, C32<HD>>(c, p, s);
+        return launch_shape<bf16, C64<HD>>(c, p, s);
     }
-    return need <= 4 ? launch_shape<float, HD, 4, 6, 6>(c, p, s) : launch_shape<float, HD, 8, 6, 6>(c, p, s);
+    return need <= 4 ? launch_shape<float, F4<HD>>(c, p, s) : launch_shape<float, F8<HD>>(c, p, s);
 }
 
 }  // namespace
 
+// scratch: two pieces for every CTA of the largest launch
+template <typename S> constexpr size_t pieces() { return (size_t)S::CTAS * 2 * S::PIECE; }
 size_t kv8_part_floats(int num_sms) {
-    size_t most = 0;
-    const size_t shapes[][2] = {{3, 8}, {2, 16}, {2, 32}};               // CTAs per SM, columns
-    for (auto& s : shapes) most = s[0] * s[1] > most ? s[0] * s[1] : most;
-    return most * num_sms * 2 * (128 + 2);
+    const size_t sizes[] = {pieces<C4<128>>(), pieces<C8<128>>(), pieces<C16<128>>(), pieces<C32<128>>(), pieces<C64<128>>(),
+                            pieces<F4<128>>(), pieces<F8<128>>()};
+    return *std::max_element(std::begin(sizes), std::end(sizes)) * num_sms;
 }
 int kv8_most_ctas(int num_sms) { return 3 * num_sms; }
 
