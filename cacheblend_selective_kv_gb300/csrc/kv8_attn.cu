@@ -55,9 +55,9 @@ struct AttnArgs {
     int min_tiles;                       // tiles per CTA, at least
     float* part;                         // [cta][2][NC][HD + 2] pieces of items that span CTAs
     unsigned* arrived;                   // [cta] pieces finished of the item that begins in this CTA (0 between calls)
-    float* scores;                       // weights: [n_q][Hq][score_ld] scores in the exp2 domain
+    float* scores;                       // weights: [Hkv][n_q][G][score_ld] scores in the exp2 domain
     int score_ld;
-    float2* stats;                       // weights: [n_q][Hq] (max, 1 / sum)
+    float2* stats;                       // weights: [Hkv][n_q][G] (max, 1 / sum)
 };
 
 constexpr int round16(int x) { return (x + 15) / 16 * 16; }
@@ -433,6 +433,7 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
             const Seq q = cur.q;
             const int q0 = cur.qt * p.QT, rows = min(p.QT, q.n - q0), cols = rows * p.G;
             const int pos0 = q.len - q.n + q0;                   // position of the item's first query row
+            const int64_t stat0 = ((int64_t)g * p.r.n_rows + q.r0 + q0) * p.G;     // the item's first column in scores, stats
             const T* qbase = (const T*)p.a.q + (int64_t)(q.r0 + q0) * p.a.q_stride + (int64_t)g * p.G * HD;
 
             auto page_of = [&](int t) -> int {                   // page of this thread's key in tile t of the item
@@ -547,10 +548,11 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
                         if (k < hidden) x[k] = -INFINITY;
                 }
                 if (p.scores) {
+                    float* score = p.scores + (stat0 + c0) * p.score_ld + j;
 #pragma unroll
                     for (int k = 0; k < NW; ++k)
                         if (c0 + k < cols)
-                            p.scores[((int64_t)(q.r0 + q0 + (c0 + k) / p.G) * p.Hq + g * p.G + (c0 + k) % p.G) * p.score_ld + j] = x[k];
+                            score[(int64_t)k * p.score_ld] = x[k];
                 }
                 // maxima over the tile's keys of the scores, and of scores with V's scale: y = x + log2(scale), which says
                 // how far a column's P can be scaled up.  A warp's keys lie in one block unless pages have 16 rows.
@@ -668,14 +670,13 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
             const auto out_at = [&](int k) {                     // output row of column k
                 return (T*)p.a.out + (int64_t)(q.r0 + q0 + k / p.G) * p.a.out_stride + (int64_t)(g * p.G + k % p.G) * HD;
             };
-            const auto stat_at = [&](int k) { return p.stats + (int64_t)(q.r0 + q0 + k / p.G) * p.Hq + g * p.G + k % p.G; };
             if (first == 0 && n_here == cur.nt) {
 #pragma unroll
                 for (int k = 0; k < NW; ++k) {
                     if (c0 + k >= cols) continue;
                     const float inv = 1.f / lsum[k];
                     if (key < HD) out_at(c0 + k)[key] = from_f<T>(pos0 + (c0 + k) / p.G >= 0 ? acc[k] * inv : 0.f);
-                    if (p.scores && key == 0) *stat_at(c0 + k) = make_float2(colm[c0 + k], inv);
+                    if (p.scores && key == 0) p.stats[stat0 + c0 + k] = make_float2(colm[c0 + k], inv);
                 }
             } else {
                 const long long begin = t0 + (i - n_here) - first;           // the item's first tile in the list
@@ -750,7 +751,7 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
                             o[2] = from_f<T>(sees ? a.z * inv : 0.f);
                             o[3] = from_f<T>(sees ? a.w * inv : 0.f);
                         }
-                        if (p.scores && lane == 0) *stat_at(k) = make_float2(m, inv);
+                        if (p.scores && lane == 0) p.stats[stat0 + k] = make_float2(m, inv);
                     }
                 }
             }
@@ -765,22 +766,34 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
     }
 }
 
-// weights[s][g][j] = sum over the sequence's rows and the group's heads of exp2(score - max) / sum, in row order
-__global__ void __launch_bounds__(128) kv8_weights_kernel(const AttnArgs p) {
-    const int j = blockIdx.x * 128 + threadIdx.x, g = blockIdx.y;
+// weights[s][g][j] = sum over the sequence's rows and the group's heads of exp2(score - max) / sum: four sums of every
+// fourth column, joined in order
+__global__ void __launch_bounds__(512) kv8_weights_kernel(const AttnArgs p) {
+    __shared__ float part[4][128];
+    const int j = blockIdx.x * 128 + threadIdx.x, y = threadIdx.y, g = blockIdx.y;
     const Seq q = seq_at(p, blockIdx.z);
-    if (j >= q.len) return;
+    if (blockIdx.x * 128 >= q.len) return;
     float w = 0.f;
-    for (int i = max(0, j - (q.len - q.n)); i < q.n; ++i) {
-        const int64_t at = (int64_t)(q.r0 + i) * p.Hq + g * p.G;
-        for (int h = 0; h < p.G; ++h) {
-            const float x = p.scores[(at + h) * p.score_ld + j];
-            const float2 st = p.stats[at + h];
-            w += x == -INFINITY ? 0.f : exp2_fast(x - st.x) * st.y;
+    if (j < q.len) {
+        const int64_t at = ((int64_t)g * p.r.n_rows + q.r0) * p.G;
+        const float* score = p.scores + at * p.score_ld + j;
+        const float2* st = p.stats + at;
+        const int seen = max(0, j - (q.len - q.n)) * p.G, cols = q.n * p.G;      // columns that see key j: [seen, cols)
+#pragma unroll 8
+        for (int k = (seen & ~3) + y; k < cols; k += 4) {
+            if (k < seen) continue;
+            const float x = __ldcs(score + (int64_t)k * p.score_ld);
+            const float2 m = st[k];
+            w += x == -INFINITY ? 0.f : exp2_fast(x - m.x) * m.y;
         }
     }
-    float* dst = p.a.weights + ((int64_t)blockIdx.z * p.Hkv + g) * p.a.weights_ld + j;
-    *dst = p.a.add ? *dst + w : w;
+    part[y][threadIdx.x] = w;
+    __syncthreads();
+    if (y == 0 && j < q.len) {
+        w = (part[0][threadIdx.x] + part[1][threadIdx.x]) + (part[2][threadIdx.x] + part[3][threadIdx.x]);
+        float* dst = p.a.weights + ((int64_t)blockIdx.z * p.Hkv + g) * p.a.weights_ld + j;
+        *dst = p.a.add ? *dst + w : w;
+    }
 }
 
 template <typename T, typename S>
@@ -874,7 +887,7 @@ cudaError_t launch_kv8_attention(const Kv8& c, const Kv8Seqs& q, const Kv8Rows& 
         if (e != cudaSuccess) return e;
     }
     if (a.weights && q.max_len > 0)
-        kv8_weights_kernel<<<dim3((q.max_len + 127) / 128, Hkv, q.n), 128, 0, s>>>(p);
+        kv8_weights_kernel<<<dim3((q.max_len + 127) / 128, Hkv, q.n), dim3(128, 4), 0, s>>>(p);
     return cudaGetLastError();
 }
 

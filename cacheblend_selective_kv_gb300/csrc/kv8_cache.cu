@@ -73,20 +73,31 @@ __device__ __forceinline__ bool kv8_block(const Kv8Seqs& q, const Kv8Rows& r, in
 }
 
 // maximum over the TPB threads of a group (TPB a power of two from 32 to 256)
-__device__ __forceinline__ float group_max(float v, int tpb, float* sm) {
-    v = warp_max(v);
+__device__ __forceinline__ unsigned group_max(unsigned v, int tpb, unsigned* sm) {
+    v = __reduce_max_sync(0xffffffffu, v);
     if (tpb == 32) return v;
     const int warp = threadIdx.x >> 5, per = tpb >> 5, g0 = warp / per * per;
     if ((threadIdx.x & 31) == 0) sm[warp] = v;
     __syncthreads();
     v = sm[g0];
-    for (int i = 1; i < per; ++i) v = fmaxf(v, sm[g0 + i]);
+    for (int i = 1; i < per; ++i) v = max(v, sm[g0 + i]);
     return v;
 }
 
-template <typename T> struct Vec;                      // 16 bytes of a row
+// 16 bytes of a row.  Magnitudes compare as integers, so the largest is found on the packed words; the bits of an
+// infinity or a NaN are above every finite number's, which is how a block that holds one is noticed.
+template <typename T> struct Vec;
 template <> struct Vec<bf16> {
     static constexpr int N = 8;
+    static constexpr unsigned INF = 0x7f80u;
+    __device__ static unsigned top(const uint4& u, unsigned m) {           // two running maxima in m
+        m = __vmaxu2(m, u.x & 0x7fff7fffu);
+        m = __vmaxu2(m, u.y & 0x7fff7fffu);
+        m = __vmaxu2(m, u.z & 0x7fff7fffu);
+        return __vmaxu2(m, u.w & 0x7fff7fffu);
+    }
+    __device__ static unsigned joined(unsigned m) { return max(m & 0xffffu, m >> 16); }
+    __device__ static float value(unsigned bits) { return __uint_as_float(bits << 16); }
     __device__ static void get(const uint4& u, float* f) {
         const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
@@ -98,6 +109,13 @@ template <> struct Vec<bf16> {
 };
 template <> struct Vec<float> {
     static constexpr int N = 4;
+    static constexpr unsigned INF = 0x7f800000u;
+    __device__ static unsigned top(const uint4& u, unsigned m) {
+        m = max(m, max(u.x & 0x7fffffffu, u.y & 0x7fffffffu));
+        return max(m, max(u.z & 0x7fffffffu, u.w & 0x7fffffffu));
+    }
+    __device__ static unsigned joined(unsigned m) { return m; }
+    __device__ static float value(unsigned bits) { return __uint_as_float(bits); }
     __device__ static void get(const uint4& u, float* f) {
         f[0] = __uint_as_float(u.x);
         f[1] = __uint_as_float(u.y);
@@ -115,49 +133,64 @@ struct CacheArgs {
     float* scales;
     int per_seq, units;       // units = slots * Hkv
     int Hkv, hd, layer;
-    int tpb;                  // threads of a block's group
+    int tpb_shift;            // log2 of the threads of a block's group
+    int vpr_shift;            // log2 of the vectors of a row
 };
 
+// NP vectors per thread: vector t + i * tpb of the block, tpb / vpr rows apart
 template <typename T, int NP>
 __global__ void __launch_bounds__(THREADS) kv8_write_kernel(const CacheArgs a) {
     constexpr int VN = Vec<T>::N;
-    __shared__ float sm[2][THREADS / 32];
-    const int groups = THREADS / a.tpb, group = threadIdx.x / a.tpb, t = threadIdx.x - group * a.tpb;
-    const int unit = blockIdx.x * groups + group;
+    __shared__ unsigned sm[THREADS / 32];
+    const int tpb = 1 << a.tpb_shift, group = threadIdx.x >> a.tpb_shift, t = threadIdx.x & (tpb - 1);
+    const int unit = blockIdx.x * (THREADS >> a.tpb_shift) + group;
     const int lk = blockIdx.y, kv = lk & 1, l = lk >> 1;
-    const int P = 1 << a.q.shift, vpr = a.hd / VN;     // vectors per row
+    const int P = 1 << a.q.shift;
     Block b{};
     const int slot = unit / a.Hkv, head = unit - slot * a.Hkv;
     const bool live = unit < a.units && kv8_block(a.q, a.r, a.per_seq, slot, b);
-    uint4 x[NP];
-    float top = 0.f;
-    const T* src = (const T*)a.src[kv] + l * a.layer_stride + (int64_t)head * a.hd;
-#pragma unroll
-    for (int i = 0; i < NP; ++i) {
-        const int v = t + i * a.tpb, row = v / vpr, e = v - row * vpr;
-        x[i] = make_uint4(0, 0, 0, 0);
-        if (live && row >= b.lo && row < b.hi)
-            x[i] = *reinterpret_cast<const uint4*>(src + (int64_t)(b.src_row + row - b.lo) * a.row_stride + e * VN);
-    }
-#pragma unroll
-    for (int i = 0; i < NP; ++i) {
-        float f[VN];
-        Vec<T>::get(x[i], f);
-#pragma unroll
-        for (int k = 0; k < VN; ++k) top = fmaxf(top, kv8_mag(f[k]));
-    }
-    top = group_max(top, a.tpb, sm[0]);
-    if (!live) return;                                 // no barrier below
+    const int row0 = t >> a.vpr_shift, rows = tpb >> a.vpr_shift, e = (t & ((1 << a.vpr_shift) - 1)) * VN;
     const int64_t blk = ((int64_t)((a.layer + l) * 2 + kv) * a.q.n_pages + b.page) * a.Hkv + head;
+    uint4 x[NP];
+    float was = 0.f;
+    if (live) {
+        const T* src = (const T*)a.src[kv] + l * a.layer_stride + (int64_t)head * a.hd + e +
+                       (int64_t)(b.src_row - b.lo) * a.row_stride;
+        if (b.lo > 0) was = a.scales[blk];             // earlier rows of the sequence stay in the block
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+            const int row = row0 + i * rows;
+            x[i] = row >= b.lo && row < b.hi ? __ldcs(reinterpret_cast<const uint4*>(src + row * a.row_stride)) : make_uint4(0, 0, 0, 0);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < NP; ++i) x[i] = make_uint4(0, 0, 0, 0);
+    }
+    unsigned m = 0;
+#pragma unroll
+    for (int i = 0; i < NP; ++i) m = Vec<T>::top(x[i], m);
+    unsigned top = group_max(Vec<T>::joined(m), tpb, sm);
+    const bool special = top >= Vec<T>::INF;           // an infinity or a NaN: the finite maximum, and infinities to NaN
+    if (__syncthreads_or(special)) {
+        float f[VN], f_top = 0.f;
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+            Vec<T>::get(x[i], f);
+#pragma unroll
+            for (int k = 0; k < VN; ++k) f_top = fmaxf(f_top, kv8_mag(f[k]));
+        }
+        f_top = __uint_as_float(group_max(__float_as_uint(f_top), tpb, sm));
+        if (special) top = sizeof(T) == 2 ? __float_as_uint(f_top) >> 16 : __float_as_uint(f_top);
+    }
+    if (!live) return;                                 // no barrier of all threads below
     uint8_t* dst = a.codes + blk * P * a.hd;
-    float sc = kv8_scale(top);
-    if (b.lo > 0) {                                    // earlier rows of the sequence stay in the block
-        const float was = a.scales[blk];
+    float sc = kv8_scale(Vec<T>::value(top));
+    if (b.lo > 0) {
         if (was >= sc) {
             sc = was;
         } else if (was > 0.f) {                        // (codes of a block of zeros stay as they are)
             const float f = was * kv8_inverse(sc);
-            for (int i = t; i < b.lo * a.hd / 16; i += a.tpb) {
+            for (int i = t; i < b.lo * a.hd / 16; i += tpb) {
                 uint4 c = reinterpret_cast<uint4*>(dst)[i];
                 c.x = kv8_rescale4(c.x, f);
                 c.y = kv8_rescale4(c.y, f);
@@ -170,24 +203,26 @@ __global__ void __launch_bounds__(THREADS) kv8_write_kernel(const CacheArgs a) {
     const float inv = kv8_inverse(sc);
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
-        const int v = t + i * a.tpb, row = v / vpr, e = v - row * vpr;
-        if (row < b.lo || row >= b.hi) continue;
+        const int row = row0 + i * rows;
         float f[VN];
         Vec<T>::get(x[i], f);
+        if (special) {
+#pragma unroll
+            for (int k = 0; k < VN; ++k) f[k] = kv8_nan_inf(f[k]);
+        }
         uint32_t w[VN / 4];
 #pragma unroll
-        for (int k = 0; k < VN / 4; ++k) {
-            const float* g = f + 4 * k;
-            w[k] = kv8_code2(kv8_nan_inf(g[0]) * inv, kv8_nan_inf(g[1]) * inv) |
-                   (kv8_code2(kv8_nan_inf(g[2]) * inv, kv8_nan_inf(g[3]) * inv) << 16);
-        }
-        uint8_t* d = dst + row * a.hd + e * VN;
+        for (int k = 0; k < VN / 4; ++k)
+            w[k] = kv8_code2(f[4 * k] * inv, f[4 * k + 1] * inv) | (kv8_code2(f[4 * k + 2] * inv, f[4 * k + 3] * inv) << 16);
+        if (row < b.lo || row >= b.hi) continue;
+        uint8_t* d = dst + row * a.hd + e;
         if (VN == 8) *reinterpret_cast<uint2*>(d) = make_uint2(w[0], w[VN / 4 - 1]);
         else *reinterpret_cast<uint32_t*>(d) = w[0];
     }
-    // every thread of the group has read the old scale before one of them replaces it
-    if (a.tpb > 32) asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(a.tpb) : "memory");
-    else __syncwarp();
+    if (b.lo > 0) {                                    // every thread of the group has read the old scale
+        if (tpb > 32) asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(tpb) : "memory");
+        else __syncwarp();
+    }
     if (t == 0) a.scales[blk] = sc;
 }
 
@@ -205,34 +240,58 @@ template <> __device__ __forceinline__ uint4 pack_values<float>(const float* f) 
     return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
 }
 
+// one vector of values (8 or 4 codes) per step, four steps loaded before the first is stored
 template <typename T>
 __global__ void __launch_bounds__(THREADS) kv8_read_kernel(const CacheArgs a) {
-    constexpr int VN = Vec<T>::N;
-    const int groups = THREADS / a.tpb, group = threadIdx.x / a.tpb, t = threadIdx.x - group * a.tpb;
-    const int unit = blockIdx.x * groups + group;
+    constexpr int VN = Vec<T>::N, NB = 4;
+    const int tpb = 1 << a.tpb_shift, group = threadIdx.x >> a.tpb_shift, t = threadIdx.x & (tpb - 1);
+    const int unit = blockIdx.x * (THREADS >> a.tpb_shift) + group;
     const int lk = blockIdx.y, kv = lk & 1, l = lk >> 1;
-    const int P = 1 << a.q.shift, vpr = a.hd / VN;
+    const int P = 1 << a.q.shift;
     Block b{};
     const int slot = unit / a.Hkv, head = unit - slot * a.Hkv;
     if (unit >= a.units || !kv8_block(a.q, a.r, a.per_seq, slot, b)) return;
+    const int row0 = t >> a.vpr_shift, rows = tpb >> a.vpr_shift, e = (t & ((1 << a.vpr_shift) - 1)) * VN;
     const int64_t blk = ((int64_t)((a.layer + l) * 2 + kv) * a.q.n_pages + b.page) * a.Hkv + head;
-    const uint8_t* src = a.codes + blk * P * a.hd;
+    const uint8_t* src = a.codes + blk * P * a.hd + e;
     const float sc = a.scales[blk];
-    T* dst = (T*)a.src[kv] + l * a.layer_stride + (int64_t)head * a.hd;
-    for (int v = b.lo * vpr + t; v < b.hi * vpr; v += a.tpb) {
-        const int row = v / vpr, e = v - row * vpr;
-        float f[VN];
+    T* dst = (T*)a.src[kv] + l * a.layer_stride + (int64_t)head * a.hd + e + (int64_t)(b.src_row - b.lo) * a.row_stride;
+    for (int r0 = row0 + b.lo; r0 < b.hi; r0 += NB * rows) {
+        uint32_t c[NB][VN / 4];
 #pragma unroll
-        for (int k = 0; k < VN / 4; ++k) {
-            const uint32_t c = reinterpret_cast<const uint32_t*>(src)[v * (VN / 4) + k];
-            const float2 p = kv8_value2(c), z = kv8_value2(c >> 16);
-            f[4 * k] = p.x * sc;
-            f[4 * k + 1] = p.y * sc;
-            f[4 * k + 2] = z.x * sc;
-            f[4 * k + 3] = z.y * sc;
+        for (int i = 0; i < NB; ++i) {
+            const int row = r0 + i * rows;
+            if (row >= b.hi) continue;
+            if constexpr (VN == 8) {
+                const uint2 u = __ldcs(reinterpret_cast<const uint2*>(src + row * a.hd));
+                c[i][0] = u.x;
+                c[i][1] = u.y;
+            } else {
+                c[i][0] = __ldcs(reinterpret_cast<const uint32_t*>(src + row * a.hd));
+            }
         }
-        *reinterpret_cast<uint4*>(dst + (int64_t)(b.src_row + row - b.lo) * a.row_stride + e * VN) = pack_values<T>(f);
+#pragma unroll
+        for (int i = 0; i < NB; ++i) {
+            const int row = r0 + i * rows;
+            if (row >= b.hi) continue;
+            float f[VN];
+#pragma unroll
+            for (int k = 0; k < VN / 4; ++k) {
+                const float2 p = kv8_value2(c[i][k]), z = kv8_value2(c[i][k] >> 16);
+                f[4 * k] = p.x * sc;
+                f[4 * k + 1] = p.y * sc;
+                f[4 * k + 2] = z.x * sc;
+                f[4 * k + 3] = z.y * sc;
+            }
+            __stcs(reinterpret_cast<uint4*>(dst + row * a.row_stride), pack_values<T>(f));
+        }
     }
+}
+
+int log2_of(int x) {
+    int s = 0;
+    while ((1 << s) < x) ++s;
+    return s;
 }
 
 CacheArgs cache_args(const Kv8& c, const Kv8Seqs& q, const Kv8Rows& r, const Kv8Io& io, int layer, int es) {
@@ -253,18 +312,22 @@ CacheArgs cache_args(const Kv8& c, const Kv8Seqs& q, const Kv8Rows& r, const Kv8
     a.layer = layer;
     // four 16-byte vectors per thread where the block is small enough for that
     const int want = (1 << q.shift) * a.hd * es / 64;
-    a.tpb = want < 32 ? 32 : (want > THREADS ? THREADS : want);
+    a.tpb_shift = log2_of(want < 32 ? 32 : (want > THREADS ? THREADS : want));
+    a.vpr_shift = log2_of(a.hd * es / 16);
     return a;
 }
 
 template <typename T>
 cudaError_t write_typed(const CacheArgs& a, int n_layers, int np, cudaStream_t s) {
-    const dim3 grid((a.units + THREADS / a.tpb - 1) / (THREADS / a.tpb), 2 * n_layers);
+    const int groups = THREADS >> a.tpb_shift;
+    const dim3 grid((a.units + groups - 1) / groups, 2 * n_layers);
     switch (np) {
         case 4: kv8_write_kernel<T, 4><<<grid, THREADS, 0, s>>>(a); break;
         case 8: kv8_write_kernel<T, 8><<<grid, THREADS, 0, s>>>(a); break;
         case 16: kv8_write_kernel<T, 16><<<grid, THREADS, 0, s>>>(a); break;
-        default: kv8_write_kernel<T, 32><<<grid, THREADS, 0, s>>>(a); break;
+        default:                                       // fp32 rows, head_dim 128, 256 rows per page
+            if constexpr (sizeof(T) == 4) kv8_write_kernel<T, 32><<<grid, THREADS, 0, s>>>(a);
+            else return cudaErrorInvalidValue;
     }
     return cudaGetLastError();
 }
@@ -276,7 +339,7 @@ cudaError_t launch_kv8_write(const Kv8& c, const Kv8Seqs& q, const Kv8Rows& r, c
     const int es = io.bf16 ? 2 : 4;
     const CacheArgs a = cache_args(c, q, r, io, layer, es);
     if (a.units == 0 || n_layers == 0) return cudaSuccess;
-    const int np = (1 << q.shift) * a.hd * es / 16 / a.tpb;
+    const int np = ((1 << q.shift) * a.hd * es / 16) >> a.tpb_shift;
     return io.bf16 ? write_typed<bf16>(a, n_layers, np, s) : write_typed<float>(a, n_layers, np, s);
 }
 
@@ -284,7 +347,8 @@ cudaError_t launch_kv8_read(const Kv8& c, const Kv8Seqs& q, const Kv8Rows& r, co
                             cudaStream_t s) {
     const CacheArgs a = cache_args(c, q, r, io, layer, io.bf16 ? 2 : 4);
     if (a.units == 0 || n_layers == 0) return cudaSuccess;
-    const dim3 grid((a.units + THREADS / a.tpb - 1) / (THREADS / a.tpb), 2 * n_layers);
+    const int groups = THREADS >> a.tpb_shift;
+    const dim3 grid((a.units + groups - 1) / groups, 2 * n_layers);
     if (io.bf16) kv8_read_kernel<bf16><<<grid, THREADS, 0, s>>>(a);
     else kv8_read_kernel<float><<<grid, THREADS, 0, s>>>(a);
     return cudaGetLastError();

@@ -5,10 +5,15 @@
 // would be, and their weights move along.
 //
 //   select   one CTA per (layer, sequence, KV head): the weights' bits order as unsigned integers, so four rounds of a
-//            256-bin histogram fix the threshold, then one pass in row order writes the kept rows and their weights.
-//   move     one CTA per (layer, K|V, KV head, sequence) and range of destination pages; each page's rows are in
-//            registers before the page is written.  Destination row r comes from a row >= r, so with equal tables (in
-//            place) and the pages done in order nothing is overwritten before it is read.
+//            256-bin histogram fix the threshold (and, when more rows equal it than are wanted, rounds over the row
+//            numbers of those fix the last one taken); a warp then counts and writes the kept rows of its own stretch.
+//   move     one CTA per (layer, K|V, KV head, sequence) and destination page; a page's rows are in registers before it is
+//            written.  Destination row r comes from a row >= r, so with equal tables (in place) one CTA does a head's
+//            pages in order and nothing is overwritten before it is read.
+// The moved rows are most of the bytes: move is bound by HBM, at the latency of rows -> table -> codes, which many
+// small CTAs (or, in place, the next page's addresses fetched ahead) cover.
+#include <climits>
+
 #include "cb_kv8.cuh"
 
 namespace cb {
@@ -16,7 +21,7 @@ namespace cb {
 namespace {
 
 constexpr int ST = 512;       // select threads
-constexpr int MT = 256;       // move threads
+constexpr int MT = 128;       // move threads
 
 struct EvictArgs {
     Kv8Seqs q;
@@ -28,35 +33,38 @@ struct EvictArgs {
 
 __device__ __forceinline__ unsigned rank_bits(float w) { return w > 0.f ? __float_as_uint(w) : 0u; }
 
-// exclusive prefix of v over the CTA's ST threads, and the total; sm holds ST / 32 + 1 ints
-__device__ __forceinline__ int block_prefix(int v, int* sm, int& total) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int x = v;
+// In a 256-bin histogram, the bin in which a running count from the top (or the bottom) reaches `want`, and how many of
+// that bin are wanted.  Called by warp 0.
+template <bool TOP> __device__ __forceinline__ void find_bin(const int* hist, int want, unsigned* pick) {
+    const int lane = threadIdx.x & 31;
+    int h[8], sum = 0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {                      // lane 0 holds the first bins in counting order
+        const int i = lane * 8 + k;
+        h[k] = hist[TOP ? 255 - i : i];
+        sum += h[k];
+    }
+    int before = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
+        const int y = __shfl_up_sync(0xffffffffu, before, o);
+        if (lane >= o) before += y;
     }
-    __syncthreads();                                   // sm is free again
-    if (lane == 31) sm[warp] = x;
-    __syncthreads();
-    int before = 0, all = 0;
-#pragma unroll
-    for (int w = 0; w < ST / 32; ++w) {
-        const int t = sm[w];
-        if (w < warp) before += t;
-        all += t;
+    before -= sum;
+    if (before < want && want <= before + sum) {
+        int k = 0;
+        while (before + h[k] < want) before += h[k++];
+        pick[0] = (unsigned)(TOP ? 255 - (lane * 8 + k) : lane * 8 + k);
+        pick[1] = (unsigned)(want - before);
     }
-    total = all;
-    return before + x - v;
 }
 
 __global__ void __launch_bounds__(ST) kv8_select_kernel(const EvictArgs a) {
     __shared__ int hist[256];
-    __shared__ int sm[ST / 32 + 1];
-    __shared__ unsigned pick[2];                       // digit chosen, rows still wanted below it
-    const int g = blockIdx.x, s = blockIdx.y, l = blockIdx.z, t = threadIdx.x;
-    int len = kv8_len(a.q, s);
+    __shared__ int sm[ST / 32];
+    __shared__ unsigned pick[2];                       // bin chosen, rows wanted of it
+    const int g = blockIdx.x, s = blockIdx.y, l = blockIdx.z, t = threadIdx.x, lane = t & 31, warp = t >> 5;
+    const int len = kv8_len(a.q, s);
     if (len < 0 || len > a.q.max_len) {
         if (t == 0) atomicOr(a.q.status, ST_BAD_ROW);
         return;
@@ -66,64 +74,93 @@ __global__ void __launch_bounds__(ST) kv8_select_kernel(const EvictArgs a) {
     float* ow = a.e.out_weights + seg * a.e.weights_ld;
     int* rows = a.e.out_rows + seg * a.e.keep;
     const int kept = min(len, a.e.keep);
-    unsigned thr = 0;                                  // rows with rank bits above it are kept ...
-    int ties = 0;                                      // ... and the first `ties` rows equal to it
     const int c0 = a.e.sink, c1 = len - a.e.recent;    // candidates [c0, c1)
+    unsigned thr = 0;                                  // candidates with rank bits above it are kept ...
+    int cut = -1;                                      // ... and those equal to it up to this row
     if (len > a.e.keep) {
-        int want = a.e.keep - a.e.sink - a.e.recent;   // > = 0; fewer than the candidates
-        unsigned prefix = 0;
-        for (int shift = 24; shift >= 0; shift -= 8) {
+        int want = a.e.keep - a.e.sink - a.e.recent;   // fewer than the candidates
+        // rounds of eight bits: a row counts when its bits above `shift + 8` are `prefix`; ties by row number
+        const auto round = [&](int shift, unsigned prefix, bool by_row) {
             for (int i = t; i < 256; i += ST) hist[i] = 0;
             __syncthreads();
             const unsigned mask = shift == 24 ? 0u : ~0u << (shift + 8);
+#pragma unroll 4
             for (int j = c0 + t; j < c1; j += ST) {
-                const unsigned b = rank_bits(w[j]);
-                if ((b & mask) == prefix) atomicAdd(&hist[(b >> shift) & 255u], 1);
+                const unsigned b = rank_bits(w[j]), v = by_row ? (unsigned)j : b;
+                if ((v & mask) == prefix && (!by_row || b == thr)) atomicAdd(&hist[(v >> shift) & 255u], 1);
             }
             __syncthreads();
-            if (t == 0) {                              // the digit that holds the want-th largest
-                int left = want, d = 255;
-                while (d > 0 && hist[d] < left) left -= hist[d--];
-                pick[0] = (unsigned)d;
-                pick[1] = (unsigned)left;
+            if (warp == 0) {
+                if (by_row) find_bin<false>(hist, want, pick);
+                else find_bin<true>(hist, want, pick);
             }
             __syncthreads();
-            prefix |= pick[0] << shift;
             want = (int)pick[1];
+            return prefix | (pick[0] << shift);
+        };
+        if (want > 0) {
+            for (int shift = 24; shift >= 0; shift -= 8) thr = round(shift, thr, false);
+            cut = INT_MAX;
+            if (hist[thr & 255u] > want) {             // more rows equal the threshold than are wanted
+                __syncthreads();
+                unsigned last = 0;
+                for (int shift = 24; shift >= 0; shift -= 8) last = round(shift, last, true);
+                cut = (int)last;
+            }
+        } else {
+            thr = ~0u;
         }
-        thr = prefix;
-        ties = want;
     }
-    int n_out = 0, n_tie = 0;
-    for (int j0 = 0; j0 < len; j0 += ST) {
-        const int j = j0 + t;
-        const float wj = j < len ? w[j] : 0.f;
-        const unsigned b = rank_bits(wj);
-        const bool cand = j >= c0 && j < c1;
-        bool keep = j < len && (!cand || len <= a.e.keep || b > thr);
-        const bool tie = j < len && !keep && b == thr;
-        int total;
-        const int before = block_prefix(tie ? 1 : 0, sm, total);
-        if (tie && n_tie + before < ties) keep = true;
-        n_tie += total;
-        const int at = n_out + block_prefix(keep ? 1 : 0, sm, total);
-        if (keep && at < kept) {                       // in place: at <= j, and this step's weights are in registers
-            rows[at] = j;
-            ow[at] = wj;
+    const auto keeps = [&](int j) {
+        if (j >= len) return false;
+        if (len <= a.e.keep || j < c0 || j >= c1) return true;
+        const unsigned b = rank_bits(w[j]);
+        return b > thr || (b == thr && j <= cut);
+    };
+    // a warp's stretch of rows: count what it keeps, then write it behind the stretches before
+    const int per = (len + ST - 1) / ST * 32, j_lo = warp * per, j_hi = min(len, j_lo + per);
+    int n = 0;
+#pragma unroll 4
+    for (int j = j_lo; j < j_hi; j += 32) n += __popc(__ballot_sync(0xffffffffu, keeps(j + lane)));
+    if (lane == 0) sm[warp] = n;
+    __syncthreads();
+    int at = 0;
+    for (int k = 0; k < warp; ++k) at += sm[k];
+#pragma unroll 4
+    for (int j = j_lo; j < j_hi; j += 32) {
+        const bool k = keeps(j + lane);
+        const unsigned who = __ballot_sync(0xffffffffu, k);
+        if (k) rows[at + __popc(who & ((1u << lane) - 1))] = j + lane;
+        at += __popc(who);
+    }
+    for (int j = kept + t; j < a.e.keep; j += ST) rows[j] = -1;
+    __syncthreads();
+    // the kept rows' weights; in place a weight moves down (rows[i] >= i), so a step reads before it writes
+    constexpr int STEP = 4;
+    for (int i0 = 0; i0 < kept; i0 += STEP * ST) {
+        float v[STEP];
+#pragma unroll
+        for (int k = 0; k < STEP; ++k) {
+            const int i = i0 + k * ST + t;
+            v[k] = i < kept ? w[rows[i]] : 0.f;
         }
-        n_out += total;
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < STEP; ++k) {
+            const int i = i0 + k * ST + t;
+            if (i < kept) ow[i] = v[k];
+        }
     }
     __syncthreads();
     for (int j = kept + t; j < len; j += ST) ow[j] = 0.f;
-    for (int j = kept + t; j < a.e.keep; j += ST) rows[j] = -1;
 }
 
-// NP 16-byte vectors of codes per thread: a page of P rows is P * hd / 16 vectors
+// NP 16-byte vectors of codes per thread: a page of P rows is P * hd / 16 = tpb * NP vectors
 template <int NP>
 __global__ void __launch_bounds__(MT) kv8_move_kernel(const EvictArgs a, int tpb, int ranges) {
-    __shared__ float sm[MT / 32];
+    __shared__ float sm[2][MT / 32];
     const int g = blockIdx.y % a.Hkv, lk = blockIdx.y / a.Hkv, s = blockIdx.z, t = threadIdx.x;
-    const int l = lk >> 1, kv = lk & 1, P = 1 << a.q.shift, vpr = a.hd / 16;
+    const int l = lk >> 1, kv = lk & 1, P = 1 << a.q.shift, vpr_shift = a.hd == 128 ? 3 : 2;
     const int len = kv8_len(a.q, s);
     if (len < 0 || len > a.q.max_len) return;
     const int kept = min(len, a.e.keep), pages = (kept + P - 1) >> a.q.shift;
@@ -132,27 +169,41 @@ __global__ void __launch_bounds__(MT) kv8_move_kernel(const EvictArgs a, int tpb
     const int64_t seg = ((int64_t)l * a.q.n + s) * a.Hkv + g;
     const int* rows = a.e.out_rows + seg * a.e.keep;
     const int64_t base = (int64_t)((a.layer + l) * 2 + kv) * a.q.n_pages;
-    const int per = (pages + ranges - 1) / ranges;
-    for (int b = blockIdx.x * per; b < min(pages, ((int)blockIdx.x + 1) * per); ++b) {
-        uint4 x[NP];
-        float sc[NP];
-        float top = 0.f;
-        const int n = min(P, kept - b * P);
+    const int per = (pages + ranges - 1) / ranges, b_hi = min(pages, ((int)blockIdx.x + 1) * per);
+    // source of vector t + i * tpb of page b: its pool row (page * P + row in page), or -1
+    int64_t from[NP];
+    const auto sources = [&](int b) {
+        int j[NP];
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
-            const int v = t + i * tpb, row = v / vpr, e = v - row * vpr;
+            const int row = b * P + ((t + i * tpb) >> vpr_shift);
+            j[i] = t < tpb && b < b_hi && row < kept ? rows[row] : -1;
+        }
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+            const int pg = j[i] >= 0 ? kv8_page(a.q, s, j[i] >> a.q.shift) : -1;
+            from[i] = pg >= 0 ? ((int64_t)pg << a.q.shift) + (j[i] & (P - 1)) : -1;
+        }
+    };
+    int b = blockIdx.x * per, flip = 0;
+    sources(b);
+    for (; b < b_hi; ++b, flip ^= 1) {
+        uint4 x[NP];
+        float sc[NP];
+        const int n = min(P, kept - b * P);
+        const int dst = a.e.dst_table[(int64_t)s * a.e.dst_ld + b];
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
             x[i] = make_uint4(0, 0, 0, 0);
             sc[i] = 0.f;
-            if (t < tpb && row < n) {
-                const int j = rows[b * P + row];
-                const int pg = kv8_page(a.q, s, j >> a.q.shift);
-                if (pg >= 0) {
-                    const int64_t blk = (base + pg) * a.Hkv + g;
-                    x[i] = reinterpret_cast<const uint4*>(a.codes + (blk * P + (j & (P - 1))) * a.hd)[e];
-                    sc[i] = a.scales[blk];
-                }
+            if (from[i] >= 0) {
+                const int64_t blk = (base + (from[i] >> a.q.shift)) * a.Hkv + g;
+                x[i] = reinterpret_cast<const uint4*>(a.codes + (blk * P + (from[i] & (P - 1))) * a.hd)[(t + i * tpb) & ((1 << vpr_shift) - 1)];
+                sc[i] = a.scales[blk];
             }
         }
+        sources(b + 1);
+        float top = 0.f;
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
             // the largest code without its sign (a NaN code counts as 0), times the scale
@@ -169,31 +220,29 @@ __global__ void __launch_bounds__(MT) kv8_move_kernel(const EvictArgs a, int tpb
             top = fmaxf(top, kv8_value2(m & 0xffu).x * sc[i]);
         }
         top = warp_max(top);
-        if ((t & 31) == 0) sm[t >> 5] = top;
+        if ((t & 31) == 0) sm[flip][t >> 5] = top;
         __syncthreads();                               // also: every row of this page has been read
-        for (int i = 0; i < MT / 32; ++i) top = fmaxf(top, sm[i]);
+        for (int i = 0; i < MT / 32; ++i) top = fmaxf(top, sm[flip][i]);
         const float ns = kv8_scale(top), inv = kv8_inverse(ns);
-        const int pg = a.e.dst_table[(int64_t)s * a.e.dst_ld + b];
-        if (pg < 0 || pg >= a.q.n_pages) {
+        if (dst < 0 || dst >= a.q.n_pages) {
             if (t == 0) atomicOr(a.q.status, ST_BAD_ROW);
-        } else {
-            const int64_t blk = (base + pg) * a.Hkv + g;
-#pragma unroll
-            for (int i = 0; i < NP; ++i) {
-                const int v = t + i * tpb, row = v / vpr;
-                if (t >= tpb || row >= n) continue;
-                if (sc[i] != ns) {
-                    const float f = sc[i] * inv;
-                    x[i].x = kv8_rescale4(x[i].x, f);
-                    x[i].y = kv8_rescale4(x[i].y, f);
-                    x[i].z = kv8_rescale4(x[i].z, f);
-                    x[i].w = kv8_rescale4(x[i].w, f);
-                }
-                reinterpret_cast<uint4*>(a.codes + blk * P * a.hd)[v] = x[i];
-            }
-            if (t == 0) a.scales[blk] = ns;
+            continue;
         }
-        __syncthreads();                               // the page and sm are done with before the next one
+        const int64_t blk = (base + dst) * a.Hkv + g;
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+            const int v = t + i * tpb;
+            if (t >= tpb || (v >> vpr_shift) >= n) continue;
+            if (sc[i] != ns) {
+                const float f = sc[i] * inv;
+                x[i].x = kv8_rescale4(x[i].x, f);
+                x[i].y = kv8_rescale4(x[i].y, f);
+                x[i].z = kv8_rescale4(x[i].z, f);
+                x[i].w = kv8_rescale4(x[i].w, f);
+            }
+            reinterpret_cast<uint4*>(a.codes + blk * P * a.hd)[v] = x[i];
+        }
+        if (t == 0) a.scales[blk] = ns;
     }
 }
 
@@ -206,19 +255,18 @@ cudaError_t launch_kv8_evict(const Kv8& c, const Kv8Seqs& q, const Kv8Evict& e, 
     const cudaError_t err = cudaGetLastError();
     if (err != cudaSuccess) return err;
     const int P = 1 << q.shift, vecs = P * a.hd / 16;
-    const int tpb = vecs < MT ? vecs : MT, np = vecs / tpb;
+    const int tpb = vecs < MT ? vecs : MT, np = vecs / tpb;             // 64 .. 2048 vectors
     const int pages = ((e.keep < q.max_len ? e.keep : q.max_len) + P - 1) / P;
-    // in place the pages of a head are done in order by one CTA; between two tables they are split
+    // in place the pages of a head are done in order by one CTA; between two tables each has its own
     const bool in_place = e.dst_table == q.table && e.dst_ld == q.table_ld;
-    const int64_t heads = (int64_t)2 * n_layers * a.Hkv * q.n;
-    int64_t ranges = in_place ? 1 : ((int64_t)c.num_sms * 16 + heads - 1) / heads;
-    if (ranges > pages) ranges = pages > 0 ? pages : 1;
-    const dim3 grid((unsigned)ranges, 2 * n_layers * a.Hkv, q.n);
+    const int ranges = in_place || pages == 0 ? 1 : pages;
+    const dim3 grid(ranges, 2 * n_layers * a.Hkv, q.n);
     switch (np) {
-        case 1: kv8_move_kernel<1><<<grid, MT, 0, s>>>(a, tpb, (int)ranges); break;
-        case 2: kv8_move_kernel<2><<<grid, MT, 0, s>>>(a, tpb, (int)ranges); break;
-        case 4: kv8_move_kernel<4><<<grid, MT, 0, s>>>(a, tpb, (int)ranges); break;
-        default: kv8_move_kernel<8><<<grid, MT, 0, s>>>(a, tpb, (int)ranges); break;
+        case 1: kv8_move_kernel<1><<<grid, MT, 0, s>>>(a, tpb, ranges); break;
+        case 2: kv8_move_kernel<2><<<grid, MT, 0, s>>>(a, tpb, ranges); break;
+        case 4: kv8_move_kernel<4><<<grid, MT, 0, s>>>(a, tpb, ranges); break;
+        case 8: kv8_move_kernel<8><<<grid, MT, 0, s>>>(a, tpb, ranges); break;
+        default: kv8_move_kernel<16><<<grid, MT, 0, s>>>(a, tpb, ranges); break;
     }
     return cudaGetLastError();
 }
