@@ -18,6 +18,7 @@ struct Kv8 {
     int device;
     int num_sms;
     int shift;               // log2(page_size)
+    bool pdl;                // programmatic dependent launch
     uint8_t* codes;
     float* scales;
     unsigned* status;        // ST_* bits

@@ -2,6 +2,7 @@
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
+#include <cstdlib>
 #include <new>
 
 #include "cb_kv8.cuh"
@@ -132,6 +133,8 @@ cb_status cb_kv8_create(const cb_kv8_config* cfg, void* codes, float* scales, cb
     h->scales = scales;
     h->shift = 0;
     while ((1 << h->shift) < c.page_size) ++h->shift;
+    const char* pdl = getenv("CB_PDL");
+    h->pdl = !(pdl && pdl[0] == '0');
     if (cudaGetDevice(&h->device) != cudaSuccess ||
         cudaDeviceGetAttribute(&h->num_sms, cudaDevAttrMultiProcessorCount, h->device) != cudaSuccess) {
         cudaGetLastError();

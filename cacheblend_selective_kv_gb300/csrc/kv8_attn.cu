@@ -128,6 +128,13 @@ template <int ROW> __device__ __forceinline__ uint32_t f8_at(uint32_t row, uint3
     return ROW == 128 ? row * 128 + ((((b >> 4) ^ row) & 7) << 4) + (b & 15)
                       : row * 64 + ((((b >> 4) ^ (row >> 1)) & 3) << 4) + (b & 15);
 }
+// 4 bytes to shared memory; the barrier is arrived at once this thread's copies so far have landed
+__device__ __forceinline__ void cp_async4(uint32_t dst, const float* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
 __device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2, uint32_t bar) {
     asm volatile(
         "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
@@ -179,8 +186,12 @@ struct Cursor {
 };
 
 constexpr int MAX_STAGES = 3;
+constexpr int RING = 8;                  // tiles whose scales may be under way or in use
+constexpr int LOOK = 2;                  // tiles by which the scales are asked for ahead of the codes
 struct Shared {
-    uint64_t k_full[MAX_STAGES], v_full[MAX_STAGES], empty[MAX_STAGES];
+    float scale[RING][2][8];             // K's and V's scale of each box of a tile; -1: not loaded
+    uint64_t scale_full[RING];
+    uint64_t k_full[MAX_STAGES], v_full[MAX_STAGES], k_empty[MAX_STAGES], v_empty[MAX_STAGES];
     uint64_t s_full[2], s_free[2];
     uint64_t p_full, o_full, q_full, drain;
     uint32_t tmem;
@@ -204,27 +215,90 @@ template <int HD_, int NC_, int GR_, int TQ_, int TP_, int CTAS_, int STAGES_> s
     static constexpr int P_BYTES = (NP + 127) / 128 * TK * PITCH;
     static constexpr int O_COL = 2 * NQ;
     static constexpr int TMEM = pow2_cols(2 * NQ + NP);
-    // K/V stages, Q, P (all 1024-byte aligned), then the softmax exchange and the control block
+    // K/V stages, Q (two), P (all 1024-byte aligned), then the softmax exchange and the control block
     static constexpr int OFF_Q = 2 * STAGES * KV_BYTES;
-    static constexpr int OFF_P = (OFF_Q + Q_BYTES + 1023) / 1024 * 1024;
+    static constexpr int OFF_P = (OFF_Q + 2 * Q_BYTES + 1023) / 1024 * 1024;
     static constexpr int OFF_X = (OFF_P + P_BYTES + 1023) / 1024 * 1024;
-    // floats: wmax, ymax [2][GR][4][NW]; cols [2][4 GR][4][NW]; qscale [NC]; wsum, colm [4][NC]; nan_from [HD]
-    static constexpr int X_FLOATS = 2 * 8 * NC + 2 * 4 * GR * 4 * NW + NC + 8 * NC + HD;
+    // floats: wmax, ymax [2][GR][4][NW]; cols [2][4 GR][4][NW]; qscale [2][NC]; wsum, colm [4][NC]; nan_from [HD]
+    static constexpr int X_FLOATS = 2 * 8 * NC + 2 * 4 * GR * 4 * NW + 2 * NC + 8 * NC + HD;
     static constexpr int OFF_C = (OFF_X + X_FLOATS * 4 + 63) / 64 * 64;
-    static constexpr int BYTES = OFF_C + (int)sizeof(Shared) + 1024;       // + alignment of the base
+    static constexpr int BYTES = OFF_C + (int)sizeof(Shared);
     static constexpr int PIECE = NC * (HD + 2);                            // floats of an unfinished item
     static_assert(TMEM * CTAS <= 512 && 2 * NQ + NP <= 512, "tensor memory");
     static_assert((BYTES + 1024) * CTAS <= 228 * 1024 && STAGES <= MAX_STAGES, "shared memory");
     static_assert(NW == 4 || NW == 8 || NW == 16, "columns of a group");
 };
 
+// Kept out of the tile loop, whose instructions have to stay close together:
+
+// Q of an item as terms: column r = (query row, head of the group), lane = HD / 32 of its dims.  An item's Q is written
+// (into one of two buffers) while the first tile of the item before it is worked on, so that the MMA warp runs on across
+// items.
+template <typename T, typename S>
+__device__ __noinline__ void q_terms(const AttnArgs& p, const Cursor& u, uint8_t* sQ, float* qscale, float to_exp2) {
+    constexpr int HD = S::HD, E = HD / 32;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int q0 = u.qt * p.QT, cols = min(p.QT, u.q.n - q0) * p.G;
+    const T* qbase = (const T*)p.a.q + (int64_t)(u.q.r0 + q0) * p.a.q_stride + (int64_t)u.g * p.G * HD;
+    for (int r = warp; r < S::NC; r += S::SOFT / 32) {
+        float x[E];
+        float top = 0.f;
+        const T* src = qbase + (int64_t)(r / p.G) * p.a.q_stride + (r % p.G) * HD + lane * E;
+#pragma unroll
+        for (int k = 0; k < E; ++k) {
+            x[k] = r < cols ? to_f(src[k]) : 0.f;
+            top = fmaxf(top, kv8_mag(x[k]));
+        }
+        const float sc = kv8_scale(warp_max(top)), inv = kv8_inverse(sc);
+#pragma unroll
+        for (int k = 0; k < E; ++k) x[k] = kv8_nan_inf(x[k]) * inv;
+#pragma unroll
+        for (int t = 0; t < S::TQ; ++t) {
+            uint32_t w = 0;
+#pragma unroll
+            for (int k = 0; k < E; k += 2) {
+                const uint32_t c2 = kv8_code2(x[k], x[k + 1]);
+                const float2 v = kv8_value2(c2);
+                x[k] = (x[k] - v.x) * 16.f;
+                x[k + 1] = (x[k + 1] - v.y) * 16.f;
+                w |= c2 << (8 * k);
+            }
+            uint8_t* d = sQ + f8_at<HD>(t * S::NC + r, lane * E);
+            if (E == 4) *reinterpret_cast<uint32_t*>(d) = w;
+            else *reinterpret_cast<uint16_t*>(d) = (uint16_t)w;
+        }
+        if (lane == 0) qscale[r] = sc * to_exp2;
+    }
+    fence_async_smem();
+    __syncwarp();
+}
+
+// A V row that no weight may meet: one that was not loaded or lies behind the sequence is zeroed (0 times NaN would be
+// NaN); in one that only later query rows see, NaN codes are taken out and remembered.
+template <int HD> __device__ __noinline__ void clean_v_row(uint8_t* tile, int key, bool have, int j, int* nan_from) {
+    for (int d = 0; d < HD; d += 16) {
+        uint4* v = reinterpret_cast<uint4*>(tile + f8_at<HD>(key, d));
+        if (!have) {
+            *v = make_uint4(0, 0, 0, 0);
+            continue;
+        }
+        uint32_t* w = reinterpret_cast<uint32_t*>(v);
+        for (int k = 0; k < 4; ++k) {
+            const uint32_t bad = __vcmpeq4(w[k] & 0x7f7f7f7fu, 0x7f7f7f7fu);
+            if (bad == 0) continue;
+            w[k] &= ~bad;
+            for (int n = 0; n < 4; ++n)
+                if (bad >> (8 * n) & 1) atomicMin(&nan_from[d + 4 * k + n], j);
+        }
+    }
+}
+
 template <typename T, typename S>
 __global__ void __launch_bounds__(S::THREADS, S::CTAS)
     kv8_attn_kernel(const __grid_constant__ CUtensorMap map, const AttnArgs p) {
     constexpr int HD = S::HD, NC = S::NC, NW = S::NW, GR = S::GR, TQ = S::TQ, TP = S::TP, NQ = S::NQ, NP = S::NP;
     constexpr int STAGES = S::STAGES, SOFT = S::SOFT, THREADS = S::THREADS, TMA_WARP = SOFT / 32, MMA_WARP = TMA_WARP + 1;
-    extern __shared__ uint8_t raw[];
-    uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+    extern __shared__ __align__(1024) uint8_t sm[];     // no static shared memory: the window starts on 1024 bytes
     uint8_t* sK = sm;                                   // [STAGES][TK][HD]
     uint8_t* sV = sm + STAGES * S::KV_BYTES;
     uint8_t* sQ = sm + S::OFF_Q;
@@ -233,24 +307,30 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
     float* ymax = wmax + 8 * NC;
     float* cols_of = ymax + 8 * NC;
     float* qscale = cols_of + 2 * 4 * GR * 4 * NW;
-    float* wsum = qscale + NC;
+    float* wsum = qscale + 2 * NC;
     float* colm = wsum + 4 * NC;
     int* nan_from = reinterpret_cast<int*>(colm + 4 * NC);
     Shared& c = *reinterpret_cast<Shared*>(sm + S::OFF_C);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     unsigned* status = p.q.status;
     volatile int* abort = &c.abort;
+    if (ptx::smem_u32(sm) & 1023) {                     // (the swizzled layouts would not hold)
+        if (tid == 0) atomicOr(status, ST_WAIT_TIMEOUT);
+        return;
+    }
 
     if (tid == 0) {
         for (int i = 0; i < STAGES; ++i) {
             ptx::mbar_init(ptx::smem_u32(&c.k_full[i]), 1);
             ptx::mbar_init(ptx::smem_u32(&c.v_full[i]), 1);
-            ptx::mbar_init(ptx::smem_u32(&c.empty[i]), 1);
+            ptx::mbar_init(ptx::smem_u32(&c.k_empty[i]), 1);
+            ptx::mbar_init(ptx::smem_u32(&c.v_empty[i]), 1);
         }
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(ptx::smem_u32(&c.s_full[i]), 1);
             ptx::mbar_init(ptx::smem_u32(&c.s_free[i]), SOFT / 32);
         }
+        for (int i = 0; i < RING; ++i) ptx::mbar_init(ptx::smem_u32(&c.scale_full[i]), TK / p.box);
         ptx::mbar_init(ptx::smem_u32(&c.p_full), SOFT / 32);
         ptx::mbar_init(ptx::smem_u32(&c.o_full), 1);
         ptx::mbar_init(ptx::smem_u32(&c.q_full), SOFT / 32);
@@ -264,6 +344,8 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
         ptx::tmem_relinquish();
     }
 
+    grid_dep_launch();
+    grid_dep_wait();                                     // lengths, tables, queries and the cache of the kernels before
     // ---- this CTA's piece of the list, THREADS sequences at a time (the first step's are kept)
     const Seq q_own = tid < p.q.n ? seq_at(p, tid) : Seq{0, 0, 0};
     const long long t_own = seq_tiles(p, q_own);
@@ -332,50 +414,98 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
 
     if (warp == TMA_WARP) {
         // ------------------------------------------------------------------------------------ TMA
-        const int boxes = TK / p.box, rows = p.box;              // boxes per tile, one lane each
-        const int per_page = 1 << p.q.shift;
-        uint32_t issued = 0;
-        auto page_of = [&](const Cursor& u) -> int {             // this lane's page (-1: nothing to load)
-            const int j = u.t * TK + lane * rows;
-            if (lane >= boxes || j >= u.q.len) return -1;
-            return kv8_page(p.q, u.s, j >> p.q.shift);
+        // A lane looks after one box (at most a page) of a tile.  Its page id is loaded LOOK + 1 tiles ahead; the scales go to
+        // shared memory LOOK tiles ahead, so that neither is waited for when memory is busy.  A scale slot is free again
+        // without a barrier of its own: K of tile i waits for S of tile i - STAGES, hence the softmax is past tile
+        // i - STAGES - 2, and slot i + LOOK was last used RING - LOOK tiles before i.
+        static_assert(RING - LOOK > STAGES + 2, "scale ring");
+        const int boxes = TK / p.box, rows = p.box, in_page = (1 << p.q.shift) - 1;
+        struct Ahead {
+            int page, g, off;                                    // off: first row in the page
+            bool need;                                           // the box holds rows of the sequence
         };
-        int page = count > 0 ? page_of(cur) : -1;
+        auto look = [&](const Cursor& u) {
+            const int j = u.t * TK + lane * rows;
+            Ahead a{0, u.g, j & in_page, lane < boxes && j < u.q.len};
+            if (a.need) a.page = p.q.table[(int64_t)u.s * p.q.table_ld + (j >> p.q.shift)];
+            return a;
+        };
+        auto ask_scales = [&](Ahead& a, int i) {                 // (the page id was loaded a tile ago)
+            if (a.need && (a.page < 0 || a.page >= p.q.n_pages)) {
+                atomicOr(status, ST_BAD_ROW);
+                a.need = false;
+            }
+            if (lane >= boxes) return;
+            float* dst = &c.scale[i % RING][0][lane];
+            const uint32_t bar = ptx::smem_u32(&c.scale_full[i % RING]);
+            if (a.need) {
+                const int64_t at = (int64_t)a.page * p.Hkv + a.g;
+                cp_async4(ptx::smem_u32(dst), p.ks + at);
+                cp_async4(ptx::smem_u32(dst + 8), p.vs + at);
+                cp_async_arrive(bar);
+            } else {
+                dst[0] = dst[8] = -1.f;
+                ptx::mbar_arrive(bar);
+            }
+        };
+        int k_issued = 0, v_issued = 0;
+        Ahead box[LOOK + 2];
+        int at = 0;                                              // tile that `cur` stands at
+        auto advance = [&] {
+            if (++at < count && ++cur.t == cur.nt) cur.next_item(p);
+        };
+        if (count > 0) {
+#pragma unroll
+            for (int k = 0; k <= LOOK; ++k) {                    // tiles 0 .. LOOK
+                box[k] = look(cur);
+                if (at >= count) box[k].need = false;
+                advance();
+            }
+#pragma unroll
+            for (int k = 0; k < LOOK; ++k)
+                if (k < count) ask_scales(box[k], k);
+        }
         for (int i = 0; i < count; ++i) {
             const int st = i % STAGES;
-            const int row = (page * p.Hkv + cur.g) * per_page + ((cur.t * TK + lane * rows) & (per_page - 1));
-            const bool load = page >= 0;
+            box[LOOK + 1] = Ahead{0, 0, 0, false};
+            if (at < count) box[LOOK + 1] = look(cur);           // tile i + LOOK + 1
+            advance();
+            if (i + LOOK < count) ask_scales(box[LOOK], i + LOOK);
+            const bool load = box[0].need;
+            const int row = (box[0].page * p.Hkv + box[0].g) * (in_page + 1) + box[0].off;
             const unsigned who = __ballot_sync(0xffffffffu, load);
-            if (i + 1 < count) {                                 // the next tile's pages, before this one's wait
-                if (++cur.t == cur.nt) cur.next_item(p);
-                page = page_of(cur);
-            }
-            const bool ok = ptx::mbar_wait(ptx::smem_u32(&c.empty[st]), ((i / STAGES) & 1) ^ 1, abort, status);
+#pragma unroll
+            for (int k = 0; k <= LOOK; ++k) box[k] = box[k + 1];
+            // a K tile is free as soon as its S is computed, a V tile a softmax later: K runs further ahead
+            const uint32_t par = ((i / STAGES) & 1) ^ 1, bytes = (uint32_t)__popc(who) * rows * HD;
+            bool ok = ptx::mbar_wait(ptx::smem_u32(&c.k_empty[st]), par, abort, status);
             if (!__all_sync(0xffffffffu, ok)) break;
-            const uint32_t kb = ptx::smem_u32(&c.k_full[st]), vb = ptx::smem_u32(&c.v_full[st]);
-            if (lane == 0) {
-                const uint32_t bytes = (uint32_t)__popc(who) * rows * HD;
-                ptx::mbar_arrive_expect_tx(kb, bytes);
-                ptx::mbar_arrive_expect_tx(vb, bytes);
-            }
+            if (lane == 0) ptx::mbar_arrive_expect_tx(ptx::smem_u32(&c.k_full[st]), bytes);
             __syncwarp();
-            issued = (uint32_t)(i + 1);
-            if (load) tma_3d(ptx::smem_u32(sK + st * S::KV_BYTES + lane * rows * HD), &map, 0, row, p.kz, kb);
-            if (load) tma_3d(ptx::smem_u32(sV + st * S::KV_BYTES + lane * rows * HD), &map, 0, row, p.kz + 1, vb);
+            k_issued = i + 1;
+            if (load)
+                tma_3d(ptx::smem_u32(sK + st * S::KV_BYTES + lane * rows * HD), &map, 0, row, p.kz, ptx::smem_u32(&c.k_full[st]));
+            ok = ptx::mbar_wait(ptx::smem_u32(&c.v_empty[st]), par, abort, status);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            if (lane == 0) ptx::mbar_arrive_expect_tx(ptx::smem_u32(&c.v_full[st]), bytes);
+            __syncwarp();
+            v_issued = i + 1;
+            if (load)
+                tma_3d(ptx::smem_u32(sV + st * S::KV_BYTES + lane * rows * HD), &map, 0, row, p.kz + 1, ptx::smem_u32(&c.v_full[st]));
         }
         // every copy has landed before the CTA may leave
-        for (int k = 0; k < STAGES; ++k) {
-            if (issued <= (uint32_t)k) continue;
-            const uint32_t i = (issued - 1 - k), st = i % STAGES, par = (i / STAGES) & 1;
-            int never = 0;
-            ptx::mbar_wait(ptx::smem_u32(&c.k_full[st]), par, &never, status);
-            ptx::mbar_wait(ptx::smem_u32(&c.v_full[st]), par, &never, status);
-        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        int never = 0;
+        for (int i = max(0, k_issued - STAGES); i < k_issued; ++i)
+            ptx::mbar_wait(ptx::smem_u32(&c.k_full[i % STAGES]), (i / STAGES) & 1, &never, status);
+        for (int i = max(0, v_issued - STAGES); i < v_issued; ++i)
+            ptx::mbar_wait(ptx::smem_u32(&c.v_full[i % STAGES]), (i / STAGES) & 1, &never, status);
     } else if (warp == MMA_WARP) {
         // ------------------------------------------------------------------------------------ MMA
         if (lane == 0) {
             constexpr uint32_t id_s = f8_idesc(NQ, false), id_o = f8_idesc(NP, true);
-            const uint64_t qd = f8_desc<HD>(ptx::smem_u32(sQ), 16), pd = p_desc<S::PITCH>(ptx::smem_u32(sP));
+            uint64_t qd = 0;
+            const uint64_t pd = p_desc<S::PITCH>(ptx::smem_u32(sP));
             int left = 0, item = 0;
             bool ok = true;
             auto values = [&](int i) {                           // O^T = V^T P^T of tile i
@@ -388,19 +518,16 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
 #pragma unroll
                 for (int k = 0; k < TK / 32; ++k)
                     mma_e4m3(tmem + S::O_COL, vd + (uint64_t)(k * 32 * HD >> 4), pd + (uint64_t)(k * 32 * S::PITCH >> 4), id_o, k > 0);
-                ptx::mma_commit(ptx::smem_u32(&c.empty[st]));
+                ptx::mma_commit(ptx::smem_u32(&c.v_empty[st]));
                 ptx::mma_commit(ptx::smem_u32(&c.o_full));
                 return true;
             };
             for (int i = 0; i < count && ok; ++i) {
-                const bool begins = left == 0;                   // an item's first tile waits for its Q, which is
-                if (begins) {                                    // written after the item before it is done
-                    if (i > 0) {
-                        if (!values(i - 1)) break;
-                        cur.next_item(p);
-                    }
+                if (left == 0) {                                 // an item's first tile waits for its Q
+                    if (i > 0) cur.next_item(p);
                     left = cur.nt - cur.t;
                     if (!ptx::mbar_wait(ptx::smem_u32(&c.q_full), item & 1, abort, status)) break;
+                    qd = f8_desc<HD>(ptx::smem_u32(sQ + (item & 1) * S::Q_BYTES), 16);
                     ++item;
                 }
                 const int st = i % STAGES, b = i & 1;
@@ -412,7 +539,8 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
                 for (int k = 0; k < HD / 32; ++k)
                     mma_e4m3(tmem + b * NQ, kd + (uint64_t)(k * 32 >> 4), qd + (uint64_t)(k * 32 >> 4), id_s, k > 0);
                 ptx::mma_commit(ptx::smem_u32(&c.s_full[b]));
-                if (!begins) ok = values(i - 1);
+                ptx::mma_commit(ptx::smem_u32(&c.k_empty[st]));
+                if (i > 0) ok = values(i - 1);
                 --left;
                 if (ok && i == count - 1) ok = values(i);
             }
@@ -427,57 +555,24 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
         const int gr = warp >> 2, quarter = warp & 3, key = tid & 127, c0 = gr * NW;     // this group's first column
         const uint32_t my_lanes = tmem + ((uint32_t)(quarter * 32) << 16);
         const float to_exp2 = p.a.scale * 1.4426950408889634f;
+        const int box_shift = min(p.q.shift, 7);
+        auto write_q = [&](const Cursor& u, int buf) {
+            q_terms<T, S>(p, u, sQ + buf * S::Q_BYTES, qscale + buf * NC, to_exp2);
+            if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&c.q_full));
+        };
         int item = 0;
+        Cursor next;
         for (int i = 0; i < count; ++item) {
-            const int first = cur.t, n_here = min(cur.nt - first, count - i), g = cur.g, s = cur.s;
+            const int first = cur.t, n_here = min(cur.nt - first, count - i), g = cur.g;
             const Seq q = cur.q;
             const int q0 = cur.qt * p.QT, rows = min(p.QT, q.n - q0), cols = rows * p.G;
             const int pos0 = q.len - q.n + q0;                   // position of the item's first query row
             const int64_t stat0 = ((int64_t)g * p.r.n_rows + q.r0 + q0) * p.G;     // the item's first column in scores, stats
-            const T* qbase = (const T*)p.a.q + (int64_t)(q.r0 + q0) * p.a.q_stride + (int64_t)g * p.G * HD;
 
-            auto page_of = [&](int t) -> int {                   // page of this thread's key in tile t of the item
-                const int j = t * TK + key;
-                return t < first + n_here && j < q.len ? kv8_page(p.q, s, j >> p.q.shift) : -1;
-            };
-            int page = page_of(first), page_next = page_of(first + 1);
-            float ksc = page >= 0 ? p.ks[(int64_t)page * p.Hkv + g] : 0.f, vsc = page >= 0 ? p.vs[(int64_t)page * p.Hkv + g] : 0.f;
-
-            // Q as terms: column r = (query row, head of the group), lane = HD / 32 of its dims
-            for (int r = warp; r < NC; r += SOFT / 32) {
-                constexpr int E = HD / 32;
-                float x[E];
-                float top = 0.f;
-                const T* src = qbase + (int64_t)(r / p.G) * p.a.q_stride + (r % p.G) * HD + lane * E;
-#pragma unroll
-                for (int k = 0; k < E; ++k) {
-                    x[k] = r < cols ? to_f(src[k]) : 0.f;
-                    top = fmaxf(top, kv8_mag(x[k]));
-                }
-                const float sc = kv8_scale(warp_max(top)), inv = kv8_inverse(sc);
-#pragma unroll
-                for (int k = 0; k < E; ++k) x[k] = kv8_nan_inf(x[k]) * inv;
-#pragma unroll
-                for (int t = 0; t < TQ; ++t) {
-                    uint32_t w = 0;
-#pragma unroll
-                    for (int k = 0; k < E; k += 2) {
-                        const uint32_t c2 = kv8_code2(x[k], x[k + 1]);
-                        const float2 v = kv8_value2(c2);
-                        x[k] = (x[k] - v.x) * 16.f;
-                        x[k + 1] = (x[k + 1] - v.y) * 16.f;
-                        w |= c2 << (8 * k);
-                    }
-                    uint8_t* d = sQ + f8_at<HD>(t * NC + r, lane * E);
-                    if (E == 4) *reinterpret_cast<uint32_t*>(d) = w;
-                    else *reinterpret_cast<uint16_t*>(d) = (uint16_t)w;
-                }
-                if (lane == 0) qscale[r] = sc * to_exp2;
-            }
             if (tid < HD) nan_from[tid] = INT_MAX;
-            fence_async_smem();
-            ptx::named_bar_sync(1, SOFT);
-            if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&c.q_full));
+            if (item == 0) write_q(cur, 0);
+            ptx::named_bar_sync(1, SOFT);                        // nan_from, the first item's qscale
+            const float* qsc = qscale + (item & 1) * NC + c0;
 
             float acc[NW], lsum[NW];
             float mrun = -INFINITY;                              // running maximum of column c0 + lane
@@ -512,13 +607,9 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
 
             for (int t = first; t < first + n_here; ++t, ++i) {
                 const int b = i & 1, j = t * TK + key;
-                const bool have = page >= 0;
-                const float ks_now = ksc, vs_now = vsc;
-                // the next tile's scales and the page after it, while this one is worked on
-                page = page_next;
-                page_next = page_of(t + 2);
-                ksc = page >= 0 ? p.ks[(int64_t)page * p.Hkv + g] : 0.f;
-                vsc = page >= 0 ? p.vs[(int64_t)page * p.Hkv + g] : 0.f;
+                ptx::mbar_wait(ptx::smem_u32(&c.scale_full[i % RING]), (i / RING) & 1, abort, status);
+                const float ks_now = c.scale[i % RING][0][key >> box_shift], vs_now = c.scale[i % RING][1][key >> box_shift];
+                const bool have = ks_now >= 0.f && j < q.len;
 
                 ptx::mbar_wait(ptx::smem_u32(&c.s_full[b]), (i >> 1) & 1, abort, status);
                 ptx::tc_fence_after();
@@ -537,7 +628,7 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
                         float v = __uint_as_float(w[TQ - 1][k]);
 #pragma unroll
                         for (int n = TQ - 2; n >= 0; --n) v = fmaf(v, 0.0625f, __uint_as_float(w[n][k]));
-                        x[k] = v * (ks_now * qscale[c0 + k]);
+                        x[k] = v * (ks_now * qsc[k]);
                     }
                 }
                 // column k (query row k / G) sees key j from its own position on: k >= (j - pos0) G
@@ -620,32 +711,21 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
                     else if constexpr (NW == 8) *reinterpret_cast<uint2*>(d) = make_uint2(w[0], w[1]);
                     else *reinterpret_cast<uint4*>(d) = make_uint4(w[0], w[1], w[2], w[3]);
                 }
-                // V rows that no weight may meet: one that was not loaded or lies behind the sequence is zeroed (0 times
-                // NaN would be NaN); in one that only later query rows see, NaN codes are taken out and remembered
-                if (gr == 0 && (!have || (j > pos0 && q.n > 1))) {
+                if (gr == 0 && (!have || j > pos0)) {
                     const int st = i % STAGES;
                     ptx::mbar_wait(ptx::smem_u32(&c.v_full[st]), (i / STAGES) & 1, abort, status);
-                    uint8_t* row = sV + st * S::KV_BYTES;
-                    for (int d = 0; d < HD; d += 16) {
-                        uint4* v = reinterpret_cast<uint4*>(row + f8_at<HD>(key, d));
-                        if (!have) {
-                            *v = make_uint4(0, 0, 0, 0);
-                        } else {
-                            uint32_t* w = reinterpret_cast<uint32_t*>(v);
-                            for (int k = 0; k < 4; ++k) {
-                                const uint32_t bad = __vcmpeq4(w[k] & 0x7f7f7f7fu, 0x7f7f7f7fu);
-                                if (bad == 0) continue;
-                                w[k] &= ~bad;
-                                for (int n = 0; n < 4; ++n)
-                                    if (bad >> (8 * n) & 1) atomicMin(&nan_from[d + 4 * k + n], j);
-                            }
-                        }
-                    }
+                    clean_v_row<HD>(sV + st * S::KV_BYTES, key, have, j, nan_from);
                 }
                 fence_async_smem();
                 ptx::tc_fence_before();
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&c.p_full));
+                // (S of this item's first tile is there, so its own Q has been taken and the barrier is a phase behind)
+                if (t == first && i + n_here < count + t - first) {
+                    next = cur;
+                    next.next_item(p);
+                    write_q(next, (item + 1) & 1);
+                }
             }
             add_tile(i - 1);
             ptx::tc_fence_before();
@@ -692,9 +772,9 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
                     for (int k = 0; k < NW; ++k)
                         *reinterpret_cast<float2*>(piece + NC * HD + 2 * (c0 + k)) = make_float2(colm[c0 + k], lsum[k]);
                 }
-                __threadfence();
                 ptx::named_bar_sync(1, SOFT);
                 if (tid == 0) {
+                    __threadfence();                             // the whole CTA's piece, ordered by the barrier
                     c.last = atomicAdd(p.arrived + u0, 1u) == (unsigned)n_pieces - 1;
                     if (c.last) atomicExch(p.arrived + u0, 0u);
                     __threadfence();
@@ -755,7 +835,7 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
                     }
                 }
             }
-            if (i < count) cur.next_item(p);
+            if (i < count) cur = next;
         }
     }
     ptx::tc_fence_before();
@@ -766,10 +846,12 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
     }
 }
 
-// weights[s][g][j] = sum over the sequence's rows and the group's heads of exp2(score - max) / sum: four sums of every
-// fourth column, joined in order
+// weights[s][g][j] = sum over the sequence's rows and the group's heads of exp2(score - max) / sum; with many
+// columns four sums of every fourth one, joined in order
 __global__ void __launch_bounds__(512) kv8_weights_kernel(const AttnArgs p) {
     __shared__ float part[4][128];
+    grid_dep_launch();
+    grid_dep_wait();
     const int j = blockIdx.x * 128 + threadIdx.x, y = threadIdx.y, g = blockIdx.y;
     const Seq q = seq_at(p, blockIdx.z);
     if (blockIdx.x * 128 >= q.len) return;
@@ -779,18 +861,21 @@ __global__ void __launch_bounds__(512) kv8_weights_kernel(const AttnArgs p) {
         const float* score = p.scores + at * p.score_ld + j;
         const float2* st = p.stats + at;
         const int seen = max(0, j - (q.len - q.n)) * p.G, cols = q.n * p.G;      // columns that see key j: [seen, cols)
+        const int by = blockDim.y;
 #pragma unroll 8
-        for (int k = (seen & ~3) + y; k < cols; k += 4) {
+        for (int k = (seen & ~3) + y; k < cols; k += by) {
             if (k < seen) continue;
             const float x = __ldcs(score + (int64_t)k * p.score_ld);
             const float2 m = st[k];
             w += x == -INFINITY ? 0.f : exp2_fast(x - m.x) * m.y;
         }
     }
-    part[y][threadIdx.x] = w;
-    __syncthreads();
-    if (y == 0 && j < q.len) {
+    if (blockDim.y > 1) {
+        part[y][threadIdx.x] = w;
+        __syncthreads();
         w = (part[0][threadIdx.x] + part[1][threadIdx.x]) + (part[2][threadIdx.x] + part[3][threadIdx.x]);
+    }
+    if (y == 0 && j < q.len) {
         float* dst = p.a.weights + ((int64_t)blockIdx.z * p.Hkv + g) * p.a.weights_ld + j;
         *dst = p.a.add ? *dst + w : w;
     }
@@ -807,17 +892,16 @@ cudaError_t launch_shape(const Kv8& c, AttnArgs& p, cudaStream_t s) {
     const int64_t most = (int64_t)c.num_sms * S::CTAS;
     CUtensorMap map;
     memcpy(&map, c.map, sizeof map);
-    kv8_attn_kernel<T, S><<<(int)(tiles < most ? tiles : most), S::THREADS, S::BYTES, s>>>(map, p);
-    return cudaGetLastError();
+    return launch_ex(c.pdl, kv8_attn_kernel<T, S>, dim3((unsigned)(tiles < most ? tiles : most)), dim3(S::THREADS), S::BYTES, s, map, p);
 }
 
 //                           columns, groups, terms of q and P, CTAs per SM, stages
 template <int HD> using C4 = Shape<HD, 4, 1, 2, 3, 3, 2>;
-template <int HD> using C8 = Shape<HD, 8, 1, 2, 3, 3, 2>;
+template <int HD> using C8 = Shape<HD, 8, 1, 2, 3, 2, 3>;
 template <int HD> using C16 = Shape<HD, 16, 2, 2, 3, 2, 2>;
 template <int HD> using C32 = Shape<HD, 32, 4, 2, 3, 1, 3>;
 template <int HD> using C64 = Shape<HD, 64, 4, 2, 3, 1, 3>;
-template <int HD> using F4 = Shape<HD, 4, 1, 6, 6, 3, 2>;
+template <int HD> using F4 = Shape<HD, 4, 1, 6, 6, 2, 3>;
 template <int HD> using F8 = Shape<HD, 8, 1, 6, 6, 2, 2>;
 
 template <int HD> cudaError_t launch_dim(const Kv8& c, AttnArgs& p, cudaStream_t s) {
@@ -886,9 +970,11 @@ cudaError_t launch_kv8_attention(const Kv8& c, const Kv8Seqs& q, const Kv8Rows& 
         const cudaError_t e = c.cfg.head_dim == 128 ? launch_dim<128>(c, p, s) : launch_dim<64>(c, p, s);
         if (e != cudaSuccess) return e;
     }
-    if (a.weights && q.max_len > 0)
-        kv8_weights_kernel<<<dim3((q.max_len + 127) / 128, Hkv, q.n), dim3(128, 4), 0, s>>>(p);
-    return cudaGetLastError();
+    if (a.weights && q.max_len > 0) {
+        const int split = r.n_rows > 4 * q.n ? 4 : 1;            // rows of a sequence, on average
+        return launch_ex(c.pdl, kv8_weights_kernel, dim3((q.max_len + 127) / 128, Hkv, q.n), dim3(128, split), 0, s, p);
+    }
+    return cudaSuccess;
 }
 
 }  // namespace cb

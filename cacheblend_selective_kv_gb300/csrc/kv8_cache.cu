@@ -141,6 +141,8 @@ struct CacheArgs {
 template <typename T, int NP>
 __global__ void __launch_bounds__(THREADS) kv8_write_kernel(const CacheArgs a) {
     constexpr int VN = Vec<T>::N;
+    grid_dep_launch();
+    grid_dep_wait();
     __shared__ unsigned sm[THREADS / 32];
     const int tpb = 1 << a.tpb_shift, group = threadIdx.x >> a.tpb_shift, t = threadIdx.x & (tpb - 1);
     const int unit = blockIdx.x * (THREADS >> a.tpb_shift) + group;
@@ -244,6 +246,8 @@ template <> __device__ __forceinline__ uint4 pack_values<float>(const float* f) 
 template <typename T>
 __global__ void __launch_bounds__(THREADS) kv8_read_kernel(const CacheArgs a) {
     constexpr int VN = Vec<T>::N, NB = 4;
+    grid_dep_launch();
+    grid_dep_wait();
     const int tpb = 1 << a.tpb_shift, group = threadIdx.x >> a.tpb_shift, t = threadIdx.x & (tpb - 1);
     const int unit = blockIdx.x * (THREADS >> a.tpb_shift) + group;
     const int lk = blockIdx.y, kv = lk & 1, l = lk >> 1;
@@ -318,18 +322,17 @@ CacheArgs cache_args(const Kv8& c, const Kv8Seqs& q, const Kv8Rows& r, const Kv8
 }
 
 template <typename T>
-cudaError_t write_typed(const CacheArgs& a, int n_layers, int np, cudaStream_t s) {
+cudaError_t write_typed(const CacheArgs& a, int n_layers, int np, bool pdl, cudaStream_t s) {
     const int groups = THREADS >> a.tpb_shift;
     const dim3 grid((a.units + groups - 1) / groups, 2 * n_layers);
     switch (np) {
-        case 4: kv8_write_kernel<T, 4><<<grid, THREADS, 0, s>>>(a); break;
-        case 8: kv8_write_kernel<T, 8><<<grid, THREADS, 0, s>>>(a); break;
-        case 16: kv8_write_kernel<T, 16><<<grid, THREADS, 0, s>>>(a); break;
+        case 4: return launch_ex(pdl, kv8_write_kernel<T, 4>, grid, dim3(THREADS), 0, s, a);
+        case 8: return launch_ex(pdl, kv8_write_kernel<T, 8>, grid, dim3(THREADS), 0, s, a);
+        case 16: return launch_ex(pdl, kv8_write_kernel<T, 16>, grid, dim3(THREADS), 0, s, a);
         default:                                       // fp32 rows, head_dim 128, 256 rows per page
-            if constexpr (sizeof(T) == 4) kv8_write_kernel<T, 32><<<grid, THREADS, 0, s>>>(a);
-            else return cudaErrorInvalidValue;
+            if constexpr (sizeof(T) == 4) return launch_ex(pdl, kv8_write_kernel<T, 32>, grid, dim3(THREADS), 0, s, a);
+            return cudaErrorInvalidValue;
     }
-    return cudaGetLastError();
 }
 
 }  // namespace
@@ -340,7 +343,7 @@ cudaError_t launch_kv8_write(const Kv8& c, const Kv8Seqs& q, const Kv8Rows& r, c
     const CacheArgs a = cache_args(c, q, r, io, layer, es);
     if (a.units == 0 || n_layers == 0) return cudaSuccess;
     const int np = ((1 << q.shift) * a.hd * es / 16) >> a.tpb_shift;
-    return io.bf16 ? write_typed<bf16>(a, n_layers, np, s) : write_typed<float>(a, n_layers, np, s);
+    return io.bf16 ? write_typed<bf16>(a, n_layers, np, c.pdl, s) : write_typed<float>(a, n_layers, np, c.pdl, s);
 }
 
 cudaError_t launch_kv8_read(const Kv8& c, const Kv8Seqs& q, const Kv8Rows& r, const Kv8Io& io, int layer, int n_layers,
@@ -349,9 +352,8 @@ cudaError_t launch_kv8_read(const Kv8& c, const Kv8Seqs& q, const Kv8Rows& r, co
     if (a.units == 0 || n_layers == 0) return cudaSuccess;
     const int groups = THREADS >> a.tpb_shift;
     const dim3 grid((a.units + groups - 1) / groups, 2 * n_layers);
-    if (io.bf16) kv8_read_kernel<bf16><<<grid, THREADS, 0, s>>>(a);
-    else kv8_read_kernel<float><<<grid, THREADS, 0, s>>>(a);
-    return cudaGetLastError();
+    return io.bf16 ? launch_ex(c.pdl, kv8_read_kernel<bf16>, grid, dim3(THREADS), 0, s, a)
+                   : launch_ex(c.pdl, kv8_read_kernel<float>, grid, dim3(THREADS), 0, s, a);
 }
 
 }  // namespace cb

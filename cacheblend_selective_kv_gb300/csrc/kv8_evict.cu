@@ -63,6 +63,8 @@ __global__ void __launch_bounds__(ST) kv8_select_kernel(const EvictArgs a) {
     __shared__ int hist[256];
     __shared__ int sm[ST / 32];
     __shared__ unsigned pick[2];                       // bin chosen, rows wanted of it
+    grid_dep_launch();
+    grid_dep_wait();
     const int g = blockIdx.x, s = blockIdx.y, l = blockIdx.z, t = threadIdx.x, lane = t & 31, warp = t >> 5;
     const int len = kv8_len(a.q, s);
     if (len < 0 || len > a.q.max_len) {
@@ -159,6 +161,8 @@ __global__ void __launch_bounds__(ST) kv8_select_kernel(const EvictArgs a) {
 template <int NP>
 __global__ void __launch_bounds__(MT) kv8_move_kernel(const EvictArgs a, int tpb, int ranges) {
     __shared__ float sm[2][MT / 32];
+    grid_dep_launch();
+    grid_dep_wait();
     const int g = blockIdx.y % a.Hkv, lk = blockIdx.y / a.Hkv, s = blockIdx.z, t = threadIdx.x;
     const int l = lk >> 1, kv = lk & 1, P = 1 << a.q.shift, vpr_shift = a.hd == 128 ? 3 : 2;
     const int len = kv8_len(a.q, s);
@@ -251,8 +255,7 @@ __global__ void __launch_bounds__(MT) kv8_move_kernel(const EvictArgs a, int tpb
 cudaError_t launch_kv8_evict(const Kv8& c, const Kv8Seqs& q, const Kv8Evict& e, int layer, int n_layers, cudaStream_t s) {
     EvictArgs a{q, e, c.codes, c.scales, c.cfg.n_kv_heads, c.cfg.head_dim, layer};
     if (q.n == 0 || n_layers == 0) return cudaSuccess;
-    kv8_select_kernel<<<dim3(a.Hkv, q.n, n_layers), ST, 0, s>>>(a);
-    const cudaError_t err = cudaGetLastError();
+    const cudaError_t err = launch_ex(c.pdl, kv8_select_kernel, dim3(a.Hkv, q.n, n_layers), dim3(ST), 0, s, a);
     if (err != cudaSuccess) return err;
     const int P = 1 << q.shift, vecs = P * a.hd / 16;
     const int tpb = vecs < MT ? vecs : MT, np = vecs / tpb;             // 64 .. 2048 vectors
@@ -262,13 +265,12 @@ cudaError_t launch_kv8_evict(const Kv8& c, const Kv8Seqs& q, const Kv8Evict& e, 
     const int ranges = in_place || pages == 0 ? 1 : pages;
     const dim3 grid(ranges, 2 * n_layers * a.Hkv, q.n);
     switch (np) {
-        case 1: kv8_move_kernel<1><<<grid, MT, 0, s>>>(a, tpb, ranges); break;
-        case 2: kv8_move_kernel<2><<<grid, MT, 0, s>>>(a, tpb, ranges); break;
-        case 4: kv8_move_kernel<4><<<grid, MT, 0, s>>>(a, tpb, ranges); break;
-        case 8: kv8_move_kernel<8><<<grid, MT, 0, s>>>(a, tpb, ranges); break;
-        default: kv8_move_kernel<16><<<grid, MT, 0, s>>>(a, tpb, ranges); break;
+        case 1: return launch_ex(c.pdl, kv8_move_kernel<1>, grid, dim3(MT), 0, s, a, tpb, ranges);
+        case 2: return launch_ex(c.pdl, kv8_move_kernel<2>, grid, dim3(MT), 0, s, a, tpb, ranges);
+        case 4: return launch_ex(c.pdl, kv8_move_kernel<4>, grid, dim3(MT), 0, s, a, tpb, ranges);
+        case 8: return launch_ex(c.pdl, kv8_move_kernel<8>, grid, dim3(MT), 0, s, a, tpb, ranges);
+        default: return launch_ex(c.pdl, kv8_move_kernel<16>, grid, dim3(MT), 0, s, a, tpb, ranges);
     }
-    return cudaGetLastError();
 }
 
 }  // namespace cb

@@ -50,7 +50,7 @@ def test_slots_of_ragged_rows_cover_every_block(P):
 
 class FakeHandle(ctypes.Structure):
     """The leading fields of a cache handle: its configuration and a device that is never the current one."""
-    _fields_ = [("cfg", cb.CbKV8Config), ("device", ctypes.c_int), ("num_sms", ctypes.c_int), ("shift", ctypes.c_int),
+    _fields_ = [("cfg", cb.CbKV8Config), ("device", ctypes.c_int), ("num_sms", ctypes.c_int), ("shift", ctypes.c_int), ("pdl", ctypes.c_bool),
                 ("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("status", ctypes.c_void_p),
                 ("scores", ctypes.c_void_p), ("room", ctypes.c_uint8 * 256)]
 
