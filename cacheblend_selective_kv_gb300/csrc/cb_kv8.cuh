@@ -6,6 +6,7 @@
 // by it and multiplying by it are exact in fp32, so the only rounding a value meets is the one to e4m3, and a
 // code's value is exact in bf16.
 #pragma once
+#include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
 #include "cb_common.cuh"
@@ -95,6 +96,12 @@ __device__ __forceinline__ float kv8_mag(float x) {
 // an infinity has no e4m3 code and is kept as NaN rather than as a large finite value
 __device__ __forceinline__ float kv8_nan_inf(float x) { return fabsf(x) <= 3.402823466e38f ? x : __int_as_float(0x7fc00000); }
 
+__device__ __forceinline__ unsigned kv8_max_u16x2(unsigned a, unsigned b) {
+    unsigned r;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
 __device__ __forceinline__ uint32_t kv8_code2(float a, float b) {           // codes of a (low byte) and b
     return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
 }
@@ -102,10 +109,24 @@ __device__ __forceinline__ float2 kv8_value2(uint32_t c2) {
     const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(c2 & 0xffffu), __NV_E4M3);
     return __half22float2(__half2(h));
 }
-// four codes whose values are multiplied by the power of two f and rounded to e4m3 again
-__device__ __forceinline__ uint32_t kv8_rescale4(uint32_t c4, float f) {
-    const float2 a = kv8_value2(c4), b = kv8_value2(c4 >> 16);
-    return kv8_code2(a.x * f, a.y * f) | (kv8_code2(b.x * f, b.y * f) << 16);
+__device__ __forceinline__ __half2 kv8_half2(uint32_t c2) {
+    return __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(c2 & 0xffffu), __NV_E4M3));
+}
+// A power of two by which codes are multiplied, as two factors that fit in fp16 (2^-24 .. 2^9 each): a product that is
+// neither 0 nor above 448 needs a factor within 2^-19 .. 2^18, and outside of that both give 0 or are never asked for.
+struct Kv8Factor {
+    __half2 a, b;
+};
+__device__ __forceinline__ Kv8Factor kv8_factor(float f) {
+    const float a = fminf(fmaxf(f, 5.9604645e-8f), 512.f), b = f > 512.f ? fminf(f * (1.f / 512.f), 512.f) : 1.f;
+    return Kv8Factor{__float2half2_rn(a), __float2half2_rn(b)};
+}
+// Four codes whose values are multiplied by it and rounded to e4m3 again.  An e4m3 value has four significant bits, so
+// the products are exact in fp16 down to 2^-21, far below the 2^-10 under which e4m3 rounds to 0.
+__device__ __forceinline__ uint32_t kv8_rescale4(uint32_t c4, const Kv8Factor& f) {
+    const __half2 lo = __hmul2(__hmul2(kv8_half2(c4), f.a), f.b), hi = __hmul2(__hmul2(kv8_half2(c4 >> 16), f.a), f.b);
+    return (uint32_t)__nv_cvt_halfraw2_to_fp8x2(__half2_raw(lo), __NV_SATFINITE, __NV_E4M3) |
+           ((uint32_t)__nv_cvt_halfraw2_to_fp8x2(__half2_raw(hi), __NV_SATFINITE, __NV_E4M3) << 16);
 }
 
 // ------------------------------------------------------------------------------------------------

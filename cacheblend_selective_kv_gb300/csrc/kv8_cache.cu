@@ -15,6 +15,7 @@ namespace cb {
 namespace {
 
 constexpr int THREADS = 256;
+constexpr int VECTORS = 8;             // 16-byte vectors of a row per thread, where blocks are large enough
 
 // Which block a slot stands for.  With `each` rows per sequence, they touch at most per_seq blocks of it and the
 // slots are s * per_seq ..; with ragged rows, n rows touch at most n / P + 2 blocks, so that start(s) / P + 2 s is a
@@ -91,10 +92,10 @@ template <> struct Vec<bf16> {
     static constexpr int N = 8;
     static constexpr unsigned INF = 0x7f80u;
     __device__ static unsigned top(const uint4& u, unsigned m) {           // two running maxima in m
-        m = __vmaxu2(m, u.x & 0x7fff7fffu);
-        m = __vmaxu2(m, u.y & 0x7fff7fffu);
-        m = __vmaxu2(m, u.z & 0x7fff7fffu);
-        return __vmaxu2(m, u.w & 0x7fff7fffu);
+        m = kv8_max_u16x2(m, u.x & 0x7fff7fffu);
+        m = kv8_max_u16x2(m, u.y & 0x7fff7fffu);
+        m = kv8_max_u16x2(m, u.z & 0x7fff7fffu);
+        return kv8_max_u16x2(m, u.w & 0x7fff7fffu);
     }
     __device__ static unsigned joined(unsigned m) { return max(m & 0xffffu, m >> 16); }
     __device__ static float value(unsigned bits) { return __uint_as_float(bits << 16); }
@@ -191,7 +192,7 @@ __global__ void __launch_bounds__(THREADS) kv8_write_kernel(const CacheArgs a) {
         if (was >= sc) {
             sc = was;
         } else if (was > 0.f) {                        // (codes of a block of zeros stay as they are)
-            const float f = was * kv8_inverse(sc);
+            const Kv8Factor f = kv8_factor(was * kv8_inverse(sc));
             for (int i = t; i < b.lo * a.hd / 16; i += tpb) {
                 uint4 c = reinterpret_cast<uint4*>(dst)[i];
                 c.x = kv8_rescale4(c.x, f);
@@ -314,8 +315,10 @@ CacheArgs cache_args(const Kv8& c, const Kv8Seqs& q, const Kv8Rows& r, const Kv8
     a.units = sl.total * a.Hkv;
     a.hd = c.cfg.head_dim;
     a.layer = layer;
-    // four 16-byte vectors per thread where the block is small enough for that
-    const int want = (1 << q.shift) * a.hd * es / 64;
+    // Vectors of 16 bytes per thread: what a thread does once (finding its block) is spread over more of them, and
+    // they are in flight together.  Eight (8K x 32 layers of the 8B shape written in
+    // 248 us, four in 340).
+    const int want = (1 << q.shift) * a.hd * es / (16 * VECTORS);
     a.tpb_shift = log2_of(want < 32 ? 32 : (want > THREADS ? THREADS : want));
     a.vpr_shift = log2_of(a.hd * es / 16);
     return a;

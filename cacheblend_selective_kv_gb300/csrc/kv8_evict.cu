@@ -21,7 +21,9 @@ namespace cb {
 namespace {
 
 constexpr int ST = 512;       // select threads
-constexpr int MT = 128;       // move threads
+constexpr int VPT = 20;       // weights a select thread keeps in registers (two CTAs per SM)
+constexpr int NP = 4;         // 16-byte vectors of codes per move thread
+constexpr int MT = 512;       // move threads, at most: a page of 256 rows of 128 codes
 
 struct EvictArgs {
     Kv8Seqs q;
@@ -59,24 +61,47 @@ template <bool TOP> __device__ __forceinline__ void find_bin(const int* hist, in
     }
 }
 
-__global__ void __launch_bounds__(ST) kv8_select_kernel(const EvictArgs a) {
-    __shared__ int hist[256];
-    __shared__ int sm[ST / 32];
-    __shared__ unsigned pick[2];                       // bin chosen, rows wanted of it
-    grid_dep_launch();
-    grid_dep_wait();
-    const int g = blockIdx.x, s = blockIdx.y, l = blockIdx.z, t = threadIdx.x, lane = t & 31, warp = t >> 5;
-    const int len = kv8_len(a.q, s);
-    if (len < 0 || len > a.q.max_len) {
-        if (t == 0) atomicOr(a.q.status, ST_BAD_ROW);
-        return;
+// exclusive prefix sums over N ints in shared memory, by warp 0 (N a multiple of 32)
+template <int N> __device__ __forceinline__ void warp_scan(int* v) {
+    const int lane = threadIdx.x & 31;
+    constexpr int PER = N / 32;
+    int x[PER], sum = 0;
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+        x[k] = v[lane * PER + k];
+        sum += x[k];
     }
-    const int64_t seg = ((int64_t)l * a.q.n + s) * a.Hkv + g;
-    const float* w = a.e.weights + seg * a.e.weights_ld;
-    float* ow = a.e.out_weights + seg * a.e.weights_ld;
-    int* rows = a.e.out_rows + seg * a.e.keep;
-    const int kept = min(len, a.e.keep);
-    const int c0 = a.e.sink, c1 = len - a.e.recent;    // candidates [c0, c1)
+    int at = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, at, o);
+        if (lane >= o) at += y;
+    }
+    at -= sum;
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+        v[lane * PER + k] = at;
+        at += x[k];
+    }
+}
+
+// The rows of one head.  CACHED: the sequence has at most ST * VPT rows, and a thread's VPT weights stay in registers over
+// the rounds; otherwise each round reads them again (from L2).
+template <bool CACHED>
+__device__ __forceinline__ void select_rows(const EvictArgs& a, const float* w, float* ow, int* rows, int len) {
+    __shared__ int hist[256];
+    __shared__ int count[VPT * ST / 32];
+    __shared__ unsigned pick[2];                       // bin chosen, rows wanted of it
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+    const int kept = min(len, a.e.keep), c0 = a.e.sink, c1 = len - a.e.recent;       // candidates [c0, c1)
+    // rank bits of the candidates; NONE for every other row (above all bits of a float that is not negative)
+    constexpr unsigned NONE = ~0u;
+    const auto rank_of = [&](int j) { return j >= c0 && j < c1 ? rank_bits(w[j]) : NONE; };
+    unsigned u[VPT];
+    if (CACHED) {
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) u[k] = rank_of(k * ST + t);
+    }
     unsigned thr = 0;                                  // candidates with rank bits above it are kept ...
     int cut = -1;                                      // ... and those equal to it up to this row
     if (len > a.e.keep) {
@@ -85,11 +110,17 @@ __global__ void __launch_bounds__(ST) kv8_select_kernel(const EvictArgs a) {
         const auto round = [&](int shift, unsigned prefix, bool by_row) {
             for (int i = t; i < 256; i += ST) hist[i] = 0;
             __syncthreads();
-            const unsigned mask = shift == 24 ? 0u : ~0u << (shift + 8);
+            const unsigned mask = shift == 24 ? 0x80000000u : ~0u << (shift + 8);        // (the sign bit keeps NONE out)
+            const auto add = [&](int j, unsigned b) {
+                const unsigned y = by_row ? (unsigned)j : b;
+                if ((y & mask) == prefix && (!by_row || b == thr)) atomicAdd(&hist[(y >> shift) & 255u], 1);
+            };
+            if (CACHED) {
+#pragma unroll
+                for (int k = 0; k < VPT; ++k) add(k * ST + t, u[k]);
+            } else {
 #pragma unroll 4
-            for (int j = c0 + t; j < c1; j += ST) {
-                const unsigned b = rank_bits(w[j]), v = by_row ? (unsigned)j : b;
-                if ((v & mask) == prefix && (!by_row || b == thr)) atomicAdd(&hist[(v >> shift) & 255u], 1);
+                for (int j = c0 + t; j < c1; j += ST) add(j, rank_of(j));
             }
             __syncthreads();
             if (warp == 0) {
@@ -113,140 +144,211 @@ __global__ void __launch_bounds__(ST) kv8_select_kernel(const EvictArgs a) {
             thr = ~0u;
         }
     }
-    const auto keeps = [&](int j) {
-        if (j >= len) return false;
-        if (len <= a.e.keep || j < c0 || j >= c1) return true;
-        const unsigned b = rank_bits(w[j]);
-        return b > thr || (b == thr && j <= cut);
+    const auto keeps = [&](int j, unsigned b) {
+        return j < len && (len <= a.e.keep || b == NONE || b > thr || (b == thr && j <= cut));
     };
-    // a warp's stretch of rows: count what it keeps, then write it behind the stretches before
-    const int per = (len + ST - 1) / ST * 32, j_lo = warp * per, j_hi = min(len, j_lo + per);
-    int n = 0;
-#pragma unroll 4
-    for (int j = j_lo; j < j_hi; j += 32) n += __popc(__ballot_sync(0xffffffffu, keeps(j + lane)));
-    if (lane == 0) sm[warp] = n;
-    __syncthreads();
-    int at = 0;
-    for (int k = 0; k < warp; ++k) at += sm[k];
-#pragma unroll 4
-    for (int j = j_lo; j < j_hi; j += 32) {
-        const bool k = keeps(j + lane);
-        const unsigned who = __ballot_sync(0xffffffffu, k);
-        if (k) rows[at + __popc(who & ((1u << lane) - 1))] = j + lane;
-        at += __popc(who);
-    }
-    for (int j = kept + t; j < a.e.keep; j += ST) rows[j] = -1;
-    __syncthreads();
-    // the kept rows' weights; in place a weight moves down (rows[i] >= i), so a step reads before it writes
-    constexpr int STEP = 4;
-    for (int i0 = 0; i0 < kept; i0 += STEP * ST) {
-        float v[STEP];
+    if (CACHED) {                                      // 32 rows at a time: count, scan, write
+        unsigned who[VPT];
 #pragma unroll
-        for (int k = 0; k < STEP; ++k) {
-            const int i = i0 + k * ST + t;
-            v[k] = i < kept ? w[rows[i]] : 0.f;
+        for (int k = 0; k < VPT; ++k) {
+            who[k] = __ballot_sync(0xffffffffu, keeps(k * ST + t, u[k]));
+            if (lane == 0) count[k * (ST / 32) + warp] = __popc(who[k]);
         }
+        float v[VPT];                                  // the kept weights, all read before one is written (in place)
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) v[k] = who[k] >> lane & 1 ? w[k * ST + t] : 0.f;
+        __syncthreads();
+        if (warp == 0) warp_scan<VPT * ST / 32>(count);
         __syncthreads();
 #pragma unroll
-        for (int k = 0; k < STEP; ++k) {
-            const int i = i0 + k * ST + t;
-            if (i < kept) ow[i] = v[k];
+        for (int k = 0; k < VPT; ++k) {
+            if (!(who[k] >> lane & 1)) continue;
+            const int at = count[k * (ST / 32) + warp] + __popc(who[k] & ((1u << lane) - 1));
+            rows[at] = k * ST + t;
+            ow[at] = v[k];
         }
+    } else {                                           // a warp's stretch of rows: count, scan, write
+        const int per = (len + ST - 1) / ST * 32, j_lo = min(len, warp * per), j_hi = min(len, j_lo + per);
+        int n = 0;
+#pragma unroll 4
+        for (int j = j_lo; j < j_hi; j += 32) n += __popc(__ballot_sync(0xffffffffu, keeps(j + lane, rank_of(j + lane))));
+        if (lane == 0) count[warp] = n;
+        if (t >= ST / 32 && t < 32) count[t] = 0;
+        __syncthreads();
+        if (warp == 0) warp_scan<32>(count);
+        __syncthreads();
+        int at = count[warp];
+#pragma unroll 4
+        for (int j = j_lo; j < j_hi; j += 32) {
+            const bool k = keeps(j + lane, rank_of(j + lane));
+            const unsigned who = __ballot_sync(0xffffffffu, k);
+            if (k) rows[at + __popc(who & ((1u << lane) - 1))] = j + lane;
+            at += __popc(who);
+        }
+        __syncthreads();
+        // the kept rows' weights; in place a weight moves down (rows[i] >= i), so a step reads before it writes
+        constexpr int STEP = 4;
+        for (int i0 = 0; i0 < kept; i0 += STEP * ST) {
+            float x[STEP];
+#pragma unroll
+            for (int k = 0; k < STEP; ++k) {
+                const int i = i0 + k * ST + t;
+                x[k] = i < kept ? w[rows[i]] : 0.f;
+            }
+            __syncthreads();
+#pragma unroll
+            for (int k = 0; k < STEP; ++k) {
+                const int i = i0 + k * ST + t;
+                if (i < kept) ow[i] = x[k];
+            }
+        }
+        __syncthreads();
     }
-    __syncthreads();
+    for (int j = kept + t; j < a.e.keep; j += ST) rows[j] = -1;
     for (int j = kept + t; j < len; j += ST) ow[j] = 0.f;
 }
 
-// NP 16-byte vectors of codes per thread: a page of P rows is P * hd / 16 = tpb * NP vectors
-template <int NP>
-__global__ void __launch_bounds__(MT) kv8_move_kernel(const EvictArgs a, int tpb, int ranges) {
-    __shared__ float sm[2][MT / 32];
+__global__ void __launch_bounds__(ST, 2) kv8_select_kernel(const EvictArgs a) {
     grid_dep_launch();
     grid_dep_wait();
-    const int g = blockIdx.y % a.Hkv, lk = blockIdx.y / a.Hkv, s = blockIdx.z, t = threadIdx.x;
+    const int g = blockIdx.x, s = blockIdx.y, l = blockIdx.z;
+    const int len = kv8_len(a.q, s);
+    if (len < 0 || len > a.q.max_len) {
+        if (threadIdx.x == 0) atomicOr(a.q.status, ST_BAD_ROW);
+        return;
+    }
+    const int64_t seg = ((int64_t)l * a.q.n + s) * a.Hkv + g;
+    const float* w = a.e.weights + seg * a.e.weights_ld;
+    float* ow = a.e.out_weights + seg * a.e.weights_ld;
+    int* rows = a.e.out_rows + seg * a.e.keep;
+    if (len <= ST * VPT) select_rows<true>(a, w, ow, rows, len);
+    else select_rows<false>(a, w, ow, rows, len);
+}
+
+// Codes are worked on four to a word: the conversions to and from fp16 cost several times as much.  The magnitudes of
+// codes compare as integers, and a factor 2^k adds k to every exponent field as long as all values are and stay normal;
+// zeros, subnormals and NaN go through the conversions.
+__device__ __forceinline__ unsigned largest_code(const uint4& x) {
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    unsigned m = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        m = kv8_max_u16x2(m, w[k] & 0x007f007fu);
+        m = kv8_max_u16x2(m, (w[k] >> 8) & 0x007f007fu);
+    }
+    m = max(m & 0xffffu, m >> 16);
+    if (m == 0x7f) {                                   // a NaN: the largest of the others
+        m = 0;
+        for (int k = 0; k < 4; ++k)
+            for (int n = 0; n < 32; n += 8) {
+                const unsigned c = w[k] >> n & 0x7fu;
+                if (c != 0x7f && c > m) m = c;
+            }
+    }
+    return m;
+}
+__device__ __forceinline__ void times_power(uint4& x, float from, float inv_to) {
+    uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    const float f = from * inv_to;
+    const int k = (int)(__float_as_uint(f) >> 23) - 127;
+    if (k == 0) return;
+    bool fast = f > 0.f && k >= -14 && k <= 14;
+    if (fast) {
+        const uint32_t least = (uint32_t)(k < 0 ? 1 - k : 1) * 0x08080808u;      // smallest code that stays normal
+        uint32_t all = 0x80808080u, nan = 0;
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+            all &= (w[n] | 0x80808080u) - least;
+            nan |= (w[n] & 0x7f7f7f7fu) + 0x01010101u;
+        }
+        fast = (all & 0x80808080u) == 0x80808080u && !(nan & 0x80808080u);
+    }
+    if (fast) {
+#pragma unroll
+        for (int n = 0; n < 4; ++n) w[n] += (uint32_t)k * 0x08080808u;
+    } else {
+        const Kv8Factor f2 = kv8_factor(f);
+#pragma unroll
+        for (int n = 0; n < 4; ++n) w[n] = kv8_rescale4(w[n], f2);
+    }
+    x = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// A page of P rows is P * hd / 16 vectors: NP for each of the CTA's threads (half the warp's, for 16 rows of 64)
+__global__ void __launch_bounds__(MT) kv8_move_kernel(const EvictArgs a, int vecs, int ranges) {
+    // a page's rows: index among the pool's rows of this layer's K or V (-1: none) and scale, for this page and the next
+    __shared__ int from[2][256];
+    __shared__ float scale[2][256];
+    __shared__ float sm[MT / 32];
+    grid_dep_launch();
+    grid_dep_wait();
+    const int g = blockIdx.y % a.Hkv, lk = blockIdx.y / a.Hkv, s = blockIdx.z, t = threadIdx.x, threads = blockDim.x;
     const int l = lk >> 1, kv = lk & 1, P = 1 << a.q.shift, vpr_shift = a.hd == 128 ? 3 : 2;
     const int len = kv8_len(a.q, s);
     if (len < 0 || len > a.q.max_len) return;
     const int kept = min(len, a.e.keep), pages = (kept + P - 1) >> a.q.shift;
     // out_lens may be the lengths read above: a CTA that sees the new one finds the same `kept`
     if (blockIdx.x == 0 && blockIdx.y == 0 && t == 0) a.e.out_lens[s] = kept;
-    const int64_t seg = ((int64_t)l * a.q.n + s) * a.Hkv + g;
-    const int* rows = a.e.out_rows + seg * a.e.keep;
-    const int64_t base = (int64_t)((a.layer + l) * 2 + kv) * a.q.n_pages;
-    const int per = (pages + ranges - 1) / ranges, b_hi = min(pages, ((int)blockIdx.x + 1) * per);
-    // source of vector t + i * tpb of page b: its pool row (page * P + row in page), or -1
-    int64_t from[NP];
-    const auto sources = [&](int b) {
-        int j[NP];
-#pragma unroll
-        for (int i = 0; i < NP; ++i) {
-            const int row = b * P + ((t + i * tpb) >> vpr_shift);
-            j[i] = t < tpb && b < b_hi && row < kept ? rows[row] : -1;
-        }
-#pragma unroll
-        for (int i = 0; i < NP; ++i) {
-            const int pg = j[i] >= 0 ? kv8_page(a.q, s, j[i] >> a.q.shift) : -1;
-            from[i] = pg >= 0 ? ((int64_t)pg << a.q.shift) + (j[i] & (P - 1)) : -1;
-        }
-    };
-    int b = blockIdx.x * per, flip = 0;
-    sources(b);
-    for (; b < b_hi; ++b, flip ^= 1) {
-        uint4 x[NP];
-        float sc[NP];
-        const int n = min(P, kept - b * P);
-        const int dst = a.e.dst_table[(int64_t)s * a.e.dst_ld + b];
-#pragma unroll
-        for (int i = 0; i < NP; ++i) {
-            x[i] = make_uint4(0, 0, 0, 0);
-            sc[i] = 0.f;
-            if (from[i] >= 0) {
-                const int64_t blk = (base + (from[i] >> a.q.shift)) * a.Hkv + g;
-                x[i] = reinterpret_cast<const uint4*>(a.codes + (blk * P + (from[i] & (P - 1))) * a.hd)[(t + i * tpb) & ((1 << vpr_shift) - 1)];
-                sc[i] = a.scales[blk];
+    const int* rows = a.e.out_rows + (((int64_t)l * a.q.n + s) * a.Hkv + g) * a.e.keep;
+    const int64_t base = (int64_t)((a.layer + l) * 2 + kv) * a.q.n_pages * a.Hkv;
+    uint8_t* codes = a.codes + base * P * a.hd;
+    float* scales = a.scales + base;
+    const int per = (pages + ranges - 1) / ranges, b_lo = blockIdx.x * per, b_hi = min(pages, b_lo + per);
+    // Rows of a page by thread: the addresses go to shared memory at once, the scales, which only the next step needs,
+    // when the codes have been asked for.
+    float sc = 0.f;                                    // (there are at least as many threads as rows)
+    const auto resolve = [&](int b, int buf) {
+        int at = -1;
+        sc = 0.f;
+        if (t < P && b * P + t < kept) {
+            const int j = rows[b * P + t], pg = kv8_page(a.q, s, j >> a.q.shift);
+            if (pg >= 0) {
+                at = (pg * a.Hkv + g) * P + (j & (P - 1));
+                sc = scales[pg * a.Hkv + g];
             }
         }
-        sources(b + 1);
+        if (t < P) from[buf][t] = at;
+    };
+    if (b_lo >= b_hi) return;
+    resolve(b_lo, 0);
+    for (int b = b_lo, buf = 0; b < b_hi; ++b, buf ^= 1) {
+        const int dst = a.e.dst_table[(int64_t)s * a.e.dst_ld + b];
+        __syncthreads();                               // this page's addresses are there, the page before is written
+        uint4 x[NP];
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+            const int v = t + i * threads, at = v < vecs ? from[buf][v >> vpr_shift] : -1;
+            x[i] = make_uint4(0, 0, 0, 0);
+            if (at >= 0) x[i] = reinterpret_cast<const uint4*>(codes + (int64_t)at * a.hd)[v & ((1 << vpr_shift) - 1)];
+        }
+        if (t < P) scale[buf][t] = sc;
+        if (b + 1 < b_hi) resolve(b + 1, buf ^ 1);
+        __syncthreads();
         float top = 0.f;
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
-            // the largest code without its sign (a NaN code counts as 0), times the scale
-            const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-            uint32_t m = 0;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                uint32_t c = w[k] & 0x7f7f7f7fu;
-                c &= ~__vcmpeq4(c, 0x7f7f7f7fu);
-                m = __vmaxu4(m, c);
-            }
-            m = __vmaxu4(m, m >> 16);
-            m = __vmaxu4(m, m >> 8);
-            top = fmaxf(top, kv8_value2(m & 0xffu).x * sc[i]);
+            const int v = t + i * threads;
+            top = fmaxf(top, kv8_value2(largest_code(x[i])).x * (v < vecs ? scale[buf][v >> vpr_shift] : 0.f));
         }
         top = warp_max(top);
-        if ((t & 31) == 0) sm[flip][t >> 5] = top;
+        if ((t & 31) == 0) sm[t >> 5] = top;
         __syncthreads();                               // also: every row of this page has been read
-        for (int i = 0; i < MT / 32; ++i) top = fmaxf(top, sm[flip][i]);
+        for (int i = 0; i < threads / 32; ++i) top = fmaxf(top, sm[i]);
         const float ns = kv8_scale(top), inv = kv8_inverse(ns);
         if (dst < 0 || dst >= a.q.n_pages) {
             if (t == 0) atomicOr(a.q.status, ST_BAD_ROW);
             continue;
         }
-        const int64_t blk = (base + dst) * a.Hkv + g;
+        const int n = min(P, kept - b * P), blk = dst * a.Hkv + g;
+        uint4* out = reinterpret_cast<uint4*>(codes + (int64_t)blk * P * a.hd);
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
-            const int v = t + i * tpb;
-            if (t >= tpb || (v >> vpr_shift) >= n) continue;
-            if (sc[i] != ns) {
-                const float f = sc[i] * inv;
-                x[i].x = kv8_rescale4(x[i].x, f);
-                x[i].y = kv8_rescale4(x[i].y, f);
-                x[i].z = kv8_rescale4(x[i].z, f);
-                x[i].w = kv8_rescale4(x[i].w, f);
-            }
-            reinterpret_cast<uint4*>(a.codes + blk * P * a.hd)[v] = x[i];
+            const int v = t + i * threads, row = v >> vpr_shift;
+            if (v >= vecs || row >= n) continue;
+            times_power(x[i], scale[buf][row], inv);
+            out[v] = x[i];
         }
-        if (t == 0) a.scales[blk] = ns;
+        if (t == 0) scales[blk] = ns;
     }
 }
 
@@ -257,20 +359,16 @@ cudaError_t launch_kv8_evict(const Kv8& c, const Kv8Seqs& q, const Kv8Evict& e, 
     if (q.n == 0 || n_layers == 0) return cudaSuccess;
     const cudaError_t err = launch_ex(c.pdl, kv8_select_kernel, dim3(a.Hkv, q.n, n_layers), dim3(ST), 0, s, a);
     if (err != cudaSuccess) return err;
-    const int P = 1 << q.shift, vecs = P * a.hd / 16;
-    const int tpb = vecs < MT ? vecs : MT, np = vecs / tpb;             // 64 .. 2048 vectors
+    const int P = 1 << q.shift, vecs = P * a.hd / 16;                    // 64 .. 2048 vectors
+    const int threads = vecs / NP < 32 ? 32 : vecs / NP;                 // P or 2 P, at least 32
     const int pages = ((e.keep < q.max_len ? e.keep : q.max_len) + P - 1) / P;
-    // in place the pages of a head are done in order by one CTA; between two tables each has its own
+    // In place the pages of a head are done in order by one CTA.  Between two tables they are divided until there are 24
+    // CTAs per SM: a CTA that has several looks up the next one's rows while it moves one (8K to 2K, 32 layers: one page
+    // per CTA 57 us, four 53 us).
     const bool in_place = e.dst_table == q.table && e.dst_ld == q.table_ld;
-    const int ranges = in_place || pages == 0 ? 1 : pages;
-    const dim3 grid(ranges, 2 * n_layers * a.Hkv, q.n);
-    switch (np) {
-        case 1: return launch_ex(c.pdl, kv8_move_kernel<1>, grid, dim3(MT), 0, s, a, tpb, ranges);
-        case 2: return launch_ex(c.pdl, kv8_move_kernel<2>, grid, dim3(MT), 0, s, a, tpb, ranges);
-        case 4: return launch_ex(c.pdl, kv8_move_kernel<4>, grid, dim3(MT), 0, s, a, tpb, ranges);
-        case 8: return launch_ex(c.pdl, kv8_move_kernel<8>, grid, dim3(MT), 0, s, a, tpb, ranges);
-        default: return launch_ex(c.pdl, kv8_move_kernel<16>, grid, dim3(MT), 0, s, a, tpb, ranges);
-    }
+    const int64_t heads = (int64_t)2 * n_layers * a.Hkv * q.n, most = ((int64_t)24 * c.num_sms + heads - 1) / heads;
+    const int ranges = in_place || pages == 0 ? 1 : (int)(pages < most ? pages : most);
+    return launch_ex(c.pdl, kv8_move_kernel, dim3(ranges, 2 * n_layers * a.Hkv, q.n), dim3(threads), 0, s, a, vecs, ranges);
 }
 
 }  // namespace cb
