@@ -1,0 +1,216 @@
+// What the two kernels of attention over the 8-bit cache share: their arguments and the list of tiles that divides the
+// work.  An item is (sequence, tile of QT query rows, KV head), cut into tiles of 128 keys; the tiles of all items form one
+// list, in this order, and every CTA takes an equal, contiguous piece of it.  An item that spans CTAs leaves a partial
+// result per CTA; the CTA that finishes last joins them in their order.
+#pragma once
+#include <climits>
+
+#include "cb_kv8.cuh"
+#include "cb_ptx.cuh"
+
+namespace cb {
+
+namespace {
+
+constexpr int TK = 128;                  // keys per tile
+
+__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+struct AttnArgs {
+    Kv8Seqs q;
+    Kv8Rows r;
+    Kv8Attn a;
+    const float* ks;                     // this layer's scales [n_pages][Hkv]
+    const float* vs;
+    int Hq, Hkv, G, QT;                  // QT = query rows per item
+    int kz;                              // z coordinate of this layer's K in the map (V is kz + 1)
+    int box;                             // rows of a TMA box: min(page_size, 128)
+    int min_tiles;                       // tiles per CTA, at least
+    float* part;                         // [cta][2][NC][HD + 2] pieces of items that span CTAs
+    unsigned* arrived;                   // [cta] pieces finished of the item that begins in this CTA (0 between calls)
+    float* scores;                       // weights: [Hkv][n_q][G][score_ld] scores in the exp2 domain
+    int score_ld;
+    float2* stats;                       // weights: [Hkv][n_q][G] (max, 1 / sum)
+};
+
+__device__ __forceinline__ float exp2_fast(float x) {          // special-function unit, about 2 ulp
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// ------------------------------------------------------------------------------------------------
+// the list of tiles
+// ------------------------------------------------------------------------------------------------
+struct Seq {                             // one sequence: its query rows and length
+    int r0, n, len;
+    __device__ __forceinline__ int q_tiles(int QT) const { return (n + QT - 1) / QT; }
+    // keys that the last row of query tile qt sees
+    __device__ __forceinline__ int visible(int qt, int QT) const { return max(0, len - n + min((qt + 1) * QT, n)); }
+    __device__ __forceinline__ int tiles(int qt, int QT) const { return max(1, (visible(qt, QT) + TK - 1) / TK); }
+};
+__device__ __forceinline__ Seq seq_at(const AttnArgs& p, int s) {
+    Seq q;
+    int r1;
+    if (!kv8_rows(p.q, p.r, s, q.r0, r1, q.len)) return Seq{0, 0, 0};
+    q.n = r1 - q.r0;
+    return q;
+}
+__device__ __forceinline__ long long seq_tiles(const AttnArgs& p, const Seq& q) {
+    long long t = 0;
+    for (int qt = 0; qt < q.q_tiles(p.QT); ++qt) t += q.tiles(qt, p.QT);
+    return t * p.Hkv;
+}
+
+// A position in the list: item (s, qt, g) and tile t of its nt.
+struct Cursor {
+    int s, qt, g, t, nt;
+    Seq q;
+    __device__ __forceinline__ void settle(const AttnArgs& p) { nt = q.tiles(qt, p.QT); }
+    // to the first tile of the next item
+    __device__ __forceinline__ void next_item(const AttnArgs& p) {
+        t = 0;
+        if (++g < p.Hkv) return;
+        g = 0;
+        if (++qt >= q.q_tiles(p.QT)) {
+            qt = 0;
+            do {
+                q = ++s < p.q.n ? seq_at(p, s) : Seq{0, 1, 0};
+            } while (q.n == 0);
+        }
+        settle(p);
+    }
+};
+
+// Joins one row of an item's pieces in their order, by a warp: piece u holds the row's HD sums at offset `row` and its
+// (maximum, sum) at offset `stat` of piece_at(u).  Lanes below HD / 4 return four dims each, every lane the joint m and l.
+template <int HD, typename F>
+__device__ __forceinline__ float4 join_pieces(const F& piece_at, int n_pieces, int row, int stat, float& m, float& l) {
+    constexpr int LANES = HD / 4, SIDE = 32 / LANES;             // lanes of a row; pieces side by side
+    const int lane = threadIdx.x & 31, side = lane / LANES, d = (lane % LANES) * 4;
+    m = -INFINITY;
+    for (int u = lane; u < n_pieces; u += 32) m = fmaxf(m, __ldcg(piece_at(u) + stat));
+    m = warp_max(m);
+    l = 0.f;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int ub = 0; ub < n_pieces; ub += 32) {
+        float f = 0.f;
+        if (ub + lane < n_pieces) {
+            const float2 ml = __ldcg(reinterpret_cast<const float2*>(piece_at(ub + lane) + stat));
+            f = ml.x == -INFINITY ? 0.f : exp2_fast(ml.x - m);
+            l = fmaf(ml.y, f, l);
+        }
+        const int n = min(32, n_pieces - ub);
+        for (int v0 = 0; v0 < n; v0 += 8 * SIDE) {
+            float4 o[8];
+#pragma unroll
+            for (int v = 0; v < 8; ++v) {
+                const int u = v0 + v * SIDE + side;
+                o[v] = u < n ? __ldcg(reinterpret_cast<const float4*>(piece_at(ub + u) + row + d)) : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+#pragma unroll
+            for (int v = 0; v < 8; ++v) {
+                const float w = __shfl_sync(0xffffffffu, f, (v0 + v * SIDE + side) & 31);
+                a.x = fmaf(o[v].x, w, a.x);
+                a.y = fmaf(o[v].y, w, a.y);
+                a.z = fmaf(o[v].z, w, a.z);
+                a.w = fmaf(o[v].w, w, a.w);
+            }
+        }
+    }
+    l = warp_sum(l);
+    if (SIDE == 2) {
+        a.x += __shfl_xor_sync(0xffffffffu, a.x, 16);
+        a.y += __shfl_xor_sync(0xffffffffu, a.y, 16);
+        a.z += __shfl_xor_sync(0xffffffffu, a.z, 16);
+        a.w += __shfl_xor_sync(0xffffffffu, a.w, 16);
+    }
+    return a;
+}
+// four dims of a result row: a * inv, or 0 for a row that sees nothing
+template <typename T> __device__ __forceinline__ void store4(T* o, const float4& a, float inv, bool sees) {
+    o[0] = from_f<T>(sees ? a.x * inv : 0.f);
+    o[1] = from_f<T>(sees ? a.y * inv : 0.f);
+    o[2] = from_f<T>(sees ? a.z * inv : 0.f);
+    o[3] = from_f<T>(sees ? a.w * inv : 0.f);
+}
+
+// This CTA's piece of the list: tiles t0 .. t0 + count - 1, `per` for every CTA but the last.
+struct Piece {
+    long long per, t0;
+    int count;
+};
+struct Find {                            // shared memory of find_piece
+    int s, qt, g, t;
+    Seq q;
+    long long sums[32];
+};
+
+// Finds it and the cursor at its first tile, THREADS sequences at a time (the first step's are kept); before and after run
+// around the first barrier, which also publishes what the caller has set up in shared memory.
+template <int THREADS, typename F, typename H>
+__device__ __forceinline__ void find_piece(const AttnArgs& p, Find& f, Piece& mine, Cursor& cur, F before_sync, H after_sync) {
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const Seq q_own = tid < p.q.n ? seq_at(p, tid) : Seq{0, 0, 0};
+    const long long t_own = seq_tiles(p, q_own);
+    {
+        long long sum = t_own;
+        for (int s = tid + THREADS; s < p.q.n; s += THREADS) sum += seq_tiles(p, seq_at(p, s));
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if (lane == 0) f.sums[warp] = sum;
+    }
+    before_sync();
+    __syncthreads();
+    after_sync();
+    long long total = 0;
+    for (int w = 0; w < THREADS / 32; ++w) total += f.sums[w];
+    mine.per = max((total + gridDim.x - 1) / gridDim.x, (long long)p.min_tiles);
+    mine.t0 = blockIdx.x * mine.per;
+    mine.count = (int)min(mine.per, max(0ll, total - mine.t0));
+    if (mine.count == 0) return;
+    long long base = 0;                                          // tiles of the sequences before this step's
+    for (int s0 = 0; s0 < p.q.n; s0 += THREADS) {
+        const int s = s0 + tid;
+        const Seq q = s0 == 0 ? q_own : (s < p.q.n ? seq_at(p, s) : Seq{0, 0, 0});
+        const long long n = s0 == 0 ? t_own : seq_tiles(p, q);
+        long long x = n;
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += y;
+        }
+        __syncthreads();                                         // sums has been read
+        if (lane == 31) f.sums[warp] = x;
+        __syncthreads();
+        long long before = base, all = base;
+        for (int w = 0; w < THREADS / 32; ++w) {
+            if (w < warp) before += f.sums[w];
+            all += f.sums[w];
+        }
+        before += x - n;
+        if (n > 0 && before <= mine.t0 && mine.t0 < before + n) {
+            long long left = mine.t0 - before;
+            int qt = 0, nt = q.tiles(0, p.QT);
+            while (left >= (long long)nt * p.Hkv) {
+                left -= (long long)nt * p.Hkv;
+                nt = q.tiles(++qt, p.QT);
+            }
+            f.s = s;
+            f.qt = qt;
+            f.g = (int)(left / nt);
+            f.t = (int)(left % nt);
+            f.q = q;
+        }
+        if (all > mine.t0) break;
+        base = all;
+    }
+    __syncthreads();
+    cur.s = f.s;
+    cur.qt = f.qt;
+    cur.g = f.g;
+    cur.t = f.t;
+    cur.q = f.q;
+    cur.settle(p);
+}
+
+}  // namespace
+
+}  // namespace cb

@@ -34,46 +34,21 @@
 #include <cstring>
 #include <iterator>
 
-#include "cb_kv8.cuh"
-#include "cb_ptx.cuh"
+#include "cb_kv8_attn.cuh"
 
 namespace cb {
 
 namespace {
 
-constexpr int TK = 128;                  // keys per tile
-
-struct AttnArgs {
-    Kv8Seqs q;
-    Kv8Rows r;
-    Kv8Attn a;
-    const float* ks;                     // this layer's scales [n_pages][Hkv]
-    const float* vs;
-    int Hq, Hkv, G, QT;                  // QT = query rows per item
-    int kz;                              // z coordinate of this layer's K in the map (V is kz + 1)
-    int box;                             // rows of a TMA box: min(page_size, 128)
-    int min_tiles;                       // tiles per CTA, at least
-    float* part;                         // [cta][2][NC][HD + 2] pieces of items that span CTAs
-    unsigned* arrived;                   // [cta] pieces finished of the item that begins in this CTA (0 between calls)
-    float* scores;                       // weights: [Hkv][n_q][G][score_ld] scores in the exp2 domain
-    int score_ld;
-    float2* stats;                       // weights: [Hkv][n_q][G] (max, 1 / sum)
-};
 
 constexpr int round16(int x) { return (x + 15) / 16 * 16; }
 constexpr int pow2_cols(int x) { return x <= 32 ? 32 : x <= 64 ? 64 : x <= 128 ? 128 : x <= 256 ? 256 : 512; }
 
-__device__ __forceinline__ float exp2_fast(float x) {          // special-function unit, about 2 ulp
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 __device__ __forceinline__ float redux_max(float v) {
     float r;
     asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
     return r;
 }
-__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 // D[tmem] (+)= A[smem] B[smem]^T, e4m3 operands, fp32 accumulator; one thread issues it
 __device__ __forceinline__ void mma_e4m3(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
@@ -142,49 +117,6 @@ __device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* map, int
         : "memory");
 }
 
-// ------------------------------------------------------------------------------------------------
-// the list of tiles
-// ------------------------------------------------------------------------------------------------
-struct Seq {                             // one sequence: its query rows and length
-    int r0, n, len;
-    __device__ __forceinline__ int q_tiles(int QT) const { return (n + QT - 1) / QT; }
-    // keys that the last row of query tile qt sees
-    __device__ __forceinline__ int visible(int qt, int QT) const { return max(0, len - n + min((qt + 1) * QT, n)); }
-    __device__ __forceinline__ int tiles(int qt, int QT) const { return max(1, (visible(qt, QT) + TK - 1) / TK); }
-};
-__device__ __forceinline__ Seq seq_at(const AttnArgs& p, int s) {
-    Seq q;
-    int r1;
-    if (!kv8_rows(p.q, p.r, s, q.r0, r1, q.len)) return Seq{0, 0, 0};
-    q.n = r1 - q.r0;
-    return q;
-}
-__device__ __forceinline__ long long seq_tiles(const AttnArgs& p, const Seq& q) {
-    long long t = 0;
-    for (int qt = 0; qt < q.q_tiles(p.QT); ++qt) t += q.tiles(qt, p.QT);
-    return t * p.Hkv;
-}
-
-// A position in the list: item (s, qt, g) and tile t of its nt.
-struct Cursor {
-    int s, qt, g, t, nt;
-    Seq q;
-    __device__ __forceinline__ void settle(const AttnArgs& p) { nt = q.tiles(qt, p.QT); }
-    // to the first tile of the next item
-    __device__ __forceinline__ void next_item(const AttnArgs& p) {
-        t = 0;
-        if (++g < p.Hkv) return;
-        g = 0;
-        if (++qt >= q.q_tiles(p.QT)) {
-            qt = 0;
-            do {
-                q = ++s < p.q.n ? seq_at(p, s) : Seq{0, 1, 0};
-            } while (q.n == 0);
-        }
-        settle(p);
-    }
-};
-
 constexpr int MAX_STAGES = 3;
 constexpr int RING = 8;                  // tiles whose scales may be under way or in use
 constexpr int LOOK = 2;                  // tiles by which the scales are asked for ahead of the codes
@@ -196,10 +128,8 @@ struct Shared {
     uint64_t p_full, o_full, q_full, drain;
     uint32_t tmem;
     int abort;
-    int s0, qt0, g0, tile0;              // where this CTA begins
-    Seq seq0;
+    Find find;
     int last;                            // this CTA joins the item
-    long long sums[32];
 };
 
 // ------------------------------------------------------------------------------------------------
@@ -346,71 +276,12 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
 
     grid_dep_launch();
     grid_dep_wait();                                     // lengths, tables, queries and the cache of the kernels before
-    // ---- this CTA's piece of the list, THREADS sequences at a time (the first step's are kept)
-    const Seq q_own = tid < p.q.n ? seq_at(p, tid) : Seq{0, 0, 0};
-    const long long t_own = seq_tiles(p, q_own);
-    {
-        long long mine = t_own;
-        for (int s = tid + THREADS; s < p.q.n; s += THREADS) mine += seq_tiles(p, seq_at(p, s));
-        for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-        if (lane == 0) c.sums[warp] = mine;
-    }
-    ptx::tc_fence_before();
-    __syncthreads();
-    ptx::tc_fence_after();
-    long long total = 0;
-    for (int w = 0; w < THREADS / 32; ++w) total += c.sums[w];
-    const long long per = max((total + gridDim.x - 1) / gridDim.x, (long long)p.min_tiles);
-    const long long t0 = blockIdx.x * per;
-    const int count = (int)min(per, max(0ll, total - t0));       // tiles of this CTA
-    if (count > 0) {
-        long long base = 0;                                      // tiles of the sequences before this step's
-        for (int s0 = 0; s0 < p.q.n; s0 += THREADS) {
-            const int s = s0 + tid;
-            const Seq q = s0 == 0 ? q_own : (s < p.q.n ? seq_at(p, s) : Seq{0, 0, 0});
-            const long long mine = s0 == 0 ? t_own : seq_tiles(p, q);
-            long long x = mine;
-            for (int o = 1; o < 32; o <<= 1) {
-                const long long y = __shfl_up_sync(0xffffffffu, x, o);
-                if (lane >= o) x += y;
-            }
-            __syncthreads();                                     // sums has been read
-            if (lane == 31) c.sums[warp] = x;
-            __syncthreads();
-            long long before = base, all = base;
-            for (int w = 0; w < THREADS / 32; ++w) {
-                if (w < warp) before += c.sums[w];
-                all += c.sums[w];
-            }
-            before += x - mine;
-            if (mine > 0 && before <= t0 && t0 < before + mine) {
-                long long left = t0 - before;
-                int qt = 0, nt = q.tiles(0, p.QT);
-                while (left >= (long long)nt * p.Hkv) {
-                    left -= (long long)nt * p.Hkv;
-                    nt = q.tiles(++qt, p.QT);
-                }
-                c.s0 = s;
-                c.qt0 = qt;
-                c.g0 = (int)(left / nt);
-                c.tile0 = (int)(left % nt);
-                c.seq0 = q;
-            }
-            if (all > t0) break;
-            base = all;
-        }
-        __syncthreads();
-    }
-    const uint32_t tmem = c.tmem;
+    Piece mine;
     Cursor cur;
-    if (count > 0) {
-        cur.s = c.s0;
-        cur.qt = c.qt0;
-        cur.g = c.g0;
-        cur.t = c.tile0;
-        cur.q = c.seq0;
-        cur.settle(p);
-    }
+    find_piece<THREADS>(p, c.find, mine, cur, [] { ptx::tc_fence_before(); }, [] { ptx::tc_fence_after(); });
+    const long long per = mine.per, t0 = mine.t0;
+    const int count = mine.count;                        // tiles of this CTA
+    const uint32_t tmem = c.tmem;
 
     if (warp == TMA_WARP) {
         // ------------------------------------------------------------------------------------ TMA
@@ -781,57 +652,11 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
                 }
                 ptx::named_bar_sync(1, SOFT);
                 if (c.last) {                                    // join the pieces in their order, a warp per column
-                    constexpr int LANES = HD / 4, SIDE = 32 / LANES;         // lanes of a row; rows side by side
-                    const int side = lane / LANES, d = (lane % LANES) * 4;
                     for (int k = warp; k < cols; k += SOFT / 32) {
-                        float m = -INFINITY;
-                        for (int u = lane; u < n_pieces; u += 32) m = fmaxf(m, __ldcg(piece_at(u) + NC * HD + 2 * k));
-                        m = warp_max(m);
-                        float l = 0.f;
-                        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-                        for (int ub = 0; ub < n_pieces; ub += 32) {
-                            float f = 0.f;
-                            if (ub + lane < n_pieces) {
-                                const float2 ml = __ldcg(reinterpret_cast<const float2*>(piece_at(ub + lane) + NC * HD + 2 * k));
-                                f = ml.x == -INFINITY ? 0.f : exp2_fast(ml.x - m);
-                                l = fmaf(ml.y, f, l);
-                            }
-                            const int n = min(32, n_pieces - ub);
-                            for (int v0 = 0; v0 < n; v0 += 8 * SIDE) {
-                                float4 o[8];
-#pragma unroll
-                                for (int v = 0; v < 8; ++v) {
-                                    const int u = v0 + v * SIDE + side;
-                                    o[v] = u < n ? __ldcg(reinterpret_cast<const float4*>(piece_at(ub + u) + k * HD + d))
-                                                 : make_float4(0.f, 0.f, 0.f, 0.f);
-                                }
-#pragma unroll
-                                for (int v = 0; v < 8; ++v) {
-                                    const float w = __shfl_sync(0xffffffffu, f, (v0 + v * SIDE + side) & 31);
-                                    a.x = fmaf(o[v].x, w, a.x);
-                                    a.y = fmaf(o[v].y, w, a.y);
-                                    a.z = fmaf(o[v].z, w, a.z);
-                                    a.w = fmaf(o[v].w, w, a.w);
-                                }
-                            }
-                        }
-                        l = warp_sum(l);
-                        if (SIDE == 2) {
-                            a.x += __shfl_xor_sync(0xffffffffu, a.x, 16);
-                            a.y += __shfl_xor_sync(0xffffffffu, a.y, 16);
-                            a.z += __shfl_xor_sync(0xffffffffu, a.z, 16);
-                            a.w += __shfl_xor_sync(0xffffffffu, a.w, 16);
-                        }
-                        const float inv = 1.f / l;
-                        const bool sees = pos0 + k / p.G >= 0;
-                        if (side == 0) {
-                            T* o = out_at(k) + d;
-                            o[0] = from_f<T>(sees ? a.x * inv : 0.f);
-                            o[1] = from_f<T>(sees ? a.y * inv : 0.f);
-                            o[2] = from_f<T>(sees ? a.z * inv : 0.f);
-                            o[3] = from_f<T>(sees ? a.w * inv : 0.f);
-                        }
-                        if (p.scores && lane == 0) p.stats[stat0 + k] = make_float2(m, inv);
+                        float m, l;
+                        const float4 a = join_pieces<HD>(piece_at, n_pieces, k * HD, NC * HD + 2 * k, m, l);
+                        if (lane < HD / 4) store4(out_at(k) + lane * 4, a, 1.f / l, pos0 + k / p.G >= 0);
+                        if (p.scores && lane == 0) p.stats[stat0 + k] = make_float2(m, 1.f / l);
                     }
                 }
             }
@@ -900,7 +725,6 @@ template <int HD> using C4 = Shape<HD, 4, 1, 2, 3, 3, 2>;
 template <int HD> using C8 = Shape<HD, 8, 1, 2, 3, 2, 3>;
 template <int HD> using C16 = Shape<HD, 16, 2, 2, 3, 2, 2>;
 template <int HD> using C32 = Shape<HD, 32, 4, 2, 3, 1, 3>;
-template <int HD> using C64 = Shape<HD, 64, 4, 2, 3, 1, 3>;
 template <int HD> using F4 = Shape<HD, 4, 1, 6, 6, 2, 3>;
 template <int HD> using F8 = Shape<HD, 8, 1, 6, 6, 2, 2>;
 
@@ -911,8 +735,7 @@ template <int HD> cudaError_t launch_dim(const Kv8& c, AttnArgs& p, cudaStream_t
         if (need <= 4) return launch_shape<bf16, C4<HD>>(c, p, s);
         if (need <= 8) return launch_shape<bf16, C8<HD>>(c, p, s);
         if (need <= 16) return launch_shape<bf16, C16<HD>>(c, p, s);
-        if (need <= 32) return launch_shape<bf16, C32<HD>>(c, p, s);
-        return launch_shape<bf16, C64<HD>>(c, p, s);
+        return launch_shape<bf16, C32<HD>>(c, p, s);
     }
     return need <= 4 ? launch_shape<float, F4<HD>>(c, p, s) : launch_shape<float, F8<HD>>(c, p, s);
 }
@@ -922,9 +745,9 @@ template <int HD> cudaError_t launch_dim(const Kv8& c, AttnArgs& p, cudaStream_t
 // scratch: two pieces for every CTA of the largest launch
 template <typename S> constexpr size_t pieces() { return (size_t)S::CTAS * 2 * S::PIECE; }
 size_t kv8_part_floats(int num_sms) {
-    const size_t sizes[] = {pieces<C4<128>>(), pieces<C8<128>>(), pieces<C16<128>>(), pieces<C32<128>>(), pieces<C64<128>>(),
+    const size_t sizes[] = {pieces<C4<128>>(), pieces<C8<128>>(), pieces<C16<128>>(), pieces<C32<128>>(),
                             pieces<F4<128>>(), pieces<F8<128>>()};
-    return *std::max_element(std::begin(sizes), std::end(sizes)) * num_sms;
+    return std::max(*std::max_element(std::begin(sizes), std::end(sizes)) * num_sms, kv8_rows_part_floats(num_sms));
 }
 int kv8_most_ctas(int num_sms) { return 3 * num_sms; }
 
@@ -967,7 +790,10 @@ cudaError_t launch_kv8_attention(const Kv8& c, const Kv8Seqs& q, const Kv8Rows& 
     p.stats = c.stats;
     p.score_ld = (q.max_len + TK - 1) / TK * TK;
     if (r.n_rows > 0) {
-        const cudaError_t e = c.cfg.head_dim == 128 ? launch_dim<128>(c, p, s) : launch_dim<64>(c, p, s);
+        const int rows = (r.n_rows + q.n - 1) / q.n;             // of a sequence, on average
+        const bool many = c.cfg.dtype == CB_BF16 && rows * p.G > 32;
+        const cudaError_t e = many ? launch_kv8_rows(c, &p, layer, s)
+                                   : c.cfg.head_dim == 128 ? launch_dim<128>(c, p, s) : launch_dim<64>(c, p, s);
         if (e != cudaSuccess) return e;
     }
     if (a.weights && q.max_len > 0) {

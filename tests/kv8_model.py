@@ -96,9 +96,10 @@ class Model:
     def attention(self, table, lens, q, starts, layer, scale):
         """out [n_q][Hq][hd], weights list of [H][len] per sequence, and for error bounds: spread, sum p|v|
         [n_q][Hq][hd]; the largest sum |q k| scale of any row and key; self.floor [n_q][Hq][hd], the sum over tiles of
-        128 keys of (largest p * scale of V in the tile) * (sum of |codes of V|)."""
+        128 keys of (largest p * scale of V in the tile) * (sum of |codes of V|); self.floor_all, the same with all keys
+        as one tile."""
         out, spread = np.zeros(q.shape), np.zeros(q.shape)
-        self.floor = np.zeros(q.shape)
+        self.floor, self.floor_all = np.zeros(q.shape), np.zeros(q.shape)
         ws, big = [], 0.0
         G = q.shape[1] // self.H
         for s, n in enumerate(lens):
@@ -124,6 +125,7 @@ class Model:
                     w[h // G, :seen] += p
                     ss = sv[:seen, h // G]
                     code = np.abs(vv) / np.where(ss > 0, ss, 1.0)[:, None]
+                    self.floor_all[i, h] = (p * ss).max() * code.sum(axis=0)
                     for t in range(0, seen, 128):
                         self.floor[i, h] += (p * ss)[t:t + 128].max() * code[t:t + 128].sum(axis=0)
             ws.append(w)

@@ -14,7 +14,10 @@ scaled so that the largest of a tile of 128 keys lies between 128 and 256.  A te
 below the terms' range is off by at most half of it in the last term, 2^-10 16^-(T-1): relative to the tile's largest
 p * scale, Y >= 128 in those units, at most 2^-17 16^-(T-1), that is 2^-25 for T = 3 (bf16) and 2^-37 for T = 6 (fp32).
 An output element meets it once per key, times the key's code: 2^-25 or 2^-37 of the sum over tiles of
-Y sum|code| (the model's `floor`).  It shows only where keys of one tile differ by 2^14 and more in p * scale."""
+Y sum|code| (the model's `floor`).  It shows only where keys of one tile differ by 2^14 and more in p * scale.
+With many query rows (bf16, more than 32 rows times heads of a group) p times the scale is an fp16 number, 2^7 times its
+size relative to a reference that is at most the largest so far: half of fp16's last place is 2^-25, so an element is off
+by at most 2^-32 of (largest p * scale) * sum|code| over all keys (`floor_all`), besides 2^-12 of p."""
 import numpy as np
 import pytest
 
@@ -218,7 +221,7 @@ def check_attention(c, q, q64, starts, out, w=None, layer=0, w_before=0.0, scale
     owned = np.zeros(len(q64), bool)
     for s in range(len(c.lens)):
         owned[starts[s]:starts[s + 1]] = True
-    tol = rnd * np.abs(ref) + (2 * ds + (16 + steps) * U + p_rep) * spread + last * c.model.floor
+    tol = rnd * np.abs(ref) + (2 * ds + (16 + steps) * U + p_rep) * spread + last * c.model.floor + 2.0 ** -32 * c.model.floor_all
     err = np.abs(got - ref)[owned]
     assert np.all(err <= tol[owned] + 1e-30), (err.max(), float((err / (tol[owned] + 1e-30)).max()))
     if w is not None:
@@ -272,25 +275,26 @@ def test_attention(cb, hd, dtype, H, G, P, lens, rows):
     c.done()
 
 
-@pytest.mark.parametrize("dtype", ["bf16", "f32"])
-def test_attention_large_scores_and_scales(cb, dtype):
+@pytest.mark.parametrize("dtype,rows", [("bf16", 2), ("f32", 2), ("bf16", 25)])
+def test_attention_large_scores_and_scales(cb, dtype, rows):
     """Scores spread over hundreds (most weights vanish), a sink that outweighs the rest, and V blocks whose scales
     differ by 2^20."""
     lens = [900, 400]
-    c = Case(cb, lens, H=1, G=4, hd=128, P=16, dtype=dtype, seed=21, cells=cb.KV8Cache.cells(4, 4, 900))
+    c = Case(cb, lens, H=1, G=4, hd=128, P=16, dtype=dtype, seed=21, cells=cb.KV8Cache.cells(2 * rows, 4, 900))
     sc = c.model.scales
     sc[0, 1] = 2.0 ** c.rng.integers(-20, 1, sc[0, 1].shape)
     sc[0, 0, c.table_np[1, 0]] *= 64
     c.scales.copy_(torch.from_numpy(sc.astype(np.float32)))
-    q, q64 = c.values(4, 4, 128, size=4.0)
+    q, q64 = c.values(2 * rows, 4, 128, size=4.0)
     out = torch.empty_like(q)
     w = torch.zeros((2, 1, 900), device="cuda")
     c.cache.attention(c.table, c.lens_t, q, out, weights=w, max_len=900)
-    check_attention(c, q, q64, [0, 2, 4], out, w)
+    check_attention(c, q, q64, [0, rows, 2 * rows], out, w)
     c.done()
 
 
-def test_attention_one_key_outweighs_a_long_cache(cb):
+@pytest.mark.parametrize("rows", [1, 17])
+def test_attention_one_key_outweighs_a_long_cache(cb, rows):
     """A first key whose weight is about 2^17 times any other's, over a cache long enough for the others to count."""
     n = 20000
     c = Case(cb, [n], H=1, G=2, hd=64, P=64, seed=5)
@@ -301,19 +305,19 @@ def test_attention_one_key_outweighs_a_long_cache(cb):
     m.codes[0, 0, c.table_np[0, 0], 0, 0, 0] = 0x7E     # 448 in the first key's
     c.codes.copy_(torch.from_numpy(m.codes))
     c.scales.copy_(torch.from_numpy(m.scales.astype(np.float32)))
-    q = torch.zeros((1, 2, 64), dtype=torch.bfloat16, device="cuda")
+    q = torch.zeros((rows, 2, 64), dtype=torch.bfloat16, device="cuda")
     q[:, :, 0] = 108.0                                  # (448 - 1) * 2^-9 * 108 / 8 = 11.8 = ln 2^17
     out = torch.empty_like(q)
     c.cache.attention(c.table, c.lens_t, q, out)
-    check_attention(c, q, f64(q), [0, 1], out)
+    check_attention(c, q, f64(q), [0, rows], out)
     c.done()
 
 
-@pytest.mark.parametrize("dtype,hd", [("bf16", 128), ("f32", 64)])
-def test_nan_does_not_pass_the_mask(cb, dtype, hd):
+@pytest.mark.parametrize("dtype,hd,G", [("bf16", 128, 2), ("f32", 64, 2), ("bf16", 128, 4), ("bf16", 64, 8)])
+def test_nan_does_not_pass_the_mask(cb, dtype, hd, G):
     """NaN in the K or V of a row reaches the query rows that see it and no others."""
-    lens, rows, G = [140, 60], [20, 4], 2
-    c = Case(cb, lens, H=2, G=G, hd=hd, P=16, dtype=dtype, seed=8, cells=cb.KV8Cache.cells(24, 4, 140))
+    lens, rows = [140, 60], [20, 4]
+    c = Case(cb, lens, H=2, G=G, hd=hd, P=16, dtype=dtype, seed=8)
     m = c.model
 
     def spoil(kv, s, j, h, d):
@@ -323,7 +327,7 @@ def test_nan_does_not_pass_the_mask(cb, dtype, hd):
     spoil(1, 0, 125, 1, 5)
     spoil(0, 1, 58, 1, 0)                               # K: seen by rows 2 and 3 of the second sequence
     c.codes.copy_(torch.from_numpy(m.codes))
-    q, q64 = c.values(24, 4, hd)
+    q, q64 = c.values(24, 2 * G, hd)
     out = torch.empty_like(q)
     st = starts_of(rows)
     c.cache.attention(c.table, c.lens_t, q, out, q_start=i32(st))
@@ -373,6 +377,28 @@ def test_many_sequences(cb, G):
     tab[:, c.table.shape[1]:] = 10 ** 6                 # never read: behind every length
     c.cache.attention(tab, c.lens_t, q, out, weights=w, max_len=4000)
     check_attention(c, q, q64, list(range(91)), out, w)
+    c.done()
+
+
+@pytest.mark.parametrize("G,hd,P", [(4, 128, 16), (8, 64, 128), (5, 128, 256)])
+def test_many_rows_of_many_sequences(cb, G, hd, P):
+    """Query rows in numbers that end anywhere in a tile, over sequences of every length and some without rows or keys:
+    items of one tile and of many, divided between CTAs."""
+    rng = np.random.default_rng(G)
+    lens = [0, 1, 700, 127, 128, 129, 30, 2100, 64, 300, 1]
+    rows = [3, 1, 60, 40, 128, 2, 30, 33, 0, 90, 5]
+    n = sum(rows)
+    c = Case(cb, lens, H=2, G=G, hd=hd, P=P, seed=hd, cells=cb.KV8Cache.cells(n + 1, 2 * G, max(lens)))
+    st = starts_of(rows, 1)
+    q, q64 = c.values(n + 1, 2 * G, hd)
+    out = torch.full_like(q, 2.0)
+    w = torch.zeros((len(lens), 2, max(lens)), device="cuda")
+    c.cache.attention(c.table, c.lens_t, q, out, q_start=i32(st), weights=w, max_len=max(lens))
+    check_attention(c, q, q64, st, out, w)
+    assert torch.all(out[0] == 2.0)
+    again = torch.empty_like(out)
+    c.cache.attention(c.table, c.lens_t, q, again, q_start=i32(st), max_len=max(lens))
+    assert torch.equal(again[1:], out[1:])
     c.done()
 
 
@@ -483,6 +509,25 @@ def test_evict_long_sequence_selects_like_a_sort(cb):
 # ------------------------------------------------------------------------------------------------
 # bad ids, streams, devices
 # ------------------------------------------------------------------------------------------------
+def test_bad_pages_with_many_rows(cb):
+    """Keys of bad pages are not seen: the rows give what the remaining keys give."""
+    c = Case(cb, [192], H=1, G=4, hd=128, P=16, seed=13, cells=cb.KV8Cache.cells(12, 4, 192))
+    bad = c.table.clone()
+    bad[0, 2] = 10 ** 6
+    bad[0, 5] = -7
+    q, q64 = c.values(12, 4, 128)
+    out = torch.empty_like(q)
+    w = torch.zeros((1, 1, 192), device="cuda")
+    c.cache.attention(bad, c.lens_t, q, out, weights=w)
+    torch.cuda.synchronize()
+    assert c.cache.status(clear=True) == cb.CB_STATUS_BAD_ROW
+    assert torch.all(w[0, 0, 32:48] == 0) and torch.all(w[0, 0, 80:96] == 0)
+    c.table_np = np.delete(c.table_np, [2, 5], axis=1)
+    c.lens = [160]
+    check_attention(c, q, q64, [0, 12], out)
+    c.done()
+
+
 def test_bad_ids_are_recorded_not_faulted(cb):
     H, hd, P = 2, 64, 16
     c = Case(cb, [64, 40, 20], H=H, G=2, hd=hd, P=P, seed=12, cells=cb.KV8Cache.cells(3, 4, 64))
