@@ -160,7 +160,7 @@ cudaError_t launch_kv8_attention(const Kv8& c, const Kv8Seqs& q, const Kv8Rows& 
 size_t kv8_part_floats(int num_sms);
 size_t kv8_rows_part_floats(int num_sms);
 // many query rows per sequence (kv8_attn_rows.cu); attn_args: the AttnArgs of launch_kv8_attention
-cudaError_t launch_kv8_rows(const Kv8& c, const void* attn_args, int layer, cudaStream_t s);
+cudaError_t launch_kv8_rows(const Kv8& c, const void* attn_args, cudaStream_t s);
 int kv8_most_ctas(int num_sms);
 bool kv8_make_map(const Kv8& c, void* out);
 

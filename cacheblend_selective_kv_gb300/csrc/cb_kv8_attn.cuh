@@ -211,6 +211,126 @@ __device__ __forceinline__ void find_piece(const AttnArgs& p, Find& f, Piece& mi
     cur.settle(p);
 }
 
+// byte `b` of row `row` of a tile of codes: rows of ROW bytes in the ROW-byte swizzle
+template <int ROW> __device__ __forceinline__ uint32_t f8_at(uint32_t row, uint32_t b) {
+    return ROW == 128 ? row * 128 + ((((b >> 4) ^ row) & 7) << 4) + (b & 15)
+                      : row * 64 + ((((b >> 4) ^ (row >> 1)) & 3) << 4) + (b & 15);
+}
+
+// ------------------------------------------------------------------------------------------------
+// tiles of codes and their scales into shared memory
+// ------------------------------------------------------------------------------------------------
+// 4 bytes to shared memory; the barrier is arrived at once this thread's copies so far have landed
+__device__ __forceinline__ void cp_async4(uint32_t dst, const float* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
+        ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+        : "memory");
+}
+
+constexpr int LOOK = 2;                  // tiles by which the scales are asked for ahead of the codes
+template <int N> struct ScaleRing {      // scales of N tiles, under way or in use
+    static constexpr int SLOTS = N;
+    float scale[N][2][8];                // K's and V's scale of each box of a tile; -1: not loaded
+    uint64_t full[N];                    // one arrival per box
+};
+
+// The TMA warp: this CTA's tiles of K and V codes into rings of KS and VS stages (swizzled as the tensor map says).  A lane
+// looks after one box (at most a page) of a tile.  Its page id is loaded LOOK + 1 tiles ahead and the scales are asked for
+// LOOK tiles ahead, so that neither is waited for when memory is busy.  Rows that belong to no page of the pool or lie
+// behind the sequence's last page are not loaded.  Returns when every copy has landed.
+template <int HD, int KS, int VS, int RING>
+__device__ __forceinline__ void produce_tiles(const AttnArgs& p, const CUtensorMap& map, Cursor cur, int count, uint8_t* sK,
+                                              uint8_t* sV, uint64_t* k_full, uint64_t* k_empty, uint64_t* v_full,
+                                              uint64_t* v_empty, ScaleRing<RING>& ring, volatile int* abort) {
+    const int lane = threadIdx.x & 31, boxes = TK / p.box, rows = p.box, in_page = (1 << p.q.shift) - 1;
+    unsigned* status = p.q.status;
+    struct Ahead {
+        int page, g, off;                                        // off: first row in the page
+        bool need;                                               // the box holds rows of the sequence
+    };
+    auto look = [&](const Cursor& u) {
+        const int j = u.t * TK + lane * rows;
+        Ahead a{0, u.g, j & in_page, lane < boxes && j < u.q.len};
+        if (a.need) a.page = p.q.table[(int64_t)u.s * p.q.table_ld + (j >> p.q.shift)];
+        return a;
+    };
+    auto ask_scales = [&](Ahead& a, int i) {                     // (the page id was loaded a tile ago)
+        if (a.need && (a.page < 0 || a.page >= p.q.n_pages)) {
+            atomicOr(status, ST_BAD_ROW);
+            a.need = false;
+        }
+        if (lane >= boxes) return;
+        float* dst = &ring.scale[i % RING][0][lane];
+        const uint32_t bar = ptx::smem_u32(&ring.full[i % RING]);
+        if (a.need) {
+            const int64_t at = (int64_t)a.page * p.Hkv + a.g;
+            cp_async4(ptx::smem_u32(dst), p.ks + at);
+            cp_async4(ptx::smem_u32(dst + 8), p.vs + at);
+            cp_async_arrive(bar);
+        } else {
+            dst[0] = dst[8] = -1.f;
+            ptx::mbar_arrive(bar);
+        }
+    };
+    int k_issued = 0, v_issued = 0;
+    Ahead box[LOOK + 2];
+    int at = 0;                                                  // tile that `cur` stands at
+    auto advance = [&] {
+        if (++at < count && ++cur.t == cur.nt) cur.next_item(p);
+    };
+    if (count > 0) {
+#pragma unroll
+        for (int k = 0; k <= LOOK; ++k) {                        // tiles 0 .. LOOK
+            box[k] = look(cur);
+            if (at >= count) box[k].need = false;
+            advance();
+        }
+#pragma unroll
+        for (int k = 0; k < LOOK; ++k)
+            if (k < count) ask_scales(box[k], k);
+    }
+    for (int i = 0; i < count; ++i) {
+        box[LOOK + 1] = Ahead{0, 0, 0, false};
+        if (at < count) box[LOOK + 1] = look(cur);               // tile i + LOOK + 1
+        advance();
+        if (i + LOOK < count) ask_scales(box[LOOK], i + LOOK);
+        const bool load = box[0].need;
+        const int row = (box[0].page * p.Hkv + box[0].g) * (in_page + 1) + box[0].off;
+        const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, load)) * rows * HD;
+#pragma unroll
+        for (int k = 0; k <= LOOK; ++k) box[k] = box[k + 1];
+        // K and V have barriers of their own: a K tile is free as soon as its S is computed, a V tile a softmax later
+        const int sk = i % KS, sv = i % VS;
+        bool ok = ptx::mbar_wait(ptx::smem_u32(&k_empty[sk]), ((i / KS) & 1) ^ 1, abort, status);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        if (lane == 0) ptx::mbar_arrive_expect_tx(ptx::smem_u32(&k_full[sk]), bytes);
+        __syncwarp();
+        k_issued = i + 1;
+        if (load)
+            tma_3d(ptx::smem_u32(sK + (sk * TK + lane * rows) * HD), &map, 0, row, p.kz, ptx::smem_u32(&k_full[sk]));
+        ok = ptx::mbar_wait(ptx::smem_u32(&v_empty[sv]), ((i / VS) & 1) ^ 1, abort, status);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        if (lane == 0) ptx::mbar_arrive_expect_tx(ptx::smem_u32(&v_full[sv]), bytes);
+        __syncwarp();
+        v_issued = i + 1;
+        if (load)
+            tma_3d(ptx::smem_u32(sV + (sv * TK + lane * rows) * HD), &map, 0, row, p.kz + 1, ptx::smem_u32(&v_full[sv]));
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    int never = 0;
+    for (int i = max(0, k_issued - KS); i < k_issued; ++i)
+        ptx::mbar_wait(ptx::smem_u32(&k_full[i % KS]), (i / KS) & 1, &never, status);
+    for (int i = max(0, v_issued - VS); i < v_issued; ++i)
+        ptx::mbar_wait(ptx::smem_u32(&v_full[i % VS]), (i / VS) & 1, &never, status);
+}
+
 }  // namespace
 
 }  // namespace cb

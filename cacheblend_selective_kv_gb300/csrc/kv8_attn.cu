@@ -98,31 +98,10 @@ template <int N> __device__ __forceinline__ void tmem_ld_done(uint32_t* r) {
     for (int k = 0; k < N; k += 4)
         asm volatile("tcgen05.wait::ld.sync.aligned;" : "+r"(r[k]), "+r"(r[k + 1]), "+r"(r[k + 2]), "+r"(r[k + 3])::"memory");
 }
-// byte `b` of row `row` in that swizzled layout
-template <int ROW> __device__ __forceinline__ uint32_t f8_at(uint32_t row, uint32_t b) {
-    return ROW == 128 ? row * 128 + ((((b >> 4) ^ row) & 7) << 4) + (b & 15)
-                      : row * 64 + ((((b >> 4) ^ (row >> 1)) & 3) << 4) + (b & 15);
-}
-// 4 bytes to shared memory; the barrier is arrived at once this thread's copies so far have landed
-__device__ __forceinline__ void cp_async4(uint32_t dst, const float* src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
-    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
-}
-__device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2, uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
-        ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
-        : "memory");
-}
-
 constexpr int MAX_STAGES = 3;
-constexpr int RING = 8;                  // tiles whose scales may be under way or in use
-constexpr int LOOK = 2;                  // tiles by which the scales are asked for ahead of the codes
+constexpr int RING = 8;
 struct Shared {
-    float scale[RING][2][8];             // K's and V's scale of each box of a tile; -1: not loaded
-    uint64_t scale_full[RING];
+    ScaleRing<RING> ring;
     uint64_t k_full[MAX_STAGES], v_full[MAX_STAGES], k_empty[MAX_STAGES], v_empty[MAX_STAGES];
     uint64_t s_full[2], s_free[2];
     uint64_t p_full, o_full, q_full, drain;
@@ -260,7 +239,7 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
             ptx::mbar_init(ptx::smem_u32(&c.s_full[i]), 1);
             ptx::mbar_init(ptx::smem_u32(&c.s_free[i]), SOFT / 32);
         }
-        for (int i = 0; i < RING; ++i) ptx::mbar_init(ptx::smem_u32(&c.scale_full[i]), TK / p.box);
+        for (int i = 0; i < RING; ++i) ptx::mbar_init(ptx::smem_u32(&c.ring.full[i]), TK / p.box);
         ptx::mbar_init(ptx::smem_u32(&c.p_full), SOFT / 32);
         ptx::mbar_init(ptx::smem_u32(&c.o_full), 1);
         ptx::mbar_init(ptx::smem_u32(&c.q_full), SOFT / 32);
@@ -285,92 +264,10 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
 
     if (warp == TMA_WARP) {
         // ------------------------------------------------------------------------------------ TMA
-        // A lane looks after one box (at most a page) of a tile.  Its page id is loaded LOOK + 1 tiles ahead; the scales go to
-        // shared memory LOOK tiles ahead, so that neither is waited for when memory is busy.  A scale slot is free again
-        // without a barrier of its own: K of tile i waits for S of tile i - STAGES, hence the softmax is past tile
-        // i - STAGES - 2, and slot i + LOOK was last used RING - LOOK tiles before i.
-        static_assert(RING - LOOK > STAGES + 2, "scale ring");
-        const int boxes = TK / p.box, rows = p.box, in_page = (1 << p.q.shift) - 1;
-        struct Ahead {
-            int page, g, off;                                    // off: first row in the page
-            bool need;                                           // the box holds rows of the sequence
-        };
-        auto look = [&](const Cursor& u) {
-            const int j = u.t * TK + lane * rows;
-            Ahead a{0, u.g, j & in_page, lane < boxes && j < u.q.len};
-            if (a.need) a.page = p.q.table[(int64_t)u.s * p.q.table_ld + (j >> p.q.shift)];
-            return a;
-        };
-        auto ask_scales = [&](Ahead& a, int i) {                 // (the page id was loaded a tile ago)
-            if (a.need && (a.page < 0 || a.page >= p.q.n_pages)) {
-                atomicOr(status, ST_BAD_ROW);
-                a.need = false;
-            }
-            if (lane >= boxes) return;
-            float* dst = &c.scale[i % RING][0][lane];
-            const uint32_t bar = ptx::smem_u32(&c.scale_full[i % RING]);
-            if (a.need) {
-                const int64_t at = (int64_t)a.page * p.Hkv + a.g;
-                cp_async4(ptx::smem_u32(dst), p.ks + at);
-                cp_async4(ptx::smem_u32(dst + 8), p.vs + at);
-                cp_async_arrive(bar);
-            } else {
-                dst[0] = dst[8] = -1.f;
-                ptx::mbar_arrive(bar);
-            }
-        };
-        int k_issued = 0, v_issued = 0;
-        Ahead box[LOOK + 2];
-        int at = 0;                                              // tile that `cur` stands at
-        auto advance = [&] {
-            if (++at < count && ++cur.t == cur.nt) cur.next_item(p);
-        };
-        if (count > 0) {
-#pragma unroll
-            for (int k = 0; k <= LOOK; ++k) {                    // tiles 0 .. LOOK
-                box[k] = look(cur);
-                if (at >= count) box[k].need = false;
-                advance();
-            }
-#pragma unroll
-            for (int k = 0; k < LOOK; ++k)
-                if (k < count) ask_scales(box[k], k);
-        }
-        for (int i = 0; i < count; ++i) {
-            const int st = i % STAGES;
-            box[LOOK + 1] = Ahead{0, 0, 0, false};
-            if (at < count) box[LOOK + 1] = look(cur);           // tile i + LOOK + 1
-            advance();
-            if (i + LOOK < count) ask_scales(box[LOOK], i + LOOK);
-            const bool load = box[0].need;
-            const int row = (box[0].page * p.Hkv + box[0].g) * (in_page + 1) + box[0].off;
-            const unsigned who = __ballot_sync(0xffffffffu, load);
-#pragma unroll
-            for (int k = 0; k <= LOOK; ++k) box[k] = box[k + 1];
-            // a K tile is free as soon as its S is computed, a V tile a softmax later: K runs further ahead
-            const uint32_t par = ((i / STAGES) & 1) ^ 1, bytes = (uint32_t)__popc(who) * rows * HD;
-            bool ok = ptx::mbar_wait(ptx::smem_u32(&c.k_empty[st]), par, abort, status);
-            if (!__all_sync(0xffffffffu, ok)) break;
-            if (lane == 0) ptx::mbar_arrive_expect_tx(ptx::smem_u32(&c.k_full[st]), bytes);
-            __syncwarp();
-            k_issued = i + 1;
-            if (load)
-                tma_3d(ptx::smem_u32(sK + st * S::KV_BYTES + lane * rows * HD), &map, 0, row, p.kz, ptx::smem_u32(&c.k_full[st]));
-            ok = ptx::mbar_wait(ptx::smem_u32(&c.v_empty[st]), par, abort, status);
-            if (!__all_sync(0xffffffffu, ok)) break;
-            if (lane == 0) ptx::mbar_arrive_expect_tx(ptx::smem_u32(&c.v_full[st]), bytes);
-            __syncwarp();
-            v_issued = i + 1;
-            if (load)
-                tma_3d(ptx::smem_u32(sV + st * S::KV_BYTES + lane * rows * HD), &map, 0, row, p.kz + 1, ptx::smem_u32(&c.v_full[st]));
-        }
-        // every copy has landed before the CTA may leave
-        asm volatile("cp.async.wait_all;" ::: "memory");
-        int never = 0;
-        for (int i = max(0, k_issued - STAGES); i < k_issued; ++i)
-            ptx::mbar_wait(ptx::smem_u32(&c.k_full[i % STAGES]), (i / STAGES) & 1, &never, status);
-        for (int i = max(0, v_issued - STAGES); i < v_issued; ++i)
-            ptx::mbar_wait(ptx::smem_u32(&c.v_full[i % STAGES]), (i / STAGES) & 1, &never, status);
+        // A scale slot is free again without a barrier of its own: K of tile i - 1 waited for S of tile i - 1 - STAGES, which
+        // waited for the softmax to have read tile i - 3 - STAGES, and slot i + LOOK was last used for tile i + LOOK - RING.
+        static_assert(RING - LOOK >= STAGES + 3, "scale ring");
+        produce_tiles<HD, STAGES, STAGES>(p, map, cur, count, sK, sV, c.k_full, c.k_empty, c.v_full, c.v_empty, c.ring, abort);
     } else if (warp == MMA_WARP) {
         // ------------------------------------------------------------------------------------ MMA
         if (lane == 0) {
@@ -478,8 +375,8 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
 
             for (int t = first; t < first + n_here; ++t, ++i) {
                 const int b = i & 1, j = t * TK + key;
-                ptx::mbar_wait(ptx::smem_u32(&c.scale_full[i % RING]), (i / RING) & 1, abort, status);
-                const float ks_now = c.scale[i % RING][0][key >> box_shift], vs_now = c.scale[i % RING][1][key >> box_shift];
+                ptx::mbar_wait(ptx::smem_u32(&c.ring.full[i % RING]), (i / RING) & 1, abort, status);
+                const float ks_now = c.ring.scale[i % RING][0][key >> box_shift], vs_now = c.ring.scale[i % RING][1][key >> box_shift];
                 const bool have = ks_now >= 0.f && j < q.len;
 
                 ptx::mbar_wait(ptx::smem_u32(&c.s_full[b]), (i >> 1) & 1, abort, status);
@@ -792,7 +689,7 @@ cudaError_t launch_kv8_attention(const Kv8& c, const Kv8Seqs& q, const Kv8Rows& 
     if (r.n_rows > 0) {
         const int rows = (r.n_rows + q.n - 1) / q.n;             // of a sequence, on average
         const bool many = c.cfg.dtype == CB_BF16 && rows * p.G > 32;
-        const cudaError_t e = many ? launch_kv8_rows(c, &p, layer, s)
+        const cudaError_t e = many ? launch_kv8_rows(c, &p, s)
                                    : c.cfg.head_dim == 128 ? launch_dim<128>(c, p, s) : launch_dim<64>(c, p, s);
         if (e != cudaSuccess) return e;
     }

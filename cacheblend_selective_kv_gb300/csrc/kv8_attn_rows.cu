@@ -1,12 +1,13 @@
 // Attention over the 8-bit paged K/V cache for many query rows per sequence (a query over a blended context, a prompt in
 // pieces): bf16 queries, an item's 128 rows = 128 / G query rows x the G heads of their group in the lanes of tensor memory.
 //
-// With this many rows a tile of keys is used often enough to widen it once: warps 8-11 read the codes (page by page through
-// the block table), write K as bf16 with its block scale multiplied in (exact: four significant bits times a power of two)
-// and V as fp16 codes, in the swizzled layouts of the MMA operands, and S = Q K^T, O += P V run on kind::f16.  Against the
-// e4m3 terms of kv8_attn.cu this costs a conversion per cached value and tile, and saves the terms of q and P for each of
-// 128 rows, the shuffles of maxima over keys (a row is one thread's) and the products with the scales of K.  P is
-// fp16: 11 bits, 2^-12 relative.
+// With this many rows a tile of keys is used often enough to widen it once: four warps turn the codes that TMA has brought
+// into shared memory into fp16 (exact, without the block scales), in the swizzled layouts of the MMA operands, and
+// S = Q K^T, O += P V run on kind::f16.  Against the e4m3 terms of kv8_attn.cu this costs a conversion per cached value and
+// tile, and saves the terms of q and P for each of 128 rows and the maxima over keys in other threads (a row is one
+// thread's).  Q is brought to fp16 by a power of two per row that puts its largest value at 2^14 .. 2^15: exact down to
+// 2^-29 of that.  P is fp16: 11 bits, 2^-12 relative.  Block scales hold for 16 keys at least: K's multiplies the scores
+// of a block together with the constants of the softmax, V's multiplies P.
 //
 // V's block scales differ, so P carries them: p_j = 2^(x_j - R) s_j with x the score in the exp2 domain, s_j the scale of
 // key j's block and R a reference of the row no more than 2^8 below the largest x_j + log2 s_j so far.  It grows lazily (O
@@ -16,6 +17,8 @@
 // Each of the two halves of a tile's keys has its own R, sum and O (as the blend's attention kernel does, so that the warps
 // of a row need not meet for every tile); they are joined at the end of an item.  Per tile and SM: 32 MMAs of 128 x 128 x 16
 // at about 99 cycles, 128 x 128 exponentials, 2 x 128 x HD conversions.
+#include <cstring>
+
 #include "cb_kv8_attn.cuh"
 
 namespace cb {
@@ -23,32 +26,39 @@ namespace cb {
 namespace {
 
 constexpr int ROWS = 128;
-constexpr int SOFT = 256, CONV = 128, THREADS = SOFT + CONV + 32;
-constexpr int CONV_WARP = SOFT / 32, MMA_WARP = CONV_WARP + CONV / 32;
+constexpr int SOFT = 256, CONV = 128, THREADS = SOFT + CONV + 64;
+constexpr int CONV_WARP = SOFT / 32, MMA_WARP = CONV_WARP + CONV / 32, TMA_WARP = MMA_WARP + 1;
 constexpr int HK = 64;                   // keys of a half
-constexpr int RING = 4;                  // tiles whose scales are kept; items whose NaN marks are
+constexpr int MARKS = 4;                 // items whose row scales and NaN marks are kept; tiles whose conversion is announced
+constexpr int RING = 16;                 // tiles whose block scales are kept
+constexpr int KT = 2, VT = 1;            // tiles of K and V codes
 constexpr float GROW = 8.f;              // how far (log2) P may outgrow its reference
 constexpr float P_UP = 128.f;            // P is stored this much larger: its largest values are 2^7 .. 2^15 of fp16's 2^16
 
 struct RowsShared {
-    uint64_t k_full[2], k_empty[2], v_full[2], pv_done[2], s_full[2], p_full[2], scale_full[RING], q_full, o_free, drain;
+    uint64_t kc_full[KT], kc_empty[KT], vc_full[VT], vc_empty[VT];          // codes
+    uint64_t k_full[2], k_empty[2], v_full[2], pv_done[2], s_full[2], p_full[2];
+    uint64_t rows_full[MARKS];           // an item's row scales are written
+    uint64_t v_seen[MARKS];              // a tile's V is converted, its NaN marked
+    uint64_t q_full, o_free, drain;
+    ScaleRing<RING> ring;
     uint32_t tmem;
     int abort;
     Find find;
     int last;
-    int holes[RING];                     // a key of the tile is not loaded
-    int any_nan[RING];                   // an item's V held NaN that not all of its rows see
+    int any_nan[MARKS];                  // an item's V held NaN that not all of its rows see
 };
 
 template <int HD> struct Rows {
-    static constexpr int TILE = TK * HD * 2;                     // a K or V tile, or Q, in 16-bit elements
-    static constexpr int OFF_K = TILE, OFF_V = 3 * TILE;
-    static constexpr int OFF_X = 5 * TILE;
-    // floats: scale of V [RING][TK], its logarithm [RING][TK], (R, sum) [2][ROWS][2]; ints: nan_from [RING][HD]
-    static constexpr int X_FLOATS = 2 * RING * TK + 4 * ROWS + RING * HD;
+    static constexpr int TILE = TK * HD * 2, CODES = TK * HD;    // a K or V tile, or Q, in fp16; a tile of codes
+    static constexpr int OFF_K = TILE, OFF_V = 3 * TILE, OFF_KC = 5 * TILE, OFF_VC = OFF_KC + KT * CODES;
+    static constexpr int OFF_X = OFF_VC + VT * CODES;
+    // floats: row scales [MARKS][ROWS], (R, sum) [2][ROWS][2]; ints: nan_from [MARKS][HD]
+    static constexpr int X_FLOATS = MARKS * ROWS + 4 * ROWS + MARKS * HD;
     static constexpr int OFF_C = OFF_X + X_FLOATS * 4;
     static constexpr int BYTES = OFF_C + (int)sizeof(RowsShared);
     static constexpr int PIECE = ROWS * (HD + 2);
+    static_assert(BYTES <= 227 * 1024, "shared memory");
 };
 
 // a swizzled tile: halves of 64 elements (128 bytes) of the row, 128 rows each
@@ -67,12 +77,10 @@ __device__ __forceinline__ void mma_f16_tmem_a(uint32_t d, uint32_t a, uint64_t 
         ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc)
         : "memory");
 }
-__device__ __forceinline__ void tmem_st16_words(uint32_t addr, const uint32_t* v) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};"
-        ::"r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]),
-          "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
-        : "memory");
+__device__ __forceinline__ void tmem_st8_words(uint32_t addr, const uint32_t* v) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+                 ::"r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
 }
 __device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
     const __nv_bfloat162 t = __floats2bfloat162_rn(a, b);
@@ -84,17 +92,29 @@ __device__ __forceinline__ uint32_t f16_pair(float a, float b) {
 }
 __device__ __forceinline__ uint32_t half2_word(const __half2& h) { return *reinterpret_cast<const uint32_t*>(&h); }
 
+// NaN codes out of 16 codes of a V row that not all query rows see, and row j noted as the first to hold one in those dims
+__device__ __noinline__ void take_nan(uint4& x, int j, int* marks, int* any) {
+    uint32_t cw[4] = {x.x, x.y, x.z, x.w};
+    for (int k = 0; k < 4; ++k) {
+        const uint32_t bad = __vcmpeq4(cw[k] & 0x7f7f7f7fu, 0x7f7f7f7fu);
+        if (bad == 0) continue;
+        cw[k] &= ~bad;
+        for (int y = 0; y < 4; ++y)
+            if (bad >> (8 * y) & 1) atomicMin(marks + 4 * k + y, j);
+        *any = 1;
+    }
+    x = make_uint4(cw[0], cw[1], cw[2], cw[3]);
+}
+
 template <int HD>
-__global__ void __launch_bounds__(THREADS, 1) kv8_rows_kernel(const AttnArgs p, const uint8_t* __restrict__ kc,
-                                                             const uint8_t* __restrict__ vc) {
+__global__ void __launch_bounds__(THREADS, 1) kv8_rows_kernel(const __grid_constant__ CUtensorMap map, const AttnArgs p) {
     using S = Rows<HD>;
     extern __shared__ __align__(1024) uint8_t sm[];
     uint8_t* sQ = sm;
     uint8_t* sK = sm + S::OFF_K;                        // [2]
     uint8_t* sV = sm + S::OFF_V;                        // [2]
-    float* v_scale = reinterpret_cast<float*>(sm + S::OFF_X);
-    float* v_log = v_scale + RING * TK;
-    float* halves = v_log + RING * TK;
+    float* row_scale = reinterpret_cast<float*>(sm + S::OFF_X);
+    float* halves = row_scale + MARKS * ROWS;
     int* nan_marks = reinterpret_cast<int*>(halves + 4 * ROWS);
     RowsShared& c = *reinterpret_cast<RowsShared*>(sm + S::OFF_C);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -113,15 +133,26 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_rows_kernel(const AttnArgs p, 
             ptx::mbar_init(ptx::smem_u32(&c.s_full[i]), 1);
             ptx::mbar_init(ptx::smem_u32(&c.p_full[i]), SOFT / 32);
         }
-        for (int i = 0; i < RING; ++i) {
-            ptx::mbar_init(ptx::smem_u32(&c.scale_full[i]), CONV / 32);
-            c.holes[i] = c.any_nan[i] = 0;
+        for (int i = 0; i < KT; ++i) {
+            ptx::mbar_init(ptx::smem_u32(&c.kc_full[i]), 1);
+            ptx::mbar_init(ptx::smem_u32(&c.kc_empty[i]), CONV / 32);
         }
+        for (int i = 0; i < VT; ++i) {
+            ptx::mbar_init(ptx::smem_u32(&c.vc_full[i]), 1);
+            ptx::mbar_init(ptx::smem_u32(&c.vc_empty[i]), CONV / 32);
+        }
+        for (int i = 0; i < MARKS; ++i) {
+            ptx::mbar_init(ptx::smem_u32(&c.rows_full[i]), CONV / 32);
+            ptx::mbar_init(ptx::smem_u32(&c.v_seen[i]), CONV / 32);
+            c.any_nan[i] = 0;
+        }
+        for (int i = 0; i < RING; ++i) ptx::mbar_init(ptx::smem_u32(&c.ring.full[i]), TK / p.box);
         ptx::mbar_init(ptx::smem_u32(&c.q_full), CONV / 32);
         ptx::mbar_init(ptx::smem_u32(&c.o_free), SOFT / 32);
         ptx::mbar_init(ptx::smem_u32(&c.drain), 1);
         c.abort = 0;
         ptx::fence_barrier_init();
+        ptx::prefetch_tmap(&map);
     }
     if (warp == MMA_WARP) {
         ptx::tmem_alloc(ptx::smem_u32(&c.tmem), 512);
@@ -137,37 +168,11 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_rows_kernel(const AttnArgs p, 
     constexpr uint32_t O_COL = 256;
 
     if (warp >= CONV_WARP && warp < MMA_WARP) {
-        // ------------------------------------------------------------------------------------ codes to operands
-        // Like the softmax warps, these run on to their last tile when a wait has given up.  The codes of V are asked for
-        // before K's are converted, the next tile's K before V's are.
+        // ------------------------------------------------------------------------------------ codes to fp16
+        // Like the softmax warps, these run on to their last tile when a wait has given up.
         constexpr int LPR = HD / 16, RPW = 32 / LPR, NI = TK / (4 * RPW);           // lanes per row, rows per warp and step, steps
-        const int w = warp - CONV_WARP, t = tid - SOFT, sub = lane / LPR, e = lane % LPR, P = 1 << p.q.shift;
-        const auto row_of = [&](int n) { return (n * 4 + w) * RPW + sub; };
-        int at[NI];                                     // this thread's rows among the layer's rows of all heads, or -1
-        float ks[NI];
-        float vs_key = 0.f;                             // V's scale of key t (-1: not loaded)
-        uint4 k[NI], v[NI];
-        const auto find_rows = [&](const Cursor& u) {
-#pragma unroll
-            for (int n = 0; n < NI; ++n) {
-                const int j = u.t * TK + row_of(n);
-                const int pg = j < u.q.len ? kv8_page(p.q, u.s, j >> p.q.shift) : -1;
-                at[n] = pg >= 0 ? (pg * p.Hkv + u.g) * P + (j & (P - 1)) : -1;
-                ks[n] = pg >= 0 ? p.ks[(int64_t)pg * p.Hkv + u.g] : 0.f;
-            }
-            const int j = u.t * TK + t;
-            const int pg = j < u.q.len ? kv8_page(p.q, u.s, j >> p.q.shift) : -1;
-            vs_key = pg >= 0 ? p.vs[(int64_t)pg * p.Hkv + u.g] : -1.f;
-        };
-        const auto load = [&](const uint8_t* codes, uint4* x) {
-#pragma unroll
-            for (int n = 0; n < NI; ++n)
-                x[n] = at[n] >= 0 ? *reinterpret_cast<const uint4*>(codes + (int64_t)at[n] * HD + e * 16) : make_uint4(0, 0, 0, 0);
-        };
-        if (count > 0) {
-            find_rows(cur);
-            load(kc, k);
-        }
+        const int w = warp - CONV_WARP, t = tid - SOFT, e = lane % LPR, row0 = w * RPW + lane / LPR;
+        const int box_shift = min(p.q.shift, 7);
         int item = -1;
         bool begins = true;
         for (int i = 0; i < count; ++i) {
@@ -178,106 +183,106 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_rows_kernel(const AttnArgs p, 
             if (begins) {
                 ++item;
                 // Q once the products with the item before's are done; then the softmax is past tile i - 3, hence past the item
-                // whose marks these were
+                // whose marks and row scales these were
                 if (i > 0) ptx::mbar_wait(ptx::smem_u32(&c.k_empty[(i - 1) & 1]), ((i - 1) >> 1) & 1, abort, status);
-                if (t < HD) nan_marks[(item % RING) * HD + t] = INT_MAX;
-                if (t == 0) c.any_nan[item % RING] = 0;
+                if (t < HD) nan_marks[(item % MARKS) * HD + t] = INT_MAX;
+                if (t == 0) c.any_nan[item % MARKS] = 0;
                 const bf16* qbase = (const bf16*)p.a.q + (int64_t)(q.r0 + q0) * p.a.q_stride + (int64_t)cur.g * p.G * HD;
-                for (int x = t; x < ROWS * (HD / 8); x += CONV) {
-                    const int row = x / (HD / 8), ch = x % (HD / 8);
+                constexpr int QL = HD / 8;                       // lanes of a row, 8 values each
+#pragma unroll 2
+                for (int r = w * (32 / QL) + lane / QL; r < ROWS; r += 4 * (32 / QL)) {
                     uint4 val = make_uint4(0, 0, 0, 0);
-                    if (row < cols)
-                        val = *reinterpret_cast<const uint4*>(qbase + (int64_t)(row / p.G) * p.a.q_stride + (row % p.G) * HD + ch * 8);
-                    *reinterpret_cast<uint4*>(sQ + wide_at(row, ch)) = val;
+                    if (r < cols)
+                        val = *reinterpret_cast<const uint4*>(qbase + (int64_t)(r / p.G) * p.a.q_stride + (r % p.G) * HD + lane % QL * 8);
+                    const uint32_t word[4] = {val.x, val.y, val.z, val.w};
+                    float f[8], top = 0.f;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        f[2 * k] = __uint_as_float(word[k] << 16);
+                        f[2 * k + 1] = __uint_as_float(word[k] & 0xffff0000u);
+                        top = fmaxf(top, fmaxf(kv8_mag(f[2 * k]), kv8_mag(f[2 * k + 1])));
+                    }
+#pragma unroll
+                    for (int o = QL / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                    // kv8_scale brings the largest value to 224 .. 448; 2^6 more is 2^14 .. 2^15 less a little
+                    const float sc = kv8_scale(top), up = kv8_inverse(sc) * 64.f;
+                    uint32_t o[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) o[k] = f16_pair(f[2 * k] * up, f[2 * k + 1] * up);
+                    *reinterpret_cast<uint4*>(sQ + wide_at(r, lane % QL)) = make_uint4(o[0], o[1], o[2], o[3]);
+                    if (lane % QL == 0) row_scale[(item % MARKS) * ROWS + r] = sc * (1.f / 64.f);
                 }
                 fence_async_smem();
                 ptx::named_bar_sync(2, CONV);                    // also: the marks
-                if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&c.q_full));
+                if (lane == 0) {
+                    ptx::mbar_arrive(ptx::smem_u32(&c.q_full));
+                    ptx::mbar_arrive(ptx::smem_u32(&c.rows_full[item % MARKS]));
+                }
             }
-            load(vc, v);
-            float ks_now[NI];
-            bool gone[NI];
+            const auto widen = [&](uint8_t* to, int row, const uint4& x) {
+                const uint32_t cw[4] = {x.x, x.y, x.z, x.w};
+                uint32_t o[8];
 #pragma unroll
-            for (int n = 0; n < NI; ++n) {
-                ks_now[n] = ks[n];
-                gone[n] = at[n] < 0;
-            }
-            const float vs_now = vs_key;
-            // K: free once S of two tiles before is done, which also means that the softmax is past the tile four before
+                for (int k = 0; k < 4; ++k) {
+                    o[2 * k] = half2_word(kv8_half2(cw[k]));
+                    o[2 * k + 1] = half2_word(kv8_half2(cw[k] >> 16));
+                }
+                *reinterpret_cast<uint4*>(to + wide_at(row, 2 * e)) = make_uint4(o[0], o[1], o[2], o[3]);
+                *reinterpret_cast<uint4*>(to + wide_at(row, 2 * e + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
+            };
+            // K: free once S of two tiles before is done (rows that are not loaded stay as they were: their scores are masked)
+            ptx::mbar_wait(ptx::smem_u32(&c.kc_full[i % KT]), (i / KT) & 1, abort, status);
             ptx::mbar_wait(ptx::smem_u32(&c.k_empty[st]), par, abort, status);
-            v_scale[(i % RING) * TK + t] = vs_now < 0.f ? 0.f : vs_now * P_UP;
-            v_log[(i % RING) * TK + t] = vs_now < 0.f ? -INFINITY : fmaxf(log2f(vs_now), -100.f);
-            const unsigned hole = __ballot_sync(0xffffffffu, vs_now < 0.f);
-            if (t == 0) c.holes[i % RING] = 0;
-            ptx::named_bar_sync(2, CONV);
+#pragma unroll 2
+            for (int n = 0; n < NI; ++n) {
+                const int row = row0 + n * 4 * RPW;
+                widen(sK + st * S::TILE, row, *reinterpret_cast<const uint4*>(sm + S::OFF_KC + (i % KT) * S::CODES + f8_at<HD>(row, e * 16)));
+            }
+            fence_async_smem();
+            __syncwarp();
             if (lane == 0) {
-                if (hole) c.holes[i % RING] = 1;
-                ptx::mbar_arrive(ptx::smem_u32(&c.scale_full[i % RING]));
+                ptx::mbar_arrive(ptx::smem_u32(&c.k_full[st]));
+                ptx::mbar_arrive(ptx::smem_u32(&c.kc_empty[i % KT]));
             }
-            uint8_t* dk = sK + st * S::TILE;
-#pragma unroll
-            for (int n = 0; n < NI; ++n) {
-                const uint32_t cw[4] = {k[n].x, k[n].y, k[n].z, k[n].w};
-                uint32_t o[8];
-#pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    const float2 lo = kv8_value2(cw[x]), hi = kv8_value2(cw[x] >> 16);
-                    o[2 * x] = bf16_pair(lo.x * ks_now[n], lo.y * ks_now[n]);
-                    o[2 * x + 1] = bf16_pair(hi.x * ks_now[n], hi.y * ks_now[n]);
-                }
-                *reinterpret_cast<uint4*>(dk + wide_at(row_of(n), 2 * e)) = make_uint4(o[0], o[1], o[2], o[3]);
-                *reinterpret_cast<uint4*>(dk + wide_at(row_of(n), 2 * e + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
-            }
-            fence_async_smem();
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&c.k_full[st]));
-            // the next tile's rows and K
             begins = false;
-            if (i + 1 < count) {
-                if (++cur.t == cur.nt) {
-                    cur.next_item(p);
-                    begins = true;
-                }
-                find_rows(cur);
-                load(kc, k);
+            if (i + 1 < count && ++cur.t == cur.nt) {
+                cur.next_item(p);
+                begins = true;
             }
-            // V: zero where nothing is loaded; a NaN that only later rows see is taken out and remembered
+            // V: zero where nothing is loaded or behind the sequence; a NaN that only later rows see is taken out and remembered
+            ptx::mbar_wait(ptx::smem_u32(&c.ring.full[i % RING]), (i / RING) & 1, abort, status);
+            ptx::mbar_wait(ptx::smem_u32(&c.vc_full[i % VT]), (i / VT) & 1, abort, status);
             ptx::mbar_wait(ptx::smem_u32(&c.pv_done[st]), par, abort, status);
-            uint8_t* dv = sV + st * S::TILE;
-#pragma unroll
+#pragma unroll 2
             for (int n = 0; n < NI; ++n) {
-                uint32_t cw[4] = {v[n].x, v[n].y, v[n].z, v[n].w};
-                const int j = tile * TK + row_of(n);
-                if (gone[n]) {
-                    cw[0] = cw[1] = cw[2] = cw[3] = 0;
+                const int row = row0 + n * 4 * RPW, j = tile * TK + row;
+                uint4 x = *reinterpret_cast<const uint4*>(sm + S::OFF_VC + (i % VT) * S::CODES + f8_at<HD>(row, e * 16));
+                if (j >= q.len || c.ring.scale[i % RING][0][row >> box_shift] < 0.f) {
+                    x = make_uint4(0, 0, 0, 0);
                 } else if (j > pos0) {
-                    for (int x = 0; x < 4; ++x) {
-                        const uint32_t bad = __vcmpeq4(cw[x] & 0x7f7f7f7fu, 0x7f7f7f7fu);
-                        if (bad == 0) continue;
-                        cw[x] &= ~bad;
-                        for (int y = 0; y < 4; ++y)
-                            if (bad >> (8 * y) & 1) atomicMin(nan_marks + (item % RING) * HD + e * 16 + 4 * x + y, j);
-                        c.any_nan[item % RING] = 1;
-                    }
+                    take_nan(x, j, nan_marks + (item % MARKS) * HD + e * 16, &c.any_nan[item % MARKS]);
                 }
-                uint32_t o[8];
-#pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    o[2 * x] = half2_word(kv8_half2(cw[x]));
-                    o[2 * x + 1] = half2_word(kv8_half2(cw[x] >> 16));
-                }
-                *reinterpret_cast<uint4*>(dv + wide_at(row_of(n), 2 * e)) = make_uint4(o[0], o[1], o[2], o[3]);
-                *reinterpret_cast<uint4*>(dv + wide_at(row_of(n), 2 * e + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
+                widen(sV + st * S::TILE, row, x);
             }
             fence_async_smem();
             __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&c.v_full[st]));
+            if (lane == 0) {
+                ptx::mbar_arrive(ptx::smem_u32(&c.v_full[st]));
+                ptx::mbar_arrive(ptx::smem_u32(&c.vc_empty[i % VT]));
+                ptx::mbar_arrive(ptx::smem_u32(&c.v_seen[i % MARKS]));
+            }
         }
+    } else if (warp == TMA_WARP) {
+        // ------------------------------------------------------------------------------------ TMA
+        // A scale slot is free again without a barrier of its own: K's codes of tile i - 1 waited for the conversion of tile
+        // i - 1 - KT, which waited for S of two tiles before, which waited for P V of two before that.
+        static_assert(RING - LOOK >= KT + 1 + 2 + 2, "scale ring");
+        produce_tiles<HD, KT, VT>(p, map, cur, count, sm + S::OFF_KC, sm + S::OFF_VC, c.kc_full, c.kc_empty, c.vc_full, c.vc_empty, c.ring, abort);
     } else if (warp == MMA_WARP) {
         // ------------------------------------------------------------------------------------ MMA
         if (lane == 0) {
-            constexpr uint32_t id_s = ptx::idesc_bf16(ROWS, TK);
-            constexpr uint32_t id_o = (1u << 4) | (1u << 16) | ((uint32_t)(HD >> 3) << 17) | (8u << 24);     // f16, B MN-major
+            constexpr uint32_t id_s = (1u << 4) | ((uint32_t)(TK >> 3) << 17) | (8u << 24);                  // fp16, 128 rows
+            constexpr uint32_t id_o = (1u << 4) | (1u << 16) | ((uint32_t)(HD >> 3) << 17) | (8u << 24);     // B MN-major
             const uint64_t qd = ptx::sdesc_sw128(ptx::smem_u32(sQ));
             int left = 0, item = 0, items_o = 0;
             bool ok = true;
@@ -336,6 +341,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_rows_kernel(const AttnArgs p, 
         const int quarter = warp & 3, hf = warp >> 2, row = quarter * 32 + lane;
         const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
         const float to_exp2 = p.a.scale * 1.4426950408889634f;
+        const int box_shift = min(p.q.shift, 7);
         int item = 0;
         for (int i = 0; i < count; ++item) {
             const int first = cur.t, n_here = min(cur.nt - first, count - i), g = cur.g;
@@ -343,40 +349,52 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_rows_kernel(const AttnArgs p, 
             const int q0 = cur.qt * p.QT, cols = min(p.QT, q.n - q0) * p.G;
             const int pos0 = q.len - q.n + q0, pos = pos0 + row / p.G;       // positions of the item's first row and of this one
             const int64_t stat0 = ((int64_t)g * p.r.n_rows + q.r0 + q0) * p.G;
-            float ref = -INFINITY, l = 0.f;                      // R and the sum of 2^(x - R)
+            float ref = -INFINITY, l = 0.f, row_mul = 0.f;       // R, the sum of 2^(x - R)
             for (int t = first; t < first + n_here; ++t, ++i) {
                 const int b = i & 1, j0 = t * TK + hf * HK;
-                ptx::mbar_wait(ptx::smem_u32(&c.scale_full[i % RING]), (i / RING) & 1, abort, status);
-                const float* vl = v_log + (i % RING) * TK + hf * HK;
-                const float* vs = v_scale + (i % RING) * TK + hf * HK;
-                const bool masked = c.holes[i % RING] != 0 || j0 + HK - 1 > pos0;
+                ptx::mbar_wait(ptx::smem_u32(&c.ring.full[i % RING]), (i / RING) & 1, abort, status);
+                if (t == first) {
+                    ptx::mbar_wait(ptx::smem_u32(&c.rows_full[item % MARKS]), (item / MARKS) & 1, abort, status);
+                    row_mul = row_scale[(item % MARKS) * ROWS + row] * to_exp2;
+                }
                 ptx::mbar_wait(ptx::smem_u32(&c.s_full[b]), (i >> 1) & 1, abort, status);
                 ptx::tc_fence_after();
                 const uint32_t s_at = lanes + b * 128 + hf * HK;
-                float x[HK];                                     // scores in the exp2 domain
-#pragma unroll
-                for (int k = 0; k < HK; k += 16) {
+                // Scores of a block of 16 keys in the exp2 domain: S times K's scale (with the row's and the softmax's
+                // constants); -inf for a block that is not loaded and for keys the row does not see.  Computed twice, for the
+                // maximum and for P: the loops stay short, and so do the instructions to fetch (unrolled over the 64 keys in
+                // registers, most cycles went to waiting for instructions).
+                const float* scales = c.ring.scale[i % RING][0];
+                const auto scores = [&](int k, float* x) {
                     uint32_t w[16];
-                    ptx::tmem_ld16_issue(s_at + k, w);
+                    ptx::tmem_ld16_issue(s_at + k * 16, w);
+                    const float ks = scales[(hf * HK + k * 16) >> box_shift], m = ks * row_mul;
                     ptx::tmem_ld_wait16(w);
 #pragma unroll
-                    for (int y = 0; y < 16; ++y) x[k + y] = __uint_as_float(w[y]) * to_exp2;
-                }
-                if (masked) {
+                    for (int y = 0; y < 16; ++y) x[y] = __uint_as_float(w[y]) * m;
+                    if (ks < 0.f || j0 + k * 16 + 15 > pos0) {
+                        const int seen = ks < 0.f ? 0 : pos - (j0 + k * 16) + 1;
 #pragma unroll
-                    for (int k = 0; k < HK; ++k)
-                        if (j0 + k > pos || vl[k] == -INFINITY) x[k] = -INFINITY;
-                }
-                if (p.scores && row < cols) {
-                    float* score = p.scores + (stat0 + row) * p.score_ld + j0;
+                        for (int y = 0; y < 16; ++y)
+                            if (y >= seen) x[y] = -INFINITY;
+                    }
+                };
+                float top = -INFINITY;                           // the largest of score + log2 of V's scale
+#pragma unroll 1
+                for (int k = 0; k < HK / 16; ++k) {
+                    float x[16];
+                    scores(k, x);
+                    const float v = scales[8 + ((hf * HK + k * 16) >> box_shift)];
+                    const float vl = v > 0.f ? fmaxf((float)((int)(__float_as_uint(v) >> 23) - 127), -100.f) : -100.f;
+                    float m = x[0];
 #pragma unroll
-                    for (int k = 0; k < HK; k += 4) *reinterpret_cast<float4*>(score + k) = make_float4(x[k], x[k + 1], x[k + 2], x[k + 3]);
-                }
-                float top = -INFINITY;
+                    for (int y = 1; y < 16; ++y) m = fmaxf(m, x[y]);
+                    top = fmaxf(top, m + vl);
+                    if (p.scores && row < cols) {
+                        float4* score = reinterpret_cast<float4*>(p.scores + (stat0 + row) * p.score_ld + j0 + k * 16);
 #pragma unroll
-                for (int k = 0; k < HK; k += 4) {
-                    const float4 lg = *reinterpret_cast<const float4*>(vl + k);
-                    top = fmaxf(top, fmaxf(fmaxf(x[k] + lg.x, x[k + 1] + lg.y), fmaxf(x[k + 2] + lg.z, x[k + 3] + lg.w)));
+                        for (int y = 0; y < 4; ++y) score[y] = make_float4(x[4 * y], x[4 * y + 1], x[4 * y + 2], x[4 * y + 3]);
+                    }
                 }
                 if (__any_sync(0xffffffffu, ref != -INFINITY && top > ref + GROW)) {
                     // O_h holds the tiles before: the whole warp rescales, each row by its own factor
@@ -384,7 +402,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_rows_kernel(const AttnArgs p, 
                         ptx::mbar_wait(ptx::smem_u32(&c.pv_done[(i - 1) & 1]), ((i - 1) >> 1) & 1, abort, status);
                         ptx::tc_fence_after();
                         const float to = fmaxf(ref, top), f = ref == -INFINITY ? 1.f : exp2_fast(ref - to);
-#pragma unroll
+#pragma unroll 1
                         for (int k = 0; k < HD; k += 16) {
                             float o[16];
                             ptx::tmem_ld16(lanes + O_COL + hf * HD + k, o);
@@ -400,19 +418,19 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_rows_kernel(const AttnArgs p, 
                 if (ref == -INFINITY) ref = top;                 // nothing summed yet
                 const float neg = ref == -INFINITY ? 0.f : -ref;
                 float sum = 0.f;
+#pragma unroll 1
+                for (int k = 0; k < HK / 16; ++k) {              // P over S columns that have been read
+                    float x[16];
+                    scores(k, x);
+                    const float v = scales[8 + ((hf * HK + k * 16) >> box_shift)] * P_UP;
+                    uint32_t w[8];
 #pragma unroll
-                for (int h = 0; h < HK; h += 32) {               // P over the S columns that have been read
-                    uint32_t w[16];
-#pragma unroll
-                    for (int k = 0; k < 32; k += 4) {
-                        const float4 sc = *reinterpret_cast<const float4*>(vs + h + k);
-                        const float e0 = exp2_fast(x[h + k] + neg), e1 = exp2_fast(x[h + k + 1] + neg);
-                        const float e2 = exp2_fast(x[h + k + 2] + neg), e3 = exp2_fast(x[h + k + 3] + neg);
-                        sum += (e0 + e1) + (e2 + e3);
-                        w[k / 2] = f16_pair(e0 * sc.x, e1 * sc.y);
-                        w[k / 2 + 1] = f16_pair(e2 * sc.z, e3 * sc.w);
+                    for (int y = 0; y < 16; y += 2) {
+                        const float e0 = exp2_fast(x[y] + neg), e1 = exp2_fast(x[y + 1] + neg);
+                        sum += e0 + e1;
+                        w[y / 2] = f16_pair(e0 * v, e1 * v);
                     }
-                    tmem_st16_words(s_at + h / 2, w);
+                    tmem_st8_words(s_at + k * 8, w);
                 }
                 l += sum;
                 ptx::tmem_wait_st();
@@ -420,6 +438,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_rows_kernel(const AttnArgs p, 
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&c.p_full[b]));
             }
+            ptx::mbar_wait(ptx::smem_u32(&c.v_seen[(i - 1) % MARKS]), ((i - 1) / MARKS) & 1, abort, status);
             ptx::mbar_wait(ptx::smem_u32(&c.pv_done[(i - 1) & 1]), ((i - 1) >> 1) & 1, abort, status);
             ptx::tc_fence_after();
             *reinterpret_cast<float2*>(halves + (hf * ROWS + row) * 2) = make_float2(ref, l);
@@ -436,11 +455,11 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_rows_kernel(const AttnArgs p, 
             const auto out_at = [&](int r) {
                 return (bf16*)p.a.out + (int64_t)(q.r0 + q0 + r / p.G) * p.a.out_stride + (int64_t)(g * p.G + r % p.G) * HD;
             };
-            const bool marked = c.any_nan[item % RING] != 0;
-            const int* marks = nan_marks + (item % RING) * HD;
+            const bool marked = c.any_nan[item % MARKS] != 0;
+            const int* marks = nan_marks + (item % MARKS) * HD;
             const float inv = 1.f / L;
             // this thread's half of the row's dims
-#pragma unroll
+#pragma unroll 1
             for (int k = 0; k < HD / 2; k += 16) {
                 const int d = hf * (HD / 2) + k;
                 float a0[16], a1[16];
@@ -507,27 +526,26 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_rows_kernel(const AttnArgs p, 
     }
 }
 
-template <int HD> cudaError_t launch_dim(const Kv8& c, AttnArgs& p, const uint8_t* kc, const uint8_t* vc, cudaStream_t s) {
+template <int HD> cudaError_t launch_dim(const Kv8& c, AttnArgs& p, cudaStream_t s) {
     static std::atomic<uint64_t> done{0};
     const cudaError_t e = smem_limit_once(kv8_rows_kernel<HD>, Rows<HD>::BYTES, done);
     if (e != cudaSuccess) return e;
     p.QT = ROWS / p.G;
     const int64_t items = ((int64_t)p.r.n_rows / p.QT + p.q.n) * p.Hkv;
     const int64_t tiles = items * ((p.q.max_len + TK - 1) / TK + 1);
+    CUtensorMap map;
+    memcpy(&map, c.map, sizeof map);
     return launch_ex(c.pdl, kv8_rows_kernel<HD>, dim3((unsigned)(tiles < c.num_sms ? tiles : c.num_sms)), dim3(THREADS), Rows<HD>::BYTES, s,
-                     p, kc, vc);
+                     map, p);
 }
 
 }  // namespace
 
 size_t kv8_rows_part_floats(int num_sms) { return (size_t)num_sms * 2 * Rows<128>::PIECE; }
 
-cudaError_t launch_kv8_rows(const Kv8& c, const void* attn_args, int layer, cudaStream_t s) {
+cudaError_t launch_kv8_rows(const Kv8& c, const void* attn_args, cudaStream_t s) {
     AttnArgs p = *static_cast<const AttnArgs*>(attn_args);
-    const int64_t blocks = c.cfg.n_pages * c.cfg.n_kv_heads, bytes = (int64_t)c.cfg.head_dim << c.shift;
-    const uint8_t* kc = c.codes + (int64_t)layer * 2 * blocks * bytes;
-    const uint8_t* vc = kc + blocks * bytes;
-    return c.cfg.head_dim == 128 ? launch_dim<128>(c, p, kc, vc, s) : launch_dim<64>(c, p, kc, vc, s);
+    return c.cfg.head_dim == 128 ? launch_dim<128>(c, p, s) : launch_dim<64>(c, p, s);
 }
 
 }  // namespace cb
