@@ -1,7 +1,7 @@
 // What the two kernels of attention over the 8-bit cache share: their arguments and the list of tiles that divides the
 // work.  An item is (sequence, tile of QT query rows, KV head), cut into tiles of 128 keys; the tiles of all items form one
 // list, in this order, and every CTA takes an equal, contiguous piece of it.  An item that spans CTAs leaves a partial
-// result per CTA; the CTA that finishes last joins them in their order.
+// result per CTA, and the partial results are joined in their order.
 #pragma once
 #include <climits>
 
@@ -28,6 +28,7 @@ struct AttnArgs {
     int min_tiles;                       // tiles per CTA, at least
     float* part;                         // [cta][2][NC][HD + 2] pieces of items that span CTAs
     unsigned* arrived;                   // [cta] pieces finished of the item that begins in this CTA (0 between calls)
+    int* todo;                           // many rows: [cta] what the joining kernel has to do (5 ints)
     float* scores;                       // weights: [Hkv][n_q][G][score_ld] scores in the exp2 domain
     int score_ld;
     float2* stats;                       // weights: [Hkv][n_q][G] (max, 1 / sum)

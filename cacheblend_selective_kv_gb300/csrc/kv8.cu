@@ -141,12 +141,13 @@ cb_status cb_kv8_create(const cb_kv8_config* cfg, void* codes, float* scales, cb
         delete h;
         return fail(CB_ERR_CUDA, "cb_kv8_create: no CUDA device");
     }
-    // one allocation: status, arrival counts (both zero between calls), pieces, statistics, scores
+    // one allocation: status, arrival counts (both zero between calls), pieces, statistics, what is to be joined, scores
     const size_t head = 256 + ((size_t)kv8_most_ctas(h->num_sms) * 4 + 255) / 256 * 256;
     const size_t part = (kv8_part_floats(h->num_sms) * 4 + 255) / 256 * 256;
     // a row of a call that returns weights takes at least 129 cells
     const size_t stats = c.weight_cells > 0 ? (((size_t)c.weight_cells / 129 + 1) * sizeof(float2) + 255) / 256 * 256 : 0;
-    if (cudaMalloc(&h->scratch, head + part + stats + (size_t)c.weight_cells * 4) != cudaSuccess) {
+    const size_t todo = ((size_t)h->num_sms * 5 * 4 + 255) / 256 * 256;
+    if (cudaMalloc(&h->scratch, head + part + stats + todo + (size_t)c.weight_cells * 4) != cudaSuccess) {
         cudaGetLastError();
         delete h;
         return fail(CB_ERR_OOM, "cb_kv8_create: workspace allocation failed");
@@ -156,7 +157,8 @@ cb_status cb_kv8_create(const cb_kv8_config* cfg, void* codes, float* scales, cb
     h->arrived = (unsigned*)(at + 256);
     h->part = (float*)(at + head);
     h->stats = (float2*)(at + head + part);
-    h->scores = (float*)(at + head + part + stats);
+    h->todo = (int*)(at + head + part + stats);
+    h->scores = (float*)(at + head + part + stats + todo);
     // cleared before the handle is given out, whatever stream its first call uses
     if (!kv8_make_map(*h, h->map) || cudaMemset(h->scratch, 0, head) != cudaSuccess ||
         cudaStreamSynchronize(cudaStreamLegacy) != cudaSuccess) {

@@ -584,9 +584,8 @@ __global__ void __launch_bounds__(512) kv8_weights_kernel(const AttnArgs p) {
         const float2* st = p.stats + at;
         const int seen = max(0, j - (q.len - q.n)) * p.G, cols = q.n * p.G;      // columns that see key j: [seen, cols)
         const int by = blockDim.y;
-#pragma unroll 8
-        for (int k = (seen & ~3) + y; k < cols; k += by) {
-            if (k < seen) continue;
+#pragma unroll 16
+        for (int k = seen + y; k < cols; k += by) {
             const float x = __ldcs(score + (int64_t)k * p.score_ld);
             const float2 m = st[k];
             w += x == -INFINITY ? 0.f : exp2_fast(x - m.x) * m.y;

@@ -35,6 +35,10 @@ constexpr int KT = 2, VT = 1;            // tiles of K and V codes
 constexpr float GROW = 8.f;              // how far (log2) P may outgrow its reference
 constexpr float P_UP = 128.f;            // P is stored this much larger: its largest values are 2^7 .. 2^15 of fp16's 2^16
 
+struct Todo {                            // an item that begins in a CTA and ends in another: its rows and pieces
+    int row0, cols, g, pos0, pieces;
+};
+
 struct RowsShared {
     uint64_t kc_full[KT], kc_empty[KT], vc_full[VT], vc_empty[VT];          // codes
     uint64_t k_full[2], k_empty[2], v_full[2], pv_done[2], s_full[2], p_full[2];
@@ -45,7 +49,6 @@ struct RowsShared {
     uint32_t tmem;
     int abort;
     Find find;
-    int last;
     int any_nan[MARKS];                  // an item's V held NaN that not all of its rows see
 };
 
@@ -77,10 +80,12 @@ __device__ __forceinline__ void mma_f16_tmem_a(uint32_t d, uint32_t a, uint64_t 
         ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc)
         : "memory");
 }
-__device__ __forceinline__ void tmem_st8_words(uint32_t addr, const uint32_t* v) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
-                 ::"r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-                 : "memory");
+__device__ __forceinline__ void tmem_st16_words(uint32_t addr, const uint32_t* v) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};"
+        ::"r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]),
+          "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        : "memory");
 }
 __device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
     const __nv_bfloat162 t = __floats2bfloat162_rn(a, b);
@@ -182,35 +187,46 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_rows_kernel(const __grid_const
             const int q0 = cur.qt * p.QT, cols = min(p.QT, q.n - q0) * p.G, pos0 = q.len - q.n + q0, tile = cur.t;
             if (begins) {
                 ++item;
-                // Q once the products with the item before's are done; then the softmax is past tile i - 3, hence past the item
-                // whose marks and row scales these were
-                if (i > 0) ptx::mbar_wait(ptx::smem_u32(&c.k_empty[(i - 1) & 1]), ((i - 1) >> 1) & 1, abort, status);
-                if (t < HD) nan_marks[(item % MARKS) * HD + t] = INT_MAX;
-                if (t == 0) c.any_nan[item % MARKS] = 0;
                 const bf16* qbase = (const bf16*)p.a.q + (int64_t)(q.r0 + q0) * p.a.q_stride + (int64_t)cur.g * p.G * HD;
-                constexpr int QL = HD / 8;                       // lanes of a row, 8 values each
-#pragma unroll 2
-                for (int r = w * (32 / QL) + lane / QL; r < ROWS; r += 4 * (32 / QL)) {
-                    uint4 val = make_uint4(0, 0, 0, 0);
-                    if (r < cols)
-                        val = *reinterpret_cast<const uint4*>(qbase + (int64_t)(r / p.G) * p.a.q_stride + (r % p.G) * HD + lane % QL * 8);
-                    const uint32_t word[4] = {val.x, val.y, val.z, val.w};
-                    float f[8], top = 0.f;
+                constexpr int QL = HD / 8, QR = 32 / QL, QB = ROWS / (4 * QR) / 2;  // lanes of a row (8 values each), rows of a warp, batch
+#pragma unroll 1
+                for (int h = 0; h < 2; ++h) {
+                    uint4 val[QB];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        f[2 * k] = __uint_as_float(word[k] << 16);
-                        f[2 * k + 1] = __uint_as_float(word[k] & 0xffff0000u);
-                        top = fmaxf(top, fmaxf(kv8_mag(f[2 * k]), kv8_mag(f[2 * k + 1])));
+                    for (int n = 0; n < QB; ++n) {
+                        const int r = ((h * QB + n) * 4 + w) * QR + lane / QL;
+                        val[n] = r < cols ? *reinterpret_cast<const uint4*>(qbase + (int64_t)(r / p.G) * p.a.q_stride + (r % p.G) * HD +
+                                                                            lane % QL * 8)
+                                          : make_uint4(0, 0, 0, 0);
+                    }
+                    if (h == 0) {
+                        // once the products with the item before's Q are done; then the softmax is past tile i - 3, hence past the
+                        // item whose marks and row scales these were
+                        if (i > 0) ptx::mbar_wait(ptx::smem_u32(&c.k_empty[(i - 1) & 1]), ((i - 1) >> 1) & 1, abort, status);
+                        if (t < HD) nan_marks[(item % MARKS) * HD + t] = INT_MAX;
+                        if (t == 0) c.any_nan[item % MARKS] = 0;
                     }
 #pragma unroll
-                    for (int o = QL / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-                    // kv8_scale brings the largest value to 224 .. 448; 2^6 more is 2^14 .. 2^15 less a little
-                    const float sc = kv8_scale(top), up = kv8_inverse(sc) * 64.f;
-                    uint32_t o[4];
+                    for (int n = 0; n < QB; ++n) {
+                        const int r = ((h * QB + n) * 4 + w) * QR + lane / QL;
+                        const uint32_t word[4] = {val[n].x, val[n].y, val[n].z, val[n].w};
+                        float f[8], top = 0.f;
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) o[k] = f16_pair(f[2 * k] * up, f[2 * k + 1] * up);
-                    *reinterpret_cast<uint4*>(sQ + wide_at(r, lane % QL)) = make_uint4(o[0], o[1], o[2], o[3]);
-                    if (lane % QL == 0) row_scale[(item % MARKS) * ROWS + r] = sc * (1.f / 64.f);
+                        for (int k = 0; k < 4; ++k) {
+                            f[2 * k] = __uint_as_float(word[k] << 16);
+                            f[2 * k + 1] = __uint_as_float(word[k] & 0xffff0000u);
+                            top = fmaxf(top, fmaxf(kv8_mag(f[2 * k]), kv8_mag(f[2 * k + 1])));
+                        }
+#pragma unroll
+                        for (int o = QL / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                        // kv8_scale brings the largest value to 224 .. 448; 2^6 more is 2^14 .. 2^15 less a little
+                        const float sc = kv8_scale(top), up = kv8_inverse(sc) * 64.f;
+                        uint32_t o[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) o[k] = f16_pair(f[2 * k] * up, f[2 * k + 1] * up);
+                        *reinterpret_cast<uint4*>(sQ + wide_at(r, lane % QL)) = make_uint4(o[0], o[1], o[2], o[3]);
+                        if (lane % QL == 0) row_scale[(item % MARKS) * ROWS + r] = sc * (1.f / 64.f);
+                    }
                 }
                 fence_async_smem();
                 ptx::named_bar_sync(2, CONV);                    // also: the marks
@@ -253,16 +269,24 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_rows_kernel(const __grid_const
             ptx::mbar_wait(ptx::smem_u32(&c.ring.full[i % RING]), (i / RING) & 1, abort, status);
             ptx::mbar_wait(ptx::smem_u32(&c.vc_full[i % VT]), (i / VT) & 1, abort, status);
             ptx::mbar_wait(ptx::smem_u32(&c.pv_done[st]), par, abort, status);
+            const float* loaded = c.ring.scale[i % RING][0];
+            const bool plain = (tile + 1) * TK <= min(q.len, pos0 + 1) &&
+                               !__any_sync(0xffffffffu, lane < (TK >> box_shift) && loaded[lane] < 0.f);
+            const auto codes_of = [&](int row) {
+                return *reinterpret_cast<const uint4*>(sm + S::OFF_VC + (i % VT) * S::CODES + f8_at<HD>(row, e * 16));
+            };
+            if (plain) {
 #pragma unroll 2
-            for (int n = 0; n < NI; ++n) {
-                const int row = row0 + n * 4 * RPW, j = tile * TK + row;
-                uint4 x = *reinterpret_cast<const uint4*>(sm + S::OFF_VC + (i % VT) * S::CODES + f8_at<HD>(row, e * 16));
-                if (j >= q.len || c.ring.scale[i % RING][0][row >> box_shift] < 0.f) {
-                    x = make_uint4(0, 0, 0, 0);
-                } else if (j > pos0) {
-                    take_nan(x, j, nan_marks + (item % MARKS) * HD + e * 16, &c.any_nan[item % MARKS]);
+                for (int n = 0; n < NI; ++n) widen(sV + st * S::TILE, row0 + n * 4 * RPW, codes_of(row0 + n * 4 * RPW));
+            } else {
+#pragma unroll 1
+                for (int n = 0; n < NI; ++n) {
+                    const int row = row0 + n * 4 * RPW, j = tile * TK + row;
+                    uint4 x = codes_of(row);
+                    if (j >= q.len || loaded[row >> box_shift] < 0.f) x = make_uint4(0, 0, 0, 0);
+                    else if (j > pos0) take_nan(x, j, nan_marks + (item % MARKS) * HD + e * 16, &c.any_nan[item % MARKS]);
+                    widen(sV + st * S::TILE, row, x);
                 }
-                widen(sV + st * S::TILE, row, x);
             }
             fence_async_smem();
             __syncwarp();
@@ -342,6 +366,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_rows_kernel(const __grid_const
         const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
         const float to_exp2 = p.a.scale * 1.4426950408889634f;
         const int box_shift = min(p.q.shift, 7);
+        Todo todo{0, 0, 0, 0, 0};
         int item = 0;
         for (int i = 0; i < count; ++item) {
             const int first = cur.t, n_here = min(cur.nt - first, count - i), g = cur.g;
@@ -360,40 +385,49 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_rows_kernel(const __grid_const
                 ptx::mbar_wait(ptx::smem_u32(&c.s_full[b]), (i >> 1) & 1, abort, status);
                 ptx::tc_fence_after();
                 const uint32_t s_at = lanes + b * 128 + hf * HK;
-                // Scores of a block of 16 keys in the exp2 domain: S times K's scale (with the row's and the softmax's
-                // constants); -inf for a block that is not loaded and for keys the row does not see.  Computed twice, for the
+                // Scores of 32 keys in the exp2 domain: S times the scale of K's block (16 keys at least) with the row's and the
+                // softmax's constants; -inf for a block that is not loaded and for keys the row does not see.  Computed twice, for the
                 // maximum and for P: the loops stay short, and so do the instructions to fetch (unrolled over the 64 keys in
                 // registers, most cycles went to waiting for instructions).
                 const float* scales = c.ring.scale[i % RING][0];
                 const auto scores = [&](int k, float* x) {
-                    uint32_t w[16];
-                    ptx::tmem_ld16_issue(s_at + k * 16, w);
-                    const float ks = scales[(hf * HK + k * 16) >> box_shift], m = ks * row_mul;
+                    uint32_t w[32];
+                    ptx::tmem_ld16_issue(s_at + k, w);
+                    ptx::tmem_ld16_issue(s_at + k + 16, w + 16);
+                    const float* ks = scales + ((hf * HK + k) >> box_shift);
+                    const int second = box_shift == 4 ? 1 : 0;   // the other 16 keys' block
+                    const float m0 = ks[0] * row_mul, m1 = ks[second] * row_mul;
                     ptx::tmem_ld_wait16(w);
+                    ptx::tmem_ld_wait16(w + 16);
 #pragma unroll
-                    for (int y = 0; y < 16; ++y) x[y] = __uint_as_float(w[y]) * m;
-                    if (ks < 0.f || j0 + k * 16 + 15 > pos0) {
-                        const int seen = ks < 0.f ? 0 : pos - (j0 + k * 16) + 1;
+                    for (int y = 0; y < 32; ++y) x[y] = __uint_as_float(w[y]) * (y < 16 ? m0 : m1);
+                    if (ks[0] < 0.f || ks[second] < 0.f || j0 + k + 31 > pos0) {
+                        const int seen = pos - (j0 + k) + 1, low = ks[0] < 0.f ? 0 : seen, high = ks[second] < 0.f ? 0 : seen;
 #pragma unroll
-                        for (int y = 0; y < 16; ++y)
-                            if (y >= seen) x[y] = -INFINITY;
+                        for (int y = 0; y < 32; ++y)
+                            if (y >= (y < 16 ? low : high)) x[y] = -INFINITY;
                     }
+                };
+                const auto v_log = [](float v) {                 // log2 of V's scale, a power of two
+                    return v > 0.f ? fmaxf((float)((int)(__float_as_uint(v) >> 23) - 127), -100.f) : -100.f;
                 };
                 float top = -INFINITY;                           // the largest of score + log2 of V's scale
 #pragma unroll 1
-                for (int k = 0; k < HK / 16; ++k) {
-                    float x[16];
+                for (int k = 0; k < HK; k += 32) {
+                    float x[32];
                     scores(k, x);
-                    const float v = scales[8 + ((hf * HK + k * 16) >> box_shift)];
-                    const float vl = v > 0.f ? fmaxf((float)((int)(__float_as_uint(v) >> 23) - 127), -100.f) : -100.f;
-                    float m = x[0];
+                    float m[2] = {x[0], x[16]};
 #pragma unroll
-                    for (int y = 1; y < 16; ++y) m = fmaxf(m, x[y]);
-                    top = fmaxf(top, m + vl);
+                    for (int y = 1; y < 16; ++y) {
+                        m[0] = fmaxf(m[0], x[y]);
+                        m[1] = fmaxf(m[1], x[16 + y]);
+                    }
+                    const float* v = scales + 8 + ((hf * HK + k) >> box_shift);
+                    top = fmaxf(top, fmaxf(m[0] + v_log(v[0]), m[1] + v_log(v[box_shift == 4 ? 1 : 0])));
                     if (p.scores && row < cols) {
-                        float4* score = reinterpret_cast<float4*>(p.scores + (stat0 + row) * p.score_ld + j0 + k * 16);
+                        float4* score = reinterpret_cast<float4*>(p.scores + (stat0 + row) * p.score_ld + j0 + k);
 #pragma unroll
-                        for (int y = 0; y < 4; ++y) score[y] = make_float4(x[4 * y], x[4 * y + 1], x[4 * y + 2], x[4 * y + 3]);
+                        for (int y = 0; y < 8; ++y) score[y] = make_float4(x[4 * y], x[4 * y + 1], x[4 * y + 2], x[4 * y + 3]);
                     }
                 }
                 if (__any_sync(0xffffffffu, ref != -INFINITY && top > ref + GROW)) {
@@ -419,18 +453,19 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_rows_kernel(const __grid_const
                 const float neg = ref == -INFINITY ? 0.f : -ref;
                 float sum = 0.f;
 #pragma unroll 1
-                for (int k = 0; k < HK / 16; ++k) {              // P over S columns that have been read
-                    float x[16];
+                for (int k = 0; k < HK; k += 32) {               // P over S columns that have been read
+                    float x[32];
                     scores(k, x);
-                    const float v = scales[8 + ((hf * HK + k * 16) >> box_shift)] * P_UP;
-                    uint32_t w[8];
+                    const float* v = scales + 8 + ((hf * HK + k) >> box_shift);
+                    const float v0 = v[0] * P_UP, v1 = v[box_shift == 4 ? 1 : 0] * P_UP;
+                    uint32_t w[16];
 #pragma unroll
-                    for (int y = 0; y < 16; y += 2) {
+                    for (int y = 0; y < 32; y += 2) {
                         const float e0 = exp2_fast(x[y] + neg), e1 = exp2_fast(x[y + 1] + neg);
                         sum += e0 + e1;
-                        w[y / 2] = f16_pair(e0 * v, e1 * v);
+                        w[y / 2] = f16_pair(e0 * (y < 16 ? v0 : v1), e1 * (y < 16 ? v0 : v1));
                     }
-                    tmem_st8_words(s_at + k * 8, w);
+                    tmem_st16_words(s_at + k / 2, w);
                 }
                 l += sum;
                 ptx::tmem_wait_st();
@@ -497,32 +532,39 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_rows_kernel(const __grid_const
             } else {
                 if (hf == 0 && row < cols)
                     *reinterpret_cast<float2*>(piece_at(blockIdx.x - u0) + ROWS * HD + 2 * row) = make_float2(M, L);
-                ptx::named_bar_sync(1, SOFT);
-                if (tid == 0) {
-                    __threadfence();                             // the whole CTA's piece, ordered by the barrier
-                    c.last = atomicAdd(p.arrived + u0, 1u) == (unsigned)n_pieces - 1;
-                    if (c.last) atomicExch(p.arrived + u0, 0u);
-                    __threadfence();
-                }
-                ptx::named_bar_sync(1, SOFT);
-                if (c.last) {
-                    for (int k = warp; k < cols; k += SOFT / 32) {
-                        float m, sum;
-                        const float4 a = join_pieces<HD>(piece_at, n_pieces, k * HD, ROWS * HD + 2 * k, m, sum);
-                        if (lane < HD / 4) store4(out_at(k) + lane * 4, a, 1.f / sum, pos0 + k / p.G >= 0);
-                        if (p.scores && lane == 0) p.stats[stat0 + k] = make_float2(m, 1.f / sum);
-                    }
-                    ptx::named_bar_sync(1, SOFT);                // `last` has been read
-                }
+                // (the CTA in which the item begins says so to the joining kernel)
+                if (first == 0 && tid == 0) todo = Todo{q.r0 + q0, cols, g, pos0, n_pieces};
+                ptx::named_bar_sync(3 + quarter, 64);            // `halves` has been read
             }
             if (i < count) cur.next_item(p);
         }
+        if (tid == 0) reinterpret_cast<Todo*>(p.todo)[blockIdx.x] = todo;
     }
     ptx::tc_fence_before();
     __syncthreads();
     if (warp == MMA_WARP) {
         ptx::tc_fence_after();
         ptx::tmem_dealloc(tmem, 512);
+    }
+}
+
+// The items that span CTAs, a row per warp: block (u, y) has rows y, y + gridDim.y, .. (8 at a time) of the item that begins
+// in CTA u.  A kernel of its own, because a piece is 128 rows: joined by the CTA that ends last, the 64 rows of a query over
+// 8K took 15 us of one CTA's time.
+template <int HD>
+__global__ void __launch_bounds__(256) kv8_join_kernel(const AttnArgs p) {
+    grid_dep_launch();
+    grid_dep_wait();
+    const Todo d = reinterpret_cast<const Todo*>(p.todo)[blockIdx.x];
+    if (d.pieces == 0) return;
+    const int lane = threadIdx.x & 31, u0 = blockIdx.x;
+    const auto piece_at = [&](int u) { return p.part + (int64_t)((u0 + u) * 2 + (u == 0 ? 1 : 0)) * Rows<HD>::PIECE; };
+    for (int k = blockIdx.y * 8 + (threadIdx.x >> 5); k < d.cols; k += gridDim.y * 8) {
+        float m, l;
+        const float4 a = join_pieces<HD>(piece_at, d.pieces, k * HD, ROWS * HD + 2 * k, m, l);
+        bf16* out = (bf16*)p.a.out + (int64_t)(d.row0 + k / p.G) * p.a.out_stride + (int64_t)(d.g * p.G + k % p.G) * HD;
+        if (lane < HD / 4) store4(out + lane * 4, a, 1.f / l, d.pos0 + k / p.G >= 0);
+        if (p.scores && lane == 0) p.stats[((int64_t)d.g * p.r.n_rows + d.row0) * p.G + k] = make_float2(m, 1.f / l);
     }
 }
 
@@ -535,8 +577,10 @@ template <int HD> cudaError_t launch_dim(const Kv8& c, AttnArgs& p, cudaStream_t
     const int64_t tiles = items * ((p.q.max_len + TK - 1) / TK + 1);
     CUtensorMap map;
     memcpy(&map, c.map, sizeof map);
-    return launch_ex(c.pdl, kv8_rows_kernel<HD>, dim3((unsigned)(tiles < c.num_sms ? tiles : c.num_sms)), dim3(THREADS), Rows<HD>::BYTES, s,
-                     map, p);
+    const unsigned ctas = (unsigned)(tiles < c.num_sms ? tiles : c.num_sms);
+    const cudaError_t err = launch_ex(c.pdl, kv8_rows_kernel<HD>, dim3(ctas), dim3(THREADS), Rows<HD>::BYTES, s, map, p);
+    if (err != cudaSuccess) return err;
+    return launch_ex(c.pdl, kv8_join_kernel<HD>, dim3(ctas, 8), dim3(256), 0, s, p);
 }
 
 }  // namespace
@@ -545,6 +589,7 @@ size_t kv8_rows_part_floats(int num_sms) { return (size_t)num_sms * 2 * Rows<128
 
 cudaError_t launch_kv8_rows(const Kv8& c, const void* attn_args, cudaStream_t s) {
     AttnArgs p = *static_cast<const AttnArgs*>(attn_args);
+    p.todo = c.todo;
     return c.cfg.head_dim == 128 ? launch_dim<128>(c, p, s) : launch_dim<64>(c, p, s);
 }
 
