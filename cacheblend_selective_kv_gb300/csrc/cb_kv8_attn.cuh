@@ -23,6 +23,7 @@ struct AttnArgs {
     const float* ks;                     // this layer's scales [n_pages][Hkv]
     const float* vs;
     int Hq, Hkv, G, QT;                  // QT = query rows per item
+    unsigned inv_g;                      // ceil(2^16 / G): k / G for k below 2^13
     int kz;                              // z coordinate of this layer's K in the map (V is kz + 1)
     int box;                             // rows of a TMA box: min(page_size, 128)
     int min_tiles;                       // tiles per CTA, at least
@@ -33,6 +34,10 @@ struct AttnArgs {
     int score_ld;
     float2* stats;                       // weights: [Hkv][n_q][G] (max, 1 / sum)
 };
+
+// k / G and k % G of a column or row of an item
+__device__ __forceinline__ int div_g(const AttnArgs& p, int k) { return (int)(((unsigned)k * p.inv_g) >> 16); }
+__device__ __forceinline__ int mod_g(const AttnArgs& p, int k) { return k - div_g(p, k) * p.G; }
 
 __device__ __forceinline__ float exp2_fast(float x) {          // special-function unit, about 2 ulp
     float y;
@@ -56,8 +61,9 @@ __device__ __forceinline__ Seq seq_at(const AttnArgs& p, int s) {
     q.n = r1 - q.r0;
     return q;
 }
-__device__ __forceinline__ long long seq_tiles(const AttnArgs& p, const Seq& q) {
-    long long t = 0;
+__device__ __forceinline__ int seq_tiles(const AttnArgs& p, const Seq& q) {
+    int t = 0;
+#pragma unroll 1
     for (int qt = 0; qt < q.q_tiles(p.QT); ++qt) t += q.tiles(qt, p.QT);
     return t * p.Hkv;
 }
@@ -93,6 +99,7 @@ __device__ __forceinline__ float4 join_pieces(const F& piece_at, int n_pieces, i
     m = warp_max(m);
     l = 0.f;
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
     for (int ub = 0; ub < n_pieces; ub += 32) {
         float f = 0.f;
         if (ub + lane < n_pieces) {
@@ -101,6 +108,7 @@ __device__ __forceinline__ float4 join_pieces(const F& piece_at, int n_pieces, i
             l = fmaf(ml.y, f, l);
         }
         const int n = min(32, n_pieces - ub);
+#pragma unroll 1
         for (int v0 = 0; v0 < n; v0 += 8 * SIDE) {
             float4 o[8];
 #pragma unroll
@@ -137,71 +145,75 @@ template <typename T> __device__ __forceinline__ void store4(T* o, const float4&
 
 // This CTA's piece of the list: tiles t0 .. t0 + count - 1, `per` for every CTA but the last.
 struct Piece {
-    long long per, t0;
-    int count;
+    int per, t0, count;
 };
 struct Find {                            // shared memory of find_piece
     int s, qt, g, t;
     Seq q;
-    long long sums[32];
+    int sums[32];
 };
 
 // Finds it and the cursor at its first tile, THREADS sequences at a time (the first step's are kept); before and after run
-// around the first barrier, which also publishes what the caller has set up in shared memory.
+// around the first barrier, which also publishes what the caller has set up in shared memory.  (The host refuses calls of
+// 2^31 tiles.  This and what ends an item run once or twice per CTA, from instructions that have to be fetched first: short
+// loops and 32-bit arithmetic are worth more here than fewer steps.)
 template <int THREADS, typename F, typename H>
 __device__ __forceinline__ void find_piece(const AttnArgs& p, Find& f, Piece& mine, Cursor& cur, F before_sync, H after_sync) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const Seq q_own = tid < p.q.n ? seq_at(p, tid) : Seq{0, 0, 0};
-    const long long t_own = seq_tiles(p, q_own);
+    const int t_own = seq_tiles(p, q_own);
     {
-        long long sum = t_own;
+        int sum = t_own;
+#pragma unroll 1
         for (int s = tid + THREADS; s < p.q.n; s += THREADS) sum += seq_tiles(p, seq_at(p, s));
-        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        sum = __reduce_add_sync(0xffffffffu, sum);
         if (lane == 0) f.sums[warp] = sum;
     }
     before_sync();
     __syncthreads();
     after_sync();
-    long long total = 0;
-    for (int w = 0; w < THREADS / 32; ++w) total += f.sums[w];
-    mine.per = max((total + gridDim.x - 1) / gridDim.x, (long long)p.min_tiles);
-    mine.t0 = blockIdx.x * mine.per;
-    mine.count = (int)min(mine.per, max(0ll, total - mine.t0));
+    const int total = __reduce_add_sync(0xffffffffu, lane < THREADS / 32 ? f.sums[lane] : 0);
+    mine.per = max((int)(((unsigned)total + gridDim.x - 1) / gridDim.x), p.min_tiles);
+    const long long t0 = (long long)blockIdx.x * mine.per;
+    mine.t0 = (int)min(t0, (long long)total);
+    mine.count = min(mine.per, total - mine.t0);
     if (mine.count == 0) return;
-    long long base = 0;                                          // tiles of the sequences before this step's
+    int base = 0;                                                // tiles of the sequences before this step's
+#pragma unroll 1
     for (int s0 = 0; s0 < p.q.n; s0 += THREADS) {
         const int s = s0 + tid;
-        const Seq q = s0 == 0 ? q_own : (s < p.q.n ? seq_at(p, s) : Seq{0, 0, 0});
-        const long long n = s0 == 0 ? t_own : seq_tiles(p, q);
-        long long x = n;
+        Seq q = q_own;
+        int n = t_own;
+        if (s0 > 0) {
+            q = s < p.q.n ? seq_at(p, s) : Seq{0, 0, 0};
+            n = seq_tiles(p, q);
+        }
+        int x = n;
+#pragma unroll 1
         for (int o = 1; o < 32; o <<= 1) {
-            const long long y = __shfl_up_sync(0xffffffffu, x, o);
+            const int y = __shfl_up_sync(0xffffffffu, x, o);
             if (lane >= o) x += y;
         }
         __syncthreads();                                         // sums has been read
         if (lane == 31) f.sums[warp] = x;
         __syncthreads();
-        long long before = base, all = base;
-        for (int w = 0; w < THREADS / 32; ++w) {
-            if (w < warp) before += f.sums[w];
-            all += f.sums[w];
-        }
-        before += x - n;
+        const int w = lane < THREADS / 32 ? f.sums[lane] : 0;
+        const int before = base + __reduce_add_sync(0xffffffffu, lane < warp ? w : 0) + x - n;
+        base += __reduce_add_sync(0xffffffffu, w);
         if (n > 0 && before <= mine.t0 && mine.t0 < before + n) {
-            long long left = mine.t0 - before;
-            int qt = 0, nt = q.tiles(0, p.QT);
-            while (left >= (long long)nt * p.Hkv) {
-                left -= (long long)nt * p.Hkv;
+            int left = mine.t0 - before, qt = 0, nt = q.tiles(0, p.QT);
+#pragma unroll 1
+            while (left >= nt * p.Hkv) {
+                left -= nt * p.Hkv;
                 nt = q.tiles(++qt, p.QT);
             }
             f.s = s;
             f.qt = qt;
-            f.g = (int)(left / nt);
-            f.t = (int)(left % nt);
+            f.g = left / nt;
+            f.t = left - f.g * nt;
             f.q = q;
         }
-        if (all > mine.t0) break;
-        base = all;
+        if (base > mine.t0) break;
     }
     __syncthreads();
     cur.s = f.s;

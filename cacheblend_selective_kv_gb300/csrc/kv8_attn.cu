@@ -152,7 +152,7 @@ __device__ __noinline__ void q_terms(const AttnArgs& p, const Cursor& u, uint8_t
     for (int r = warp; r < S::NC; r += S::SOFT / 32) {
         float x[E];
         float top = 0.f;
-        const T* src = qbase + (int64_t)(r / p.G) * p.a.q_stride + (r % p.G) * HD + lane * E;
+        const T* src = qbase + (int64_t)(div_g(p, r)) * p.a.q_stride + (mod_g(p, r)) * HD + lane * E;
 #pragma unroll
         for (int k = 0; k < E; ++k) {
             x[k] = r < cols ? to_f(src[k]) : 0.f;
@@ -258,7 +258,7 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
     Piece mine;
     Cursor cur;
     find_piece<THREADS>(p, c.find, mine, cur, [] { ptx::tc_fence_before(); }, [] { ptx::tc_fence_after(); });
-    const long long per = mine.per, t0 = mine.t0;
+    const int per = mine.per, t0 = mine.t0;
     const int count = mine.count;                        // tiles of this CTA
     const uint32_t tmem = c.tmem;
 
@@ -516,19 +516,19 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
                     if (k >= k0) acc[k] = __int_as_float(0x7fc00000);
             }
             const auto out_at = [&](int k) {                     // output row of column k
-                return (T*)p.a.out + (int64_t)(q.r0 + q0 + k / p.G) * p.a.out_stride + (int64_t)(g * p.G + k % p.G) * HD;
+                return (T*)p.a.out + (int64_t)(q.r0 + q0 + div_g(p, k)) * p.a.out_stride + (int64_t)(g * p.G + mod_g(p, k)) * HD;
             };
             if (first == 0 && n_here == cur.nt) {
 #pragma unroll
                 for (int k = 0; k < NW; ++k) {
                     if (c0 + k >= cols) continue;
                     const float inv = 1.f / lsum[k];
-                    if (key < HD) out_at(c0 + k)[key] = from_f<T>(pos0 + (c0 + k) / p.G >= 0 ? acc[k] * inv : 0.f);
+                    if (key < HD) out_at(c0 + k)[key] = from_f<T>(pos0 + div_g(p, c0 + k) >= 0 ? acc[k] * inv : 0.f);
                     if (p.scores && key == 0) p.stats[stat0 + c0 + k] = make_float2(colm[c0 + k], inv);
                 }
             } else {
-                const long long begin = t0 + (i - n_here) - first;           // the item's first tile in the list
-                const int u0 = (int)(begin / per), n_pieces = (int)((begin + cur.nt - 1) / per) - u0 + 1;
+                const int begin = t0 + (i - n_here) - first;           // the item's first tile in the list
+                const int u0 = (unsigned)begin / (unsigned)per, n_pieces = (int)((unsigned)(begin + cur.nt - 1) / (unsigned)per) - u0 + 1;
                 const auto piece_at = [&](int u) { return p.part + (int64_t)((u0 + u) * 2 + (u == 0 ? 1 : 0)) * S::PIECE; };
                 float* piece = piece_at(blockIdx.x - u0);
                 if (key < HD) {
@@ -552,7 +552,7 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
                     for (int k = warp; k < cols; k += SOFT / 32) {
                         float m, l;
                         const float4 a = join_pieces<HD>(piece_at, n_pieces, k * HD, NC * HD + 2 * k, m, l);
-                        if (lane < HD / 4) store4(out_at(k) + lane * 4, a, 1.f / l, pos0 + k / p.G >= 0);
+                        if (lane < HD / 4) store4(out_at(k) + lane * 4, a, 1.f / l, pos0 + div_g(p, k) >= 0);
                         if (p.scores && lane == 0) p.stats[stat0 + k] = make_float2(m, 1.f / l);
                     }
                 }
@@ -677,6 +677,7 @@ cudaError_t launch_kv8_attention(const Kv8& c, const Kv8Seqs& q, const Kv8Rows& 
     p.Hq = c.cfg.n_heads;
     p.Hkv = Hkv;
     p.G = p.Hq / Hkv;
+    p.inv_g = (65536 + p.G - 1) / p.G;
     p.kz = 2 * layer;
     p.box = c.cfg.page_size < TK ? c.cfg.page_size : TK;
     p.min_tiles = 2;

@@ -188,45 +188,39 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_rows_kernel(const __grid_const
             if (begins) {
                 ++item;
                 const bf16* qbase = (const bf16*)p.a.q + (int64_t)(q.r0 + q0) * p.a.q_stride + (int64_t)cur.g * p.G * HD;
-                constexpr int QL = HD / 8, QR = 32 / QL, QB = ROWS / (4 * QR) / 2;  // lanes of a row (8 values each), rows of a warp, batch
+                constexpr int QL = HD / 8, QR = 32 / QL;         // lanes of a row (8 values each), rows of a warp
+                const auto q_of = [&](int r) {
+                    return r < cols ? *reinterpret_cast<const uint4*>(qbase + (int64_t)div_g(p, r) * p.a.q_stride + mod_g(p, r) * HD + lane % QL * 8)
+                                    : make_uint4(0, 0, 0, 0);
+                };
+                uint4 val = q_of(w * QR + lane / QL), next = q_of((4 + w) * QR + lane / QL);
+                // once the products with the item before's Q are done; then the softmax is past tile i - 3, hence past the item whose
+                // marks and row scales these were
+                if (i > 0) ptx::mbar_wait(ptx::smem_u32(&c.k_empty[(i - 1) & 1]), ((i - 1) >> 1) & 1, abort, status);
+                if (t < HD) nan_marks[(item % MARKS) * HD + t] = INT_MAX;
+                if (t == 0) c.any_nan[item % MARKS] = 0;
 #pragma unroll 1
-                for (int h = 0; h < 2; ++h) {
-                    uint4 val[QB];
+                for (int r = w * QR + lane / QL; r < ROWS; r += 4 * QR) {
+                    const uint32_t word[4] = {val.x, val.y, val.z, val.w};
+                    val = next;
+                    next = q_of(r + 8 * QR);                     // two steps ahead
+                    float f[8], top = 0.f;
 #pragma unroll
-                    for (int n = 0; n < QB; ++n) {
-                        const int r = ((h * QB + n) * 4 + w) * QR + lane / QL;
-                        val[n] = r < cols ? *reinterpret_cast<const uint4*>(qbase + (int64_t)(r / p.G) * p.a.q_stride + (r % p.G) * HD +
-                                                                            lane % QL * 8)
-                                          : make_uint4(0, 0, 0, 0);
-                    }
-                    if (h == 0) {
-                        // once the products with the item before's Q are done; then the softmax is past tile i - 3, hence past the
-                        // item whose marks and row scales these were
-                        if (i > 0) ptx::mbar_wait(ptx::smem_u32(&c.k_empty[(i - 1) & 1]), ((i - 1) >> 1) & 1, abort, status);
-                        if (t < HD) nan_marks[(item % MARKS) * HD + t] = INT_MAX;
-                        if (t == 0) c.any_nan[item % MARKS] = 0;
+                    for (int k = 0; k < 4; ++k) {
+                        f[2 * k] = __uint_as_float(word[k] << 16);
+                        f[2 * k + 1] = __uint_as_float(word[k] & 0xffff0000u);
+                        top = fmaxf(top, fmaxf(kv8_mag(f[2 * k]), kv8_mag(f[2 * k + 1])));
                     }
 #pragma unroll
-                    for (int n = 0; n < QB; ++n) {
-                        const int r = ((h * QB + n) * 4 + w) * QR + lane / QL;
-                        const uint32_t word[4] = {val[n].x, val[n].y, val[n].z, val[n].w};
-                        float f[8], top = 0.f;
+                    for (int o = QL / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                    // kv8_scale brings the largest value to 224 .. 448; 2^6 more is 2^14 .. 2^15 less a little (the softmax's
+                    // scale gives its sign, and nothing when it is 0)
+                    const float sc = kv8_scale(top), up = kv8_inverse(sc) * (p.a.scale < 0.f ? -64.f : p.a.scale > 0.f ? 64.f : 0.f);
+                    uint32_t o[4];
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            f[2 * k] = __uint_as_float(word[k] << 16);
-                            f[2 * k + 1] = __uint_as_float(word[k] & 0xffff0000u);
-                            top = fmaxf(top, fmaxf(kv8_mag(f[2 * k]), kv8_mag(f[2 * k + 1])));
-                        }
-#pragma unroll
-                        for (int o = QL / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-                        // kv8_scale brings the largest value to 224 .. 448; 2^6 more is 2^14 .. 2^15 less a little
-                        const float sc = kv8_scale(top), up = kv8_inverse(sc) * 64.f;
-                        uint32_t o[4];
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) o[k] = f16_pair(f[2 * k] * up, f[2 * k + 1] * up);
-                        *reinterpret_cast<uint4*>(sQ + wide_at(r, lane % QL)) = make_uint4(o[0], o[1], o[2], o[3]);
-                        if (lane % QL == 0) row_scale[(item % MARKS) * ROWS + r] = sc * (1.f / 64.f);
-                    }
+                    for (int k = 0; k < 4; ++k) o[k] = f16_pair(f[2 * k] * up, f[2 * k + 1] * up);
+                    *reinterpret_cast<uint4*>(sQ + wide_at(r, lane % QL)) = make_uint4(o[0], o[1], o[2], o[3]);
+                    if (lane % QL == 0) row_scale[(item % MARKS) * ROWS + r] = sc * (1.f / 64.f);
                 }
                 fence_async_smem();
                 ptx::named_bar_sync(2, CONV);                    // also: the marks
@@ -364,7 +358,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_rows_kernel(const __grid_const
         // ------------------------------------------------------------------------------------ softmax, output
         const int quarter = warp & 3, hf = warp >> 2, row = quarter * 32 + lane;
         const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
-        const float to_exp2 = p.a.scale * 1.4426950408889634f;
+        const float to_exp2 = fabsf(p.a.scale) * 1.4426950408889634f;
         const int box_shift = min(p.q.shift, 7);
         Todo todo{0, 0, 0, 0, 0};
         int item = 0;
@@ -372,7 +366,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_rows_kernel(const __grid_const
             const int first = cur.t, n_here = min(cur.nt - first, count - i), g = cur.g;
             const Seq q = cur.q;
             const int q0 = cur.qt * p.QT, cols = min(p.QT, q.n - q0) * p.G;
-            const int pos0 = q.len - q.n + q0, pos = pos0 + row / p.G;       // positions of the item's first row and of this one
+            const int pos0 = q.len - q.n + q0, pos = pos0 + div_g(p, row);       // positions of the item's first row and of this one
             const int64_t stat0 = ((int64_t)g * p.r.n_rows + q.r0 + q0) * p.G;
             float ref = -INFINITY, l = 0.f, row_mul = 0.f;       // R, the sum of 2^(x - R)
             for (int t = first; t < first + n_here; ++t, ++i) {
@@ -385,50 +379,53 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_rows_kernel(const __grid_const
                 ptx::mbar_wait(ptx::smem_u32(&c.s_full[b]), (i >> 1) & 1, abort, status);
                 ptx::tc_fence_after();
                 const uint32_t s_at = lanes + b * 128 + hf * HK;
-                // Scores of 32 keys in the exp2 domain: S times the scale of K's block (16 keys at least) with the row's and the
-                // softmax's constants; -inf for a block that is not loaded and for keys the row does not see.  Computed twice, for the
-                // maximum and for P: the loops stay short, and so do the instructions to fetch (unrolled over the 64 keys in
-                // registers, most cycles went to waiting for instructions).
                 const float* scales = c.ring.scale[i % RING][0];
-                const auto scores = [&](int k, float* x) {
-                    uint32_t w[32];
-                    ptx::tmem_ld16_issue(s_at + k, w);
-                    ptx::tmem_ld16_issue(s_at + k + 16, w + 16);
-                    const float* ks = scales + ((hf * HK + k) >> box_shift);
-                    const int second = box_shift == 4 ? 1 : 0;   // the other 16 keys' block
-                    const float m0 = ks[0] * row_mul, m1 = ks[second] * row_mul;
-                    ptx::tmem_ld_wait16(w);
-                    ptx::tmem_ld_wait16(w + 16);
+                // Blocks of 16 keys: what makes S scores in the exp2 domain (the scale of K's block with the row's and the
+                // softmax's constants), V's scale and its logarithm.  Where the first is 0 S is too, and 1 serves: a key that is
+                // not seen has S = -inf, which stays that way.
+                float mul[HK / 16], vs[HK / 16], vl[HK / 16];
+                bool hole = false;
 #pragma unroll
-                    for (int y = 0; y < 32; ++y) x[y] = __uint_as_float(w[y]) * (y < 16 ? m0 : m1);
-                    if (ks[0] < 0.f || ks[second] < 0.f || j0 + k + 31 > pos0) {
-                        const int seen = pos - (j0 + k) + 1, low = ks[0] < 0.f ? 0 : seen, high = ks[second] < 0.f ? 0 : seen;
-#pragma unroll
-                        for (int y = 0; y < 32; ++y)
-                            if (y >= (y < 16 ? low : high)) x[y] = -INFINITY;
-                    }
-                };
-                const auto v_log = [](float v) {                 // log2 of V's scale, a power of two
-                    return v > 0.f ? fmaxf((float)((int)(__float_as_uint(v) >> 23) - 127), -100.f) : -100.f;
-                };
-                float top = -INFINITY;                           // the largest of score + log2 of V's scale
+                for (int k = 0; k < HK / 16; ++k) {
+                    const int box = (hf * HK + k * 16) >> box_shift;
+                    const float ks = scales[box], v = scales[8 + box];
+                    hole |= ks < 0.f;
+                    mul[k] = ks > 0.f && row_mul > 0.f ? fmaxf(ks * row_mul, 1.1754944e-38f) : 1.f;
+                    vs[k] = v * P_UP;
+                    vl[k] = v > 0.f ? fmaxf((float)((int)(__float_as_uint(v) >> 23) - 127), -100.f) : -100.f;
+                }
+                // Away from the tile loop's usual path, which has to stay short (with everything unrolled in place, most cycles
+                // went to waiting for instructions): -inf into S for keys that are not loaded or not seen, scores kept
+                if (hole || j0 + HK - 1 > pos0 || p.scores) {
 #pragma unroll 1
-                for (int k = 0; k < HK; k += 32) {
-                    float x[32];
-                    scores(k, x);
-                    float m[2] = {x[0], x[16]};
+                    for (int k = 0; k < HK; k += 16) {
+                        float w[16];
+                        ptx::tmem_ld16(s_at + k, w);
+                        const float ks = scales[(hf * HK + k) >> box_shift];
+                        const int seen = ks < 0.f ? 0 : pos - (j0 + k) + 1;
+                        const float m = ks > 0.f && row_mul > 0.f ? fmaxf(ks * row_mul, 1.1754944e-38f) : 1.f;
 #pragma unroll
-                    for (int y = 1; y < 16; ++y) {
-                        m[0] = fmaxf(m[0], x[y]);
-                        m[1] = fmaxf(m[1], x[16 + y]);
-                    }
-                    const float* v = scales + 8 + ((hf * HK + k) >> box_shift);
-                    top = fmaxf(top, fmaxf(m[0] + v_log(v[0]), m[1] + v_log(v[box_shift == 4 ? 1 : 0])));
-                    if (p.scores && row < cols) {
-                        float4* score = reinterpret_cast<float4*>(p.scores + (stat0 + row) * p.score_ld + j0 + k);
+                        for (int y = 0; y < 16; ++y) w[y] = y < seen ? w[y] : -INFINITY;
+                        ptx::tmem_st16(s_at + k, w);
+                        if (p.scores && row < cols) {
+                            float4* score = reinterpret_cast<float4*>(p.scores + (stat0 + row) * p.score_ld + j0 + k);
 #pragma unroll
-                        for (int y = 0; y < 8; ++y) score[y] = make_float4(x[4 * y], x[4 * y + 1], x[4 * y + 2], x[4 * y + 3]);
+                            for (int y = 0; y < 4; ++y) score[y] = make_float4(w[4 * y] * m, w[4 * y + 1] * m, w[4 * y + 2] * m, w[4 * y + 3] * m);
+                        }
                     }
+                    ptx::tmem_wait_st();
+                }
+                uint32_t x[HK];
+#pragma unroll
+                for (int k = 0; k < HK; k += 16) ptx::tmem_ld16_issue(s_at + k, x + k);
+                float top = -INFINITY;                           // the largest of score + log2 of V's scale
+#pragma unroll
+                for (int k = 0; k < HK; k += 16) {
+                    ptx::tmem_ld_wait16(x + k);
+                    float m = __uint_as_float(x[k]);
+#pragma unroll
+                    for (int y = 1; y < 16; ++y) m = fmaxf(m, __uint_as_float(x[k + y]));
+                    top = fmaxf(top, fmaf(m, mul[k / 16], vl[k / 16]));
                 }
                 if (__any_sync(0xffffffffu, ref != -INFINITY && top > ref + GROW)) {
                     // O_h holds the tiles before: the whole warp rescales, each row by its own factor
@@ -452,18 +449,16 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_rows_kernel(const __grid_const
                 if (ref == -INFINITY) ref = top;                 // nothing summed yet
                 const float neg = ref == -INFINITY ? 0.f : -ref;
                 float sum = 0.f;
-#pragma unroll 1
-                for (int k = 0; k < HK; k += 32) {               // P over S columns that have been read
-                    float x[32];
-                    scores(k, x);
-                    const float* v = scales + 8 + ((hf * HK + k) >> box_shift);
-                    const float v0 = v[0] * P_UP, v1 = v[box_shift == 4 ? 1 : 0] * P_UP;
+#pragma unroll
+                for (int k = 0; k < HK; k += 32) {               // P over the S columns that have been read
                     uint32_t w[16];
 #pragma unroll
                     for (int y = 0; y < 32; y += 2) {
-                        const float e0 = exp2_fast(x[y] + neg), e1 = exp2_fast(x[y + 1] + neg);
+                        const float m = mul[(k + y) / 16], v = vs[(k + y) / 16];
+                        const float e0 = exp2_fast(fmaf(__uint_as_float(x[k + y]), m, neg));
+                        const float e1 = exp2_fast(fmaf(__uint_as_float(x[k + y + 1]), m, neg));
                         sum += e0 + e1;
-                        w[y / 2] = f16_pair(e0 * (y < 16 ? v0 : v1), e1 * (y < 16 ? v0 : v1));
+                        w[y / 2] = f16_pair(e0 * v, e1 * v);
                     }
                     tmem_st16_words(s_at + k / 2, w);
                 }
@@ -484,11 +479,11 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_rows_kernel(const __grid_const
             const float f0 = hf == 0 ? f_own : f_other, f1 = hf == 0 ? f_other : f_own;
             const float L = hf == 0 ? l * f_own + other.y * f_other : other.y * f_other + l * f_own;
             const bool whole = first == 0 && n_here == cur.nt;
-            const long long begin = mine.t0 + (i - n_here) - first;          // the item's first tile in the list
-            const int u0 = (int)(begin / mine.per), n_pieces = (int)((begin + cur.nt - 1) / mine.per) - u0 + 1;
+            const int begin = mine.t0 + (i - n_here) - first;          // the item's first tile in the list
+            const int u0 = (unsigned)begin / (unsigned)mine.per, n_pieces = (int)((unsigned)(begin + cur.nt - 1) / (unsigned)mine.per) - u0 + 1;
             const auto piece_at = [&](int u) { return p.part + (int64_t)((u0 + u) * 2 + (u == 0 ? 1 : 0)) * S::PIECE; };
             const auto out_at = [&](int r) {
-                return (bf16*)p.a.out + (int64_t)(q.r0 + q0 + r / p.G) * p.a.out_stride + (int64_t)(g * p.G + r % p.G) * HD;
+                return (bf16*)p.a.out + (int64_t)(q.r0 + q0 + div_g(p, r)) * p.a.out_stride + (int64_t)(g * p.G + mod_g(p, r)) * HD;
             };
             const bool marked = c.any_nan[item % MARKS] != 0;
             const int* marks = nan_marks + (item % MARKS) * HD;
@@ -562,8 +557,8 @@ __global__ void __launch_bounds__(256) kv8_join_kernel(const AttnArgs p) {
     for (int k = blockIdx.y * 8 + (threadIdx.x >> 5); k < d.cols; k += gridDim.y * 8) {
         float m, l;
         const float4 a = join_pieces<HD>(piece_at, d.pieces, k * HD, ROWS * HD + 2 * k, m, l);
-        bf16* out = (bf16*)p.a.out + (int64_t)(d.row0 + k / p.G) * p.a.out_stride + (int64_t)(d.g * p.G + k % p.G) * HD;
-        if (lane < HD / 4) store4(out + lane * 4, a, 1.f / l, d.pos0 + k / p.G >= 0);
+        bf16* out = (bf16*)p.a.out + (int64_t)(d.row0 + div_g(p, k)) * p.a.out_stride + (int64_t)(d.g * p.G + mod_g(p, k)) * HD;
+        if (lane < HD / 4) store4(out + lane * 4, a, 1.f / l, d.pos0 + div_g(p, k) >= 0);
         if (p.scores && lane == 0) p.stats[((int64_t)d.g * p.r.n_rows + d.row0) * p.G + k] = make_float2(m, 1.f / l);
     }
 }
