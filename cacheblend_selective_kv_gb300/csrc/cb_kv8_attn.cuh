@@ -30,8 +30,8 @@ struct AttnArgs {
     float* part;                         // [cta][2][NC][HD + 2] pieces of items that span CTAs
     unsigned* arrived;                   // [cta] pieces finished of the item that begins in this CTA (0 between calls)
     int* todo;                           // many rows: [cta] what the joining kernel has to do (5 ints)
-    float* scores;                       // weights: [Hkv][n_q][G][score_ld] scores in the exp2 domain
-    int score_ld;
+    float* scores;                       // weights: scores in the exp2 domain (score_of), score_ld per column
+    int score_ld;                        // max_len rounded up to TK
     float2* stats;                       // weights: [Hkv][n_q][G] (max, 1 / sum)
 };
 
@@ -66,6 +66,12 @@ __device__ __forceinline__ int seq_tiles(const AttnArgs& p, const Seq& q) {
 #pragma unroll 1
     for (int qt = 0; qt < q.q_tiles(p.QT); ++qt) t += q.tiles(qt, p.QT);
     return t * p.Hkv;
+}
+
+// Scores of a column (query row of the sequence x head of the group) with the keys of tile t: a tile's columns lie together,
+// so that what sums over them reads one contiguous piece.
+__device__ __forceinline__ float* score_of(const AttnArgs& p, const Seq& q, int g, int t, int col) {
+    return p.scores + ((int64_t)g * p.r.n_rows + q.r0) * p.G * p.score_ld + ((int64_t)t * q.n * p.G + col) * TK;
 }
 
 // A position in the list: item (s, qt, g) and tile t of its nt.

@@ -407,11 +407,11 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
                         if (k < hidden) x[k] = -INFINITY;
                 }
                 if (p.scores) {
-                    float* score = p.scores + (stat0 + c0) * p.score_ld + j;
+                    float* score = score_of(p, q, g, t, q0 * p.G + c0) + key;
 #pragma unroll
                     for (int k = 0; k < NW; ++k)
                         if (c0 + k < cols)
-                            score[(int64_t)k * p.score_ld] = x[k];
+                            score[k * TK] = x[k];
                 }
                 // maxima over the tile's keys of the scores, and of scores with V's scale: y = x + log2(scale), which says
                 // how far a column's P can be scaled up.  A warp's keys lie in one block unless pages have 16 rows.
@@ -568,33 +568,32 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
     }
 }
 
-// weights[s][g][j] = sum over the sequence's rows and the group's heads of exp2(score - max) / sum; with many
-// columns four sums of every fourth one, joined in order
-__global__ void __launch_bounds__(512) kv8_weights_kernel(const AttnArgs p) {
-    __shared__ float part[4][128];
+// weights[s][g][j] = sum over the sequence's rows and the group's heads of exp2(score - max) / sum; with many columns
+// blockDim.y sums of every so-manieth one, joined in order
+__global__ void __launch_bounds__(1024) kv8_weights_kernel(const AttnArgs p) {
+    __shared__ float part[8][TK];
     grid_dep_launch();
     grid_dep_wait();
-    const int j = blockIdx.x * 128 + threadIdx.x, y = threadIdx.y, g = blockIdx.y;
+    const int key = threadIdx.x, j = blockIdx.x * TK + key, y = threadIdx.y, by = blockDim.y, g = blockIdx.y;
     const Seq q = seq_at(p, blockIdx.z);
-    if (blockIdx.x * 128 >= q.len) return;
+    if (blockIdx.x * TK >= q.len) return;
     float w = 0.f;
     if (j < q.len) {
-        const int64_t at = ((int64_t)g * p.r.n_rows + q.r0) * p.G;
-        const float* score = p.scores + at * p.score_ld + j;
-        const float2* st = p.stats + at;
+        const float* score = score_of(p, q, g, blockIdx.x, 0) + key;
+        const float2* st = p.stats + ((int64_t)g * p.r.n_rows + q.r0) * p.G;
         const int seen = max(0, j - (q.len - q.n)) * p.G, cols = q.n * p.G;      // columns that see key j: [seen, cols)
-        const int by = blockDim.y;
-#pragma unroll 16
+#pragma unroll 8
         for (int k = seen + y; k < cols; k += by) {
-            const float x = __ldcs(score + (int64_t)k * p.score_ld);
+            const float x = __ldcs(score + (int64_t)k * TK);
             const float2 m = st[k];
             w += x == -INFINITY ? 0.f : exp2_fast(x - m.x) * m.y;
         }
     }
-    if (blockDim.y > 1) {
-        part[y][threadIdx.x] = w;
+    if (by > 1) {
+        part[y][key] = w;
         __syncthreads();
-        w = (part[0][threadIdx.x] + part[1][threadIdx.x]) + (part[2][threadIdx.x] + part[3][threadIdx.x]);
+        if (y == 0)
+            for (int k = 1; k < by; ++k) w += part[k][key];
     }
     if (y == 0 && j < q.len) {
         float* dst = p.a.weights + ((int64_t)blockIdx.z * p.Hkv + g) * p.a.weights_ld + j;
@@ -694,8 +693,8 @@ cudaError_t launch_kv8_attention(const Kv8& c, const Kv8Seqs& q, const Kv8Rows& 
         if (e != cudaSuccess) return e;
     }
     if (a.weights && q.max_len > 0) {
-        const int split = r.n_rows > 4 * q.n ? 4 : 1;            // rows of a sequence, on average
-        return launch_ex(c.pdl, kv8_weights_kernel, dim3((q.max_len + 127) / 128, Hkv, q.n), dim3(128, split), 0, s, p);
+        const int split = r.n_rows > 4 * q.n ? 8 : 1;            // rows of a sequence, on average
+        return launch_ex(c.pdl, kv8_weights_kernel, dim3((q.max_len + TK - 1) / TK, Hkv, q.n), dim3(TK, split), 0, s, p);
     }
     return cudaSuccess;
 }

@@ -408,7 +408,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_rows_kernel(const __grid_const
                         for (int y = 0; y < 16; ++y) w[y] = y < seen ? w[y] : -INFINITY;
                         ptx::tmem_st16(s_at + k, w);
                         if (p.scores && row < cols) {
-                            float4* score = reinterpret_cast<float4*>(p.scores + (stat0 + row) * p.score_ld + j0 + k);
+                            float4* score = reinterpret_cast<float4*>(score_of(p, q, g, t, q0 * p.G + row) + hf * HK + k);
 #pragma unroll
                             for (int y = 0; y < 4; ++y) score[y] = make_float4(w[4 * y] * m, w[4 * y + 1] * m, w[4 * y + 2] * m, w[4 * y + 3] * m);
                         }
