@@ -688,8 +688,8 @@ cudaError_t launch_kv8_attention(const Kv8& c, const Kv8Seqs& q, const Kv8Rows& 
     if (r.n_rows > 0) {
         const int rows = (r.n_rows + q.n - 1) / q.n;             // of a sequence, on average
         const bool many = c.cfg.dtype == CB_BF16 && rows * p.G > 32;
-        const cudaError_t e = many ? launch_kv8_rows(c, &p, s)
-                                   : c.cfg.head_dim == 128 ? launch_dim<128>(c, p, s) : launch_dim<64>(c, p, s);
+        if (many) return launch_kv8_rows(c, &p, s);              // sums its weights too
+        const cudaError_t e = c.cfg.head_dim == 128 ? launch_dim<128>(c, p, s) : launch_dim<64>(c, p, s);
         if (e != cudaSuccess) return e;
     }
     if (a.weights && q.max_len > 0) {

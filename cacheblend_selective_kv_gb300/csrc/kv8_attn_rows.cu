@@ -97,6 +97,12 @@ __device__ __forceinline__ uint32_t f16_pair(float a, float b) {
 }
 __device__ __forceinline__ uint32_t half2_word(const __half2& h) { return *reinterpret_cast<const uint32_t*>(&h); }
 
+// Scores of a tile of keys: [TK / 4][columns], four keys each.  A thread has a row's scores, so that neighbouring threads
+// write next to each other (a row's scores side by side had every store touch 32 sectors).
+__device__ __forceinline__ float4* quads_of(const AttnArgs& p, const Seq& q, int g, int t) {
+    return reinterpret_cast<float4*>(score_of(p, q, g, t, 0));
+}
+
 // NaN codes out of 16 codes of a V row that not all query rows see, and row j noted as the first to hold one in those dims
 __device__ __noinline__ void take_nan(uint4& x, int j, int* marks, int* any) {
     uint32_t cw[4] = {x.x, x.y, x.z, x.w};
@@ -111,7 +117,7 @@ __device__ __noinline__ void take_nan(uint4& x, int j, int* marks, int* any) {
     x = make_uint4(cw[0], cw[1], cw[2], cw[3]);
 }
 
-template <int HD>
+template <int HD, bool SCORES>
 __global__ void __launch_bounds__(THREADS, 1) kv8_rows_kernel(const __grid_constant__ CUtensorMap map, const AttnArgs p) {
     using S = Rows<HD>;
     extern __shared__ __align__(1024) uint8_t sm[];
@@ -395,23 +401,16 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_rows_kernel(const __grid_const
                     vl[k] = v > 0.f ? fmaxf((float)((int)(__float_as_uint(v) >> 23) - 127), -100.f) : -100.f;
                 }
                 // Away from the tile loop's usual path, which has to stay short (with everything unrolled in place, most cycles
-                // went to waiting for instructions): -inf into S for keys that are not loaded or not seen, scores kept
-                if (hole || j0 + HK - 1 > pos0 || p.scores) {
+                // went to waiting for instructions): -inf into S for keys that are not loaded or not seen
+                if (hole || j0 + HK - 1 > pos0) {
 #pragma unroll 1
                     for (int k = 0; k < HK; k += 16) {
                         float w[16];
                         ptx::tmem_ld16(s_at + k, w);
-                        const float ks = scales[(hf * HK + k) >> box_shift];
-                        const int seen = ks < 0.f ? 0 : pos - (j0 + k) + 1;
-                        const float m = ks > 0.f && row_mul > 0.f ? fmaxf(ks * row_mul, 1.1754944e-38f) : 1.f;
+                        const int seen = scales[(hf * HK + k) >> box_shift] < 0.f ? 0 : pos - (j0 + k) + 1;
 #pragma unroll
                         for (int y = 0; y < 16; ++y) w[y] = y < seen ? w[y] : -INFINITY;
                         ptx::tmem_st16(s_at + k, w);
-                        if (p.scores && row < cols) {
-                            float4* score = reinterpret_cast<float4*>(score_of(p, q, g, t, q0 * p.G + row) + hf * HK + k);
-#pragma unroll
-                            for (int y = 0; y < 4; ++y) score[y] = make_float4(w[4 * y] * m, w[4 * y + 1] * m, w[4 * y + 2] * m, w[4 * y + 3] * m);
-                        }
                     }
                     ptx::tmem_wait_st();
                 }
@@ -426,6 +425,14 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_rows_kernel(const __grid_const
 #pragma unroll
                     for (int y = 1; y < 16; ++y) m = fmaxf(m, __uint_as_float(x[k + y]));
                     top = fmaxf(top, fmaf(m, mul[k / 16], vl[k / 16]));
+                }
+                if (SCORES && row < cols) {
+                    float4* score = quads_of(p, q, g, t) + (int64_t)(hf * (HK / 4)) * (q.n * p.G) + q0 * p.G + row;
+#pragma unroll
+                    for (int k = 0; k < HK; k += 4, score += q.n * p.G) {
+                        const float m = mul[k / 16];
+                        *score = make_float4(__uint_as_float(x[k]) * m, __uint_as_float(x[k + 1]) * m, __uint_as_float(x[k + 2]) * m, __uint_as_float(x[k + 3]) * m);
+                    }
                 }
                 if (__any_sync(0xffffffffu, ref != -INFINITY && top > ref + GROW)) {
                     // O_h holds the tiles before: the whole warp rescales, each row by its own factor
@@ -522,7 +529,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_rows_kernel(const __grid_const
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&c.o_free));
             if (whole) {
-                if (p.scores && hf == 0 && row < cols) p.stats[stat0 + row] = make_float2(M, inv);
+                if (SCORES && hf == 0 && row < cols) p.stats[stat0 + row] = make_float2(M, inv);
                 ptx::named_bar_sync(3 + quarter, 64);            // `halves` has been read
             } else {
                 if (hf == 0 && row < cols)
@@ -563,9 +570,41 @@ __global__ void __launch_bounds__(256) kv8_join_kernel(const AttnArgs p) {
     }
 }
 
-template <int HD> cudaError_t launch_dim(const Kv8& c, AttnArgs& p, cudaStream_t s) {
+// weights[s][g][j] = sum over the sequence's rows and the group's heads of exp2(score - max) / sum: four keys per warp, the
+// columns over its lanes
+__global__ void __launch_bounds__(256) kv8_rows_weights_kernel(const AttnArgs p) {
+    grid_dep_launch();
+    grid_dep_wait();
+    const int at = blockIdx.x * 8 + (threadIdx.x >> 5), quad = at % (TK / 4), lane = threadIdx.x & 31, j = at * 4, g = blockIdx.y;
+    const Seq q = seq_at(p, blockIdx.z);
+    if (j >= q.len) return;
+    const int seen = max(0, j - (q.len - q.n)) * p.G, cols = q.n * p.G;      // columns that see key j: [seen, cols)
+    const float4* score = quads_of(p, q, g, at / (TK / 4)) + (int64_t)quad * cols;
+    const float2* st = p.stats + ((int64_t)g * p.r.n_rows + q.r0) * p.G;
+    float w[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
+    for (int k = seen + lane; k < cols; k += 32) {
+        const float4 x = __ldcs(score + k);
+        const float2 m = st[k];
+        w[0] += x.x == -INFINITY ? 0.f : exp2_fast(x.x - m.x) * m.y;
+        w[1] += x.y == -INFINITY ? 0.f : exp2_fast(x.y - m.x) * m.y;
+        w[2] += x.z == -INFINITY ? 0.f : exp2_fast(x.z - m.x) * m.y;
+        w[3] += x.w == -INFINITY ? 0.f : exp2_fast(x.w - m.x) * m.y;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+        for (int y = 0; y < 4; ++y) w[y] += __shfl_xor_sync(0xffffffffu, w[y], o);
+    const float mine = lane == 0 ? w[0] : lane == 1 ? w[1] : lane == 2 ? w[2] : w[3];
+    if (lane < 4 && j + lane < q.len) {
+        float* dst = p.a.weights + ((int64_t)blockIdx.z * p.Hkv + g) * p.a.weights_ld + j + lane;
+        *dst = p.a.add ? *dst + mine : mine;
+    }
+}
+
+template <int HD, bool SCORES> cudaError_t launch_dim(const Kv8& c, AttnArgs& p, cudaStream_t s) {
     static std::atomic<uint64_t> done{0};
-    const cudaError_t e = smem_limit_once(kv8_rows_kernel<HD>, Rows<HD>::BYTES, done);
+    const cudaError_t e = smem_limit_once(kv8_rows_kernel<HD, SCORES>, Rows<HD>::BYTES, done);
     if (e != cudaSuccess) return e;
     p.QT = ROWS / p.G;
     const int64_t items = ((int64_t)p.r.n_rows / p.QT + p.q.n) * p.Hkv;
@@ -573,9 +612,11 @@ template <int HD> cudaError_t launch_dim(const Kv8& c, AttnArgs& p, cudaStream_t
     CUtensorMap map;
     memcpy(&map, c.map, sizeof map);
     const unsigned ctas = (unsigned)(tiles < c.num_sms ? tiles : c.num_sms);
-    const cudaError_t err = launch_ex(c.pdl, kv8_rows_kernel<HD>, dim3(ctas), dim3(THREADS), Rows<HD>::BYTES, s, map, p);
-    if (err != cudaSuccess) return err;
-    return launch_ex(c.pdl, kv8_join_kernel<HD>, dim3(ctas, 8), dim3(256), 0, s, p);
+    cudaError_t err = launch_ex(c.pdl, kv8_rows_kernel<HD, SCORES>, dim3(ctas), dim3(THREADS), Rows<HD>::BYTES, s, map, p);
+    if (err == cudaSuccess) err = launch_ex(c.pdl, kv8_join_kernel<HD>, dim3(ctas, 8), dim3(256), 0, s, p);
+    if (err == cudaSuccess && SCORES)
+        err = launch_ex(c.pdl, kv8_rows_weights_kernel, dim3((p.q.max_len + 31) / 32, p.Hkv, p.q.n), dim3(256), 0, s, p);
+    return err;
 }
 
 }  // namespace
@@ -585,7 +626,8 @@ size_t kv8_rows_part_floats(int num_sms) { return (size_t)num_sms * 2 * Rows<128
 cudaError_t launch_kv8_rows(const Kv8& c, const void* attn_args, cudaStream_t s) {
     AttnArgs p = *static_cast<const AttnArgs*>(attn_args);
     p.todo = c.todo;
-    return c.cfg.head_dim == 128 ? launch_dim<128>(c, p, s) : launch_dim<64>(c, p, s);
+    if (p.scores) return c.cfg.head_dim == 128 ? launch_dim<128, true>(c, p, s) : launch_dim<64, true>(c, p, s);
+    return c.cfg.head_dim == 128 ? launch_dim<128, false>(c, p, s) : launch_dim<64, false>(c, p, s);
 }
 
 }  // namespace cb
