@@ -4,8 +4,8 @@
 // The kept rows, in order, become rows 0 .. of the destination pages, quantised anew as a write of their values
 // would be, and their weights move along.
 //
-//   select   one CTA per (layer, sequence, KV head): the weights' bits order as unsigned integers, so four rounds of a
-//            256-bin histogram fix the threshold (and, when more rows equal it than are wanted, rounds over the row
+//   select   one CTA per (layer, sequence, KV head): the weights' bits order as unsigned integers, so three rounds of
+//            histograms of 11 and 10 bits fix the threshold (and, when more rows equal it than are wanted, rounds over the row
 //            numbers of those fix the last one taken); a warp then counts and writes the kept rows of its own stretch.
 //   move     one CTA per (layer, K|V, KV head, sequence) and destination page; a page's rows are in registers before it is
 //            written.  Destination row r comes from a row >= r, so with equal tables (in place) one CTA does a head's
@@ -21,7 +21,8 @@ namespace cb {
 namespace {
 
 constexpr int ST = 512;       // select threads
-constexpr int VPT = 20;       // weights a select thread keeps in registers (two CTAs per SM)
+constexpr int BINS = 2048;    // of select's histogram: digits of 11, 10 and 10 bits
+constexpr int CACHE = 32 * ST;  // weights that a select CTA keeps in shared memory (two CTAs per SM)
 constexpr int NP = 4;         // 16-byte vectors of codes per move thread
 constexpr int MT = 512;       // move threads, at most: a page of 256 rows of 128 codes
 
@@ -35,30 +36,39 @@ struct EvictArgs {
 
 __device__ __forceinline__ unsigned rank_bits(float w) { return w > 0.f ? __float_as_uint(w) : 0u; }
 
-// In a 256-bin histogram, the bin in which a running count from the top (or the bottom) reaches `want`, and how many of
-// that bin are wanted.  Called by warp 0.
-template <bool TOP> __device__ __forceinline__ void find_bin(const int* hist, int want, unsigned* pick) {
-    const int lane = threadIdx.x & 31;
-    int h[8], sum = 0;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {                      // lane 0 holds the first bins in counting order
-        const int i = lane * 8 + k;
-        h[k] = hist[TOP ? 255 - i : i];
-        sum += h[k];
-    }
+struct Pick {
+    int bin, want, count;     // the bin chosen, how many of its rows are wanted, how many it has
+};
+
+// In the histogram, the bin in which a running count from the top (or the bottom) reaches `want`.  Called by all threads,
+// each with BINS / ST bins that follow each other in counting order; leaves the histogram zero.
+template <bool TOP> __device__ __forceinline__ Pick find_bin(int* hist, int* totals, Pick* found, int want) {
+    constexpr int PER = BINS / ST;
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+    int4& mine = reinterpret_cast<int4*>(hist)[TOP ? ST - 1 - t : t];
+    static_assert(PER == 4, "one vector per thread");
+    const int4 x = mine;
+    mine = make_int4(0, 0, 0, 0);
+    const int h[4] = {TOP ? x.w : x.x, TOP ? x.z : x.y, TOP ? x.y : x.z, TOP ? x.x : x.w};
+    const int sum = h[0] + h[1] + h[2] + h[3];
     int before = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const int y = __shfl_up_sync(0xffffffffu, before, o);
         if (lane >= o) before += y;
     }
+    if (lane == 31) totals[warp] = before;
     before -= sum;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < ST / 32; ++k) before += k < warp ? totals[k] : 0;
     if (before < want && want <= before + sum) {
         int k = 0;
         while (before + h[k] < want) before += h[k++];
-        pick[0] = (unsigned)(TOP ? 255 - (lane * 8 + k) : lane * 8 + k);
-        pick[1] = (unsigned)(want - before);
+        *found = Pick{TOP ? BINS - 1 - (t * PER + k) : t * PER + k, want - before, h[k]};
     }
+    __syncthreads();
+    return *found;
 }
 
 // exclusive prefix sums over N ints in shared memory, by warp 0 (N a multiple of 32)
@@ -85,59 +95,53 @@ template <int N> __device__ __forceinline__ void warp_scan(int* v) {
     }
 }
 
-// The rows of one head.  CACHED: the sequence has at most ST * VPT rows, and a thread's VPT weights stay in registers over
-// the rounds; otherwise each round reads them again (from L2).
+// The rows of one head.  CACHED: the weights are brought into shared memory first; otherwise each round reads them again
+// (from L2).  The loops stay short: with the weights in registers, hence everything unrolled, the instructions of so many
+// lines run once took longer to fetch than to execute (8K rows, 32 layers x 8 heads: OLD us against NEW).
 template <bool CACHED>
-__device__ __forceinline__ void select_rows(const EvictArgs& a, const float* w, float* ow, int* rows, int len) {
-    __shared__ int hist[256];
-    __shared__ int count[VPT * ST / 32];
-    __shared__ unsigned pick[2];                       // bin chosen, rows wanted of it
+__device__ __forceinline__ void select_rows(const EvictArgs& a, const float* w, float* cache, float* ow, int* rows, int len) {
+    __shared__ __align__(16) int hist[BINS];
+    __shared__ int totals[ST / 32];
+    __shared__ Pick found;
+    __shared__ int count[32];
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
     const int kept = min(len, a.e.keep), c0 = a.e.sink, c1 = len - a.e.recent;       // candidates [c0, c1)
     // rank bits of the candidates; NONE for every other row (above all bits of a float that is not negative)
     constexpr unsigned NONE = ~0u;
-    const auto rank_of = [&](int j) { return j >= c0 && j < c1 ? rank_bits(w[j]) : NONE; };
-    unsigned u[VPT];
+    const float* src = CACHED ? cache : w;
+    const auto rank_of = [&](int j) { return j >= c0 && j < c1 ? rank_bits(src[j]) : NONE; };
     if (CACHED) {
-#pragma unroll
-        for (int k = 0; k < VPT; ++k) u[k] = rank_of(k * ST + t);
+#pragma unroll 8
+        for (int j = t; j < len; j += ST) cache[j] = w[j];
     }
+    for (int i = t; i < BINS; i += ST) hist[i] = 0;
+    __syncthreads();
     unsigned thr = 0;                                  // candidates with rank bits above it are kept ...
     int cut = -1;                                      // ... and those equal to it up to this row
     if (len > a.e.keep) {
         int want = a.e.keep - a.e.sink - a.e.recent;   // fewer than the candidates
-        // rounds of eight bits: a row counts when its bits above `shift + 8` are `prefix`; ties by row number
+        // rounds of a digit: a row counts when its bits above the digit are `prefix`; ties by row number.  No rank and no row
+        // number has the sign bit, which keeps NONE out.
+        Pick got{0, 0, 0};
         const auto round = [&](int shift, unsigned prefix, bool by_row) {
-            for (int i = t; i < 256; i += ST) hist[i] = 0;
-            __syncthreads();
-            const unsigned mask = shift == 24 ? 0x80000000u : ~0u << (shift + 8);        // (the sign bit keeps NONE out)
+            const unsigned mask = shift == 20 ? 0x80000000u : ~0u << (shift + 10), digit = shift == 20 ? 2047u : 1023u;
             const auto add = [&](int j, unsigned b) {
                 const unsigned y = by_row ? (unsigned)j : b;
-                if ((y & mask) == prefix && (!by_row || b == thr)) atomicAdd(&hist[(y >> shift) & 255u], 1);
+                if ((y & mask) == prefix && (!by_row || b == thr)) atomicAdd(&hist[(y >> shift) & digit], 1);
             };
-            if (CACHED) {
-#pragma unroll
-                for (int k = 0; k < VPT; ++k) add(k * ST + t, u[k]);
-            } else {
 #pragma unroll 4
-                for (int j = c0 + t; j < c1; j += ST) add(j, rank_of(j));
-            }
+            for (int j = c0 + t; j < c1; j += ST) add(j, rank_of(j));
             __syncthreads();
-            if (warp == 0) {
-                if (by_row) find_bin<false>(hist, want, pick);
-                else find_bin<true>(hist, want, pick);
-            }
-            __syncthreads();
-            want = (int)pick[1];
-            return prefix | (pick[0] << shift);
+            got = by_row ? find_bin<false>(hist, totals, &found, want) : find_bin<true>(hist, totals, &found, want);
+            want = got.want;
+            return prefix | ((unsigned)got.bin << shift);
         };
         if (want > 0) {
-            for (int shift = 24; shift >= 0; shift -= 8) thr = round(shift, thr, false);
+            for (int shift = 20; shift >= 0; shift -= 10) thr = round(shift, thr, false);
             cut = INT_MAX;
-            if (hist[thr & 255u] > want) {             // more rows equal the threshold than are wanted
-                __syncthreads();
+            if (got.count > want) {                    // more rows equal the threshold than are wanted
                 unsigned last = 0;
-                for (int shift = 24; shift >= 0; shift -= 8) last = round(shift, last, true);
+                for (int shift = 20; shift >= 0; shift -= 10) last = round(shift, last, true);
                 cut = (int)last;
             }
         } else {
@@ -147,44 +151,29 @@ __device__ __forceinline__ void select_rows(const EvictArgs& a, const float* w, 
     const auto keeps = [&](int j, unsigned b) {
         return j < len && (len <= a.e.keep || b == NONE || b > thr || (b == thr && j <= cut));
     };
-    if (CACHED) {                                      // 32 rows at a time: count, scan, write
-        unsigned who[VPT];
-#pragma unroll
-        for (int k = 0; k < VPT; ++k) {
-            who[k] = __ballot_sync(0xffffffffu, keeps(k * ST + t, u[k]));
-            if (lane == 0) count[k * (ST / 32) + warp] = __popc(who[k]);
-        }
-        float v[VPT];                                  // the kept weights, all read before one is written (in place)
-#pragma unroll
-        for (int k = 0; k < VPT; ++k) v[k] = who[k] >> lane & 1 ? w[k * ST + t] : 0.f;
-        __syncthreads();
-        if (warp == 0) warp_scan<VPT * ST / 32>(count);
-        __syncthreads();
-#pragma unroll
-        for (int k = 0; k < VPT; ++k) {
-            if (!(who[k] >> lane & 1)) continue;
-            const int at = count[k * (ST / 32) + warp] + __popc(who[k] & ((1u << lane) - 1));
-            rows[at] = k * ST + t;
-            ow[at] = v[k];
-        }
-    } else {                                           // a warp's stretch of rows: count, scan, write
-        const int per = (len + ST - 1) / ST * 32, j_lo = min(len, warp * per), j_hi = min(len, j_lo + per);
-        int n = 0;
+    // a warp's stretch of rows: count, scan, write
+    const int per = (len + ST - 1) / ST * 32, j_lo = min(len, warp * per), j_hi = min(len, j_lo + per);
+    int n = 0;
 #pragma unroll 4
-        for (int j = j_lo; j < j_hi; j += 32) n += __popc(__ballot_sync(0xffffffffu, keeps(j + lane, rank_of(j + lane))));
-        if (lane == 0) count[warp] = n;
-        if (t >= ST / 32 && t < 32) count[t] = 0;
-        __syncthreads();
-        if (warp == 0) warp_scan<32>(count);
-        __syncthreads();
-        int at = count[warp];
+    for (int j = j_lo; j < j_hi; j += 32) n += __popc(__ballot_sync(0xffffffffu, keeps(j + lane, rank_of(j + lane))));
+    if (lane == 0) count[warp] = n;
+    if (t >= ST / 32 && t < 32) count[t] = 0;
+    __syncthreads();
+    if (warp == 0) warp_scan<32>(count);
+    __syncthreads();
+    int at = count[warp];
 #pragma unroll 4
-        for (int j = j_lo; j < j_hi; j += 32) {
-            const bool k = keeps(j + lane, rank_of(j + lane));
-            const unsigned who = __ballot_sync(0xffffffffu, k);
-            if (k) rows[at + __popc(who & ((1u << lane) - 1))] = j + lane;
-            at += __popc(who);
+    for (int j = j_lo; j < j_hi; j += 32) {
+        const bool k = keeps(j + lane, rank_of(j + lane));
+        const unsigned who = __ballot_sync(0xffffffffu, k);
+        if (k) {
+            const int to = at + __popc(who & ((1u << lane) - 1));
+            rows[to] = j + lane;
+            if (CACHED) ow[to] = src[j + lane];        // (in place too: all were read before one is written)
         }
+        at += __popc(who);
+    }
+    if (!CACHED) {
         __syncthreads();
         // the kept rows' weights; in place a weight moves down (rows[i] >= i), so a step reads before it writes
         constexpr int STEP = 4;
@@ -208,7 +197,8 @@ __device__ __forceinline__ void select_rows(const EvictArgs& a, const float* w, 
     for (int j = kept + t; j < len; j += ST) ow[j] = 0.f;
 }
 
-__global__ void __launch_bounds__(ST, 2) kv8_select_kernel(const EvictArgs a) {
+__global__ void __launch_bounds__(ST, 2) kv8_select_kernel(const EvictArgs a, int cached) {
+    extern __shared__ float cache[];                    // [cached]
     grid_dep_launch();
     grid_dep_wait();
     const int g = blockIdx.x, s = blockIdx.y, l = blockIdx.z;
@@ -221,8 +211,8 @@ __global__ void __launch_bounds__(ST, 2) kv8_select_kernel(const EvictArgs a) {
     const float* w = a.e.weights + seg * a.e.weights_ld;
     float* ow = a.e.out_weights + seg * a.e.weights_ld;
     int* rows = a.e.out_rows + seg * a.e.keep;
-    if (len <= ST * VPT) select_rows<true>(a, w, ow, rows, len);
-    else select_rows<false>(a, w, ow, rows, len);
+    if (len <= cached) select_rows<true>(a, w, cache, ow, rows, len);
+    else select_rows<false>(a, w, cache, ow, rows, len);
 }
 
 // Codes are worked on four to a word: the conversions to and from fp16 cost several times as much.  The magnitudes of
@@ -357,7 +347,11 @@ __global__ void __launch_bounds__(MT) kv8_move_kernel(const EvictArgs a, int vec
 cudaError_t launch_kv8_evict(const Kv8& c, const Kv8Seqs& q, const Kv8Evict& e, int layer, int n_layers, cudaStream_t s) {
     EvictArgs a{q, e, c.codes, c.scales, c.cfg.n_kv_heads, c.cfg.head_dim, layer};
     if (q.n == 0 || n_layers == 0) return cudaSuccess;
-    const cudaError_t err = launch_ex(c.pdl, kv8_select_kernel, dim3(a.Hkv, q.n, n_layers), dim3(ST), 0, s, a);
+    static std::atomic<uint64_t> done{0};
+    cudaError_t err = smem_limit_once(kv8_select_kernel, CACHE * 4, done);
+    if (err != cudaSuccess) return err;
+    const int cached = q.max_len < CACHE ? q.max_len : CACHE;
+    err = launch_ex(c.pdl, kv8_select_kernel, dim3(a.Hkv, q.n, n_layers), dim3(ST), cached * 4, s, a, cached);
     if (err != cudaSuccess) return err;
     const int P = 1 << q.shift, vecs = P * a.hd / 16;                    // 64 .. 2048 vectors
     const int threads = vecs / NP < 32 ? 32 : vecs / NP;                 // P or 2 P, at least 32
