@@ -79,13 +79,20 @@ cb_status check_rows(const Kv8Seqs& q, const int32_t* start, int32_t n_rows, con
     return CB_OK;
 }
 
+// blocks that a write or a read looks at, counted in 32 bits
+cb_status check_blocks(const cb_kv8& c, const Kv8Seqs& q, const Kv8Rows& r, const char* who) {
+    if (((int64_t)(r.n_rows >> q.shift) + 2 * (int64_t)q.n) * c.cfg.n_kv_heads > 0x7fffffff - 256)
+        return fail(CB_ERR_UNSUPPORTED, "%s: %d rows are too many for one call", who, r.n_rows);
+    return CB_OK;
+}
+
 cb_status cuda_result(cudaError_t e, const char* who) {
     return e == cudaSuccess ? CB_OK : fail(CB_ERR_CUDA, "%s: %s", who, cudaGetErrorString(e));
 }
 
 // K and V rows beside the cache: [n_layers][rows][Hkv][hd], 16-byte vectors
 cb_status check_io(const cb_kv8& c, const void* k, const void* v, int64_t layer_stride, int64_t row_stride, int32_t n_layers,
-                   int32_t n_rows, const char* who, Kv8Io& io) {
+                   int32_t n_rows, bool output, const char* who, Kv8Io& io) {
     const int64_t w = (int64_t)c.cfg.n_kv_heads * c.cfg.head_dim, es = c.cfg.dtype == CB_BF16 ? 2 : 4;
     if (!k || !v) return fail(CB_ERR_INVALID_ARG, "%s: null k or v", who);
     if ((uintptr_t)k % 16 || (uintptr_t)v % 16 || row_stride * es % 16 || layer_stride * es % 16)
@@ -94,8 +101,11 @@ cb_status check_io(const cb_kv8& c, const void* k, const void* v, int64_t layer_
         layer_stride > ((int64_t)1 << 50))
         return fail(CB_ERR_INVALID_ARG, "%s: row stride %lld below a row's %lld elements, or a stride out of range", who,
                     (long long)row_stride, (long long)w);
-    if (n_layers > 1 && n_rows > 0 && layer_stride < (n_rows - 1) * row_stride + w && row_stride < (n_layers - 1) * layer_stride + w)
+    // layers behind each other, or interleaved row by row (what is only read may also be one layer for all)
+    const bool apart = layer_stride >= (n_rows - 1) * row_stride + w || (layer_stride >= w && row_stride >= (n_layers - 1) * layer_stride + w);
+    if (n_layers > 1 && !apart && (output || layer_stride != 0))
         return fail(CB_ERR_INVALID_ARG, "%s: the layers' rows overlap (layer stride %lld)", who, (long long)layer_stride);
+    if (output && overlap(k, w * es, v, w * es)) return fail(CB_ERR_INVALID_ARG, "%s: k and v overlap", who);
     io = Kv8Io{const_cast<void*>(k), const_cast<void*>(v), layer_stride, row_stride, c.cfg.dtype == CB_BF16};
     return CB_OK;
 }
@@ -207,7 +217,8 @@ cb_status cb_kv8_write(cb_kv8* c, const cb_kv8_seqs* seqs, int32_t layer, int32_
     if (st == CB_OK) st = check_rows(q, row_start, n_rows, who, r);
     if (st != CB_OK) return st;
     if (n_rows == 0 || n_layers == 0 || q.n == 0) return CB_OK;
-    st = check_io(*c, k, v, layer_stride, row_stride, n_layers, n_rows, who, io);
+    st = check_blocks(*c, q, r, who);
+    if (st == CB_OK) st = check_io(*c, k, v, layer_stride, row_stride, n_layers, n_rows, false, who, io);
     OnDevice on;
     if (st == CB_OK) st = on.to(c, who);
     if (st != CB_OK) return st;
@@ -226,7 +237,8 @@ cb_status cb_kv8_read(cb_kv8* c, const cb_kv8_seqs* seqs, int32_t layer, int32_t
     if (st == CB_OK) st = check_rows(q, row_start, n_rows, who, r);
     if (st != CB_OK) return st;
     if (n_rows == 0 || n_layers == 0 || q.n == 0) return CB_OK;
-    st = check_io(*c, k, v, layer_stride, row_stride, n_layers, n_rows, who, io);
+    st = check_blocks(*c, q, r, who);
+    if (st == CB_OK) st = check_io(*c, k, v, layer_stride, row_stride, n_layers, n_rows, true, who, io);
     OnDevice on;
     if (st == CB_OK) st = on.to(c, who);
     if (st != CB_OK) return st;
@@ -257,13 +269,13 @@ cb_status cb_kv8_attention(cb_kv8* c, const cb_kv8_seqs* seqs, int32_t layer, co
     }
     if (weights) {
         if (weights_ld < sq.max_len) return fail(CB_ERR_INVALID_ARG, "%s: weights_ld %d below max_len %d", who, weights_ld, sq.max_len);
-        const int64_t cells = (int64_t)n_q * c->cfg.n_heads * ((((int64_t)sq.max_len + 127) / 128) * 128 + 1);
-        if (cells > c->cfg.weight_cells)
-            return fail(CB_ERR_INVALID_ARG, "%s: returning weights needs %lld cells, the cache was created with %lld", who,
-                        (long long)cells, (long long)c->cfg.weight_cells);
+        const int64_t row = (((int64_t)sq.max_len + 127) / 128) * 128 + 1, rows = (int64_t)n_q * c->cfg.n_heads;
+        if (sq.max_len > 0 && rows > c->cfg.weight_cells / row)          // (rows * row may pass 64 bits)
+            return fail(CB_ERR_INVALID_ARG, "%s: returning weights needs %.0f cells, the cache was created with %lld", who,
+                        (double)rows * (double)row, (long long)c->cfg.weight_cells);
     }
     // tiles of 128 keys and at least one query row, of every KV head
-    if (((int64_t)n_q + sq.n) * c->cfg.n_kv_heads * ((int64_t)sq.max_len / 128 + 2) > 0x7fffffff)
+    if (((int64_t)n_q + sq.n) * c->cfg.n_kv_heads > 0x7fffffff / ((int64_t)sq.max_len / 128 + 2))
         return fail(CB_ERR_UNSUPPORTED, "%s: %d query rows over %d keys are too many for one call", who, n_q, sq.max_len);
     if (sq.n == 0 || (n_q == 0 && !weights)) return CB_OK;
     OnDevice on;
@@ -291,6 +303,12 @@ cb_status cb_kv8_evict(cb_kv8* c, const cb_kv8_seqs* seqs, const int32_t* dst_ta
     const int most = n_keep < q.max_len ? n_keep : q.max_len;
     if ((int64_t)dst_ld * c->cfg.page_size < most)
         return fail(CB_ERR_INVALID_ARG, "%s: the destination tables' %d pages hold fewer than %d rows", who, dst_ld, most);
+    // one table at two widths would be evicted in place by CTAs that take it for two tables
+    const int64_t src_end = ((int64_t)(q.n - 1) * q.table_ld + (q.max_len + c->cfg.page_size - 1) / c->cfg.page_size) * 4;
+    const int64_t dst_end = ((int64_t)(q.n - 1) * dst_ld + (most + c->cfg.page_size - 1) / c->cfg.page_size) * 4;
+    const bool same = dst_table == q.table && (dst_ld == q.table_ld || q.n == 1);
+    if (!same && overlap(dst_table, dst_end, q.table, src_end))
+        return fail(CB_ERR_INVALID_ARG, "%s: dst_table overlaps the sequences' table without being the same", who);
     if (weights_ld < q.max_len) return fail(CB_ERR_INVALID_ARG, "%s: weights_ld %d below max_len %d", who, weights_ld, q.max_len);
     const int64_t cells = (int64_t)n_layers * q.n * c->cfg.n_kv_heads * weights_ld * 4;
     if (weights != out_weights && overlap(weights, cells, out_weights, cells))
@@ -298,7 +316,7 @@ cb_status cb_kv8_evict(cb_kv8* c, const cb_kv8_seqs* seqs, const int32_t* dst_ta
     OnDevice on;
     st = on.to(c, who);
     if (st != CB_OK) return st;
-    const Kv8Evict e{dst_table, dst_ld, weights, out_weights, weights_ld, n_keep, n_sink, n_recent, out_rows, out_lens};
+    const Kv8Evict e{dst_table, same ? q.table_ld : dst_ld, weights, out_weights, weights_ld, n_keep, n_sink, n_recent, out_rows, out_lens};
     return cuda_result(launch_kv8_evict(*c, q, e, layer, n_layers, (cudaStream_t)stream), who);
 }
 

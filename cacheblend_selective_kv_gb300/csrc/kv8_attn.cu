@@ -682,7 +682,7 @@ cudaError_t launch_kv8_attention(const Kv8& c, const Kv8Seqs& q, const Kv8Rows& 
     p.min_tiles = 2;
     p.part = c.part;
     p.arrived = c.arrived;
-    p.scores = a.weights ? c.scores : nullptr;
+    p.scores = a.weights && q.max_len > 0 ? c.scores : nullptr;      // (no keys: no weights to return)
     p.stats = c.stats;
     p.score_ld = (q.max_len + TK - 1) / TK * TK;
     if (r.n_rows > 0) {

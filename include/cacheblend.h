@@ -337,7 +337,8 @@ cb_status cb_kv8_status(cb_kv8* cache, uint32_t* bits, int32_t clear);
  *   write  quantises the rows into their blocks.  A block that also holds earlier rows of its sequence keeps the larger
  *          of its old scale and the new rows' own, and its old codes are rounded to it if it grew.  The pages written
  *          must belong to one sequence (cb_pages_plan_write gives a shared block a page of its own).
- *   read   writes code * scale.
+ *   read   writes code * scale; k, v and their layers must not overlap.
+ * (write may be given one layer for all: layer_stride 0.)
  * Async on `stream`; no allocation. */
 cb_status cb_kv8_write(cb_kv8* cache, const cb_kv8_seqs* seqs, int32_t layer, int32_t n_layers, const void* k,
                        const void* v, int64_t layer_stride, int64_t row_stride, const int32_t* row_start,
@@ -358,6 +359,7 @@ cb_status cb_kv8_read(cb_kv8* cache, const cb_kv8_seqs* seqs, int32_t layer, int
  *                0 .. len - 1 (others are left as they were); add != 0 adds to what stands there.  What cb_kv8_evict
  *                ranks by: written once for a query window, or added up over decoding steps.
  * NaN behind what a row sees (in a later row's K or V, or behind the sequence) does not reach it.
+ * (n_q + n_seqs) * n_kv_heads * (max_len / 128 + 2) has to stay below 2^31 (else CB_ERR_UNSUPPORTED).
  * Every sum runs in a fixed order: the same call gives the same bits.  Async on `stream`; no allocation. */
 cb_status cb_kv8_attention(cb_kv8* cache, const cb_kv8_seqs* seqs, int32_t layer, const void* q, int64_t q_stride,
                            const int32_t* q_start, int32_t n_q, float scale, void* out, int64_t out_stride,
@@ -368,12 +370,12 @@ cb_status cb_kv8_attention(cb_kv8* cache, const cb_kv8_seqs* seqs, int32_t layer
  * not positive, or NaN, ranks as 0): n_keep rows, or all of a sequence with no more than that.  The kept rows, in
  * order, become rows 0, 1, .. of the destination pages, quantised as cb_kv8_write would quantise their values.  Heads
  * keep different rows; K was rotated at its own position when it was stored, so attention needs no positions.
- *   dst_table    device int32 [n_seqs][dst_ld]: seqs->table itself (with its table_ld) evicts in place; any other table
- *                must name pages that seqs->table does not.
+ *   dst_table    device int32 [n_seqs][dst_ld]: seqs->table itself (with its table_ld) evicts in place, where no two
+ *                sequences may share a page; any other table must name pages that seqs->table does not, each once.
  *   weights      device float32 [n_layers][n_seqs][n_kv_heads][weights_ld]
  *   out_weights  the same shape, or weights itself: the kept rows' weights at entries 0 .. kept - 1, 0 at kept .. len - 1
  *   out_rows     device int32 [n_layers][n_seqs][n_kv_heads][n_keep]: the kept rows, ascending, -1 behind the last
- *   out_lens     device int32 [n_seqs]: min(len, n_keep); may be seqs->lens
+ *   out_lens     device int32 [n_seqs]: min(len, n_keep); may be seqs->lens (where one call evicts all layers)
  * Async on `stream`; no allocation. */
 cb_status cb_kv8_evict(cb_kv8* cache, const cb_kv8_seqs* seqs, const int32_t* dst_table, int32_t dst_ld, int32_t layer,
                        int32_t n_layers, const float* weights, int32_t weights_ld, int32_t n_keep, int32_t n_sink,

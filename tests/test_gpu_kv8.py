@@ -275,6 +275,70 @@ def test_attention(cb, hd, dtype, H, G, P, lens, rows):
     c.done()
 
 
+@pytest.mark.parametrize("dtype,rows", [("bf16", 1), ("f32", 3), ("bf16", 40)])
+@pytest.mark.parametrize("scale", [-0.3, 0.0, 2.5])
+def test_attention_scale_of_any_sign(cb, dtype, rows, scale):
+    """A negative scale turns the order of the keys round; with 0 every key that is seen weighs the same."""
+    lens = [150, 300]
+    c = Case(cb, lens, H=2, G=2, hd=64, P=32, dtype=dtype, seed=rows, cells=cb.KV8Cache.cells(2 * rows, 4, 300))
+    q, q64 = c.values(2 * rows, 4, 64)
+    out, w = torch.empty_like(q), torch.zeros((2, 2, 300), device="cuda")
+    c.cache.attention(c.table, c.lens_t, q, out, scale=scale, weights=w, max_len=300)
+    check_attention(c, q, q64, [0, rows, 2 * rows], out, w, scale=scale)
+    c.done()
+
+
+@pytest.mark.parametrize("rows", [[2, 0, 1, 3], [40, 9, 0, 70]])
+def test_attention_with_empty_sequences(cb, rows):
+    """Sequences without rows, without keys, and with more rows than keys, in one call; and calls without rows or keys."""
+    lens = [400, 0, 129, 3]
+    n, G = sum(rows), 3
+    c = Case(cb, lens, H=2, G=G, hd=64, P=16, seed=sum(rows), cells=cb.KV8Cache.cells(n, 6, 400))
+    q, q64 = c.values(n, 2 * G, 64)
+    st, out = starts_of(rows), torch.full_like(q, 7.0)
+    w = torch.full((4, 2, 400), 3.0, device="cuda")
+    c.cache.attention(c.table, c.lens_t, q, out, q_start=i32(st), weights=w, max_len=400)
+    check_attention(c, q, q64, st, out, w)
+    assert torch.count_nonzero(out[st[1]:st[2]]) == 0   # no keys
+    for s, m in enumerate(lens):
+        assert torch.all(w[s, :, m:] == 3.0)
+    assert torch.count_nonzero(w[[s for s in range(4) if rows[s] == 0], :, :0]) == 0
+    # no keys at all: zeros, and nothing of the weights (nor of the scratch, which holds fewer rows than these)
+    many = torch.ones((4 * 1000, 2 * G, 64), dtype=q.dtype, device="cuda")
+    o = c.cache.attention(c.table, i32([0] * 4), many, weights=w, max_len=0)
+    assert torch.count_nonzero(o) == 0 and torch.all(w[1] == 3.0)
+    # no rows: every key's weight is 0, or what it was
+    before = w.clone()
+    none = q[:0]
+    c.cache.attention(c.table, c.lens_t, none, weights=w, add=True, max_len=400)
+    assert torch.equal(w, before)
+    c.cache.attention(c.table, c.lens_t, none, weights=w, max_len=400)
+    for s, m in enumerate(lens):
+        assert torch.count_nonzero(w[s, :, :m]) == 0 and torch.all(w[s, :, m:] == 3.0)
+    c.done()
+
+
+@pytest.mark.parametrize("rows", [1, 40])
+def test_two_handles_on_one_pool_at_once(cb, rows):
+    lens = [3000, 1500]
+    c = Case(cb, lens, H=2, G=4, hd=128, P=64, seed=3, cells=cb.KV8Cache.cells(2 * rows, 8, 3000))
+    other = cb.KV8Cache(c.codes, c.scales, n_heads=8, weight_cells=cb.KV8Cache.cells(2 * rows, 8, 3000))
+    qs = [c.values(2 * rows, 8, 128)[0] for _ in range(2)]
+    ws = [torch.zeros((2, 2, 3000), device="cuda") for _ in range(4)]
+    want = [c.cache.attention(c.table, c.lens_t, qs[i], weights=ws[i], max_len=3000) for i in range(2)]
+    outs, streams = [torch.empty_like(q) for q in qs], [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for i, cache in enumerate((c.cache, other)):
+            cache.attention(c.table, c.lens_t, qs[i], outs[i], weights=ws[2 + i], max_len=3000, stream=streams[i])
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert torch.equal(outs[i], want[i]) and torch.equal(ws[2 + i], ws[i])
+    assert other.status() == 0
+    other.close()
+    c.done()
+
+
 @pytest.mark.parametrize("dtype,rows", [("bf16", 2), ("f32", 2), ("bf16", 25)])
 def test_attention_large_scores_and_scales(cb, dtype, rows):
     """Scores spread over hundreds (most weights vanish), a sink that outweighs the rest, and V blocks whose scales
@@ -506,6 +570,36 @@ def test_evict_long_sequence_selects_like_a_sort(cb):
     cache.close()
 
 
+@pytest.mark.parametrize("n", [16384, 16385, 20000])
+def test_evict_long_sequence_in_place(cb, n):
+    """In place, through a view of the table that is only as wide as what is kept."""
+    keep, P = 5000, 64
+    cache = cb.KV8Cache.empty(1, n // P + 1, 1, P, 64, 4)
+    g = torch.Generator(device="cuda").manual_seed(n)
+    k = torch.randn((n, 1, 64), generator=g, device="cuda").bfloat16()
+    table = torch.randperm(n // P + 1, generator=g, device="cuda").int()[None]
+    cache.write(table, i32([n]), k, -k, max_len=n)
+    back = [torch.empty_like(k) for _ in range(2)]
+    cache.read(table, i32([n]), *back, max_len=n)
+    w = torch.randint(0, 2000, (1, 1, 1, n), generator=g, device="cuda").float() / 128
+    was, lens = w.clone(), i32([n])
+    out = cache.evict(table, lens, table[:, :-(-keep // P)], w, keep, 3, 30, max_len=n, out_lens=lens)
+    r = was[0, 0, 0].clone()
+    r[:3] = r[n - 30:] = float("inf")
+    want = torch.sort(r, descending=True, stable=True).indices[:keep].sort().values
+    assert torch.equal(out["rows"][0, 0, 0], want.int()) and lens.tolist() == [keep]
+    assert torch.equal(w[0, 0, 0, :keep], was[0, 0, 0, want]) and torch.count_nonzero(w[0, 0, 0, keep:]) == 0
+    got = [torch.empty_like(k[:keep]) for _ in range(2)]
+    cache.read(table, lens, *got, max_len=n)
+    # a value that meets a larger scale is off by half a step at most: 2^-4 of it, or 2^-10 of the scale, which is
+    # below 2^-4 here (448 times a scale is less than twice the block's largest value, itself less than 8)
+    for a, b in zip(got, back):
+        x, y = a.double(), b[want].double()
+        assert torch.all((x - y).abs() <= 2.0 ** -4 * y.abs() + 2.0 ** -10 * 2.0 ** -4)
+    assert cache.status() == 0
+    cache.close()
+
+
 # ------------------------------------------------------------------------------------------------
 # bad ids, streams, devices
 # ------------------------------------------------------------------------------------------------
@@ -638,6 +732,8 @@ def test_python_refusals(cb):
               lambda: a.attention(c.table, c.lens_t, q, out=q),
               lambda: a.attention(c.table, c.lens_t, q, weights=torch.zeros((2, 2, 48), device="cuda")),
               lambda: a.write(c.table, c.lens_t, kv[:, :1], kv[:, :1]),
+              lambda: a.read(c.table, c.lens_t, kv, kv),
+              lambda: a.evict(c.table, c.lens_t, c.table.view(-1)[:4].view(2, 2), torch.zeros((1, 2, 2, 48), device="cuda"), 4),
               lambda: a.evict(c.table, c.lens_t, c.table, torch.zeros((1, 2, 2, 48), device="cuda"), 4, 3, 2)):
         with pytest.raises(cb.CacheBlendError) as ei:
             f()

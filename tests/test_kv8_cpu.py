@@ -185,3 +185,63 @@ def test_evict_refusals(lib):
 def test_blend_kv8_refuses_null(lib):
     assert lib.cb_blend_kv8(None, None, 1, None, None, None, None, 0, None, 0, None, None, None, None, None, None) == \
         cb.CB_ERR_INVALID_ARG
+
+
+def unsupported(code, word):
+    assert code == cb.CB_ERR_UNSUPPORTED and word in cb.cb_last_error(), (code, cb.cb_last_error())
+
+
+@pytest.mark.parametrize("name", ["cb_kv8_write", "cb_kv8_read"])
+def test_rows_overlaps_and_counts(lib, name):
+    f, h = getattr(lib, name), fake(n_kv_heads=2)
+    read = name == "cb_kv8_read"
+
+    def call(n_layers=2, k=A, v=2 * A, ls=10 * 128, rs=128, rows=10, handle=h, sq=None):
+        return f(ctypes.addressof(handle), sq or seqs(), 0, n_layers, k, v, ls, rs, A, rows, None)
+
+    one_for_all = call(ls=0)                           # an input may be one layer for all, an output may not
+    refused(one_for_all, "overlap") if read else reaches_device(one_for_all)
+    one_for_all = call(ls=0, rs=2 * 128)
+    refused(one_for_all, "overlap") if read else reaches_device(one_for_all)
+    refused(call(ls=64, rs=2 * 128), "overlap")        # interleaved, but not by a whole row
+    same = call(v=A)
+    refused(same, "k and v overlap") if read else reaches_device(same)
+    reaches_device(call(v=A + 256, rs=256, ls=10 * 256))           # K and V side by side in a row
+    many = fake(n_kv_heads=1024, n_heads=1024, n_layers=4, page_size=16, n_pages=1000)
+    w = 1024 * 64                                      # blocks: (n_rows / 16 + 2 * 3) * 1024 below 2^31
+    reaches_device(call(n_layers=1, rs=w, rows=16 * ((1 << 21) - 8), handle=many, sq=seqs(top=60)))
+    unsupported(call(n_layers=1, rs=w, rows=1 << 26, handle=many, sq=seqs(top=60)), "rows")
+    unsupported(call(n_layers=1, rs=w, rows=1 << 30, handle=many, sq=seqs(top=60)), "rows")
+
+
+def test_attention_counts_pass_64_bits(lib):
+    """Sizes whose products pass 32 or 64 bits are refused and do not wrap around to small ones."""
+    h = fake(n_kv_heads=1024, n_heads=8192, weight_cells=5000)
+    w = 8192 * 64
+
+    def call(n, top, weights=None, handle=h, qs=w):
+        return lib.cb_kv8_attention(ctypes.addressof(handle), seqs(n=1, ld=1 << 26, top=top), 0, A, qs, None, n, 0.125, 1 << 55, qs, weights,
+                                    1 << 30, 0, None)
+
+    reaches_device(call(1, 4096))
+    for n, top in ((1 << 30, 1 << 30), (1 << 30, (1 << 30) - 256), (1 << 20, 1 << 20), (1 << 21, 0), (1 << 12, 1 << 16)):
+        unsupported(call(n, top), "too many")
+    for n, top in ((1 << 30, 1 << 30), (1 << 28, (1 << 23) - 1), (1, 4096), (1 << 30, 1)):
+        refused(call(n, top, weights=A), "cells")
+    small = fake(weight_cells=5000)
+    # no keys: no weights to return, and no scratch
+    reaches_device(lib.cb_kv8_attention(ctypes.addressof(small), seqs(n=1, top=0), 0, A, 512, None, 5000, 0.125, 1 << 50, 512, A, 0, 0, None))
+
+
+def test_evict_refuses_overlapping_tables(lib):
+    h = fake()
+
+    def call(n=3, dst=2 * A, dld=4, ld=4, keep=50):
+        return lib.cb_kv8_evict(ctypes.addressof(h), seqs(n=n, ld=ld), dst, dld, 0, 4, A, 100, keep, 4, 8, A, 9 * A, A, None)
+
+    reaches_device(call(dst=A))
+    refused(call(dst=A, dld=2), "overlaps")            # the same table at another width names other pages
+    refused(call(dst=A + 4), "overlaps")
+    refused(call(dst=A + 2 * 4 * 4), "overlaps")
+    reaches_device(call(dst=A, dld=2, n=1))            # one sequence: its first pages, in place
+    reaches_device(call(dst=A + 3 * 4 * 4))
