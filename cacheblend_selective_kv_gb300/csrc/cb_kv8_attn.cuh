@@ -96,40 +96,45 @@ struct Cursor {
 
 // Joins one row of an item's pieces in their order, by a warp: piece u holds the row's HD sums at offset `row` and its
 // (maximum, sum) at offset `stat` of piece_at(u).  Lanes below HD / 4 return four dims each, every lane the joint m and l.
-template <int HD, typename F>
+template <int HD, int NB, typename F>
 __device__ __forceinline__ float4 join_pieces(const F& piece_at, int n_pieces, int row, int stat, float& m, float& l) {
-    constexpr int LANES = HD / 4, SIDE = 32 / LANES;             // lanes of a row; pieces side by side
+    constexpr int LANES = HD / 4, SIDE = 32 / LANES, STEP = NB * SIDE;      // lanes of a row; pieces side by side, per step
     const int lane = threadIdx.x & 31, side = lane / LANES, d = (lane % LANES) * 4;
-    m = -INFINITY;
-    for (int u = lane; u < n_pieces; u += 32) m = fmaxf(m, __ldcg(piece_at(u) + stat));
-    m = warp_max(m);
-    l = 0.f;
+    const auto stat_of = [&](int u) {
+        return u < n_pieces ? __ldcg(reinterpret_cast<const float2*>(piece_at(u) + stat)) : make_float2(-INFINITY, 0.f);
+    };
+    float2 ml = stat_of(lane);
+    float f = 0.f;
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    m = -INFINITY;
+    l = 0.f;
 #pragma unroll 1
-    for (int ub = 0; ub < n_pieces; ub += 32) {
-        float f = 0.f;
-        if (ub + lane < n_pieces) {
-            const float2 ml = __ldcg(reinterpret_cast<const float2*>(piece_at(ub + lane) + stat));
+    for (int u0 = 0; u0 < n_pieces; u0 += STEP) {
+        float4 o[NB];                                            // under way together, the first ones with the maxima
+#pragma unroll
+        for (int v = 0; v < NB; ++v) {
+            const int u = u0 + v * SIDE + side;
+            o[v] = u < n_pieces ? __ldcg(reinterpret_cast<const float4*>(piece_at(u) + row + d)) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        if (u0 % 32 == 0) {                                      // the factors of 32 pieces
+            if (u0 == 0) {
+                m = ml.x;
+#pragma unroll 1
+                for (int u = lane + 32; u < n_pieces; u += 32) m = fmaxf(m, __ldcg(piece_at(u) + stat));
+                m = warp_max(m);
+            } else {
+                ml = stat_of(u0 + lane);
+            }
             f = ml.x == -INFINITY ? 0.f : exp2_fast(ml.x - m);
             l = fmaf(ml.y, f, l);
         }
-        const int n = min(32, n_pieces - ub);
-#pragma unroll 1
-        for (int v0 = 0; v0 < n; v0 += 8 * SIDE) {
-            float4 o[8];
 #pragma unroll
-            for (int v = 0; v < 8; ++v) {
-                const int u = v0 + v * SIDE + side;
-                o[v] = u < n ? __ldcg(reinterpret_cast<const float4*>(piece_at(ub + u) + row + d)) : make_float4(0.f, 0.f, 0.f, 0.f);
-            }
-#pragma unroll
-            for (int v = 0; v < 8; ++v) {
-                const float w = __shfl_sync(0xffffffffu, f, (v0 + v * SIDE + side) & 31);
-                a.x = fmaf(o[v].x, w, a.x);
-                a.y = fmaf(o[v].y, w, a.y);
-                a.z = fmaf(o[v].z, w, a.z);
-                a.w = fmaf(o[v].w, w, a.w);
-            }
+        for (int v = 0; v < NB; ++v) {
+            const float w = __shfl_sync(0xffffffffu, f, (u0 + v * SIDE + side) & 31);
+            a.x = fmaf(o[v].x, w, a.x);
+            a.y = fmaf(o[v].y, w, a.y);
+            a.z = fmaf(o[v].z, w, a.z);
+            a.w = fmaf(o[v].w, w, a.w);
         }
     }
     l = warp_sum(l);

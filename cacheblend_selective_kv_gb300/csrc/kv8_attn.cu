@@ -549,9 +549,10 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
                 }
                 ptx::named_bar_sync(1, SOFT);
                 if (c.last) {                                    // join the pieces in their order, a warp per column
+#pragma unroll 1
                     for (int k = warp; k < cols; k += SOFT / 32) {
                         float m, l;
-                        const float4 a = join_pieces<HD>(piece_at, n_pieces, k * HD, NC * HD + 2 * k, m, l);
+                        const float4 a = join_pieces<HD, 8>(piece_at, n_pieces, k * HD, NC * HD + 2 * k, m, l);
                         if (lane < HD / 4) store4(out_at(k) + lane * 4, a, 1.f / l, pos0 + div_g(p, k) >= 0);
                         if (p.scores && lane == 0) p.stats[stat0 + k] = make_float2(m, 1.f / l);
                     }
