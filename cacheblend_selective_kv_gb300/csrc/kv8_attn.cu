@@ -100,6 +100,10 @@ template <int N> __device__ __forceinline__ void tmem_ld_done(uint32_t* r) {
 }
 constexpr int MAX_STAGES = 3;
 constexpr int RING = 8;
+struct Open {                            // an item of which this CTA has a piece
+    int u0, pieces;                      // the CTA it begins in, how many have a piece of it
+    int row0, cols, pos0, g;
+};
 struct Shared {
     ScaleRing<RING> ring;
     uint64_t k_full[MAX_STAGES], v_full[MAX_STAGES], k_empty[MAX_STAGES], v_empty[MAX_STAGES];
@@ -108,7 +112,8 @@ struct Shared {
     uint32_t tmem;
     int abort;
     Find find;
-    int last;                            // this CTA joins the item
+    Open open[2];                        // at the beginning of this CTA's tiles, at their end
+    int last[2];                         // this CTA joins it
 };
 
 // ------------------------------------------------------------------------------------------------
@@ -128,8 +133,8 @@ template <int HD_, int NC_, int GR_, int TQ_, int TP_, int CTAS_, int STAGES_> s
     static constexpr int OFF_Q = 2 * STAGES * KV_BYTES;
     static constexpr int OFF_P = (OFF_Q + 2 * Q_BYTES + 1023) / 1024 * 1024;
     static constexpr int OFF_X = (OFF_P + P_BYTES + 1023) / 1024 * 1024;
-    // floats: wmax, ymax [2][GR][4][NW]; cols [2][4 GR][4][NW]; qscale [2][NC]; wsum, colm [4][NC]; nan_from [HD]
-    static constexpr int X_FLOATS = 2 * 8 * NC + 2 * 4 * GR * 4 * NW + 2 * NC + 8 * NC + HD;
+    // floats: wmax, ymax [2][GR][4][NW]; cols [2][4 GR][4][NW]; qscale [2][NC]; wsum, colm [4][NC]; nan_from [2][HD]
+    static constexpr int X_FLOATS = 2 * 8 * NC + 2 * 4 * GR * 4 * NW + 2 * NC + 8 * NC + 2 * HD;
     static constexpr int OFF_C = (OFF_X + X_FLOATS * 4 + 63) / 64 * 64;
     static constexpr int BYTES = OFF_C + (int)sizeof(Shared);
     static constexpr int PIECE = NC * (HD + 2);                            // floats of an unfinished item
@@ -137,6 +142,11 @@ template <int HD_, int NC_, int GR_, int TQ_, int TP_, int CTAS_, int STAGES_> s
     static_assert((BYTES + 1024) * CTAS <= 228 * 1024 && STAGES <= MAX_STAGES, "shared memory");
     static_assert(NW == 4 || NW == 8 || NW == 16, "columns of a group");
 };
+
+// piece u of the item that begins in CTA u0: a CTA's first one is of an item that began before
+template <typename S> __device__ __forceinline__ float* piece_at(const AttnArgs& p, int u0, int u) {
+    return p.part + (int64_t)((u0 + u) * 2 + (u == 0 ? 1 : 0)) * S::PIECE;
+}
 
 // Kept out of the tile loop, whose instructions have to stay close together:
 
@@ -218,7 +228,7 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
     float* qscale = cols_of + 2 * 4 * GR * 4 * NW;
     float* wsum = qscale + 2 * NC;
     float* colm = wsum + 4 * NC;
-    int* nan_from = reinterpret_cast<int*>(colm + 4 * NC);
+    int* nan_marks = reinterpret_cast<int*>(colm + 4 * NC);
     Shared& c = *reinterpret_cast<Shared*>(sm + S::OFF_C);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     unsigned* status = p.q.status;
@@ -328,7 +338,7 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
             q_terms<T, S>(p, u, sQ + buf * S::Q_BYTES, qscale + buf * NC, to_exp2);
             if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&c.q_full));
         };
-        int item = 0;
+        int item = 0, n_open = 0;
         Cursor next;
         for (int i = 0; i < count; ++item) {
             const int first = cur.t, n_here = min(cur.nt - first, count - i), g = cur.g;
@@ -337,6 +347,7 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
             const int pos0 = q.len - q.n + q0;                   // position of the item's first query row
             const int64_t stat0 = ((int64_t)g * p.r.n_rows + q.r0 + q0) * p.G;     // the item's first column in scores, stats
 
+            int* nan_from = nan_marks + (item & 1) * HD;         // (the item before's may still be read)
             if (tid < HD) nan_from[tid] = INT_MAX;
             if (item == 0) write_q(cur, 0);
             ptx::named_bar_sync(1, SOFT);                        // nan_from, the first item's qscale
@@ -527,10 +538,11 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
                     if (p.scores && key == 0) p.stats[stat0 + c0 + k] = make_float2(colm[c0 + k], inv);
                 }
             } else {
+                // A piece.  It is announced, and joined if it was the last, when the CTA has done all its tiles: here every warp
+                // would wait for the fence and the count (decode of 64 x 8K: 100.5 us that way, 96 this way).
                 const int begin = t0 + (i - n_here) - first;           // the item's first tile in the list
                 const int u0 = (unsigned)begin / (unsigned)per, n_pieces = (int)((unsigned)(begin + cur.nt - 1) / (unsigned)per) - u0 + 1;
-                const auto piece_at = [&](int u) { return p.part + (int64_t)((u0 + u) * 2 + (u == 0 ? 1 : 0)) * S::PIECE; };
-                float* piece = piece_at(blockIdx.x - u0);
+                float* piece = piece_at<S>(p, u0, blockIdx.x - u0);
                 if (key < HD) {
 #pragma unroll
                     for (int k = 0; k < NW; ++k) piece[(c0 + k) * HD + key] = acc[k];
@@ -540,25 +552,36 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
                     for (int k = 0; k < NW; ++k)
                         *reinterpret_cast<float2*>(piece + NC * HD + 2 * (c0 + k)) = make_float2(colm[c0 + k], lsum[k]);
                 }
-                ptx::named_bar_sync(1, SOFT);
-                if (tid == 0) {
-                    __threadfence();                             // the whole CTA's piece, ordered by the barrier
-                    c.last = atomicAdd(p.arrived + u0, 1u) == (unsigned)n_pieces - 1;
-                    if (c.last) atomicExch(p.arrived + u0, 0u);
-                    __threadfence();
-                }
-                ptx::named_bar_sync(1, SOFT);
-                if (c.last) {                                    // join the pieces in their order, a warp per column
-#pragma unroll 1
-                    for (int k = warp; k < cols; k += SOFT / 32) {
-                        float m, l;
-                        const float4 a = join_pieces<HD, 8>(piece_at, n_pieces, k * HD, NC * HD + 2 * k, m, l);
-                        if (lane < HD / 4) store4(out_at(k) + lane * 4, a, 1.f / l, pos0 + div_g(p, k) >= 0);
-                        if (p.scores && lane == 0) p.stats[stat0 + k] = make_float2(m, 1.f / l);
-                    }
-                }
+                if (tid == 0) c.open[n_open] = Open{u0, n_pieces, q.r0 + q0, cols, pos0, g};
+                ++n_open;
             }
             if (i < count) cur = next;
+        }
+        if (n_open > 0) {
+            ptx::named_bar_sync(1, SOFT);
+            if (tid < n_open) {
+                const Open& o = c.open[tid];
+                __threadfence();                                 // the whole CTA's pieces, ordered by the barrier
+                c.last[tid] = atomicAdd(p.arrived + o.u0, 1u) == (unsigned)o.pieces - 1;
+                if (c.last[tid]) atomicExch(p.arrived + o.u0, 0u);
+                __threadfence();
+            }
+            ptx::named_bar_sync(1, SOFT);
+#pragma unroll 1
+            for (int n = 0; n < n_open; ++n) {
+                if (!c.last[n]) continue;
+                const Open o = c.open[n];                        // join the pieces in their order, a warp per column
+#pragma unroll 1
+                for (int k = warp; k < o.cols; k += SOFT / 32) {
+                    float m, l;
+                    const auto at = [&](int u) { return piece_at<S>(p, o.u0, u); };
+                    const float4 a = join_pieces<HD, 8>(at, o.pieces, k * HD, NC * HD + 2 * k, m, l);
+                    const int row = div_g(p, k);
+                    T* out = (T*)p.a.out + (int64_t)(o.row0 + row) * p.a.out_stride + (int64_t)(o.g * p.G + mod_g(p, k)) * HD;
+                    if (lane < HD / 4) store4(out + lane * 4, a, 1.f / l, o.pos0 + row >= 0);
+                    if (p.scores && lane == 0) p.stats[((int64_t)o.g * p.r.n_rows + o.row0) * p.G + k] = make_float2(m, 1.f / l);
+                }
+            }
         }
     }
     ptx::tc_fence_before();
