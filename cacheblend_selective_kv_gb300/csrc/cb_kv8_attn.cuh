@@ -14,6 +14,10 @@ namespace {
 
 constexpr int TK = 128;                  // keys per tile
 
+// 16 bytes to shared memory, past L1
+__device__ __forceinline__ void cp_async16(uint32_t dst, const float* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 struct AttnArgs {
@@ -96,9 +100,12 @@ struct Cursor {
 
 // Joins one row of an item's pieces in their order, by a warp: piece u holds the row's HD sums at offset `row` and its
 // (maximum, sum) at offset `stat` of piece_at(u).  Lanes below HD / 4 return four dims each, every lane the joint m and l.
+// NB loads of a lane are under way together, the first of them with the maxima; they land in `buf` (shared memory, NB * 32
+// vectors of this warp), because the attention kernel has no registers to spare for them.
 template <int HD, int NB, typename F>
-__device__ __forceinline__ float4 join_pieces(const F& piece_at, int n_pieces, int row, int stat, float& m, float& l) {
+__device__ __forceinline__ float4 join_pieces(const F& piece_at, int n_pieces, int row, int stat, float& m, float& l, float4* buf) {
     constexpr int LANES = HD / 4, SIDE = 32 / LANES, STEP = NB * SIDE;      // lanes of a row; pieces side by side, per step
+    static_assert(STEP % 32 == 0 || 32 % STEP == 0, "steps and the factors' blocks of 32 pieces");
     const int lane = threadIdx.x & 31, side = lane / LANES, d = (lane % LANES) * 4;
     const auto stat_of = [&](int u) {
         return u < n_pieces ? __ldcg(reinterpret_cast<const float2*>(piece_at(u) + stat)) : make_float2(-INFINITY, 0.f);
@@ -110,11 +117,12 @@ __device__ __forceinline__ float4 join_pieces(const F& piece_at, int n_pieces, i
     l = 0.f;
 #pragma unroll 1
     for (int u0 = 0; u0 < n_pieces; u0 += STEP) {
-        float4 o[NB];                                            // under way together, the first ones with the maxima
-#pragma unroll
-        for (int v = 0; v < NB; ++v) {
+        float4* to = buf + lane;
+        const int nv = min(NB, (n_pieces - u0 + SIDE - 1) / SIDE);
+#pragma unroll 1
+        for (int v = 0; v < nv; ++v) {
             const int u = u0 + v * SIDE + side;
-            o[v] = u < n_pieces ? __ldcg(reinterpret_cast<const float4*>(piece_at(u) + row + d)) : make_float4(0.f, 0.f, 0.f, 0.f);
+            if (u < n_pieces) cp_async16(ptx::smem_u32(to + v * 32), piece_at(u) + row + d);
         }
         if (u0 % 32 == 0) {                                      // the factors of 32 pieces
             if (u0 == 0) {
@@ -128,13 +136,17 @@ __device__ __forceinline__ float4 join_pieces(const F& piece_at, int n_pieces, i
             f = ml.x == -INFINITY ? 0.f : exp2_fast(ml.x - m);
             l = fmaf(ml.y, f, l);
         }
-#pragma unroll
-        for (int v = 0; v < NB; ++v) {
-            const float w = __shfl_sync(0xffffffffu, f, (u0 + v * SIDE + side) & 31);
-            a.x = fmaf(o[v].x, w, a.x);
-            a.y = fmaf(o[v].y, w, a.y);
-            a.z = fmaf(o[v].z, w, a.z);
-            a.w = fmaf(o[v].w, w, a.w);
+        asm volatile("cp.async.wait_all;" ::: "memory");         // a lane reads what it has asked for itself
+#pragma unroll 1
+        for (int v = 0; v < nv; ++v) {
+            const int k = v * SIDE + side;
+            const float w = __shfl_sync(0xffffffffu, f, (u0 + k) & 31);
+            if (u0 + k >= n_pieces) continue;
+            const float4 o = to[v * 32];
+            a.x = fmaf(o.x, w, a.x);
+            a.y = fmaf(o.y, w, a.y);
+            a.z = fmaf(o.z, w, a.z);
+            a.w = fmaf(o.w, w, a.w);
         }
     }
     l = warp_sum(l);

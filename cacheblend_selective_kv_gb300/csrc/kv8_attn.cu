@@ -138,6 +138,9 @@ template <int HD_, int NC_, int GR_, int TQ_, int TP_, int CTAS_, int STAGES_> s
     static constexpr int OFF_C = (OFF_X + X_FLOATS * 4 + 63) / 64 * 64;
     static constexpr int BYTES = OFF_C + (int)sizeof(Shared);
     static constexpr int PIECE = NC * (HD + 2);                            // floats of an unfinished item
+    // vectors per lane that a joining warp has under way, where K and V were
+    static constexpr int JOIN = HD / 4 / GR;
+    static_assert(JOIN * 512 * (SOFT / 32) <= OFF_Q, "joining buffers");
     static_assert(TMEM * CTAS <= 512 && 2 * NQ + NP <= 512, "tensor memory");
     static_assert((BYTES + 1024) * CTAS <= 228 * 1024 && STAGES <= MAX_STAGES, "shared memory");
     static_assert(NW == 4 || NW == 8 || NW == 16, "columns of a group");
@@ -567,6 +570,8 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
                 __threadfence();
             }
             ptx::named_bar_sync(1, SOFT);
+            // (K and V of all tiles have been used: O of the last tile has been read)
+            float4* buf = reinterpret_cast<float4*>(sm) + warp * S::JOIN * 32;
 #pragma unroll 1
             for (int n = 0; n < n_open; ++n) {
                 if (!c.last[n]) continue;
@@ -575,7 +580,7 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
                 for (int k = warp; k < o.cols; k += SOFT / 32) {
                     float m, l;
                     const auto at = [&](int u) { return piece_at<S>(p, o.u0, u); };
-                    const float4 a = join_pieces<HD, 8>(at, o.pieces, k * HD, NC * HD + 2 * k, m, l);
+                    const float4 a = join_pieces<HD, S::JOIN>(at, o.pieces, k * HD, NC * HD + 2 * k, m, l, buf);
                     const int row = div_g(p, k);
                     T* out = (T*)p.a.out + (int64_t)(o.row0 + row) * p.a.out_stride + (int64_t)(o.g * p.G + mod_g(p, k)) * HD;
                     if (lane < HD / 4) store4(out + lane * 4, a, 1.f / l, o.pos0 + row >= 0);

@@ -559,11 +559,12 @@ __global__ void __launch_bounds__(256) kv8_join_kernel(const AttnArgs p) {
     grid_dep_wait();
     const Todo d = reinterpret_cast<const Todo*>(p.todo)[blockIdx.x];
     if (d.pieces == 0) return;
-    const int lane = threadIdx.x & 31, u0 = blockIdx.x;
+    __shared__ float4 buf[8][8 * 32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, u0 = blockIdx.x;
     const auto piece_at = [&](int u) { return p.part + (int64_t)((u0 + u) * 2 + (u == 0 ? 1 : 0)) * Rows<HD>::PIECE; };
-    for (int k = blockIdx.y * 8 + (threadIdx.x >> 5); k < d.cols; k += gridDim.y * 8) {
+    for (int k = blockIdx.y * 8 + warp; k < d.cols; k += gridDim.y * 8) {
         float m, l;
-        const float4 a = join_pieces<HD, 16>(piece_at, d.pieces, k * HD, ROWS * HD + 2 * k, m, l);
+        const float4 a = join_pieces<HD, 8>(piece_at, d.pieces, k * HD, ROWS * HD + 2 * k, m, l, buf[warp]);
         bf16* out = (bf16*)p.a.out + (int64_t)(d.row0 + div_g(p, k)) * p.a.out_stride + (int64_t)(d.g * p.G + mod_g(p, k)) * HD;
         if (lane < HD / 4) store4(out + lane * 4, a, 1.f / l, d.pos0 + div_g(p, k) >= 0);
         if (p.scores && lane == 0) p.stats[((int64_t)d.g * p.r.n_rows + d.row0) * p.G + k] = make_float2(m, 1.f / l);
