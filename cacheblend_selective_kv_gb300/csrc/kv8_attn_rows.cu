@@ -389,17 +389,12 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_rows_kernel(const __grid_const
                 // Blocks of 16 keys: what makes S scores in the exp2 domain (the scale of K's block with the row's and the
                 // softmax's constants), V's scale and its logarithm.  Where the first is 0 S is too, and 1 serves: a key that is
                 // not seen has S = -inf, which stays that way.
-                float mul[HK / 16], vs[HK / 16], vl[HK / 16];
-                bool hole = false;
-#pragma unroll
-                for (int k = 0; k < HK / 16; ++k) {
-                    const int box = (hf * HK + k * 16) >> box_shift;
-                    const float ks = scales[box], v = scales[8 + box];
-                    hole |= ks < 0.f;
-                    mul[k] = ks > 0.f && row_mul > 0.f ? fmaxf(ks * row_mul, 1.1754944e-38f) : 1.f;
-                    vs[k] = v * P_UP;
-                    vl[k] = v > 0.f ? fmaxf((float)((int)(__float_as_uint(v) >> 23) - 127), -100.f) : -100.f;
-                }
+                const auto box_at = [&](int k) { return (hf * HK + k) >> box_shift; };
+                const auto mul_at = [&](int k) {
+                    const float ks = scales[box_at(k)];
+                    return ks > 0.f && row_mul > 0.f ? fmaxf(ks * row_mul, 1.1754944e-38f) : 1.f;
+                };
+                const bool hole = fminf(fminf(scales[box_at(0)], scales[box_at(16)]), fminf(scales[box_at(32)], scales[box_at(48)])) < 0.f;
                 // Away from the tile loop's usual path, which has to stay short (with everything unrolled in place, most cycles
                 // went to waiting for instructions): -inf into S for keys that are not loaded or not seen
                 if (hole || j0 + HK - 1 > pos0) {
@@ -414,24 +409,31 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_rows_kernel(const __grid_const
                     }
                     ptx::tmem_wait_st();
                 }
-                uint32_t x[HK];
-#pragma unroll
-                for (int k = 0; k < HK; k += 16) ptx::tmem_ld16_issue(s_at + k, x + k);
+                // Both passes read S in steps of 32 keys, as loops: unrolled over the half's 64 keys their instructions took longer
+                // to fetch than what the second read costs.
                 float top = -INFINITY;                           // the largest of score + log2 of V's scale
+#pragma unroll 1
+                for (int k = 0; k < HK; k += 32) {
+                    uint32_t x[32];
+                    ptx::tmem_ld16_issue(s_at + k, x);
+                    ptx::tmem_ld16_issue(s_at + k + 16, x + 16);
 #pragma unroll
-                for (int k = 0; k < HK; k += 16) {
-                    ptx::tmem_ld_wait16(x + k);
-                    float m = __uint_as_float(x[k]);
+                    for (int h = 0; h < 32; h += 16) {
+                        const float v = scales[8 + box_at(k + h)];
+                        const float vl = v > 0.f ? fmaxf((float)((int)(__float_as_uint(v) >> 23) - 127), -100.f) : -100.f;
+                        const float mul = mul_at(k + h);
+                        ptx::tmem_ld_wait16(x + h);
+                        float m = __uint_as_float(x[h]);
 #pragma unroll
-                    for (int y = 1; y < 16; ++y) m = fmaxf(m, __uint_as_float(x[k + y]));
-                    top = fmaxf(top, fmaf(m, mul[k / 16], vl[k / 16]));
-                }
-                if (SCORES && row < cols) {
-                    float4* score = quads_of(p, q, g, t) + (int64_t)(hf * (HK / 4)) * (q.n * p.G) + q0 * p.G + row;
+                        for (int y = 1; y < 16; ++y) m = fmaxf(m, __uint_as_float(x[h + y]));
+                        top = fmaxf(top, fmaf(m, mul, vl));
+                        if (SCORES && row < cols) {
+                            float4* score = quads_of(p, q, g, t) + (int64_t)((hf * HK + k + h) / 4) * (q.n * p.G) + q0 * p.G + row;
 #pragma unroll
-                    for (int k = 0; k < HK; k += 4, score += q.n * p.G) {
-                        const float m = mul[k / 16];
-                        *score = make_float4(__uint_as_float(x[k]) * m, __uint_as_float(x[k + 1]) * m, __uint_as_float(x[k + 2]) * m, __uint_as_float(x[k + 3]) * m);
+                            for (int y = 0; y < 16; y += 4, score += q.n * p.G)
+                                *score = make_float4(__uint_as_float(x[h + y]) * mul, __uint_as_float(x[h + y + 1]) * mul,
+                                                     __uint_as_float(x[h + y + 2]) * mul, __uint_as_float(x[h + y + 3]) * mul);
+                        }
                     }
                 }
                 if (__any_sync(0xffffffffu, ref != -INFINITY && top > ref + GROW)) {
@@ -456,16 +458,22 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_rows_kernel(const __grid_const
                 if (ref == -INFINITY) ref = top;                 // nothing summed yet
                 const float neg = ref == -INFINITY ? 0.f : -ref;
                 float sum = 0.f;
-#pragma unroll
+#pragma unroll 1
                 for (int k = 0; k < HK; k += 32) {               // P over the S columns that have been read
-                    uint32_t w[16];
+                    uint32_t x[32], w[16];
+                    ptx::tmem_ld16_issue(s_at + k, x);
+                    ptx::tmem_ld16_issue(s_at + k + 16, x + 16);
 #pragma unroll
-                    for (int y = 0; y < 32; y += 2) {
-                        const float m = mul[(k + y) / 16], v = vs[(k + y) / 16];
-                        const float e0 = exp2_fast(fmaf(__uint_as_float(x[k + y]), m, neg));
-                        const float e1 = exp2_fast(fmaf(__uint_as_float(x[k + y + 1]), m, neg));
-                        sum += e0 + e1;
-                        w[y / 2] = f16_pair(e0 * v, e1 * v);
+                    for (int h = 0; h < 32; h += 16) {
+                        const float m = mul_at(k + h), v = scales[8 + box_at(k + h)] * P_UP;
+                        ptx::tmem_ld_wait16(x + h);
+#pragma unroll
+                        for (int y = h; y < h + 16; y += 2) {
+                            const float e0 = exp2_fast(fmaf(__uint_as_float(x[y]), m, neg));
+                            const float e1 = exp2_fast(fmaf(__uint_as_float(x[y + 1]), m, neg));
+                            sum += e0 + e1;
+                            w[y / 2] = f16_pair(e0 * v, e1 * v);
+                        }
                     }
                     tmem_st16_words(s_at + k / 2, w);
                 }
