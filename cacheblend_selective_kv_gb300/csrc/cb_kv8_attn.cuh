@@ -1,7 +1,9 @@
 // What the two kernels of attention over the 8-bit cache share: their arguments and the list of tiles that divides the
 // work.  An item is (sequence, tile of QT query rows, KV head), cut into tiles of 128 keys; the tiles of all items form one
-// list, in this order, and every CTA takes an equal, contiguous piece of it.  An item that spans CTAs leaves a partial
-// result per CTA, and the partial results are joined in their order.
+// list, in this order, and every CTA takes an equal, contiguous piece of it.  What an item costs besides its tiles (its Q,
+// its output, a pipeline that runs empty) stands in the list as places before its first tile, so that a CTA of many short
+// items gets fewer of them.  An item that spans CTAs leaves a partial result per CTA, and the partial results are joined
+// in their order.
 #pragma once
 #include <climits>
 
@@ -15,7 +17,7 @@ namespace {
 constexpr int TK = 128;                  // keys per tile
 
 // 16 bytes to shared memory, past L1
-__device__ __forceinline__ void cp_async16(uint32_t dst, const float* src) {
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
@@ -30,7 +32,8 @@ struct AttnArgs {
     unsigned inv_g;                      // ceil(2^16 / G): k / G for k below 2^13
     int kz;                              // z coordinate of this layer's K in the map (V is kz + 1)
     int box;                             // rows of a TMA box: min(page_size, 128)
-    int min_tiles;                       // tiles per CTA, at least
+    int ahead;                           // places before an item's first tile
+    int min_places;                      // places per CTA, at least
     float* part;                         // [cta][2][NC][HD + 2] pieces of items that span CTAs
     unsigned* arrived;                   // [cta] pieces finished of the item that begins in this CTA (0 between calls)
     int* todo;                           // many rows: [cta] what the joining kernel has to do (5 ints)
@@ -65,10 +68,10 @@ __device__ __forceinline__ Seq seq_at(const AttnArgs& p, int s) {
     q.n = r1 - q.r0;
     return q;
 }
-__device__ __forceinline__ int seq_tiles(const AttnArgs& p, const Seq& q) {
+__device__ __forceinline__ int seq_places(const AttnArgs& p, const Seq& q) {
     int t = 0;
 #pragma unroll 1
-    for (int qt = 0; qt < q.q_tiles(p.QT); ++qt) t += q.tiles(qt, p.QT);
+    for (int qt = 0; qt < q.q_tiles(p.QT); ++qt) t += p.ahead + q.tiles(qt, p.QT);
     return t * p.Hkv;
 }
 
@@ -78,7 +81,7 @@ __device__ __forceinline__ float* score_of(const AttnArgs& p, const Seq& q, int 
     return p.scores + ((int64_t)g * p.r.n_rows + q.r0) * p.G * p.score_ld + ((int64_t)t * q.n * p.G + col) * TK;
 }
 
-// A position in the list: item (s, qt, g) and tile t of its nt.
+// A tile in the list: item (s, query tile qt, g) and tile t of its nt.
 struct Cursor {
     int s, qt, g, t, nt;
     Seq q;
@@ -166,29 +169,35 @@ template <typename T> __device__ __forceinline__ void store4(T* o, const float4&
     o[3] = from_f<T>(sees ? a.w * inv : 0.f);
 }
 
-// This CTA's piece of the list: tiles t0 .. t0 + count - 1, `per` for every CTA but the last.
+// This CTA's piece of the list: `per` places for every CTA but the last, `count` tiles among them; the first one's item
+// begins at place `begin`.
 struct Piece {
-    int per, t0, count;
+    int per, begin, count;
+    // the CTA in which an item of nt tiles begins, whose first place is `at`, and how many CTAs have a piece of it
+    __device__ __forceinline__ int first_cta(const AttnArgs& p, int at) const { return (unsigned)(at + p.ahead) / (unsigned)per; }
+    __device__ __forceinline__ int pieces(const AttnArgs& p, int at, int nt) const {
+        return (int)((unsigned)(at + p.ahead + nt - 1) / (unsigned)per) - first_cta(p, at) + 1;
+    }
 };
 struct Find {                            // shared memory of find_piece
-    int s, qt, g, t;
-    Seq q;
+    Cursor cur;
+    int begin, count;
     int sums[32];
 };
 
 // Finds it and the cursor at its first tile, THREADS sequences at a time (the first step's are kept); before and after run
 // around the first barrier, which also publishes what the caller has set up in shared memory.  (The host refuses calls of
-// 2^31 tiles.  This and what ends an item run once or twice per CTA, from instructions that have to be fetched first: short
+// 2^31 places.  This and what ends an item run once or twice per CTA, from instructions that have to be fetched first: short
 // loops and 32-bit arithmetic are worth more here than fewer steps.)
 template <int THREADS, typename F, typename H>
 __device__ __forceinline__ void find_piece(const AttnArgs& p, Find& f, Piece& mine, Cursor& cur, F before_sync, H after_sync) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const Seq q_own = tid < p.q.n ? seq_at(p, tid) : Seq{0, 0, 0};
-    const int t_own = seq_tiles(p, q_own);
+    const int n_own = seq_places(p, q_own);
     {
-        int sum = t_own;
+        int sum = n_own;
 #pragma unroll 1
-        for (int s = tid + THREADS; s < p.q.n; s += THREADS) sum += seq_tiles(p, seq_at(p, s));
+        for (int s = tid + THREADS; s < p.q.n; s += THREADS) sum += seq_places(p, seq_at(p, s));
         sum = __reduce_add_sync(0xffffffffu, sum);
         if (lane == 0) f.sums[warp] = sum;
     }
@@ -196,20 +205,20 @@ __device__ __forceinline__ void find_piece(const AttnArgs& p, Find& f, Piece& mi
     __syncthreads();
     after_sync();
     const int total = __reduce_add_sync(0xffffffffu, lane < THREADS / 32 ? f.sums[lane] : 0);
-    mine.per = max((int)(((unsigned)total + gridDim.x - 1) / gridDim.x), p.min_tiles);
-    const long long t0 = (long long)blockIdx.x * mine.per;
-    mine.t0 = (int)min(t0, (long long)total);
-    mine.count = min(mine.per, total - mine.t0);
-    if (mine.count == 0) return;
-    int base = 0;                                                // tiles of the sequences before this step's
+    mine.per = max((int)(((unsigned)total + gridDim.x - 1) / gridDim.x), p.min_places);
+    mine.count = 0;
+    const long long at = (long long)blockIdx.x * mine.per;
+    if (at >= total) return;
+    const int p0 = (int)at;
+    int base = 0;                                                // places of the sequences before this step's
 #pragma unroll 1
     for (int s0 = 0; s0 < p.q.n; s0 += THREADS) {
         const int s = s0 + tid;
         Seq q = q_own;
-        int n = t_own;
+        int n = n_own;
         if (s0 > 0) {
             q = s < p.q.n ? seq_at(p, s) : Seq{0, 0, 0};
-            n = seq_tiles(p, q);
+            n = seq_places(p, q);
         }
         int x = n;
 #pragma unroll 1
@@ -223,28 +232,37 @@ __device__ __forceinline__ void find_piece(const AttnArgs& p, Find& f, Piece& mi
         const int w = lane < THREADS / 32 ? f.sums[lane] : 0;
         const int before = base + __reduce_add_sync(0xffffffffu, lane < warp ? w : 0) + x - n;
         base += __reduce_add_sync(0xffffffffu, w);
-        if (n > 0 && before <= mine.t0 && mine.t0 < before + n) {
-            int left = mine.t0 - before, qt = 0, nt = q.tiles(0, p.QT);
+        if (n > 0 && before <= p0 && p0 < before + n) {
+            int left = p0 - before;
+            Cursor u{s, 0, 0, 0, 0, q};
+            u.settle(p);
 #pragma unroll 1
-            while (left >= nt * p.Hkv) {
-                left -= nt * p.Hkv;
-                nt = q.tiles(++qt, p.QT);
+            while (left >= (p.ahead + u.nt) * p.Hkv) {
+                left -= (p.ahead + u.nt) * p.Hkv;
+                ++u.qt;
+                u.settle(p);
             }
-            f.s = s;
-            f.qt = qt;
-            f.g = left / nt;
-            f.t = left - f.g * nt;
-            f.q = q;
+            u.g = left / (p.ahead + u.nt);
+            left -= u.g * (p.ahead + u.nt);                      // place within the item
+            f.begin = p0 - left;
+            u.t = max(left - p.ahead, 0);
+            f.cur = u;
+            int count = 0, room = min(mine.per, total - p0) + left;      // places from the item's first one on
+#pragma unroll 1
+            while (true) {                                       // the tiles among them
+                count += max(0, min(u.nt, room - p.ahead) - u.t);
+                room -= p.ahead + u.nt;
+                if (room <= 0) break;
+                u.next_item(p);
+            }
+            f.count = count;
         }
-        if (base > mine.t0) break;
+        if (base > p0) break;
     }
     __syncthreads();
-    cur.s = f.s;
-    cur.qt = f.qt;
-    cur.g = f.g;
-    cur.t = f.t;
-    cur.q = f.q;
-    cur.settle(p);
+    cur = f.cur;
+    mine.begin = f.begin;
+    mine.count = f.count;
 }
 
 // byte `b` of row `row` of a tile of codes: rows of ROW bytes in the ROW-byte swizzle

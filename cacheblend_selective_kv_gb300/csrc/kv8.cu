@@ -274,8 +274,8 @@ cb_status cb_kv8_attention(cb_kv8* c, const cb_kv8_seqs* seqs, int32_t layer, co
             return fail(CB_ERR_INVALID_ARG, "%s: returning weights needs %.0f cells, the cache was created with %lld", who,
                         (double)rows * (double)row, (long long)c->cfg.weight_cells);
     }
-    // tiles of 128 keys and at least one query row, of every KV head
-    if (((int64_t)n_q + sq.n) * c->cfg.n_kv_heads > 0x7fffffff / ((int64_t)sq.max_len / 128 + 2))
+    // tiles of 128 keys and at least one query row, of every KV head, and what an item counts besides
+    if (((int64_t)n_q + sq.n) * c->cfg.n_kv_heads > 0x7fffffff / ((int64_t)sq.max_len / 128 + 8))
         return fail(CB_ERR_UNSUPPORTED, "%s: %d query rows over %d keys are too many for one call", who, n_q, sq.max_len);
     if (sq.n == 0 || (n_q == 0 && !weights)) return CB_OK;
     OnDevice on;

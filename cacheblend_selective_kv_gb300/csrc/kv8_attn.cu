@@ -271,7 +271,6 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
     Piece mine;
     Cursor cur;
     find_piece<THREADS>(p, c.find, mine, cur, [] { ptx::tc_fence_before(); }, [] { ptx::tc_fence_after(); });
-    const int per = mine.per, t0 = mine.t0;
     const int count = mine.count;                        // tiles of this CTA
     const uint32_t tmem = c.tmem;
 
@@ -341,7 +340,7 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
             q_terms<T, S>(p, u, sQ + buf * S::Q_BYTES, qscale + buf * NC, to_exp2);
             if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&c.q_full));
         };
-        int item = 0, n_open = 0;
+        int item = 0, n_open = 0, begin = mine.begin;             // the item's first place in the list
         Cursor next;
         for (int i = 0; i < count; ++item) {
             const int first = cur.t, n_here = min(cur.nt - first, count - i), g = cur.g;
@@ -543,8 +542,7 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
             } else {
                 // A piece.  It is announced, and joined if it was the last, when the CTA has done all its tiles: here every warp
                 // would wait for the fence and the count (decode of 64 x 8K: 100.5 us that way, 96 this way).
-                const int begin = t0 + (i - n_here) - first;           // the item's first tile in the list
-                const int u0 = (unsigned)begin / (unsigned)per, n_pieces = (int)((unsigned)(begin + cur.nt - 1) / (unsigned)per) - u0 + 1;
+                const int u0 = mine.first_cta(p, begin), n_pieces = mine.pieces(p, begin, cur.nt);
                 float* piece = piece_at<S>(p, u0, blockIdx.x - u0);
                 if (key < HD) {
 #pragma unroll
@@ -558,6 +556,7 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
                 if (tid == 0) c.open[n_open] = Open{u0, n_pieces, q.r0 + q0, cols, pos0, g};
                 ++n_open;
             }
+            begin += p.ahead + cur.nt;
             if (i < count) cur = next;
         }
         if (n_open > 0) {
@@ -636,6 +635,8 @@ cudaError_t launch_shape(const Kv8& c, AttnArgs& p, cudaStream_t s) {
     const cudaError_t e = smem_limit_once(kv8_attn_kernel<T, S>, S::BYTES, done);
     if (e != cudaSuccess) return e;
     p.QT = S::NC / p.G;
+    p.ahead = 2;
+    p.min_places = 2 + p.ahead;
     const int64_t items = ((int64_t)p.r.n_rows / p.QT + p.q.n) * p.Hkv;
     const int64_t tiles = items * ((p.q.max_len + TK - 1) / TK + 1);
     const int64_t most = (int64_t)c.num_sms * S::CTAS;
@@ -708,7 +709,6 @@ cudaError_t launch_kv8_attention(const Kv8& c, const Kv8Seqs& q, const Kv8Rows& 
     p.inv_g = (65536 + p.G - 1) / p.G;
     p.kz = 2 * layer;
     p.box = c.cfg.page_size < TK ? c.cfg.page_size : TK;
-    p.min_tiles = 2;
     p.part = c.part;
     p.arrived = c.arrived;
     p.scores = a.weights && q.max_len > 0 ? c.scores : nullptr;      // (no keys: no weights to return)

@@ -195,21 +195,25 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_rows_kernel(const __grid_const
                 ++item;
                 const bf16* qbase = (const bf16*)p.a.q + (int64_t)(q.r0 + q0) * p.a.q_stride + (int64_t)cur.g * p.G * HD;
                 constexpr int QL = HD / 8, QR = 32 / QL;         // lanes of a row (8 values each), rows of a warp
-                const auto q_of = [&](int r) {
-                    return r < cols ? *reinterpret_cast<const uint4*>(qbase + (int64_t)div_g(p, r) * p.a.q_stride + mod_g(p, r) * HD + lane % QL * 8)
-                                    : make_uint4(0, 0, 0, 0);
-                };
-                uint4 val = q_of(w * QR + lane / QL), next = q_of((4 + w) * QR + lane / QL);
-                // once the products with the item before's Q are done; then the softmax is past tile i - 3, hence past the item whose
-                // marks and row scales these were
+                // Once the products with the item before's Q are done; then the softmax is past tile i - 3, hence past the item
+                // whose marks and row scales these were.  Q lands where it will stand and is converted in place, by the thread
+                // that has asked for it (all of it under way at once; two rows ahead in registers cost an item 1.5 us more).
                 if (i > 0) ptx::mbar_wait(ptx::smem_u32(&c.k_empty[(i - 1) & 1]), ((i - 1) >> 1) & 1, abort, status);
+                const int r0 = w * QR + lane / QL;
+#pragma unroll 1
+                for (int r = r0; r < ROWS; r += 4 * QR) {
+                    uint8_t* to = sQ + wide_at(r, lane % QL);
+                    if (r < cols) cp_async16(ptx::smem_u32(to), qbase + (int64_t)div_g(p, r) * p.a.q_stride + mod_g(p, r) * HD + lane % QL * 8);
+                    else *reinterpret_cast<uint4*>(to) = make_uint4(0, 0, 0, 0);
+                }
                 if (t < HD) nan_marks[(item % MARKS) * HD + t] = INT_MAX;
                 if (t == 0) c.any_nan[item % MARKS] = 0;
+                asm volatile("cp.async.wait_all;" ::: "memory");
 #pragma unroll 1
-                for (int r = w * QR + lane / QL; r < ROWS; r += 4 * QR) {
+                for (int r = r0; r < ROWS; r += 4 * QR) {
+                    uint4* at = reinterpret_cast<uint4*>(sQ + wide_at(r, lane % QL));
+                    const uint4 val = *at;
                     const uint32_t word[4] = {val.x, val.y, val.z, val.w};
-                    val = next;
-                    next = q_of(r + 8 * QR);                     // two steps ahead
                     float f[8], top = 0.f;
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
@@ -225,7 +229,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_rows_kernel(const __grid_const
                     uint32_t o[4];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) o[k] = f16_pair(f[2 * k] * up, f[2 * k + 1] * up);
-                    *reinterpret_cast<uint4*>(sQ + wide_at(r, lane % QL)) = make_uint4(o[0], o[1], o[2], o[3]);
+                    *at = make_uint4(o[0], o[1], o[2], o[3]);
                     if (lane % QL == 0) row_scale[(item % MARKS) * ROWS + r] = sc * (1.f / 64.f);
                 }
                 fence_async_smem();
@@ -367,7 +371,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_rows_kernel(const __grid_const
         const float to_exp2 = fabsf(p.a.scale) * 1.4426950408889634f;
         const int box_shift = min(p.q.shift, 7);
         Todo todo{0, 0, 0, 0, 0};
-        int item = 0;
+        int item = 0, begin = mine.begin;                        // the item's first place in the list
         for (int i = 0; i < count; ++item) {
             const int first = cur.t, n_here = min(cur.nt - first, count - i), g = cur.g;
             const Seq q = cur.q;
@@ -494,8 +498,8 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_rows_kernel(const __grid_const
             const float f0 = hf == 0 ? f_own : f_other, f1 = hf == 0 ? f_other : f_own;
             const float L = hf == 0 ? l * f_own + other.y * f_other : other.y * f_other + l * f_own;
             const bool whole = first == 0 && n_here == cur.nt;
-            const int begin = mine.t0 + (i - n_here) - first;          // the item's first tile in the list
-            const int u0 = (unsigned)begin / (unsigned)mine.per, n_pieces = (int)((unsigned)(begin + cur.nt - 1) / (unsigned)mine.per) - u0 + 1;
+            const int u0 = mine.first_cta(p, begin), n_pieces = mine.pieces(p, begin, cur.nt);
+            begin += p.ahead + cur.nt;
             const auto piece_at = [&](int u) { return p.part + (int64_t)((u0 + u) * 2 + (u == 0 ? 1 : 0)) * S::PIECE; };
             const auto out_at = [&](int r) {
                 return (bf16*)p.a.out + (int64_t)(q.r0 + q0 + div_g(p, r)) * p.a.out_stride + (int64_t)(g * p.G + mod_g(p, r)) * HD;
@@ -616,6 +620,8 @@ template <int HD, bool SCORES> cudaError_t launch_dim(const Kv8& c, AttnArgs& p,
     const cudaError_t e = smem_limit_once(kv8_rows_kernel<HD, SCORES>, Rows<HD>::BYTES, done);
     if (e != cudaSuccess) return e;
     p.QT = ROWS / p.G;
+    p.ahead = 4;
+    p.min_places = 1 + p.ahead;
     const int64_t items = ((int64_t)p.r.n_rows / p.QT + p.q.n) * p.Hkv;
     const int64_t tiles = items * ((p.q.max_len + TK - 1) / TK + 1);
     CUtensorMap map;

@@ -359,7 +359,7 @@ cb_status cb_kv8_read(cb_kv8* cache, const cb_kv8_seqs* seqs, int32_t layer, int
  *                0 .. len - 1 (others are left as they were); add != 0 adds to what stands there.  What cb_kv8_evict
  *                ranks by: written once for a query window, or added up over decoding steps.
  * NaN behind what a row sees (in a later row's K or V, or behind the sequence) does not reach it.
- * (n_q + n_seqs) * n_kv_heads * (max_len / 128 + 2) has to stay below 2^31 (else CB_ERR_UNSUPPORTED).
+ * (n_q + n_seqs) * n_kv_heads * (max_len / 128 + 8) has to stay below 2^31 (else CB_ERR_UNSUPPORTED).
  * Every sum runs in a fixed order: the same call gives the same bits.  Async on `stream`; no allocation. */
 cb_status cb_kv8_attention(cb_kv8* cache, const cb_kv8_seqs* seqs, int32_t layer, const void* q, int64_t q_stride,
                            const int32_t* q_start, int32_t n_q, float scale, void* out, int64_t out_stride,
