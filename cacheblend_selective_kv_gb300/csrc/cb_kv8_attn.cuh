@@ -169,21 +169,24 @@ template <typename T> __device__ __forceinline__ void store4(T* o, const float4&
     o[3] = from_f<T>(sees ? a.w * inv : 0.f);
 }
 
-// This CTA's piece of the list: `per` places for every CTA but the last, `count` tiles among them; the first one's item
-// begins at place `begin`.
+// This CTA's piece of the list: `per` places for every CTA but the last, `count` tiles among them.
 struct Piece {
-    int per, begin, count;
-    // the CTA in which an item of nt tiles begins, whose first place is `at`, and how many CTAs have a piece of it
-    __device__ __forceinline__ int first_cta(const AttnArgs& p, int at) const { return (unsigned)(at + p.ahead) / (unsigned)per; }
-    __device__ __forceinline__ int pieces(const AttnArgs& p, int at, int nt) const {
-        return (int)((unsigned)(at + p.ahead + nt - 1) / (unsigned)per) - first_cta(p, at) + 1;
-    }
+    int per, count;
 };
 struct Find {                            // shared memory of find_piece
     Cursor cur;
-    int begin, count;
+    int begin, count;                    // place at which the first tile's item begins
     int sums[32];
 };
+// Of an item of nt tiles, of which this CTA has n_here from tile `first` on but not all: the CTA it begins in, and how many
+// CTAs have a piece of it.  One that began before is this CTA's first; of one that begins here the others have what is left.
+__device__ __forceinline__ int first_cta(const AttnArgs& p, const Find& f, int per, int first) {
+    return first > 0 ? (int)((unsigned)(f.begin + p.ahead) / (unsigned)per) : (int)blockIdx.x;
+}
+__device__ __forceinline__ int piece_count(const AttnArgs& p, const Find& f, int per, int first, int n_here, int nt) {
+    const unsigned rest = first > 0 ? (unsigned)(f.begin + p.ahead) % (unsigned)per + nt : (unsigned)(per + nt - n_here);
+    return (int)((rest + per - 1) / (unsigned)per);
+}
 
 // Finds it and the cursor at its first tile, THREADS sequences at a time (the first step's are kept); before and after run
 // around the first barrier, which also publishes what the caller has set up in shared memory.  (The host refuses calls of
@@ -261,7 +264,6 @@ __device__ __forceinline__ void find_piece(const AttnArgs& p, Find& f, Piece& mi
     }
     __syncthreads();
     cur = f.cur;
-    mine.begin = f.begin;
     mine.count = f.count;
 }
 

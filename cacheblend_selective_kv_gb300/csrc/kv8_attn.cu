@@ -112,6 +112,7 @@ struct Shared {
     uint32_t tmem;
     int abort;
     Find find;
+    Cursor next;                         // the softmax warps' next item
     Open open[2];                        // at the beginning of this CTA's tiles, at their end
     int last[2];                         // this CTA joins it
 };
@@ -340,8 +341,7 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
             q_terms<T, S>(p, u, sQ + buf * S::Q_BYTES, qscale + buf * NC, to_exp2);
             if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&c.q_full));
         };
-        int item = 0, n_open = 0, begin = mine.begin;             // the item's first place in the list
-        Cursor next;
+        int item = 0, n_open = 0;
         for (int i = 0; i < count; ++item) {
             const int first = cur.t, n_here = min(cur.nt - first, count - i), g = cur.g;
             const Seq q = cur.q;
@@ -503,9 +503,10 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
                 if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&c.p_full));
                 // (S of this item's first tile is there, so its own Q has been taken and the barrier is a phase behind)
                 if (t == first && i + n_here < count + t - first) {
-                    next = cur;
+                    Cursor next = cur;
                     next.next_item(p);
                     write_q(next, (item + 1) & 1);
+                    if (tid == 0) c.next = next;                 // (kept there: registers are short in the tile loop)
                 }
             }
             add_tile(i - 1);
@@ -542,7 +543,7 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
             } else {
                 // A piece.  It is announced, and joined if it was the last, when the CTA has done all its tiles: here every warp
                 // would wait for the fence and the count (decode of 64 x 8K: 100.5 us that way, 96 this way).
-                const int u0 = mine.first_cta(p, begin), n_pieces = mine.pieces(p, begin, cur.nt);
+                const int u0 = first_cta(p, c.find, mine.per, first), n_pieces = piece_count(p, c.find, mine.per, first, n_here, cur.nt);
                 float* piece = piece_at<S>(p, u0, blockIdx.x - u0);
                 if (key < HD) {
 #pragma unroll
@@ -556,8 +557,7 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
                 if (tid == 0) c.open[n_open] = Open{u0, n_pieces, q.r0 + q0, cols, pos0, g};
                 ++n_open;
             }
-            begin += p.ahead + cur.nt;
-            if (i < count) cur = next;
+            if (i < count) cur = c.next;                         // written before the last barrier, again behind the next
         }
         if (n_open > 0) {
             ptx::named_bar_sync(1, SOFT);
@@ -635,7 +635,7 @@ cudaError_t launch_shape(const Kv8& c, AttnArgs& p, cudaStream_t s) {
     const cudaError_t e = smem_limit_once(kv8_attn_kernel<T, S>, S::BYTES, done);
     if (e != cudaSuccess) return e;
     p.QT = S::NC / p.G;
-    p.ahead = 2;
+    p.ahead = 2;                         // (64 x 8K decode 102 us with 0, 100 with 1, 98 with 2 and 3)
     p.min_places = 2 + p.ahead;
     const int64_t items = ((int64_t)p.r.n_rows / p.QT + p.q.n) * p.Hkv;
     const int64_t tiles = items * ((p.q.max_len + TK - 1) / TK + 1);
