@@ -598,7 +598,7 @@ class KV8Cache:
         if out_rows is None:
             out_rows = table.new_empty((n_layers, n, self.n_kv_heads, max(int(n_keep), 0)))
         ld = weights.shape[-1]
-        for t, name in ((weights, "weights"), (out_weights, "out_weights")):
+        for t, name in ((weights, "weights"),) if out_weights is weights else ((weights, "weights"), (out_weights, "out_weights")):
             if t.dtype is not self._f32 or t.get_device() != self._dev or not t.is_contiguous() or \
                     t.shape != (n_layers, n, self.n_kv_heads, ld):
                 raise ValueError(f"{name} must be contiguous float32 [{n_layers}][{n}][{self.n_kv_heads}][rows] on {self.device}")

@@ -654,7 +654,9 @@ template <int HD> using F4 = Shape<HD, 4, 1, 6, 6, 2, 3>;
 template <int HD> using F8 = Shape<HD, 8, 1, 6, 6, 2, 2>;
 
 template <int HD> cudaError_t launch_dim(const Kv8& c, AttnArgs& p, cudaStream_t s) {
-    // query columns per item: what a sequence's rows need on average, within what tensor memory holds
+    // Query columns per item: what a sequence's rows need on average, within what tensor memory holds.  Fewer columns leave
+    // room for more CTAs on an SM and shorter tiles, too few double the tiles (64 x 8K, us with shapes of 4 / 8 / 16 / 32: 4 columns
+    // 167 / 171 / 188 / 328, 8 columns 322 / 175 / 192 / 334, 16 columns 626 / 328 / 195 / 335).
     const int rows = (p.r.n_rows + p.q.n - 1) / p.q.n, need = rows * p.G;
     if (c.cfg.dtype == CB_BF16) {
         if (need <= 4) return launch_shape<bf16, C4<HD>>(c, p, s);
@@ -716,13 +718,19 @@ cudaError_t launch_kv8_attention(const Kv8& c, const Kv8Seqs& q, const Kv8Rows& 
     p.score_ld = (q.max_len + TK - 1) / TK * TK;
     if (r.n_rows > 0) {
         const int rows = (r.n_rows + q.n - 1) / q.n;             // of a sequence, on average
+        // Up to 32 columns of a sequence stand in one item here, and beyond that keys and values are read and P is formed once
+        // per item of 32 (64 sequences of 2K: 32 columns 112 us here, 132 there; 48 columns 206 here, 133 there).
         const bool many = c.cfg.dtype == CB_BF16 && rows * p.G > 32;
         if (many) return launch_kv8_rows(c, &p, s);              // sums its weights too
         const cudaError_t e = c.cfg.head_dim == 128 ? launch_dim<128>(c, p, s) : launch_dim<64>(c, p, s);
         if (e != cudaSuccess) return e;
     }
     if (a.weights && q.max_len > 0) {
-        const int split = r.n_rows > 4 * q.n ? 8 : 1;            // rows of a sequence, on average
+        // A block sums 128 keys of a head.  Few blocks with several columns each: eight sums side by side (one sequence of 4K, 8
+        // rows: 23.7 us against 28.2 in all, 64 fp32 rows 66.5 against 115).  Many blocks fill the SMs as they are (16 sequences,
+        // 8 rows: 83 us, 114 split).
+        const int64_t blocks = (int64_t)((q.max_len + TK - 1) / TK) * Hkv * q.n;
+        const int split = blocks <= 4 * c.num_sms && (int64_t)r.n_rows * p.G > 8 * (int64_t)q.n ? 8 : 1;
         return launch_ex(c.pdl, kv8_weights_kernel, dim3((q.max_len + TK - 1) / TK, Hkv, q.n), dim3(TK, split), 0, s, p);
     }
     return cudaSuccess;
