@@ -27,6 +27,10 @@
 // tile's sum its own.  P is stored [key][column], the B operand MN-major, so that a thread's terms are a few vector
 // stores instead of a byte store for each; what belongs to a column (its maximum, its factors) is computed by one lane
 // per warp and read back from shared memory.
+//
+// Measured (32 heads, 8 KV heads of 128, bf16): 64 sequences of up to 8K keys, each its own length, 96 us, 89 % of the measured
+// copy rate; 64 x 8192 keys 167 us, 95 %; 1 x 131071 keys 54 us, 74 %; 1 x 200 keys 7 us.  Bound by HBM in the long run (the
+// difference between two lengths is read at the copy rate), with about 7 us for the launch, the first tile and the end.
 #include <cudaTypedefs.h>
 
 #include <algorithm>

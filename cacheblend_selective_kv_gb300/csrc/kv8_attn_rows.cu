@@ -16,7 +16,9 @@
 //
 // Each of the two halves of a tile's keys has its own R, sum and O (as the blend's attention kernel does, so that the warps
 // of a row need not meet for every tile); they are joined at the end of an item.  Per tile and SM: 32 MMAs of 128 x 128 x 16
-// at about 99 cycles, 128 x 128 exponentials, 2 x 128 x HD conversions.
+// at about 99 cycles, 128 x 128 exponentials, 2 x 128 x HD conversions; about 3900 cycles a tile, bound by the softmax warps'
+// chain (two warps a scheduler, 1.2 instructions a cycle) and not by the matrix unit.  2048 rows over 8K: 382 us, 33 % of
+// the measured bf16 rate; the 64 rows of a query over 8K: 33 us, 50 us with weights.
 #include <cstring>
 
 #include "cb_kv8_attn.cuh"

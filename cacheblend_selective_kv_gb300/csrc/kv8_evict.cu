@@ -12,7 +12,7 @@
 //            pages in order and nothing is overwritten before it is read.
 // The moved rows are most of the bytes: move is bound by HBM, at the latency of rows -> table -> codes, which many
 // small CTAs (or, in place, the next page's addresses fetched ahead) cover.  8K to 2K rows, 32 layers x 8 heads of 128: select
-// 19 us, move 51 us for 268 MB of kept codes (5.3 TB/s; a kept row is 128 scattered bytes).  Fewer CTAs per SM, the next
+// 19 us, move 51 us for 268 MB of kept codes read and written (5.3 TB/s; a kept row is 128 scattered bytes).  Fewer CTAs per SM, the next
 // page's codes loaded ahead and fewer instructions per code were all slower (72 .. 100 us in all against 70).
 #include <climits>
 
