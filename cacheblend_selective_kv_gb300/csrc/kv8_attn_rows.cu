@@ -563,25 +563,23 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_rows_kernel(const __grid_const
     }
 }
 
-// The items that span CTAs, a row per warp: block (u, y) has rows y, y + gridDim.y, .. (8 at a time) of the item that begins
-// in CTA u.  A kernel of its own, because a piece is 128 rows: joined by the CTA that ends last, the 64 rows of a query over
-// 8K took 15 us of one CTA's time.
+// The items that span CTAs, a row per warp: block (u, y) has rows 8 y .. 8 y + 7 of the item that begins in CTA u.  A kernel
+// of its own, because a piece is 128 rows: joined by the CTA that ends last, the 64 rows of a query over 8K took 15 us of
+// one CTA's time, and with two rows per warp 1 us more than this way.
 template <int HD>
 __global__ void __launch_bounds__(256) kv8_join_kernel(const AttnArgs p) {
+    __shared__ float4 buf[8][8 * 32];
     grid_dep_launch();
     grid_dep_wait();
     const Todo d = reinterpret_cast<const Todo*>(p.todo)[blockIdx.x];
-    if (d.pieces == 0) return;
-    __shared__ float4 buf[8][8 * 32];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, u0 = blockIdx.x;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, u0 = blockIdx.x, k = blockIdx.y * 8 + warp;
+    if (d.pieces == 0 || k >= d.cols) return;
     const auto piece_at = [&](int u) { return p.part + (int64_t)((u0 + u) * 2 + (u == 0 ? 1 : 0)) * Rows<HD>::PIECE; };
-    for (int k = blockIdx.y * 8 + warp; k < d.cols; k += gridDim.y * 8) {
-        float m, l;
-        const float4 a = join_pieces<HD, 8>(piece_at, d.pieces, k * HD, ROWS * HD + 2 * k, m, l, buf[warp]);
-        bf16* out = (bf16*)p.a.out + (int64_t)(d.row0 + div_g(p, k)) * p.a.out_stride + (int64_t)(d.g * p.G + mod_g(p, k)) * HD;
-        if (lane < HD / 4) store4(out + lane * 4, a, 1.f / l, d.pos0 + div_g(p, k) >= 0);
-        if (p.scores && lane == 0) p.stats[((int64_t)d.g * p.r.n_rows + d.row0) * p.G + k] = make_float2(m, 1.f / l);
-    }
+    float m, l;
+    const float4 a = join_pieces<HD, 8>(piece_at, d.pieces, k * HD, ROWS * HD + 2 * k, m, l, buf[warp]);
+    bf16* out = (bf16*)p.a.out + (int64_t)(d.row0 + div_g(p, k)) * p.a.out_stride + (int64_t)(d.g * p.G + mod_g(p, k)) * HD;
+    if (lane < HD / 4) store4(out + lane * 4, a, 1.f / l, d.pos0 + div_g(p, k) >= 0);
+    if (p.scores && lane == 0) p.stats[((int64_t)d.g * p.r.n_rows + d.row0) * p.G + k] = make_float2(m, 1.f / l);
 }
 
 // weights[s][g][j] = sum over the sequence's rows and the group's heads of exp2(score - max) / sum: four keys per warp, the
@@ -630,7 +628,7 @@ template <int HD, bool SCORES> cudaError_t launch_dim(const Kv8& c, AttnArgs& p,
     memcpy(&map, c.map, sizeof map);
     const unsigned ctas = (unsigned)(tiles < c.num_sms ? tiles : c.num_sms);
     cudaError_t err = launch_ex(c.pdl, kv8_rows_kernel<HD, SCORES>, dim3(ctas), dim3(THREADS), Rows<HD>::BYTES, s, map, p);
-    if (err == cudaSuccess) err = launch_ex(c.pdl, kv8_join_kernel<HD>, dim3(ctas, 8), dim3(256), 0, s, p);
+    if (err == cudaSuccess) err = launch_ex(c.pdl, kv8_join_kernel<HD>, dim3(ctas, ROWS / 8), dim3(256), 0, s, p);
     if (err == cudaSuccess && SCORES)
         err = launch_ex(c.pdl, kv8_rows_weights_kernel, dim3((p.q.max_len + 31) / 32, p.Hkv, p.q.n), dim3(256), 0, s, p);
     return err;
