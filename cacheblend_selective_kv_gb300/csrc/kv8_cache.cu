@@ -62,7 +62,7 @@ __device__ __forceinline__ bool kv8_block(const Kv8Seqs& q, const Kv8Rows& r, in
     const int n = r1 - r0;
     if (n == 0) return false;
     if (n > len) {
-        atomicOr(q.status, ST_BAD_ROW);
+        if (len > 0) atomicOr(q.status, ST_BAD_ROW);   // (no length: a free place of the batch)
         return false;
     }
     const int P = 1 << q.shift, first = len - n;

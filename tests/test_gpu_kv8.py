@@ -711,6 +711,45 @@ def test_other_stream_and_graph(cb):
     c.done()
 
 
+def test_free_places_of_a_captured_batch(cb):
+    """A decoding step captured for four places, of which some are free at each replay: length 0, a table of no pages."""
+    H, G, hd, P = 2, 4, 64, 16
+    c = Case(cb, [20, 30, 15, 33], H=H, G=G, hd=hd, P=P, seed=41, spare=10, cells=cb.KV8Cache.cells(4, 8, 43))
+    kv, kv64 = c.values(1, 4, H, hd)
+    q, q64 = c.values(4, H * G, hd)
+    lens, table, out = c.lens_t.clone(), c.table.clone(), torch.empty_like(q)
+    w, rows, kept = torch.zeros((1, 4, H, 48), device="cuda"), i32(np.zeros((1, 4, H, 40))), i32([0] * 4)
+    g = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        c.cache.write(table, lens, kv, kv, max_len=43)
+        c.cache.attention(table, lens, q, out, weights=w[0], max_len=43)
+        c.cache.evict(table, lens, table, w, 40, 1, 2, out_rows=rows, out_lens=kept, max_len=43)
+    now = [20, 30, 15, 33]
+    for free in ([1], [0, 2, 3], [], [0, 1, 2, 3], [2]):
+        t = c.table_np.copy()
+        t[free] = -5
+        step = [0 if s in free else now[s] + 1 for s in range(4)]
+        lens.copy_(i32(step))
+        table.copy_(i32(t))
+        out.fill_(9.0)
+        g.replay()
+        torch.cuda.synchronize()
+        c.lens = step
+        for s in range(4):
+            if s in free:
+                assert torch.count_nonzero(out[s]) == 0 and kept[s].item() == 0 and torch.all(rows[0, s] == -1)
+            else:
+                c.model.write(c.table_np[s:s + 1], step[s:s + 1], kv64[:, s:s + 1], kv64[:, s:s + 1], [0, 1])
+                now[s] += 1
+                assert kept[s].item() == step[s]
+        check_attention(c, q, q64, [0, 1, 2, 3, 4], out)
+        for s in set(range(4)) - set(free):             # all rows stay, quantised anew
+            c.model.evict(c.table_np[s:s + 1], step[s:s + 1], c.table_np[s:s + 1], np.zeros((1, 1, H, 48), np.float32), 40, 1, 2)
+        c.check_pool()
+    c.done()
+
+
 def test_python_refusals(cb):
     c = Case(cb, [40, 20], H=2, G=2, hd=64, P=16, seed=1)
     q = torch.zeros((2, 4, 64), dtype=torch.bfloat16, device="cuda")
