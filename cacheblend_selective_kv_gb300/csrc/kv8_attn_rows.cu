@@ -16,9 +16,9 @@
 //
 // Each of the two halves of a tile's keys has its own R, sum and O (as the blend's attention kernel does, so that the warps
 // of a row need not meet for every tile); they are joined at the end of an item.  Per tile and SM: 32 MMAs of 128 x 128 x 16
-// at about 99 cycles, 128 x 128 exponentials, 2 x 128 x HD conversions; about 3900 cycles a tile, bound by the softmax warps'
-// chain (two warps a scheduler, 1.2 instructions a cycle) and not by the matrix unit.  2048 rows over 8K: 382 us, 33 % of
-// the measured bf16 rate; the 64 rows of a query over 8K: 33 us, 50 us with weights.
+// at about 99 cycles, 128 x 128 exponentials, 2 x 128 x HD conversions; about 3800 cycles a tile, bound by the softmax warps'
+// chain (two warps a scheduler, 1.2 instructions a cycle) and not by the matrix unit.  2048 rows over 8K: 371 us, 34 % of
+// the measured bf16 rate; the 64 rows of a query over 8K: 32 us, 48 us with weights.
 #include <cstring>
 
 #include "cb_kv8_attn.cuh"
@@ -82,12 +82,10 @@ __device__ __forceinline__ void mma_f16_tmem_a(uint32_t d, uint32_t a, uint64_t 
         ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc)
         : "memory");
 }
-__device__ __forceinline__ void tmem_st16_words(uint32_t addr, const uint32_t* v) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};"
-        ::"r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]),
-          "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
-        : "memory");
+__device__ __forceinline__ void tmem_st8_words(uint32_t addr, const uint32_t* v) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+                 ::"r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
 }
 __device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
     const __nv_bfloat162 t = __floats2bfloat162_rn(a, b);
@@ -415,31 +413,27 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_rows_kernel(const __grid_const
                     }
                     ptx::tmem_wait_st();
                 }
-                // Both passes read S in steps of 32 keys, as loops: unrolled over the half's 64 keys their instructions took longer
-                // to fetch than what the second read costs.
+                // Both passes read S in steps of 16 keys, as loops: the fewer instructions the warps of the SM go through, the less
+                // they wait for them, which is more than the second read and the steps' latency cost (2048 rows over 8K: one
+                // pass unrolled over 64 keys 467 us, steps of 32 keys 382, of 16 371).
                 float top = -INFINITY;                           // the largest of score + log2 of V's scale
 #pragma unroll 1
-                for (int k = 0; k < HK; k += 32) {
-                    uint32_t x[32];
+                for (int k = 0; k < HK; k += 16) {
+                    uint32_t x[16];
                     ptx::tmem_ld16_issue(s_at + k, x);
-                    ptx::tmem_ld16_issue(s_at + k + 16, x + 16);
+                    const float v = scales[8 + box_at(k)], mul = mul_at(k);
+                    const float vl = v > 0.f ? fmaxf((float)((int)(__float_as_uint(v) >> 23) - 127), -100.f) : -100.f;
+                    ptx::tmem_ld_wait16(x);
+                    float m = __uint_as_float(x[0]);
 #pragma unroll
-                    for (int h = 0; h < 32; h += 16) {
-                        const float v = scales[8 + box_at(k + h)];
-                        const float vl = v > 0.f ? fmaxf((float)((int)(__float_as_uint(v) >> 23) - 127), -100.f) : -100.f;
-                        const float mul = mul_at(k + h);
-                        ptx::tmem_ld_wait16(x + h);
-                        float m = __uint_as_float(x[h]);
+                    for (int y = 1; y < 16; ++y) m = fmaxf(m, __uint_as_float(x[y]));
+                    top = fmaxf(top, fmaf(m, mul, vl));
+                    if (SCORES && row < cols) {
+                        float4* score = quads_of(p, q, g, t) + (int64_t)((hf * HK + k) / 4) * (q.n * p.G) + q0 * p.G + row;
 #pragma unroll
-                        for (int y = 1; y < 16; ++y) m = fmaxf(m, __uint_as_float(x[h + y]));
-                        top = fmaxf(top, fmaf(m, mul, vl));
-                        if (SCORES && row < cols) {
-                            float4* score = quads_of(p, q, g, t) + (int64_t)((hf * HK + k + h) / 4) * (q.n * p.G) + q0 * p.G + row;
-#pragma unroll
-                            for (int y = 0; y < 16; y += 4, score += q.n * p.G)
-                                *score = make_float4(__uint_as_float(x[h + y]) * mul, __uint_as_float(x[h + y + 1]) * mul,
-                                                     __uint_as_float(x[h + y + 2]) * mul, __uint_as_float(x[h + y + 3]) * mul);
-                        }
+                        for (int y = 0; y < 16; y += 4, score += q.n * p.G)
+                            *score = make_float4(__uint_as_float(x[y]) * mul, __uint_as_float(x[y + 1]) * mul, __uint_as_float(x[y + 2]) * mul,
+                                                 __uint_as_float(x[y + 3]) * mul);
                     }
                 }
                 if (__any_sync(0xffffffffu, ref != -INFINITY && top > ref + GROW)) {
@@ -465,23 +459,19 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_rows_kernel(const __grid_const
                 const float neg = ref == -INFINITY ? 0.f : -ref;
                 float sum = 0.f;
 #pragma unroll 1
-                for (int k = 0; k < HK; k += 32) {               // P over the S columns that have been read
-                    uint32_t x[32], w[16];
+                for (int k = 0; k < HK; k += 16) {               // P over the S columns that have been read
+                    uint32_t x[16], w[8];
                     ptx::tmem_ld16_issue(s_at + k, x);
-                    ptx::tmem_ld16_issue(s_at + k + 16, x + 16);
+                    const float m = mul_at(k), v = scales[8 + box_at(k)] * P_UP;
+                    ptx::tmem_ld_wait16(x);
 #pragma unroll
-                    for (int h = 0; h < 32; h += 16) {
-                        const float m = mul_at(k + h), v = scales[8 + box_at(k + h)] * P_UP;
-                        ptx::tmem_ld_wait16(x + h);
-#pragma unroll
-                        for (int y = h; y < h + 16; y += 2) {
-                            const float e0 = exp2_fast(fmaf(__uint_as_float(x[y]), m, neg));
-                            const float e1 = exp2_fast(fmaf(__uint_as_float(x[y + 1]), m, neg));
-                            sum += e0 + e1;
-                            w[y / 2] = f16_pair(e0 * v, e1 * v);
-                        }
+                    for (int y = 0; y < 16; y += 2) {
+                        const float e0 = exp2_fast(fmaf(__uint_as_float(x[y]), m, neg));
+                        const float e1 = exp2_fast(fmaf(__uint_as_float(x[y + 1]), m, neg));
+                        sum += e0 + e1;
+                        w[y / 2] = f16_pair(e0 * v, e1 * v);
                     }
-                    tmem_st16_words(s_at + k / 2, w);
+                    tmem_st8_words(s_at + k / 2, w);
                 }
                 l += sum;
                 ptx::tmem_wait_st();
