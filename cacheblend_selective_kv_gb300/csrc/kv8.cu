@@ -87,7 +87,9 @@ cb_status check_blocks(const cb_kv8& c, const Kv8Seqs& q, const Kv8Rows& r, cons
 }
 
 cb_status cuda_result(cudaError_t e, const char* who) {
-    return e == cudaSuccess ? CB_OK : fail(CB_ERR_CUDA, "%s: %s", who, cudaGetErrorString(e));
+    if (e == cudaSuccess) return CB_OK;
+    cudaGetLastError();                                // a refused launch is reported here, not by the caller's next call
+    return fail(CB_ERR_CUDA, "%s: %s", who, cudaGetErrorString(e));
 }
 
 // K and V rows beside the cache: [n_layers][rows][Hkv][hd], 16-byte vectors

@@ -362,6 +362,8 @@ cb_status cb_kv8_read(cb_kv8* cache, const cb_kv8_seqs* seqs, int32_t layer, int
  *                ranks by: written once for a query window, or added up over decoding steps.
  * NaN behind what a row sees (in a later row's K or V, or behind the sequence) does not reach it.
  * (n_q + n_seqs) * n_kv_heads * (max_len / 128 + 8) has to stay below 2^31 (else CB_ERR_UNSUPPORTED).
+ * What a call is tuned for follows from the rows a sequence has on average, so decoding steps and long queries are better
+ * given to calls of their own.
  * Every sum runs in a fixed order: the same call gives the same bits.  Async on `stream`; no allocation. */
 cb_status cb_kv8_attention(cb_kv8* cache, const cb_kv8_seqs* seqs, int32_t layer, const void* q, int64_t q_stride,
                            const int32_t* q_start, int32_t n_q, float scale, void* out, int64_t out_stride,
