@@ -600,37 +600,49 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
     }
 }
 
-// weights[s][g][j] = sum over the sequence's rows and the group's heads of exp2(score - max) / sum; with many columns
-// blockDim.y sums of every so-manieth one, joined in order
-__global__ void __launch_bounds__(1024) kv8_weights_kernel(const AttnArgs p) {
-    __shared__ float part[8][TK];
+// weights[s][g][j] = sum over the sequence's rows and the group's heads of exp2(score - max) / sum: four keys per thread,
+// blockDim.x threads side by side (one key per thread took 64 sequences of 4K, one row, from 106 us in all to 125).  With
+// blockDim.y > 1 there are that many sums of every so-manieth column, joined in order.
+__global__ void __launch_bounds__(512) kv8_weights_kernel(const AttnArgs p) {
+    extern __shared__ __align__(16) float4 part[];      // [blockDim.y][blockDim.x]; none for one sum, to fit in beside the attention's CTAs
     grid_dep_launch();
     grid_dep_wait();
-    const int key = threadIdx.x, j = blockIdx.x * TK + key, y = threadIdx.y, by = blockDim.y, g = blockIdx.y;
+    const int x = threadIdx.x, y = threadIdx.y, bx = blockDim.x, by = blockDim.y, g = blockIdx.y;
+    const int quad = blockIdx.x * bx + x, t = quad / (TK / 4), j = quad * 4;
     const Seq q = seq_at(p, blockIdx.z);
-    if (blockIdx.x * TK >= q.len) return;
-    float w = 0.f;
+    if (blockIdx.x * 4 * bx >= q.len) return;
+    float w[4] = {0.f, 0.f, 0.f, 0.f};
     if (j < q.len) {
-        const float* score = score_of(p, q, g, blockIdx.x, 0) + key;
+        const float* score = score_of(p, q, g, t, 0) + (j - t * TK);
         const float2* st = p.stats + ((int64_t)g * p.r.n_rows + q.r0) * p.G;
         const int seen = max(0, j - (q.len - q.n)) * p.G, cols = q.n * p.G;      // columns that see key j: [seen, cols)
-#pragma unroll 8
+#pragma unroll 4
         for (int k = seen + y; k < cols; k += by) {
-            const float x = __ldcs(score + (int64_t)k * TK);
+            const float4 s4 = __ldcs(reinterpret_cast<const float4*>(score + (int64_t)k * TK));
             const float2 m = st[k];
-            w += x == -INFINITY ? 0.f : exp2_fast(x - m.x) * m.y;
+            w[0] += s4.x == -INFINITY ? 0.f : exp2_fast(s4.x - m.x) * m.y;
+            w[1] += s4.y == -INFINITY ? 0.f : exp2_fast(s4.y - m.x) * m.y;
+            w[2] += s4.z == -INFINITY ? 0.f : exp2_fast(s4.z - m.x) * m.y;
+            w[3] += s4.w == -INFINITY ? 0.f : exp2_fast(s4.w - m.x) * m.y;
         }
     }
     if (by > 1) {
-        part[y][key] = w;
+        part[y * bx + x] = make_float4(w[0], w[1], w[2], w[3]);
         __syncthreads();
-        if (y == 0)
-            for (int k = 1; k < by; ++k) w += part[k][key];
+        if (y > 0) return;
+#pragma unroll 1
+        for (int k = 1; k < by; ++k) {
+            const float4 o = part[k * bx + x];
+            w[0] += o.x;
+            w[1] += o.y;
+            w[2] += o.z;
+            w[3] += o.w;
+        }
     }
-    if (y == 0 && j < q.len) {
-        float* dst = p.a.weights + ((int64_t)blockIdx.z * p.Hkv + g) * p.a.weights_ld + j;
-        *dst = p.a.add ? *dst + w : w;
-    }
+    float* dst = p.a.weights + ((int64_t)blockIdx.z * p.Hkv + g) * p.a.weights_ld + j;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        if (j + k < q.len) dst[k] = p.a.add ? dst[k] + w[k] : w[k];
 }
 
 template <typename T, typename S>
@@ -730,12 +742,13 @@ cudaError_t launch_kv8_attention(const Kv8& c, const Kv8Seqs& q, const Kv8Rows& 
         if (e != cudaSuccess) return e;
     }
     if (a.weights && q.max_len > 0) {
-        // A block sums 128 keys of a head.  Few blocks with several columns each: eight sums side by side (one sequence of 4K, 8
-        // rows: 23.7 us against 28.2 in all, 64 fp32 rows 66.5 against 115).  Many blocks fill the SMs as they are (16 sequences,
-        // 8 rows: 83 us, 114 split).
-        const int64_t blocks = (int64_t)((q.max_len + TK - 1) / TK) * Hkv * q.n;
-        const int split = blocks <= 4 * c.num_sms && (int64_t)r.n_rows * p.G > 8 * (int64_t)q.n ? 8 : 1;
-        return launch_ex(c.pdl, kv8_weights_kernel, dim3((q.max_len + TK - 1) / TK, Hkv, q.n), dim3(TK, split), 0, s, p);
+        // A block sums 512 keys of a head.  Where those blocks are few and have several columns each, a block has 128 keys and 16
+        // sums side by side (64 fp32 rows over 4K: 66 us in all against 115); many blocks fill the SMs as they are (16 sequences, 8
+        // rows: 82 us, 114 split).
+        const int64_t wide = ((int64_t)q.max_len + 511) / 512;
+        const bool few = wide * Hkv * q.n <= c.num_sms && (int64_t)r.n_rows * p.G > 8 * (int64_t)q.n;
+        if (few) return launch_ex(c.pdl, kv8_weights_kernel, dim3((q.max_len + 127) / 128, Hkv, q.n), dim3(32, 16), 512 * sizeof(float4), s, p);
+        return launch_ex(c.pdl, kv8_weights_kernel, dim3((unsigned)wide, Hkv, q.n), dim3(128), 0, s, p);
     }
     return cudaSuccess;
 }
