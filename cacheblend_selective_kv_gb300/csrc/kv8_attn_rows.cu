@@ -1,7 +1,7 @@
 // Attention over the 8-bit paged K/V cache for many query rows per sequence (a query over a blended context, a prompt in
 // pieces): bf16 queries, an item's 128 rows = 128 / G query rows x the G heads of their group in the lanes of tensor memory.
 //
-// With this many rows a tile of keys is used often enough to widen it once: four warps turn the codes that TMA has brought
+// With this many rows a tile of keys is used often enough to widen it once: eight warps turn the codes that TMA has brought
 // into shared memory into fp16 (exact, without the block scales), in the swizzled layouts of the MMA operands, and
 // S = Q K^T, O += P V run on kind::f16.  Against the e4m3 terms of kv8_attn.cu this costs a conversion per cached value and
 // tile, and saves the terms of q and P for each of 128 rows and the maxima over keys in other threads (a row is one
@@ -16,9 +16,9 @@
 //
 // Each of the two halves of a tile's keys has its own R, sum and O (as the blend's attention kernel does, so that the warps
 // of a row need not meet for every tile); they are joined at the end of an item.  Per tile and SM: 32 MMAs of 128 x 128 x 16
-// at about 99 cycles, 128 x 128 exponentials, 2 x 128 x HD conversions; about 3800 cycles a tile, bound by the softmax warps'
-// chain (two warps a scheduler, 1.2 instructions a cycle) and not by the matrix unit.  2048 rows over 8K: 371 us, 34 % of
-// the measured bf16 rate; the 64 rows of a query over 8K: 32 us, 48 us with weights.
+// at about 99 cycles, 128 x 128 exponentials, 2 x 128 x HD conversions; about 3600 cycles a tile, bound by the softmax warps'
+// chain (two warps a scheduler, 1.2 instructions a cycle) and not by the matrix unit.  2048 rows over 8K: 357 us, 35 % of
+// the measured bf16 rate; the 64 rows of a query over 8K: 29 us, 45 us with weights (with four warps that widen: 371, 32 and 48).
 #include <cstring>
 
 #include "cb_kv8_attn.cuh"
@@ -28,7 +28,7 @@ namespace cb {
 namespace {
 
 constexpr int ROWS = 128;
-constexpr int SOFT = 256, CONV = 128, THREADS = SOFT + CONV + 64;
+constexpr int SOFT = 256, CONV = 256, THREADS = SOFT + CONV + 64;
 constexpr int CONV_WARP = SOFT / 32, MMA_WARP = CONV_WARP + CONV / 32, TMA_WARP = MMA_WARP + 1;
 constexpr int HK = 64;                   // keys of a half
 constexpr int MARKS = 4;                 // items whose row scales and NaN marks are kept; tiles whose conversion is announced
@@ -181,7 +181,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_rows_kernel(const __grid_const
     if (warp >= CONV_WARP && warp < MMA_WARP) {
         // ------------------------------------------------------------------------------------ codes to fp16
         // Like the softmax warps, these run on to their last tile when a wait has given up.
-        constexpr int LPR = HD / 16, RPW = 32 / LPR, NI = TK / (4 * RPW);           // lanes per row, rows per warp and step, steps
+        constexpr int LPR = HD / 16, RPW = 32 / LPR, NI = TK / (CONV / 32 * RPW);           // lanes per row, rows per warp and step, steps
         const int w = warp - CONV_WARP, t = tid - SOFT, e = lane % LPR, row0 = w * RPW + lane / LPR;
         const int box_shift = min(p.q.shift, 7);
         int item = -1;
@@ -201,7 +201,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_rows_kernel(const __grid_const
                 if (i > 0) ptx::mbar_wait(ptx::smem_u32(&c.k_empty[(i - 1) & 1]), ((i - 1) >> 1) & 1, abort, status);
                 const int r0 = w * QR + lane / QL;
 #pragma unroll 1
-                for (int r = r0; r < ROWS; r += 4 * QR) {
+                for (int r = r0; r < ROWS; r += CONV / 32 * QR) {
                     uint8_t* to = sQ + wide_at(r, lane % QL);
                     if (r < cols) cp_async16(ptx::smem_u32(to), qbase + (int64_t)div_g(p, r) * p.a.q_stride + mod_g(p, r) * HD + lane % QL * 8);
                     else *reinterpret_cast<uint4*>(to) = make_uint4(0, 0, 0, 0);
@@ -210,7 +210,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_rows_kernel(const __grid_const
                 if (t == 0) c.any_nan[item % MARKS] = 0;
                 asm volatile("cp.async.wait_all;" ::: "memory");
 #pragma unroll 1
-                for (int r = r0; r < ROWS; r += 4 * QR) {
+                for (int r = r0; r < ROWS; r += CONV / 32 * QR) {
                     uint4* at = reinterpret_cast<uint4*>(sQ + wide_at(r, lane % QL));
                     const uint4 val = *at;
                     const uint32_t word[4] = {val.x, val.y, val.z, val.w};
@@ -255,7 +255,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_rows_kernel(const __grid_const
             ptx::mbar_wait(ptx::smem_u32(&c.k_empty[st]), par, abort, status);
 #pragma unroll 2
             for (int n = 0; n < NI; ++n) {
-                const int row = row0 + n * 4 * RPW;
+                const int row = row0 + n * CONV / 32 * RPW;
                 widen(sK + st * S::TILE, row, *reinterpret_cast<const uint4*>(sm + S::OFF_KC + (i % KT) * S::CODES + f8_at<HD>(row, e * 16)));
             }
             fence_async_smem();
@@ -281,11 +281,11 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_rows_kernel(const __grid_const
             };
             if (plain) {
 #pragma unroll 2
-                for (int n = 0; n < NI; ++n) widen(sV + st * S::TILE, row0 + n * 4 * RPW, codes_of(row0 + n * 4 * RPW));
+                for (int n = 0; n < NI; ++n) widen(sV + st * S::TILE, row0 + n * CONV / 32 * RPW, codes_of(row0 + n * CONV / 32 * RPW));
             } else {
 #pragma unroll 1
                 for (int n = 0; n < NI; ++n) {
-                    const int row = row0 + n * 4 * RPW, j = tile * TK + row;
+                    const int row = row0 + n * CONV / 32 * RPW, j = tile * TK + row;
                     uint4 x = codes_of(row);
                     if (j >= q.len || loaded[row >> box_shift] < 0.f) x = make_uint4(0, 0, 0, 0);
                     else if (j > pos0) take_nan(x, j, nan_marks + (item % MARKS) * HD + e * 16, &c.any_nan[item % MARKS]);
