@@ -17,7 +17,7 @@
 // Each of the two halves of a tile's keys has its own R, sum and O (as the blend's attention kernel does, so that the warps
 // of a row need not meet for every tile); they are joined at the end of an item.  Per tile and SM: 32 MMAs of 128 x 128 x 16
 // at about 99 cycles, 128 x 128 exponentials, 2 x 128 x HD conversions; about 3600 cycles a tile, bound by the softmax warps'
-// chain (two warps a scheduler, 1.2 instructions a cycle) and not by the matrix unit.  2048 rows over 8K: 357 us, 35 % of
+// chain (two warps a scheduler, 1.2 instructions a cycle) and not by the matrix unit.  2048 rows over 8K: 352 us, 36 % of
 // the measured bf16 rate; the 64 rows of a query over 8K: 29 us, 45 us with weights (with four warps that widen: 371, 32 and 48).
 #include <cstring>
 
@@ -253,7 +253,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_rows_kernel(const __grid_const
             // K: free once S of two tiles before is done (rows that are not loaded stay as they were: their scores are masked)
             ptx::mbar_wait(ptx::smem_u32(&c.kc_full[i % KT]), (i / KT) & 1, abort, status);
             ptx::mbar_wait(ptx::smem_u32(&c.k_empty[st]), par, abort, status);
-#pragma unroll 2
+#pragma unroll 1
             for (int n = 0; n < NI; ++n) {
                 const int row = row0 + n * CONV / 32 * RPW;
                 widen(sK + st * S::TILE, row, *reinterpret_cast<const uint4*>(sm + S::OFF_KC + (i % KT) * S::CODES + f8_at<HD>(row, e * 16)));
@@ -280,7 +280,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_rows_kernel(const __grid_const
                 return *reinterpret_cast<const uint4*>(sm + S::OFF_VC + (i % VT) * S::CODES + f8_at<HD>(row, e * 16));
             };
             if (plain) {
-#pragma unroll 2
+#pragma unroll 1
                 for (int n = 0; n < NI; ++n) widen(sV + st * S::TILE, row0 + n * CONV / 32 * RPW, codes_of(row0 + n * CONV / 32 * RPW));
             } else {
 #pragma unroll 1
@@ -609,8 +609,9 @@ template <int HD, bool SCORES> cudaError_t launch_dim(const Kv8& c, AttnArgs& p,
     const cudaError_t e = smem_limit_once(kv8_rows_kernel<HD, SCORES>, Rows<HD>::BYTES, done);
     if (e != cudaSuccess) return e;
     p.QT = ROWS / p.G;
-    // 4096 rows over 4096 keys: 975 us when only tiles counted, 424 with 2 places, 293 with 4, 279 with 5, 283 with 6
-    p.ahead = 5;
+    // 4096 rows over 4096 keys: 975 us when only tiles counted, 424 with 2 places; 256 with 4 and 5, 261 with 6 as the kernel
+    // is now; 16 ragged sequences x 512 rows: 182, 185 and 193 us
+    p.ahead = 4;
     p.min_places = 1 + p.ahead;
     const int64_t items = ((int64_t)p.r.n_rows / p.QT + p.q.n) * p.Hkv;
     const int64_t tiles = items * ((p.q.max_len + TK - 1) / TK + 1);
