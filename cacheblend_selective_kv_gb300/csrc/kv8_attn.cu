@@ -735,7 +735,7 @@ cudaError_t launch_kv8_attention(const Kv8& c, const Kv8Seqs& q, const Kv8Rows& 
     if (r.n_rows > 0) {
         const int rows = (r.n_rows + q.n - 1) / q.n;             // of a sequence, on average
         // Up to 32 columns of a sequence stand in one item here, and beyond that keys and values are read and P is formed once
-        // per item of 32 (64 sequences of 2K: 32 columns 112 us here, 132 there; 48 columns 206 here, 133 there).
+        // per item of 32 (64 sequences of 2K: 32 columns 112 us here, 121 there; 48 columns 205 here, 122 there).
         const bool many = c.cfg.dtype == CB_BF16 && rows * p.G > 32;
         if (many) return launch_kv8_rows(c, &p, s);              // sums its weights too
         const cudaError_t e = c.cfg.head_dim == 128 ? launch_dim<128>(c, p, s) : launch_dim<64>(c, p, s);
