@@ -473,7 +473,7 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
                     for (int n = 0; n < 4; ++n) {
                         const float e = exp2_fast(x[k + n] - rv[n]);
                         lsum[k + n] = fmaf(lsum[k + n], av[n], e);
-                        x[k + n] = e * (v_mul * pv[n]);
+                        x[k + n] = (e * pv[n]) * v_mul;          // (pv * v_mul may pass fp32 where e has vanished)
                     }
                 }
                 if (t > first) add_tile(i - 1);

@@ -1,0 +1,63 @@
+"""GPU tests of the 8-bit paged K/V cache at the edges of what its calls accept: values of any finite size in q, K and
+V, keys that cannot be read, offsets and lengths out of order, outputs that a call makes on a stream of its own.  The
+model, the cases and the attention tolerances are those of test_gpu_kv8.py; what a test adds to them is derived at it."""
+import numpy as np
+import pytest
+
+import kv8_model as km
+from test_gpu_kv8 import Case, U, cb, check_attention, f64, i32, starts_of                  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+torch = pytest.importorskip("torch")
+
+
+def set_pool(c):
+    """The model's pool onto the device."""
+    c.codes.copy_(torch.from_numpy(c.model.codes))
+    c.scales.copy_(torch.from_numpy(c.model.scales.astype(np.float32)))
+
+
+def attend(c, rows, size=1.0, q=None, weights=True):
+    """One call with `rows` query rows per sequence, checked against the model."""
+    n, heads = rows * len(c.lens), c.H * c.G
+    if q is None:
+        q, _ = c.values(n, heads, c.hd, size=size)
+    out = torch.full_like(q, 9.0)
+    w = torch.zeros((len(c.lens), c.H, max(c.lens)), device="cuda") if weights else None
+    c.cache.attention(c.table, c.lens_t, q, out, weights=w, max_len=max(c.lens))
+    check_attention(c, q, f64(q), [rows * s for s in range(len(c.lens) + 1)], out, w)
+    return q, out, w
+
+
+def v_scales(c, s, j0, j1, value):
+    """V's scale of the blocks that hold rows j0 .. j1 - 1 of sequence s."""
+    for b in range(j0 // c.P, -(-j1 // c.P)):
+        c.model.scales[0, 1, c.table_np[s, b]] = value
+
+
+# every kernel: query columns of 4, 8, 16 and 32, fp32 ones of 4 and 8, and many rows
+KERNELS = [("bf16", 1), ("bf16", 2), ("bf16", 4), ("bf16", 8), ("f32", 1), ("f32", 2), ("bf16", 40)]
+
+
+@pytest.mark.parametrize("dtype,rows", KERNELS)
+@pytest.mark.parametrize("ahead,scale", [(130, 2.0 ** -3), (130, 4.0), (90, 2.0 ** 20), (170, 2.0 ** 20), (230, 2.0 ** 100)])
+def test_attention_first_key_far_ahead(cb, dtype, rows, ahead, scale):
+    """A first key whose score is `ahead` octaves (a factor 2^ahead in weight) above the others', whose V blocks have large
+    scales: what vanishes beside it is 0 and not 0 times an overflow.  With (230, 2^100) a weight is below the smallest
+    number of fp32."""
+    n, hd = 400, 64
+    c = Case(cb, [n], H=1, G=4, hd=hd, P=16, dtype=dtype, seed=rows, cells=cb.KV8Cache.cells(rows, 4, n))
+    m = c.model
+    m.scales[0, 0] = 2.0 ** -9
+    m.codes[0, 0, :, :, :, 0] = 0
+    m.codes[0, 0, c.table_np[0, 0], 0, 0, 0] = 0x7E     # 448 * 2^-9 = 0.875 in the first key's first channel
+    v_scales(c, 0, 0, 128, 2.0 ** -3)
+    v_scales(c, 0, 128, n, scale)
+    # in the last page only the last row is not 0: its scale is another one, and most rows do not see what it stands for
+    m.codes[0, 1, c.table_np[0, n // 16 - 1], :, :15] = 0
+    v_scales(c, 0, n - 16, n, scale * 2.0 ** 6)
+    set_pool(c)
+    q, _ = c.values(rows, 4, hd)
+    q[:, :, 0] = ahead * np.log(2.0) * 8 / 0.875
+    attend(c, rows, q=q)
+    c.done()
