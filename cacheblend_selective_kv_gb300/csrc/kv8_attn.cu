@@ -360,10 +360,10 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
             const float* qsc = qscale + (item & 1) * NC + c0;
 
             float acc[NW], lsum[NW];
-            float mrun = -INFINITY;                              // running maximum of column c0 + lane
+            float mrun = -INFINITY;                              // running reference of column c0 + lane
 #pragma unroll
             for (int k = 0; k < NW; ++k) acc[k] = lsum[k] = 0.f;
-            // factors of this warp's columns in a tile: [0] running maximum, [1] scale of P, [2] factor of what was summed
+            // factors of this warp's columns in a tile: [0] reference, [1] scale of P, [2] factor of what was summed
             // before, [3] scale of O
             auto col = [&](int i_, int what) { return cols_of + (((i_ & 1) * 4 * GR + warp) * 4 + what) * NW; };
             auto add_tile = [&](int done) {                      // acc = acc * factor + O of a finished tile
@@ -453,9 +453,11 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
                 if (lane < NW) {
                     const float mt = fmaxf(fmaxf(wm[lane], wm[NW + lane]), fmaxf(wm[2 * NW + lane], wm[3 * NW + lane]));
                     const float yt = fmaxf(fmaxf(wy[lane], wy[NW + lane]), fmaxf(wy[2 * NW + lane], wy[3 * NW + lane]));
-                    const float mn = fmaxf(mrun, mt), ref = mn == -INFINITY ? 0.f : mn;
+                    // The reference of the exponentials: the largest score, or what keeps exponential times V's scale within
+                    // 2^60, so that a sum of the largest values does not pass fp32 before it is divided.
+                    const float mn = fmaxf(fmaxf(mrun, mt), yt - 60.f), ref = mn == -INFINITY ? 0.f : mn;
                     // P of the column times V's scale, scaled by the power of two that brings its largest value to 128 .. 256
-                    const int up = 8 + (yt == -INFINITY ? 0 : (int)floorf(fminf(fmaxf(ref - yt, -118.f), 118.f)));
+                    const int up = 8 + (yt == -INFINITY ? 0 : (int)floorf(fminf(ref - yt, 118.f)));          // 2^-52 .. 2^126
                     col(i, 0)[lane] = ref;
                     col(i, 1)[lane] = __uint_as_float((unsigned)(127 + up) << 23);
                     col(i, 2)[lane] = mn == mrun ? 1.f : exp2_fast(mrun - ref);

@@ -61,3 +61,24 @@ def test_attention_first_key_far_ahead(cb, dtype, rows, ahead, scale):
     q[:, :, 0] = ahead * np.log(2.0) * 8 / 0.875
     attend(c, rows, q=q)
     c.done()
+
+
+def largest_values(cb, dtype, rows, n):
+    c = Case(cb, [n], H=1, G=4, hd=64, P=32, dtype=dtype, seed=rows, cells=cb.KV8Cache.cells(rows, 4, n))
+    for scale in (2.0 ** 120, 2.0 ** 119, 2.0 ** 70):
+        c.model.scales[0, 1] = scale
+        set_pool(c)
+        attend(c, rows)
+    c.model.codes[0, 1, c.table_np[0]] &= 0x7F           # all of one sign: nothing cancels
+    c.model.scales[0, 1] = 2.0 ** 120
+    set_pool(c)
+    attend(c, rows)
+    c.done()
+
+
+@pytest.mark.parametrize("dtype,rows", KERNELS[:-1])
+@pytest.mark.parametrize("n", [300, 5000])
+def test_attention_largest_values(cb, dtype, rows, n):
+    """V near the largest finite number (codes up to 120 at a scale of 2^120): means of such values are finite, whatever the
+    number of keys, and as exact as any other."""
+    largest_values(cb, dtype, rows, n)
