@@ -26,7 +26,7 @@ struct Kv8 {
     float* scores;           // weight_cells floats: attention calls that return weights
     float2* stats;           // their rows' (max, 1 / sum)
     float* part;             // attention: pieces of items that span CTAs
-    int* todo;               // attention of many rows: items to be joined, five ints per CTA
+    int* todo;               // attention of many rows: items to be joined, four ints per CTA
     unsigned* arrived;       // attention: pieces finished, one count per CTA (0 between calls)
     void* scratch;           // the allocation that holds the six above
     alignas(64) unsigned char map[128];   // tensor map of the codes

@@ -36,7 +36,7 @@ struct AttnArgs {
     int min_places;                      // places per CTA, at least
     float* part;                         // [cta][2][NC][HD + 2] pieces of items that span CTAs
     unsigned* arrived;                   // [cta] pieces finished of the item that begins in this CTA (0 between calls)
-    int* todo;                           // many rows: [cta] what the joining kernel has to do (5 ints)
+    int* todo;                           // many rows: [cta] what the joining kernel has to do (4 ints)
     float* scores;                       // weights: scores in the exp2 domain (score_of), score_ld per column
     int score_ld;                        // max_len rounded up to TK
     float2* stats;                       // weights: [Hkv][n_q][G] (max, 1 / sum)
@@ -161,8 +161,10 @@ __device__ __forceinline__ float4 join_pieces(const F& piece_at, int n_pieces, i
     }
     return a;
 }
-// four dims of a result row: a * inv, or 0 for a row that sees nothing
-template <typename T> __device__ __forceinline__ void store4(T* o, const float4& a, float inv, bool sees) {
+// four dims of a result row: a / l, or 0 for a row that sees nothing
+template <typename T> __device__ __forceinline__ void store4(T* o, const float4& a, float l) {
+    const float inv = 1.f / l;
+    const bool sees = l != 0.f;                        // (a NaN is one that sees)
     o[0] = from_f<T>(sees ? a.x * inv : 0.f);
     o[1] = from_f<T>(sees ? a.y * inv : 0.f);
     o[2] = from_f<T>(sees ? a.z * inv : 0.f);

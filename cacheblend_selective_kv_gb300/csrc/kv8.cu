@@ -158,7 +158,7 @@ cb_status cb_kv8_create(const cb_kv8_config* cfg, void* codes, float* scales, cb
     const size_t part = (kv8_part_floats(h->num_sms) * 4 + 255) / 256 * 256;
     // a row of a call that returns weights takes at least 129 cells
     const size_t stats = c.weight_cells > 0 ? (((size_t)c.weight_cells / 129 + 1) * sizeof(float2) + 255) / 256 * 256 : 0;
-    const size_t todo = ((size_t)h->num_sms * 5 * 4 + 255) / 256 * 256;
+    const size_t todo = ((size_t)h->num_sms * 4 * 4 + 255) / 256 * 256;
     if (cudaMalloc(&h->scratch, head + part + stats + todo + (size_t)c.weight_cells * 4) != cudaSuccess) {
         cudaGetLastError();
         delete h;

@@ -1,6 +1,6 @@
 // Attention over the 8-bit paged K/V cache on the sm_103a tensor cores.  Query row i of a sequence's n sits at position
 // len - n + i and sees keys 0 .. that position: out = softmax(q k * scale) v, the G query heads of a group sharing a KV
-// head.  A row that sees nothing (its position is negative) gives 0.  With weights, every key gets the sum of its
+// head.  A row that sees nothing (its position is negative, or all its keys lie in bad pages) gives 0.  With weights, every key gets the sum of its
 // softmax weights over the call's query rows and the group's heads.
 //
 // A decoding step reads every cached byte once and does 4 G FLOPs for it, so it is bound by HBM as long as the codes
@@ -106,7 +106,7 @@ constexpr int MAX_STAGES = 3;
 constexpr int RING = 8;
 struct Open {                            // an item of which this CTA has a piece
     int u0, pieces;                      // the CTA it begins in, how many have a piece of it
-    int row0, cols, pos0, g;
+    int row0, cols, g;
 };
 struct Shared {
     ScaleRing<RING> ring;
@@ -543,7 +543,7 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
                 for (int k = 0; k < NW; ++k) {
                     if (c0 + k >= cols) continue;
                     const float inv = 1.f / lsum[k];
-                    if (key < HD) out_at(c0 + k)[key] = from_f<T>(pos0 + div_g(p, c0 + k) >= 0 ? acc[k] * inv : 0.f);
+                    if (key < HD) out_at(c0 + k)[key] = from_f<T>(lsum[k] != 0.f ? acc[k] * inv : 0.f);
                     if (p.scores && key == 0) p.stats[stat0 + c0 + k] = make_float2(colm[c0 + k], inv);
                 }
             } else {
@@ -560,7 +560,7 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
                     for (int k = 0; k < NW; ++k)
                         *reinterpret_cast<float2*>(piece + NC * HD + 2 * (c0 + k)) = make_float2(colm[c0 + k], lsum[k]);
                 }
-                if (tid == 0) c.open[n_open] = Open{u0, n_pieces, q.r0 + q0, cols, pos0, g};
+                if (tid == 0) c.open[n_open] = Open{u0, n_pieces, q.r0 + q0, cols, g};
                 ++n_open;
             }
             if (i < count) cur = c.next;                         // written before the last barrier, again behind the next
@@ -586,9 +586,8 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
                     float m, l;
                     const auto at = [&](int u) { return piece_at<S>(p, o.u0, u); };
                     const float4 a = join_pieces<HD, S::JOIN>(at, o.pieces, k * HD, NC * HD + 2 * k, m, l, buf);
-                    const int row = div_g(p, k);
-                    T* out = (T*)p.a.out + (int64_t)(o.row0 + row) * p.a.out_stride + (int64_t)(o.g * p.G + mod_g(p, k)) * HD;
-                    if (lane < HD / 4) store4(out + lane * 4, a, 1.f / l, o.pos0 + row >= 0);
+                    T* out = (T*)p.a.out + (int64_t)(o.row0 + div_g(p, k)) * p.a.out_stride + (int64_t)(o.g * p.G + mod_g(p, k)) * HD;
+                    if (lane < HD / 4) store4(out + lane * 4, a, l);
                     if (p.scores && lane == 0) p.stats[((int64_t)o.g * p.r.n_rows + o.row0) * p.G + k] = make_float2(m, 1.f / l);
                 }
             }

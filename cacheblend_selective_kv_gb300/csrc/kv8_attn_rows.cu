@@ -38,7 +38,7 @@ constexpr float GROW = 8.f;              // how far (log2) P may outgrow its ref
 constexpr float P_UP = 128.f;            // P is stored this much larger: its largest values are 2^7 .. 2^15 of fp16's 2^16
 
 struct Todo {                            // an item that begins in a CTA and ends in another: its rows and pieces
-    int row0, cols, g, pos0, pieces;
+    int row0, cols, g, pieces;
 };
 
 struct RowsShared {
@@ -224,11 +224,12 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_rows_kernel(const __grid_const
 #pragma unroll
                     for (int o = QL / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
                     // kv8_scale brings the largest value to 224 .. 448; 2^6 more is 2^14 .. 2^15 less a little (the softmax's
-                    // scale gives its sign, and nothing when it is 0)
+                    // scale gives its sign, and nothing when it is 0).  An infinity counts as NaN: it could give scores of -inf
+                    // alone, which is how a row that sees nothing looks.
                     const float sc = kv8_scale(top), up = kv8_inverse(sc) * (p.a.scale < 0.f ? -64.f : p.a.scale > 0.f ? 64.f : 0.f);
                     uint32_t o[4];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) o[k] = f16_pair(f[2 * k] * up, f[2 * k + 1] * up);
+                    for (int k = 0; k < 4; ++k) o[k] = f16_pair(kv8_nan_inf(f[2 * k]) * up, kv8_nan_inf(f[2 * k + 1]) * up);
                     *at = make_uint4(o[0], o[1], o[2], o[3]);
                     if (lane % QL == 0) row_scale[(item % MARKS) * ROWS + r] = sc * (1.f / 64.f);
                 }
@@ -370,7 +371,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_rows_kernel(const __grid_const
         const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
         const float to_exp2 = fabsf(p.a.scale) * 1.4426950408889634f;
         const int box_shift = min(p.q.shift, 7);
-        Todo todo{0, 0, 0, 0, 0};
+        Todo todo{0, 0, 0, 0};
         int item = 0;
         for (int i = 0; i < count; ++item) {
             const int first = cur.t, n_here = min(cur.nt - first, count - i), g = cur.g;
@@ -517,7 +518,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_rows_kernel(const __grid_const
                     if (whole) {
                         uint32_t w[8];
 #pragma unroll
-                        for (int y = 0; y < 8; ++y) w[y] = pos >= 0 ? bf16_pair(a0[2 * y] * inv, a0[2 * y + 1] * inv) : 0u;
+                        for (int y = 0; y < 8; ++y) w[y] = L != 0.f ? bf16_pair(a0[2 * y] * inv, a0[2 * y + 1] * inv) : 0u;
                         uint4* o = reinterpret_cast<uint4*>(out_at(row) + d);
                         o[0] = make_uint4(w[0], w[1], w[2], w[3]);
                         o[1] = make_uint4(w[4], w[5], w[6], w[7]);
@@ -538,7 +539,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_rows_kernel(const __grid_const
                 if (hf == 0 && row < cols)
                     *reinterpret_cast<float2*>(piece_at(blockIdx.x - u0) + ROWS * HD + 2 * row) = make_float2(M, L);
                 // (the CTA in which the item begins says so to the joining kernel)
-                if (first == 0 && tid == 0) todo = Todo{q.r0 + q0, cols, g, pos0, n_pieces};
+                if (first == 0 && tid == 0) todo = Todo{q.r0 + q0, cols, g, n_pieces};
                 ptx::named_bar_sync(3 + quarter, 64);            // `halves` has been read
             }
             if (i < count) cur.next_item(p);
@@ -568,7 +569,7 @@ __global__ void __launch_bounds__(256) kv8_join_kernel(const AttnArgs p) {
     float m, l;
     const float4 a = join_pieces<HD, 8>(piece_at, d.pieces, k * HD, ROWS * HD + 2 * k, m, l, buf[warp]);
     bf16* out = (bf16*)p.a.out + (int64_t)(d.row0 + div_g(p, k)) * p.a.out_stride + (int64_t)(d.g * p.G + mod_g(p, k)) * HD;
-    if (lane < HD / 4) store4(out + lane * 4, a, 1.f / l, d.pos0 + div_g(p, k) >= 0);
+    if (lane < HD / 4) store4(out + lane * 4, a, l);
     if (p.scores && lane == 0) p.stats[((int64_t)d.g * p.r.n_rows + d.row0) * p.G + k] = make_float2(m, 1.f / l);
 }
 

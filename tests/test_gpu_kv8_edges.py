@@ -82,3 +82,67 @@ def test_attention_largest_values(cb, dtype, rows, n):
     """V near the largest finite number (codes up to 120 at a scale of 2^120): means of such values are finite, whatever the
     number of keys, and as exact as any other."""
     largest_values(cb, dtype, rows, n)
+
+
+@pytest.mark.parametrize("dtype,rows", KERNELS)
+@pytest.mark.parametrize("n", [100, 3000])
+def test_rows_that_see_only_bad_pages(cb, dtype, rows, n):
+    """Keys of bad pages are not seen, and a row that sees nothing gives 0: a whole sequence of bad pages, and one whose first
+    pages are bad, so that its first rows see nothing; items of one CTA and of many."""
+    H, G, hd, P = 2, 4, 64, 16
+    c = Case(cb, [n, rows + 5, n], H=H, G=G, hd=hd, P=P, dtype=dtype, seed=rows, cells=cb.KV8Cache.cells(3 * rows, H * G, n))
+    bad = c.table.clone()
+    bad[0] = -1
+    blind = min(rows, max(0, P - 5))                     # rows of the second sequence at positions below P
+    bad[1, 0] = 10 ** 6
+    q, q64 = c.values(3 * rows, H * G, hd)
+    out = torch.full_like(q, 9.0)
+    w = torch.full((3, H, n), 5.0, device="cuda")
+    c.cache.attention(bad, c.lens_t, q, out, weights=w, max_len=n)
+    torch.cuda.synchronize()
+    assert c.cache.status(clear=True) == cb.CB_STATUS_BAD_ROW
+    got, wg = f64(out), f64(w)
+    assert not got[:rows].any() and not got[rows:rows + blind].any()
+    assert not wg[0].any() and not wg[1, :, :min(P, rows + 5)].any()
+    # the rows that see something: the second sequence without its first page, and the third as it is
+    c.table_np = np.concatenate([c.table_np[:1], np.roll(c.table_np[1:2], -1, axis=1), c.table_np[2:]])
+    c.lens = [n, max(0, rows + 5 - P), n]
+    st = [0, rows, 2 * rows, 3 * rows]
+    ref, ws, spread, big = c.model.attention(c.table_np, c.lens, q64, st, 0, hd ** -0.5)
+    lo = rows + blind
+    p_rep, rnd, last = (2.0 ** -11, 2.0 ** -8, 2.0 ** -25) if dtype == "bf16" else (2.0 ** -23, 2.0 ** -24, 2.0 ** -37)
+    tol = rnd * np.abs(ref) + (2 * (hd + 8) * U * big + (144 + n / 128) * U + p_rep) * spread + last * c.model.floor + \
+        2.0 ** -32 * c.model.floor_all
+    assert np.all(np.abs(got - ref)[lo:] <= tol[lo:] + 1e-30)
+    assert np.allclose(wg[2], ws[2], rtol=1e-4, atol=1e-12)
+    assert np.allclose(wg[1, :, P:rows + 5], ws[1], rtol=1e-4, atol=1e-12)
+    c.done()
+
+
+@pytest.mark.parametrize("dtype,rows", KERNELS)
+def test_queries_with_infinities_and_nan(cb, dtype, rows):
+    """An infinity or a NaN in a query head's row makes that result NaN, and no other."""
+    n = 200
+    c = Case(cb, [n], H=2, G=4, hd=64, P=16, dtype=dtype, seed=rows, cells=cb.KV8Cache.cells(rows, 8, n))
+    codes = c.model.codes[0, 0, c.table_np[0]]
+    c.model.codes[0, 0, c.table_np[0]] = np.where((codes & 0x7F) == 0x7F, codes, codes & 0x7F | 0x08)
+    # (keys above 0: against an infinite q every score would be -inf, as if nothing were seen)
+    set_pool(c)
+    q, _ = c.values(rows, 8, 64)
+    r = rows - 1
+    q[r, 1, :] = -float("inf")
+    q[0, 2, 7] = float("nan")
+    q[r, 6, 3] = float("inf")
+    out, w = torch.empty_like(q), torch.zeros((1, 2, n), device="cuda")
+    c.cache.attention(c.table, c.lens_t, q, out, weights=w, max_len=n)
+    want = np.zeros((rows, 8), bool)
+    want[r, 1] = want[0, 2] = want[r, 6] = True
+    got = f64(out)
+    assert np.array_equal(np.isnan(got), np.repeat(want[:, :, None], 64, axis=2))
+    clean = torch.where(torch.isfinite(q), q, torch.zeros_like(q))
+    ref = torch.empty_like(q)
+    c.cache.attention(c.table, c.lens_t, clean, ref, max_len=n)
+    keep = torch.from_numpy(want).cuda()[:, :, None]
+    check_attention(c, clean, f64(clean), [0, rows], torch.where(keep, ref, out))
+    assert torch.isnan(w[0]).all()
+    c.done()
