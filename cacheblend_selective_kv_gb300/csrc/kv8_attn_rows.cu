@@ -226,7 +226,8 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_rows_kernel(const __grid_const
                     // kv8_scale brings the largest value to 224 .. 448; 2^6 more is 2^14 .. 2^15 less a little (the softmax's
                     // scale gives its sign, and nothing when it is 0).  An infinity counts as NaN: it could give scores of -inf
                     // alone, which is how a row that sees nothing looks.
-                    const float sc = kv8_scale(top), up = kv8_inverse(sc) * (p.a.scale < 0.f ? -64.f : p.a.scale > 0.f ? 64.f : 0.f);
+                    // (not below 2^-119, so that 1 / scale * 2^6 stays finite)
+                    const float sc = top > 0.f ? fmaxf(kv8_scale(top), 1.5046328e-36f) : 0.f, up = kv8_inverse(sc) * (p.a.scale < 0.f ? -64.f : p.a.scale > 0.f ? 64.f : 0.f);
                     uint32_t o[4];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) o[k] = f16_pair(kv8_nan_inf(f[2 * k]) * up, kv8_nan_inf(f[2 * k + 1]) * up);

@@ -146,3 +146,19 @@ def test_queries_with_infinities_and_nan(cb, dtype, rows):
     check_attention(c, clean, f64(clean), [0, rows], torch.where(keep, ref, out))
     assert torch.isnan(w[0]).all()
     c.done()
+
+
+@pytest.mark.parametrize("dtype,rows", [("bf16", 1), ("bf16", 8), ("bf16", 9), ("f32", 3)])
+def test_attention_tiny_queries(cb, dtype, rows):
+    """Rows of q from the smallest numbers up, on either side of 32 columns: their scores are next to 0 and their weights
+    next to equal."""
+    sizes = (1e-36, 1e-39, 2e-37, 0.0, 1.0, 1e-30, 3e-36, 8e-35)
+    c = Case(cb, [260], H=1, G=4, hd=64, P=16, dtype=dtype, seed=rows, cells=cb.KV8Cache.cells(rows, 4, 260))
+    for first in range(0, len(sizes), 4):
+        x = c.rng.normal(size=(rows, 4, 64))
+        for r in range(rows):
+            for h in range(4):
+                x[r, h] *= sizes[(first + r * 4 + h) % len(sizes)]
+        x[:, :, 5] = 0.0
+        attend(c, rows, q=torch.from_numpy(x.astype(np.float32)).to(c.td).cuda())
+    c.done()
