@@ -11,11 +11,16 @@
 //
 // V's block scales differ, so P carries them: p_j = 2^(x_j - R) s_j with x the score in the exp2 domain, s_j the scale of
 // key j's block and R a reference of the row no more than 2^8 below the largest x_j + log2 s_j so far.  It grows lazily (O
-// is rescaled in tensor memory when it must), which keeps P within fp16; the softmax sum takes 2^(x_j - R) in fp32.  A
-// scale below 2^-100 counts as 2^-100 for R, so that no exponent overflows.
+// is rescaled in tensor memory when it must), which keeps P within fp16.  A scale below 2^-100 counts as 2^-100 for R.
 //
-// Each of the two halves of a tile's keys has its own R, sum and O (as the blend's attention kernel does, so that the warps
-// of a row need not meet for every tile); they are joined at the end of an item.  Per tile and SM: 32 MMAs of 128 x 128 x 16
+// The softmax sum takes 2^(x_j - X) in fp32.  X is R as long as R lies up to 30 below the row's largest score M, which it
+// does for scales of 2^-30 to 1, and follows M otherwise: a key's weight in the sum has nothing to do with its V, and
+// with R as its reference the weights of keys of small V would vanish beside a V that is 2^126 times larger, or all of
+// them before a V of 2^100.  X is max(min(R, M), R - 60, M - 30): near enough to M for the sum, near enough to R for
+// the factor 2^(R - X) between O and the sum.  It only grows, as R and M do.
+//
+// Each of the two halves of a tile's keys has its own R, X, sum and O (as the blend's attention kernel does, so that the
+// warps of a row need not meet for every tile); they are joined at the end of an item, relative to X.  Per tile and SM: 32 MMAs of 128 x 128 x 16
 // at about 99 cycles, 128 x 128 exponentials, 2 x 128 x HD conversions; about 3600 cycles a tile, bound by the softmax warps'
 // chain (two warps a scheduler, 1.2 instructions a cycle) and not by the matrix unit.  2048 rows over 8K: 352 us, 36 % of
 // the measured bf16 rate; the 64 rows of a query over 8K: 29 us, 45 us with weights (with four warps that widen: 371, 32 and 48).
@@ -35,6 +40,7 @@ constexpr int MARKS = 4;                 // items whose row scales and NaN marks
 constexpr int RING = 16;                 // tiles whose block scales are kept
 constexpr int KT = 2, VT = 1;            // tiles of K and V codes
 constexpr float GROW = 8.f;              // how far (log2) P may outgrow its reference
+constexpr float SLACK = 38.f;            // how far (log2) a term of the sum may get above 1
 constexpr float P_UP = 128.f;            // P is stored this much larger: its largest values are 2^7 .. 2^15 of fp16's 2^16
 
 struct Todo {                            // an item that begins in a CTA and ends in another: its rows and pieces
@@ -58,8 +64,8 @@ template <int HD> struct Rows {
     static constexpr int TILE = TK * HD * 2, CODES = TK * HD;    // a K or V tile, or Q, in fp16; a tile of codes
     static constexpr int OFF_K = TILE, OFF_V = 3 * TILE, OFF_KC = 5 * TILE, OFF_VC = OFF_KC + KT * CODES;
     static constexpr int OFF_X = OFF_VC + VT * CODES;
-    // floats: row scales [MARKS][ROWS], (R, sum) [2][ROWS][2]; ints: nan_from [MARKS][HD]
-    static constexpr int X_FLOATS = MARKS * ROWS + 4 * ROWS + MARKS * HD;
+    // floats: row scales [MARKS][ROWS], (X, sum, R, -) [2][ROWS][4]; ints: nan_from [MARKS][HD]
+    static constexpr int X_FLOATS = MARKS * ROWS + 8 * ROWS + MARKS * HD;
     static constexpr int OFF_C = OFF_X + X_FLOATS * 4;
     static constexpr int BYTES = OFF_C + (int)sizeof(RowsShared);
     static constexpr int PIECE = ROWS * (HD + 2);
@@ -126,7 +132,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_rows_kernel(const __grid_const
     uint8_t* sV = sm + S::OFF_V;                        // [2]
     float* row_scale = reinterpret_cast<float*>(sm + S::OFF_X);
     float* halves = row_scale + MARKS * ROWS;
-    int* nan_marks = reinterpret_cast<int*>(halves + 4 * ROWS);
+    int* nan_marks = reinterpret_cast<int*>(halves + 8 * ROWS);
     RowsShared& c = *reinterpret_cast<RowsShared*>(sm + S::OFF_C);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     unsigned* status = p.q.status;
@@ -380,7 +386,12 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_rows_kernel(const __grid_const
             const int q0 = cur.qt * p.QT, cols = min(p.QT, q.n - q0) * p.G;
             const int pos0 = q.len - q.n + q0, pos = pos0 + div_g(p, row);       // positions of the item's first row and of this one
             const int64_t stat0 = ((int64_t)g * p.r.n_rows + q.r0 + q0) * p.G;
-            float ref = -INFINITY, l = 0.f, row_mul = 0.f;       // R, the sum of 2^(x - R)
+            float ref = -INFINITY, at = -INFINITY, most = -INFINITY;     // R, X and M
+            float l = 0.f, up = 0.f, row_mul = 0.f;              // the sum of 2^(x - X); 2^(X - R) P_UP
+            const auto set_at = [&] {
+                at = fmaxf(fminf(ref, most), fmaxf(ref - 60.f, most - 30.f));
+                up = at == ref ? P_UP : P_UP * exp2_fast(at - ref);
+            };
             for (int t = first; t < first + n_here; ++t, ++i) {
                 const int b = i & 1, j0 = t * TK + hf * HK;
                 ptx::mbar_wait(ptx::smem_u32(&c.ring.full[i % RING]), (i / RING) & 1, abort, status);
@@ -430,6 +441,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_rows_kernel(const __grid_const
 #pragma unroll
                     for (int y = 1; y < 16; ++y) m = fmaxf(m, __uint_as_float(x[y]));
                     top = fmaxf(top, fmaf(m, mul, vl));
+                    most = fmaxf(most, m * mul);
                     if (SCORES && row < cols) {
                         float4* score = quads_of(p, q, g, t) + (int64_t)((hf * HK + k) / 4) * (q.n * p.G) + q0 * p.G + row;
 #pragma unroll
@@ -438,7 +450,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_rows_kernel(const __grid_const
                                                  __uint_as_float(x[y + 3]) * mul);
                     }
                 }
-                if (__any_sync(0xffffffffu, ref != -INFINITY && top > ref + GROW)) {
+                if (__any_sync(0xffffffffu, ref != -INFINITY && (top > ref + GROW || most > at + SLACK))) {
                     // O_h holds the tiles before: the whole warp rescales, each row by its own factor
                     {
                         ptx::mbar_wait(ptx::smem_u32(&c.pv_done[(i - 1) & 1]), ((i - 1) >> 1) & 1, abort, status);
@@ -453,18 +465,26 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_rows_kernel(const __grid_const
                             ptx::tmem_st16(lanes + O_COL + hf * HD + k, o);
                         }
                         ptx::tmem_wait_st();
-                        l *= f;
-                        if (ref != -INFINITY) ref = to;
+                        if (ref != -INFINITY) {
+                            const float was = at;
+                            ref = to;
+                            set_at();
+                            l *= exp2_fast(was - at);
+                        }
                     }
                 }
-                if (ref == -INFINITY) ref = top;                 // nothing summed yet
-                const float neg = ref == -INFINITY ? 0.f : -ref;
+                if (ref == -INFINITY) {                          // nothing summed yet
+                    ref = top;
+                    set_at();
+                }
+                const float neg = at == -INFINITY ? 0.f : -at;
                 float sum = 0.f;
 #pragma unroll 1
                 for (int k = 0; k < HK; k += 16) {               // P over the S columns that have been read
                     uint32_t x[16], w[8];
                     ptx::tmem_ld16_issue(s_at + k, x);
-                    const float m = mul_at(k), v = scales[8 + box_at(k)] * P_UP;
+                    // (held to finite numbers where the exponentials it meets have vanished)
+                    const float m = mul_at(k), v = fminf(scales[8 + box_at(k)] * up, 3.402823466e38f);
                     ptx::tmem_ld_wait16(x);
 #pragma unroll
                     for (int y = 0; y < 16; y += 2) {
@@ -484,13 +504,13 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_rows_kernel(const __grid_const
             ptx::mbar_wait(ptx::smem_u32(&c.v_seen[(i - 1) % MARKS]), ((i - 1) / MARKS) & 1, abort, status);
             ptx::mbar_wait(ptx::smem_u32(&c.pv_done[(i - 1) & 1]), ((i - 1) >> 1) & 1, abort, status);
             ptx::tc_fence_after();
-            *reinterpret_cast<float2*>(halves + (hf * ROWS + row) * 2) = make_float2(ref, l);
+            *reinterpret_cast<float4*>(halves + (hf * ROWS + row) * 4) = make_float4(at, l, ref, 0.f);
             ptx::named_bar_sync(3 + quarter, 64);                // the two warps of these rows
-            const float2 other = *reinterpret_cast<const float2*>(halves + ((hf ^ 1) * ROWS + row) * 2);
-            const float M = fmaxf(ref, other.x);
-            const float f_own = ref == -INFINITY ? 0.f : exp2_fast(ref - M), f_other = other.x == -INFINITY ? 0.f : exp2_fast(other.x - M);
-            const float f0 = hf == 0 ? f_own : f_other, f1 = hf == 0 ? f_other : f_own;
-            const float L = hf == 0 ? l * f_own + other.y * f_other : other.y * f_other + l * f_own;
+            const float4 h0 = *reinterpret_cast<const float4*>(halves + row * 4), h1 = *reinterpret_cast<const float4*>(halves + (ROWS + row) * 4);
+            const float X = fmaxf(h0.x, h1.x);
+            const auto power = [&](float x) { return x == -INFINITY ? 0.f : exp2_fast(x - X); };
+            const float L = h0.y * power(h0.x) + h1.y * power(h1.x);
+            const float f0 = power(h0.z), f1 = power(h1.z);      // of the halves' O
             const bool whole = first == 0 && n_here == cur.nt;
             const int u0 = first_cta(p, c.find, mine.per, first), n_pieces = piece_count(p, c.find, mine.per, first, n_here, cur.nt);
             const auto piece_at = [&](int u) { return p.part + (int64_t)((u0 + u) * 2 + (u == 0 ? 1 : 0)) * S::PIECE; };
@@ -534,11 +554,11 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_rows_kernel(const __grid_const
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&c.o_free));
             if (whole) {
-                if (SCORES && hf == 0 && row < cols) p.stats[stat0 + row] = make_float2(M, inv);
+                if (SCORES && hf == 0 && row < cols) p.stats[stat0 + row] = make_float2(X, inv);
                 ptx::named_bar_sync(3 + quarter, 64);            // `halves` has been read
             } else {
                 if (hf == 0 && row < cols)
-                    *reinterpret_cast<float2*>(piece_at(blockIdx.x - u0) + ROWS * HD + 2 * row) = make_float2(M, L);
+                    *reinterpret_cast<float2*>(piece_at(blockIdx.x - u0) + ROWS * HD + 2 * row) = make_float2(X, L);
                 // (the CTA in which the item begins says so to the joining kernel)
                 if (first == 0 && tid == 0) todo = Todo{q.r0 + q0, cols, g, n_pieces};
                 ptx::named_bar_sync(3 + quarter, 64);            // `halves` has been read

@@ -162,3 +162,53 @@ def test_attention_tiny_queries(cb, dtype, rows):
         x[:, :, 5] = 0.0
         attend(c, rows, q=torch.from_numpy(x.astype(np.float32)).to(c.td).cuda())
     c.done()
+
+
+@pytest.mark.parametrize("dtype,rows", KERNELS)
+@pytest.mark.parametrize("n", [200, 4000])
+@pytest.mark.parametrize("low,high", [(0.0, 2.0 ** 30), (0.0, 2.0 ** 120), (2.0 ** -90, 2.0 ** 40), (2.0 ** -126, 2.0 ** 100),
+                                      (2.0 ** -90, 2.0 ** -90), (2.0 ** 110, 2.0 ** 110)])
+def test_attention_scales_far_apart(cb, dtype, rows, n, low, high):
+    """V blocks of very different sizes beside each other: half of the keys low, half high, in one order and the other, and
+    in turn.  Each key's weight counts in the sum whatever its V."""
+    c = Case(cb, [n], H=1, G=4, hd=64, P=16, dtype=dtype, seed=rows, cells=cb.KV8Cache.cells(rows, 4, n))
+    was = c.model.codes.copy()
+    h = n // 2 // 16 * 16
+    for order in range(3):
+        c.model.codes = was.copy()
+        v_scales(c, 0, 0, h, (low, high, high)[order])
+        v_scales(c, 0, h, n, (high, low, low)[order])
+        if order == 2:
+            for b in range(0, -(-n // 16), 2):
+                v_scales(c, 0, 16 * b, 16 * b + 16, low)
+        zero = c.model.scales[0, 1] == 0                 # a block whose scale is 0 holds zeros
+        c.model.codes[0, 1][zero] = 0
+        set_pool(c)
+        attend(c, rows)
+    c.done()
+
+
+@pytest.mark.parametrize("gap", [60, 100])
+@pytest.mark.parametrize("dtype,rows", KERNELS)
+def test_attention_large_v_behind_a_small_weight(cb, dtype, rows, gap):
+    """Keys of a weight 2^-gap, beside one of weight 1, whose V is as much larger: both count in the result."""
+    n, hd = 200, 64
+    for top, rest in ((2.0 ** -100, 2.0 ** (gap - 100)), (1.0, 2.0 ** gap), (2.0 ** 15, 2.0 ** 115)):
+        c = Case(cb, [n], H=1, G=4, hd=hd, P=16, dtype=dtype, seed=rows, cells=cb.KV8Cache.cells(rows, 4, n))
+        m = c.model
+        m.scales[0, 0] = 2.0 ** -9
+        m.codes[0, 0, :, :, :, 0] = 0
+        m.codes[0, 0, c.table_np[0, 0], 0, 0, 0] = 0x7E
+        v_scales(c, 0, 0, 16, top)
+        v_scales(c, 0, 16, n, rest)
+        m.codes[0, 1, c.table_np[0, 0], 0, 1:] = 0       # in the first block only the first key's V
+        set_pool(c)
+        q, _ = c.values(rows, 4, hd)
+        q[:, :, 0] = gap * np.log(2.0) * 8 / 0.875
+        attend(c, rows, q=q)
+        c.done()
+
+
+@pytest.mark.parametrize("n", [300, 5000])
+def test_many_rows_largest_values(cb, n):
+    largest_values(cb, "bf16", 40, n)
