@@ -11,6 +11,7 @@ with the operators on it (write, read, attention, evict).
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -450,7 +451,8 @@ class KV8Cache:
     Every call takes the batch as ``table`` (device int32 [n_seqs][pages]) and ``lens`` (device int32 [n_seqs], or None:
     max_len each); ``max_len`` bounds the lengths (default: all the table can hold).  Calls are asynchronous on `stream`
     (default: the current one) and allocate nothing, so they can be captured into a graph.  A tensor of another shape,
-    type or device raises ValueError before anything is enqueued."""
+    type or device raises ValueError before anything is enqueued.  An output that is left to a call is made on the call's
+    stream: another stream that uses it waits for that one first (and Tensor.record_stream tells the allocator so)."""
 
     def __init__(self, codes, scales, n_heads: int, dtype: str = "bf16", weight_cells: int = 0):
         import torch
@@ -510,6 +512,17 @@ class KV8Cache:
             return self._raw_stream(self._dev)
         return stream if isinstance(stream, int) else stream.cuda_stream
 
+    def _made_on(self, stream):
+        """Outputs that a call makes are made on its stream: a fill is then in order with the kernels, and the memory is
+        none that the current stream still uses."""
+        raw = self._stream(stream)
+        if stream is None or raw == self._raw_stream(self._dev):
+            return contextlib.nullcontext()
+        import torch
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(raw, device=self.device) if raw else torch.cuda.default_stream(self.device)
+        return torch.cuda.stream(stream)
+
     def _kv(self, t, name, n_layers):
         """(pointer, layer stride, row stride, rows) of K/V rows [n_layers][rows][n_kv_heads][head_dim] (or without the
         layers when there is one)."""
@@ -558,8 +571,9 @@ class KV8Cache:
         (causal); returns out.  weights (device float32 [n_seqs][n_kv_heads][ld >= max_len]) receives, or with add
         accumulates, the weight of every key.  q_start as row_start of write; scale defaults to head_dim ** -0.5."""
         if out is None:
-            # rows that belong to no sequence are not written: zeros there
-            out = q.new_empty(q.shape) if q_start is None else q.new_zeros(q.shape)
+            with self._made_on(stream):
+                # rows that belong to no sequence are not written: zeros there
+                out = q.new_empty(q.shape) if q_start is None else q.new_zeros(q.shape)
         qp, qs, n = self._q(q, "q")
         op, os_, n_out = self._q(out, "out")
         if n_out != n:
@@ -593,10 +607,11 @@ class KV8Cache:
         dp = self._int(dst_table, "dst_table", n, dst_ld)
         if out_weights is None:
             out_weights = weights
-        if out_lens is None:
-            out_lens = table.new_empty(n)
-        if out_rows is None:
-            out_rows = table.new_empty((n_layers, n, self.n_kv_heads, max(int(n_keep), 0)))
+        with self._made_on(stream):
+            if out_lens is None:
+                out_lens = table.new_empty(n)
+            if out_rows is None:
+                out_rows = table.new_empty((n_layers, n, self.n_kv_heads, max(int(n_keep), 0)))
         ld = weights.shape[-1]
         for t, name in ((weights, "weights"),) if out_weights is weights else ((weights, "weights"), (out_weights, "out_weights")):
             if t.dtype is not self._f32 or t.get_device() != self._dev or not t.is_contiguous() or \

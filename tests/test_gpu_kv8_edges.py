@@ -212,3 +212,62 @@ def test_attention_large_v_behind_a_small_weight(cb, dtype, rows, gap):
 @pytest.mark.parametrize("n", [300, 5000])
 def test_many_rows_largest_values(cb, n):
     largest_values(cb, "bf16", 40, n)
+
+
+def busy(ms_of_work=16):
+    """Work that keeps the current stream busy for some milliseconds."""
+    x = torch.ones(1 << 28, device="cuda")
+    for _ in range(3 * ms_of_work):
+        x.add_(1.0)
+    return x
+
+
+@pytest.mark.parametrize("rows", [1, 40])
+def test_outputs_made_by_a_call_on_a_stream(cb, rows):
+    """out left to the call, on another stream than the current one, which has work to do: rows of no sequence are 0, the
+    others are what the call gives on the current stream."""
+    c = Case(cb, [150, 90], H=2, G=4, hd=64, P=16, seed=rows)
+    n = 2 * rows + 3
+    q, _ = c.values(n, 8, 64)
+    st = i32([1, 1 + rows, 1 + 2 * rows])
+    want = c.cache.attention(c.table, c.lens_t, q, q_start=st)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for stream in (side, side.cuda_stream):
+        # blocks that the allocator may give out again, full of NaN
+        trash = [torch.full_like(q, float("nan")) for _ in range(4)]
+        torch.cuda.synchronize()
+        del trash
+        keep = busy()
+        out = c.cache.attention(c.table, c.lens_t, q, q_start=st, stream=stream)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and torch.count_nonzero(out[0]) == 0 and torch.count_nonzero(out[-2:]) == 0
+        del keep
+    c.done()
+
+
+def test_evict_outputs_made_by_a_call_on_a_stream(cb):
+    """Blocks that the current stream still writes are not handed to another stream's eviction."""
+    c = Case(cb, [150, 90], H=2, G=4, hd=64, P=16, seed=3)
+    w = torch.rand((1, 2, 2, 160), device="cuda")
+    side = torch.cuda.Stream()
+    want = None
+    for stream in (None, side, side.cuda_stream):
+        ow = torch.empty_like(w)
+        t, held = torch.empty(25000, dtype=torch.int32, device="cuda"), []
+        was = torch.cuda.memory_reserved()
+        while torch.cuda.memory_reserved() == was:       # so that t's is the smallest free block
+            held.append(torch.empty(128, dtype=torch.int32, device="cuda"))
+        torch.cuda.synchronize()
+        keep = busy() if stream is not None else None
+        t.fill_(-77)                                     # behind that work
+        del t
+        e = c.cache.evict(c.table, c.lens_t, c.table, w, 40, 2, 5, out_weights=ow, stream=stream)
+        torch.cuda.synchronize()
+        got = [e["rows"].clone(), e["lens"].clone()]
+        if want is None:
+            want = got
+        set_pool(c)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        del keep, e, held
+    c.done()
