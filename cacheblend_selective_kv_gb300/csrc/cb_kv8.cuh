@@ -28,7 +28,8 @@ struct Kv8 {
     float* part;             // attention: pieces of items that span CTAs
     int* todo;               // attention of many rows: items to be joined, four ints per CTA
     unsigned* arrived;       // attention: pieces finished, one count per CTA (0 between calls)
-    void* scratch;           // the allocation that holds the six above
+    unsigned* voided;        // attention: the last call's offsets decrease
+    void* scratch;           // the allocation that holds the seven above
     alignas(64) unsigned char map[128];   // tensor map of the codes
 };
 

@@ -40,6 +40,7 @@ struct AttnArgs {
     float* scores;                       // weights: scores in the exp2 domain (score_of), score_ld per column
     int score_ld;                        // max_len rounded up to TK
     float2* stats;                       // weights: [Hkv][n_q][G] (max, 1 / sum)
+    unsigned* voided;                    // weights: the call's offsets decrease, nothing was computed (NULL: no query rows)
 };
 
 // k / G and k % G of a column or row of an item
@@ -54,7 +55,7 @@ __device__ __forceinline__ float exp2_fast(float x) {          // special-functi
 // ------------------------------------------------------------------------------------------------
 // the list of tiles
 // ------------------------------------------------------------------------------------------------
-struct Seq {                             // one sequence: its query rows and length
+struct Seq {                             // one sequence: its query rows and length (-1: its offsets decrease)
     int r0, n, len;
     __device__ __forceinline__ int q_tiles(int QT) const { return (n + QT - 1) / QT; }
     // keys that the last row of query tile qt sees
@@ -64,7 +65,7 @@ struct Seq {                             // one sequence: its query rows and len
 __device__ __forceinline__ Seq seq_at(const AttnArgs& p, int s) {
     Seq q;
     int r1;
-    if (!kv8_rows(p.q, p.r, s, q.r0, r1, q.len)) return Seq{0, 0, 0};
+    if (!kv8_rows(p.q, p.r, s, q.r0, r1, q.len)) return Seq{0, 0, r1 < q.r0 ? -1 : 0};
     q.n = r1 - q.r0;
     return q;
 }
@@ -192,26 +193,34 @@ __device__ __forceinline__ int piece_count(const AttnArgs& p, const Find& f, int
 
 // Finds it and the cursor at its first tile, THREADS sequences at a time (the first step's are kept); before and after run
 // around the first barrier, which also publishes what the caller has set up in shared memory.  (The host refuses calls of
-// 2^31 places.  This and what ends an item run once or twice per CTA, from instructions that have to be fetched first: short
+// 2^31 places, counted for rows that each belong to one sequence at most.  Offsets that decrease could give rows to several,
+// whose scores would lie on one another and whose places could pass 32 bits: then every CTA gets an empty piece.  This and what ends an item run once or twice per CTA, from instructions that have to be fetched first: short
 // loops and 32-bit arithmetic are worth more here than fewer steps.)
 template <int THREADS, typename F, typename H>
 __device__ __forceinline__ void find_piece(const AttnArgs& p, Find& f, Piece& mine, Cursor& cur, F before_sync, H after_sync) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const Seq q_own = tid < p.q.n ? seq_at(p, tid) : Seq{0, 0, 0};
     const int n_own = seq_places(p, q_own);
+    bool decrease = q_own.len < 0;
     {
         int sum = n_own;
 #pragma unroll 1
-        for (int s = tid + THREADS; s < p.q.n; s += THREADS) sum += seq_places(p, seq_at(p, s));
+        for (int s = tid + THREADS; s < p.q.n; s += THREADS) {
+            const Seq q = seq_at(p, s);
+            decrease |= q.len < 0;
+            sum += seq_places(p, q);
+        }
         sum = __reduce_add_sync(0xffffffffu, sum);
         if (lane == 0) f.sums[warp] = sum;
     }
     before_sync();
-    __syncthreads();
+    decrease = __syncthreads_or(decrease);
     after_sync();
+    if (blockIdx.x == 0 && tid == 0) *p.voided = decrease;
     const int total = __reduce_add_sync(0xffffffffu, lane < THREADS / 32 ? f.sums[lane] : 0);
     mine.per = max((int)(((unsigned)total + gridDim.x - 1) / gridDim.x), p.min_places);
     mine.count = 0;
+    if (decrease) return;
     const long long at = (long long)blockIdx.x * mine.per;
     if (at >= total) return;
     const int p0 = (int)at;

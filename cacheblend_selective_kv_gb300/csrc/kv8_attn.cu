@@ -611,7 +611,7 @@ __global__ void __launch_bounds__(512) kv8_weights_kernel(const AttnArgs p) {
     const int x = threadIdx.x, y = threadIdx.y, bx = blockDim.x, by = blockDim.y, g = blockIdx.y;
     const int quad = blockIdx.x * bx + x, t = quad / (TK / 4), j = quad * 4;
     const Seq q = seq_at(p, blockIdx.z);
-    if (blockIdx.x * 4 * bx >= q.len) return;
+    if (blockIdx.x * 4 * bx >= q.len || (p.voided && *p.voided)) return;
     float w[4] = {0.f, 0.f, 0.f, 0.f};
     if (j < q.len) {
         const float* score = score_of(p, q, g, t, 0) + (j - t * TK);
@@ -730,6 +730,7 @@ cudaError_t launch_kv8_attention(const Kv8& c, const Kv8Seqs& q, const Kv8Rows& 
     p.box = c.cfg.page_size < TK ? c.cfg.page_size : TK;
     p.part = c.part;
     p.arrived = c.arrived;
+    p.voided = r.n_rows > 0 ? c.voided : nullptr;
     p.scores = a.weights && q.max_len > 0 ? c.scores : nullptr;      // (no keys: no weights to return)
     p.stats = c.stats;
     p.score_ld = (q.max_len + TK - 1) / TK * TK;

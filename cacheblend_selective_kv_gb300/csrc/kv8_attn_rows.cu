@@ -601,7 +601,7 @@ __global__ void __launch_bounds__(256) kv8_rows_weights_kernel(const AttnArgs p)
     grid_dep_wait();
     const int at = blockIdx.x * 8 + (threadIdx.x >> 5), quad = at % (TK / 4), lane = threadIdx.x & 31, j = at * 4, g = blockIdx.y;
     const Seq q = seq_at(p, blockIdx.z);
-    if (j >= q.len) return;
+    if (j >= q.len || *p.voided) return;
     const int seen = max(0, j - (q.len - q.n)) * p.G, cols = q.n * p.G;      // columns that see key j: [seen, cols)
     const float4* score = quads_of(p, q, g, at / (TK / 4)) + (int64_t)quad * cols;
     const float2* st = p.stats + ((int64_t)g * p.r.n_rows + q.r0) * p.G;

@@ -41,6 +41,13 @@ struct Block {
     int page;
 };
 
+// Offsets that decrease are recorded by the first CTA: the search below may pass them by.
+__device__ __forceinline__ void kv8_check_offsets(const Kv8Seqs& q, const Kv8Rows& r) {
+    if (!r.start || blockIdx.x > 0 || blockIdx.y > 0) return;
+    for (int s = threadIdx.x; s < q.n; s += THREADS)
+        if (r.start[s + 1] < r.start[s]) atomicOr(q.status, ST_BAD_ROW);
+}
+
 // the block of slot u; false when the slot has none
 __device__ __forceinline__ bool kv8_block(const Kv8Seqs& q, const Kv8Rows& r, int per_seq, int u, Block& b) {
     int s, local;
@@ -147,6 +154,7 @@ __global__ void __launch_bounds__(THREADS) kv8_write_kernel(const CacheArgs a) {
     grid_dep_launch();
     grid_dep_wait();
     __shared__ unsigned sm[THREADS / 32];
+    kv8_check_offsets(a.q, a.r);
     const int tpb = 1 << a.tpb_shift, group = threadIdx.x >> a.tpb_shift, t = threadIdx.x & (tpb - 1);
     const int unit = blockIdx.x * (THREADS >> a.tpb_shift) + group;
     const int lk = blockIdx.y, kv = lk & 1, l = lk >> 1;
@@ -251,6 +259,7 @@ __global__ void __launch_bounds__(THREADS) kv8_read_kernel(const CacheArgs a) {
     constexpr int VN = Vec<T>::N, NB = 4;
     grid_dep_launch();
     grid_dep_wait();
+    kv8_check_offsets(a.q, a.r);
     const int tpb = 1 << a.tpb_shift, group = threadIdx.x >> a.tpb_shift, t = threadIdx.x & (tpb - 1);
     const int unit = blockIdx.x * (THREADS >> a.tpb_shift) + group;
     const int lk = blockIdx.y, kv = lk & 1, l = lk >> 1;

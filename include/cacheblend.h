@@ -311,7 +311,9 @@ typedef struct {
 /* A batch of sequences: row j of sequence s is row j % page_size of page table[s * table_ld + j / page_size].  All
  * arrays are device int32 and are read when the call's kernels run, so a captured graph follows their contents.
  * A page id outside the pool, a length outside [0, max_len] or row offsets out of range are recorded as
- * CB_STATUS_BAD_ROW (read with cb_kv8_status) and their rows are skipped (attention: such keys are not seen).
+ * CB_STATUS_BAD_ROW (read with cb_kv8_status) and their rows are skipped (attention: such keys are not seen).  Row
+ * offsets that decrease are recorded too; attention then computes nothing at all, and which rows a write or a read
+ * takes is not defined.
  * A length of 0 marks a free place of a batch: its table is not read and rows that fall to it are neither written nor
  * read (attention: they give 0). */
 typedef struct {

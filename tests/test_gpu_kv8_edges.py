@@ -271,3 +271,44 @@ def test_evict_outputs_made_by_a_call_on_a_stream(cb):
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
         del keep, e, held
     c.done()
+
+
+@pytest.mark.parametrize("rows", [4, 40])
+def test_offsets_that_decrease(cb, rows):
+    """Offsets that go back would give rows to two sequences: nothing is computed and the call is recorded."""
+    lens = [100, 60, 300, 80]
+    c = Case(cb, lens, H=2, G=4, hd=64, P=16, seed=rows, cells=cb.KV8Cache.cells(2 * rows, 8, 300))
+    q, q64 = c.values(2 * rows, 8, 64)
+    for st in ([0, rows, 0, rows, 2 * rows], [0, 2 * rows, rows, rows, 2 * rows], [5, 4, 4, 4, 4]):
+        out = torch.full_like(q, 3.0)
+        w = torch.full((4, 2, 300), 6.0, device="cuda")
+        c.cache.attention(c.table, c.lens_t, q, out, q_start=i32(st), weights=w, max_len=300)
+        torch.cuda.synchronize()
+        assert c.cache.status(clear=True) == cb.CB_STATUS_BAD_ROW
+        assert torch.all(out == 3.0) and torch.all(w == 6.0)
+    # the next call is as any other
+    st, out = [0, rows, rows, rows + 2, 2 * rows], torch.empty_like(q)
+    w = torch.zeros((4, 2, 300), device="cuda")
+    c.cache.attention(c.table, c.lens_t, q, out, q_start=i32(st), weights=w, max_len=300)
+    check_attention(c, q, q64, st, out, w)
+    # offsets that pass the number of rows without going back: those sequences are skipped, the others computed
+    out = torch.full_like(q, 3.0)
+    c.cache.attention(c.table, c.lens_t, q, out, q_start=i32([0, rows, rows + 2, 2 * rows + 1, 2 * rows + 7]), max_len=300)
+    torch.cuda.synchronize()
+    assert c.cache.status(clear=True) == cb.CB_STATUS_BAD_ROW
+    ref = torch.empty_like(q[:rows + 2])
+    c.cache.attention(c.table[:2].contiguous(), c.lens_t[:2].contiguous(), q[:rows + 2], ref, q_start=i32([0, rows, rows + 2]), max_len=300)
+    torch.cuda.synchronize()
+    assert torch.allclose(out[:rows + 2].float(), ref.float(), rtol=2.0 ** -7, atol=1e-6) and torch.all(out[rows + 2:] == 3.0)
+    c.done()
+
+
+@pytest.mark.parametrize("start", [[0, 64, 0, 8], [0, 64, 64, 1], [9, 8, 8, 8]])
+def test_write_and_read_record_offsets_that_decrease(cb, start):
+    c = Case(cb, [64, 64, 64], H=2, hd=64, P=16, seed=3)
+    k, _ = c.values(1, 64, 2, 64)
+    for f in (c.cache.write, c.cache.read):
+        f(c.table, c.lens_t, k, k.clone(), row_start=i32(start))
+        torch.cuda.synchronize()
+        assert c.cache.status(clear=True) == cb.CB_STATUS_BAD_ROW
+    c.done()
