@@ -28,6 +28,18 @@ bool overlap(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
     return a_bytes > 0 && b_bytes > 0 && x < y + b_bytes && y < x + a_bytes;
 }
 
+// Two arrays of n_layers x n_rows rows of w bytes at the same strides, the second `apart` bytes behind the first: does a row
+// of one overlap a row of the other?  Rows l2 - l1 layers and r2 - r1 rows apart do when those strides bring `apart` to
+// less than w; for each distance in layers the two nearest in rows are looked at.
+bool rows_overlap(int64_t apart, int64_t w, int64_t row_stride, int32_t n_rows, int64_t layer_stride, int32_t n_layers) {
+    for (int64_t l = 1 - n_layers; l < n_layers; ++l) {
+        const int64_t d = apart + l * layer_stride, below = d >= 0 ? d / row_stride : -((-d + row_stride - 1) / row_stride);
+        for (int64_t r = below; r <= below + 1; ++r)             // d - r rows: the nearest to 0 from both sides
+            if (r > -(int64_t)n_rows && r < n_rows && std::llabs(d - r * row_stride) < w) return true;
+    }
+    return false;
+}
+
 cb_status check_handle(const cb_kv8* c, const char* who) {
     set_last_error("");
     return c ? CB_OK : fail(CB_ERR_INVALID_ARG, "%s: null cache", who);
@@ -107,7 +119,10 @@ cb_status check_io(const cb_kv8& c, const void* k, const void* v, int64_t layer_
     const bool apart = layer_stride >= (n_rows - 1) * row_stride + w || (layer_stride >= w && row_stride >= (n_layers - 1) * layer_stride + w);
     if (n_layers > 1 && !apart && (output || layer_stride != 0))
         return fail(CB_ERR_INVALID_ARG, "%s: the layers' rows overlap (layer stride %lld)", who, (long long)layer_stride);
-    if (output && overlap(k, w * es, v, w * es)) return fail(CB_ERR_INVALID_ARG, "%s: k and v overlap", who);
+    // (rows that span 2^40 bytes are on no device: of those only the first are compared)
+    const int32_t looked = row_stride * es < ((int64_t)1 << 40) / n_rows ? n_rows : 1;
+    if (output && rows_overlap((const char*)v - (const char*)k, w * es, row_stride * es, looked, layer_stride * es, n_layers))
+        return fail(CB_ERR_INVALID_ARG, "%s: k and v overlap", who);
     io = Kv8Io{const_cast<void*>(k), const_cast<void*>(v), layer_stride, row_stride, c.cfg.dtype == CB_BF16};
     return CB_OK;
 }

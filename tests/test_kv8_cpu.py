@@ -245,3 +245,32 @@ def test_evict_refuses_overlapping_tables(lib):
     refused(call(dst=A + 2 * 4 * 4), "overlaps")
     reaches_device(call(dst=A, dld=2, n=1))            # one sequence: its first pages, in place
     reaches_device(call(dst=A + 3 * 4 * 4))
+
+
+def test_read_refuses_overlapping_outputs(lib):
+    """k and v that meet in any of their rows, against a search over all pairs of rows."""
+    h = fake(n_kv_heads=2)                             # rows of 128 elements, 256 bytes
+
+    def call(apart, ls, rs, rows=6, n_layers=3):
+        return lib.cb_kv8_read(ctypes.addressof(h), seqs(), 0, n_layers, 8 * A, 8 * A + 2 * apart, ls, rs, A, rows, None)
+
+    def distances(ls, rs, rows=6, n_layers=3):
+        at = [l * ls + r * rs for l in range(n_layers) for r in range(rows)]
+        return sorted({b - a for a in at for b in at})
+
+    for ls, rs in ((6 * 128, 128), (12 * 128, 128), (6 * 256, 256), (128, 3 * 128), (256, 6 * 128), (7 * 192, 192), (128, 4 * 128)):
+        both, far = set(), distances(ls, rs)
+        for apart in range(-40 * 128, 40 * 128 + 1, 8):
+            want = any(abs(apart + d) < 128 for d in far)
+            both.add(want)
+            code = call(apart, ls, rs)
+            refused(code, "k and v overlap") if want else reaches_device(code)
+        assert both == {True, False}
+    refused(call(128, 6 * 128, 128), "k and v overlap")                # v is k without its first row
+    refused(call(6 * 128, 6 * 128, 128), "k and v overlap")            # ... without its first layer
+    reaches_device(call(6 * 128, 12 * 128, 128))                       # the halves of [layers][2][rows]
+    reaches_device(call(128, 6 * 256, 256))                            # halves of a row
+    reaches_device(call(3 * 128, 128, 6 * 128))                        # layers interleaved row by row, then K and V
+    # a write's inputs may meet
+    code = lib.cb_kv8_write(ctypes.addressof(h), seqs(), 0, 3, 8 * A, 8 * A + 256, 6 * 128, 128, A, 6, None)
+    reaches_device(code)
