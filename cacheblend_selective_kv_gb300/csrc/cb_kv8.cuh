@@ -97,6 +97,11 @@ __device__ __forceinline__ float kv8_mag(float x) {
 }
 // an infinity has no e4m3 code and is kept as NaN rather than as a large finite value
 __device__ __forceinline__ float kv8_nan_inf(float x) { return fabsf(x) <= 3.402823466e38f ? x : __int_as_float(0x7fc00000); }
+// A scale of 2^120 ends at the code 240, because 256 * 2^120 is not finite: finite values above 240 times it stand for that.
+__device__ __forceinline__ float kv8_storable(float x) {
+    const float m = 3.1901471e38f;                     // 240 * 2^120
+    return fabsf(x) <= 3.402823466e38f ? fminf(fmaxf(x, -m), m) : __int_as_float(0x7fc00000);
+}
 
 __device__ __forceinline__ unsigned kv8_max_u16x2(unsigned a, unsigned b) {
     unsigned r;

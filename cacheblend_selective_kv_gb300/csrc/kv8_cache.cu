@@ -95,11 +95,12 @@ __device__ __forceinline__ unsigned group_max(unsigned v, int tpb, unsigned* sm)
 }
 
 // 16 bytes of a row.  Magnitudes compare as integers, so the largest is found on the packed words; the bits of an
-// infinity or a NaN are above every finite number's, which is how a block that holds one is noticed.
+// infinity or a NaN are above every finite number's, which is how a block that holds one is noticed, or a number from
+// 248 * 2^120 on (LAST), which would round to a code whose value is not finite.
 template <typename T> struct Vec;
 template <> struct Vec<bf16> {
     static constexpr int N = 8;
-    static constexpr unsigned INF = 0x7f80u;
+    static constexpr unsigned LAST = 0x7f78u;
     __device__ static unsigned top(const uint4& u, unsigned m) {           // two running maxima in m
         m = kv8_max_u16x2(m, u.x & 0x7fff7fffu);
         m = kv8_max_u16x2(m, u.y & 0x7fff7fffu);
@@ -119,7 +120,7 @@ template <> struct Vec<bf16> {
 };
 template <> struct Vec<float> {
     static constexpr int N = 4;
-    static constexpr unsigned INF = 0x7f800000u;
+    static constexpr unsigned LAST = 0x7f780000u;
     __device__ static unsigned top(const uint4& u, unsigned m) {
         m = max(m, max(u.x & 0x7fffffffu, u.y & 0x7fffffffu));
         return max(m, max(u.z & 0x7fffffffu, u.w & 0x7fffffffu));
@@ -183,7 +184,7 @@ __global__ void __launch_bounds__(THREADS) kv8_write_kernel(const CacheArgs a) {
 #pragma unroll
     for (int i = 0; i < NP; ++i) m = Vec<T>::top(x[i], m);
     unsigned top = group_max(Vec<T>::joined(m), tpb, sm);
-    const bool special = top >= Vec<T>::INF;           // an infinity or a NaN: the finite maximum, and infinities to NaN
+    const bool special = top >= Vec<T>::LAST;          // the finite maximum, infinities to NaN, what is storable of the rest
     if (__syncthreads_or(special)) {
         float f[VN], f_top = 0.f;
 #pragma unroll
@@ -221,7 +222,7 @@ __global__ void __launch_bounds__(THREADS) kv8_write_kernel(const CacheArgs a) {
         Vec<T>::get(x[i], f);
         if (special) {
 #pragma unroll
-            for (int k = 0; k < VN; ++k) f[k] = kv8_nan_inf(f[k]);
+            for (int k = 0; k < VN; ++k) f[k] = kv8_storable(f[k]);
         }
         uint32_t w[VN / 4];
 #pragma unroll

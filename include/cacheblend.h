@@ -289,8 +289,9 @@ int64_t cb_pages_free(const cb_pages* pages);
  *   codes   device [n_layers][2][n_pages][n_kv_heads][page_size][head_dim] e4m3 bytes (2 = K, V), 128-byte aligned
  *   scales  device float32 [n_layers][2][n_pages][n_kv_heads]; a value is code * scale
  * A scale is a power of two, or 0 for a block of zeros: the smallest s with max|x| <= 448 s over the block's finite
- * values, not below 2^-126, and a code is x / s rounded to nearest even.  Values read back are exact in bf16 and
- * fp32.  A NaN or an infinity is kept as NaN and does not count for the scale.
+ * values, not below 2^-126, and a code is x / s rounded to nearest even (at s = 2^120 to 240 at most, so that a finite
+ * value stays finite).  Values read back are exact in bf16 and fp32.  A NaN or an infinity is kept as NaN and does not
+ * count for the scale.
  * Both buffers are the caller's.  A handle borrows them, knows their geometry and owns the scratch of its calls.  It
  * lives on the device that was current at creation; its calls run there whichever device is current, on a stream of
  * that device.  Calls on one handle must not overlap on the GPU (they share its scratch and its pages); two handles

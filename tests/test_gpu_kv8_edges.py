@@ -312,3 +312,46 @@ def test_write_and_read_record_offsets_that_decrease(cb, start):
         torch.cuda.synchronize()
         assert c.cache.status(clear=True) == cb.CB_STATUS_BAD_ROW
     c.done()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_largest_finite_values_stay_finite(cb, dtype):
+    """A scale of 2^120 ends at the code 240, the last whose value is finite: values above 248 * 2^120 round to it.  Written
+    as whole pages and appended to a block that has that scale, or a smaller one, already."""
+    P, H, hd = 16, 2, 64
+    c = Case(cb, [3 * P], H=H, hd=hd, P=P, dtype=dtype, seed=2)
+    top = float(torch.finfo(c.td).max)
+    x = c.rng.uniform(2.0 ** 126, top, size=(1, 3 * P, H, hd)) * c.rng.choice([-1, 1], size=(1, 3 * P, H, hd))
+    x[0, 0, 0, :4] = top, -top, 247.9 * 2.0 ** 120, -248.1 * 2.0 ** 120
+    x[0, 1, 1, :2] = np.nan, np.inf
+    x[0, P:P + 7] *= 2.0 ** -30
+    t = torch.from_numpy(x.astype(np.float32)).to(c.td)
+    t[0, 2, 0, 0] = top                                  # (as the type rounds it, not beyond)
+    t = torch.where(torch.isinf(t) & torch.tensor(np.isfinite(x)), torch.sign(t) * top, t).cuda()
+    x = f64(t)
+    lens = []
+    for n, m in ((P + 7, P + 7), (3 * P, 2 * P - 7)):     # the second call's rows begin inside the second page
+        c.cache.write(c.table, i32([n]), t[:, n - m:n].contiguous(), t[:, n - m:n].contiguous(), max_len=3 * P)
+        lens.append(n)
+    ko, vo = torch.zeros_like(t), torch.zeros_like(t)
+    c.cache.read(c.table, i32([3 * P]), ko, vo, max_len=3 * P)
+    torch.cuda.synchronize()
+    want = np.zeros_like(x)
+    for b in range(3):
+        for h in range(H):
+            rows = x[0, b * P:(b + 1) * P, h]
+            parts = [rows] if b != 1 else [rows[:7], rows[7:]]
+            was = 0.0
+            done = np.zeros((0, hd))
+            for p in parts:
+                s = max(km.scale_of(p), was)
+                if was:
+                    done = km.VALUES[km.encode(done / s)] * s
+                limit = 240.0 if s == 2.0 ** 120 else 448.0
+                new = km.VALUES[km.encode(np.clip(km.divide(p, s), -limit, limit))] * s
+                done, was = np.concatenate([done, new]), s
+            want[0, b * P:(b + 1) * P, h] = done
+    for got in (f64(ko), f64(vo)):
+        assert np.array_equal(got, want, equal_nan=True)
+    assert np.isfinite(want).sum() == want.size - 2 and (np.abs(want) == 240 * 2.0 ** 120).sum() > 10
+    c.done()
