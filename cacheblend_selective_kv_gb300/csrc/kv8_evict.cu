@@ -205,14 +205,15 @@ __global__ void __launch_bounds__(ST, 2) kv8_select_kernel(const EvictArgs a, in
     grid_dep_wait();
     const int g = blockIdx.x, s = blockIdx.y, l = blockIdx.z;
     const int len = kv8_len(a.q, s);
-    if (len < 0 || len > a.q.max_len) {
-        if (threadIdx.x == 0) atomicOr(a.q.status, ST_BAD_ROW);
-        return;
-    }
     const int64_t seg = ((int64_t)l * a.q.n + s) * a.Hkv + g;
     const float* w = a.e.weights + seg * a.e.weights_ld;
     float* ow = a.e.out_weights + seg * a.e.weights_ld;
     int* rows = a.e.out_rows + seg * a.e.keep;
+    if (len < 0 || len > a.q.max_len) {                 // keeps nothing
+        if (threadIdx.x == 0) atomicOr(a.q.status, ST_BAD_ROW);
+        for (int j = threadIdx.x; j < a.e.keep; j += ST) rows[j] = -1;
+        return;
+    }
     if (len <= cached) select_rows<true>(a, w, cache, ow, rows, len);
     else select_rows<false>(a, w, cache, ow, rows, len);
 }
@@ -277,8 +278,7 @@ __global__ void __launch_bounds__(MT) kv8_move_kernel(const EvictArgs a, int vec
     const int g = blockIdx.y % a.Hkv, lk = blockIdx.y / a.Hkv, s = blockIdx.z, t = threadIdx.x, threads = blockDim.x;
     const int l = lk >> 1, kv = lk & 1, P = 1 << a.q.shift, vpr_shift = a.hd == 128 ? 3 : 2;
     const int len = kv8_len(a.q, s);
-    if (len < 0 || len > a.q.max_len) return;
-    const int kept = min(len, a.e.keep), pages = (kept + P - 1) >> a.q.shift;
+    const int kept = len < 0 || len > a.q.max_len ? 0 : min(len, a.e.keep), pages = (kept + P - 1) >> a.q.shift;
     // out_lens may be the lengths read above: a CTA that sees the new one finds the same `kept`
     if (blockIdx.x == 0 && blockIdx.y == 0 && t == 0) a.e.out_lens[s] = kept;
     const int* rows = a.e.out_rows + (((int64_t)l * a.q.n + s) * a.Hkv + g) * a.e.keep;

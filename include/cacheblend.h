@@ -383,6 +383,7 @@ cb_status cb_kv8_attention(cb_kv8* cache, const cb_kv8_seqs* seqs, int32_t layer
  *   out_weights  the same shape, or weights itself: the kept rows' weights at entries 0 .. kept - 1, 0 at kept .. len - 1
  *   out_rows     device int32 [n_layers][n_seqs][n_kv_heads][n_keep]: the kept rows, ascending, -1 behind the last
  *   out_lens     device int32 [n_seqs]: min(len, n_keep); may be seqs->lens (where one call evicts all layers)
+ * A sequence whose length is out of range keeps no row: its out_rows are -1, its out_lens 0, its weights as they were.
  * Async on `stream`; no allocation. */
 cb_status cb_kv8_evict(cb_kv8* cache, const cb_kv8_seqs* seqs, const int32_t* dst_table, int32_t dst_ld, int32_t layer,
                        int32_t n_layers, const float* weights, int32_t weights_ld, int32_t n_keep, int32_t n_sink,

@@ -355,3 +355,32 @@ def test_largest_finite_values_stay_finite(cb, dtype):
         assert np.array_equal(got, want, equal_nan=True)
     assert np.isfinite(want).sum() == want.size - 2 and (np.abs(want) == 240 * 2.0 ** 120).sum() > 10
     c.done()
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+def test_evict_with_lengths_out_of_range(cb, in_place):
+    """A sequence whose length is out of range is recorded and keeps nothing: 0 rows, -1 for each, whatever stood in the
+    outputs before."""
+    lens = [65, 50, -3, 20]
+    c = Case(cb, [64, 50, 30, 20], H=2, hd=64, P=16, seed=7, extra=12)
+    dst = c.table if in_place else i32(np.array(c.free[:12]).reshape(4, 3))
+    w = torch.rand((1, 4, 2, 64), device="cuda")
+    w0 = w.cpu().numpy()
+    rows, new = torch.full((1, 4, 2, 33), 12345, dtype=torch.int32, device="cuda"), i32([9, 9, 9, 9])
+    c.cache.evict(c.table, i32(lens), dst, w, 33, 1, 2, out_rows=rows, out_lens=new, max_len=64)
+    torch.cuda.synchronize()
+    assert c.cache.status(clear=True) == cb.CB_STATUS_BAD_ROW
+    assert new.tolist() == [0, 33, 0, 20]
+    assert torch.all(rows[:, 0] == -1) and torch.all(rows[:, 2] == -1)
+    assert np.array_equal(w.cpu().numpy()[:, [0, 2]], w0[:, [0, 2]])
+    tab = c.table_np if in_place else np.array(c.free[:12]).reshape(4, 3)
+    for s in (1, 3):
+        r, _, nw = c.model.evict(c.table_np[s:s + 1], lens[s:s + 1], tab[s:s + 1], w0[:, s:s + 1], 33, 1, 2)
+        assert np.array_equal(rows[:, s:s + 1].cpu().numpy(), r) and np.array_equal(w[:, s:s + 1].cpu().numpy(), nw)
+    c.check_pool()
+    # the lengths themselves as the output
+    ln = i32(lens)
+    c.cache.evict(c.table, ln, c.table, w, 33, 1, 2, out_lens=ln, max_len=64)
+    torch.cuda.synchronize()
+    assert ln.tolist() == [0, 33, 0, 20] and c.cache.status(clear=True) == cb.CB_STATUS_BAD_ROW
+    c.done()
