@@ -886,19 +886,21 @@ cb_status cb_blend_kv8(cb_model* mp, const int32_t* tokens, int32_t n_tokens, cb
     }
     ks[0] = ks[1];
     // the context rows out of the pool, into rows 0 .. n_ctx - 1 of every (layer, K|V) block of the working copy
+    cb_kv8 pool = *cache;                              // (the handle of these two calls: bad pages are the model's status too)
+    pool.also = m.status;
     const int P = cache->cfg.page_size;
     const int64_t nkv = (int64_t)c.n_kv_heads * c.head_dim, block = (int64_t)n_tokens * nkv;
     char* v0 = (char*)work_kv + block * (int64_t)act_size(m);
     if (n_ctx > 0) {
         const cb_kv8_seqs src = {1, src_table, (n_ctx + P - 1) / P, nullptr, n_ctx};
-        st = cb_kv8_read(cache, &src, 0, L, work_kv, v0, 2 * block, nkv, nullptr, n_ctx, stream);
+        st = cb_kv8_read(&pool, &src, 0, L, work_kv, v0, 2 * block, nkv, nullptr, n_ctx, stream);
         if (st != CB_OK) return st;
     }
     st = blend_impl(m, tokens, n_tokens, work_kv, t, n_chunks, n_ctx, ks, work_kv, out_logits, out_selected, out_dev, stats,
                     (cudaStream_t)stream);
     if (st != CB_OK) return st;
     const cb_kv8_seqs dst = {1, dst_table, (n_tokens + P - 1) / P, nullptr, n_tokens};
-    st = cb_kv8_write(cache, &dst, 0, L, work_kv, v0, 2 * block, nkv, nullptr, n_tokens, stream);
+    st = cb_kv8_write(&pool, &dst, 0, L, work_kv, v0, 2 * block, nkv, nullptr, n_tokens, stream);
     if (st == CB_OK && stats) {
         stats->kernel_launches += n_ctx > 0 ? 2 : 1;
         stats->kv_bytes_moved += 2.0 * L * ((double)n_ctx + n_tokens) * (double)nkv * (1.0 + (double)act_size(m));

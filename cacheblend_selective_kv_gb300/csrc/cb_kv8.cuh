@@ -30,6 +30,7 @@ struct Kv8 {
     unsigned* arrived;       // attention: pieces finished, one count per CTA (0 between calls)
     unsigned* voided;        // attention: the last call's offsets decrease
     void* scratch;           // the allocation that holds the seven above
+    unsigned* also;          // a blend's write and read: the model's status, which gets their bits too (else NULL)
     alignas(64) unsigned char map[128];   // tensor map of the codes
 };
 

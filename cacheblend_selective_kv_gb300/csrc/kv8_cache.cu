@@ -41,15 +41,20 @@ struct Block {
     int page;
 };
 
+__device__ __forceinline__ void kv8_bad_row(const Kv8Seqs& q, unsigned* also) {
+    atomicOr(q.status, ST_BAD_ROW);
+    if (also) atomicOr(also, ST_BAD_ROW);
+}
+
 // Offsets that decrease are recorded by the first CTA: the search below may pass them by.
 __device__ __forceinline__ void kv8_check_offsets(const Kv8Seqs& q, const Kv8Rows& r) {
     if (!r.start || blockIdx.x > 0 || blockIdx.y > 0) return;
     for (int s = threadIdx.x; s < q.n; s += THREADS)
-        if (r.start[s + 1] < r.start[s]) atomicOr(q.status, ST_BAD_ROW);
+        if (r.start[s + 1] < r.start[s]) kv8_bad_row(q, nullptr);
 }
 
 // the block of slot u; false when the slot has none
-__device__ __forceinline__ bool kv8_block(const Kv8Seqs& q, const Kv8Rows& r, int per_seq, int u, Block& b) {
+__device__ __forceinline__ bool kv8_block(const Kv8Seqs& q, const Kv8Rows& r, int per_seq, int u, unsigned* also, Block& b) {
     int s, local;
     if (per_seq > 0) {
         s = u / per_seq;
@@ -65,11 +70,14 @@ __device__ __forceinline__ bool kv8_block(const Kv8Seqs& q, const Kv8Rows& r, in
     }
     if (s >= q.n || local < 0) return false;
     int r0, r1, len;
-    if (!kv8_rows(q, r, s, r0, r1, len)) return false;
+    if (!kv8_rows(q, r, s, r0, r1, len)) {
+        kv8_bad_row(q, also);
+        return false;
+    }
     const int n = r1 - r0;
     if (n == 0) return false;
     if (n > len) {
-        if (len > 0) atomicOr(q.status, ST_BAD_ROW);   // (no length: a free place of the batch)
+        if (len > 0) kv8_bad_row(q, also);             // (no length: a free place of the batch)
         return false;
     }
     const int P = 1 << q.shift, first = len - n;
@@ -79,6 +87,7 @@ __device__ __forceinline__ bool kv8_block(const Kv8Seqs& q, const Kv8Rows& r, in
     b.hi = min(len - blk * P, P);
     b.src_row = r0 + blk * P + b.lo - first;           // source row of block row lo
     b.page = kv8_page(q, s, blk);
+    if (b.page < 0) kv8_bad_row(q, also);
     return b.page >= 0;
 }
 
@@ -142,6 +151,7 @@ struct CacheArgs {
     int64_t layer_stride, row_stride;
     uint8_t* codes;
     float* scales;
+    unsigned* also;           // a second status word, or NULL
     int per_seq, units;       // units = slots * Hkv
     int Hkv, hd, layer;
     int tpb_shift;            // log2 of the threads of a block's group
@@ -162,7 +172,7 @@ __global__ void __launch_bounds__(THREADS) kv8_write_kernel(const CacheArgs a) {
     const int P = 1 << a.q.shift;
     Block b{};
     const int slot = unit / a.Hkv, head = unit - slot * a.Hkv;
-    const bool live = unit < a.units && kv8_block(a.q, a.r, a.per_seq, slot, b);
+    const bool live = unit < a.units && kv8_block(a.q, a.r, a.per_seq, slot, a.also, b);
     const int row0 = t >> a.vpr_shift, rows = tpb >> a.vpr_shift, e = (t & ((1 << a.vpr_shift) - 1)) * VN;
     const int64_t blk = ((int64_t)((a.layer + l) * 2 + kv) * a.q.n_pages + b.page) * a.Hkv + head;
     uint4 x[NP];
@@ -267,7 +277,7 @@ __global__ void __launch_bounds__(THREADS) kv8_read_kernel(const CacheArgs a) {
     const int P = 1 << a.q.shift;
     Block b{};
     const int slot = unit / a.Hkv, head = unit - slot * a.Hkv;
-    if (unit >= a.units || !kv8_block(a.q, a.r, a.per_seq, slot, b)) return;
+    if (unit >= a.units || !kv8_block(a.q, a.r, a.per_seq, slot, a.also, b)) return;
     const int row0 = t >> a.vpr_shift, rows = tpb >> a.vpr_shift, e = (t & ((1 << a.vpr_shift) - 1)) * VN;
     const int64_t blk = ((int64_t)((a.layer + l) * 2 + kv) * a.q.n_pages + b.page) * a.Hkv + head;
     const uint8_t* src = a.codes + blk * P * a.hd + e;
@@ -322,6 +332,7 @@ CacheArgs cache_args(const Kv8& c, const Kv8Seqs& q, const Kv8Rows& r, const Kv8
     a.row_stride = io.row_stride;
     a.codes = c.codes;
     a.scales = c.scales;
+    a.also = c.also;
     a.per_seq = sl.per_seq;
     a.Hkv = c.cfg.n_kv_heads;
     a.units = sl.total * a.Hkv;

@@ -394,7 +394,9 @@ cb_status cb_kv8_evict(cb_kv8* cache, const cb_kv8_seqs* seqs, const int32_t* ds
  * work_kv, the blend runs there, and all n_tokens rows are written through dst_table (device int32, one entry per
  * page_size rows; copy-on-write as for cb_blend_paged).  The cache and the model must agree in n_layers, n_kv_heads,
  * head_dim and dtype.  All other arguments are those of cb_blend_paged; logits and work_kv come from the unrounded
- * blend, the pool holds it in 8 bits. */
+ * blend, the pool holds it in 8 bits.  A page id outside the pool is recorded as CB_STATUS_BAD_ROW in the model's status
+ * (cb_model_status), as cb_blend_paged records it, and in the cache's; its rows are skipped, so that the blend reads what
+ * stood in those rows of work_kv. */
 cb_status cb_blend_kv8(cb_model* model, const int32_t* tokens, int32_t n_tokens, cb_kv8* cache,
                        const int32_t* src_table, const int32_t* dst_table, const cb_chunk* chunks, int32_t n_chunks,
                        const double* ratios, int32_t n_ratios, void* work_kv, float* out_logits, int32_t* out_selected,

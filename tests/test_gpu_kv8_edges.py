@@ -384,3 +384,32 @@ def test_evict_with_lengths_out_of_range(cb, in_place):
     torch.cuda.synchronize()
     assert ln.tolist() == [0, 33, 0, 20] and c.cache.status(clear=True) == cb.CB_STATUS_BAD_ROW
     c.done()
+
+
+@pytest.mark.parametrize("which", ["src", "dst"])
+def test_blend_records_bad_pages_in_the_model(cb, which):
+    """A page id outside the pool in cb_blend_kv8's tables: in the model's status, where cb_blend_paged's are, and in the
+    cache's."""
+    import test_gpu_gradual as tg
+    w, toks, chunks, caches = tg.tiny5_case()
+    n_ctx, N, P = sum(x[2] for x in chunks), len(toks), 32
+    nb = -(-N // P)
+    model = cb.BlendModel(tg.TINY5.as_dict(), w, max_tokens=N, max_chunks=len(chunks))
+    cache = cb.KV8Cache.empty(5, 2 * nb, 2, P, 64, n_heads=tg.TINY5.n_heads, dtype="f32")
+    tabs = dict(src=torch.arange(nb, dtype=torch.int32, device="cuda"), dst=torch.arange(nb, 2 * nb, dtype=torch.int32, device="cuda"))
+    ctx = tg.device_cache(caches, "f32")
+    cache.write(tabs["src"][None, :-(-n_ctx // P)].contiguous(), None, ctx[:, 0], ctx[:, 1], n_layers=5, max_len=n_ctx)
+    t, work, logits = torch.from_numpy(toks).cuda(), model.kv_buffer(N), torch.empty(1024, device="cuda")
+    work.zero_()
+    args = (chunks, (0.4,) * 4, work, logits)
+    cb.cb_blend_kv8(model.handle, t, N, cache, tabs["src"], tabs["dst"], *args)
+    assert model.status() == 0 and cache.status() == 0
+    work.zero_()
+    tabs[which][1] = 2 * nb
+    cb.cb_blend_kv8(model.handle, t, N, cache, tabs["src"], tabs["dst"], *args)
+    assert model.status(clear=True) == cb.CB_STATUS_BAD_ROW and cache.status(clear=True) == cb.CB_STATUS_BAD_ROW
+    # the cache's own calls are recorded in the cache alone
+    cache.read(tabs[which][None].contiguous(), None, work[:, 0], work[:, 1], n_layers=5, max_len=N)
+    assert cache.status(clear=True) == cb.CB_STATUS_BAD_ROW and model.status() == 0
+    cache.close()
+    model.close()
