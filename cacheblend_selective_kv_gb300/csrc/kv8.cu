@@ -217,9 +217,12 @@ cb_status cb_kv8_status(cb_kv8* c, uint32_t* bits, int32_t clear) {
     OnDevice on;
     st = on.to(c, "cb_kv8_status");
     if (st != CB_OK) return st;
+    // (a memset may still run when it returns, and a call's stream need not wait for it)
     if (cudaDeviceSynchronize() != cudaSuccess || cudaMemcpy(bits, c->status, 4, cudaMemcpyDeviceToHost) != cudaSuccess ||
-        (clear && cudaMemset(c->status, 0, 64) != cudaSuccess))
+        (clear && (cudaMemset(c->status, 0, 64) != cudaSuccess || cudaStreamSynchronize(cudaStreamLegacy) != cudaSuccess))) {
+        cudaGetLastError();
         return fail(CB_ERR_CUDA, "cb_kv8_status: device error");
+    }
     return CB_OK;
 }
 

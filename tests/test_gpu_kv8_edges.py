@@ -413,3 +413,17 @@ def test_blend_records_bad_pages_in_the_model(cb, which):
     assert cache.status(clear=True) == cb.CB_STATUS_BAD_ROW and model.status() == 0
     cache.close()
     model.close()
+
+
+def test_cleared_status_does_not_lose_the_next_call(cb):
+    """What a call on any stream records after status(clear=True) has returned stays recorded."""
+    c = Case(cb, [20], H=1, hd=64, P=16, seed=1)
+    kv, _ = c.values(1, 1, 1, 64)
+    side, bad = torch.cuda.Stream(), i32([-1])
+    torch.cuda.synchronize()
+    for _ in range(200):
+        c.cache.status(clear=True)
+        c.cache.write(c.table, bad, kv, kv, stream=side)
+        assert c.cache.status() == cb.CB_STATUS_BAD_ROW
+    c.cache.status(clear=True)
+    c.done()
