@@ -427,3 +427,161 @@ def test_cleared_status_does_not_lose_the_next_call(cb):
         assert c.cache.status() == cb.CB_STATUS_BAD_ROW
     c.cache.status(clear=True)
     c.done()
+
+
+@pytest.mark.parametrize("dtype,rows", KERNELS)
+def test_queries_with_an_outlier_channel(cb, dtype, rows):
+    """One channel of q 2^11 .. 2^16 times the others, over keys that are 0 there, so that the scores are the small channels'.
+    A bf16 q of few rows is two e4m3 terms, scaled by the row's largest value to at most 448: an element below 2^-6 in
+    those units is off by up to 2^-14, that is 2^-14 / 224 < 2^-21 of the row's largest.  (fp32: six terms, 2^-37; many
+    rows: fp16, exact down to 2^-29 of it.)"""
+    n = 300
+    for size in (2.0 ** 11, 2.0 ** 14, 2.0 ** 16):
+        c = Case(cb, [n], H=2, G=4, hd=64, P=16, dtype=dtype, seed=rows, cells=cb.KV8Cache.cells(rows, 8, n))
+        m = c.model
+        m.codes[0, 0, :, :, :, 9] = 0
+        m.scales[0, 0] = 2.0 ** -3
+        set_pool(c)
+        q, _ = c.values(rows, 8, 64, size=0.25)
+        q[:, :, 9] = size
+        q64 = f64(q)
+        out = torch.empty_like(q)
+        c.cache.attention(c.table, c.lens_t, q, out, max_len=n)
+        ref, _, spread, big = m.attention(c.table_np, c.lens, q64, [0, rows], 0, 0.125)
+        k = m.rows(c.table_np[0], n, 0)[0]
+        ds = 72 * U * big + (2.0 ** -21 * size * np.abs(k).sum(axis=2).max() * 0.125 if dtype == "bf16" and rows <= 8 else 0.0)
+        p_rep, rnd, last = (2.0 ** -11, 2.0 ** -8, 2.0 ** -25) if dtype == "bf16" else (2.0 ** -23, 2.0 ** -24, 2.0 ** -37)
+        tol = rnd * np.abs(ref) + (np.expm1(2 * ds) + 160 * U + p_rep) * spread + last * m.floor + 2.0 ** -32 * m.floor_all
+        assert np.all(np.abs(f64(out) - ref) <= tol)
+        c.done()
+
+
+@pytest.mark.parametrize("rows", [[2, 0, 1, 0, 3], [40, 0, 9, 0, 70]])
+def test_weights_of_sequences_without_rows(cb, rows):
+    """Their keys have received nothing: 0 where the call writes, what was there where it adds."""
+    lens = [400, 77, 129, 256, 90]
+    n = sum(rows)
+    c = Case(cb, lens, H=2, G=3, hd=64, P=16, seed=n, cells=cb.KV8Cache.cells(n, 6, 400))
+    q, q64 = c.values(n, 6, 64)
+    st, out = starts_of(rows), torch.empty_like(q)
+    for add in (False, True):
+        w = torch.full((5, 2, 400), 3.0, device="cuda")
+        c.cache.attention(c.table, c.lens_t, q, out, q_start=i32(st), weights=w, add=add, max_len=400)
+        check_attention(c, q, q64, st, out, w, w_before=3.0 if add else 0.0)
+        for s in (1, 3):
+            assert torch.all(w[s, :, :lens[s]] == (3.0 if add else 0.0)) and torch.all(w[s, :, lens[s]:] == 3.0)
+    c.done()
+
+
+@pytest.mark.parametrize("P,dtype", [(16, "bf16"), (64, "f32"), (256, "bf16")])
+def test_ragged_rows_that_begin_anywhere(cb, P, dtype):
+    """Many sequences whose rows begin and end at any place of a page, in an order of lengths that moves every sequence's
+    blocks: all are written, and read back."""
+    rng = np.random.default_rng(P)
+    for _ in range(4):
+        rows = (rng.integers(0, 3 * P, 40) * rng.integers(0, 2, 40)).tolist()
+        lens = [r + int(rng.integers(0, P + 1)) for r in rows]
+        c = Case(cb, lens, H=1, G=1, hd=64, P=P, dtype=dtype, seed=int(rng.integers(1000)))
+        st = starts_of(rows, int(rng.integers(0, 5)))
+        k, k64 = c.values(1, st[-1] + 1, 1, 64)
+        v, v64 = c.values(1, st[-1] + 1, 1, 64, size=8.0)
+        c.cache.write(c.table, c.lens_t, k, v, row_start=i32(st))
+        c.model.write(c.table_np, lens, k64, v64, st)
+        torch.cuda.synchronize()
+        c.check_pool()
+        ko, vo = torch.full_like(k, 7.0), torch.full_like(v, 7.0)
+        c.cache.read(c.table, c.lens_t, ko, vo, row_start=i32(st))
+        for got, kv in ((f64(ko)[0], 0), (f64(vo)[0], 1)):
+            want = np.full((st[-1] + 1, 1, 64), 7.0)
+            for s, n in enumerate(lens):
+                if rows[s]:
+                    want[st[s]:st[s + 1]] = c.model.rows(c.table_np[s], n, 0)[kv][n - rows[s]:]
+            assert np.array_equal(got, want)
+        c.done()
+
+
+def test_fp32_heads_of_128_of_many_sequences(cb):
+    rng = np.random.default_rng(3)
+    lens = [int(x) for x in rng.integers(0, 700, 70)]
+    lens[3] = 3000
+    c = Case(cb, lens, H=2, G=2, hd=128, P=32, dtype="f32", seed=5, cells=cb.KV8Cache.cells(70, 4, 3000))
+    q, q64 = c.values(70, 4, 128)
+    out, w = torch.empty_like(q), torch.zeros((70, 2, 3000), device="cuda")
+    c.cache.attention(c.table, c.lens_t, q, out, weights=w, max_len=3000)
+    check_attention(c, q, q64, list(range(71)), out, w)
+    c.done()
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+def test_evict_long_sequences_of_several_layers(cb, in_place):
+    """More rows than a selecting block keeps in shared memory, of several layers and sequences at once: rows and weights against
+    a stable sort, and the rows' codes, which a page of one scale keeps."""
+    lens, keep, sink, recent, P, L, H = [20000, 16384, 17001, 500], 3000, 4, 60, 64, 2, 2
+    width = -(-max(lens) // P)
+    need = -(-keep // P)
+    n_pages = 4 * width + 4 * need
+    g = torch.Generator(device="cuda").manual_seed(1)
+    cache = cb.KV8Cache.empty(L, n_pages, H, P, 64, 2 * H)
+    cache.codes.copy_(torch.randint(0, 0x77, cache.codes.shape, generator=g, device="cuda", dtype=torch.uint8))
+    cache.codes[..., 0] = 0x78                           # 256 in every row: each page has the scale of its values
+    cache.scales.fill_(2.0 ** -5)
+    before = cache.codes.clone()
+    order = torch.randperm(n_pages, generator=g, device="cuda").int()
+    table = order[:4 * width].view(4, width).contiguous()
+    dst = table if in_place else order[4 * width:].view(4, need).contiguous()
+    w = torch.randint(0, 500, (L, 4, H, max(lens)), generator=g, device="cuda").float() / 64
+    was, lt = w.clone(), i32(lens)
+    e = cache.evict(table, lt, dst, w, keep, sink, recent, n_layers=L, max_len=max(lens))
+    torch.cuda.synchronize()
+    assert e["lens"].tolist() == [min(n, keep) for n in lens] and cache.status() == 0
+    for l in range(L):
+        for s, n in enumerate(lens):
+            m = min(n, keep)
+            for h in range(H):
+                r = was[l, s, h, :n].clone()
+                r[:sink] = r[n - recent:] = float("inf")
+                want = torch.sort(r, descending=True, stable=True).indices[:m].sort().values
+                assert torch.equal(e["rows"][l, s, h, :m], want.int()) and torch.all(e["rows"][l, s, h, m:] == -1)
+                assert torch.equal(w[l, s, h, :m], was[l, s, h, want]) and torch.count_nonzero(w[l, s, h, m:n]) == 0
+                assert torch.equal(w[l, s, h, n:], was[l, s, h, n:])
+                at = torch.arange(m, device="cuda")
+                for kv in range(2):
+                    got = cache.codes[l, kv, dst[s, at // P].long(), h, at % P]
+                    ref = before[l, kv, table[s, want // P].long(), h, want % P]
+                    assert torch.equal(got, ref)
+                    assert torch.all(cache.scales[l, kv, dst[s, :-(-m // P)].long(), h] == 2.0 ** -5)
+    cache.close()
+
+
+def test_blend_over_the_8bit_pool_in_bf16(cb):
+    """cb_blend_kv8 of a bf16 model on the tensor cores is the read, the gradual blend in place and the write, bit for bit."""
+    import workload
+    shape = workload.ModelShape(3, 1024, 8, 2, 128, 2816, 4096, 5e5, "bf16")
+    w = workload.make_weights(shape, 7)
+    chunks, P = [(0, 256 * i, 256) for i in range(3)], 32
+    n_ctx, N = 768, 768 + 40
+    toks = torch.from_numpy(workload.tokens(0, 5, N, 4096)).cuda()
+    model = cb.BlendModel(shape.as_dict(), w, max_tokens=N, max_chunks=3)
+    nb = -(-N // P)
+    cache = cb.KV8Cache.empty(3, 2 * nb, 2, P, 128, n_heads=8)
+    src = torch.arange(nb, dtype=torch.int32, device="cuda")
+    dst = src + nb
+    g = torch.Generator(device="cuda").manual_seed(4)
+    ctx = torch.randn((3, 2, n_ctx, 2, 128), generator=g, device="cuda").bfloat16()
+    cache.write(src[None, :n_ctx // P].contiguous(), None, ctx[:, 0], ctx[:, 1], n_layers=3, max_len=n_ctx)
+    work, ratios = model.kv_buffer(N), (0.3, 0.2)
+    logits = torch.empty(4096, device="cuda", dtype=torch.float32)
+    cb.cb_blend_kv8(model.handle, toks, N, cache, src, dst, chunks, ratios, work, logits)
+    ref = model.kv_buffer(N)
+    cache.read(src[None].contiguous(), None, ref[:, 0, :n_ctx], ref[:, 1, :n_ctx], n_layers=3, max_len=n_ctx)
+    out = model.blend_gradual(toks, ref, chunks, ratios, out_kv=ref)
+    fresh = cb.KV8Cache.empty(3, nb, 2, P, 128, n_heads=8)
+    fresh.write(src[None].contiguous(), None, ref[:, 0], ref[:, 1], n_layers=3, max_len=N)
+    torch.cuda.synchronize()
+    assert torch.equal(work, ref) and torch.equal(logits, out["logits"].float())
+    full = N // P                                        # whole pages, and of the last one the rows that were written
+    assert torch.equal(cache.codes[:, :, nb:nb + full], fresh.codes[:, :, :full])
+    assert torch.equal(cache.codes[:, :, nb + full, :, :N % P], fresh.codes[:, :, full, :, :N % P])
+    assert torch.equal(cache.scales[:, :, nb:], fresh.scales) and model.status() == 0 and cache.status() == 0
+    for x in (fresh, cache, model):
+        x.close()
