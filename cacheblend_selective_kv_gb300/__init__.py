@@ -569,7 +569,8 @@ class KV8Cache:
                   max_len=None, stream=None):
         """softmax(q k * scale) v of the query rows q [n_q][n_heads][head_dim], each sequence's last rows, over its cache
         (causal); returns out.  weights (device float32 [n_seqs][n_kv_heads][ld >= max_len]) receives, or with add
-        accumulates, the weight of every key.  q_start as row_start of write; scale defaults to head_dim ** -0.5."""
+        accumulates, the weight of every key.  q_start as row_start of write; scale defaults to head_dim ** -0.5.  Rows of
+        a sequence whose length is out of range are not written."""
         if out is None:
             with self._made_on(stream):
                 # rows that belong to no sequence are not written: zeros there

@@ -11,7 +11,8 @@
 //
 // q and P are not 8-bit values.  Each is written as a sum of e4m3 numbers c_0 + c_1 / 16 + c_2 / 256 + .., every term the
 // rounding of 16 times the residue before it, as columns of their own (column t * NC + c holds term t of column c), and
-// the columns of a sum are added in fp32 after the MMA.  A term carries 4 bits: a bf16 q is two terms, exactly; P gets
+// the columns of a sum are added in fp32 after the MMA.  A term carries 4 bits: a bf16 q is two terms, exactly for elements
+// down to 2^-14 of the row's largest and within 2^-21 of that largest below (where e4m3 runs out of exponents); P gets
 // three (2^-12 relative), which keeps the result's error well below its bf16 rounding.  fp32 calls use six of each.
 // e4m3 products and their fp32 accumulation were checked to be as exact as an fp32 sum of the same products.
 //
@@ -28,8 +29,8 @@
 // stores instead of a byte store for each; what belongs to a column (its maximum, its factors) is computed by one lane
 // per warp and read back from shared memory.
 //
-// Measured (32 heads, 8 KV heads of 128, bf16): 64 sequences of up to 8K keys, each its own length, 96 us, 89 % of the measured
-// copy rate; 64 x 8192 keys 167 us, 95 %; 1 x 131071 keys 54 us, 74 %; 1 x 200 keys 7 us.  Bound by HBM in the long run (the
+// Measured (32 heads, 8 KV heads of 128, bf16): 64 sequences of up to 8K keys, each its own length, 97 us, 88 % of the measured
+// copy rate; 64 x 8192 keys 167 us, 95 %; 1 x 131071 keys 54 us, 73 %; 1 x 200 keys 7 us.  Bound by HBM in the long run (the
 // difference between two lengths is read at the copy rate), with about 7 us for the launch, the first tile and the end.
 #include <cudaTypedefs.h>
 
@@ -673,7 +674,7 @@ template <int HD> using F8 = Shape<HD, 8, 1, 6, 6, 2, 2>;
 template <int HD> cudaError_t launch_dim(const Kv8& c, AttnArgs& p, cudaStream_t s) {
     // Query columns per item: what a sequence's rows need on average, within what tensor memory holds.  Fewer columns leave
     // room for more CTAs on an SM and shorter tiles, too few double the tiles (64 x 8K, us with shapes of 4 / 8 / 16 / 32: 4 columns
-    // 167 / 171 / 188 / 328, 8 columns 322 / 175 / 192 / 334, 16 columns 626 / 328 / 195 / 335).
+    // 167 / 171 / 188 / 328, 8 columns 322 / 175 / 192 / 334, 16 columns 626 / 328 / 197 / 335).
     const int rows = (p.r.n_rows + p.q.n - 1) / p.q.n, need = rows * p.G;
     if (c.cfg.dtype == CB_BF16) {
         if (need <= 4) return launch_shape<bf16, C4<HD>>(c, p, s);
@@ -737,7 +738,7 @@ cudaError_t launch_kv8_attention(const Kv8& c, const Kv8Seqs& q, const Kv8Rows& 
     if (r.n_rows > 0) {
         const int rows = (r.n_rows + q.n - 1) / q.n;             // of a sequence, on average
         // Up to 32 columns of a sequence stand in one item here, and beyond that keys and values are read and P is formed once
-        // per item of 32 (64 sequences of 2K: 32 columns 112 us here, 121 there; 48 columns 205 here, 122 there).
+        // per item of 32 (64 sequences of 2K: 32 columns 111 us here, 121 there; 48 columns 205 here, 122 there).
         const bool many = c.cfg.dtype == CB_BF16 && rows * p.G > 32;
         if (many) return launch_kv8_rows(c, &p, s);              // sums its weights too
         const cudaError_t e = c.cfg.head_dim == 128 ? launch_dim<128>(c, p, s) : launch_dim<64>(c, p, s);

@@ -23,7 +23,7 @@
 // warps of a row need not meet for every tile); they are joined at the end of an item, relative to X.  Per tile and SM: 32 MMAs of 128 x 128 x 16
 // at about 99 cycles, 128 x 128 exponentials, 2 x 128 x HD conversions; about 3600 cycles a tile, bound by the softmax warps'
 // chain (two warps a scheduler, 1.2 instructions a cycle) and not by the matrix unit.  2048 rows over 8K: 352 us, 36 % of
-// the measured bf16 rate; the 64 rows of a query over 8K: 29 us, 45 us with weights (with four warps that widen: 371, 32 and 48).
+// the measured bf16 rate; the 64 rows of a query over 8K: 29.5 us, 45 us with weights (with four warps that widen: 371, 32 and 48).
 #include <cstring>
 
 #include "cb_kv8_attn.cuh"
@@ -632,7 +632,7 @@ template <int HD, bool SCORES> cudaError_t launch_dim(const Kv8& c, AttnArgs& p,
     if (e != cudaSuccess) return e;
     p.QT = ROWS / p.G;
     // 4096 rows over 4096 keys: 975 us when only tiles counted, 424 with 2 places; 256 with 4 and 5, 261 with 6 as the kernel
-    // is now; 16 ragged sequences x 512 rows: 182, 185 and 193 us
+    // was then (252 now); 16 ragged sequences x 512 rows: 182, 185 and 193 us (184 now)
     p.ahead = 4;
     p.min_places = 1 + p.ahead;
     const int64_t items = ((int64_t)p.r.n_rows / p.QT + p.q.n) * p.Hkv;

@@ -8,7 +8,7 @@
 // Both are bound by HBM: 2 or 4 bytes a value on one side, 1 on the other.  Work is split by block: TPB threads
 // (32..256) hold one block's rows in registers as NP 16-byte vectors each, find the block's largest value with one
 // reduction and store the codes, so every row is read once and a code block is written as one contiguous piece.
-// 8256 rows x 32 layers of 8 heads of 128 (1.62 GB in all): written in 248 us (97 % of the measured copy rate), 8192 rows read
+// 8256 rows x 32 layers of 8 heads of 128 (1.62 GB in all): written in 250 us (96 % of the measured copy rate), 8192 rows read
 // back in 233 us (102 %).
 #include "cb_kv8.cuh"
 
@@ -340,7 +340,7 @@ CacheArgs cache_args(const Kv8& c, const Kv8Seqs& q, const Kv8Rows& r, const Kv8
     a.layer = layer;
     // Vectors of 16 bytes per thread: what a thread does once (finding its block) is spread over more of them, and
     // they are in flight together.  Eight (8K x 32 layers of the 8B shape written in
-    // 248 us, four in 340).
+    // 250 us, four in 340).
     const int want = (1 << q.shift) * a.hd * es / (16 * VECTORS);
     a.tpb_shift = log2_of(want < 32 ? 32 : (want > THREADS ? THREADS : want));
     a.vpr_shift = log2_of(a.hd * es / 16);

@@ -363,7 +363,13 @@ cb_status cb_kv8_read(cb_kv8* cache, const cb_kv8_seqs* seqs, int32_t layer, int
  *                sum of its softmax weights over the call's rows of its sequence and the heads of its group, at entries
  *                0 .. len - 1 (others are left as they were); add != 0 adds to what stands there.  What cb_kv8_evict
  *                ranks by: written once for a query window, or added up over decoding steps.
- * NaN behind what a row sees (in a later row's K or V, or behind the sequence) does not reach it.
+ * NaN behind what a row sees (in a later row's K or V, or behind the sequence) does not reach it.  A NaN or an infinity in
+ * a row of q makes that head's result NaN.
+ * Precision: scores, statistics and sums are fp32.  Where it meets V, a softmax weight has 12 bits in bf16 calls (11 in
+ * those of more than 32 rows times heads of a group, on average) and 24 in fp32 ones.  A bf16 q is exact down to 2^-14 of its
+ * row's largest element and within 2^-21 of that below.  A weight below 2^-126 of the row's largest counts as 0, or below
+ * 2^-58 where V's scales pass 2^60.  The largest |q| of a row times |scale| times the scale of a K block has to stay below
+ * 2^126, as scores have to anyway (else scores of 0 in that block may be NaN).
  * (n_q + n_seqs) * n_kv_heads * (max_len / 128 + 8) has to stay below 2^31 (else CB_ERR_UNSUPPORTED).
  * What a call is tuned for follows from the rows a sequence has on average, so decoding steps and long queries are better
  * given to calls of their own.
