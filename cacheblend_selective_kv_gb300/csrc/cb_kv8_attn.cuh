@@ -192,9 +192,10 @@ __device__ __forceinline__ int piece_count(const AttnArgs& p, const Find& f, int
 }
 
 // Finds it and the cursor at its first tile, THREADS sequences at a time (the first step's are kept); before and after run
-// around the first barrier, which also publishes what the caller has set up in shared memory.  (The host refuses calls of
-// 2^31 places, counted for rows that each belong to one sequence at most.  Offsets that decrease could give rows to several,
-// whose scores would lie on one another and whose places could pass 32 bits: then every CTA gets an empty piece.  This and what ends an item run once or twice per CTA, from instructions that have to be fetched first: short
+// around the first barrier, which also publishes what the caller has set up in shared memory.  The host refuses calls of
+// 2^31 places, counted for rows that each belong to one sequence at most; offsets that decrease could give rows to
+// several, whose scores would lie on one another and whose places could pass 32 bits, and then every CTA gets an empty
+// piece.  (This and what ends an item run once or twice per CTA, from instructions that have to be fetched first: short
 // loops and 32-bit arithmetic are worth more here than fewer steps.)
 template <int THREADS, typename F, typename H>
 __device__ __forceinline__ void find_piece(const AttnArgs& p, Find& f, Piece& mine, Cursor& cur, F before_sync, H after_sync) {

@@ -1,7 +1,7 @@
 // Attention over the 8-bit paged K/V cache on the sm_103a tensor cores.  Query row i of a sequence's n sits at position
 // len - n + i and sees keys 0 .. that position: out = softmax(q k * scale) v, the G query heads of a group sharing a KV
-// head.  A row that sees nothing (its position is negative, or all its keys lie in bad pages) gives 0.  With weights, every key gets the sum of its
-// softmax weights over the call's query rows and the group's heads.
+// head.  A row that sees nothing (its position is negative, or all its keys lie in bad pages) gives 0.  With weights,
+// every key gets the sum of its softmax weights over the call's query rows and the group's heads.
 //
 // A decoding step reads every cached byte once and does 4 G FLOPs for it, so it is bound by HBM as long as the codes
 // reach the matrix unit without being touched.  They do: tcgen05 kind::f8f6f4 takes e4m3 operands, so the keys are the

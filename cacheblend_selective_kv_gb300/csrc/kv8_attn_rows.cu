@@ -20,10 +20,12 @@
 // the factor 2^(R - X) between O and the sum.  It only grows, as R and M do.
 //
 // Each of the two halves of a tile's keys has its own R, X, sum and O (as the blend's attention kernel does, so that the
-// warps of a row need not meet for every tile); they are joined at the end of an item, relative to X.  Per tile and SM: 32 MMAs of 128 x 128 x 16
-// at about 99 cycles, 128 x 128 exponentials, 2 x 128 x HD conversions; about 3600 cycles a tile, bound by the softmax warps'
-// chain (two warps a scheduler, 1.2 instructions a cycle) and not by the matrix unit.  2048 rows over 8K: 352 us, 36 % of
-// the measured bf16 rate; the 64 rows of a query over 8K: 29.5 us, 45 us with weights (with four warps that widen: 371, 32 and 48).
+// warps of a row need not meet for every tile); they are joined at the end of an item, relative to X.
+//
+// Per tile and SM: 32 MMAs of 128 x 128 x 16 at about 99 cycles, 128 x 128 exponentials, 2 x 128 x HD conversions; about
+// 3600 cycles a tile, bound by the softmax warps' chain (two warps a scheduler, 1.2 instructions a cycle) and not by the
+// matrix unit.  2048 rows over 8K: 352 us, 36 % of the measured bf16 rate; the 64 rows of a query over 8K: 29.5 us, 45 us
+// with weights (with four warps that widen: 371, 32 and 48).
 #include <cstring>
 
 #include "cb_kv8_attn.cuh"
@@ -233,7 +235,8 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_rows_kernel(const __grid_const
                     // scale gives its sign, and nothing when it is 0).  An infinity counts as NaN: it could give scores of -inf
                     // alone, which is how a row that sees nothing looks.
                     // (not below 2^-119, so that 1 / scale * 2^6 stays finite)
-                    const float sc = top > 0.f ? fmaxf(kv8_scale(top), 1.5046328e-36f) : 0.f, up = kv8_inverse(sc) * (p.a.scale < 0.f ? -64.f : p.a.scale > 0.f ? 64.f : 0.f);
+                    const float sc = top > 0.f ? fmaxf(kv8_scale(top), 1.5046328e-36f) : 0.f;
+                    const float up = kv8_inverse(sc) * (p.a.scale < 0.f ? -64.f : p.a.scale > 0.f ? 64.f : 0.f);
                     uint32_t o[4];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) o[k] = f16_pair(kv8_nan_inf(f[2 * k]) * up, kv8_nan_inf(f[2 * k + 1]) * up);
