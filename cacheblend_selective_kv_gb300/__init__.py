@@ -33,6 +33,7 @@ EXPORTED = ("cb_model_create", "cb_model_destroy", "cb_rerope", "cb_blend", "cb_
             "cb_select_hkvd", "cb_blend_hkvd", "cb_gradual_layout", "cb_kv8_create", "cb_kv8_destroy", "cb_kv8_status",
             "cb_kv8_write", "cb_kv8_read", "cb_kv8_attention", "cb_kv8_evict", "cb_blend_kv8")
 CB_STATIC_MAX_CHUNKS = 256
+_I32 = 1 << 31
 CB_STATUS_BAD_TOKEN, CB_STATUS_WAIT_TIMEOUT, CB_STATUS_BAD_ROW = 1, 2, 4
 
 
@@ -500,12 +501,16 @@ class KV8Cache:
             raise ValueError(f"{name} must be a contiguous int32 tensor {list(shape)} on {self.device}")
         return t.data_ptr()
 
-    def _seqs(self, table, lens, max_len):
+    def _seqs(self, table, lens, max_len, layer, n_layers=1):
         if table.dim() != 2:
             raise ValueError("table must be int32 [n_seqs][pages]")
         n, ld = table.shape
-        return CbKV8Seqs(n, self._int(table, "table", n, ld), ld, None if lens is None else self._int(lens, "lens", n),
-                         ld * self.page_size if max_len is None else max_len)
+        if max_len is None:
+            max_len = ld * self.page_size
+        # (ctypes would take the lower 32 bits of a larger number)
+        if not (-_I32 <= max_len < _I32 and -_I32 <= layer < _I32 and -_I32 <= n_layers < _I32):
+            raise ValueError(f"max_len {max_len}, layer {layer} or n_layers {n_layers} passes 32 bits")
+        return CbKV8Seqs(n, self._int(table, "table", n, ld), ld, None if lens is None else self._int(lens, "lens", n), max_len)
 
     def _stream(self, stream):
         if stream is None:
@@ -541,7 +546,7 @@ class KV8Cache:
         vp, *lay_v = self._kv(v, "v", n_layers)
         if lay != lay_v:
             raise ValueError("k and v must have the same number of rows and the same strides")
-        sq = self._seqs(table, lens, max_len)
+        sq = self._seqs(table, lens, max_len, layer, n_layers)
         code = f(self.handle, sq, layer, n_layers, kp, vp, lay[0], lay[1],
                  None if row_start is None else self._int(row_start, "row_start", sq.n_seqs + 1), lay[2], self._stream(stream))
         if code:
@@ -579,7 +584,7 @@ class KV8Cache:
         op, os_, n_out = self._q(out, "out")
         if n_out != n:
             raise ValueError(f"out must have q's {n} rows")
-        sq = self._seqs(table, lens, max_len)
+        sq = self._seqs(table, lens, max_len, layer)
         wp, ld = None, 0
         if weights is not None:
             ld = weights.shape[-1]
@@ -600,7 +605,9 @@ class KV8Cache:
         largest weight (weights: device float32 [n_layers][n_seqs][n_kv_heads][ld]).  The kept rows move to dst_table
         (table itself: in place; else pages that table does not name).  Returns dict(rows, lens, weights); out_weights
         defaults to weights itself, out_lens may be lens."""
-        sq = self._seqs(table, lens, max_len)
+        sq = self._seqs(table, lens, max_len, layer, n_layers)
+        if not (-_I32 <= n_keep < _I32 and -_I32 <= n_sink < _I32 and -_I32 <= n_recent < _I32):
+            raise ValueError(f"n_keep {n_keep}, n_sink {n_sink} or n_recent {n_recent} passes 32 bits")
         n = sq.n_seqs
         if dst_table.dim() != 2:
             raise ValueError("dst_table must be int32 [n_seqs][pages]")

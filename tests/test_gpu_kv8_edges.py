@@ -585,3 +585,97 @@ def test_blend_over_the_8bit_pool_in_bf16(cb):
     assert torch.equal(cache.scales[:, :, nb:], fresh.scales) and model.status() == 0 and cache.status() == 0
     for x in (fresh, cache, model):
         x.close()
+
+
+def test_most_sequences(cb):
+    """65535 sequences, one page each: written, attended to with weights, read back, evicted."""
+    n, P, hd, G = 65535, 16, 64, 2
+    cache = cb.KV8Cache.empty(1, n, 1, P, hd, G, weight_cells=cb.KV8Cache.cells(n, G, P))
+    g = torch.Generator(device="cuda").manual_seed(9)
+    table = torch.randperm(n, generator=g, device="cuda").int()[:, None].contiguous()
+    lens = torch.randint(0, P + 1, (n,), generator=g, device="cuda").int()
+    start = torch.cat([torch.zeros(1, device="cuda"), lens.cumsum(0)]).int()
+    total = int(start[-1])
+    k = torch.randn((total, 1, hd), generator=g, device="cuda").bfloat16()
+    v = torch.randn((total, 1, hd), generator=g, device="cuda").bfloat16()
+    cache.write(table, lens, k, v, row_start=start)
+    ko, vo = torch.zeros_like(k), torch.zeros_like(v)
+    cache.read(table, lens, ko, vo, row_start=start)
+    # half a step of a number (2^-4), or of a block's scale (2^-10 of 2^-6: its largest value is below 7)
+    for a, b in ((ko, k), (vo, v)):
+        assert torch.all((a.float() - b.float()).abs() <= 2.0 ** -4 * b.float().abs() + 2.0 ** -16)
+    q = torch.randn((n, G, hd), generator=g, device="cuda").bfloat16()
+    w = torch.full((n, 1, P), -1.0, device="cuda")
+    out = cache.attention(table, lens, q, weights=w)
+    seen = torch.arange(P, device="cuda")[None, :] < lens[:, None]
+    kk, vv = (torch.zeros((n, P, hd), device="cuda", dtype=torch.float64) for _ in range(2))
+    kk[seen], vv[seen] = ko[:, 0].double(), vo[:, 0].double()
+    x = torch.einsum("nhd,npd->nhp", q.double(), kk) * hd ** -0.5
+    p = torch.softmax(x.masked_fill(~seen[:, None], -torch.inf), dim=2).nan_to_num(0.0)
+    ref, spread = torch.einsum("nhp,npd->nhd", p, vv), torch.einsum("nhp,npd->nhd", p, vv.abs())
+    # (as in test_gpu_kv8.py, with scores of sum |q k| scale below 64; P's floor: 2^-25 of at most 448 * 16 codes * scale)
+    tol = 2.0 ** -8 * ref.abs() + (2 * 72 * U * 64 + 160 * U + 2.0 ** -11) * spread + 2.0 ** -25 * 448 * 16 * 2.0 ** -6
+    assert torch.all((out.double() - ref).abs() <= tol)
+    assert torch.all(torch.where(seen, (w[:, 0] - p.sum(1)).abs() <= 1e-3 * p.sum(1) + 1e-12, w[:, 0] == -1.0))
+    e = cache.evict(table, lens, table, w[None], 5, 1, 1)
+    torch.cuda.synchronize()
+    assert torch.equal(e["lens"], lens.clamp(max=5)) and cache.status() == 0
+    rows = e["rows"][0, :, 0]
+    kept = torch.arange(5, device="cuda")[None, :] < e["lens"][:, None]
+    assert torch.all((rows >= 0) == kept)
+    assert torch.all((rows[:, 1:] > rows[:, :-1]) | (rows[:, 1:] < 0))
+    cache.close()
+
+
+def test_scores_of_more_than_32_bits(cb):
+    """1024 rows of 32 heads over 140 000 keys with weights: 4.6e9 scores.  The same rows in two calls, the second of which
+    adds, give the same sums."""
+    n, rows, P, hd = 140000, 1024, 256, 64
+    cells = cb.KV8Cache.cells(rows, 32, n)
+    assert cells > 2 ** 32
+    cache = cb.KV8Cache.empty(1, n // P + 1, 8, P, hd, 32, weight_cells=cells)
+    g = torch.Generator(device="cuda").manual_seed(2)
+    k = torch.randn((n, 8, hd), generator=g, device="cuda").bfloat16()
+    table = torch.randperm(n // P + 1, generator=g, device="cuda").int()[None]
+    cache.write(table, i32([n]), k, k.flip(0).contiguous(), max_len=n)
+    q = torch.randn((rows, 32, hd), generator=g, device="cuda").bfloat16()
+    w, two = torch.zeros((1, 8, n), device="cuda"), torch.zeros((1, 8, n), device="cuda")
+    out = cache.attention(table, i32([n]), q, weights=w, max_len=n)
+    h = rows // 2
+    a = cache.attention(table, i32([n - h]), q[:h], weights=two, max_len=n)
+    b = cache.attention(table, i32([n]), q[h:], weights=two, add=True, max_len=n)
+    torch.cuda.synchronize()
+    assert cache.status() == 0
+    # both within (2 ds + (16 + 128 + n / 128 + columns) u) of the weight, ds = 72 u 64 at most
+    assert torch.all((w - two).abs() <= 2 * (2 * 72 * 64 + 144 + n / 128 + 4096) * U * two)
+    assert abs(float(w.double().sum()) / (rows * 32) - 1) < 1e-3
+    both = torch.cat([a, b]).float()
+    assert torch.all((out.float() - both).abs() <= 2 * 2.0 ** -8 * both.abs() + 2.0 ** -10)
+    cache.close()
+
+
+def test_numbers_beyond_32_bits_are_refused(cb):
+    """2^32 + 40 keys or layer 2^32 are not 40 keys and layer 0."""
+    c = Case(cb, [40], H=1, hd=64, P=16, seed=1)
+    q, _ = c.values(1, 2, 64)
+    kv, _ = c.values(1, 1, 1, 64)
+    w = torch.zeros((1, 1, 1, 48), device="cuda")
+    for top in (2 ** 31, 2 ** 32, 2 ** 32 + 40, -2 ** 32 + 40, -1):
+        for f in (lambda: c.cache.attention(c.table, c.lens_t, q, max_len=top), lambda: c.cache.write(c.table, c.lens_t, kv, kv, max_len=top),
+                  lambda: c.cache.read(c.table, c.lens_t, kv, kv.clone(), max_len=top),
+                  lambda: c.cache.evict(c.table, c.lens_t, c.table, w, 4, max_len=top)):
+            with pytest.raises((ValueError, cb.CacheBlendError)):
+                f()
+    big = 2 ** 32
+    for f in (lambda: c.cache.attention(c.table, c.lens_t, q, layer=big), lambda: c.cache.write(c.table, c.lens_t, kv, kv, layer=big),
+              lambda: c.cache.read(c.table, c.lens_t, kv, kv.clone(), layer=-big),
+              lambda: c.cache.evict(c.table, c.lens_t, c.table, w, 4, layer=big),
+              lambda: c.cache.evict(c.table, c.lens_t, c.table, w, 4, big + 1), lambda: c.cache.evict(c.table, c.lens_t, c.table, w, 4, 0, big),
+              lambda: c.cache.evict(c.table, c.lens_t, c.table, w, big + 4)):
+        with pytest.raises((ValueError, cb.CacheBlendError)):
+            f()
+    c.check_pool()
+    # numbers of numpy's are numbers
+    a = c.cache.attention(c.table, c.lens_t, q, layer=np.int64(0), max_len=np.int32(40))
+    assert torch.equal(a, c.cache.attention(c.table, c.lens_t, q, max_len=40))
+    c.done()
