@@ -31,7 +31,7 @@ EXPORTED = ("cb_model_create", "cb_model_destroy", "cb_rerope", "cb_blend", "cb_
             "cb_pages_alloc", "cb_pages_retain", "cb_pages_release", "cb_pages_plan_write", "cb_pages_count",
             "cb_pages_free", "cb_index_create", "cb_index_destroy", "cb_index_size", "cb_index_match",
             "cb_select_hkvd", "cb_blend_hkvd", "cb_gradual_layout", "cb_kv8_create", "cb_kv8_destroy", "cb_kv8_status",
-            "cb_kv8_write", "cb_kv8_read", "cb_kv8_attention", "cb_kv8_evict", "cb_blend_kv8")
+            "cb_kv8_write", "cb_kv8_read", "cb_kv8_attention", "cb_kv8_evict", "cb_blend_kv8", "cb_kv8_append")
 CB_STATIC_MAX_CHUNKS = 256
 _I32 = 1 << 31
 CB_STATUS_BAD_TOKEN, CB_STATUS_WAIT_TIMEOUT, CB_STATUS_BAD_ROW = 1, 2, 4
@@ -186,6 +186,8 @@ def lib() -> ctypes.CDLL:
         for f in (L.cb_kv8_write, L.cb_kv8_read):
             f.restype = ctypes.c_int
             f.argtypes = [vp, sq, i32, i32, vp, vp, i64, i64, vp, i32, vp]
+        L.cb_kv8_append.restype = ctypes.c_int
+        L.cb_kv8_append.argtypes = [vp, sq, i32, vp, i64, vp, i64, vp, vp, i64, vp, ctypes.c_double, vp, i32, vp]
         L.cb_kv8_attention.restype = ctypes.c_int
         L.cb_kv8_attention.argtypes = [vp, sq, i32, vp, i64, vp, i32, ctypes.c_float, vp, i64, vp, i32, i32, vp]
         L.cb_kv8_evict.restype = ctypes.c_int
@@ -569,6 +571,37 @@ class KV8Cache:
         if stride[2] != 1 or (stride[1] != self.head_dim and self.n_heads > 1):
             raise ValueError(f"{name}: the heads of a row must be contiguous")
         return t.data_ptr(), stride[0] if shape[0] > 1 else self._q_width, shape[0]
+
+    def append(self, table, lens, q, k, v, rope_theta: float, out_q=None, layer: int = 0, positions=None, row_start=None,
+               max_len=None, stream=None):
+        """New rows of one layer, q and k not yet rotated: k ([n_rows][n_kv_heads][head_dim]) is rotated at its rows'
+        positions, and k and v become the last rows of their sequences (as write puts them there); q ([n_rows][n_heads]
+        [head_dim], or None) is rotated into out_q, which may be q itself; returns out_q.  positions: device int32 [n_rows];
+        None: a row's place in its sequence.  row_start as for write.  Rows of no sequence are left as they were."""
+        kp, _, kv_stride, n = self._kv(k, "k", 1)
+        vp, _, v_stride, n_v = self._kv(v, "v", 1)
+        if (n, kv_stride) != (n_v, v_stride):
+            raise ValueError("k and v must have the same number of rows and the same strides")
+        qp, qs, op, os_ = None, 0, None, 0
+        if q is not None:
+            if out_q is None:
+                with self._made_on(stream):
+                    # rows that belong to no sequence are not written: zeros there
+                    out_q = q.new_empty(q.shape) if row_start is None else q.new_zeros(q.shape)
+            qp, qs, n_q = self._q(q, "q")
+            op, os_, n_out = self._q(out_q, "out_q")
+            if n_q != n or n_out != n:
+                raise ValueError(f"q and out_q must have k's {n} rows")
+        elif out_q is not None:
+            raise ValueError("out_q without q")
+        sq = self._seqs(table, lens, max_len, layer)
+        code = self._lib.cb_kv8_append(self.handle, sq, layer, qp, qs, op, os_, kp, vp, kv_stride,
+                                       None if positions is None else self._int(positions, "positions", n), rope_theta,
+                                       None if row_start is None else self._int(row_start, "row_start", sq.n_seqs + 1), n,
+                                       self._stream(stream))
+        if code:
+            _check(code)
+        return out_q
 
     def attention(self, table, lens, q, out=None, layer: int = 0, q_start=None, scale=None, weights=None, add: bool = False,
                   max_len=None, stream=None):

@@ -152,6 +152,19 @@ cudaError_t launch_kv8_write(const Kv8& c, const Kv8Seqs& q, const Kv8Rows& r, c
 cudaError_t launch_kv8_read(const Kv8& c, const Kv8Seqs& q, const Kv8Rows& r, const Kv8Io& io, int layer, int n_layers,
                             cudaStream_t s);
 
+struct Kv8Append {            // rows of a fused projection or of their own; [heads][hd] inside a row is contiguous
+    const void* q;            // or NULL
+    int64_t q_stride;
+    void* out_q;
+    int64_t out_q_stride;
+    const void* k;
+    const void* v;
+    int64_t kv_stride;
+    const int* positions;     // [n_rows] or NULL
+    double theta;
+};
+cudaError_t launch_kv8_append(const Kv8& c, const Kv8Seqs& q, const Kv8Rows& r, const Kv8Append& p, int layer, cudaStream_t s);
+
 struct Kv8Attn {
     const void* q;            // [n_q][Hq][hd]
     int64_t q_stride;         // elements between rows

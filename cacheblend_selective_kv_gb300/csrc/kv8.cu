@@ -40,6 +40,18 @@ bool rows_overlap(int64_t apart, int64_t w, int64_t row_stride, int32_t n_rows, 
     return false;
 }
 
+// Do any of n rows of a_w bytes overlap any of n rows of b_w bytes?  At the same stride row by row (slices of one projection's
+// rows lie between each other), else as whole arrays.
+bool rows_touch(const void* a, int64_t a_w, int64_t a_stride, const void* b, int64_t b_w, int64_t b_stride, int64_t n) {
+    if (a_stride != b_stride) return overlap(a, (n - 1) * a_stride + a_w, b, (n - 1) * b_stride + b_w);
+    const int64_t d = (const char*)b - (const char*)a, below = d >= 0 ? d / a_stride : -((-d + a_stride - 1) / a_stride);
+    for (int64_t m = below; m <= below + 1; ++m) {               // a's row i + m beside b's row i
+        const int64_t gap = d - m * a_stride;
+        if (m > -n && m < n && gap < a_w && -gap < b_w) return true;
+    }
+    return false;
+}
+
 cb_status check_handle(const cb_kv8* c, const char* who) {
     set_last_error("");
     return c ? CB_OK : fail(CB_ERR_INVALID_ARG, "%s: null cache", who);
@@ -264,6 +276,46 @@ cb_status cb_kv8_read(cb_kv8* c, const cb_kv8_seqs* seqs, int32_t layer, int32_t
     if (st == CB_OK) st = on.to(c, who);
     if (st != CB_OK) return st;
     return cuda_result(launch_kv8_read(*c, q, r, io, layer, n_layers, (cudaStream_t)stream), who);
+}
+
+cb_status cb_kv8_append(cb_kv8* c, const cb_kv8_seqs* seqs, int32_t layer, const void* q, int64_t q_stride, void* out_q,
+                        int64_t out_q_stride, const void* k, const void* v, int64_t kv_stride, const int32_t* positions,
+                        double rope_theta, const int32_t* row_start, int32_t n_rows, void* stream) {
+    const char* who = "cb_kv8_append";
+    Kv8Seqs sq;
+    Kv8Rows r;
+    Kv8Io io;
+    cb_status st = check_handle(c, who);
+    if (st == CB_OK) st = check_layers(*c, layer, 1, who);
+    if (st == CB_OK) st = check_seqs(*c, seqs, who, sq);
+    if (st == CB_OK) st = check_rows(sq, row_start, n_rows, who, r);
+    if (st != CB_OK) return st;
+    if (!(rope_theta >= 1.0) || !std::isfinite(rope_theta)) return fail(CB_ERR_INVALID_ARG, "%s: rope_theta %g is not a number from 1 on", who, rope_theta);
+    if (n_rows == 0 || sq.n == 0) return CB_OK;
+    st = check_blocks(*c, sq, r, who);
+    if (st == CB_OK) st = check_io(*c, k, v, 0, kv_stride, 1, n_rows, false, who, io);
+    if (st != CB_OK) return st;
+    const int64_t es = c->cfg.dtype == CB_BF16 ? 2 : 4, w = (int64_t)c->cfg.n_heads * c->cfg.head_dim * es;
+    const int64_t kv_w = (int64_t)c->cfg.n_kv_heads * c->cfg.head_dim * es;
+    if ((q == nullptr) != (out_q == nullptr)) return fail(CB_ERR_INVALID_ARG, "%s: q and out_q are both given or both null", who);
+    if (q) {
+        if ((uintptr_t)q % 16 || (uintptr_t)out_q % 16 || q_stride * es % 16 || out_q_stride * es % 16)
+            return fail(CB_ERR_INVALID_ARG, "%s: q, out_q and their strides must be multiples of 16 bytes", who);
+        if (q_stride * es < w || out_q_stride * es < w || q_stride > ((int64_t)1 << 40) || out_q_stride > ((int64_t)1 << 40))
+            return fail(CB_ERR_INVALID_ARG, "%s: a row stride below a row's %lld elements, or out of range", who, (long long)(w / es));
+        if ((q != out_q || q_stride != out_q_stride) && rows_touch(q, w, q_stride * es, out_q, w, out_q_stride * es, n_rows))
+            return fail(CB_ERR_INVALID_ARG, "%s: q and out_q overlap without being the same", who);
+        if (rows_touch(out_q, w, out_q_stride * es, k, kv_w, kv_stride * es, n_rows) ||
+            rows_touch(out_q, w, out_q_stride * es, v, kv_w, kv_stride * es, n_rows))
+            return fail(CB_ERR_INVALID_ARG, "%s: out_q overlaps k or v", who);
+        if ((int64_t)n_rows * c->cfg.n_heads > (int64_t)1 << 33)
+            return fail(CB_ERR_UNSUPPORTED, "%s: %d rows of q are too many for one call", who, n_rows);
+    }
+    OnDevice on;
+    st = on.to(c, who);
+    if (st != CB_OK) return st;
+    const Kv8Append p{q, q_stride, out_q, out_q_stride, k, v, kv_stride, positions, rope_theta};
+    return cuda_result(launch_kv8_append(*c, sq, r, p, layer, (cudaStream_t)stream), who);
 }
 
 cb_status cb_kv8_attention(cb_kv8* c, const cb_kv8_seqs* seqs, int32_t layer, const void* q, int64_t q_stride,

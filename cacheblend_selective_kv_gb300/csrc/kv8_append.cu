@@ -1,0 +1,320 @@
+// 8-bit paged K/V cache: appending rows whose q and k are rotated on the way (a decoding step, a prompt in pieces).
+//
+// Pair (2i, 2i + 1) of a head turns by the angle p theta^(-2i / hd) of its row's position p; k and v then go into their
+// blocks as cb_kv8_write puts rows there, q goes to its output.  K meets one rounding, from the rotated fp32 value to its code.
+//
+// The angle.  The host gives every pair's frequency as a 64-bit fraction of a turn, so that p times it modulo 2^64 is the phase
+// of any int32 position, exact to the frequency's own rounding: no reduction of a large angle in floating point.  The
+// phase less the nearest quarter turn goes to fp32 (an angle within pi / 4, off by 2^-25), and the Taylor series of sine and
+// cosine to x^9 and x^10 are off by at most 2e-9 there; quarter turns exchange the two and change their signs.  About 25
+// instructions for a pair, which stay below what the same bytes cost in HBM.
+//
+// Work, in one launch: the blocks that get rows of K, those of V, then q.  A block's rows stand in one group of 32 .. 512 threads,
+// as 32 values per thread where there are that many, from the load to the largest value to the code; a decoding step's single
+// rows are a warp each.  A thread of q has one vector of a row in several heads, which share its sines and cosines.
+#include <cmath>
+
+#include "cb_kv8_block.cuh"
+
+namespace cb {
+
+namespace {
+
+constexpr int MOST = 512;                // threads of a block's group, at most
+constexpr int QB = 4;                    // heads of q that a thread has under way
+
+struct Turns {
+    unsigned long long of[64];           // pair i turns by of[i] / 2^64 per position
+};
+
+struct AppendArgs {
+    Kv8Seqs q;
+    Kv8Rows r;
+    const void* src[2];                  // K, V rows
+    int64_t kv_stride;
+    const void* in_q;                    // or NULL
+    void* out_q;
+    int64_t q_stride, out_q_stride;
+    const int* positions;                // [n_rows] or NULL: a row's place in its sequence
+    uint8_t* codes;
+    float* scales;
+    int per_seq, units;                  // units = slots * Hkv
+    int Hkv, Hq, hd, layer;
+    int tpb_shift, vpr_shift;            // log2 of a group's threads, of a row's 16-byte vectors
+    int kv_ctas;                         // CTAs of K, and of V; q's follow
+    int q_heads, q_chunks;               // heads per thread of q, threads per row's vector
+};
+
+// cosine and sine of `phase` / 2^64 turns
+__device__ __forceinline__ float2 cos_sin(unsigned long long phase) {
+    const unsigned hi = (unsigned)(phase >> 32), quarter = (hi + 0x20000000u) >> 30;
+    const float x = (float)(int)(hi - (quarter << 30)) * 1.4629180792671596e-9f;      // 2 pi 2^-32
+    const float z = x * x;
+    float s = fmaf(z, 2.7557319e-6f, -1.9841270e-4f), c = fmaf(z, -2.7557319e-7f, 2.4801587e-5f);
+    s = fmaf(z, s, 8.3333333e-3f);
+    c = fmaf(z, c, -1.3888889e-3f);
+    s = fmaf(z, s, -1.6666667e-1f);
+    c = fmaf(z, c, 4.1666667e-2f);
+    s = fmaf(x * z, s, x);
+    c = fmaf(z, c, -0.5f);
+    c = fmaf(z, c, 1.f);
+    const float a = quarter & 1 ? s : c, b = quarter & 1 ? c : s;
+    return make_float2((quarter + 1) & 2 ? -a : a, quarter & 2 ? -b : b);
+}
+
+// a vector's values turned by its pairs' angles at one position
+template <typename T> struct Rotation {
+    static constexpr int NP = Vec<T>::N / 2;
+    float2 cs[NP];
+    __device__ __forceinline__ void set(const unsigned long long* turn, int position) {
+#pragma unroll
+        for (int k = 0; k < NP; ++k) cs[k] = cos_sin((unsigned long long)(long long)position * turn[k]);
+    }
+    __device__ __forceinline__ void apply(float* f) const {
+#pragma unroll
+        for (int k = 0; k < NP; ++k) {
+            const float2 y = rotate_pair(f[2 * k], f[2 * k + 1], cs[k]);
+            f[2 * k] = y.x;
+            f[2 * k + 1] = y.y;
+        }
+    }
+};
+
+template <typename T> __device__ __forceinline__ uint4 pack(const float* f);
+template <> __device__ __forceinline__ uint4 pack<bf16>(const float* f) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 p = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t*>(&p);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+template <> __device__ __forceinline__ uint4 pack<float>(const float* f) {
+    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+}
+
+// place of row `row` in its sequence; false where it is not written (as kv8_block decides for K and V)
+__device__ __forceinline__ bool place_of(const Kv8Seqs& q, const Kv8Rows& r, int row, int& place) {
+    int s = 0;
+    if (r.start) {
+        int z = q.n - 1;                               // the last sequence that begins at or before the row
+        while (s < z) {
+            const int m = (s + z + 1) >> 1;
+            if (r.start[m] <= row) s = m; else z = m - 1;
+        }
+    } else {
+        s = row / r.each;
+    }
+    int r0, r1, len;
+    if (!kv8_rows(q, r, s, r0, r1, len) || row < r0 || row >= r1 || r1 - r0 > len) return false;
+    place = len - (r1 - r0) + row - r0;
+    return true;
+}
+
+// NV vectors per thread: vector t + i * tpb of the call's rows in the block, tpb / vpr rows apart
+template <typename T, int NV>
+__device__ __forceinline__ void append_kv(const AppendArgs& a, const Turns& turns, int kv, int cta) {
+    constexpr int VN = Vec<T>::N;
+    __shared__ unsigned sm[MOST / 32];
+    const int tpb = 1 << a.tpb_shift, group = threadIdx.x >> a.tpb_shift, t = threadIdx.x & (tpb - 1);
+    const int unit = cta * ((int)blockDim.x >> a.tpb_shift) + group;
+    const int P = 1 << a.q.shift;
+    Block b{};
+    const int slot = unit / a.Hkv, head = unit - slot * a.Hkv;
+    const bool live = unit < a.units && kv8_block(a.q, a.r, a.per_seq, slot, nullptr, b);
+    const int row0 = b.lo + (t >> a.vpr_shift), rows = tpb >> a.vpr_shift, e = (t & ((1 << a.vpr_shift) - 1)) * VN;
+    const int64_t blk = ((int64_t)(a.layer * 2 + kv) * a.q.n_pages + b.page) * a.Hkv + head;
+    float f[NV][VN];
+    float top = 0.f, was = 0.f;
+    if (live) {
+        const T* src = (const T*)a.src[kv] + (int64_t)head * a.hd + e;
+        if (b.lo > 0) was = a.scales[blk];             // earlier rows of the sequence stay in the block
+        uint4 x[NV];
+        int position[NV];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int row = row0 + i * rows, from = b.src_row + row - b.lo;
+            x[i] = make_uint4(0, 0, 0, 0);
+            position[i] = 0;
+            if (row >= b.hi) continue;
+            x[i] = __ldcs(reinterpret_cast<const uint4*>(src + (int64_t)from * a.kv_stride));
+            if (kv == 0) position[i] = a.positions ? a.positions[from] : b.place + row - b.lo;
+        }
+        unsigned long long turn[VN / 2];
+#pragma unroll
+        for (int k = 0; k < VN / 2; ++k) turn[k] = turns.of[e / 2 + k];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            Vec<T>::get(x[i], f[i]);
+            if (row0 + i * rows >= b.hi) continue;
+            if (kv == 0) {
+                Rotation<T> turned;
+                turned.set(turn, position[i]);
+                turned.apply(f[i]);
+            }
+#pragma unroll
+            for (int k = 0; k < VN; ++k) top = fmaxf(top, kv8_mag(f[i][k]));
+        }
+    }
+    top = __uint_as_float(group_max(__float_as_uint(top), tpb, sm));
+    if (!live) return;                                 // no barrier of all threads below
+    uint8_t* dst = a.codes + blk * P * a.hd;
+    float sc = kv8_scale(top);
+    if (b.lo > 0) {
+        if (was >= sc) {
+            sc = was;
+        } else if (was > 0.f) {                        // (codes of a block of zeros stay as they are)
+            const Kv8Factor by = kv8_factor(was * kv8_inverse(sc));
+            for (int i = t; i < b.lo * a.hd / 16; i += tpb) {
+                uint4 c = reinterpret_cast<uint4*>(dst)[i];
+                c.x = kv8_rescale4(c.x, by);
+                c.y = kv8_rescale4(c.y, by);
+                c.z = kv8_rescale4(c.z, by);
+                c.w = kv8_rescale4(c.w, by);
+                reinterpret_cast<uint4*>(dst)[i] = c;
+            }
+        }
+    }
+    const float inv = kv8_inverse(sc);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int row = row0 + i * rows;
+        if (row >= b.hi) continue;
+        uint32_t w[VN / 4];
+#pragma unroll
+        for (int k = 0; k < VN; ++k) f[i][k] = kv8_storable(f[i][k]) * inv;
+#pragma unroll
+        for (int k = 0; k < VN / 4; ++k)
+            w[k] = kv8_code2(f[i][4 * k], f[i][4 * k + 1]) | (kv8_code2(f[i][4 * k + 2], f[i][4 * k + 3]) << 16);
+        uint8_t* d = dst + row * a.hd + e;
+        if (VN == 8) *reinterpret_cast<uint2*>(d) = make_uint2(w[0], w[VN / 4 - 1]);
+        else *reinterpret_cast<uint32_t*>(d) = w[0];
+    }
+    if (b.lo > 0) {                                    // every thread of the group has read the old scale
+        if (tpb > 32) asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(tpb) : "memory");
+        else __syncwarp();
+    }
+    if (t == 0) a.scales[blk] = sc;
+}
+
+template <typename T> __device__ __forceinline__ void append_q(const AppendArgs& a, const Turns& turns, int cta) {
+    constexpr int VN = Vec<T>::N;
+    const int64_t at = (int64_t)cta * blockDim.x + threadIdx.x, item = at >> a.vpr_shift;
+    const int64_t row = item / a.q_chunks;
+    if (row >= a.r.n_rows) return;
+    const int chunk = (int)(item - row * a.q_chunks), e = ((int)at & ((1 << a.vpr_shift) - 1)) * VN;
+    int place;
+    if (!place_of(a.q, a.r, (int)row, place)) return;
+    unsigned long long turn[VN / 2];
+#pragma unroll
+    for (int k = 0; k < VN / 2; ++k) turn[k] = turns.of[e / 2 + k];
+    Rotation<T> turned;
+    turned.set(turn, a.positions ? a.positions[row] : place);
+    const T* src = (const T*)a.in_q + row * a.q_stride + e;
+    T* dst = (T*)a.out_q + row * a.out_q_stride + e;
+    const int h1 = min(a.Hq, (chunk + 1) * a.q_heads);
+    for (int h0 = chunk * a.q_heads; h0 < h1; h0 += QB) {
+        uint4 x[QB];
+#pragma unroll
+        for (int i = 0; i < QB; ++i)
+            if (h0 + i < h1) x[i] = __ldcs(reinterpret_cast<const uint4*>(src + (h0 + i) * a.hd));
+#pragma unroll
+        for (int i = 0; i < QB; ++i) {
+            if (h0 + i >= h1) continue;
+            float f[VN];
+            Vec<T>::get(x[i], f);
+            turned.apply(f);
+            *reinterpret_cast<uint4*>(dst + (h0 + i) * a.hd) = pack<T>(f);
+        }
+    }
+}
+
+template <typename T, int NV>
+__global__ void __launch_bounds__(MOST) kv8_append_kernel(const __grid_constant__ AppendArgs a, const __grid_constant__ Turns turns) {
+    grid_dep_launch();
+    grid_dep_wait();
+    kv8_check_offsets(a.q, a.r);
+    const int cta = blockIdx.x;
+    if (cta < 2 * a.kv_ctas) append_kv<T, NV>(a, turns, cta >= a.kv_ctas, cta >= a.kv_ctas ? cta - a.kv_ctas : cta);
+    else append_q<T>(a, turns, cta - 2 * a.kv_ctas);
+}
+
+// the fractions of a turn, kept with the thread for the model's next call
+const Turns& turns_of(double theta, int hd) {
+    static thread_local Turns turns;
+    static thread_local double of_theta = 0.0;
+    static thread_local int of_hd = 0;
+    if (of_theta != theta || of_hd != hd) {
+        for (int i = 0; i < hd / 2; ++i) {
+            const double turn = std::pow(theta, -2.0 * i / hd) / 6.283185307179586477;
+            turns.of[i] = (unsigned long long)std::ldexp(turn, 64);
+        }
+        of_theta = theta;
+        of_hd = hd;
+    }
+    return turns;
+}
+
+template <typename T> cudaError_t append_typed(const AppendArgs& a, const Turns& turns, int nv, dim3 grid, dim3 block, bool pdl, cudaStream_t s) {
+    switch (nv) {
+        case 1: return launch_ex(pdl, kv8_append_kernel<T, 1>, grid, block, 0, s, a, turns);
+        case 2: return launch_ex(pdl, kv8_append_kernel<T, 2>, grid, block, 0, s, a, turns);
+        case 4: return launch_ex(pdl, kv8_append_kernel<T, 4>, grid, block, 0, s, a, turns);
+        case 8: return launch_ex(pdl, kv8_append_kernel<T, 8>, grid, block, 0, s, a, turns);
+        default:                                       // fp32 rows, head_dim 128, 256 rows per page
+            if constexpr (sizeof(T) == 4) return launch_ex(pdl, kv8_append_kernel<T, 16>, grid, block, 0, s, a, turns);
+            return cudaErrorInvalidValue;
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_kv8_append(const Kv8& c, const Kv8Seqs& q, const Kv8Rows& r, const Kv8Append& p, int layer, cudaStream_t s) {
+    const Slots sl = kv8_slots(q, r);
+    const bool wide = c.cfg.dtype == CB_F32;
+    const int es = wide ? 4 : 2, P = 1 << q.shift;
+    AppendArgs a{};
+    a.q = q;
+    a.r = r;
+    a.src[0] = p.k;
+    a.src[1] = p.v;
+    a.kv_stride = p.kv_stride;
+    a.in_q = p.q;
+    a.out_q = p.out_q;
+    a.q_stride = p.q_stride;
+    a.out_q_stride = p.out_q_stride;
+    a.positions = p.positions;
+    a.codes = c.codes;
+    a.scales = c.scales;
+    a.per_seq = sl.per_seq;
+    a.Hkv = c.cfg.n_kv_heads;
+    a.Hq = c.cfg.n_heads;
+    a.units = sl.total * a.Hkv;
+    a.hd = c.cfg.head_dim;
+    a.layer = layer;
+    a.vpr_shift = log2_of(a.hd * es / 16);
+    // a group holds the rows that a call may have in a block
+    const int most_rows = r.start ? r.n_rows : r.each, in_block = 1 << log2_of(most_rows < P ? most_rows : P);
+    const int vectors = in_block << a.vpr_shift, per_thread = wide ? 8 : 4;
+    int tpb = vectors / per_thread;
+    tpb = tpb < 32 ? 32 : tpb > MOST ? MOST : tpb;
+    a.tpb_shift = log2_of(tpb);
+    const int nv = vectors < tpb ? 1 : vectors >> a.tpb_shift;
+    const int threads = tpb < 256 ? 256 : tpb, groups = threads >> a.tpb_shift;
+    a.kv_ctas = (a.units + groups - 1) / groups;
+    int64_t q_ctas = 0;
+    if (p.q) {
+        // as many heads per thread as leave every SM two thousand threads, up to eight
+        const int64_t vectors_of_q = ((int64_t)r.n_rows * a.Hq) << a.vpr_shift;
+        const int64_t heads = vectors_of_q / ((int64_t)c.num_sms * 2048);
+        a.q_heads = heads < 1 ? 1 : heads > 8 ? 8 : (int)heads;
+        a.q_chunks = (a.Hq + a.q_heads - 1) / a.q_heads;
+        q_ctas = ((((int64_t)r.n_rows * a.q_chunks) << a.vpr_shift) + threads - 1) / threads;
+    }
+    const dim3 grid((unsigned)(2 * (int64_t)a.kv_ctas + q_ctas));
+    const Turns& turns = turns_of(p.theta, a.hd);
+    return wide ? append_typed<float>(a, turns, nv, grid, dim3(threads), c.pdl, s) : append_typed<bf16>(a, turns, nv, grid, dim3(threads), c.pdl, s);
+}
+
+}  // namespace cb

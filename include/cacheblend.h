@@ -351,6 +351,27 @@ cb_status cb_kv8_write(cb_kv8* cache, const cb_kv8_seqs* seqs, int32_t layer, in
 cb_status cb_kv8_read(cb_kv8* cache, const cb_kv8_seqs* seqs, int32_t layer, int32_t n_layers, void* k, void* v,
                       int64_t layer_stride, int64_t row_stride, const int32_t* row_start, int32_t n_rows, void* stream);
 
+/* New rows of one layer as its projections give them, q and k not yet rotated (a decoding step, a prompt in pieces): k is
+ * rotated at its rows' positions and k and v become the last rows of their sequences, as cb_kv8_write puts them there; q
+ * is rotated into out_q, ready for cb_kv8_attention.  Pair (2i, 2i + 1) of a head turns by position * rope_theta^(-2i /
+ * head_dim), the blend's rotation.
+ *   q, out_q      device [n_rows][n_heads][head_dim] in cfg.dtype, q_stride and out_q_stride elements between rows; out_q may be
+ *                 q itself (at its stride) and must not overlap k or v.  Both NULL: there is no q to rotate.
+ *   k, v          device [n_rows][n_kv_heads][head_dim] in cfg.dtype, kv_stride elements between rows (all 16-byte aligned,
+ *                 strides multiples of 16 bytes: slices of a fused projection's rows will do)
+ *   positions     device int32 [n_rows]: each row's position, any int32 (where rows were evicted, or in front of the sequence
+ *                 stands a prefix that it shares).  NULL: the row's place in its sequence, len - n + i for row i of its n.
+ *   rope_theta    the rotation's base, 1 or larger
+ *   row_start, n_rows: as for cb_kv8_write.  Rows that belong to no sequence, or to one whose length is out of range or below
+ *                 its number of rows, are neither stored nor rotated; a bad page id skips its rows of k and v only.
+ * Angles are those of float64 positions and frequencies for every int32 position; rotated values are fp32 with errors of
+ * about 2^-24 of their pair's magnitude, rounded once: to out_q's type, or to k's code.  A rotated value that passes fp32 is
+ * kept as an infinity in out_q, as NaN in the cache.
+ * Async on `stream`; no allocation. */
+cb_status cb_kv8_append(cb_kv8* cache, const cb_kv8_seqs* seqs, int32_t layer, const void* q, int64_t q_stride, void* out_q,
+                        int64_t out_q_stride, const void* k, const void* v, int64_t kv_stride, const int32_t* positions,
+                        double rope_theta, const int32_t* row_start, int32_t n_rows, void* stream);
+
 /* Attention of new query rows over the cache of one layer (decoding steps, speculated tokens, a query's rows over a
  * blended context).  The n query rows of a sequence belong to its last n cache rows: row i sees keys
  * 0 .. len - n + i and gives softmax(q k * scale) v over them, query head h reading KV head h / (n_heads /
