@@ -31,7 +31,8 @@ EXPORTED = ("cb_model_create", "cb_model_destroy", "cb_rerope", "cb_blend", "cb_
             "cb_pages_alloc", "cb_pages_retain", "cb_pages_release", "cb_pages_plan_write", "cb_pages_count",
             "cb_pages_free", "cb_index_create", "cb_index_destroy", "cb_index_size", "cb_index_match",
             "cb_select_hkvd", "cb_blend_hkvd", "cb_gradual_layout", "cb_kv8_create", "cb_kv8_destroy", "cb_kv8_status",
-            "cb_kv8_write", "cb_kv8_read", "cb_kv8_attention", "cb_kv8_evict", "cb_blend_kv8", "cb_kv8_append")
+            "cb_kv8_write", "cb_kv8_read", "cb_kv8_attention", "cb_kv8_evict", "cb_blend_kv8", "cb_kv8_append",
+            "cb_kv8_attention_shared")
 CB_STATIC_MAX_CHUNKS = 256
 _I32 = 1 << 31
 CB_STATUS_BAD_TOKEN, CB_STATUS_WAIT_TIMEOUT, CB_STATUS_BAD_ROW = 1, 2, 4
@@ -190,6 +191,8 @@ def lib() -> ctypes.CDLL:
         L.cb_kv8_append.argtypes = [vp, sq, i32, vp, i64, vp, i64, vp, vp, i64, vp, ctypes.c_double, vp, i32, vp]
         L.cb_kv8_attention.restype = ctypes.c_int
         L.cb_kv8_attention.argtypes = [vp, sq, i32, vp, i64, vp, i32, ctypes.c_float, vp, i64, vp, i32, i32, vp]
+        L.cb_kv8_attention_shared.restype = ctypes.c_int
+        L.cb_kv8_attention_shared.argtypes = [vp, sq, vp, sq, i32, vp, i64, vp, i32, ctypes.c_float, vp, i64, vp]
         L.cb_kv8_evict.restype = ctypes.c_int
         L.cb_kv8_evict.argtypes = [vp, sq, vp, i32, i32, i32, vp, i32, i32, i32, i32, vp, vp, vp, vp]
         L.cb_blend_kv8.restype = ctypes.c_int
@@ -497,6 +500,11 @@ class KV8Cache:
         """weight_cells that an attention call of n_q query rows over at most max_len keys needs to return weights."""
         return n_q * n_heads * (-(-max_len // 128) * 128 + 1)
 
+    @staticmethod
+    def shared_cells(n_q: int, n_heads: int, head_dim: int) -> int:
+        """weight_cells that an attention_shared call of n_q query rows needs."""
+        return n_q * n_heads * (head_dim + 2)
+
     # A decoding step calls write and attention once per layer, so the checks below stay within a few microseconds.
     def _int(self, t, name, *shape):
         if t.dtype is not self._i32 or t.get_device() != self._dev or not t.is_contiguous() or t.shape != shape:
@@ -628,6 +636,29 @@ class KV8Cache:
         code = self._lib.cb_kv8_attention(self.handle, sq, layer, qp, qs,
                                           None if q_start is None else self._int(q_start, "q_start", sq.n_seqs + 1), n,
                                           self._scale if scale is None else scale, op, os_, wp, ld, add, self._stream(stream))
+        if code:
+            _check(code)
+        return out
+
+    def attention_shared(self, prefix_table, prefix_lens, table, lens, q, out=None, layer: int = 0, prefix_start=None, q_start=None,
+                         scale=None, prefix_max_len=None, max_len=None, stream=None):
+        """attention where groups of sequences share rows that stand in front of their own: prefix_table (device int32
+        [groups][pages]) and prefix_lens ([groups]) name each group's, which are read once for all its sequences; prefix_start
+        (device int32 [groups + 1]) gives the groups their sequences, None shares them evenly.  A query row sees its whole
+        prefix and then its own sequence's rows as in attention.  The cache needs weight_cells >= shared_cells(n_q, ..)."""
+        if out is None:
+            with self._made_on(stream):
+                out = q.new_empty(q.shape) if q_start is None else q.new_zeros(q.shape)
+        qp, qs, n = self._q(q, "q")
+        op, os_, n_out = self._q(out, "out")
+        if n_out != n:
+            raise ValueError(f"out must have q's {n} rows")
+        pre = self._seqs(prefix_table, prefix_lens, prefix_max_len, layer)
+        sq = self._seqs(table, lens, max_len, layer)
+        code = self._lib.cb_kv8_attention_shared(
+            self.handle, pre, None if prefix_start is None else self._int(prefix_start, "prefix_start", pre.n_seqs + 1), sq, layer,
+            qp, qs, None if q_start is None else self._int(q_start, "q_start", sq.n_seqs + 1), n,
+            self._scale if scale is None else scale, op, os_, self._stream(stream))
         if code:
             _check(code)
         return out

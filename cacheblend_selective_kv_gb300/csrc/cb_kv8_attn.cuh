@@ -16,6 +16,13 @@ namespace {
 
 constexpr int TK = 128;                  // keys per tile
 
+// What a launch computes.  Attention over a prefix that sequences share is two launches, joined by the second:
+//   PLAIN   the rows' results over their sequence's keys
+//   PREFIX  a sequence is a group's prefix, its rows are those of all the group's sequences and see all of it; their sums,
+//           not divided, go to scratch with their references
+//   OWN     PLAIN, and what PREFIX has left is added to a row's sums before they are divided
+enum : int { PLAIN, PREFIX, OWN };
+
 // 16 bytes to shared memory, past L1
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
@@ -41,6 +48,12 @@ struct AttnArgs {
     int score_ld;                        // max_len rounded up to TK
     float2* stats;                       // weights: [Hkv][n_q][G] (max, 1 / sum)
     unsigned* voided;                    // weights: the call's offsets decrease, nothing was computed (NULL: no query rows)
+    // PREFIX and OWN
+    const int* first;                    // [groups + 1] first sequence of each group, or NULL: `per_group` each
+    int per_group, groups, members;      // members: sequences
+    float* prefix_sum;                   // [n_q][Hq][HD]
+    float2* prefix_stat;                 // [n_q][Hq] reference and sum of the exponentials
+    const unsigned* prefix_voided;       // OWN: PREFIX has computed nothing
 };
 
 // k / G and k % G of a column or row of an item
@@ -59,20 +72,40 @@ struct Seq {                             // one sequence: its query rows and len
     int r0, n, len;
     __device__ __forceinline__ int q_tiles(int QT) const { return (n + QT - 1) / QT; }
     // keys that the last row of query tile qt sees
-    __device__ __forceinline__ int visible(int qt, int QT) const { return max(0, len - n + min((qt + 1) * QT, n)); }
-    __device__ __forceinline__ int tiles(int qt, int QT) const { return max(1, (visible(qt, QT) + TK - 1) / TK); }
+    template <int MODE> __device__ __forceinline__ int visible(int qt, int QT) const {
+        return MODE == PREFIX ? len : max(0, len - n + min((qt + 1) * QT, n));
+    }
+    template <int MODE> __device__ __forceinline__ int tiles(int qt, int QT) const { return max(1, (visible<MODE>(qt, QT) + TK - 1) / TK); }
+    // the last key that row q0 sees (PREFIX: and every other row)
+    template <int MODE> __device__ __forceinline__ int position(int q0) const { return MODE == PREFIX ? len - 1 : len - n + q0; }
 };
-__device__ __forceinline__ Seq seq_at(const AttnArgs& p, int s) {
+// the rows of a group: those of its sequences, which see a prefix of no rows where its length is out of range
+__device__ __forceinline__ Seq group_at(const AttnArgs& p, int g) {
+    const int s0 = p.first ? p.first[g] : g * p.per_group, s1 = p.first ? p.first[g + 1] : s0 + p.per_group;
+    if (s0 >= 0 && s1 >= s0 && s1 <= p.members) {
+        const int r0 = p.r.start ? p.r.start[s0] : s0 * p.r.each, r1 = p.r.start ? p.r.start[s1] : s1 * p.r.each;
+        if (r0 >= 0 && r1 >= r0 && r1 <= p.r.n_rows) {
+            const int len = kv8_len(p.q, g);
+            const bool good = len >= 0 && len <= p.q.max_len;
+            if (!good) atomicOr(p.q.status, ST_BAD_ROW);
+            return Seq{r0, r1 - r0, good ? len : 0};
+        }
+    }
+    atomicOr(p.q.status, ST_BAD_ROW);
+    return Seq{0, 0, -1};
+}
+template <int MODE = PLAIN> __device__ __forceinline__ Seq seq_at(const AttnArgs& p, int s) {
+    if constexpr (MODE == PREFIX) return group_at(p, s);
     Seq q;
     int r1;
     if (!kv8_rows(p.q, p.r, s, q.r0, r1, q.len)) return Seq{0, 0, r1 < q.r0 ? -1 : 0};
     q.n = r1 - q.r0;
     return q;
 }
-__device__ __forceinline__ int seq_places(const AttnArgs& p, const Seq& q) {
+template <int MODE> __device__ __forceinline__ int seq_places(const AttnArgs& p, const Seq& q) {
     int t = 0;
 #pragma unroll 1
-    for (int qt = 0; qt < q.q_tiles(p.QT); ++qt) t += p.ahead + q.tiles(qt, p.QT);
+    for (int qt = 0; qt < q.q_tiles(p.QT); ++qt) t += p.ahead + q.tiles<MODE>(qt, p.QT);
     return t * p.Hkv;
 }
 
@@ -83,10 +116,10 @@ __device__ __forceinline__ float* score_of(const AttnArgs& p, const Seq& q, int 
 }
 
 // A tile in the list: item (s, query tile qt, g) and tile t of its nt.
-struct Cursor {
+template <int MODE> struct Cursor {
     int s, qt, g, t, nt;
     Seq q;
-    __device__ __forceinline__ void settle(const AttnArgs& p) { nt = q.tiles(qt, p.QT); }
+    __device__ __forceinline__ void settle(const AttnArgs& p) { nt = q.tiles<MODE>(qt, p.QT); }
     // to the first tile of the next item
     __device__ __forceinline__ void next_item(const AttnArgs& p) {
         t = 0;
@@ -95,7 +128,7 @@ struct Cursor {
         if (++qt >= q.q_tiles(p.QT)) {
             qt = 0;
             do {
-                q = ++s < p.q.n ? seq_at(p, s) : Seq{0, 1, 0};
+                q = ++s < p.q.n ? seq_at<MODE>(p, s) : Seq{0, 1, 0};
             } while (q.n == 0);
         }
         settle(p);
@@ -176,17 +209,18 @@ template <typename T> __device__ __forceinline__ void store4(T* o, const float4&
 struct Piece {
     int per, count;
 };
-struct Find {                            // shared memory of find_piece
-    Cursor cur;
+template <int MODE> struct Find {        // shared memory of find_piece
+    Cursor<MODE> cur;
     int begin, count;                    // place at which the first tile's item begins
     int sums[32];
 };
 // Of an item of nt tiles, of which this CTA has n_here from tile `first` on but not all: the CTA it begins in, and how many
 // CTAs have a piece of it.  One that began before is this CTA's first; of one that begins here the others have what is left.
-__device__ __forceinline__ int first_cta(const AttnArgs& p, const Find& f, int per, int first) {
+template <int MODE> __device__ __forceinline__ int first_cta(const AttnArgs& p, const Find<MODE>& f, int per, int first) {
     return first > 0 ? (int)((unsigned)(f.begin + p.ahead) / (unsigned)per) : (int)blockIdx.x;
 }
-__device__ __forceinline__ int piece_count(const AttnArgs& p, const Find& f, int per, int first, int n_here, int nt) {
+template <int MODE>
+__device__ __forceinline__ int piece_count(const AttnArgs& p, const Find<MODE>& f, int per, int first, int n_here, int nt) {
     const unsigned rest = first > 0 ? (unsigned)(f.begin + p.ahead) % (unsigned)per + nt : (unsigned)(per + nt - n_here);
     return (int)((rest + per - 1) / (unsigned)per);
 }
@@ -197,19 +231,20 @@ __device__ __forceinline__ int piece_count(const AttnArgs& p, const Find& f, int
 // several, whose scores would lie on one another and whose places could pass 32 bits, and then every CTA gets an empty
 // piece.  (This and what ends an item run once or twice per CTA, from instructions that have to be fetched first: short
 // loops and 32-bit arithmetic are worth more here than fewer steps.)
-template <int THREADS, typename F, typename H>
-__device__ __forceinline__ void find_piece(const AttnArgs& p, Find& f, Piece& mine, Cursor& cur, F before_sync, H after_sync) {
+template <int THREADS, int MODE, typename F, typename H>
+__device__ __forceinline__ void find_piece(const AttnArgs& p, Find<MODE>& f, Piece& mine, Cursor<MODE>& cur, F before_sync, H after_sync) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const Seq q_own = tid < p.q.n ? seq_at(p, tid) : Seq{0, 0, 0};
-    const int n_own = seq_places(p, q_own);
+    const Seq q_own = tid < p.q.n ? seq_at<MODE>(p, tid) : Seq{0, 0, 0};
+    const int n_own = seq_places<MODE>(p, q_own);
     bool decrease = q_own.len < 0;
+    if constexpr (MODE == OWN) decrease |= *p.prefix_voided != 0;
     {
         int sum = n_own;
 #pragma unroll 1
         for (int s = tid + THREADS; s < p.q.n; s += THREADS) {
-            const Seq q = seq_at(p, s);
+            const Seq q = seq_at<MODE>(p, s);
             decrease |= q.len < 0;
-            sum += seq_places(p, q);
+            sum += seq_places<MODE>(p, q);
         }
         sum = __reduce_add_sync(0xffffffffu, sum);
         if (lane == 0) f.sums[warp] = sum;
@@ -232,8 +267,8 @@ __device__ __forceinline__ void find_piece(const AttnArgs& p, Find& f, Piece& mi
         Seq q = q_own;
         int n = n_own;
         if (s0 > 0) {
-            q = s < p.q.n ? seq_at(p, s) : Seq{0, 0, 0};
-            n = seq_places(p, q);
+            q = s < p.q.n ? seq_at<MODE>(p, s) : Seq{0, 0, 0};
+            n = seq_places<MODE>(p, q);
         }
         int x = n;
 #pragma unroll 1
@@ -249,7 +284,7 @@ __device__ __forceinline__ void find_piece(const AttnArgs& p, Find& f, Piece& mi
         base += __reduce_add_sync(0xffffffffu, w);
         if (n > 0 && before <= p0 && p0 < before + n) {
             int left = p0 - before;
-            Cursor u{s, 0, 0, 0, 0, q};
+            Cursor<MODE> u{s, 0, 0, 0, 0, q};
             u.settle(p);
 #pragma unroll 1
             while (left >= (p.ahead + u.nt) * p.Hkv) {
@@ -285,6 +320,55 @@ template <int ROW> __device__ __forceinline__ uint32_t f8_at(uint32_t row, uint3
                       : row * 64 + ((((b >> 4) ^ (row >> 1)) & 3) << 4) + (b & 15);
 }
 
+// A row's sums over its own keys and over the prefix, relative to their references m and pre.x: the factors that bring
+// both to the larger one, and the joint sum of exponentials.
+struct Merge {
+    float own, pre, l;
+    __device__ __forceinline__ Merge(float m, float l_own, float2 before) {
+        const float top = fmaxf(m, before.x);
+        own = m == -INFINITY ? 0.f : exp2_fast(m - top);
+        pre = before.x == -INFINITY ? 0.f : exp2_fast(before.x - top);
+        l = l_own * own + before.y * pre;
+    }
+    __device__ __forceinline__ float operator()(float o, float before) const { return o * own + before * pre; }
+    __device__ __forceinline__ float4 operator()(const float4& o, const float4& b) const {
+        return make_float4((*this)(o.x, b.x), (*this)(o.y, b.y), (*this)(o.z, b.z), (*this)(o.w, b.w));
+    }
+};
+// whether sequence s has a prefix (OWN; its group's offsets were in order)
+__device__ __forceinline__ bool has_prefix(const AttnArgs& p, int s) {
+    return !p.first || (s >= p.first[0] && s < p.first[p.groups]);
+}
+__device__ __forceinline__ int64_t prefix_at(const AttnArgs& p, int row, int head) { return (int64_t)row * p.Hq + head; }
+
+inline AttnArgs attn_args(const Kv8& c, const Kv8Seqs& q, const Kv8Rows& r, const Kv8Attn& a, int layer) {
+    const int64_t blocks = c.cfg.n_pages * c.cfg.n_kv_heads, k0 = (int64_t)layer * 2 * blocks;
+    AttnArgs p{};
+    p.q = q;
+    p.r = r;
+    p.a = a;
+    p.ks = c.scales + k0;
+    p.vs = p.ks + blocks;
+    p.Hq = c.cfg.n_heads;
+    p.Hkv = c.cfg.n_kv_heads;
+    p.G = p.Hq / p.Hkv;
+    p.inv_g = (65536 + p.G - 1) / p.G;
+    p.kz = 2 * layer;
+    p.box = c.cfg.page_size < TK ? c.cfg.page_size : TK;
+    p.part = c.part;
+    p.arrived = c.arrived;
+    p.stats = c.stats;
+    p.score_ld = (q.max_len + TK - 1) / TK * TK;
+    return p;
+}
+// Up to 32 columns (rows of a sequence, on average, times heads of a group) stand in one item of the kernel for few rows, and
+// beyond that keys and values are read and P is formed once per item of 32 (64 sequences of 2K: 32 columns 111 us there, 121
+// in the kernel for many rows; 48 columns 205 and 122).
+inline bool many_rows(const Kv8& c, const AttnArgs& p) {
+    const int rows = (p.r.n_rows + p.q.n - 1) / p.q.n;
+    return c.cfg.dtype == CB_BF16 && rows * p.G > 32;
+}
+
 // ------------------------------------------------------------------------------------------------
 // tiles of codes and their scales into shared memory
 // ------------------------------------------------------------------------------------------------
@@ -313,8 +397,8 @@ template <int N> struct ScaleRing {      // scales of N tiles, under way or in u
 // looks after one box (at most a page) of a tile.  Its page id is loaded LOOK + 1 tiles ahead and the scales are asked for
 // LOOK tiles ahead, so that neither is waited for when memory is busy.  Rows that belong to no page of the pool or lie
 // behind the sequence's last page are not loaded.  Returns when every copy has landed.
-template <int HD, int KS, int VS, int RING>
-__device__ __forceinline__ void produce_tiles(const AttnArgs& p, const CUtensorMap& map, Cursor cur, int count, uint8_t* sK,
+template <int HD, int KS, int VS, int RING, int MODE>
+__device__ __forceinline__ void produce_tiles(const AttnArgs& p, const CUtensorMap& map, Cursor<MODE> cur, int count, uint8_t* sK,
                                               uint8_t* sV, uint64_t* k_full, uint64_t* k_empty, uint64_t* v_full,
                                               uint64_t* v_empty, ScaleRing<RING>& ring, volatile int* abort) {
     const int lane = threadIdx.x & 31, boxes = TK / p.box, rows = p.box, in_page = (1 << p.q.shift) - 1;
@@ -323,7 +407,7 @@ __device__ __forceinline__ void produce_tiles(const AttnArgs& p, const CUtensorM
         int page, g, off;                                        // off: first row in the page
         bool need;                                               // the box holds rows of the sequence
     };
-    auto look = [&](const Cursor& u) {
+    auto look = [&](const Cursor<MODE>& u) {
         const int j = u.t * TK + lane * rows;
         Ahead a{0, u.g, j & in_page, lane < boxes && j < u.q.len};
         if (a.need) a.page = p.q.table[(int64_t)u.s * p.q.table_ld + (j >> p.q.shift)];

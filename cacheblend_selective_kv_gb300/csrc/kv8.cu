@@ -139,6 +139,29 @@ cb_status check_io(const cb_kv8& c, const void* k, const void* v, int64_t layer_
     return CB_OK;
 }
 
+// query and output rows of an attention call
+cb_status check_q(const cb_kv8& c, const void* q, int64_t q_stride, int32_t n_q, float scale, const void* out, int64_t out_stride,
+                  const char* who) {
+    const int64_t w = (int64_t)c.cfg.n_heads * c.cfg.head_dim, es = c.cfg.dtype == CB_BF16 ? 2 : 4;
+    if (!std::isfinite(scale)) return fail(CB_ERR_INVALID_ARG, "%s: scale is not finite", who);
+    if (n_q == 0) return CB_OK;
+    if (!q || !out) return fail(CB_ERR_INVALID_ARG, "%s: null q or out", who);
+    if ((uintptr_t)q % 16 || (uintptr_t)out % 16 || q_stride * es % 16 || out_stride * es % 16)
+        return fail(CB_ERR_INVALID_ARG, "%s: q, out and their strides must be multiples of 16 bytes", who);
+    if (q_stride < w || out_stride < w || q_stride > ((int64_t)1 << 40) || out_stride > ((int64_t)1 << 40))
+        return fail(CB_ERR_INVALID_ARG, "%s: a row stride below a row's %lld elements, or out of range", who, (long long)w);
+    if (overlap(q, ((n_q - 1) * q_stride + w) * es, out, ((n_q - 1) * out_stride + w) * es))
+        return fail(CB_ERR_INVALID_ARG, "%s: q and out overlap", who);
+    return CB_OK;
+}
+
+// tiles of 128 keys and at least one query row, of every KV head, and what an item counts besides
+cb_status check_places(const cb_kv8& c, int32_t n_q, const Kv8Seqs& q, const char* who) {
+    if (((int64_t)n_q + q.n) * c.cfg.n_kv_heads > 0x7fffffff / ((int64_t)q.max_len / 128 + 8))
+        return fail(CB_ERR_UNSUPPORTED, "%s: %d query rows over %d keys are too many for one call", who, n_q, q.max_len);
+    return CB_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -329,17 +352,8 @@ cb_status cb_kv8_attention(cb_kv8* c, const cb_kv8_seqs* seqs, int32_t layer, co
     if (st == CB_OK) st = check_seqs(*c, seqs, who, sq);
     if (st == CB_OK) st = check_rows(sq, q_start, n_q, who, r);
     if (st != CB_OK) return st;
-    const int64_t w = (int64_t)c->cfg.n_heads * c->cfg.head_dim, es = c->cfg.dtype == CB_BF16 ? 2 : 4;
-    if (!std::isfinite(scale)) return fail(CB_ERR_INVALID_ARG, "%s: scale is not finite", who);
-    if (n_q > 0) {
-        if (!q || !out) return fail(CB_ERR_INVALID_ARG, "%s: null q or out", who);
-        if ((uintptr_t)q % 16 || (uintptr_t)out % 16 || q_stride * es % 16 || out_stride * es % 16)
-            return fail(CB_ERR_INVALID_ARG, "%s: q, out and their strides must be multiples of 16 bytes", who);
-        if (q_stride < w || out_stride < w || q_stride > ((int64_t)1 << 40) || out_stride > ((int64_t)1 << 40))
-            return fail(CB_ERR_INVALID_ARG, "%s: a row stride below a row's %lld elements, or out of range", who, (long long)w);
-        if (overlap(q, ((n_q - 1) * q_stride + w) * es, out, ((n_q - 1) * out_stride + w) * es))
-            return fail(CB_ERR_INVALID_ARG, "%s: q and out overlap", who);
-    }
+    st = check_q(*c, q, q_stride, n_q, scale, out, out_stride, who);
+    if (st != CB_OK) return st;
     if (weights) {
         if (weights_ld < sq.max_len) return fail(CB_ERR_INVALID_ARG, "%s: weights_ld %d below max_len %d", who, weights_ld, sq.max_len);
         const int64_t row = (((int64_t)sq.max_len + 127) / 128) * 128 + 1, rows = (int64_t)n_q * c->cfg.n_heads;
@@ -347,15 +361,47 @@ cb_status cb_kv8_attention(cb_kv8* c, const cb_kv8_seqs* seqs, int32_t layer, co
             return fail(CB_ERR_INVALID_ARG, "%s: returning weights needs %.0f cells, the cache was created with %lld", who,
                         (double)rows * (double)row, (long long)c->cfg.weight_cells);
     }
-    // tiles of 128 keys and at least one query row, of every KV head, and what an item counts besides
-    if (((int64_t)n_q + sq.n) * c->cfg.n_kv_heads > 0x7fffffff / ((int64_t)sq.max_len / 128 + 8))
-        return fail(CB_ERR_UNSUPPORTED, "%s: %d query rows over %d keys are too many for one call", who, n_q, sq.max_len);
+    st = check_places(*c, n_q, sq, who);
+    if (st != CB_OK) return st;
     if (sq.n == 0 || (n_q == 0 && !weights)) return CB_OK;
     OnDevice on;
     st = on.to(c, who);
     if (st != CB_OK) return st;
     const Kv8Attn a{q, q_stride, out, out_stride, scale, weights, weights_ld, add != 0};
     return cuda_result(launch_kv8_attention(*c, sq, r, a, layer, (cudaStream_t)stream), who);
+}
+
+cb_status cb_kv8_attention_shared(cb_kv8* c, const cb_kv8_seqs* prefixes, const int32_t* prefix_start, const cb_kv8_seqs* seqs,
+                                  int32_t layer, const void* q, int64_t q_stride, const int32_t* q_start, int32_t n_q, float scale,
+                                  void* out, int64_t out_stride, void* stream) {
+    const char* who = "cb_kv8_attention_shared";
+    Kv8Seqs pre, sq;
+    Kv8Rows r;
+    cb_status st = check_handle(c, who);
+    if (st == CB_OK) st = check_layers(*c, layer, 1, who);
+    if (st == CB_OK) st = check_seqs(*c, prefixes, who, pre);
+    if (st == CB_OK) st = check_seqs(*c, seqs, who, sq);
+    if (st == CB_OK) st = check_rows(sq, q_start, n_q, who, r);
+    if (st == CB_OK) st = check_q(*c, q, q_stride, n_q, scale, out, out_stride, who);
+    if (st != CB_OK) return st;
+    if (!prefix_start && pre.n > 0 && sq.n % pre.n != 0)
+        return fail(CB_ERR_INVALID_ARG, "%s: %d sequences cannot be shared evenly by %d prefixes (give their first sequences)", who, sq.n, pre.n);
+    st = check_places(*c, n_q, pre, who);
+    if (st == CB_OK) st = check_places(*c, n_q, sq, who);
+    if (st != CB_OK) return st;
+    const bool shared = pre.n > 0 && pre.max_len > 0;
+    const int64_t row = (int64_t)c->cfg.n_heads * (c->cfg.head_dim + 2);
+    if (shared && n_q > c->cfg.weight_cells / row)
+        return fail(CB_ERR_INVALID_ARG, "%s: %d query rows need %lld cells of scratch, the cache was created with %lld", who, n_q,
+                    (long long)(n_q * row), (long long)c->cfg.weight_cells);
+    if (sq.n == 0 || n_q == 0) return CB_OK;
+    OnDevice on;
+    st = on.to(c, who);
+    if (st != CB_OK) return st;
+    const Kv8Attn a{q, q_stride, out, out_stride, scale, nullptr, 0, false};
+    if (!shared) return cuda_result(launch_kv8_attention(*c, sq, r, a, layer, (cudaStream_t)stream), who);
+    const Kv8Prefix p{pre, prefix_start, prefix_start ? 0 : sq.n / pre.n, c->scores};
+    return cuda_result(launch_kv8_shared(*c, p, sq, r, a, layer, (cudaStream_t)stream), who);
 }
 
 cb_status cb_kv8_evict(cb_kv8* c, const cb_kv8_seqs* seqs, const int32_t* dst_table, int32_t dst_ld, int32_t layer,

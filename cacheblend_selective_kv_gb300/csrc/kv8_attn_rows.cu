@@ -46,10 +46,11 @@ constexpr float SLACK = 38.f;            // how far (log2) a term of the sum may
 constexpr float P_UP = 128.f;            // P is stored this much larger: its largest values are 2^7 .. 2^15 of fp16's 2^16
 
 struct Todo {                            // an item that begins in a CTA and ends in another: its rows and pieces
-    int row0, cols, g, pieces;
+    int row0, cols, g, pieces;           // g: its KV head, and HAS_PREFIX
 };
+constexpr int HAS_PREFIX = 1 << 16;      // OWN: its rows have a prefix
 
-struct RowsShared {
+template <int MODE> struct RowsShared {
     uint64_t kc_full[KT], kc_empty[KT], vc_full[VT], vc_empty[VT];          // codes
     uint64_t k_full[2], k_empty[2], v_full[2], pv_done[2], s_full[2], p_full[2];
     uint64_t rows_full[MARKS];           // an item's row scales are written
@@ -58,7 +59,7 @@ struct RowsShared {
     ScaleRing<RING> ring;
     uint32_t tmem;
     int abort;
-    Find find;
+    Find<MODE> find;
     int any_nan[MARKS];                  // an item's V held NaN that not all of its rows see
 };
 
@@ -69,7 +70,7 @@ template <int HD> struct Rows {
     // floats: row scales [MARKS][ROWS], (X, sum, R, -) [2][ROWS][4]; ints: nan_from [MARKS][HD]
     static constexpr int X_FLOATS = MARKS * ROWS + 8 * ROWS + MARKS * HD;
     static constexpr int OFF_C = OFF_X + X_FLOATS * 4;
-    static constexpr int BYTES = OFF_C + (int)sizeof(RowsShared);
+    static constexpr int BYTES = OFF_C + (int)sizeof(RowsShared<PLAIN>);
     static constexpr int PIECE = ROWS * (HD + 2);
     static_assert(BYTES <= 227 * 1024, "shared memory");
 };
@@ -125,7 +126,7 @@ __device__ __noinline__ void take_nan(uint4& x, int j, int* marks, int* any) {
     x = make_uint4(cw[0], cw[1], cw[2], cw[3]);
 }
 
-template <int HD, bool SCORES>
+template <int HD, bool SCORES, int MODE>
 __global__ void __launch_bounds__(THREADS, 1) kv8_rows_kernel(const __grid_constant__ CUtensorMap map, const AttnArgs p) {
     using S = Rows<HD>;
     extern __shared__ __align__(1024) uint8_t sm[];
@@ -135,7 +136,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_rows_kernel(const __grid_const
     float* row_scale = reinterpret_cast<float*>(sm + S::OFF_X);
     float* halves = row_scale + MARKS * ROWS;
     int* nan_marks = reinterpret_cast<int*>(halves + 8 * ROWS);
-    RowsShared& c = *reinterpret_cast<RowsShared*>(sm + S::OFF_C);
+    RowsShared<MODE>& c = *reinterpret_cast<RowsShared<MODE>*>(sm + S::OFF_C);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     unsigned* status = p.q.status;
     volatile int* abort = &c.abort;
@@ -180,7 +181,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_rows_kernel(const __grid_const
     grid_dep_launch();
     grid_dep_wait();
     Piece mine;
-    Cursor cur;
+    Cursor<MODE> cur;
     find_piece<THREADS>(p, c.find, mine, cur, [] { ptx::tc_fence_before(); }, [] { ptx::tc_fence_after(); });
     const int count = mine.count;
     const uint32_t tmem = c.tmem;                       // S and P: two buffers of 128 columns; O of each half at 256
@@ -198,7 +199,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_rows_kernel(const __grid_const
             const int st = i & 1;
             const uint32_t par = ((i >> 1) & 1) ^ 1;
             const Seq q = cur.q;
-            const int q0 = cur.qt * p.QT, cols = min(p.QT, q.n - q0) * p.G, pos0 = q.len - q.n + q0, tile = cur.t;
+            const int q0 = cur.qt * p.QT, cols = min(p.QT, q.n - q0) * p.G, pos0 = q.position<MODE>(q0), tile = cur.t;
             if (begins) {
                 ++item;
                 const bf16* qbase = (const bf16*)p.a.q + (int64_t)(q.r0 + q0) * p.a.q_stride + (int64_t)cur.g * p.G * HD;
@@ -387,7 +388,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_rows_kernel(const __grid_const
             const int first = cur.t, n_here = min(cur.nt - first, count - i), g = cur.g;
             const Seq q = cur.q;
             const int q0 = cur.qt * p.QT, cols = min(p.QT, q.n - q0) * p.G;
-            const int pos0 = q.len - q.n + q0, pos = pos0 + div_g(p, row);       // positions of the item's first row and of this one
+            const int pos0 = q.position<MODE>(q0), pos = MODE == PREFIX ? pos0 : pos0 + div_g(p, row);       // positions of the item's first row and of this one
             const int64_t stat0 = ((int64_t)g * p.r.n_rows + q.r0 + q0) * p.G;
             float ref = -INFINITY, at = -INFINITY, most = -INFINITY;     // R, X and M
             float l = 0.f, up = 0.f, row_mul = 0.f;              // the sum of 2^(x - X); 2^(X - R) P_UP
@@ -522,7 +523,12 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_rows_kernel(const __grid_const
             };
             const bool marked = c.any_nan[item % MARKS] != 0;
             const int* marks = nan_marks + (item % MARKS) * HD;
-            const float inv = 1.f / L;
+            float2 before = make_float2(-INFINITY, 0.f);
+            const bool prefix = MODE == OWN && has_prefix(p, cur.s);
+            const int64_t pre_at = MODE == PLAIN ? 0 : prefix_at(p, q.r0 + q0 + div_g(p, row), g * p.G + mod_g(p, row));
+            if (MODE == OWN && prefix && whole && row < cols) before = p.prefix_stat[pre_at];
+            const Merge merge(X, L, before);                     // (unused but by OWN)
+            const float inv = 1.f / (MODE == OWN ? merge.l : L);
             // this thread's half of the row's dims
 #pragma unroll 1
             for (int k = 0; k < HD / 2; k += 16) {
@@ -539,7 +545,28 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_rows_kernel(const __grid_const
                     a0[y] = o;
                 }
                 if (row < cols) {
-                    if (whole) {
+                    if (MODE == PREFIX && whole) {
+                        float4* o = reinterpret_cast<float4*>(p.prefix_sum + pre_at * HD + d);
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) o[y] = make_float4(a0[4 * y], a0[4 * y + 1], a0[4 * y + 2], a0[4 * y + 3]);
+                    } else if (MODE == OWN && whole) {
+                        const float4* b = reinterpret_cast<const float4*>(p.prefix_sum + pre_at * HD + d);
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) {
+                            const float4 x = prefix ? b[y] : make_float4(0.f, 0.f, 0.f, 0.f);
+                            a1[4 * y] = x.x;
+                            a1[4 * y + 1] = x.y;
+                            a1[4 * y + 2] = x.z;
+                            a1[4 * y + 3] = x.w;
+                        }
+                        uint32_t w[8];
+#pragma unroll
+                        for (int y = 0; y < 8; ++y)
+                            w[y] = merge.l != 0.f ? bf16_pair(merge(a0[2 * y], a1[2 * y]) * inv, merge(a0[2 * y + 1], a1[2 * y + 1]) * inv) : 0u;
+                        uint4* o = reinterpret_cast<uint4*>(out_at(row) + d);
+                        o[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                        o[1] = make_uint4(w[4], w[5], w[6], w[7]);
+                    } else if (whole) {
                         uint32_t w[8];
 #pragma unroll
                         for (int y = 0; y < 8; ++y) w[y] = L != 0.f ? bf16_pair(a0[2 * y] * inv, a0[2 * y + 1] * inv) : 0u;
@@ -558,12 +585,13 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_rows_kernel(const __grid_const
             if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&c.o_free));
             if (whole) {
                 if (SCORES && hf == 0 && row < cols) p.stats[stat0 + row] = make_float2(X, inv);
+                if (MODE == PREFIX && hf == 0 && row < cols) p.prefix_stat[pre_at] = make_float2(X, L);
                 ptx::named_bar_sync(3 + quarter, 64);            // `halves` has been read
             } else {
                 if (hf == 0 && row < cols)
                     *reinterpret_cast<float2*>(piece_at(blockIdx.x - u0) + ROWS * HD + 2 * row) = make_float2(X, L);
                 // (the CTA in which the item begins says so to the joining kernel)
-                if (first == 0 && tid == 0) todo = Todo{q.r0 + q0, cols, g, n_pieces};
+                if (first == 0 && tid == 0) todo = Todo{q.r0 + q0, cols, g | (prefix ? HAS_PREFIX : 0), n_pieces};
                 ptx::named_bar_sync(3 + quarter, 64);            // `halves` has been read
             }
             if (i < count) cur.next_item(p);
@@ -581,7 +609,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_rows_kernel(const __grid_const
 // The items that span CTAs, a row per warp: block (u, y) has rows 8 y .. 8 y + 7 of the item that begins in CTA u.  A kernel
 // of its own, because a piece is 128 rows: joined by the CTA that ends last, the 64 rows of a query over 8K took 15 us of
 // one CTA's time, and with two rows per warp 1 us more than this way.
-template <int HD>
+template <int HD, int MODE>
 __global__ void __launch_bounds__(256) kv8_join_kernel(const AttnArgs p) {
     __shared__ float4 buf[8][8 * 32];
     grid_dep_launch();
@@ -592,9 +620,22 @@ __global__ void __launch_bounds__(256) kv8_join_kernel(const AttnArgs p) {
     const auto piece_at = [&](int u) { return p.part + (int64_t)((u0 + u) * 2 + (u == 0 ? 1 : 0)) * Rows<HD>::PIECE; };
     float m, l;
     const float4 a = join_pieces<HD, 8>(piece_at, d.pieces, k * HD, ROWS * HD + 2 * k, m, l, buf[warp]);
-    bf16* out = (bf16*)p.a.out + (int64_t)(d.row0 + div_g(p, k)) * p.a.out_stride + (int64_t)(d.g * p.G + mod_g(p, k)) * HD;
+    const int g = d.g & (HAS_PREFIX - 1), row = d.row0 + div_g(p, k), head = g * p.G + mod_g(p, k);
+    bf16* out = (bf16*)p.a.out + (int64_t)row * p.a.out_stride + (int64_t)head * HD;
+    if constexpr (MODE == PREFIX) {
+        const int64_t at = prefix_at(p, row, head);
+        if (lane < HD / 4) *reinterpret_cast<float4*>(p.prefix_sum + at * HD + lane * 4) = a;
+        if (lane == 0) p.prefix_stat[at] = make_float2(m, l);
+        return;
+    }
+    if (MODE == OWN && (d.g & HAS_PREFIX)) {
+        const int64_t at = prefix_at(p, row, head);
+        const Merge merge(m, l, p.prefix_stat[at]);
+        if (lane < HD / 4) store4(out + lane * 4, merge(a, *reinterpret_cast<const float4*>(p.prefix_sum + at * HD + lane * 4)), merge.l);
+        return;
+    }
     if (lane < HD / 4) store4(out + lane * 4, a, l);
-    if (p.scores && lane == 0) p.stats[((int64_t)d.g * p.r.n_rows + d.row0) * p.G + k] = make_float2(m, 1.f / l);
+    if (p.scores && lane == 0) p.stats[((int64_t)g * p.r.n_rows + d.row0) * p.G + k] = make_float2(m, 1.f / l);
 }
 
 // weights[s][g][j] = sum over the sequence's rows and the group's heads of exp2(score - max) / sum: four keys per warp, the
@@ -629,9 +670,9 @@ __global__ void __launch_bounds__(256) kv8_rows_weights_kernel(const AttnArgs p)
     }
 }
 
-template <int HD, bool SCORES> cudaError_t launch_dim(const Kv8& c, AttnArgs& p, cudaStream_t s) {
+template <int HD, bool SCORES, int MODE> cudaError_t launch_dim(const Kv8& c, AttnArgs& p, cudaStream_t s) {
     static std::atomic<uint64_t> done{0};
-    const cudaError_t e = smem_limit_once(kv8_rows_kernel<HD, SCORES>, Rows<HD>::BYTES, done);
+    const cudaError_t e = smem_limit_once(kv8_rows_kernel<HD, SCORES, MODE>, Rows<HD>::BYTES, done);
     if (e != cudaSuccess) return e;
     p.QT = ROWS / p.G;
     // 4096 rows over 4096 keys: 975 us when only tiles counted, 424 with 2 places; 256 with 4 and 5, 261 with 6 as the kernel
@@ -643,8 +684,8 @@ template <int HD, bool SCORES> cudaError_t launch_dim(const Kv8& c, AttnArgs& p,
     CUtensorMap map;
     memcpy(&map, c.map, sizeof map);
     const unsigned ctas = (unsigned)(tiles < c.num_sms ? tiles : c.num_sms);
-    cudaError_t err = launch_ex(c.pdl, kv8_rows_kernel<HD, SCORES>, dim3(ctas), dim3(THREADS), Rows<HD>::BYTES, s, map, p);
-    if (err == cudaSuccess) err = launch_ex(c.pdl, kv8_join_kernel<HD>, dim3(ctas, ROWS / 8), dim3(256), 0, s, p);
+    cudaError_t err = launch_ex(c.pdl, kv8_rows_kernel<HD, SCORES, MODE>, dim3(ctas), dim3(THREADS), Rows<HD>::BYTES, s, map, p);
+    if (err == cudaSuccess) err = launch_ex(c.pdl, kv8_join_kernel<HD, MODE>, dim3(ctas, ROWS / 8), dim3(256), 0, s, p);
     if (err == cudaSuccess && SCORES)
         err = launch_ex(c.pdl, kv8_rows_weights_kernel, dim3((p.q.max_len + 31) / 32, p.Hkv, p.q.n), dim3(256), 0, s, p);
     return err;
@@ -654,11 +695,14 @@ template <int HD, bool SCORES> cudaError_t launch_dim(const Kv8& c, AttnArgs& p,
 
 size_t kv8_rows_part_floats(int num_sms) { return (size_t)num_sms * 2 * Rows<128>::PIECE; }
 
-cudaError_t launch_kv8_rows(const Kv8& c, const void* attn_args, cudaStream_t s) {
+cudaError_t launch_kv8_rows(const Kv8& c, const void* attn_args, int mode, cudaStream_t s) {
     AttnArgs p = *static_cast<const AttnArgs*>(attn_args);
     p.todo = c.todo;
-    if (p.scores) return c.cfg.head_dim == 128 ? launch_dim<128, true>(c, p, s) : launch_dim<64, true>(c, p, s);
-    return c.cfg.head_dim == 128 ? launch_dim<128, false>(c, p, s) : launch_dim<64, false>(c, p, s);
+    const bool wide = c.cfg.head_dim == 128;
+    if (mode == PREFIX) return wide ? launch_dim<128, false, PREFIX>(c, p, s) : launch_dim<64, false, PREFIX>(c, p, s);
+    if (mode == OWN) return wide ? launch_dim<128, false, OWN>(c, p, s) : launch_dim<64, false, OWN>(c, p, s);
+    if (p.scores) return wide ? launch_dim<128, true, PLAIN>(c, p, s) : launch_dim<64, true, PLAIN>(c, p, s);
+    return wide ? launch_dim<128, false, PLAIN>(c, p, s) : launch_dim<64, false, PLAIN>(c, p, s);
 }
 
 }  // namespace cb

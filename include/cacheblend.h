@@ -305,8 +305,9 @@ typedef struct {
     int32_t dtype;           /* cb_dtype of the K/V rows, queries and outputs of the calls */
     int32_t page_size;       /* rows per page: 16, 32, 64, 128 or 256 */
     int64_t n_pages;         /* n_pages * page_size * n_kv_heads < 2^31 */
-    int64_t weight_cells;    /* floats of scratch for attention calls that return weights (0: none): such a call needs
-                                n_q * n_heads * (max_len rounded up to 128, plus 1) */
+    int64_t weight_cells;    /* floats of scratch (0: none) for attention calls that return weights: such a call needs
+                                n_q * n_heads * (max_len rounded up to 128, plus 1); and for cb_kv8_attention_shared:
+                                n_q * n_heads * (head_dim + 2) */
 } cb_kv8_config;
 
 /* A batch of sequences: row j of sequence s is row j % page_size of page table[s * table_ld + j / page_size].  All
@@ -398,6 +399,27 @@ cb_status cb_kv8_append(cb_kv8* cache, const cb_kv8_seqs* seqs, int32_t layer, c
 cb_status cb_kv8_attention(cb_kv8* cache, const cb_kv8_seqs* seqs, int32_t layer, const void* q, int64_t q_stride,
                            const int32_t* q_start, int32_t n_q, float scale, void* out, int64_t out_stride,
                            float* weights, int32_t weights_ld, int32_t add, void* stream);
+
+/* cb_kv8_attention where sequences share what stands in front of them (many requests on one retrieved context, several
+ * answers to one prompt): the shared rows are stored once and read once for all the rows that see them.
+ *   prefixes      the shared rows: one sequence per group (table, lens, max_len as for any batch; its rows were written as a
+ *                 sequence of its own and may be another request's).  No groups, or max_len 0: cb_kv8_attention.
+ *   prefix_start  device int32 [groups + 1] or NULL: sequences prefix_start[g] .. prefix_start[g + 1] - 1 stand behind prefix g,
+ *                 sequences before the first and behind the last group behind none; NULL: the sequences are shared evenly,
+ *                 in order
+ *   seqs          the sequences' own rows, behind the prefix: lengths and tables count and name only those
+ *   q, out, q_start, scale: as for cb_kv8_attention.  A row sees all of its prefix and of its sequence's own rows those that
+ *                 cb_kv8_attention would show it (none, where the sequence has no length).
+ * Keys of a prefix were rotated at positions before those of the sequences' own rows (cb_kv8_append's positions).
+ * The result is that of attention over prefix and own rows in one: both parts keep sums and maxima in fp32 and are divided once.
+ * Precision, NaN and bad page ids: as for cb_kv8_attention, the kernels being chosen by the rows of a group, on average, and of a
+ * sequence.  A prefix whose length is out of range has no rows; group or row offsets that decrease or are out of range
+ * compute nothing at all; either is recorded as CB_STATUS_BAD_ROW.  No weights are returned.
+ * Needs weight_cells >= n_q * n_heads * (head_dim + 2), and cb_kv8_attention's limits for the prefixes too.
+ * Every sum runs in a fixed order: the same call gives the same bits.  Async on `stream`; no allocation. */
+cb_status cb_kv8_attention_shared(cb_kv8* cache, const cb_kv8_seqs* prefixes, const int32_t* prefix_start,
+                                  const cb_kv8_seqs* seqs, int32_t layer, const void* q, int64_t q_stride,
+                                  const int32_t* q_start, int32_t n_q, float scale, void* out, int64_t out_stride, void* stream);
 
 /* Eviction by accumulated weight: each KV head of each layer layer .. layer + n_layers - 1 keeps its first n_sink rows,
  * its last n_recent rows and, of the rows between, those of largest weight (ties to the lower row; a weight that is

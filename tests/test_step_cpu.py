@@ -51,3 +51,40 @@ def test_append_refusals(lib):
     big = fake(n_heads=512, n_kv_heads=64, page_size=256, n_pages=1000)
     unsupported(lib.cb_kv8_append(ctypes.addressof(big), seqs(n=1, ld=1 << 23, top=1 << 30), 0, A, 1 << 15, 1 << 55, 1 << 15, 1 << 58, 1 << 59,
                                   1 << 12, None, 1e4, None, 1 << 25, None), "rows of q")
+
+
+def test_shared_attention_refusals(lib):
+    h = fake(weight_cells=5 * 8 * 66)                  # rows of 8 heads of 64: five of them
+
+    def call(pre=None, first=A, sq=None, layer=3, q=A, qs=512, start=A, nq=5, scale=0.125, out=3 * A, os=512, handle=h):
+        return lib.cb_kv8_attention_shared(ctypes.addressof(handle) if handle else None, pre or seqs(n=2), first, sq or seqs(), layer, q, qs,
+                                           start, nq, scale, out, os, None)
+
+    reaches_device(call())
+    reaches_device(call(pre=seqs(n=3), first=None))
+    reaches_device(call(pre=seqs(n=0), nq=9, first=None))          # no prefix: no scratch
+    reaches_device(call(pre=seqs(n=2, top=0), nq=9))
+    refused(call(handle=None), "null cache")
+    refused(call(layer=4), "layers")
+    refused(call(pre=seqs(n=-1)), "n_seqs")
+    refused(call(pre=seqs(ld=3)), "max_len")
+    refused(call(pre=seqs(table=None)), "block table")
+    refused(call(sq=seqs(ld=3)), "max_len")
+    refused(call(first=None), "shared evenly by 2 prefixes")
+    refused(call(start=None), "shared evenly by 3 sequences")
+    refused(call(nq=6), "cells")
+    refused(call(scale=float("nan")), "scale")
+    refused(call(q=None), "null q or out")
+    refused(call(q=A + 2), "16 bytes")
+    refused(call(qs=256), "row stride")
+    refused(call(out=A + 4 * 512 * 2), "overlap")
+    assert call(nq=0, q=None, out=None) == cb.CB_OK
+    assert call(sq=seqs(n=0), nq=0, first=None) == cb.CB_OK
+    big = fake(n_kv_heads=1024, n_heads=8192, weight_cells=1 << 36)
+
+    def large(n, top, own):
+        return lib.cb_kv8_attention_shared(ctypes.addressof(big), seqs(n=1, ld=1 << 26, top=top), None, seqs(n=1, ld=1 << 26, top=own), 0, A,
+                                           8192 * 64, None, n, 0.125, 1 << 55, 8192 * 64, None)
+    reaches_device(large(1, 4096, 4096))
+    unsupported(large(1 << 12, 1 << 16, 1), "too many")
+    unsupported(large(1 << 12, 1, 1 << 16), "too many")
