@@ -32,8 +32,9 @@ EXPORTED = ("cb_model_create", "cb_model_destroy", "cb_rerope", "cb_blend", "cb_
             "cb_pages_free", "cb_index_create", "cb_index_destroy", "cb_index_size", "cb_index_match",
             "cb_select_hkvd", "cb_blend_hkvd", "cb_gradual_layout", "cb_kv8_create", "cb_kv8_destroy", "cb_kv8_status",
             "cb_kv8_write", "cb_kv8_read", "cb_kv8_attention", "cb_kv8_evict", "cb_blend_kv8", "cb_kv8_append",
-            "cb_kv8_attention_shared")
+            "cb_kv8_attention_shared", "cb_sample")
 CB_STATIC_MAX_CHUNKS = 256
+CB_SAMPLE_MAX_VOCAB = 393216
 _I32 = 1 << 31
 CB_STATUS_BAD_TOKEN, CB_STATUS_WAIT_TIMEOUT, CB_STATUS_BAD_ROW = 1, 2, 4
 
@@ -174,6 +175,8 @@ def lib() -> ctypes.CDLL:
         L.cb_gradual_layout.argtypes = [i32, ctypes.POINTER(ctypes.c_double), i32, vp, vp, vp, i32]
         L.cb_select_hkvd.restype = ctypes.c_int
         L.cb_select_hkvd.argtypes = [vp, i32, i32, vp, vp]
+        L.cb_sample.restype = ctypes.c_int
+        L.cb_sample.argtypes = [vp, i32, i32, i32, i64, vp, vp, vp, vp, vp, vp, vp, vp]
         L.cb_blend_hkvd.restype = ctypes.c_int
         L.cb_blend_hkvd.argtypes = [vp, vp, i32, vp, ctypes.POINTER(CbChunk), i32, vp, i32, vp, vp,
                                     ctypes.POINTER(CbStats), vp]
@@ -243,6 +246,50 @@ def cb_gradual_layout(n_ctx: int, ratios):
 def cb_select_hkvd(dev, n: int, k: int, out_rows, stream=None) -> None:
     """The k rows of largest dev[0..n) (ties to the lower row), ascending, into out_rows (device tensors)."""
     _check(lib().cb_select_hkvd(_ptr(dev), n, k, _ptr(out_rows), _stream(stream)))
+
+
+def cb_sample(logits, uniform, temperature=None, top_k=None, top_p=None, min_p=None, out_tokens=None, out_probs=None, stream=None):
+    """The next token of each row of logits (device float32 or bfloat16 [n_rows][vocab], or [vocab] for one row; a row's
+    elements contiguous) from uniform (device float32 [n_rows]); temperature, top_p and min_p (float32) and top_k (int32) are
+    [n_rows] or None.  Returns out_tokens (int32 [n_rows]); out_probs (float32 [n_rows]) receives the tokens' probabilities.
+    Asynchronous on `stream` (default: the current one of the logits' device), without synchronisation or scratch.  A tensor
+    of another shape, type or device raises ValueError before anything is enqueued."""
+    import torch
+    if logits.dim() == 1:
+        logits = logits[None]
+    dtype, dev = logits.dtype, logits.get_device()
+    if logits.dim() != 2 or dev < 0 or (dtype is not torch.float32 and dtype is not torch.bfloat16):
+        raise ValueError("logits must be a float32 or bfloat16 device tensor [n_rows][vocab]")
+    n, vocab = logits.shape
+    stride = logits.stride()
+    if vocab > 1 and stride[1] != 1:
+        raise ValueError("the logits of a row must be contiguous")
+
+    def of(t, name, want):
+        if t is None:
+            return None
+        if t.dtype is not want or t.get_device() != dev or t.shape != (n,) or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous {want} tensor [{n}] on {logits.device}")
+        return t.data_ptr()
+    f32, i32 = torch.float32, torch.int32
+    if uniform is None:
+        raise ValueError("uniform is missing")
+    settings = of(temperature, "temperature", f32), of(top_k, "top_k", i32), of(top_p, "top_p", f32), of(min_p, "min_p", f32)
+    drawn, probs = of(uniform, "uniform", f32), of(out_probs, "out_probs", f32)
+    here = torch.cuda.current_device()
+    with contextlib.nullcontext() if here == dev else torch.cuda.device(dev):
+        raw = torch._C._cuda_getCurrentRawStream(dev)
+        at = raw if stream is None else stream if isinstance(stream, int) else stream.cuda_stream
+        if out_tokens is None:
+            # made on the call's stream
+            other = None if at == raw else torch.cuda.ExternalStream(at, device=dev) if at else torch.cuda.default_stream(dev)
+            with torch.cuda.stream(other):
+                out_tokens = uniform.new_empty(n, dtype=i32)
+        code = lib().cb_sample(logits.data_ptr(), CB_BF16 if dtype is torch.bfloat16 else CB_F32, n, vocab, stride[0] if n > 1 else vocab,
+                               *settings, drawn, of(out_tokens, "out_tokens", i32), probs, at)
+    if code:
+        _check(code)
+    return out_tokens
 
 
 def _chunks(chunks):

@@ -550,6 +550,30 @@ cb_status cb_rerope_static(void* kv, int64_t n_rows, int32_t n_layers, int32_t n
  * concurrent calls are independent. */
 cb_status cb_select_hkvd(const float* dev, int32_t n, int32_t k, int32_t* out_rows, void* stream);
 
+/* The next token of each row of logits (a blend's out_logits, or a decoding step's), from a uniform random number that the
+ * caller gives.  With weights w_i = exp((x_i - max) / temperature) and the tokens in descending order of x (ties to the lower
+ * token):
+ *   top_k   keeps the first top_k tokens;
+ *   top_p   of those, the ones before which the weights sum to less than top_p times the sum of all of those (the first always);
+ *   min_p   of those, the ones of w_i >= min_p times the largest weight.
+ * The token is the lowest i for which the kept weights of tokens 0 .. i sum to more than uniform times the sum of all kept ones.
+ *   logits       device [n_rows][vocab] of dtype (cb_dtype), row_stride elements between rows; aligned to its elements
+ *   temperature, top_k, top_p, min_p   device float32 (top_k: int32) [n_rows], or NULL: 1, off, off, off.  A row's are off with
+ *                top_k <= 0 or >= vocab, top_p >= 1 or NaN, min_p <= 0 or NaN; min_p above 1 counts as 1.  A temperature that is
+ *                NaN or below the smallest normal number (0 among them) takes the most likely token, the lowest of equal ones.
+ *   uniform      device float32 [n_rows] in [0, 1); below, or NaN: as 0; from 1 on: the last kept token
+ *   out_tokens   device int32 [n_rows]; -1 where no logit is above -infinity
+ *   out_probs    device float32 [n_rows] or NULL: the token's weight over the sum of the kept ones (0 where there is no token)
+ * A NaN counts as -infinity; infinities, where there are any, share all the weight.  Weights are held to about 2^-32 of
+ * themselves, in integers of at least 2^-45 of the largest (below which they count as 0), and summed exactly, so that the token
+ * is the formula's but for borders nearer than that; no sum depends on an order.
+ * vocab at most CB_SAMPLE_MAX_VOCAB (else CB_ERR_UNSUPPORTED), n_rows at most 2^24.  Async on `stream`, on the current device;
+ * no allocation; concurrent calls are independent. */
+#define CB_SAMPLE_MAX_VOCAB 393216
+cb_status cb_sample(const void* logits, int32_t dtype, int32_t n_rows, int32_t vocab, int64_t row_stride,
+                    const float* temperature, const int32_t* top_k, const float* top_p, const float* min_p,
+                    const float* uniform, int32_t* out_tokens, float* out_probs, void* stream);
+
 /* Loading controller (section "位置恢复、KV 存储与加载流水线", Figure 11).  Host arithmetic only.
  * cb_load_time: T_load = per_token_kv_bytes * n_tokens / throughput (seconds); -1 for a non-positive
  *   throughput or negative sizes.

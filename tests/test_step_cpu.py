@@ -88,3 +88,23 @@ def test_shared_attention_refusals(lib):
     reaches_device(large(1, 4096, 4096))
     unsupported(large(1 << 12, 1 << 16, 1), "too many")
     unsupported(large(1 << 12, 1, 1 << 16), "too many")
+
+
+def test_sample_refusals(lib):
+    def call(x=A, dtype=cb.CB_F32, n=3, v=100, ld=100, t=A, k=A, p=A, m=A, u=A, out=A, probs=A):
+        return lib.cb_sample(x, dtype, n, v, ld, t, k, p, m, u, out, probs, None)
+
+    assert call(n=0, x=None, u=None, out=None) == cb.CB_OK
+    refused(call(dtype=2), "dtype")
+    refused(call(n=-1), "n_rows")
+    refused(call(n=(1 << 24) + 1), "n_rows")
+    refused(call(v=0), "vocab")
+    refused(call(v=-5), "vocab")
+    unsupported(call(v=cb.CB_SAMPLE_MAX_VOCAB + 1, ld=1 << 20), "vocabulary")
+    refused(call(ld=99), "stride")
+    refused(call(ld=1 << 41), "stride")
+    for name in ("x", "u", "out"):
+        refused(call(**{name: None}), "null")
+    for name in ("t", "k", "p", "m", "u", "out", "probs", "x"):
+        refused(call(**{name: A + 2}), "aligned")
+    refused(call(x=A + 1, dtype=cb.CB_BF16), "aligned")
