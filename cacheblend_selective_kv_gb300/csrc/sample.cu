@@ -11,11 +11,17 @@
 // 32-bit integers, and 2^r - 1 for the rest (|r| <= 2^-9) by three terms of the series, all in fp32 and one wide integer product.
 // A weight below 2^-45 of the largest is 0.
 //
-// A row is a cluster's: its CTAs hold the row in shared memory, as fp32, and every pass over it reads it there.  What passes
-// find out is left in shared memory for all CTAs of the cluster, and each works out the same next step from it.
-// Threshold of top-k or top-p: a histogram of the values (of counts, or of weights as two 32-bit words and a carry) over 1024
-// equal steps from the largest value down, the step in which the sum crosses, and the items of that step one by one; a step with
-// too many of them is divided again, and equal values are counted off in the tokens' order.
+// A row is a cluster's, each of whose CTAs has a part of it.  Only the first pass over a row meets HBM: the rows under way fit in
+// L2, so that passes read them there again, and CTAs need little shared memory and are many (held in shared memory, 64 rows of
+// 128K came in two waves of clusters: 32 us without a filter, 20 this way).  What a pass finds out is left in shared memory for all
+// CTAs of the cluster, and each works out the same next step from it.
+//   few candidates   With c CTAs, at least k values reach the smallest of their ceil(k / c)-th largest thread maxima, and hardly
+//                    more than twice as many do.  They go to the first CTA, which compares each with each and draws.
+//   thresholds       else: the items' counts over equal steps from the largest value down, the step in which the sum crosses, and
+//                    the items of that step one by one; a step with too many of them is divided again, and equal values are
+//                    counted off in the tokens' order.  Top-p first sums all weights and counts items by steps of their weight, which
+//                    leaves a window of few steps where its sum can cross; there weights are summed by step as three words of 16 bits.
+//   the token        the kept weights' sums by warp, then the warp's part by the CTA's warps, then a warp's items in their order.
 #include <cstdarg>
 #include <cstdio>
 
@@ -25,12 +31,12 @@ using namespace cb;
 
 namespace {
 
-constexpr int THREADS = 1024, WARPS = THREADS / 32;
+constexpr int THREADS = 512, WARPS = THREADS / 32;
 constexpr int BINS = THREADS;            // a thread per bin where they are summed
-constexpr int CAP = 256;                 // items of a bin that are looked at one by one
-constexpr int GRAIN = 4 * THREADS;       // a CTA's part of a row is a multiple of it
+constexpr int CAP = 256;                 // items that are compared each with each
+constexpr int MOST_K = 128;              // top-k up to which there are few candidates
 constexpr int MOST_CTAS = 8;
-constexpr int MOST_PART = 49152;         // floats of a row in a CTA
+static_assert(CB_SAMPLE_MAX_VOCAB <= 60000 * MOST_CTAS, "the largest vocabulary");
 constexpr float MAGIC = 12582912.f;      // 1.5 * 2^23: adding it rounds to a whole number
 constexpr int MAGIC_BITS = 0x4B400000;
 
@@ -56,7 +62,7 @@ __device__ constexpr PowerTable kPowers = make_powers();
 struct SampleArgs {
     const void* logits;
     int64_t stride;                      // elements between rows
-    int vocab, part, ctas;               // part: floats of a row per CTA; CTAs per row
+    int vocab, part, ctas;               // part: elements of a row per CTA; CTAs per row
     const float* temperature;
     const int* top_k;
     const float* top_p;
@@ -74,15 +80,18 @@ struct Shared {
     unsigned power[256];
     // left for the cluster
     unsigned long long best;             // key of the CTA's largest value and its first token
-    unsigned low;                        // key of its smallest finite value
-    unsigned hist[2][2][BINS];           // counts, or weights' low and high words; two buffers
-    unsigned found[2], low_of[2], high_of[2];      // items of the bin: how many, keys of the smallest and the largest value
+    unsigned low;                        // key of the smallest of its threads' maxima
+    unsigned bound;                      // key of its share of the top-k's lower bound
+    unsigned hist[2][4][BINS];           // counts, and weights in words of 16 bits; two buffers
+    unsigned long long over[2], rest[2]; // weights above the first and in the last step
+    unsigned found[2], low_of[2], high_of[2];      // items of the step: how many, keys of the smallest and the largest value
+    unsigned listed[2];
     Item list[2][CAP];
     int tie;                             // the token at which equal values are cut off
     unsigned long long warp_sum[WARPS];
     // of the CTA
     unsigned long long scan[WARPS];
-    int bin;
+    int bin, items, first, last;
     unsigned long long above;
     Item joined[CAP];
     unsigned long long weight[CAP];
@@ -110,6 +119,33 @@ __device__ __forceinline__ void sync_cluster() {
     ptx::cluster_sync();
 }
 
+// a value of every CTA: lane r has rank r's (lanes behind the last: `none`)
+__device__ __forceinline__ unsigned of_all(const unsigned* p, int ctas, unsigned none) {
+    const int lane = threadIdx.x & 31;
+    return lane < ctas ? ld_cluster(of_rank(p, lane)) : none;
+}
+__device__ __forceinline__ unsigned long long of_all(const unsigned long long* p, int ctas) {
+    const int lane = threadIdx.x & 31;
+    return lane < ctas ? ld_cluster64(of_rank(p, lane)) : 0ull;
+}
+// the sum over all CTAs
+template <typename V> __device__ __forceinline__ unsigned long long sum_of_all(const V* p, int ctas) {
+    unsigned long long v[MOST_CTAS], sum = 0;
+#pragma unroll
+    for (int r = 0; r < MOST_CTAS; ++r) {                        // all under way together
+        if constexpr (sizeof(V) == 8) v[r] = r < ctas ? ld_cluster64(of_rank(p, r)) : 0ull;
+        else v[r] = r < ctas ? ld_cluster(of_rank(p, r)) : 0u;
+    }
+#pragma unroll
+    for (int r = 0; r < MOST_CTAS; ++r) sum += v[r];
+    return sum;
+}
+// adds to a 64-bit word in shared memory by its halves
+__device__ __forceinline__ void add64(unsigned long long* to, unsigned long long v) {
+    unsigned* w = reinterpret_cast<unsigned*>(to);
+    const unsigned lo = (unsigned)v, was = atomicAdd(w, lo), hi = (unsigned)(v >> 32) + (was + lo < was);
+    if (hi) atomicAdd(w + 1, hi);
+}
 // unsigned integers that order like the floats (no NaN, no -0)
 __device__ __forceinline__ unsigned key_of(float x) {
     const unsigned b = __float_as_uint(x);
@@ -142,34 +178,34 @@ __device__ __forceinline__ unsigned long long block_scan(unsigned long long v, u
     __syncthreads();
     if (lane == 31) sm[warp] = v;
     __syncthreads();
-    const unsigned long long sums = warp_scan64(sm[lane]);
+    const unsigned long long sums = warp_scan64(lane < WARPS ? sm[lane] : 0ull);
     total = shfl64(sums, 31);
     const unsigned long long before = shfl64(sums, warp > 0 ? warp - 1 : 0);
     return warp > 0 ? v + before : v;
 }
 
-// Weights of a row: 2^(x t - m t) in units of 2^-44 of the power of two at or below the largest.
+// Weights of a row: 2^(x t) in units of 2^-44 of the power of two at or below the largest, t = log2(e) / T.
 struct Weigh {
-    float th, tl, shift;                 // t = log2(e) / T as a sum; x is taken relative to `shift`
-    int top;                             // floor of the largest x t
+    float t, rest;                       // 256 t as a sum
+    float lowest;                        // a value whose weight is 0 and stands for all lower ones (and for NaN)
+    int base;                            // `bits` >> 8 from which a weight is a product shifted by nothing
     const unsigned* power;
-    __device__ __forceinline__ int split(float x, float& r) const {             // x t = k / 256 + r
-        x -= shift;
-        const float hi = fmaxf(x * th, -16000.f);
-        const float lo = fmaf(x, tl, fmaf(x, th, -hi));
-        const float km = fmaf(hi, 256.f, MAGIC);
-        r = fmaf(km - MAGIC, -1.f / 256.f, hi) + lo;
-        return __float_as_int(km) - MAGIC_BITS;
+    // 256 x t rounded to a whole number k, as the bits of MAGIC + k
+    __device__ __forceinline__ int bits(float x) const { return __float_as_int(fmaf(fmaxf(x, lowest), t, MAGIC)); }
+    __device__ __forceinline__ unsigned long long of_bits(int bits, unsigned mantissa) const {
+        const unsigned long long product = (unsigned long long)power[bits & 255] * mantissa;
+        return product >> (base - (bits >> 8));        // 18 .. 63
     }
-    __device__ __forceinline__ unsigned long long operator()(float x) const {
-        float r;
-        const int k = split(x, r);
-        const float q = fmaf(r, fmaf(r, 5.5504109e-2f, 2.4022651e-1f), 6.9314718e-1f);
-        const int v = __float_as_int(fmaf(r * 2147483648.f, q, MAGIC)) - MAGIC_BITS;     // (2^r - 1) 2^31
-        const unsigned long long product = (unsigned long long)power[k & 255] * (0x80000000u + (unsigned)v);
-        const int down = 18 + top - (k >> 8);
-        return down < 64 ? product >> down : 0ull;
+    __device__ __forceinline__ unsigned long long operator()(float x, int b) const {         // b: its bits
+        x = fmaxf(x, lowest);
+        const float r = fmaf(x, rest, fmaf(x, t, -(__int_as_float(b) - MAGIC)));             // in 256ths, |r| <= 1 / 2
+        // (2^(r / 256) - 1) 2^31 by the series: (ln 2 / 256)^n / n!
+        const float v = fmaf(r, fmaf(r, fmaf(r, 7.1045254f, 7871.7417f), 5814540.f), MAGIC);
+        return of_bits(b, (unsigned)(__float_as_int(v) - MAGIC_BITS) + 0x80000000u);
     }
+    __device__ __forceinline__ unsigned long long operator()(float x) const { return (*this)(x, bits(x)); }
+    // of the whole number itself, and 0 where it lies below `lowest`
+    __device__ __forceinline__ unsigned long long of_whole(int bits) const { return base - (bits >> 8) < 64 ? of_bits(bits, 0x80000000u) : 0ull; }
 };
 
 // ceil(f s) and floor(f s) for f in [0, 1) (multiples of 2^-64, as every fp32 from 2^-40 on is)
@@ -188,112 +224,276 @@ struct Cut {
     __device__ __forceinline__ bool keeps(float y, int j) const { return y > x || (y == x && j <= i); }
 };
 
-struct Row {
-    const float* x;                      // this CTA's part
-    int part, first, ctas, rank;         // first: its first token
-    template <typename F> __device__ __forceinline__ void each(F f) const {      // in the tokens' order within a warp's steps
+__device__ __forceinline__ float4 four_of(const float* p) { return *reinterpret_cast<const float4*>(p); }
+__device__ __forceinline__ float4 four_of(const bf16* p) {
+    const uint2 u = *reinterpret_cast<const uint2*>(p);
+    return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
+                       __uint_as_float(u.y & 0xffff0000u));
+}
+
+// A row and this CTA's part of it.  Places are tokens counted from the last 16 (8) bytes boundary at or before the row's first:
+// place j + off is token j, and vectors of four places are aligned.
+template <typename T> struct Row {
+    const T* x;                          // token 0
+    int vocab, off;
+    int part, first, ctas, rank;         // places of this CTA: first .. first + part - 1
+    // Rows whose values stand for others.  Infinities share all the weight: they become 0, all others -inf.  At low temperatures
+    // values are taken less the largest (what has weight lies so near to it that the difference is exact), and at the very
+    // lowest times 2^32, so that 1 / T stays within fp32.
+    bool special, infinite;
+    float less, times;
+    __device__ __forceinline__ float see(float v) const {
+        return !special ? v : !infinite ? (v - less) * times : v == INFINITY ? 0.f : -INFINITY;
+    }
+    __device__ __forceinline__ float4 raw(int place) const {     // four from here on; -inf where there is no token
+        const int j = place - off;
+        if (j >= 0 && j + 4 <= vocab) return four_of(x + j);
+        const auto one = [&](int k) { return k >= 0 && k < vocab ? to_f(x[k]) : -INFINITY; };
+        return make_float4(one(j), one(j + 1), one(j + 2), one(j + 3));
+    }
+    // f(four values, the first one's token) for the places of [from, from + n) that this thread of a warp has, n a multiple of
+    // 128: in the tokens' order within a step of the warp, all lanes together.  Two vectors are under way beside the one that
+    // is worked on.
+    template <typename F> __device__ __forceinline__ void each_of(int from, int n, F f) const {
+        const int end = from + n;
+        int p = from + (threadIdx.x & 31) * 4;
+        const auto load = [&](int q) { return q < end ? raw(q) : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY); };
+        float4 v0 = load(p), v1 = load(p + 128);
+#pragma unroll 1
+        for (; p < end; p += 128) {
+            float v[4] = {v0.x, v0.y, v0.z, v0.w};
+            v0 = v1;
+            v1 = load(p + 256);
+            if (special) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) v[k] = see(v[k]);
+            }
+            f(v, p - off);
+        }
+    }
+    template <typename F> __device__ __forceinline__ void each(F f) const {
         const int per = part / WARPS;
-        const float* from = x + (threadIdx.x >> 5) * per;
-        const int j0 = first + (threadIdx.x >> 5) * per;
-        for (int at = (threadIdx.x & 31) * 4; at < per; at += 128) {
-            const float4 v = *reinterpret_cast<const float4*>(from + at);
-            f(v.x, j0 + at);
-            f(v.y, j0 + at + 1);
-            f(v.z, j0 + at + 2);
-            f(v.w, j0 + at + 3);
+        each_of(first + (threadIdx.x >> 5) * per, per, f);
+    }
+};
+// whether a lane of the warp has a value from `low` on
+__device__ __forceinline__ bool any_from(const float* x, float low) {
+    return __any_sync(0xffffffffu, fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) >= low);
+}
+
+// steps of equal size from `high` down over `range`
+struct Steps {
+    float high, up, step;
+    __device__ __forceinline__ Steps(float high_, float range) : high(high_) {
+        // (differences of small numbers are brought up first: 1 / range could pass fp32, and all values be in one step for ever)
+        up = range < 0x1p-60f ? 0x1p100f : 1.f;
+        step = range > 0.f ? (BINS - 1) / (range * up) : 0.f;
+    }
+    __device__ __forceinline__ int operator()(float x) const { return (int)fminf(fminf(high - x, 3.4e38f) * up * step, BINS - 1); }
+};
+
+// what ranks below make of the first CTAs' lists: which list and entry thread tid takes, and how many there are in all
+struct Gathered {
+    unsigned n, before, mine;            // before: in the lists of lower ranks
+    int from;
+    __device__ __forceinline__ Gathered(unsigned by_lane, int rank) : n(0), before(0), mine(0), from(0) {
+#pragma unroll
+        for (int r = 0; r < MOST_CTAS; ++r) {
+            const unsigned k = __shfl_sync(0xffffffffu, by_lane, r);
+            if (threadIdx.x >= n && threadIdx.x < n + k) {
+                from = r;
+                mine = threadIdx.x - n;
+            }
+            if (r < rank) before += k;
+            n += k;
         }
     }
 };
+__device__ __forceinline__ Item remote_item(const Item* p, int rank) {
+    const uint32_t at = of_rank(p, rank);
+    return Item{__uint_as_float(ld_cluster(at)), (int)ld_cluster(at + 4)};
+}
 
-// Lowers the cut to the first kept item, in descending order, at which the sum of counts (MASS: of weights) reaches the target:
-// `most` items, or p of the sum.  All CTAs of the cluster come to the same cut.  `phase` alternates the buffers that others
-// read: one is written again only when all have passed the next barrier of the cluster.
-template <bool MASS>
-__device__ __forceinline__ void select(const Row& row, const Weigh& w, Shared& s, float m, float low, int most, float p, Cut& cut, int& phase) {
+// Steps of weights: 2^shift 256ths of log2 each, from the largest value's down; a value and its weight share the bits they are
+// found by.
+struct Scale {
+    int top, shift;                      // the bits of the largest value
+    __device__ __forceinline__ int operator()(int bits) const { return min((top - bits) >> shift, BINS - 1); }
+};
+// Where a search begins: the items whose step is first .. last.  It divides them into equal steps from `high` down over `range`;
+// none of them lies below `low`.  What lies above sums to what the search's first level finds, of `target` to be reached.
+struct Window {
+    Scale scale;
+    int first, last;
+    float high, range, low;
+    unsigned long long target;
+};
+
+// The window of top-p: weights are summed and items counted by step.  A step's items weigh at least what its lower edge does and
+// at most what its upper edge does, so that the sum must cross within the steps where the sum of the largest possible weights
+// has reached the target and that of the smallest has not.
+template <typename T>
+__device__ __forceinline__ Window nucleus(const Row<T>& row, const Weigh& w, Shared& s, float m, float p, const Cut& cut, int& phase) {
+    const int tid = threadIdx.x, lane = tid & 31, b = phase++ & 1;
+    // weights below (1 - p) / n of the largest sum to less than 1 - p of all
+    const float covers = 256.f * fminf(fmaxf(1.f - log2f(fmaxf(1.f - p, 1e-9f) / row.vocab), 1.f), 47.f);
+    Window win{};
+    win.scale = Scale{w.bits(m), 0};
+    while ((int)covers >> win.scale.shift >= BINS - 1) ++win.scale.shift;
+    const Scale scale = win.scale;
+    s.hist[b][0][tid] = 0;
+    if (tid == 0) {
+        s.rest[b] = 0;
+        s.first = s.last = BINS - 1;
+    }
+    __syncthreads();
+    unsigned long long sum = 0;
+    const float from = cut.x > -INFINITY ? cut.x : w.lowest;     // (below the lowest there is no weight)
+    row.each([&](const float* x, int j) {
+        if (!any_from(x, from)) return;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int bits = w.bits(x[k]), at = scale(bits);
+            const unsigned long long y = w(x[k], bits);
+            if (!cut.keeps(x[k], j + k)) continue;
+            sum += y;
+            if (at < BINS - 1) atomicAdd(&s.hist[b][0][at], 1u);
+        }
+    });
+    sum = warp_sum64(sum);
+    if (lane == 0 && sum) add64(&s.rest[b], sum);
+    sync_cluster();
+    win.target = max(ceil_of(p, sum_of_all(&s.rest[b], row.ctas)), 1ull);
+    const unsigned long long n = sum_of_all(&s.hist[b][0][tid], row.ctas);
+    // a value is within half of a 256th of its whole number: a factor of less than 1 + 2^-9
+    unsigned long long most = w.of_whole(scale.top - (tid << scale.shift)), least = w.of_whole(scale.top - ((tid + 1) << scale.shift) + 1);
+    most += (most >> 9) + 1;
+    least -= least >> 8;
+    least = least > 0 ? least - 1 : 0;
+    unsigned long long total;
+    if (block_scan(n * most, s.scan, total) >= win.target) atomicMin(&s.first, tid);
+    if (block_scan(n * least, s.scan, total) >= win.target) atomicMin(&s.last, tid);
+    __syncthreads();
+    win.first = s.first;
+    win.last = s.last;
+    const auto value = [&](int k) { return (float)(scale.top - MAGIC_BITS - k) / w.t; };     // about where x t 256 is k below the largest
+    win.high = value((win.first << scale.shift) - 2);
+    win.low = win.last == BINS - 1 ? -INFINITY : value(((win.last + 1) << scale.shift) + 2) - fabsf(m) * 1e-6f;
+    win.range = win.high - value(((win.last + 1) << scale.shift) + 2);
+    return win;
+}
+
+// Lowers the cut to the first kept item, in descending order, at which the sum of counts (MASS: of weights) reaches the target.
+// All CTAs of the cluster come to the same cut.  `phase` alternates the buffers that others read: one is written again only
+// when all have passed the next barrier of the cluster.
+template <bool MASS, typename T>
+__device__ __forceinline__ void select(const Row<T>& row, const Weigh& w, Shared& s, const Window& win, Cut& cut, int& phase) {
     const int tid = threadIdx.x, lane = tid & 31;
-    float high = m;
-    float range = fminf(m - low, 3.4e38f);
-    const float reach = 47.f / w.th;                   // below it weights are 0
-    const bool cut_off = reach < range;
-    range = cut_off ? reach : range;
-    unsigned long long above = 0, target = MASS ? 0ull : (unsigned long long)most;
-    // The largest and the smallest value of a level never share a step and a step is at most 1 / 1022 of its level's range, so
-    // that 28 levels lead from the largest difference of two fp32 numbers to the smallest.
+    float high = win.high, low = win.low, range = win.range;
+    unsigned long long above = 0;
+    const unsigned long long target = win.target;
+    // The largest and the smallest value of a level never share a step and a step is at most 1 / 510 of its level's range, so
+    // that 31 levels lead from the largest difference of two fp32 numbers to the smallest.
     for (int level = 0; level < 40; ++level) {
         const int b = phase++ & 1;
-        // (differences of small numbers are brought up first: 1 / range could pass fp32, and all values be in one step for ever)
-        const float up = range < 0x1p-60f ? 0x1p100f : 1.f, step = range > 0.f ? (BINS - 1) / (range * up) : 0.f;
-        const auto bin_of = [&](float x) { return (int)fminf(fminf(high - x, 3.4e38f) * up * step, BINS - 1); };
-        const auto inside = [&](float x, int j) { return cut.keeps(x, j) && (level == 0 || (x <= high && x >= low)); };
-        s.hist[b][0][tid] = 0;
-        s.hist[b][1][tid] = 0;
+        const Steps step_of(high, range);
+        // -1: not of this level; -2: above the window
+        const auto place = [&](float x, int j) {
+            if (!cut.keeps(x, j)) return -1;
+            if (level == 0) {
+                if constexpr (MASS) {
+                    const int at = win.scale(w.bits(x));
+                    if (at < win.first) return -2;
+                    if (at > win.last) return -1;
+                }
+            } else if (!(x <= high && x >= low)) {
+                return -1;
+            }
+            return max(step_of(x), 0);
+        };
+        for (int k = 0; k < (MASS ? 4 : 1); ++k) s.hist[b][k][tid] = 0;
         if (tid == 0) {
-            s.found[b] = 0;
+            s.over[b] = s.rest[b] = 0;
+            s.found[b] = s.listed[b] = 0;
             s.low_of[b] = 0xffffffffu;
             s.high_of[b] = 0;
         }
         __syncthreads();
-        row.each([&](float x, int j) {
-            if (!inside(x, j)) return;
-            const int at = bin_of(x);
-            if constexpr (MASS) {
-                const unsigned long long y = w(x);
-                const unsigned lo = (unsigned)y, was = atomicAdd(&s.hist[b][0][at], lo);
-                const unsigned hi = (unsigned)(y >> 32) + (was + lo < was);
-                if (hi) atomicAdd(&s.hist[b][1][at], hi);
-            } else {
-                atomicAdd(&s.hist[b][0][at], 1u);
+        unsigned long long over = 0;
+        row.each([&](const float* x, int j) {
+            if (!any_from(x, low)) return;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int at = place(x[k], j + k);
+                unsigned long long y = 0;
+                if constexpr (MASS) {
+                    y = w(x[k]);
+                    over += at == -2 ? y : 0ull;
+                }
+                if (at < 0) continue;
+                if (MASS || at < BINS - 1) atomicAdd(&s.hist[b][0][at], 1u);
+                if constexpr (MASS) {              // (a part has less than 2^16 items: no word overflows)
+                    atomicAdd(&s.hist[b][1][at], (unsigned)y & 0xffffu);
+                    atomicAdd(&s.hist[b][2][at], (unsigned)(y >> 16) & 0xffffu);
+                    atomicAdd(&s.hist[b][3][at], (unsigned)(y >> 32));
+                }
             }
         });
+        if constexpr (MASS) {
+            over = warp_sum64(over);
+            if (lane == 0 && over) add64(&s.over[b], over);
+        }
         sync_cluster();
-        unsigned long long here = 0;
-        for (int r = 0; r < row.ctas; ++r) {
-            here += ld_cluster(of_rank(&s.hist[b][0][tid], r));
-            if (MASS) here += (unsigned long long)ld_cluster(of_rank(&s.hist[b][1][tid], r)) << 32;
+        // (counts: the last step, which holds whatever lies below, is not counted)
+        const unsigned long long items = !MASS && tid == BINS - 1 ? 1ull << 32 : sum_of_all(&s.hist[b][0][tid], row.ctas);
+        unsigned long long here = items;
+        if constexpr (MASS) {
+            here = sum_of_all(&s.hist[b][1][tid], row.ctas) + (sum_of_all(&s.hist[b][2][tid], row.ctas) << 16) +
+                   (sum_of_all(&s.hist[b][3][tid], row.ctas) << 32);
+            if (level == 0) above = sum_of_all(&s.over[b], row.ctas);
         }
         unsigned long long total;
         const unsigned long long upto = above + block_scan(here, s.scan, total);
-        if (MASS && level == 0) target = max(ceil_of(p, total), 1ull);
-        if (level == 0 && total < target) return;      // fewer items than top-k keeps
         if (upto - here < target && target <= upto) {
             s.bin = tid;
             s.above = upto - here;
+            s.items = items > CAP ? CAP + 1 : (int)items;
         }
         __syncthreads();
         const int bin = s.bin;
+        const bool few = s.items <= CAP;
         above = s.above;
-        if (level == 0 && cut_off && bin == BINS - 1) return;      // what is cut has no weight
-        // the bin's items
+        // the step's items
         float least = INFINITY, largest = -INFINITY;
-        row.each([&](float x, int j) {
-            if (!inside(x, j) || bin_of(x) != bin) return;
-            const unsigned n = atomicAdd(&s.found[b], 1u);
-            if (n < CAP) s.list[b][n] = Item{x, j};
-            least = fminf(least, x);
-            largest = fmaxf(largest, x);
+        unsigned count = 0;
+        row.each([&](const float* x, int j) {
+            if (!any_from(x, low)) return;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if (place(x[k], j + k) != bin) continue;
+                ++count;
+                least = fminf(least, x[k]);
+                largest = fmaxf(largest, x[k]);
+                if (few) s.list[b][min(atomicAdd(&s.listed[b], 1u), CAP - 1u)] = Item{x[k], j + k};
+            }
         });
-        if (largest >= least) {
-            atomicMin(&s.low_of[b], key_of(least));
-            atomicMax(&s.high_of[b], key_of(largest));
+        count = __reduce_add_sync(0xffffffffu, count);
+        const unsigned lo = __reduce_min_sync(0xffffffffu, key_of(least + 0.f)), hi = __reduce_max_sync(0xffffffffu, key_of(largest + 0.f));
+        if (lane == 0 && count) {                      // (-0 counts as 0)
+            atomicAdd(&s.found[b], count);
+            atomicMin(&s.low_of[b], lo);
+            atomicMax(&s.high_of[b], hi);
         }
         sync_cluster();
-        unsigned n = 0, before = 0, mine = 0, lo_key = 0xffffffffu, hi_key = 0;
-        int from = 0;
-        for (int r = 0; r < row.ctas; ++r) {
-            const unsigned k = ld_cluster(of_rank(&s.found[b], r));
-            if ((unsigned)tid >= n && (unsigned)tid < n + k) {
-                from = r;
-                mine = tid - n;
-            }
-            if (r < row.rank) before += k;
-            n += k;
-            lo_key = min(lo_key, ld_cluster(of_rank(&s.low_of[b], r)));
-            hi_key = max(hi_key, ld_cluster(of_rank(&s.high_of[b], r)));
-        }
-        if (n <= CAP) {
+        const unsigned mine_n = of_all(&s.found[b], row.ctas, 0u);               // by lane: of each rank
+        const unsigned lo_key = __reduce_min_sync(0xffffffffu, of_all(&s.low_of[b], row.ctas, 0xffffffffu));
+        const unsigned hi_key = __reduce_max_sync(0xffffffffu, of_all(&s.high_of[b], row.ctas, 0u));
+        const Gathered g(mine_n, row.rank);
+        const unsigned n = g.n, before = g.before;
+        if (!MASS && above + n < target) return;       // fewer items than top-k keeps
+        if (few) {
             if (tid < (int)n) {
-                const uint32_t at = of_rank(&s.list[b][mine], from);
-                const Item it{__uint_as_float(ld_cluster(at)), (int)ld_cluster(at + 4)};
+                const Item it = remote_item(&s.list[b][g.mine], g.from);
                 s.joined[tid] = it;
                 s.weight[tid] = MASS ? w(it.x) : 1ull;
             }
@@ -301,9 +501,11 @@ __device__ __forceinline__ void select(const Row& row, const Weigh& w, Shared& s
             if (tid < (int)n) {
                 const Item it = s.joined[tid];
                 unsigned long long sum = above;
+#pragma unroll 8
                 for (int k = 0; k < (int)n; ++k) {
                     const Item o = s.joined[k];
-                    if (o.x > it.x || (o.x == it.x && o.i < it.i)) sum += s.weight[k];
+                    const unsigned long long z = s.weight[k];
+                    sum += o.x > it.x || (o.x == it.x && o.i < it.i) ? z : 0ull;
                 }
                 if (sum < target && target <= sum + s.weight[tid]) {
                     s.cut_x = it.x;
@@ -327,19 +529,22 @@ __device__ __forceinline__ void select(const Row& row, const Weigh& w, Shared& s
             const unsigned here_n = s.found[b];
             if (keep > before && keep <= before + here_n) {
                 // this CTA has the token: by warp, then step by step
-                int count = 0;
-                row.each([&](float x, int j) { count += x == high && cut.keeps(x, j); });
-                const unsigned long long warps = __reduce_add_sync(0xffffffffu, (unsigned)count);
+                int mine = 0;
+                row.each([&](const float* x, int j) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) mine += x[k] == high && cut.keeps(x[k], j + k);
+                });
+                const unsigned long long warps = __reduce_add_sync(0xffffffffu, (unsigned)mine);
                 unsigned long long all;
                 const unsigned long long end = before + block_scan(lane == 31 ? warps : 0ull, s.scan, all);
                 // (the sum up to lane 31 of this warp; other lanes have what stands before the warp)
                 const unsigned long long begin = shfl64(end, 0);
                 if (keep > begin && keep <= begin + warps) {
                     unsigned left = (unsigned)(keep - begin);
-                    const int per = row.part / WARPS, w0 = (tid >> 5) * per;
-                    for (int at = w0; at < w0 + per; at += 32) {
-                        const int j = row.first + at + lane;
-                        const bool is = row.x[at + lane] == high && cut.keeps(high, j);
+                    const int per = row.part / WARPS, p0 = row.first + (tid >> 5) * per;
+                    for (int p = p0; p < p0 + per; p += 32) {
+                        const int j = p + lane - row.off;
+                        const bool is = j >= 0 && j < row.vocab && row.see(to_f(row.x[j])) == high && cut.keeps(high, j);
                         const unsigned votes = __ballot_sync(0xffffffffu, is);
                         if ((unsigned)__popc(votes) >= left) {
                             if (is && __popc(votes & ((2u << lane) - 1u)) == (int)left) s.tie = j;
@@ -352,8 +557,9 @@ __device__ __forceinline__ void select(const Row& row, const Weigh& w, Shared& s
             sync_cluster();
             int owner = 0;
             unsigned upto_r = 0;
-            for (int r = 0; r < row.ctas; ++r) {
-                const unsigned k = ld_cluster(of_rank(&s.found[b], r));
+#pragma unroll
+            for (int r = 0; r < MOST_CTAS; ++r) {
+                const unsigned k = __shfl_sync(0xffffffffu, mine_n, r);
                 if (keep > upto_r && keep <= upto_r + k) owner = r;
                 upto_r += k;
             }
@@ -364,136 +570,251 @@ __device__ __forceinline__ void select(const Row& row, const Weigh& w, Shared& s
     }
 }
 
-__device__ __forceinline__ float load_one(const float* p) { return *p; }
-__device__ __forceinline__ float load_one(const bf16* p) { return __bfloat162float(*p); }
-__device__ __forceinline__ float4 load_four(const float* p) { return __ldcs(reinterpret_cast<const float4*>(p)); }
-__device__ __forceinline__ float4 load_four(const bf16* p) {
-    const uint2 u = __ldcs(reinterpret_cast<const uint2*>(p));
-    return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
-                       __uint_as_float(u.y & 0xffff0000u));
+// top-k of few, the lower bound of the candidates being known: see above.  True where they were few enough; the first CTA has
+// then written the row's token.
+template <typename T>
+__device__ __forceinline__ bool draw_of_few(const Row<T>& row, const Weigh& w, Shared& s, float m, float bound, float own, int top_k,
+                                            float top_p, float min_p, float u, const SampleArgs& a, int r_out, int& phase) {
+    const int tid = threadIdx.x, b = phase++ & 1;
+    if (tid == 0) s.found[b] = 0;
+    __syncthreads();
+    if (own >= bound) {                                // (a thread whose largest value lies below has none)
+        const int per = row.part / WARPS, end = row.first + (tid >> 5) * per + per;
+        for (int p = end - per + (tid & 31) * 4; p < end; p += 128) {
+            const float4 v = row.raw(p);
+            const auto look = [&](float x, int j) {
+                x = row.see(x);
+                if (!(x >= bound)) return;
+                const unsigned n = atomicAdd(&s.found[b], 1u);
+                if (n < CAP) s.list[b][n] = Item{x, j};
+            };
+            look(v.x, p - row.off);
+            look(v.y, p - row.off + 1);
+            look(v.z, p - row.off + 2);
+            look(v.w, p - row.off + 3);
+        }
+    }
+    sync_cluster();
+    const Gathered g(of_all(&s.found[b], row.ctas, 0u), row.rank);
+    const int n = (int)g.n;
+    if (n > CAP || n < top_k) return false;
+    if (row.rank == 0) {
+        Item it{0.f, 0};
+        unsigned long long y = 0;
+        if (tid < n) {
+            it = remote_item(&s.list[b][g.mine], g.from);
+            y = w(it.x);
+            s.joined[tid] = it;
+            s.weight[tid] = y;
+        }
+        __syncthreads();
+        int ahead = 0;
+        unsigned long long before = 0;
+        if (tid < n) {
+#pragma unroll 8
+            for (int k = 0; k < n; ++k) {
+                const Item o = s.joined[k];
+                const unsigned long long z = s.weight[k];
+                const bool first = o.x > it.x || (o.x == it.x && o.i < it.i);
+                ahead += first;
+                before += first ? z : 0ull;
+            }
+        }
+        bool keep = tid < n && ahead < top_k;
+        unsigned long long sum;
+        if (top_p < 1.f) {
+            block_scan(keep ? y : 0ull, s.scan, sum);
+            keep = keep && before < max(ceil_of(top_p, sum), 1ull);
+        }
+        keep = keep && y >= (min_p >= 1.f ? w(m) : ceil_of(min_p, w(m)));
+        __syncthreads();                               // every weight has been read
+        if (tid < n) s.weight[tid] = keep ? y : 0ull;
+        block_scan(keep ? y : 0ull, s.scan, sum);
+        const unsigned long long target = u >= 1.f ? sum - 1 : floor_of(u, sum);
+        if (keep) {
+            before = 0;
+#pragma unroll 8
+            for (int k = 0; k < n; ++k) {
+                const unsigned long long z = s.weight[k];
+                before += s.joined[k].i < it.i ? z : 0ull;
+            }
+            if (before <= target && target < before + y) {
+                a.out_tokens[r_out] = it.i;
+                if (a.out_probs) a.out_probs[r_out] = (float)((double)y / (double)sum);
+            }
+        }
+    }
+    return true;
+}
+
+// key of the j-th largest of the threads' maxima, or less; 0 where there are fewer
+__device__ __forceinline__ unsigned jth_largest(Shared& s, float own, int j) {
+    const int tid = threadIdx.x;
+    s.hist[1][0][tid] = 0;                             // (not yet anyone's)
+    if (tid == 0) s.bound = 0xffffffffu;
+    const float most = of_key((unsigned)(s.best >> 32));
+    const float least = s.low == 0xffffffffu ? most : of_key(s.low);
+    __syncthreads();
+    const Steps step_of(most, fminf(most - least, 3.4e38f));
+    const bool some = own > -INFINITY;
+    const int bin = some && most < INFINITY ? step_of(own) : 0;
+    if (some) atomicAdd(&s.hist[1][0][bin], 1u);
+    __syncthreads();
+    unsigned long long total;
+    const unsigned long long here = s.hist[1][0][tid], upto = block_scan(here, s.scan, total);
+    if (upto - here < (unsigned)j && (unsigned)j <= upto) s.bin = tid;
+    __syncthreads();
+    if (total < (unsigned)j) return 0;
+    const unsigned l = __reduce_min_sync(0xffffffffu, some && bin <= s.bin ? key_of(own + 0.f) : 0xffffffffu);
+    if ((tid & 31) == 0) atomicMin(&s.bound, l);
+    __syncthreads();
+    return s.bound;
 }
 
 template <typename T>
-__global__ void __launch_bounds__(THREADS, 1) sample_kernel(const SampleArgs a) {
-    extern __shared__ __align__(16) float xs[];        // [part]
+__global__ void __launch_bounds__(THREADS, 2) sample_kernel(const SampleArgs a) {
     __shared__ Shared s;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int ctas = a.ctas, rank = (int)ptx::cluster_rank();
     const int r = blockIdx.x / ctas;
     if (tid < 256) s.power[tid] = kPowers.of[tid];
-    const float temperature = a.temperature ? a.temperature[r] : 1.f;
-    const int top_k = a.top_k ? a.top_k[r] : 0;
-    const float top_p = a.top_p ? a.top_p[r] : 1.f, min_p = a.min_p ? a.min_p[r] : 0.f, u = a.uniform[r];
-
-    // The row into shared memory, a NaN as -inf and -0 as 0; its largest value and that one's first token
-    const Row row{xs, a.part, rank * a.part, ctas, rank};
-    float best = -INFINITY, low = INFINITY;
-    int best_i = 0x7fffffff;
-    {
-        const T* src = (const T*)a.logits + (int64_t)r * a.stride;
-        const int per = a.part / WARPS, n = a.vocab;
-        const bool wide = ((uintptr_t)src & (4 * sizeof(T) - 1)) == 0;
-#pragma unroll 4
-        for (int at = lane * 4; at < per; at += 128) {
-            const int to = warp * per + at, j = row.first + to;
-            float v[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-            if (wide && j + 4 <= n) {
-                const float4 f = load_four(src + j);
-                v[0] = f.x;
-                v[1] = f.y;
-                v[2] = f.z;
-                v[3] = f.w;
-            } else {
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    if (j + k < n) v[k] = load_one(src + j + k);
-            }
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                v[k] = v[k] == v[k] ? v[k] + 0.f : -INFINITY;
-                if (v[k] > best) {
-                    best = v[k];
-                    best_i = j + k;
-                }
-                if (v[k] > -INFINITY) low = fminf(low, v[k]);
-            }
-            *reinterpret_cast<float4*>(xs + to) = make_float4(v[0], v[1], v[2], v[3]);
-        }
-    }
     if (tid == 0) {
         s.best = 0;
         s.low = 0xffffffffu;
     }
+    const float temperature = a.temperature ? a.temperature[r] : 1.f;
+    const int top_k = a.top_k ? a.top_k[r] : 0;
+    const float top_p = a.top_p ? a.top_p[r] : 1.f, min_p = a.min_p ? a.min_p[r] : 0.f, u = a.uniform[r];
+    const T* src = (const T*)a.logits + (int64_t)r * a.stride;
+    Row<T> row{src, a.vocab, (int)((uintptr_t)src / sizeof(T) & 3), a.part, rank * a.part, ctas, rank, false, false, 0.f, 1.f};
+
+    // the largest value and its first token (a NaN is never larger)
+    float own = -INFINITY;                             // of this thread's values
+    int own_i = 0x7fffffff;
+    {
+        constexpr int AHEAD = 4;                       // vectors under way
+        const int per = a.part / WARPS, end = row.first + warp * per + per;
+        int own_p = -1;                                // the first place of the vector that has it
+#pragma unroll 1
+        for (int p = end - per + lane * 4; p < end; p += AHEAD * 128) {
+            float4 v[AHEAD];
+#pragma unroll
+            for (int k = 0; k < AHEAD; ++k) v[k] = p + k * 128 < end ? row.raw(p + k * 128) : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+#pragma unroll
+            for (int k = 0; k < AHEAD; ++k) {
+                const float x = fmaxf(fmaxf(v[k].x, v[k].y), fmaxf(v[k].z, v[k].w));
+                if (x > own) {
+                    own = x;
+                    own_p = p + k * 128;
+                }
+            }
+        }
+        if (own_p >= 0) {
+            const float4 v = row.raw(own_p);
+            own_i = own_p - row.off + (v.x == own ? 0 : v.y == own ? 1 : v.z == own ? 2 : 3);
+        }
+    }
     __syncthreads();
     {
-        unsigned long long k = ((unsigned long long)key_of(best) << 32) | (unsigned)~best_i;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) k = max(k, __shfl_xor_sync(0xffffffffu, k, o));
-        const unsigned l = __reduce_min_sync(0xffffffffu, key_of(low));
+        const unsigned k = key_of(own + 0.f), top = __reduce_max_sync(0xffffffffu, k);       // (-0 counts as 0)
+        const unsigned i = __reduce_min_sync(0xffffffffu, k == top ? (unsigned)own_i : 0xffffffffu);
+        const unsigned l = __reduce_min_sync(0xffffffffu, own > -INFINITY ? k : 0xffffffffu);
         if (lane == 0) {
-            atomicMax(&s.best, k);
+            atomicMax(&s.best, ((unsigned long long)top << 32) | ~i);
             atomicMin(&s.low, l);
         }
     }
-    sync_cluster();
-    unsigned long long k_best = 0;
-    unsigned k_low = 0xffffffffu;
-    for (int c = 0; c < ctas; ++c) {
-        k_best = max(k_best, ld_cluster64(of_rank(&s.best, c)));
-        k_low = min(k_low, ld_cluster(of_rank(&s.low, c)));
+    const bool greedy = !(temperature >= 1.1754944e-38f), cuts = top_k > 0 && top_k < a.vocab;
+    const bool few = cuts && top_k <= MOST_K && !greedy;
+    if (few) {
+        __syncthreads();
+        const unsigned k = jth_largest(s, own, (top_k + ctas - 1) / ctas);
+        if (tid == 0) s.bound = k;
     }
-    float m = of_key((unsigned)(k_best >> 32));
-    low = of_key(k_low);
-    const bool greedy = !(temperature >= 1.1754944e-38f);
+    sync_cluster();
+    const unsigned long long bests = of_all(&s.best, ctas);
+    const unsigned top = __reduce_max_sync(0xffffffffu, (unsigned)(bests >> 32));
+    const unsigned best_i = ~__reduce_max_sync(0xffffffffu, (unsigned)(bests >> 32) == top ? (unsigned)bests : 0u);
+    float m = of_key(top), low = of_key(__reduce_min_sync(0xffffffffu, of_all(&s.low, ctas, 0xffffffffu)));
     if (m == -INFINITY || greedy) {                    // no token, or the most likely one
         if (rank == 0 && tid == 0) {
-            a.out_tokens[r] = m == -INFINITY ? -1 : (int)~(unsigned)k_best;
+            a.out_tokens[r] = m == -INFINITY ? -1 : (int)best_i;
             if (a.out_probs) a.out_probs[r] = m == -INFINITY ? 0.f : 1.f;
         }
-        sync_cluster();                           // no CTA exits while another reads its shared memory
+        sync_cluster();                                // no CTA exits while another reads its shared memory
         return;
     }
-    if (m == INFINITY) {                               // infinities share all the weight (a thread reads what it has written)
-        const int per = a.part / WARPS;
-        for (int at = lane * 4; at < per; at += 128)
-            for (int k = 0; k < 4; ++k) {
-                float& x = xs[warp * per + at + k];
-                x = x == INFINITY ? 0.f : -INFINITY;
-            }
-        m = low = 0.f;
-        __syncthreads();
-    }
+    unsigned bound = few ? __reduce_min_sync(0xffffffffu, of_all(&s.bound, ctas, 0xffffffffu)) : 0u;     // 0: a CTA has fewer values
     Weigh w;
     {
-        const float T1 = fminf(temperature, 3.4e38f);
-        w.th = 1.44269502f / T1;                       // log2(e) = 1.44269502 + 1.92596299e-8
-        w.tl = (fmaf(-w.th, T1, 1.44269502f) + 1.92596299e-8f) / T1;
-        w.shift = fabsf(m) * w.th >= 8192.f ? m : 0.f; // (what has weight lies so near to m then that x - m is exact)
+        float T1 = fminf(temperature, 3.4e38f);
+        if (m == INFINITY) {
+            row.special = row.infinite = true;
+            m = low = 0.f;
+            bound = 0;
+        } else if (!(fabsf(m) * (1.442695f / T1) < 8192.f) || T1 < 0x1p-100f) {
+            row.special = true;
+            row.less = m;
+            row.times = T1 < 0x1p-100f ? 0x1p32f : 1.f;
+            T1 *= row.times;
+            own = row.see(own);
+            low = row.see(low);
+            m = 0.f;
+        }
+        const float t = 1.44269502f / T1;              // log2(e) = 1.44269502 + 1.92596299e-8
+        w.t = 256.f * t;
+        w.rest = 256.f * ((fmaf(-t, T1, 1.44269502f) + 1.92596299e-8f) / T1);
         w.power = s.power;
-        float rest;
-        w.top = w.split(m, rest) >> 8;
+        w.lowest = -INFINITY;
+        const int top8 = (w.bits(m) - MAGIC_BITS) >> 8;
+        w.base = 18 + top8 + (MAGIC_BITS >> 8);
+        w.lowest = fmaxf((top8 - 44.5f) / t, -3.402823466e38f);
     }
     Cut cut{-INFINITY, -1};
     int phase = 0;
-    if (top_k > 0 && top_k < a.vocab) select<false>(row, w, s, m, low, top_k, 1.f, cut, phase);
-    if (top_p < 1.f) select<true>(row, w, s, m, low, 0, top_p, cut, phase);
+    if (bound > 0 && draw_of_few(row, w, s, m, row.see(of_key(bound)), own, top_k, top_p, min_p, u, a, r, phase)) {
+        sync_cluster();
+        return;
+    }
+    if (cuts) {
+        // As many items as there are threads reach the smallest of the threads' maxima, and below 2^-47 of the largest weight
+        // there is none to cut.
+        const float range = fminf(fminf(m - low, 47.f * 256.f / w.t), 3.4e38f);
+        select<false>(row, w, s, Window{Scale{}, 0, 0, m, range, -INFINITY, (unsigned long long)top_k}, cut, phase);
+    }
+    if (top_p < 1.f) select<true>(row, w, s, nucleus(row, w, s, m, top_p, cut, phase), cut, phase);
     const unsigned long long least = min_p >= 1.f ? w(m) : ceil_of(min_p, w(m));
 
-    // sums of what is kept, per warp; the warp in which they pass u of their sum; the token in it
-    const auto kept = [&](float x, int j) {
-        if (!cut.keeps(x, j)) return 0ull;
-        const unsigned long long y = w(x);
-        return y >= least ? y : 0ull;
+    // sums of what is kept, per warp; the warp's part in which they pass u of their sum; the token in it
+    float from = cut.x;                                // nothing below is kept
+    if (min_p > 0.f) from = fmaxf(from, m + 256.f * (log2f(fminf(min_p, 1.f)) - 0.01f) / w.t - fabsf(m) * 1e-6f);
+    const bool all = from == -INFINITY && w.lowest > -3.4e38f;             // (then -inf has no weight by itself)
+    const auto kept = [&](const float* x, int j, unsigned long long* y) {  // false: none of the warp's
+        if (!all && !any_from(x, from)) return false;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) y[k] = w(x[k]);
+        if (!all) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) y[k] = cut.keeps(x[k], j + k) && y[k] >= least ? y[k] : 0ull;
+        }
+        return true;
     };
-    {
+    const auto sum_of = [&](int at, int n) {
         unsigned long long sum = 0;
-        row.each([&](float x, int j) { sum += kept(x, j); });
-        sum = warp_sum64(sum);
+        row.each_of(at, n, [&](const float* x, int j) {
+            unsigned long long y[4];
+            if (kept(x, j, y)) sum += (y[0] + y[1]) + (y[2] + y[3]);
+        });
+        return warp_sum64(sum);
+    };
+    const int per = a.part / WARPS;
+    {
+        const unsigned long long sum = sum_of(row.first + warp * per, per);
         if (lane == 0) s.warp_sum[warp] = sum;
     }
     sync_cluster();
     unsigned long long total;
-    const unsigned long long part = tid < ctas * WARPS ? ld_cluster64(of_rank(&s.warp_sum[lane], warp)) : 0ull;
+    const unsigned long long part = tid < ctas * WARPS ? ld_cluster64(of_rank(&s.warp_sum[tid % WARPS], tid / WARPS)) : 0ull;
     const unsigned long long upto = block_scan(part, s.scan, total);
     const unsigned long long target = u >= 1.f ? total - 1 : floor_of(u, total);
     if (upto - part <= target && target < upto) {
@@ -501,50 +822,49 @@ __global__ void __launch_bounds__(THREADS, 1) sample_kernel(const SampleArgs a) 
         s.above = upto - part;
     }
     __syncthreads();
-    if (s.segment / WARPS == rank && s.segment % WARPS == warp) {
-        unsigned long long before = s.above;
-        const int per = a.part / WARPS;
-        for (int at = 0; at < per; at += 128) {
-            const int to = warp * per + at + lane * 4;
-            const float4 v = *reinterpret_cast<const float4*>(xs + to);
-            const float x[4] = {v.x, v.y, v.z, v.w};
-            unsigned long long y[4], sum = 0;
+    if (s.segment / WARPS == rank) {                   // in this CTA: the part again, by all its warps
+        const int small = (per / 128 + WARPS - 1) / WARPS * 128, piece = row.first + s.segment % WARPS * per;
+        const int at = min(warp * small, per), n = min(small, per - at);
+        const unsigned long long mine = sum_of(piece + at, n), above = s.above;
+        unsigned long long of_piece;
+        const unsigned long long end = above + block_scan(lane == 31 ? mine : 0ull, s.scan, of_piece);
+        unsigned long long before = shfl64(end, 0);    // what stands before this warp's piece
+        if (before <= target && target < before + mine) {
+            for (int p = piece + at; p < piece + at + n; p += 128) {
+                const float4 v = row.raw(p + lane * 4);
+                const int j = p + lane * 4 - row.off;
+                const float x[4] = {row.see(v.x), row.see(v.y), row.see(v.z), row.see(v.w)};
+                unsigned long long y[4], sum = 0;
+                if (kept(x, j, y)) sum = (y[0] + y[1]) + (y[2] + y[3]);
+                else y[0] = y[1] = y[2] = y[3] = 0ull;
+                const unsigned long long stop = before + warp_scan64(sum);
+                unsigned long long c = stop - sum;
+                if (c <= target && target < stop) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                y[k] = kept(x[k], row.first + to + k);
-                sum += y[k];
-            }
-            const unsigned long long end = before + warp_scan64(sum);
-            unsigned long long c = end - sum;
-            if (c <= target && target < end) {
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    if (c <= target && target < c + y[k]) {
-                        a.out_tokens[r] = row.first + to + k;
-                        if (a.out_probs) a.out_probs[r] = (float)((double)y[k] / (double)total);
+                    for (int k = 0; k < 4; ++k) {
+                        if (c <= target && target < c + y[k]) {
+                            a.out_tokens[r] = j + k;
+                            if (a.out_probs) a.out_probs[r] = (float)((double)y[k] / (double)total);
+                        }
+                        c += y[k];
                     }
-                    c += y[k];
                 }
+                before = shfl64(stop, 31);
+                if (target < before) break;
             }
-            before = shfl64(end, 31);
-            if (target < before) break;
         }
     }
     sync_cluster();
 }
 
-template <typename T> cudaError_t launch_sample(const SampleArgs& a, int n_rows, int ctas, cudaStream_t s) {
-    static std::atomic<uint64_t> done{0};
-    const cudaError_t e = smem_limit_once(sample_kernel<T>, MOST_PART * 4, done);
-    if (e != cudaSuccess) return e;
+template <typename T> cudaError_t launch_sample(const SampleArgs& a, int n_rows, cudaStream_t s) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(n_rows * ctas));
+    cfg.gridDim = dim3((unsigned)(n_rows * a.ctas));
     cfg.blockDim = dim3(THREADS);
-    cfg.dynamicSmemBytes = (size_t)a.part * 4;
     cfg.stream = s;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = (unsigned)ctas;
+    at[0].val.clusterDim.x = (unsigned)a.ctas;
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
@@ -584,13 +904,14 @@ extern "C" cb_status cb_sample(const void* logits, int32_t dtype, int32_t n_rows
         cudaGetLastError();
         return fail(CB_ERR_CUDA, "cb_sample: no CUDA device");
     }
-    // as few CTAs per row as hold it, and more while that leaves SMs idle
+    // Threads of a row: as many as all rows' find room for at once (two CTAs to an SM), up to a cluster of eight; a CTA more only
+    // for every 4096 tokens.  (A part has less than 2^16 tokens, see the histograms.)
     int ctas = 1;
-    const auto part = [&](int c) { return ((vocab + c - 1) / c + GRAIN - 1) / GRAIN * GRAIN; };
-    while (ctas < MOST_CTAS && (part(ctas) > MOST_PART || ((int64_t)n_rows * ctas * 2 <= sms && part(ctas) > GRAIN))) ctas *= 2;
-    const SampleArgs a{logits, row_stride, vocab, part(ctas), ctas, temperature, top_k, top_p, min_p, uniform, out_tokens, out_probs};
-    const cudaError_t e = dtype == CB_BF16 ? launch_sample<bf16>(a, n_rows, ctas, (cudaStream_t)stream)
-                                           : launch_sample<float>(a, n_rows, ctas, (cudaStream_t)stream);
+    while (ctas < MOST_CTAS && (vocab > 60000 * ctas || ((int64_t)n_rows * ctas * 2 <= 2 * sms && vocab > 4096 * ctas))) ctas *= 2;
+    const int places = vocab + 3;                      // (a row may begin up to three elements behind a boundary)
+    const int grain = 4 * THREADS, part = ((places + ctas - 1) / ctas + grain - 1) / grain * grain;
+    const SampleArgs a{logits, row_stride, vocab, part, ctas, temperature, top_k, top_p, min_p, uniform, out_tokens, out_probs};
+    const cudaError_t e = dtype == CB_BF16 ? launch_sample<bf16>(a, n_rows, (cudaStream_t)stream) : launch_sample<float>(a, n_rows, (cudaStream_t)stream);
     if (e == cudaSuccess) return CB_OK;
     cudaGetLastError();
     return fail(CB_ERR_CUDA, "cb_sample: %s", cudaGetErrorString(e));
