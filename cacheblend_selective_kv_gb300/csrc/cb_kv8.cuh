@@ -193,6 +193,7 @@ cudaError_t launch_kv8_shared(const Kv8& c, const Kv8Prefix& pre, const Kv8Seqs&
                               cudaStream_t s);
 cudaError_t launch_kv8_few_prefix(const Kv8& c, const void* attn_args, cudaStream_t s);
 cudaError_t launch_kv8_few_own(const Kv8& c, const void* attn_args, cudaStream_t s);
+cudaError_t launch_kv8_few_joint(const Kv8& c, const void* attn_args, cudaStream_t s);
 int kv8_most_ctas(int num_sms);
 bool kv8_make_map(const Kv8& c, void* out);
 

@@ -21,7 +21,9 @@ constexpr int TK = 128;                  // keys per tile
 //   PREFIX  a sequence is a group's prefix, its rows are those of all the group's sequences and see all of it; their sums,
 //           not divided, go to scratch with their references
 //   OWN     PLAIN, and what PREFIX has left is added to a row's sums before they are divided
-enum : int { PLAIN, PREFIX, OWN };
+// or one, where reading the prefix again for each sequence costs less than a second launch:
+//   JOINT   PLAIN, and a sequence's tiles begin with those of its prefix, which all its rows see
+enum : int { PLAIN, PREFIX, OWN, JOINT };
 
 // 16 bytes to shared memory, past L1
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
@@ -48,7 +50,8 @@ struct AttnArgs {
     int score_ld;                        // max_len rounded up to TK
     float2* stats;                       // weights: [Hkv][n_q][G] (max, 1 / sum)
     unsigned* voided;                    // weights: the call's offsets decrease, nothing was computed (NULL: no query rows)
-    // PREFIX and OWN
+    // PREFIX, OWN and JOINT
+    Kv8Seqs pre;                         // JOINT: the groups' prefixes
     const int* first;                    // [groups + 1] first sequence of each group, or NULL: `per_group` each
     int per_group, groups, members;      // members: sequences
     float* prefix_sum;                   // [n_q][Hq][HD]
@@ -70,12 +73,14 @@ __device__ __forceinline__ float exp2_fast(float x) {          // special-functi
 // ------------------------------------------------------------------------------------------------
 struct Seq {                             // one sequence: its query rows and length (-1: its offsets decrease)
     int r0, n, len;
+    int pre, group;                      // JOINT: rows of its prefix, and whose they are
+    template <int MODE> __device__ __forceinline__ int pre_tiles() const { return MODE == JOINT ? (pre + TK - 1) / TK : 0; }
     __device__ __forceinline__ int q_tiles(int QT) const { return (n + QT - 1) / QT; }
     // keys that the last row of query tile qt sees
     template <int MODE> __device__ __forceinline__ int visible(int qt, int QT) const {
         return MODE == PREFIX ? len : max(0, len - n + min((qt + 1) * QT, n));
     }
-    template <int MODE> __device__ __forceinline__ int tiles(int qt, int QT) const { return max(1, (visible<MODE>(qt, QT) + TK - 1) / TK); }
+    template <int MODE> __device__ __forceinline__ int tiles(int qt, int QT) const { return max(1, pre_tiles<MODE>() + (visible<MODE>(qt, QT) + TK - 1) / TK); }
     // the last key that row q0 sees (PREFIX: and every other row)
     template <int MODE> __device__ __forceinline__ int position(int q0) const { return MODE == PREFIX ? len - 1 : len - n + q0; }
 };
@@ -94,8 +99,37 @@ __device__ __forceinline__ Seq group_at(const AttnArgs& p, int g) {
     atomicOr(p.q.status, ST_BAD_ROW);
     return Seq{0, 0, -1};
 }
+// a sequence with its prefix
+__device__ __forceinline__ Seq joint_at(const AttnArgs& p, int s) {
+    Seq q{0, 0, 0, 0, 0};
+    int r1;
+    if (!kv8_rows(p.q, p.r, s, q.r0, r1, q.len)) return Seq{0, 0, q.r0 < 0 || r1 < q.r0 || r1 > p.r.n_rows ? -1 : 0};
+    q.n = r1 - q.r0;
+    if (p.first) {
+        if (s < p.first[0] || s >= p.first[p.groups]) return q;
+        int z = p.groups - 1;                                    // the last group that begins at or before it
+        while (q.group < z) {
+            const int m = (q.group + z + 1) >> 1;
+            if (p.first[m] <= s) q.group = m; else z = m - 1;
+        }
+    } else {
+        q.group = s / p.per_group;
+    }
+    const int pre = kv8_len(p.pre, q.group);
+    if (pre >= 0 && pre <= p.pre.max_len) q.pre = pre;
+    else atomicOr(p.q.status, ST_BAD_ROW);
+    return q;
+}
+// (JOINT) whether the groups' first sequences are in order
+__device__ __forceinline__ bool bad_groups(const AttnArgs& p, int g) {
+    const int a = p.first[g], b = p.first[g + 1];
+    const bool bad = a < 0 || b < a || b > p.members;
+    if (bad) atomicOr(p.q.status, ST_BAD_ROW);
+    return bad;
+}
 template <int MODE = PLAIN> __device__ __forceinline__ Seq seq_at(const AttnArgs& p, int s) {
     if constexpr (MODE == PREFIX) return group_at(p, s);
+    if constexpr (MODE == JOINT) return joint_at(p, s);
     Seq q;
     int r1;
     if (!kv8_rows(p.q, p.r, s, q.r0, r1, q.len)) return Seq{0, 0, r1 < q.r0 ? -1 : 0};
@@ -238,6 +272,11 @@ __device__ __forceinline__ void find_piece(const AttnArgs& p, Find<MODE>& f, Pie
     const int n_own = seq_places<MODE>(p, q_own);
     bool decrease = q_own.len < 0;
     if constexpr (MODE == OWN) decrease |= *p.prefix_voided != 0;
+    if constexpr (MODE == JOINT) {
+        if (p.first)
+#pragma unroll 1
+            for (int g = tid; g < p.groups; g += THREADS) decrease |= bad_groups(p, g);
+    }
     {
         int sum = n_own;
 #pragma unroll 1
@@ -408,7 +447,14 @@ __device__ __forceinline__ void produce_tiles(const AttnArgs& p, const CUtensorM
         bool need;                                               // the box holds rows of the sequence
     };
     auto look = [&](const Cursor<MODE>& u) {
-        const int j = u.t * TK + lane * rows;
+        const int own_t = u.t - u.q.template pre_tiles<MODE>();
+        if (MODE == JOINT && own_t < 0) {
+            const int j = u.t * TK + lane * rows;
+            Ahead a{0, u.g, j & in_page, lane < boxes && j < u.q.pre};
+            if (a.need) a.page = p.pre.table[(int64_t)u.q.group * p.pre.table_ld + (j >> p.q.shift)];
+            return a;
+        }
+        const int j = own_t * TK + lane * rows;
         Ahead a{0, u.g, j & in_page, lane < boxes && j < u.q.len};
         if (a.need) a.page = p.q.table[(int64_t)u.s * p.q.table_ld + (j >> p.q.shift)];
         return a;

@@ -390,10 +390,13 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
             };
 
             for (int t = first; t < first + n_here; ++t, ++i) {
-                const int b = i & 1, j = t * TK + key;
+                // j: the key's place in the prefix or among the sequence's own
+                const int own_t = t - q.pre_tiles<MODE>();
+                const bool shared = MODE == JOINT && own_t < 0;
+                const int b = i & 1, j = (shared ? t : own_t) * TK + key;
                 ptx::mbar_wait(ptx::smem_u32(&c.ring.full[i % RING]), (i / RING) & 1, abort, status);
                 const float ks_now = c.ring.scale[i % RING][0][key >> box_shift], vs_now = c.ring.scale[i % RING][1][key >> box_shift];
-                const bool have = ks_now >= 0.f && j < q.len;
+                const bool have = ks_now >= 0.f && j < (shared ? q.pre : q.len);
 
                 ptx::mbar_wait(ptx::smem_u32(&c.s_full[b]), (i >> 1) & 1, abort, status);
                 ptx::tc_fence_after();
@@ -416,7 +419,7 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
                     }
                 }
                 // column k (query row k / G) sees key j from its own position on: k >= (j - pos0) G
-                const int hidden = have ? min(max(j - pos0, 0), NC) * p.G - c0 : NC;
+                const int hidden = !have ? NC : shared ? 0 : min(max(j - pos0, 0), NC) * p.G - c0;
                 if (hidden > 0) {
 #pragma unroll
                     for (int k = 0; k < NW; ++k)
@@ -497,7 +500,7 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
                     else if constexpr (NW == 8) *reinterpret_cast<uint2*>(d) = make_uint2(w[0], w[1]);
                     else *reinterpret_cast<uint4*>(d) = make_uint4(w[0], w[1], w[2], w[3]);
                 }
-                if (gr == 0 && (!have || j > pos0)) {
+                if (gr == 0 && (!have || (!shared && j > pos0))) {
                     const int st = i % STAGES;
                     ptx::mbar_wait(ptx::smem_u32(&c.v_full[st]), (i / STAGES) & 1, abort, status);
                     clean_v_row<HD>(sV + st * S::KV_BYTES, key, have, j, nan_from);
@@ -641,7 +644,7 @@ cudaError_t launch_shape(const Kv8& c, AttnArgs& p, cudaStream_t s) {
     p.ahead = 2;                         // (64 x 8K decode 102 us with 0, 100 with 1, 98 with 2 and 3)
     p.min_places = 2 + p.ahead;
     const int64_t items = ((int64_t)p.r.n_rows / p.QT + p.q.n) * p.Hkv;
-    const int64_t tiles = items * ((p.q.max_len + TK - 1) / TK + 1);
+    const int64_t tiles = items * ((p.q.max_len + TK - 1) / TK + 1 + (MODE == JOINT ? (p.pre.max_len + TK - 1) / TK : 0));
     const int64_t most = (int64_t)c.num_sms * S::CTAS;
     CUtensorMap map;
     memcpy(&map, c.map, sizeof map);

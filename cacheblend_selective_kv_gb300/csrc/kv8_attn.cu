@@ -2,6 +2,7 @@
 // need of the host.
 #include <cudaTypedefs.h>
 
+#include <cstdlib>
 #include <iterator>
 
 #include "cb_kv8_few.cuh"
@@ -113,6 +114,21 @@ cudaError_t launch_kv8_shared(const Kv8& c, const Kv8Prefix& pre, const Kv8Seqs&
     p.per_group = pre.per_group;
     p.groups = pre.q.n;
     p.members = q.n;
+    {
+        // Tiles that reading the prefix again for each sequence of a group costs
+        AttnArgs own = p;
+        own.q = q;
+        own.pre = pre.q;
+        own.voided = c.voided;
+        const bool many = many_rows(c, own);
+        const int64_t columns = (int64_t)((r.n_rows + q.n - 1) / q.n) * p.G, per_item = many ? 128 : c.cfg.dtype == CB_F32 ? 8 : 32;
+        const int64_t items = (columns + per_item - 1) / per_item * p.Hkv, pre_tiles = ((int64_t)pre.q.max_len + TK - 1) / TK;
+        const int64_t again = (q.n > pre.q.n ? q.n - pre.q.n : 0) * items * pre_tiles;
+        const int64_t places = ((int64_t)r.n_rows + q.n) * p.Hkv * (pre_tiles + ((int64_t)q.max_len + TK - 1) / TK + 8);
+        const char* env = getenv("CB_SHARED_AGAIN");
+        if (again <= (env ? atoll(env) : 2400) && places < 0x7fffffff)
+            return many ? launch_kv8_rows(c, &own, JOINT, s) : launch_kv8_few_joint(c, &own, s);
+    }
     p.prefix_sum = pre.scratch;
     p.prefix_stat = reinterpret_cast<float2*>(pre.scratch + (int64_t)r.n_rows * p.Hq * c.cfg.head_dim);
     p.voided = c.voided + 16;

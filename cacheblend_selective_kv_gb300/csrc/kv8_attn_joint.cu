@@ -1,0 +1,12 @@
+// Attention over a prefix that sequences share, few rows: prefix and own keys in one launch (a translation unit of its own, for the
+// build's time).
+#include "cb_kv8_few.cuh"
+
+namespace cb {
+
+cudaError_t launch_kv8_few_joint(const Kv8& c, const void* attn_args, cudaStream_t s) {
+    AttnArgs p = *static_cast<const AttnArgs*>(attn_args);
+    return c.cfg.head_dim == 128 ? launch_few<128, JOINT>(c, p, s) : launch_few<64, JOINT>(c, p, s);
+}
+
+}  // namespace cb

@@ -199,7 +199,11 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_rows_kernel(const __grid_const
             const int st = i & 1;
             const uint32_t par = ((i >> 1) & 1) ^ 1;
             const Seq q = cur.q;
-            const int q0 = cur.qt * p.QT, cols = min(p.QT, q.n - q0) * p.G, pos0 = q.position<MODE>(q0), tile = cur.t;
+            const int q0 = cur.qt * p.QT, cols = min(p.QT, q.n - q0) * p.G, pos0 = q.position<MODE>(q0);
+            // the tile of the prefix or of the sequence's own keys, and how many of those there are
+            const int own_t = cur.t - q.pre_tiles<MODE>();
+            const bool shared = MODE == JOINT && own_t < 0;
+            const int tile = shared ? cur.t : own_t, keys = shared ? q.pre : q.len;
             if (begins) {
                 ++item;
                 const bf16* qbase = (const bf16*)p.a.q + (int64_t)(q.r0 + q0) * p.a.q_stride + (int64_t)cur.g * p.G * HD;
@@ -286,7 +290,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_rows_kernel(const __grid_const
             ptx::mbar_wait(ptx::smem_u32(&c.vc_full[i % VT]), (i / VT) & 1, abort, status);
             ptx::mbar_wait(ptx::smem_u32(&c.pv_done[st]), par, abort, status);
             const float* loaded = c.ring.scale[i % RING][0];
-            const bool plain = (tile + 1) * TK <= min(q.len, pos0 + 1) &&
+            const bool plain = (tile + 1) * TK <= (shared ? keys : min(keys, pos0 + 1)) &&
                                !__any_sync(0xffffffffu, lane < (TK >> box_shift) && loaded[lane] < 0.f);
             const auto codes_of = [&](int row) {
                 return *reinterpret_cast<const uint4*>(sm + S::OFF_VC + (i % VT) * S::CODES + f8_at<HD>(row, e * 16));
@@ -299,8 +303,8 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_rows_kernel(const __grid_const
                 for (int n = 0; n < NI; ++n) {
                     const int row = row0 + n * CONV / 32 * RPW, j = tile * TK + row;
                     uint4 x = codes_of(row);
-                    if (j >= q.len || loaded[row >> box_shift] < 0.f) x = make_uint4(0, 0, 0, 0);
-                    else if (j > pos0) take_nan(x, j, nan_marks + (item % MARKS) * HD + e * 16, &c.any_nan[item % MARKS]);
+                    if (j >= keys || loaded[row >> box_shift] < 0.f) x = make_uint4(0, 0, 0, 0);
+                    else if (!shared && j > pos0) take_nan(x, j, nan_marks + (item % MARKS) * HD + e * 16, &c.any_nan[item % MARKS]);
                     widen(sV + st * S::TILE, row, x);
                 }
             }
@@ -397,7 +401,9 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_rows_kernel(const __grid_const
                 up = at == ref ? P_UP : P_UP * exp2_fast(at - ref);
             };
             for (int t = first; t < first + n_here; ++t, ++i) {
-                const int b = i & 1, j0 = t * TK + hf * HK;
+                const int own_t = t - q.pre_tiles<MODE>();
+                const bool shared = MODE == JOINT && own_t < 0;
+                const int b = i & 1, j0 = (shared ? t : own_t) * TK + hf * HK;
                 ptx::mbar_wait(ptx::smem_u32(&c.ring.full[i % RING]), (i / RING) & 1, abort, status);
                 if (t == first) {
                     ptx::mbar_wait(ptx::smem_u32(&c.rows_full[item % MARKS]), (item / MARKS) & 1, abort, status);
@@ -418,12 +424,12 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_rows_kernel(const __grid_const
                 const bool hole = fminf(fminf(scales[box_at(0)], scales[box_at(16)]), fminf(scales[box_at(32)], scales[box_at(48)])) < 0.f;
                 // Away from the tile loop's usual path, which has to stay short (with everything unrolled in place, most cycles
                 // went to waiting for instructions): -inf into S for keys that are not loaded or not seen
-                if (hole || j0 + HK - 1 > pos0) {
+                if (hole || j0 + HK - 1 > (shared ? q.pre - 1 : pos0)) {
 #pragma unroll 1
                     for (int k = 0; k < HK; k += 16) {
                         float w[16];
                         ptx::tmem_ld16(s_at + k, w);
-                        const int seen = scales[(hf * HK + k) >> box_shift] < 0.f ? 0 : pos - (j0 + k) + 1;
+                        const int seen = scales[(hf * HK + k) >> box_shift] < 0.f ? 0 : (shared ? q.pre - 1 : pos) - (j0 + k) + 1;
 #pragma unroll
                         for (int y = 0; y < 16; ++y) w[y] = y < seen ? w[y] : -INFINITY;
                         ptx::tmem_st16(s_at + k, w);
@@ -680,7 +686,7 @@ template <int HD, bool SCORES, int MODE> cudaError_t launch_dim(const Kv8& c, At
     p.ahead = 4;
     p.min_places = 1 + p.ahead;
     const int64_t items = ((int64_t)p.r.n_rows / p.QT + p.q.n) * p.Hkv;
-    const int64_t tiles = items * ((p.q.max_len + TK - 1) / TK + 1);
+    const int64_t tiles = items * ((p.q.max_len + TK - 1) / TK + 1 + (MODE == JOINT ? (p.pre.max_len + TK - 1) / TK : 0));
     CUtensorMap map;
     memcpy(&map, c.map, sizeof map);
     const unsigned ctas = (unsigned)(tiles < c.num_sms ? tiles : c.num_sms);
@@ -700,6 +706,7 @@ cudaError_t launch_kv8_rows(const Kv8& c, const void* attn_args, int mode, cudaS
     p.todo = c.todo;
     const bool wide = c.cfg.head_dim == 128;
     if (mode == PREFIX) return wide ? launch_dim<128, false, PREFIX>(c, p, s) : launch_dim<64, false, PREFIX>(c, p, s);
+    if (mode == JOINT) return wide ? launch_dim<128, false, JOINT>(c, p, s) : launch_dim<64, false, JOINT>(c, p, s);
     if (mode == OWN) return wide ? launch_dim<128, false, OWN>(c, p, s) : launch_dim<64, false, OWN>(c, p, s);
     if (p.scores) return wide ? launch_dim<128, true, PLAIN>(c, p, s) : launch_dim<64, true, PLAIN>(c, p, s);
     return wide ? launch_dim<128, false, PLAIN>(c, p, s) : launch_dim<64, false, PLAIN>(c, p, s);

@@ -27,6 +27,12 @@ def cb():
     return cbm
 
 
+@pytest.fixture(params=["one launch", "two launches"], autouse=True)
+def path(request, monkeypatch):
+    """Both ways of a call: the prefix read again for each sequence in one launch, or once in a launch of its own."""
+    monkeypatch.setenv("CB_SHARED_AGAIN", str(1 << 40) if request.param == "one launch" else "-1")
+
+
 class Shared(Case):
     """A Case whose first sequences are the groups' prefixes, the others the batch."""
 
