@@ -559,9 +559,10 @@ class KV8Cache:
         return t.data_ptr()
 
     def _seqs(self, table, lens, max_len, layer, n_layers=1):
-        if table.dim() != 2:
+        shape = table.shape
+        if len(shape) != 2:
             raise ValueError("table must be int32 [n_seqs][pages]")
-        n, ld = table.shape
+        n, ld = shape
         if max_len is None:
             max_len = ld * self.page_size
         # (ctypes would take the lower 32 bits of a larger number)
@@ -633,10 +634,14 @@ class KV8Cache:
         positions, and k and v become the last rows of their sequences (as write puts them there); q ([n_rows][n_heads]
         [head_dim], or None) is rotated into out_q, which may be q itself; returns out_q.  positions: device int32 [n_rows];
         None: a row's place in its sequence.  row_start as for write.  Rows of no sequence are left as they were."""
-        kp, _, kv_stride, n = self._kv(k, "k", 1)
-        vp, _, v_stride, n_v = self._kv(v, "v", 1)
-        if (n, kv_stride) != (n_v, v_stride):
-            raise ValueError("k and v must have the same number of rows and the same strides")
+        shape, stride, dt, dev = k.shape, k.stride(), self.dtype, self._dev
+        if k.dtype is not dt or v.dtype is not dt or k.get_device() != dev or v.get_device() != dev or len(shape) != 3 or \
+                shape[1:] != self._kv_row or stride[2] != 1 or (stride[1] != self.head_dim and self.n_kv_heads > 1) or \
+                v.shape != shape or v.stride() != stride:
+            self._kv(k, "k", 1)
+            self._kv(v, "v", 1)
+            raise ValueError("k and v must be [n_rows][n_kv_heads][head_dim] with the same number of rows and the same strides")
+        n = shape[0]
         qp, qs, op, os_ = None, 0, None, 0
         if q is not None:
             if out_q is None:
@@ -644,13 +649,14 @@ class KV8Cache:
                     # rows that belong to no sequence are not written: zeros there
                     out_q = q.new_empty(q.shape) if row_start is None else q.new_zeros(q.shape)
             qp, qs, n_q = self._q(q, "q")
-            op, os_, n_out = self._q(out_q, "out_q")
+            op, os_, n_out = (qp, qs, n_q) if out_q is q else self._q(out_q, "out_q")
             if n_q != n or n_out != n:
                 raise ValueError(f"q and out_q must have k's {n} rows")
         elif out_q is not None:
             raise ValueError("out_q without q")
         sq = self._seqs(table, lens, max_len, layer)
-        code = self._lib.cb_kv8_append(self.handle, sq, layer, qp, qs, op, os_, kp, vp, kv_stride,
+        code = self._lib.cb_kv8_append(self.handle, sq, layer, qp, qs, op, os_, k.data_ptr(), v.data_ptr(),
+                                       stride[0] if n > 1 else self._kv_width,
                                        None if positions is None else self._int(positions, "positions", n), rope_theta,
                                        None if row_start is None else self._int(row_start, "row_start", sq.n_seqs + 1), n,
                                        self._stream(stream))

@@ -107,6 +107,16 @@ cudaError_t launch_kv8_attention(const Kv8& c, const Kv8Seqs& q, const Kv8Rows& 
     return cudaSuccess;
 }
 
+// Time of one tile of 128 keys in all items of n sequences of `columns` columns each, over all SMs, when the codes come from L2
+// (heads of 128; heads of 64 take as long).  A second launch costs 16 to 20 us: 8 sequences on 2048 keys 14.7 us in one launch,
+// 32.4 in two; 64 on 2000 keys 36.7 and 38.4; 4 of 64 rows on 8192 keys 66 and 82.
+double tiles_ns(const Kv8& c, int n, int columns) {
+    const bool wide = c.cfg.dtype == CB_F32;
+    const int per_item = wide ? (columns <= 4 ? 4 : 8) : columns <= 4 ? 4 : columns <= 8 ? 8 : columns <= 16 ? 16 : columns <= 32 ? 32 : 128;
+    const double ns = wide ? (per_item == 4 ? 3.3 : 4.3) : per_item == 4 ? 2.7 : per_item == 8 ? 3.5 : per_item == 16 ? 5.5 : per_item == 32 ? 9.5 : 10.0;
+    return (double)n * ((columns + per_item - 1) / per_item) * ns;
+}
+
 cudaError_t launch_kv8_shared(const Kv8& c, const Kv8Prefix& pre, const Kv8Seqs& q, const Kv8Rows& r, const Kv8Attn& a, int layer,
                               cudaStream_t s) {
     AttnArgs p = attn_args(c, pre.q, r, a, layer);
@@ -114,19 +124,17 @@ cudaError_t launch_kv8_shared(const Kv8& c, const Kv8Prefix& pre, const Kv8Seqs&
     p.per_group = pre.per_group;
     p.groups = pre.q.n;
     p.members = q.n;
+    AttnArgs own = p;
+    own.q = q;
+    own.pre = pre.q;
+    own.voided = c.voided;
+    const bool many = many_rows(c, own);
     {
-        // Tiles that reading the prefix again for each sequence of a group costs
-        AttnArgs own = p;
-        own.q = q;
-        own.pre = pre.q;
-        own.voided = c.voided;
-        const bool many = many_rows(c, own);
-        const int64_t columns = (int64_t)((r.n_rows + q.n - 1) / q.n) * p.G, per_item = many ? 128 : c.cfg.dtype == CB_F32 ? 8 : 32;
-        const int64_t items = (columns + per_item - 1) / per_item * p.Hkv, pre_tiles = ((int64_t)pre.q.max_len + TK - 1) / TK;
-        const int64_t again = (q.n > pre.q.n ? q.n - pre.q.n : 0) * items * pre_tiles;
-        const int64_t places = ((int64_t)r.n_rows + q.n) * p.Hkv * (pre_tiles + ((int64_t)q.max_len + TK - 1) / TK + 8);
-        const char* env = getenv("CB_SHARED_AGAIN");
-        if (again <= (env ? atoll(env) : 2400) && places < 0x7fffffff)
+        // One launch or two: the prefix read by each sequence (from L2, once one has read it) against a launch of its own.
+        const int64_t pre_tiles = ((int64_t)pre.q.max_len + TK - 1) / TK, places = ((int64_t)r.n_rows + q.n) * p.Hkv * (pre_tiles + q.max_len / TK + 9);
+        const double apart = tiles_ns(c, q.n, (r.n_rows + q.n - 1) / q.n * p.G) - tiles_ns(c, pre.q.n, (r.n_rows + pre.q.n - 1) / pre.q.n * p.G);
+        const char* again = getenv("CB_SHARED_AGAIN");           // what reading it again may cost, ns
+        if (apart * (double)(pre_tiles * p.Hkv) <= (again ? atof(again) : 17000.0) && places < 0x7fffffff)
             return many ? launch_kv8_rows(c, &own, JOINT, s) : launch_kv8_few_joint(c, &own, s);
     }
     p.prefix_sum = pre.scratch;
@@ -134,10 +142,10 @@ cudaError_t launch_kv8_shared(const Kv8& c, const Kv8Prefix& pre, const Kv8Seqs&
     p.voided = c.voided + 16;
     cudaError_t e = many_rows(c, p) ? launch_kv8_rows(c, &p, PREFIX, s) : launch_kv8_few_prefix(c, &p, s);
     if (e != cudaSuccess) return e;
-    p.prefix_voided = p.voided;
-    p.voided = c.voided;
-    p.q = q;
-    return many_rows(c, p) ? launch_kv8_rows(c, &p, OWN, s) : launch_kv8_few_own(c, &p, s);
+    own.prefix_voided = p.voided;
+    own.prefix_sum = p.prefix_sum;
+    own.prefix_stat = p.prefix_stat;
+    return many ? launch_kv8_rows(c, &own, OWN, s) : launch_kv8_few_own(c, &own, s);
 }
 
 }  // namespace cb

@@ -30,7 +30,7 @@ def cb():
 @pytest.fixture(params=["one launch", "two launches"], autouse=True)
 def path(request, monkeypatch):
     """Both ways of a call: the prefix read again for each sequence in one launch, or once in a launch of its own."""
-    monkeypatch.setenv("CB_SHARED_AGAIN", str(1 << 40) if request.param == "one launch" else "-1")
+    monkeypatch.setenv("CB_SHARED_AGAIN", "1e15" if request.param == "one launch" else "-1e15")
 
 
 class Shared(Case):
