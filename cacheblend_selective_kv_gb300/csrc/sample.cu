@@ -35,6 +35,7 @@ constexpr int THREADS = 512, WARPS = THREADS / 32;
 constexpr int BINS = THREADS;            // a thread per bin where they are summed
 constexpr int CAP = 256;                 // items that are compared each with each
 constexpr int MOST_K = 128;              // top-k up to which there are few candidates
+constexpr int LISTED = 8192, PER_WARP = LISTED / WARPS;          // candidates that a CTA, and a warp of it, may list
 constexpr int MOST_CTAS = 8;
 static_assert(CB_SAMPLE_MAX_VOCAB <= 60000 * MOST_CTAS, "the largest vocabulary");
 constexpr float MAGIC = 12582912.f;      // 1.5 * 2^23: adding it rounds to a whole number
@@ -83,13 +84,16 @@ struct Shared {
     unsigned low;                        // key of the smallest of its threads' maxima
     unsigned bound;                      // key of its share of the top-k's lower bound
     unsigned hist[2][4][BINS];           // counts, and weights in words of 16 bits; two buffers
-    unsigned long long over[2], rest[2]; // weights above the first and in the last step
+    unsigned long long mass[2][BINS];    // those as one
+    unsigned long long over[2], rest[2]; // weights above the window, and of all
     unsigned found[2], low_of[2], high_of[2];      // items of the step: how many, keys of the smallest and the largest value
     unsigned listed[2];
     Item list[2][CAP];
     int tie;                             // the token at which equal values are cut off
+    unsigned full;                       // a warp's list has overflowed
     unsigned long long warp_sum[WARPS];
     // of the CTA
+    unsigned long long over_warp[WARPS];           // weights above the window, by warp
     unsigned long long scan[WARPS];
     int bin, items, first, last;
     unsigned long long above;
@@ -119,6 +123,11 @@ __device__ __forceinline__ void sync_cluster() {
     ptx::cluster_sync();
 }
 
+__device__ __forceinline__ unsigned long long warp_sum64(unsigned long long v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
 // a value of every CTA: lane r has rank r's (lanes behind the last: `none`)
 __device__ __forceinline__ unsigned of_all(const unsigned* p, int ctas, unsigned none) {
     const int lane = threadIdx.x & 31;
@@ -140,6 +149,7 @@ template <typename V> __device__ __forceinline__ unsigned long long sum_of_all(c
     for (int r = 0; r < MOST_CTAS; ++r) sum += v[r];
     return sum;
 }
+__device__ __forceinline__ unsigned long long total_of_all(const unsigned long long* p, int ctas) { return warp_sum64(of_all(p, ctas)); }
 // adds to a 64-bit word in shared memory by its halves
 __device__ __forceinline__ void add64(unsigned long long* to, unsigned long long v) {
     unsigned* w = reinterpret_cast<unsigned*>(to);
@@ -156,11 +166,6 @@ __device__ __forceinline__ float of_key(unsigned k) { return __uint_as_float(k ^
 __device__ __forceinline__ unsigned long long shfl64(unsigned long long v, int lane) {
     const unsigned lo = __shfl_sync(0xffffffffu, (unsigned)v, lane), hi = __shfl_sync(0xffffffffu, (unsigned)(v >> 32), lane);
     return ((unsigned long long)hi << 32) | lo;
-}
-__device__ __forceinline__ unsigned long long warp_sum64(unsigned long long v) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
 }
 __device__ __forceinline__ unsigned long long warp_scan64(unsigned long long v) {        // inclusive
     const int lane = threadIdx.x & 31;
@@ -237,6 +242,9 @@ template <typename T> struct Row {
     const T* x;                          // token 0
     int vocab, off;
     int part, first, ctas, rank;         // places of this CTA: first .. first + part - 1
+    // or the part's candidates in the tokens' order, when they have been listed: places are those of the list
+    const float* values;
+    const int* tokens;
     // Rows whose values stand for others.  Infinities share all the weight: they become 0, all others -inf.  At low temperatures
     // values are taken less the largest (what has weight lies so near to it that the difference is exact), and at the very
     // lowest times 2^32, so that 1 / T stays within fp32.
@@ -246,14 +254,27 @@ template <typename T> struct Row {
         return !special ? v : !infinite ? (v - less) * times : v == INFINITY ? 0.f : -INFINITY;
     }
     __device__ __forceinline__ float4 raw(int place) const {     // four from here on; -inf where there is no token
+        if (values) return *reinterpret_cast<const float4*>(values + place);
         const int j = place - off;
         if (j >= 0 && j + 4 <= vocab) return four_of(x + j);
         const auto one = [&](int k) { return k >= 0 && k < vocab ? to_f(x[k]) : -INFINITY; };
         return make_float4(one(j), one(j + 1), one(j + 2), one(j + 3));
     }
-    // f(four values, the first one's token) for the places of [from, from + n) that this thread of a warp has, n a multiple of
+    __device__ __forceinline__ void tokens_of(int place, int* j) const {
+        if (tokens) {
+            const int4 v = *reinterpret_cast<const int4*>(tokens + place);
+            j[0] = v.x;
+            j[1] = v.y;
+            j[2] = v.z;
+            j[3] = v.w;
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) j[k] = place - off + k;
+        }
+    }
+    // f(four values, the place of the first) for the places of [from, from + n) that this thread of a warp has, n a multiple of
     // 128: in the tokens' order within a step of the warp, all lanes together.  Two vectors are under way beside the one that
-    // is worked on.
+    // is worked on (a third made nothing faster).
     template <typename F> __device__ __forceinline__ void each_of(int from, int n, F f) const {
         const int end = from + n;
         int p = from + (threadIdx.x & 31) * 4;
@@ -268,7 +289,7 @@ template <typename T> struct Row {
 #pragma unroll
                 for (int k = 0; k < 4; ++k) v[k] = see(v[k]);
             }
-            f(v, p - off);
+            f(v, p);
         }
     }
     template <typename F> __device__ __forceinline__ void each(F f) const {
@@ -327,6 +348,7 @@ struct Window {
     int first, last;
     float high, range, low;
     unsigned long long target;
+    unsigned items;                      // in the window and above it
 };
 
 // The window of top-p: weights are summed and items counted by step.  A step's items weigh at least what its lower edge does and
@@ -345,17 +367,20 @@ __device__ __forceinline__ Window nucleus(const Row<T>& row, const Weigh& w, Sha
     if (tid == 0) {
         s.rest[b] = 0;
         s.first = s.last = BINS - 1;
+        s.above = 0;
     }
     __syncthreads();
     unsigned long long sum = 0;
     const float from = cut.x > -INFINITY ? cut.x : w.lowest;     // (below the lowest there is no weight)
-    row.each([&](const float* x, int j) {
+    row.each([&](const float* x, int place) {
         if (!any_from(x, from)) return;
+        int j[4];
+        row.tokens_of(place, j);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             const int bits = w.bits(x[k]), at = scale(bits);
             const unsigned long long y = w(x[k], bits);
-            if (!cut.keeps(x[k], j + k)) continue;
+            if (!cut.keeps(x[k], j[k])) continue;
             sum += y;
             if (at < BINS - 1) atomicAdd(&s.hist[b][0][at], 1u);
         }
@@ -363,7 +388,7 @@ __device__ __forceinline__ Window nucleus(const Row<T>& row, const Weigh& w, Sha
     sum = warp_sum64(sum);
     if (lane == 0 && sum) add64(&s.rest[b], sum);
     sync_cluster();
-    win.target = max(ceil_of(p, sum_of_all(&s.rest[b], row.ctas)), 1ull);
+    win.target = max(ceil_of(p, total_of_all(&s.rest[b], row.ctas)), 1ull);
     const unsigned long long n = sum_of_all(&s.hist[b][0][tid], row.ctas);
     // a value is within half of a 256th of its whole number: a factor of less than 1 + 2^-9
     unsigned long long most = w.of_whole(scale.top - (tid << scale.shift)), least = w.of_whole(scale.top - ((tid + 1) << scale.shift) + 1);
@@ -376,11 +401,58 @@ __device__ __forceinline__ Window nucleus(const Row<T>& row, const Weigh& w, Sha
     __syncthreads();
     win.first = s.first;
     win.last = s.last;
+    const unsigned long long upto = block_scan(n, s.scan, total);
+    if (tid == win.last) s.above = upto;
+    __syncthreads();
+    win.items = (unsigned)s.above;
     const auto value = [&](int k) { return (float)(scale.top - MAGIC_BITS - k) / w.t; };     // about where x t 256 is k below the largest
     win.high = value((win.first << scale.shift) - 2);
     win.low = win.last == BINS - 1 ? -INFINITY : value(((win.last + 1) << scale.shift) + 2) - fabsf(m) * 1e-6f;
     win.range = win.high - value(((win.last + 1) << scale.shift) + 2);
     return win;
+}
+
+// Lists the part's values from `from` on, in the tokens' order, a warp's share in a piece of its own; what is done then reads
+// the list.  The row stays as it is where a warp of the cluster has more of them than its piece holds.  The first CAP of a CTA
+// stand in s.list[b] too; returns how many there are in the cluster (more than CAP: or more than that).
+template <typename T> __device__ __forceinline__ unsigned list_from(Row<T>& row, Shared& s, float from, float* values, int* tokens, int b) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, base = warp * PER_WARP;
+    if (threadIdx.x == 0) s.full = s.found[b] = 0;
+    __syncthreads();
+    int n = 0;
+    row.each([&](const float* x, int place) {
+        if (!any_from(x, from)) return;
+        int at = n;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const unsigned votes = __ballot_sync(0xffffffffu, x[k] >= from);
+            at += __popc(votes & ((1u << lane) - 1u));
+            n += __popc(votes);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if (!(x[k] >= from)) continue;
+            if (at < PER_WARP) {
+                values[base + at] = x[k];
+                tokens[base + at] = place - row.off + k;
+            }
+            ++at;
+            if (s.found[b] <= CAP) {                   // (a look at the count spares the additions behind)
+                const unsigned i = atomicAdd(&s.found[b], 1u);
+                if (i < CAP) s.list[b][i] = Item{x[k], place - row.off + k};
+            }
+        }
+    });
+    for (int i = n + lane; i < PER_WARP; i += 32) values[base + i] = -INFINITY;
+    if (n > PER_WARP && lane == 0) s.full = 1;
+    sync_cluster();
+    if (__any_sync(0xffffffffu, of_all(&s.full, row.ctas, 0u))) return CAP + 1;
+    row.values = values;
+    row.tokens = tokens;
+    row.part = LISTED;
+    row.first = 0;
+    row.special = false;
+    return __reduce_add_sync(0xffffffffu, of_all(&s.found[b], row.ctas, 0u));
 }
 
 // Lowers the cut to the first kept item, in descending order, at which the sum of counts (MASS: of weights) reaches the target.
@@ -398,11 +470,10 @@ __device__ __forceinline__ void select(const Row<T>& row, const Weigh& w, Shared
         const int b = phase++ & 1;
         const Steps step_of(high, range);
         // -1: not of this level; -2: above the window
-        const auto place = [&](float x, int j) {
+        const auto step = [&](float x, int j, int at) {
             if (!cut.keeps(x, j)) return -1;
             if (level == 0) {
                 if constexpr (MASS) {
-                    const int at = win.scale(w.bits(x));
                     if (at < win.first) return -2;
                     if (at > win.last) return -1;
                 }
@@ -420,16 +491,23 @@ __device__ __forceinline__ void select(const Row<T>& row, const Weigh& w, Shared
         }
         __syncthreads();
         unsigned long long over = 0;
-        row.each([&](const float* x, int j) {
+        row.each([&](const float* x, int place) {
             if (!any_from(x, low)) return;
+            int j[4];
+            row.tokens_of(place, j);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const int at = place(x[k], j + k);
                 unsigned long long y = 0;
+                int of_weight = 0;
                 if constexpr (MASS) {
-                    y = w(x[k]);
-                    over += at == -2 ? y : 0ull;
+                    const int bits = w.bits(x[k]);
+                    of_weight = win.scale(bits);
+                    y = w(x[k], bits);
+                    const bool above_it = level == 0 && of_weight < win.first;
+                    over += above_it && cut.keeps(x[k], j[k]) ? y : 0ull;
+                    if (above_it) continue;
                 }
+                const int at = step(x[k], j[k], of_weight);
                 if (at < 0) continue;
                 if (MASS || at < BINS - 1) atomicAdd(&s.hist[b][0][at], 1u);
                 if constexpr (MASS) {              // (a part has less than 2^16 items: no word overflows)
@@ -442,15 +520,19 @@ __device__ __forceinline__ void select(const Row<T>& row, const Weigh& w, Shared
         if constexpr (MASS) {
             over = warp_sum64(over);
             if (lane == 0 && over) add64(&s.over[b], over);
+            if (lane == 0 && level == 0) s.over_warp[tid >> 5] = over;
+        }
+        if constexpr (MASS) {                          // a step's three words as one
+            __syncthreads();
+            s.mass[b][tid] = s.hist[b][1][tid] + ((unsigned long long)s.hist[b][2][tid] << 16) + ((unsigned long long)s.hist[b][3][tid] << 32);
         }
         sync_cluster();
         // (counts: the last step, which holds whatever lies below, is not counted)
         const unsigned long long items = !MASS && tid == BINS - 1 ? 1ull << 32 : sum_of_all(&s.hist[b][0][tid], row.ctas);
         unsigned long long here = items;
         if constexpr (MASS) {
-            here = sum_of_all(&s.hist[b][1][tid], row.ctas) + (sum_of_all(&s.hist[b][2][tid], row.ctas) << 16) +
-                   (sum_of_all(&s.hist[b][3][tid], row.ctas) << 32);
-            if (level == 0) above = sum_of_all(&s.over[b], row.ctas);
+            here = sum_of_all(&s.mass[b][tid], row.ctas);
+            if (level == 0) above = total_of_all(&s.over[b], row.ctas);
         }
         unsigned long long total;
         const unsigned long long upto = above + block_scan(here, s.scan, total);
@@ -466,15 +548,25 @@ __device__ __forceinline__ void select(const Row<T>& row, const Weigh& w, Shared
         // the step's items
         float least = INFINITY, largest = -INFINITY;
         unsigned count = 0;
-        row.each([&](const float* x, int j) {
-            if (!any_from(x, low)) return;
+        // (values that may be in the step; the last one reaches to the window's end, and a step is off by its rounding)
+        const float size = range / (BINS - 1), margin = fabsf(high) * 1e-6f;
+        const bool narrow = range > 0x1p-100f && range < 0x1p100f;
+        const float no_more = narrow ? high - (bin - 0.01f) * size + margin : INFINITY;
+        const float no_less = narrow && bin < BINS - 1 ? fmaxf(high - (bin + 1.01f) * size - margin, low) : low;
+        row.each([&](const float* x, int place) {
+            bool in = false;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) in |= x[k] >= no_less && (bin == 0 || x[k] <= no_more);
+            if (!__any_sync(0xffffffffu, in)) return;
+            int j[4];
+            row.tokens_of(place, j);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                if (place(x[k], j + k) != bin) continue;
+                if (!(x[k] >= no_less) || step(x[k], j[k], MASS && level == 0 ? win.scale(w.bits(x[k])) : 0) != bin) continue;
                 ++count;
                 least = fminf(least, x[k]);
                 largest = fmaxf(largest, x[k]);
-                if (few) s.list[b][min(atomicAdd(&s.listed[b], 1u), CAP - 1u)] = Item{x[k], j + k};
+                if (few) s.list[b][min(atomicAdd(&s.listed[b], 1u), CAP - 1u)] = Item{x[k], j[k]};
             }
         });
         count = __reduce_add_sync(0xffffffffu, count);
@@ -530,9 +622,11 @@ __device__ __forceinline__ void select(const Row<T>& row, const Weigh& w, Shared
             if (keep > before && keep <= before + here_n) {
                 // this CTA has the token: by warp, then step by step
                 int mine = 0;
-                row.each([&](const float* x, int j) {
+                row.each([&](const float* x, int place) {
+                    int j[4];
+                    row.tokens_of(place, j);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) mine += x[k] == high && cut.keeps(x[k], j + k);
+                    for (int k = 0; k < 4; ++k) mine += x[k] == high && cut.keeps(x[k], j[k]);
                 });
                 const unsigned long long warps = __reduce_add_sync(0xffffffffu, (unsigned)mine);
                 unsigned long long all;
@@ -542,15 +636,24 @@ __device__ __forceinline__ void select(const Row<T>& row, const Weigh& w, Shared
                 if (keep > begin && keep <= begin + warps) {
                     unsigned left = (unsigned)(keep - begin);
                     const int per = row.part / WARPS, p0 = row.first + (tid >> 5) * per;
-                    for (int p = p0; p < p0 + per; p += 32) {
-                        const int j = p + lane - row.off;
-                        const bool is = j >= 0 && j < row.vocab && row.see(to_f(row.x[j])) == high && cut.keeps(high, j);
-                        const unsigned votes = __ballot_sync(0xffffffffu, is);
-                        if ((unsigned)__popc(votes) >= left) {
-                            if (is && __popc(votes & ((2u << lane) - 1u)) == (int)left) s.tie = j;
-                            break;
+                    for (int p = p0; p < p0 + per; p += 128) {
+                        const float4 v = row.raw(p + lane * 4);
+                        const float x[4] = {row.see(v.x), row.see(v.y), row.see(v.z), row.see(v.w)};
+                        int j[4];
+                        row.tokens_of(p + lane * 4, j);
+                        unsigned own = 0;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) own += x[k] == high && cut.keeps(high, j[k]);
+                        const unsigned stop = (unsigned)warp_scan64(own);
+                        if (stop - own < left && left <= stop) {
+                            unsigned at = stop - own;
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                if (x[k] == high && cut.keeps(high, j[k]) && ++at == left) s.tie = j[k];
                         }
-                        left -= __popc(votes);
+                        const unsigned all_of = __shfl_sync(0xffffffffu, stop, 31);
+                        if (all_of >= left) break;
+                        left -= all_of;
                     }
                 }
             }
@@ -570,81 +673,95 @@ __device__ __forceinline__ void select(const Row<T>& row, const Weigh& w, Shared
     }
 }
 
-// top-k of few, the lower bound of the candidates being known: see above.  True where they were few enough; the first CTA has
-// then written the row's token.
+// y / total for 64-bit integers, rounded once (nearly): both as sums of two fp32 numbers
+__device__ __forceinline__ float share_of(unsigned long long y, unsigned long long total) {
+    const float yh = (float)y, th = (float)total;
+    const float yl = (float)(long long)(y - (unsigned long long)yh), tl = (float)(long long)(total - (unsigned long long)th);
+    const float q = yh / th;
+    return q + ((fmaf(-q, th, yh) + yl) - q * tl) / th;
+}
+
+// The first CTA draws from the items in all CTAs' lists, which hold every item above their last: those that the cut keeps, of
+// them the first top_k, of them the ones before which the weights sum to less than `target` (0: top_p of theirs).
+__device__ __forceinline__ void draw_listed(const Weigh& w, Shared& s, int b, const Gathered& g, float m, const Cut& cut, int top_k, float top_p,
+                                            unsigned long long target_p, float min_p, float u, const SampleArgs& a, int r_out) {
+    const int tid = threadIdx.x, n = (int)g.n;
+    Item it{0.f, 0};
+    unsigned long long y = 0;
+    bool keep = false;
+    if (tid < n) {
+        it = remote_item(&s.list[b][g.mine], g.from);
+        keep = cut.keeps(it.x, it.i);
+        y = keep ? w(it.x) : 0ull;
+        s.joined[tid] = it;
+        s.weight[tid] = y;
+    }
+    __syncthreads();
+    int ahead = 0;
+    unsigned long long before = 0;
+    if (tid < n) {
+#pragma unroll 8
+        for (int k = 0; k < n; ++k) {
+            const Item o = s.joined[k];
+            const unsigned long long z = s.weight[k];
+            const bool first = o.x > it.x || (o.x == it.x && o.i < it.i);
+            ahead += first;
+            before += first ? z : 0ull;
+        }
+    }
+    keep = keep && ahead < top_k;
+    unsigned long long sum;
+    if (target_p == 0 && top_p < 1.f) {
+        block_scan(keep ? y : 0ull, s.scan, sum);
+        target_p = max(ceil_of(top_p, sum), 1ull);
+    }
+    if (target_p > 0) keep = keep && before < target_p;
+    if (min_p > 0.f) {
+        const unsigned long long most = w(m);
+        keep = keep && y >= (min_p >= 1.f ? most : ceil_of(min_p, most));
+    }
+    __syncthreads();                                   // every weight has been read
+    if (tid < n) s.weight[tid] = keep ? y : 0ull;
+    block_scan(keep ? y : 0ull, s.scan, sum);
+    const unsigned long long target = u >= 1.f ? sum - 1 : floor_of(u, sum);
+    if (!keep) return;
+    before = 0;
+#pragma unroll 8
+    for (int k = 0; k < n; ++k) {
+        const unsigned long long z = s.weight[k];
+        before += s.joined[k].i < it.i ? z : 0ull;
+    }
+    if (before <= target && target < before + y) {
+        a.out_tokens[r_out] = it.i;
+        if (a.out_probs) a.out_probs[r_out] = share_of(y, sum);
+    }
+}
+
+// The part's items from `from` on into s.list[b], as far as they fit; how many there are in the cluster.  `own`: the largest of
+// the thread's values in the row, or infinity where it is not known (a thread whose largest lies below has none).
 template <typename T>
-__device__ __forceinline__ bool draw_of_few(const Row<T>& row, const Weigh& w, Shared& s, float m, float bound, float own, int top_k,
-                                            float top_p, float min_p, float u, const SampleArgs& a, int r_out, int& phase) {
-    const int tid = threadIdx.x, b = phase++ & 1;
+__device__ __forceinline__ unsigned collect(const Row<T>& row, Shared& s, float from, float own, int b) {
+    const int tid = threadIdx.x;
     if (tid == 0) s.found[b] = 0;
     __syncthreads();
-    if (own >= bound) {                                // (a thread whose largest value lies below has none)
+    if (own >= from) {
         const int per = row.part / WARPS, end = row.first + (tid >> 5) * per + per;
         for (int p = end - per + (tid & 31) * 4; p < end; p += 128) {
             const float4 v = row.raw(p);
-            const auto look = [&](float x, int j) {
-                x = row.see(x);
-                if (!(x >= bound)) return;
+            const float x[4] = {row.see(v.x), row.see(v.y), row.see(v.z), row.see(v.w)};
+            if (!(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) >= from)) continue;
+            int j[4];
+            row.tokens_of(p, j);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if (!(x[k] >= from) || s.found[b] > CAP) continue;
                 const unsigned n = atomicAdd(&s.found[b], 1u);
-                if (n < CAP) s.list[b][n] = Item{x, j};
-            };
-            look(v.x, p - row.off);
-            look(v.y, p - row.off + 1);
-            look(v.z, p - row.off + 2);
-            look(v.w, p - row.off + 3);
+                if (n < CAP) s.list[b][n] = Item{x[k], j[k]};
+            }
         }
     }
     sync_cluster();
-    const Gathered g(of_all(&s.found[b], row.ctas, 0u), row.rank);
-    const int n = (int)g.n;
-    if (n > CAP || n < top_k) return false;
-    if (row.rank == 0) {
-        Item it{0.f, 0};
-        unsigned long long y = 0;
-        if (tid < n) {
-            it = remote_item(&s.list[b][g.mine], g.from);
-            y = w(it.x);
-            s.joined[tid] = it;
-            s.weight[tid] = y;
-        }
-        __syncthreads();
-        int ahead = 0;
-        unsigned long long before = 0;
-        if (tid < n) {
-#pragma unroll 8
-            for (int k = 0; k < n; ++k) {
-                const Item o = s.joined[k];
-                const unsigned long long z = s.weight[k];
-                const bool first = o.x > it.x || (o.x == it.x && o.i < it.i);
-                ahead += first;
-                before += first ? z : 0ull;
-            }
-        }
-        bool keep = tid < n && ahead < top_k;
-        unsigned long long sum;
-        if (top_p < 1.f) {
-            block_scan(keep ? y : 0ull, s.scan, sum);
-            keep = keep && before < max(ceil_of(top_p, sum), 1ull);
-        }
-        keep = keep && y >= (min_p >= 1.f ? w(m) : ceil_of(min_p, w(m)));
-        __syncthreads();                               // every weight has been read
-        if (tid < n) s.weight[tid] = keep ? y : 0ull;
-        block_scan(keep ? y : 0ull, s.scan, sum);
-        const unsigned long long target = u >= 1.f ? sum - 1 : floor_of(u, sum);
-        if (keep) {
-            before = 0;
-#pragma unroll 8
-            for (int k = 0; k < n; ++k) {
-                const unsigned long long z = s.weight[k];
-                before += s.joined[k].i < it.i ? z : 0ull;
-            }
-            if (before <= target && target < before + y) {
-                a.out_tokens[r_out] = it.i;
-                if (a.out_probs) a.out_probs[r_out] = (float)((double)y / (double)sum);
-            }
-        }
-    }
-    return true;
+    return __reduce_add_sync(0xffffffffu, of_all(&s.found[b], row.ctas, 0u));
 }
 
 // key of the j-th largest of the threads' maxima, or less; 0 where there are fewer
@@ -686,7 +803,7 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const SampleArgs a) 
     const int top_k = a.top_k ? a.top_k[r] : 0;
     const float top_p = a.top_p ? a.top_p[r] : 1.f, min_p = a.min_p ? a.min_p[r] : 0.f, u = a.uniform[r];
     const T* src = (const T*)a.logits + (int64_t)r * a.stride;
-    Row<T> row{src, a.vocab, (int)((uintptr_t)src / sizeof(T) & 3), a.part, rank * a.part, ctas, rank, false, false, 0.f, 1.f};
+    Row<T> row{src, a.vocab, (int)((uintptr_t)src / sizeof(T) & 3), a.part, rank * a.part, ctas, rank, nullptr, nullptr, false, false, 0.f, 1.f};
 
     // the largest value and its first token (a NaN is never larger)
     float own = -INFINITY;                             // of this thread's values
@@ -725,10 +842,12 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const SampleArgs a) 
         }
     }
     const bool greedy = !(temperature >= 1.1754944e-38f), cuts = top_k > 0 && top_k < a.vocab;
-    const bool few = cuts && top_k <= MOST_K && !greedy;
+    // (a share of the threads' maxima bounds the k-th value while it is not all of them)
+    const int share = (top_k + ctas - 1) / ctas;
+    const bool few = cuts && share <= THREADS - THREADS / 8 && !greedy;
     if (few) {
         __syncthreads();
-        const unsigned k = jth_largest(s, own, (top_k + ctas - 1) / ctas);
+        const unsigned k = jth_largest(s, own, share);
         if (tid == 0) s.bound = k;
     }
     sync_cluster();
@@ -770,46 +889,111 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const SampleArgs a) 
         w.base = 18 + top8 + (MAGIC_BITS >> 8);
         w.lowest = fmaxf((top8 - 44.5f) / t, -3.402823466e38f);
     }
-    Cut cut{-INFINITY, -1};
+    Cut cut{-INFINITY, -0x7fffffff - 1};               // (-inf, where there is no token among others, is not kept)
     int phase = 0;
-    if (bound > 0 && draw_of_few(row, w, s, m, row.see(of_key(bound)), own, top_k, top_p, min_p, u, a, r, phase)) {
-        sync_cluster();
-        return;
+    extern __shared__ __align__(16) float lists[];     // [LISTED] values, [LISTED] tokens
+    int* tokens = reinterpret_cast<int*>(lists + LISTED);
+    // where few candidates are left, the buffer they stand in; how many of them top-k keeps; what top-p's weights sum to
+    int listed = -1, first_k = 0x7fffffff;
+    unsigned long long target_p = 0;
+    // after top-p: its window's first step, and a value above the window
+    int window_first = -1;
+    Scale scale{};
+    float below = INFINITY;
+    if (bound > 0) {
+        const float from = row.see(of_key(bound));
+        if (top_k <= MOST_K) {
+            listed = phase++ & 1;
+            if (collect(row, s, from, own, listed) > CAP) listed = -1;
+        }
+        if (listed < 0) {
+            listed = phase++ & 1;
+            if (list_from(row, s, from, lists, tokens, listed) > CAP) listed = -1;
+        }
+        if (listed >= 0) first_k = top_k;
     }
-    if (cuts) {
+    if (listed < 0 && cuts) {
         // As many items as there are threads reach the smallest of the threads' maxima, and below 2^-47 of the largest weight
         // there is none to cut.
         const float range = fminf(fminf(m - low, 47.f * 256.f / w.t), 3.4e38f);
-        select<false>(row, w, s, Window{Scale{}, 0, 0, m, range, -INFINITY, (unsigned long long)top_k}, cut, phase);
+        select<false>(row, w, s, Window{Scale{}, 0, 0, m, range, -INFINITY, (unsigned long long)top_k, 0u}, cut, phase);
     }
-    if (top_p < 1.f) select<true>(row, w, s, nucleus(row, w, s, m, top_p, cut, phase), cut, phase);
+    if (listed < 0 && top_p < 1.f) {
+        const Window win = nucleus(row, w, s, m, top_p, cut, phase);
+        // (lists that would hardly hold them are not begun)
+        if (win.low > -INFINITY && win.items <= (unsigned)(ctas * LISTED / 4 * 3)) {
+            const int b = phase++ & 1;
+            if ((row.values ? collect(row, s, win.low, INFINITY, b) : list_from(row, s, win.low, lists, tokens, b)) <= CAP) {
+                listed = b;
+                target_p = win.target;
+            }
+        }
+        if (listed < 0) {
+            select<true>(row, w, s, win, cut, phase);
+            window_first = win.first;
+            scale = win.scale;
+            below = win.first > 0 ? win.high + fabsf(m) * 1e-6f : INFINITY;
+        }
+    }
+    if (listed >= 0) {
+        const Gathered g(of_all(&s.found[listed], ctas, 0u), rank);
+        if (rank == 0) draw_listed(w, s, listed, g, m, cut, first_k, top_p, target_p, min_p, u, a, r);
+        sync_cluster();
+        return;
+    }
     const unsigned long long least = min_p >= 1.f ? w(m) : ceil_of(min_p, w(m));
 
     // sums of what is kept, per warp; the warp's part in which they pass u of their sum; the token in it
     float from = cut.x;                                // nothing below is kept
     if (min_p > 0.f) from = fmaxf(from, m + 256.f * (log2f(fminf(min_p, 1.f)) - 0.01f) / w.t - fabsf(m) * 1e-6f);
     const bool all = from == -INFINITY && w.lowest > -3.4e38f;             // (then -inf has no weight by itself)
-    const auto kept = [&](const float* x, int j, unsigned long long* y) {  // false: none of the warp's
+    const auto kept = [&](const float* x, int place, unsigned long long* y) {  // false: none of the warp's
         if (!all && !any_from(x, from)) return false;
 #pragma unroll
         for (int k = 0; k < 4; ++k) y[k] = w(x[k]);
         if (!all) {
+            int j[4];
+            row.tokens_of(place, j);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) y[k] = cut.keeps(x[k], j + k) && y[k] >= least ? y[k] : 0ull;
+            for (int k = 0; k < 4; ++k) y[k] = cut.keeps(x[k], j[k]) && y[k] >= least ? y[k] : 0ull;
+        }
+        return true;
+    };
+    // What lies above top-p's window has been summed by warp (without min-p): only the window's weights are left.
+    const auto kept_of_window = [&](const float* x, int place, unsigned long long* y) {
+        bool in = false;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) in |= x[k] >= from && x[k] <= below;
+        if (!__any_sync(0xffffffffu, in)) return false;
+        int j[4];
+        row.tokens_of(place, j);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int bits = w.bits(x[k]);
+            y[k] = cut.keeps(x[k], j[k]) && scale(bits) >= window_first ? w(x[k], bits) : 0ull;
         }
         return true;
     };
     const auto sum_of = [&](int at, int n) {
         unsigned long long sum = 0;
-        row.each_of(at, n, [&](const float* x, int j) {
+        row.each_of(at, n, [&](const float* x, int place) {
             unsigned long long y[4];
-            if (kept(x, j, y)) sum += (y[0] + y[1]) + (y[2] + y[3]);
+            if (kept(x, place, y)) sum += (y[0] + y[1]) + (y[2] + y[3]);
         });
         return warp_sum64(sum);
     };
-    const int per = a.part / WARPS;
+    const int per = row.part / WARPS;
     {
-        const unsigned long long sum = sum_of(row.first + warp * per, per);
+        unsigned long long sum = 0;
+        if (window_first >= 0 && min_p <= 0.f) {
+            row.each([&](const float* x, int place) {
+                unsigned long long y[4];
+                if (kept_of_window(x, place, y)) sum += (y[0] + y[1]) + (y[2] + y[3]);
+            });
+            sum = warp_sum64(sum) + s.over_warp[warp];
+        } else {
+            sum = sum_of(row.first + warp * per, per);
+        }
         if (lane == 0) s.warp_sum[warp] = sum;
     }
     sync_cluster();
@@ -832,10 +1016,11 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const SampleArgs a) 
         if (before <= target && target < before + mine) {
             for (int p = piece + at; p < piece + at + n; p += 128) {
                 const float4 v = row.raw(p + lane * 4);
-                const int j = p + lane * 4 - row.off;
+                int j[4];
+                row.tokens_of(p + lane * 4, j);
                 const float x[4] = {row.see(v.x), row.see(v.y), row.see(v.z), row.see(v.w)};
                 unsigned long long y[4], sum = 0;
-                if (kept(x, j, y)) sum = (y[0] + y[1]) + (y[2] + y[3]);
+                if (kept(x, p + lane * 4, y)) sum = (y[0] + y[1]) + (y[2] + y[3]);
                 else y[0] = y[1] = y[2] = y[3] = 0ull;
                 const unsigned long long stop = before + warp_scan64(sum);
                 unsigned long long c = stop - sum;
@@ -843,8 +1028,8 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const SampleArgs a) 
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         if (c <= target && target < c + y[k]) {
-                            a.out_tokens[r] = j + k;
-                            if (a.out_probs) a.out_probs[r] = (float)((double)y[k] / (double)total);
+                            a.out_tokens[r] = j[k];
+                            if (a.out_probs) a.out_probs[r] = share_of(y[k], total);
                         }
                         c += y[k];
                     }
@@ -858,9 +1043,13 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const SampleArgs a) 
 }
 
 template <typename T> cudaError_t launch_sample(const SampleArgs& a, int n_rows, cudaStream_t s) {
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t e = smem_limit_once(sample_kernel<T>, LISTED * 8, done);
+    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(n_rows * a.ctas));
     cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = LISTED * 8;
     cfg.stream = s;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
