@@ -61,11 +61,11 @@ __global__ void __launch_bounds__(512) kv8_weights_kernel(const AttnArgs p) {
 // scratch: two pieces for every CTA of the largest launch
 template <typename S> constexpr size_t pieces() { return (size_t)S::CTAS * 2 * S::PIECE; }
 size_t kv8_part_floats(int num_sms) {
-    const size_t sizes[] = {pieces<C4<128>>(), pieces<C8<128>>(), pieces<C16<128>>(), pieces<C32<128>>(),
+    const size_t sizes[] = {pieces<C4<128>>(), pieces<C4S<128>>(), pieces<C8<128>>(), pieces<C16<128>>(), pieces<C32<128>>(),
                             pieces<F4<128>>(), pieces<F8<128>>()};
     return std::max(*std::max_element(std::begin(sizes), std::end(sizes)) * num_sms, kv8_rows_part_floats(num_sms));
 }
-int kv8_most_ctas(int num_sms) { return 3 * num_sms; }
+int kv8_most_ctas(int num_sms) { return 4 * num_sms; }
 
 bool kv8_make_map(const Kv8& c, void* out) {
     cudaDriverEntryPointQueryResult q;
