@@ -4,20 +4,18 @@
 // blocks as cb_kv8_write puts rows there, q goes to its output.  K meets one rounding, from the rotated fp32 value to its code.
 //
 // The angle.  The host gives every pair's frequency as a 64-bit fraction of a turn, so that p times it modulo 2^64 is the phase
-// of any int32 position, exact to the frequency's own rounding: no reduction of a large angle in floating point.  The upper 32
-// bits are taken on.  fp32 rows: the phase less the nearest quarter turn goes to fp32 (an angle within pi / 4, off by 2^-25), and
-// the Taylor series of sine and cosine to x^9 and x^10 are off by at most 2e-9 there; quarter turns exchange the two and change
-// their signs.  bf16 rows: the phase as an angle within pi, and the special-function unit's sine and cosine (sin.approx and
-// cos.approx, within 2^-20.5), whose error is 2^11 times below that of the row's own values, in a third of the instructions (8192
-// rows: 46 us with the series, 36 this way).
+// of any int32 position, exact to the frequency's own rounding: no reduction of a large angle in floating point.  Its upper 32
+// bits less the nearest quarter turn go to fp32 (an angle within pi / 4, off by 2^-25), and the Taylor series of sine and cosine to
+// x^9 and x^10 are off by at most 2e-9 there; quarter turns exchange the two and change their signs.  (The special-function
+// unit's sine and cosine, within 2^-20.5, made 8192 rows 34.0 us instead of 36.4, but moved codes at e4m3's borders.)
 //
 // Work, in one launch: the blocks that get rows of K, those of V, then q.  A block's rows stand in one group of 32 .. 512 threads,
 // as 32 values per thread where there are that many, from the load to the largest value to the code; a decoding step's single
 // rows are a warp each.  A thread of q has one vector of a row in several heads, which share its sines and cosines; the first
 // four are under way while the row's sequence is looked up.
 //
-// 32 heads and 8 KV heads of 128, bf16: 8192 rows 34 us, 80 % of the measured copy rate (bound by HBM, and by the instructions of K and
-// V, which take 15 us of it alone); one row of each of 64 sequences 2.9 us, one launch.
+// 32 heads and 8 KV heads of 128, bf16: 8192 rows 36.4 us, 75 % of the measured copy rate (bound by HBM, and by the instructions of K
+// and V, which alone take 17.7 us); one row of each of 64 sequences 3.1 us, one launch.
 #include <cmath>
 
 #include "cb_kv8_block.cuh"
@@ -71,14 +69,6 @@ __device__ __forceinline__ float2 cos_sin(unsigned phase) {
     const float a = quarter & 1 ? s : c, b = quarter & 1 ? c : s;
     return make_float2((quarter + 1) & 2 ? -a : a, quarter & 2 ? -b : b);
 }
-__device__ __forceinline__ float2 cos_sin_approx(unsigned phase) {
-    const float x = (float)(int)phase * 1.4629180792671596e-9f;
-    float2 r;
-    asm("cos.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(x));
-    asm("sin.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(x));
-    return r;
-}
-
 // a vector's values turned by its pairs' angles at one position
 template <typename T> struct Rotation {
     static constexpr int NP = Vec<T>::N / 2;
@@ -87,7 +77,7 @@ template <typename T> struct Rotation {
 #pragma unroll
         for (int k = 0; k < NP; ++k) {
             const unsigned phase = phase_of(position, turn[k]);
-            cs[k] = sizeof(T) == 2 ? cos_sin_approx(phase) : cos_sin(phase);
+            cs[k] = cos_sin(phase);
         }
     }
     __device__ __forceinline__ void apply(float* f) const {

@@ -5,8 +5,7 @@ Tolerance of a rotated value.  The phase is exact to the float64 frequency's rou
 their product are off by at most 3 * 2^-25 of an angle within pi / 4: 7.0e-8.  The series are evaluated within 2 * 2^-24 and
 truncated by 2e-9; the two products and their sum round three times at most, 3 * 2^-24 of the pair's magnitude.  Together
 less than 3.8e-7, so 2^-21 (|a| + |b|) for positions up to 2^20.  The largest positions add 2 pi 2^-25 = 1.9e-7 here and, in
-the float64 reference, 2^31 * 2^-53 of a radian, 2.4e-7: 2^-20 holds for every position.  In bf16 calls sine and cosine are the special-function
-unit's, within 2^-20.5 = 6.8e-7 of their angle's, instead of the series' 1.3e-7: 9.3e-7 in all, below 2^-20 = 9.5e-7.  A code is right if it lies
+the float64 reference, 2^31 * 2^-53 of a radian, 2.4e-7: 2^-20 holds for every position.  A code is right if it lies
 between the codes of the exact value less and plus that error, a scale if it lies between the scales of such maxima."""
 import numpy as np
 import pytest
@@ -45,7 +44,7 @@ def scale_between(top, err, was, got):
     return max(lo, was) <= got <= max(hi, was)
 
 
-EPS = {"bf16": 2.0 ** -20, "f32": 2.0 ** -21}           # positions up to 2^20
+EPS = {"bf16": 2.0 ** -21, "f32": 2.0 ** -21}           # positions up to 2^20
 
 
 def check_k(c, before, table, lens, k, size, starts, eps, layer=0):
