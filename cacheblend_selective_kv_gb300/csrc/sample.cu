@@ -349,6 +349,8 @@ struct Window {
     float high, range, low;
     unsigned long long target;
     unsigned items;                      // in the window and above it
+    bool listed;                         // the row is the list of the window's items, and what lies above weighs `over`
+    unsigned long long over;
 };
 
 // The window of top-p: weights are summed and items counted by step.  A step's items weigh at least what its lower edge does and
@@ -455,6 +457,64 @@ template <typename T> __device__ __forceinline__ unsigned list_from(Row<T>& row,
     return __reduce_add_sync(0xffffffffu, of_all(&s.found[b], row.ctas, 0u));
 }
 
+// For a wide nucleus: sums the weights above the window, by warp, and lists the window's items, which are few in any case; `use`
+// becomes that list.  False (and `use` as it was) where a warp's piece does not hold its share.
+template <typename T>
+__device__ __forceinline__ bool list_window(const Row<T>& row, Row<T>& use, const Weigh& w, Shared& s, Window& win, const Cut& cut, float* values,
+                                            int* tokens, int b) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, base = warp * PER_WARP;
+    if (threadIdx.x == 0) {
+        s.full = 0;
+        s.over[b] = 0;
+    }
+    __syncthreads();
+    int n = 0;
+    unsigned long long over = 0;
+    row.each([&](const float* x, int place) {
+        if (!any_from(x, win.low)) return;
+        int j[4];
+        bool in[4];
+        row.tokens_of(place, j);
+        int at = n;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int bits = w.bits(x[k]), of_weight = win.scale(bits);
+            const unsigned long long y = w(x[k], bits);
+            const bool keep = cut.keeps(x[k], j[k]);
+            over += keep && of_weight < win.first ? y : 0ull;
+            in[k] = keep && of_weight >= win.first && of_weight <= win.last;
+            const unsigned votes = __ballot_sync(0xffffffffu, in[k]);
+            at += __popc(votes & ((1u << lane) - 1u));
+            n += __popc(votes);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if (in[k] && at < PER_WARP) {
+                values[base + at] = x[k];
+                tokens[base + at] = j[k];
+            }
+            at += in[k];
+        }
+    });
+    for (int i = n + lane; i < PER_WARP; i += 32) values[base + i] = -INFINITY;
+    over = warp_sum64(over);
+    if (lane == 0) {
+        s.over_warp[warp] = over;
+        if (over) add64(&s.over[b], over);
+        if (n > PER_WARP) s.full = 1;
+    }
+    sync_cluster();
+    if (__any_sync(0xffffffffu, of_all(&s.full, row.ctas, 0u))) return false;
+    win.over = total_of_all(&s.over[b], row.ctas);
+    win.listed = true;
+    use.values = values;
+    use.tokens = tokens;
+    use.part = LISTED;
+    use.first = 0;
+    use.special = false;
+    return true;
+}
+
 // Lowers the cut to the first kept item, in descending order, at which the sum of counts (MASS: of weights) reaches the target.
 // All CTAs of the cluster come to the same cut.  `phase` alternates the buffers that others read: one is written again only
 // when all have passed the next barrier of the cluster.
@@ -473,7 +533,7 @@ __device__ __forceinline__ void select(const Row<T>& row, const Weigh& w, Shared
         const auto step = [&](float x, int j, int at) {
             if (!cut.keeps(x, j)) return -1;
             if (level == 0) {
-                if constexpr (MASS) {
+                if (MASS && !win.listed) {
                     if (at < win.first) return -2;
                     if (at > win.last) return -1;
                 }
@@ -503,7 +563,7 @@ __device__ __forceinline__ void select(const Row<T>& row, const Weigh& w, Shared
                     const int bits = w.bits(x[k]);
                     of_weight = win.scale(bits);
                     y = w(x[k], bits);
-                    const bool above_it = level == 0 && of_weight < win.first;
+                    const bool above_it = level == 0 && !win.listed && of_weight < win.first;
                     over += above_it && cut.keeps(x[k], j[k]) ? y : 0ull;
                     if (above_it) continue;
                 }
@@ -520,7 +580,7 @@ __device__ __forceinline__ void select(const Row<T>& row, const Weigh& w, Shared
         if constexpr (MASS) {
             over = warp_sum64(over);
             if (lane == 0 && over) add64(&s.over[b], over);
-            if (lane == 0 && level == 0) s.over_warp[tid >> 5] = over;
+            if (lane == 0 && level == 0 && !win.listed) s.over_warp[tid >> 5] = over;
         }
         if constexpr (MASS) {                          // a step's three words as one
             __syncthreads();
@@ -532,7 +592,7 @@ __device__ __forceinline__ void select(const Row<T>& row, const Weigh& w, Shared
         unsigned long long here = items;
         if constexpr (MASS) {
             here = sum_of_all(&s.mass[b][tid], row.ctas);
-            if (level == 0) above = total_of_all(&s.over[b], row.ctas);
+            if (level == 0) above = win.listed ? win.over : total_of_all(&s.over[b], row.ctas);
         }
         unsigned long long total;
         const unsigned long long upto = above + block_scan(here, s.scan, total);
@@ -893,13 +953,17 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const SampleArgs a) 
     int phase = 0;
     extern __shared__ __align__(16) float lists[];     // [LISTED] values, [LISTED] tokens
     int* tokens = reinterpret_cast<int*>(lists + LISTED);
+    // a value below which min-p keeps nothing
+    const float from_min = min_p > 0.f ? m + 256.f * (log2f(fminf(min_p, 1.f)) - 0.01f) / w.t - fabsf(m) * 1e-6f : -INFINITY;
     // where few candidates are left, the buffer they stand in; how many of them top-k keeps; what top-p's weights sum to
     int listed = -1, first_k = 0x7fffffff;
     unsigned long long target_p = 0;
     // after top-p: its window's first step, and a value above the window
     int window_first = -1;
+    bool window_listed = false;
     Scale scale{};
     float below = INFINITY;
+    Row<T> use = row;                                  // what is left to be looked at of it
     if (bound > 0) {
         const float from = row.see(of_key(bound));
         if (top_k <= MOST_K) {
@@ -916,20 +980,21 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const SampleArgs a) 
         // As many items as there are threads reach the smallest of the threads' maxima, and below 2^-47 of the largest weight
         // there is none to cut.
         const float range = fminf(fminf(m - low, 47.f * 256.f / w.t), 3.4e38f);
-        select<false>(row, w, s, Window{Scale{}, 0, 0, m, range, -INFINITY, (unsigned long long)top_k, 0u}, cut, phase);
+        select<false>(row, w, s, Window{Scale{}, 0, 0, m, range, -INFINITY, (unsigned long long)top_k, 0u, false, 0ull}, cut, phase);
     }
     if (listed < 0 && top_p < 1.f) {
-        const Window win = nucleus(row, w, s, m, top_p, cut, phase);
-        // (lists that would hardly hold them are not begun)
-        if (win.low > -INFINITY && win.items <= (unsigned)(ctas * LISTED / 4 * 3)) {
-            const int b = phase++ & 1;
-            if ((row.values ? collect(row, s, win.low, INFINITY, b) : list_from(row, s, win.low, lists, tokens, b)) <= CAP) {
-                listed = b;
-                target_p = win.target;
-            }
+        use = row;
+        Window win = nucleus(row, w, s, m, top_p, cut, phase);
+        // (of what lies below the window, or below min-p, nothing is kept)
+        if (from_min > win.low || (win.low > -INFINITY && win.items <= CAP)) {
+            listed = phase++ & 1;
+            if (collect(row, s, fmaxf(win.low, from_min), INFINITY, listed) <= CAP) target_p = win.target; else listed = -1;
+        }
+        if (listed < 0 && win.low > -INFINITY && !row.values) {
+            window_listed = list_window(row, use, w, s, win, cut, lists, tokens, phase++ & 1);
         }
         if (listed < 0) {
-            select<true>(row, w, s, win, cut, phase);
+            select<true>(use, w, s, win, cut, phase);
             window_first = win.first;
             scale = win.scale;
             below = win.first > 0 ? win.high + fabsf(m) * 1e-6f : INFINITY;
@@ -944,8 +1009,7 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const SampleArgs a) 
     const unsigned long long least = min_p >= 1.f ? w(m) : ceil_of(min_p, w(m));
 
     // sums of what is kept, per warp; the warp's part in which they pass u of their sum; the token in it
-    float from = cut.x;                                // nothing below is kept
-    if (min_p > 0.f) from = fmaxf(from, m + 256.f * (log2f(fminf(min_p, 1.f)) - 0.01f) / w.t - fabsf(m) * 1e-6f);
+    const float from = fmaxf(cut.x, from_min);         // nothing below is kept
     const bool all = from == -INFINITY && w.lowest > -3.4e38f;             // (then -inf has no weight by itself)
     const auto kept = [&](const float* x, int place, unsigned long long* y) {  // false: none of the warp's
         if (!all && !any_from(x, from)) return false;
@@ -985,7 +1049,16 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const SampleArgs a) 
     const int per = row.part / WARPS;
     {
         unsigned long long sum = 0;
-        if (window_first >= 0 && min_p <= 0.f) {
+        if (window_listed && min_p <= 0.f) {
+            use.each([&](const float* x, int place) {
+                if (!any_from(x, from)) return;
+                int j[4];
+                use.tokens_of(place, j);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) sum += cut.keeps(x[k], j[k]) ? w(x[k]) : 0ull;
+            });
+            sum = warp_sum64(sum) + s.over_warp[warp];
+        } else if (window_first >= 0 && min_p <= 0.f) {
             row.each([&](const float* x, int place) {
                 unsigned long long y[4];
                 if (kept_of_window(x, place, y)) sum += (y[0] + y[1]) + (y[2] + y[3]);
@@ -1093,8 +1166,9 @@ extern "C" cb_status cb_sample(const void* logits, int32_t dtype, int32_t n_rows
         cudaGetLastError();
         return fail(CB_ERR_CUDA, "cb_sample: no CUDA device");
     }
-    // Threads of a row: as many as all rows' find room for at once (two CTAs to an SM), up to a cluster of eight; a CTA more only
-    // for every 4096 tokens.  (A part has less than 2^16 tokens, see the histograms.)
+    // Threads of a row: as many as all rows' find room for at once (two CTAs to an SM, a few of them late), up to a cluster of eight; a
+    // CTA more only for every 4096 tokens (device us of 1 / 64 rows of 128256 without a filter with 2, 4 and 8 CTAs: 20 / 21, 13 / 20,
+    // 10 / 27; 40 rows of mixed settings, six draws: 56 with 4, 44 with 8).  A part has less than 2^16 tokens, see the histograms.
     int ctas = 1;
     while (ctas < MOST_CTAS && (vocab > 60000 * ctas || ((int64_t)n_rows * ctas * 2 <= 2 * sms && vocab > 4096 * ctas))) ctas *= 2;
     const int places = vocab + 3;                      // (a row may begin up to three elements behind a boundary)
