@@ -550,7 +550,7 @@ class KV8Cache:
     @staticmethod
     def shared_cells(n_q: int, n_heads: int, head_dim: int) -> int:
         """weight_cells that an attention_shared call of n_q query rows needs."""
-        return n_q * n_heads * (head_dim + 2)
+        return n_q * n_heads * (2 * head_dim + 6)
 
     # A decoding step calls write and attention once per layer, so the checks below stay within a few microseconds.
     def _int(self, t, name, *shape):

@@ -187,11 +187,11 @@ struct Kv8Prefix {            // prefixes that the batch's sequences share
     Kv8Seqs q;                // a group's prefix as a sequence
     const int* first;         // [groups + 1] first sequence of each group, or NULL: `per_group` each
     int per_group;
-    float* scratch;           // n_q * n_heads * (head_dim + 2) floats
+    float* scratch;           // n_q * n_heads * (2 * head_dim + 6) floats
 };
 cudaError_t launch_kv8_shared(const Kv8& c, const Kv8Prefix& pre, const Kv8Seqs& q, const Kv8Rows& r, const Kv8Attn& a, int layer,
                               cudaStream_t s);
-cudaError_t launch_kv8_few_prefix(const Kv8& c, const void* attn_args, cudaStream_t s);
+cudaError_t launch_kv8_few_prefix(const Kv8& c, void* attn_args, cudaStream_t s);
 cudaError_t launch_kv8_few_own(const Kv8& c, const void* attn_args, cudaStream_t s);
 cudaError_t launch_kv8_few_joint(const Kv8& c, const void* attn_args, cudaStream_t s);
 int kv8_most_ctas(int num_sms);

@@ -105,7 +105,6 @@ constexpr int RING = 8;
 struct Open {                            // an item of which this CTA has a piece
     int u0, pieces;                      // the CTA it begins in, how many have a piece of it
     int row0, cols, g;
-    bool prefix;                         // OWN: its rows have one
 };
 template <int MODE> struct Shared {
     ScaleRing<RING> ring;
@@ -270,11 +269,18 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
         ptx::tmem_relinquish();
     }
 
-    grid_dep_launch();
-    grid_dep_wait();                                     // lengths, tables, queries and the cache of the kernels before
+    // Lengths, tables, queries and the cache are of the kernels before.  BESIDE does not wait for PREFIX, whose CTAs let it start when
+    // they have waited for those kernels and hold their TMEM; the fences keep it from what its SM had read earlier.
+    if (MODE != PREFIX) grid_dep_launch();
+    if constexpr (MODE == BESIDE) {
+        __threadfence();
+        asm volatile("fence.proxy.async.global;" ::: "memory");
+    } else {
+        grid_dep_wait();
+    }
     Piece mine;
     Cursor<MODE> cur;
-    find_piece<THREADS>(p, c.find, mine, cur, [] { ptx::tc_fence_before(); }, [] { ptx::tc_fence_after(); });
+    find_piece<THREADS>(p, c.find, mine, cur, [] { ptx::tc_fence_before(); }, [] { ptx::tc_fence_after(); if (MODE == PREFIX) grid_dep_launch(); });
     const int count = mine.count;                        // tiles of this CTA
     const uint32_t tmem = c.tmem;
 
@@ -541,22 +547,14 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
                 return (T*)p.a.out + (int64_t)(q.r0 + q0 + div_g(p, k)) * p.a.out_stride + (int64_t)(g * p.G + mod_g(p, k)) * HD;
             };
             if (first == 0 && n_here == cur.nt) {
-                if constexpr (MODE == PREFIX) {
+                if constexpr (MODE == PREFIX || MODE == BESIDE) {
 #pragma unroll
                     for (int k = 0; k < NW; ++k) {
                         if (c0 + k >= cols) continue;
                         const int64_t at = prefix_at(p, q.r0 + q0 + div_g(p, c0 + k), g * p.G + mod_g(p, c0 + k));
-                        if (key < HD) p.prefix_sum[at * HD + key] = acc[k];
-                        if (key == 0) p.prefix_stat[at] = make_float2(colm[c0 + k], lsum[k]);
-                    }
-                } else if (MODE == OWN && has_prefix(p, cur.s)) {
-#pragma unroll
-                    for (int k = 0; k < NW; ++k) {
-                        if (c0 + k >= cols) continue;
-                        const int64_t at = prefix_at(p, q.r0 + q0 + div_g(p, c0 + k), g * p.G + mod_g(p, c0 + k));
-                        const Merge merge(colm[c0 + k], lsum[k], p.prefix_stat[at]);
-                        const float inv = 1.f / merge.l;
-                        if (key < HD) out_at(c0 + k)[key] = from_f<T>(merge.l != 0.f ? merge(acc[k], p.prefix_sum[at * HD + key]) * inv : 0.f);
+                        if (key < HD) p.side_sum[at * HD + key] = acc[k];
+                        if (key == 0) p.side_stat[at] = make_float2(colm[c0 + k], lsum[k]);
+                        if (MODE == PREFIX && p.pieces_of && key == 0) p.pieces_of[at] = make_int2(0, 0);
                     }
                 } else {
 #pragma unroll
@@ -581,8 +579,12 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
                     for (int k = 0; k < NW; ++k)
                         *reinterpret_cast<float2*>(piece + NC * HD + 2 * (c0 + k)) = make_float2(colm[c0 + k], lsum[k]);
                 }
-                if (tid == 0) c.open[n_open] = Open{u0, n_pieces, q.r0 + q0, cols, g, MODE == OWN && has_prefix(p, cur.s)};
-                ++n_open;
+                if (MODE == PREFIX && p.pieces_of) {
+                    if (first == 0 && tid < cols) p.pieces_of[prefix_at(p, q.r0 + q0 + div_g(p, tid), g * p.G + mod_g(p, tid))] = place_of_sums(u0, tid, n_pieces);
+                } else {
+                    if (tid == 0) c.open[n_open] = Open{u0, n_pieces, q.r0 + q0, cols, g};
+                    ++n_open;
+                }
             }
             if (i < count) cur = c.next;                         // written before the last barrier, again behind the next
         }
@@ -608,19 +610,13 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
                     const auto at = [&](int u) { return piece_at<S>(p, o.u0, u); };
                     const float4 a = join_pieces<HD, S::JOIN>(at, o.pieces, k * HD, NC * HD + 2 * k, m, l, buf);
                     const int row = o.row0 + div_g(p, k), head = o.g * p.G + mod_g(p, k);
-                    if constexpr (MODE == PREFIX) {
+                    if constexpr (MODE == PREFIX || MODE == BESIDE) {
                         const int64_t at = prefix_at(p, row, head);
-                        if (lane < HD / 4) *reinterpret_cast<float4*>(p.prefix_sum + at * HD + lane * 4) = a;
-                        if (lane == 0) p.prefix_stat[at] = make_float2(m, l);
+                        if (lane < HD / 4) *reinterpret_cast<float4*>(p.side_sum + at * HD + lane * 4) = a;
+                        if (lane == 0) p.side_stat[at] = make_float2(m, l);
                         continue;
                     }
                     T* out = (T*)p.a.out + (int64_t)row * p.a.out_stride + (int64_t)head * HD;
-                    if (MODE == OWN && o.prefix) {
-                        const int64_t at = prefix_at(p, row, head);
-                        const Merge merge(m, l, p.prefix_stat[at]);
-                        if (lane < HD / 4) store4(out + lane * 4, merge(a, *reinterpret_cast<const float4*>(p.prefix_sum + at * HD + lane * 4)), merge.l);
-                        continue;
-                    }
                     if (lane < HD / 4) store4(out + lane * 4, a, l);
                     if (p.scores && lane == 0) p.stats[((int64_t)o.g * p.r.n_rows + o.row0) * p.G + k] = make_float2(m, 1.f / l);
                 }
@@ -633,6 +629,7 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
         ptx::tc_fence_after();
         ptx::tmem_dealloc(tmem, S::TMEM);
     }
+    if (MODE == BESIDE) grid_dep_wait();                 // who waits for this launch waits for PREFIX
 }
 
 template <typename T, typename S, int MODE>
@@ -641,6 +638,7 @@ cudaError_t launch_shape(const Kv8& c, AttnArgs& p, cudaStream_t s) {
     const cudaError_t e = smem_limit_once(kv8_attn_kernel<T, S, MODE>, S::BYTES, done);
     if (e != cudaSuccess) return e;
     p.QT = S::NC / p.G;
+    p.piece_cols = S::NC;
     p.ahead = 2;                         // (64 x 8K decode 102 us with 0, 100 with 1, 98 with 2 and 3)
     p.min_places = 2 + p.ahead;
     if (S::STAGES == 1) {                // items of few tiles: nearly one for each CTA, and whole ones
@@ -649,9 +647,11 @@ cudaError_t launch_shape(const Kv8& c, AttnArgs& p, cudaStream_t s) {
     }
     const int64_t items = ((int64_t)p.r.n_rows / p.QT + p.q.n) * p.Hkv;
     const int64_t tiles = items * ((p.q.max_len + TK - 1) / TK + 1 + (MODE == JOINT ? (p.pre.max_len + TK - 1) / TK : 0));
-    const int64_t most = (int64_t)c.num_sms * S::CTAS;
+    const int64_t most = (int64_t)p.sms * S::CTAS;
     CUtensorMap map;
     memcpy(&map, c.map, sizeof map);
+    if (MODE == PREFIX)
+        return launch_pairs(c.pdl, kv8_attn_kernel<T, S, MODE>, in_pairs((unsigned)(tiles < most ? tiles : most)), S::THREADS, S::BYTES, s, map, p);
     return launch_ex(c.pdl, kv8_attn_kernel<T, S, MODE>, dim3((unsigned)(tiles < most ? tiles : most)), dim3(S::THREADS), S::BYTES, s, map, p);
 }
 
@@ -671,9 +671,9 @@ template <int HD, int MODE> cudaError_t launch_few(const Kv8& c, AttnArgs& p, cu
     const int rows = (p.r.n_rows + p.q.n - 1) / p.q.n, need = rows * p.G;
     if (c.cfg.dtype == CB_BF16) {
         // The own keys of sequences that share a prefix are often a tile or two: one more CTA on an SM, with one tile in flight, shortens
-        // what is a few tiles' latency in a row (64 sequences of up to 256 keys on 8192 shared: 44.7 us in all, 40.9 this way; up to 512
-        // on 4 x 4096: 48.4 and 44.9; but 8 of up to 1000 keys: 119 and 125).
-        if constexpr (MODE == OWN)
+        // what is a few tiles' latency in a row (64 sequences of up to 256 keys on 8192 shared: 37.9 us in all, 32.7 this way; up to 512
+        // on 4 x 4096: 38.9 and 38.6).
+        if constexpr (MODE == BESIDE)
             if (need <= 4 && p.q.max_len <= 4 * TK) return launch_shape<bf16, C4S<HD>, MODE>(c, p, s);
         if (need <= 4) return launch_shape<bf16, C4<HD>, MODE>(c, p, s);
         if (need <= 8) return launch_shape<bf16, C8<HD>, MODE>(c, p, s);

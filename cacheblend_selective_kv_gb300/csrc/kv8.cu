@@ -203,7 +203,8 @@ cb_status cb_kv8_create(const cb_kv8_config* cfg, void* codes, float* scales, cb
         delete h;
         return fail(CB_ERR_CUDA, "cb_kv8_create: no CUDA device");
     }
-    // one allocation: status, voided, arrival counts (zero between calls), pieces, statistics, what is to be joined, scores
+    // one allocation: status, voided, arrival counts (zero between calls), pieces, statistics, what is to be joined, scores (arrival
+    // counts and pieces twice, for two launches at a time)
     const size_t head = 256 + ((size_t)kv8_most_ctas(h->num_sms) * 4 + 255) / 256 * 256;
     const size_t part = (kv8_part_floats(h->num_sms) * 4 + 255) / 256 * 256;
     // a row of a call that returns weights takes at least 129 cells
@@ -390,7 +391,7 @@ cb_status cb_kv8_attention_shared(cb_kv8* c, const cb_kv8_seqs* prefixes, const 
     if (st == CB_OK) st = check_places(*c, n_q, sq, who);
     if (st != CB_OK) return st;
     const bool shared = pre.n > 0 && pre.max_len > 0;
-    const int64_t row = (int64_t)c->cfg.n_heads * (c->cfg.head_dim + 2);
+    const int64_t row = (int64_t)c->cfg.n_heads * (2 * c->cfg.head_dim + 6);
     if (shared && n_q > c->cfg.weight_cells / row)
         return fail(CB_ERR_INVALID_ARG, "%s: %d query rows need %lld cells of scratch, the cache was created with %lld", who, n_q,
                     (long long)(n_q * row), (long long)c->cfg.weight_cells);

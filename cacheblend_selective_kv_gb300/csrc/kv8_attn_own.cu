@@ -6,7 +6,7 @@ namespace cb {
 
 cudaError_t launch_kv8_few_own(const Kv8& c, const void* attn_args, cudaStream_t s) {
     AttnArgs p = *static_cast<const AttnArgs*>(attn_args);
-    return c.cfg.head_dim == 128 ? launch_few<128, OWN>(c, p, s) : launch_few<64, OWN>(c, p, s);
+    return c.cfg.head_dim == 128 ? launch_few<128, BESIDE>(c, p, s) : launch_few<64, BESIDE>(c, p, s);
 }
 
 }  // namespace cb

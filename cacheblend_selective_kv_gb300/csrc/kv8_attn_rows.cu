@@ -178,11 +178,12 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_rows_kernel(const __grid_const
         ptx::tmem_alloc(ptx::smem_u32(&c.tmem), 512);
         ptx::tmem_relinquish();
     }
-    grid_dep_launch();
+    if (MODE != PREFIX) grid_dep_launch();
     grid_dep_wait();
     Piece mine;
     Cursor<MODE> cur;
-    find_piece<THREADS>(p, c.find, mine, cur, [] { ptx::tc_fence_before(); }, [] { ptx::tc_fence_after(); });
+    // (BESIDE starts when all CTAs of PREFIX have waited for the kernels before and hold their TMEM)
+    find_piece<THREADS>(p, c.find, mine, cur, [] { ptx::tc_fence_before(); }, [] { ptx::tc_fence_after(); if (MODE == PREFIX) grid_dep_launch(); });
     const int count = mine.count;
     const uint32_t tmem = c.tmem;                       // S and P: two buffers of 128 columns; O of each half at 256
     constexpr uint32_t O_COL = 256;
@@ -532,7 +533,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_rows_kernel(const __grid_const
             float2 before = make_float2(-INFINITY, 0.f);
             const bool prefix = MODE == OWN && has_prefix(p, cur.s);
             const int64_t pre_at = MODE == PLAIN ? 0 : prefix_at(p, q.r0 + q0 + div_g(p, row), g * p.G + mod_g(p, row));
-            if (MODE == OWN && prefix && whole && row < cols) before = p.prefix_stat[pre_at];
+            if (MODE == OWN && prefix && whole && row < cols) before = p.side_stat[pre_at];
             const Merge merge(X, L, before);                     // (unused but by OWN)
             const float inv = 1.f / (MODE == OWN ? merge.l : L);
             // this thread's half of the row's dims
@@ -552,11 +553,11 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_rows_kernel(const __grid_const
                 }
                 if (row < cols) {
                     if (MODE == PREFIX && whole) {
-                        float4* o = reinterpret_cast<float4*>(p.prefix_sum + pre_at * HD + d);
+                        float4* o = reinterpret_cast<float4*>(p.side_sum + pre_at * HD + d);
 #pragma unroll
                         for (int y = 0; y < 4; ++y) o[y] = make_float4(a0[4 * y], a0[4 * y + 1], a0[4 * y + 2], a0[4 * y + 3]);
                     } else if (MODE == OWN && whole) {
-                        const float4* b = reinterpret_cast<const float4*>(p.prefix_sum + pre_at * HD + d);
+                        const float4* b = reinterpret_cast<const float4*>(p.side_sum + pre_at * HD + d);
 #pragma unroll
                         for (int y = 0; y < 4; ++y) {
                             const float4 x = prefix ? b[y] : make_float4(0.f, 0.f, 0.f, 0.f);
@@ -591,12 +592,16 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_rows_kernel(const __grid_const
             if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&c.o_free));
             if (whole) {
                 if (SCORES && hf == 0 && row < cols) p.stats[stat0 + row] = make_float2(X, inv);
-                if (MODE == PREFIX && hf == 0 && row < cols) p.prefix_stat[pre_at] = make_float2(X, L);
+                if (MODE == PREFIX && hf == 0 && row < cols) {
+                    p.side_stat[pre_at] = make_float2(X, L);
+                    if (p.pieces_of) p.pieces_of[pre_at] = make_int2(0, 0);
+                }
                 ptx::named_bar_sync(3 + quarter, 64);            // `halves` has been read
             } else {
                 if (hf == 0 && row < cols)
                     *reinterpret_cast<float2*>(piece_at(blockIdx.x - u0) + ROWS * HD + 2 * row) = make_float2(X, L);
                 // (the CTA in which the item begins says so to the joining kernel)
+                if (MODE == PREFIX && p.pieces_of && first == 0 && hf == 0 && row < cols) p.pieces_of[pre_at] = place_of_sums(u0, row, n_pieces);
                 if (first == 0 && tid == 0) todo = Todo{q.r0 + q0, cols, g | (prefix ? HAS_PREFIX : 0), n_pieces};
                 ptx::named_bar_sync(3 + quarter, 64);            // `halves` has been read
             }
@@ -630,14 +635,14 @@ __global__ void __launch_bounds__(256) kv8_join_kernel(const AttnArgs p) {
     bf16* out = (bf16*)p.a.out + (int64_t)row * p.a.out_stride + (int64_t)head * HD;
     if constexpr (MODE == PREFIX) {
         const int64_t at = prefix_at(p, row, head);
-        if (lane < HD / 4) *reinterpret_cast<float4*>(p.prefix_sum + at * HD + lane * 4) = a;
-        if (lane == 0) p.prefix_stat[at] = make_float2(m, l);
+        if (lane < HD / 4) *reinterpret_cast<float4*>(p.side_sum + at * HD + lane * 4) = a;
+        if (lane == 0) p.side_stat[at] = make_float2(m, l);
         return;
     }
     if (MODE == OWN && (d.g & HAS_PREFIX)) {
         const int64_t at = prefix_at(p, row, head);
-        const Merge merge(m, l, p.prefix_stat[at]);
-        if (lane < HD / 4) store4(out + lane * 4, merge(a, *reinterpret_cast<const float4*>(p.prefix_sum + at * HD + lane * 4)), merge.l);
+        const Merge merge(m, l, p.side_stat[at]);
+        if (lane < HD / 4) store4(out + lane * 4, merge(a, *reinterpret_cast<const float4*>(p.side_sum + at * HD + lane * 4)), merge.l);
         return;
     }
     if (lane < HD / 4) store4(out + lane * 4, a, l);
@@ -689,9 +694,10 @@ template <int HD, bool SCORES, int MODE> cudaError_t launch_dim(const Kv8& c, At
     const int64_t tiles = items * ((p.q.max_len + TK - 1) / TK + 1 + (MODE == JOINT ? (p.pre.max_len + TK - 1) / TK : 0));
     CUtensorMap map;
     memcpy(&map, c.map, sizeof map);
-    const unsigned ctas = (unsigned)(tiles < c.num_sms ? tiles : c.num_sms);
-    cudaError_t err = launch_ex(c.pdl, kv8_rows_kernel<HD, SCORES, MODE>, dim3(ctas), dim3(THREADS), Rows<HD>::BYTES, s, map, p);
-    if (err == cudaSuccess) err = launch_ex(c.pdl, kv8_join_kernel<HD, MODE>, dim3(ctas, ROWS / 8), dim3(256), 0, s, p);
+    const unsigned most = (unsigned)(tiles < p.sms ? tiles : p.sms), ctas = MODE == PREFIX ? in_pairs(most) : most;
+    cudaError_t err = MODE == PREFIX ? launch_pairs(c.pdl, kv8_rows_kernel<HD, SCORES, MODE>, ctas, THREADS, Rows<HD>::BYTES, s, map, p)
+                                     : launch_ex(c.pdl, kv8_rows_kernel<HD, SCORES, MODE>, dim3(ctas), dim3(THREADS), Rows<HD>::BYTES, s, map, p);
+    if (err == cudaSuccess && !p.pieces_of) err = launch_ex(c.pdl, kv8_join_kernel<HD, MODE>, dim3(ctas, ROWS / 8), dim3(256), 0, s, p);
     if (err == cudaSuccess && SCORES)
         err = launch_ex(c.pdl, kv8_rows_weights_kernel, dim3((p.q.max_len + 31) / 32, p.Hkv, p.q.n), dim3(256), 0, s, p);
     return err;

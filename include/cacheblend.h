@@ -307,7 +307,7 @@ typedef struct {
     int64_t n_pages;         /* n_pages * page_size * n_kv_heads < 2^31 */
     int64_t weight_cells;    /* floats of scratch (0: none) for attention calls that return weights: such a call needs
                                 n_q * n_heads * (max_len rounded up to 128, plus 1); and for cb_kv8_attention_shared:
-                                n_q * n_heads * (head_dim + 2) */
+                                n_q * n_heads * (2 * head_dim + 6) */
 } cb_kv8_config;
 
 /* A batch of sequences: row j of sequence s is row j % page_size of page table[s * table_ld + j / page_size].  All
@@ -415,7 +415,7 @@ cb_status cb_kv8_attention(cb_kv8* cache, const cb_kv8_seqs* seqs, int32_t layer
  * Precision, NaN and bad page ids: as for cb_kv8_attention, the kernels being chosen by the rows of a group, on average, and of a
  * sequence.  A prefix whose length is out of range has no rows; group or row offsets that decrease or are out of range
  * compute nothing at all; either is recorded as CB_STATUS_BAD_ROW.  No weights are returned.
- * Needs weight_cells >= n_q * n_heads * (head_dim + 2), and cb_kv8_attention's limits for the prefixes too.
+ * Needs weight_cells >= n_q * n_heads * (2 * head_dim + 6), and cb_kv8_attention's limits for the prefixes too.
  * Every sum runs in a fixed order: the same call gives the same bits.  Async on `stream`; no allocation. */
 cb_status cb_kv8_attention_shared(cb_kv8* cache, const cb_kv8_seqs* prefixes, const int32_t* prefix_start,
                                   const cb_kv8_seqs* seqs, int32_t layer, const void* q, int64_t q_stride,

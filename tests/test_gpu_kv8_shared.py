@@ -38,7 +38,7 @@ class Shared(Case):
 
     def __init__(self, cb, prefixes, lens, first, rows, **kw):
         n_q = sum(rows) + 5
-        cells = n_q * kw.get("H", 2) * kw.get("G", 2) * (kw.get("hd", 64) + 2)
+        cells = cb.KV8Cache.shared_cells(n_q, kw.get("H", 2) * kw.get("G", 2), kw.get("hd", 64))
         super().__init__(cb, list(prefixes) + list(lens), cells=cells, **kw)
         self.n_pre, self.own, self.first, self.rows = len(prefixes), list(lens), list(first), list(rows)
         self.pre_table, self.pre_lens = self.table[:self.n_pre].contiguous(), i32(prefixes)
@@ -257,6 +257,66 @@ def test_shared_graph_follows_lengths(cb):
         torch.cuda.synchronize()
         c.check(out, q64)
         c.cache.attention(c.own_table, c.own_lens, q, q_start=start)
+    c.done()
+
+
+def test_shared_after_calls_of_other_sizes(cb):
+    """What an earlier call of other sizes left in the cache's scratch does not reach a result (here 27 tiles of the prefix, whose items
+    span CTAs, after calls with more)."""
+    lens, rows = [19, 178, 167, 9, 176, 140, 127], [29, 19, 32, 1, 8, 14, 29]
+    c = Shared(cb, [256], [max(a, b) for a, b in zip(lens, rows)], [0, 7], rows, H=3, G=2, hd=128, P=64, seed=21)
+    q, q64 = c.values(c.n_q, 6, 128)
+    for _ in range(2):
+        c.check(c.run(q), q64)
+        c.cache.attention(c.own_table, c.own_lens, q, q_start=i32(c.start))
+        c.cache.attention(c.table[:1], i32([256]), q)
+        c.cache.attention_shared(c.pre_table, i32([200]), c.own_table, c.own_lens, q, prefix_start=i32([2, 5]), q_start=i32(c.start))
+    c.done()
+
+
+def test_shared_right_behind_what_it_reads(cb):
+    """Captured steps without a wait between them, each of which lengthens the sequences, appends their rows and attends at once: the
+    same bits as when every call is waited for.  (The launch over the own keys starts before the launch over the prefix ends.)"""
+    n, steps, P = 64, 10, 64
+    c = Shared(cb, [1500, 700], [130 + s for s in range(n)], [0, 40, n], [1] * n, H=4, G=4, hd=128, P=P, seed=12, spare=64)
+    kv = [c.values(n, 4, 128)[0] for _ in range(2 * steps)]
+    qs = [c.values(n, 16, 128)[0] for _ in range(steps)]
+    first, most = i32(c.first), 130 + n + steps
+    codes, scales, lens = c.codes.clone(), c.scales.clone(), c.own_lens.clone()
+    outs = [torch.zeros_like(x) for x in qs]
+    side = torch.cuda.Stream()
+
+    def step(i, wait):
+        c.own_lens.add_(1)
+        wait()
+        c.cache.append(c.own_table, c.own_lens, None, kv[2 * i], kv[2 * i + 1], 1e4, max_len=most, stream=side)
+        wait()
+        c.cache.attention_shared(c.pre_table, c.pre_lens, c.own_table, c.own_lens, qs[i], outs[i], prefix_start=first, max_len=most, stream=side)
+        wait()
+
+    def back():
+        for a, b in ((c.codes, codes), (c.scales, scales), (c.own_lens, lens)):
+            a.copy_(b)
+        torch.cuda.synchronize()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        for i in range(steps):
+            step(i, side.synchronize)
+    want = [o.clone() for o in outs]
+    back()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        for i in range(steps):
+            step(i, lambda: None)
+    for _ in range(5):
+        back()
+        for o in outs:
+            o.fill_(9.0)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, want))
+    assert c.cache.status() == 0
     c.done()
 
 

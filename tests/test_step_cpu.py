@@ -54,7 +54,7 @@ def test_append_refusals(lib):
 
 
 def test_shared_attention_refusals(lib):
-    h = fake(weight_cells=5 * 8 * 66)                  # rows of 8 heads of 64: five of them
+    h = fake(weight_cells=5 * 8 * 134)                 # rows of 8 heads of 64: five of them
 
     def call(pre=None, first=A, sq=None, layer=3, q=A, qs=512, start=A, nq=5, scale=0.125, out=3 * A, os=512, handle=h):
         return lib.cb_kv8_attention_shared(ctypes.addressof(handle) if handle else None, pre or seqs(n=2), first, sq or seqs(), layer, q, qs,
