@@ -36,8 +36,11 @@ constexpr int BINS = THREADS;            // a thread per bin where they are summ
 constexpr int CAP = 256;                 // items that are compared each with each
 constexpr int MOST_K = 128;              // top-k up to which there are few candidates
 constexpr int LISTED = 8192, PER_WARP = LISTED / WARPS;          // candidates that a CTA, and a warp of it, may list
+constexpr int WAITING = 160;             // of a warp's, how many may wait to be looked at: less than 32, and four for each lane
+constexpr int DYNAMIC = (LISTED + WARPS * WAITING) * 6;          // values, and places in the part
 constexpr int MOST_CTAS = 8;
-static_assert(CB_SAMPLE_MAX_VOCAB <= 60000 * MOST_CTAS, "the largest vocabulary");
+constexpr int MOST_PART = 65536;         // places of a CTA: 16 bits in its list, and see the histograms
+static_assert(CB_SAMPLE_MAX_VOCAB + 3 <= MOST_PART * MOST_CTAS && MOST_PART % (4 * THREADS) == 0, "the largest vocabulary");
 constexpr float MAGIC = 12582912.f;      // 1.5 * 2^23: adding it rounds to a whole number
 constexpr int MAGIC_BITS = 0x4B400000;
 
@@ -242,9 +245,10 @@ template <typename T> struct Row {
     const T* x;                          // token 0
     int vocab, off;
     int part, first, ctas, rank;         // places of this CTA: first .. first + part - 1
+    int start;                           // token of its first place
     // or the part's candidates in the tokens' order, when they have been listed: places are those of the list
     const float* values;
-    const int* tokens;
+    const unsigned short* places;        // from the part's first place on
     // Rows whose values stand for others.  Infinities share all the weight: they become 0, all others -inf.  At low temperatures
     // values are taken less the largest (what has weight lies so near to it that the difference is exact), and at the very
     // lowest times 2^32, so that 1 / T stays within fp32.
@@ -261,12 +265,12 @@ template <typename T> struct Row {
         return make_float4(one(j), one(j + 1), one(j + 2), one(j + 3));
     }
     __device__ __forceinline__ void tokens_of(int place, int* j) const {
-        if (tokens) {
-            const int4 v = *reinterpret_cast<const int4*>(tokens + place);
-            j[0] = v.x;
-            j[1] = v.y;
-            j[2] = v.z;
-            j[3] = v.w;
+        if (places) {
+            const uint2 v = *reinterpret_cast<const uint2*>(places + place);
+            j[0] = start + (v.x & 0xffffu);
+            j[1] = start + (v.x >> 16);
+            j[2] = start + (v.y & 0xffffu);
+            j[3] = start + (v.y >> 16);
         } else {
 #pragma unroll
             for (int k = 0; k < 4; ++k) j[k] = place - off + k;
@@ -374,19 +378,30 @@ __device__ __forceinline__ Window nucleus(const Row<T>& row, const Weigh& w, Sha
     __syncthreads();
     unsigned long long sum = 0;
     const float from = cut.x > -INFINITY ? cut.x : w.lowest;     // (below the lowest there is no weight)
-    row.each([&](const float* x, int place) {
-        if (!any_from(x, from)) return;
-        int j[4];
-        row.tokens_of(place, j);
+    if (cut.x == -INFINITY && w.lowest > -3.4e38f) {             // what is not kept has no weight
+        row.each([&](const float* x, int) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int bits = w.bits(x[k]), at = scale(bits);
-            const unsigned long long y = w(x[k], bits);
-            if (!cut.keeps(x[k], j[k])) continue;
-            sum += y;
-            if (at < BINS - 1) atomicAdd(&s.hist[b][0][at], 1u);
-        }
-    });
+            for (int k = 0; k < 4; ++k) {
+                const int bits = w.bits(x[k]), at = (scale.top - bits) >> scale.shift;
+                sum += w(x[k], bits);
+                if (at < BINS - 1 && x[k] >= w.lowest) atomicAdd(&s.hist[b][0][at], 1u);
+            }
+        });
+    } else {
+        row.each([&](const float* x, int place) {
+            if (!any_from(x, from)) return;
+            int j[4];
+            row.tokens_of(place, j);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int bits = w.bits(x[k]), at = scale(bits);
+                const unsigned long long y = w(x[k], bits);
+                if (!cut.keeps(x[k], j[k])) continue;
+                sum += y;
+                if (at < BINS - 1) atomicAdd(&s.hist[b][0][at], 1u);
+            }
+        });
+    }
     sum = warp_sum64(sum);
     if (lane == 0 && sum) add64(&s.rest[b], sum);
     sync_cluster();
@@ -417,7 +432,7 @@ __device__ __forceinline__ Window nucleus(const Row<T>& row, const Weigh& w, Sha
 // Lists the part's values from `from` on, in the tokens' order, a warp's share in a piece of its own; what is done then reads
 // the list.  The row stays as it is where a warp of the cluster has more of them than its piece holds.  The first CAP of a CTA
 // stand in s.list[b] too; returns how many there are in the cluster (more than CAP: or more than that).
-template <typename T> __device__ __forceinline__ unsigned list_from(Row<T>& row, Shared& s, float from, float* values, int* tokens, int b) {
+template <typename T> __device__ __forceinline__ unsigned list_from(Row<T>& row, Shared& s, float from, float* values, unsigned short* places, int b) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, base = warp * PER_WARP;
     if (threadIdx.x == 0) s.full = s.found[b] = 0;
     __syncthreads();
@@ -436,7 +451,7 @@ template <typename T> __device__ __forceinline__ unsigned list_from(Row<T>& row,
             if (!(x[k] >= from)) continue;
             if (at < PER_WARP) {
                 values[base + at] = x[k];
-                tokens[base + at] = place - row.off + k;
+                places[base + at] = (unsigned short)(place - row.first + k);
             }
             ++at;
             if (s.found[b] <= CAP) {                   // (a look at the count spares the additions behind)
@@ -450,7 +465,7 @@ template <typename T> __device__ __forceinline__ unsigned list_from(Row<T>& row,
     sync_cluster();
     if (__any_sync(0xffffffffu, of_all(&s.full, row.ctas, 0u))) return CAP + 1;
     row.values = values;
-    row.tokens = tokens;
+    row.places = places;
     row.part = LISTED;
     row.first = 0;
     row.special = false;
@@ -461,41 +476,63 @@ template <typename T> __device__ __forceinline__ unsigned list_from(Row<T>& row,
 // becomes that list.  False (and `use` as it was) where a warp's piece does not hold its share.
 template <typename T>
 __device__ __forceinline__ bool list_window(const Row<T>& row, Row<T>& use, const Weigh& w, Shared& s, Window& win, const Cut& cut, float* values,
-                                            int* tokens, int b) {
+                                            unsigned short* places, float* waiting, int b) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, base = warp * PER_WARP;
     if (threadIdx.x == 0) {
         s.full = 0;
         s.over[b] = 0;
     }
     __syncthreads();
-    int n = 0;
+    // What may be kept is brought together first, in the tokens' order, and looked at by whole warps.
+    float* wait = waiting + warp * WAITING;
+    unsigned short* wait_at = places + LISTED + warp * WAITING;
+    int n = 0, waits = 0;
     unsigned long long over = 0;
+    const auto look = [&](int from, int k) {           // at k of them
+        const Item v = lane < k ? Item{wait[from + lane], wait_at[from + lane]} : Item{-INFINITY, 0};
+        const int bits = w.bits(v.x), of_weight = win.scale(bits);
+        const bool keep = lane < k && cut.keeps(v.x, row.start + v.i);
+        if (keep && of_weight < win.first) over += w(v.x, bits);
+        const bool in = keep && of_weight >= win.first && of_weight <= win.last;
+        const unsigned votes = __ballot_sync(0xffffffffu, in);
+        const int at = n + __popc(votes & ((1u << lane) - 1u));
+        if (in && at < PER_WARP) {
+            values[base + at] = v.x;
+            places[base + at] = (unsigned short)v.i;
+        }
+        n += __popc(votes);
+    };
     row.each([&](const float* x, int place) {
         if (!any_from(x, win.low)) return;
-        int j[4];
-        bool in[4];
-        row.tokens_of(place, j);
-        int at = n;
+        int at = waits;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            const int bits = w.bits(x[k]), of_weight = win.scale(bits);
-            const unsigned long long y = w(x[k], bits);
-            const bool keep = cut.keeps(x[k], j[k]);
-            over += keep && of_weight < win.first ? y : 0ull;
-            in[k] = keep && of_weight >= win.first && of_weight <= win.last;
-            const unsigned votes = __ballot_sync(0xffffffffu, in[k]);
+            const unsigned votes = __ballot_sync(0xffffffffu, x[k] >= win.low);
             at += __popc(votes & ((1u << lane) - 1u));
-            n += __popc(votes);
+            waits += __popc(votes);
         }
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            if (in[k] && at < PER_WARP) {
-                values[base + at] = x[k];
-                tokens[base + at] = j[k];
+        for (int k = 0; k < 4; ++k)
+            if (x[k] >= win.low) {
+                wait[at] = x[k];
+                wait_at[at++] = (unsigned short)(place - row.first + k);
             }
-            at += in[k];
+        __syncwarp();
+        if (waits < 32) return;
+        int done = 0;
+#pragma unroll 1
+        for (; waits - done >= 32; done += 32) look(done, 32);
+        waits -= done;
+        const Item last = lane < waits ? Item{wait[done + lane], wait_at[done + lane]} : Item{0.f, 0};
+        __syncwarp();
+        if (lane < waits) {
+            wait[lane] = last.x;
+            wait_at[lane] = (unsigned short)last.i;
         }
+        __syncwarp();
     });
+    if (waits > 0) look(0, waits);
+    __syncwarp();
     for (int i = n + lane; i < PER_WARP; i += 32) values[base + i] = -INFINITY;
     over = warp_sum64(over);
     if (lane == 0) {
@@ -508,7 +545,7 @@ __device__ __forceinline__ bool list_window(const Row<T>& row, Row<T>& use, cons
     win.over = total_of_all(&s.over[b], row.ctas);
     win.listed = true;
     use.values = values;
-    use.tokens = tokens;
+    use.places = places;
     use.part = LISTED;
     use.first = 0;
     use.special = false;
@@ -570,7 +607,7 @@ __device__ __forceinline__ void select(const Row<T>& row, const Weigh& w, Shared
                 const int at = step(x[k], j[k], of_weight);
                 if (at < 0) continue;
                 if (MASS || at < BINS - 1) atomicAdd(&s.hist[b][0][at], 1u);
-                if constexpr (MASS) {              // (a part has less than 2^16 items: no word overflows)
+                if constexpr (MASS) {              // (a part has 2^16 items at most: no word overflows)
                     atomicAdd(&s.hist[b][1][at], (unsigned)y & 0xffffu);
                     atomicAdd(&s.hist[b][2][at], (unsigned)(y >> 16) & 0xffffu);
                     atomicAdd(&s.hist[b][3][at], (unsigned)(y >> 32));
@@ -863,7 +900,7 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const SampleArgs a) 
     const int top_k = a.top_k ? a.top_k[r] : 0;
     const float top_p = a.top_p ? a.top_p[r] : 1.f, min_p = a.min_p ? a.min_p[r] : 0.f, u = a.uniform[r];
     const T* src = (const T*)a.logits + (int64_t)r * a.stride;
-    Row<T> row{src, a.vocab, (int)((uintptr_t)src / sizeof(T) & 3), a.part, rank * a.part, ctas, rank, nullptr, nullptr, false, false, 0.f, 1.f};
+    Row<T> row{src, a.vocab, (int)((uintptr_t)src / sizeof(T) & 3), a.part, rank * a.part, ctas, rank, 0, nullptr, nullptr, false, false, 0.f, 1.f};
 
     // the largest value and its first token (a NaN is never larger)
     float own = -INFINITY;                             // of this thread's values
@@ -951,8 +988,10 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const SampleArgs a) 
     }
     Cut cut{-INFINITY, -0x7fffffff - 1};               // (-inf, where there is no token among others, is not kept)
     int phase = 0;
-    extern __shared__ __align__(16) float lists[];     // [LISTED] values, [LISTED] tokens
-    int* tokens = reinterpret_cast<int*>(lists + LISTED);
+    extern __shared__ __align__(16) float lists[];     // values [LISTED], [WARPS][WAITING]; places [LISTED], [WARPS][WAITING]
+    float* waiting = lists + LISTED;
+    unsigned short* places = reinterpret_cast<unsigned short*>(waiting + WARPS * WAITING);
+    row.start = row.first - row.off;
     // a value below which min-p keeps nothing
     const float from_min = min_p > 0.f ? m + 256.f * (log2f(fminf(min_p, 1.f)) - 0.01f) / w.t - fabsf(m) * 1e-6f : -INFINITY;
     // where few candidates are left, the buffer they stand in; how many of them top-k keeps; what top-p's weights sum to
@@ -972,7 +1011,7 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const SampleArgs a) 
         }
         if (listed < 0) {
             listed = phase++ & 1;
-            if (list_from(row, s, from, lists, tokens, listed) > CAP) listed = -1;
+            if (list_from(row, s, from, lists, places, listed) > CAP) listed = -1;
         }
         if (listed >= 0) first_k = top_k;
     }
@@ -991,7 +1030,7 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const SampleArgs a) 
             if (collect(row, s, fmaxf(win.low, from_min), INFINITY, listed) <= CAP) target_p = win.target; else listed = -1;
         }
         if (listed < 0 && win.low > -INFINITY && !row.values) {
-            window_listed = list_window(row, use, w, s, win, cut, lists, tokens, phase++ & 1);
+            window_listed = list_window(row, use, w, s, win, cut, lists, places, waiting, phase++ & 1);
         }
         if (listed < 0) {
             select<true>(use, w, s, win, cut, phase);
@@ -1117,12 +1156,12 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const SampleArgs a) 
 
 template <typename T> cudaError_t launch_sample(const SampleArgs& a, int n_rows, cudaStream_t s) {
     static std::atomic<uint64_t> done{0};
-    const cudaError_t e = smem_limit_once(sample_kernel<T>, LISTED * 8, done);
+    const cudaError_t e = smem_limit_once(sample_kernel<T>, DYNAMIC, done);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(n_rows * a.ctas));
     cfg.blockDim = dim3(THREADS);
-    cfg.dynamicSmemBytes = LISTED * 8;
+    cfg.dynamicSmemBytes = DYNAMIC;
     cfg.stream = s;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
@@ -1166,12 +1205,14 @@ extern "C" cb_status cb_sample(const void* logits, int32_t dtype, int32_t n_rows
         cudaGetLastError();
         return fail(CB_ERR_CUDA, "cb_sample: no CUDA device");
     }
-    // Threads of a row: as many as all rows' find room for at once (two CTAs to an SM, a few of them late), up to a cluster of eight; a
-    // CTA more only for every 4096 tokens (device us of 1 / 64 rows of 128256 without a filter with 2, 4 and 8 CTAs: 20 / 21, 13 / 20,
-    // 10 / 27; 40 rows of mixed settings, six draws: 56 with 4, 44 with 8).  A part has less than 2^16 tokens, see the histograms.
-    int ctas = 1;
-    while (ctas < MOST_CTAS && (vocab > 60000 * ctas || ((int64_t)n_rows * ctas * 2 <= 2 * sms && vocab > 4096 * ctas))) ctas *= 2;
+    // Threads of a row: as many as all rows' find room for at once (two CTAs to an SM, and fewer the larger the clusters are, which have to
+    // lie together), up to a cluster of eight; a CTA more only for every 4096 tokens.  Device us of 128256 tokens with 2, 4 and 8 CTAs, without
+    // a filter and with top-p: 1 row 22, 14, 10; 24 rows 23, 15, 15 and 66, 44, 40; 38 rows 23, 21, 23 and 64, 48, 52; 64 rows 23, 21, 29 and
+    // 65, 59, 62; 76 rows 23, 32, 36 and 66, 68, 81.
+    const auto room = [&](int c) { return (int64_t)n_rows * c <= 2 * sms - sms * c / 20; };
     const int places = vocab + 3;                      // (a row may begin up to three elements behind a boundary)
+    int ctas = 1;
+    while (ctas < MOST_CTAS && (places > MOST_PART * ctas || (room(2 * ctas) && vocab > 4096 * ctas))) ctas *= 2;
     const int grain = 4 * THREADS, part = ((places + ctas - 1) / ctas + grain - 1) / grain * grain;
     const SampleArgs a{logits, row_stride, vocab, part, ctas, temperature, top_k, top_p, min_p, uniform, out_tokens, out_probs};
     const cudaError_t e = dtype == CB_BF16 ? launch_sample<bf16>(a, n_rows, (cudaStream_t)stream) : launch_sample<float>(a, n_rows, (cudaStream_t)stream);

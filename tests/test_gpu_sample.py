@@ -107,7 +107,7 @@ F32, BF16 = torch.float32, torch.bfloat16
 
 @pytest.mark.parametrize("n,v,dtype", [(7, 1, F32), (9, 2, BF16), (20, 33, F32), (40, 1000, BF16), (30, 4097, F32), (64, 4096, F32), (12, 8200, BF16),
                                        (40, 32000, F32), (24, 50001, BF16), (20, 128256, F32), (2, 128256, BF16), (1, 128256, F32),
-                                       (3, 393216, F32), (80, 20000, F32)])
+                                       (3, 393216, F32), (80, 20000, F32), (76, 131069, F32), (146, 65533, BF16)])
 def test_settings(cb, n, v, dtype):
     """Every row its own settings, each of them off in some rows; clusters of 1 to 8 CTAs, parts of a row that end anywhere."""
     rng = np.random.default_rng(n * 1000 + v)
