@@ -200,20 +200,21 @@ struct Weigh {
     const unsigned* power;
     // 256 x t rounded to a whole number k, as the bits of MAGIC + k
     __device__ __forceinline__ int bits(float x) const { return __float_as_int(fmaf(fmaxf(x, lowest), t, MAGIC)); }
-    __device__ __forceinline__ unsigned long long of_bits(int bits, unsigned mantissa) const {
-        const unsigned long long product = (unsigned long long)power[bits & 255] * mantissa;
-        return product >> (base - (bits >> 8));        // 18 .. 63
-    }
-    __device__ __forceinline__ unsigned long long operator()(float x, int b) const {         // b: its bits
+    // a weight as a product of 2^62 .. 2^63, to be shifted by 18 .. 63
+    __device__ __forceinline__ unsigned long long product(float x, int b) const {            // b: its bits
         x = fmaxf(x, lowest);
         const float r = fmaf(x, rest, fmaf(x, t, -(__int_as_float(b) - MAGIC)));             // in 256ths, |r| <= 1 / 2
         // (2^(r / 256) - 1) 2^31 by the series: (ln 2 / 256)^n / n!
         const float v = fmaf(r, fmaf(r, fmaf(r, 7.1045254f, 7871.7417f), 5814540.f), MAGIC);
-        return of_bits(b, (unsigned)(__float_as_int(v) - MAGIC_BITS) + 0x80000000u);
+        return (unsigned long long)power[b & 255] * ((unsigned)(__float_as_int(v) - MAGIC_BITS) + 0x80000000u);
     }
+    __device__ __forceinline__ unsigned long long operator()(float x, int b) const { return product(x, b) >> (base - (b >> 8)); }
     __device__ __forceinline__ unsigned long long operator()(float x) const { return (*this)(x, bits(x)); }
-    // of the whole number itself, and 0 where it lies below `lowest`
-    __device__ __forceinline__ unsigned long long of_whole(int bits) const { return base - (bits >> 8) < 64 ? of_bits(bits, 0x80000000u) : 0ull; }
+    // a sum of products, in units of 2^48, as a sum of weights
+    __device__ __forceinline__ unsigned long long of_sum(unsigned long long sum, int b) const {
+        const int s = base - (b >> 8) - 48;
+        return s <= 0 ? sum << -s : s < 64 ? sum >> s : 0ull;
+    }
 };
 
 // ceil(f s) and floor(f s) for f in [0, 1) (multiples of 2^-64, as every fp32 from 2^-40 on is)
@@ -339,11 +340,12 @@ __device__ __forceinline__ Item remote_item(const Item* p, int rank) {
     return Item{__uint_as_float(ld_cluster(at)), (int)ld_cluster(at + 4)};
 }
 
-// Steps of weights: 2^shift 256ths of log2 each, from the largest value's down; a value and its weight share the bits they are
-// found by.
+// Steps of weights: 2^shift 256ths of log2 each, from the largest value's down, each within an octave; a value and its weight share
+// the bits they are found by.
 struct Scale {
-    int top, shift;                      // the bits of the largest value
-    __device__ __forceinline__ int operator()(int bits) const { return min((top - bits) >> shift, BINS - 1); }
+    int top, shift;                      // top: the largest value's bits >> shift
+    __device__ __forceinline__ int operator()(int bits) const { return min(top - (bits >> shift), BINS - 1); }
+    __device__ __forceinline__ int lowest_of(int step) const { return (top - step) << shift; }       // bits
 };
 // Where a search begins: the items whose step is first .. last.  It divides them into equal steps from `high` down over `range`;
 // none of them lies below `low`.  What lies above sums to what the search's first level finds, of `target` to be reached.
@@ -357,18 +359,20 @@ struct Window {
     unsigned long long over;
 };
 
-// The window of top-p: weights are summed and items counted by step.  A step's items weigh at least what its lower edge does and
-// at most what its upper edge does, so that the sum must cross within the steps where the sum of the largest possible weights
-// has reached the target and that of the smallest has not.
+// The window of top-p: all weights are summed, and the upper 15 to 16 bits of their products by step, in 32 bits.  A step's weights are
+// known within 2^-14 of themselves that way, and the sum must cross within the steps (mostly one) where the sum of what they are at most has
+// reached the target and that of what they are at least has not.  (With counts of items in place of products a step's weights were known within
+// 4.4 %: half of a row's items could lie in the window, or all below a few heavy ones, 40 rows of mixed settings 65 to 87 us.)
 template <typename T>
 __device__ __forceinline__ Window nucleus(const Row<T>& row, const Weigh& w, Shared& s, float m, float p, const Cut& cut, int& phase) {
     const int tid = threadIdx.x, lane = tid & 31, b = phase++ & 1;
     // weights below (1 - p) / n of the largest sum to less than 1 - p of all
     const float covers = 256.f * fminf(fmaxf(1.f - log2f(fmaxf(1.f - p, 1e-9f) / row.vocab), 1.f), 47.f);
     Window win{};
-    win.scale = Scale{w.bits(m), 0};
-    while ((int)covers >> win.scale.shift >= BINS - 1) ++win.scale.shift;
-    const Scale scale = win.scale;
+    int shift = 0;
+    while ((int)covers >> shift >= BINS - 2) ++shift;
+    const Scale scale{w.bits(m) >> shift, shift};
+    win.scale = scale;
     s.hist[b][0][tid] = 0;
     if (tid == 0) {
         s.rest[b] = 0;
@@ -382,9 +386,10 @@ __device__ __forceinline__ Window nucleus(const Row<T>& row, const Weigh& w, Sha
         row.each([&](const float* x, int) {
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const int bits = w.bits(x[k]), at = (scale.top - bits) >> scale.shift;
-                sum += w(x[k], bits);
-                if (at < BINS - 1 && x[k] >= w.lowest) atomicAdd(&s.hist[b][0][at], 1u);
+                const int bits = w.bits(x[k]), at = scale.top - (bits >> scale.shift);
+                const unsigned long long y = w.product(x[k], bits);
+                sum += y >> (w.base - (bits >> 8));
+                if (at < BINS - 1 && x[k] >= w.lowest) atomicAdd(&s.hist[b][0][at], (unsigned)(y >> 48));
             }
         });
     } else {
@@ -395,10 +400,10 @@ __device__ __forceinline__ Window nucleus(const Row<T>& row, const Weigh& w, Sha
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const int bits = w.bits(x[k]), at = scale(bits);
-                const unsigned long long y = w(x[k], bits);
+                const unsigned long long y = w.product(x[k], bits);
                 if (!cut.keeps(x[k], j[k])) continue;
-                sum += y;
-                if (at < BINS - 1) atomicAdd(&s.hist[b][0][at], 1u);
+                sum += y >> (w.base - (bits >> 8));
+                if (at < BINS - 1) atomicAdd(&s.hist[b][0][at], (unsigned)(y >> 48));
             }
         });
     }
@@ -406,15 +411,15 @@ __device__ __forceinline__ Window nucleus(const Row<T>& row, const Weigh& w, Sha
     if (lane == 0 && sum) add64(&s.rest[b], sum);
     sync_cluster();
     win.target = max(ceil_of(p, total_of_all(&s.rest[b], row.ctas)), 1ull);
-    const unsigned long long n = sum_of_all(&s.hist[b][0][tid], row.ctas);
-    // a value is within half of a 256th of its whole number: a factor of less than 1 + 2^-9
-    unsigned long long most = w.of_whole(scale.top - (tid << scale.shift)), least = w.of_whole(scale.top - ((tid + 1) << scale.shift) + 1);
-    most += (most >> 9) + 1;
-    least -= least >> 8;
-    least = least > 0 ? least - 1 : 0;
+    // of n items at most (a value is within half of a 256th of its whole number: a factor of 1 - 2^-9 or more), each cut off by less than 1
+    const unsigned long long sum_at = sum_of_all(&s.hist[b][0][tid], row.ctas);
+    const int edge = scale.lowest_of(tid);
+    const unsigned least = s.power[edge & 255] >> 17;
+    const unsigned long long n = tid < BINS - 1 ? sum_at / (least - (least >> 9) - 2u) : 0ull;
+    const unsigned long long most = n ? w.of_sum(sum_at + n, edge) + 1 : 0ull, less = w.of_sum(sum_at, edge);
     unsigned long long total;
-    if (block_scan(n * most, s.scan, total) >= win.target) atomicMin(&s.first, tid);
-    if (block_scan(n * least, s.scan, total) >= win.target) atomicMin(&s.last, tid);
+    if (block_scan(most, s.scan, total) >= win.target) atomicMin(&s.first, tid);
+    if (block_scan(less > n ? less - n : 0ull, s.scan, total) >= win.target) atomicMin(&s.last, tid);
     __syncthreads();
     win.first = s.first;
     win.last = s.last;
@@ -422,10 +427,11 @@ __device__ __forceinline__ Window nucleus(const Row<T>& row, const Weigh& w, Sha
     if (tid == win.last) s.above = upto;
     __syncthreads();
     win.items = (unsigned)s.above;
-    const auto value = [&](int k) { return (float)(scale.top - MAGIC_BITS - k) / w.t; };     // about where x t 256 is k below the largest
-    win.high = value((win.first << scale.shift) - 2);
-    win.low = win.last == BINS - 1 ? -INFINITY : value(((win.last + 1) << scale.shift) + 2) - fabsf(m) * 1e-6f;
-    win.range = win.high - value(((win.last + 1) << scale.shift) + 2);
+    const auto value = [&](int bits) { return (float)(bits - MAGIC_BITS) / w.t; };           // about where x t 256 is that whole number
+    const float bottom = value(scale.lowest_of(win.last) - 2);
+    win.high = value(scale.lowest_of(win.first - 1) + 2);
+    win.low = win.last == BINS - 1 ? -INFINITY : bottom - fabsf(m) * 1e-6f;
+    win.range = win.high - bottom;
     return win;
 }
 
