@@ -7,7 +7,8 @@ no fallback: if ``libcacheblend.so`` is missing or cannot be loaded, every call 
 Entry points (same names as the C ABI): ``cb_model_create``, ``cb_model_destroy``,
 ``cb_rerope``, ``cb_blend``, ``cb_blend_gradual``, ``cb_selected_count``, ``cb_last_error``;
 ``BlendModel`` bundles a handle with the device tensors it borrows, ``KV8Cache`` an 8-bit paged K/V cache
-with the operators on it (write, read, attention, evict).
+with the operators on it (write, append, read, attention, attention_shared, evict), and ``cb_sample`` takes the next
+tokens from rows of logits.
 """
 from __future__ import annotations
 
