@@ -60,7 +60,7 @@ struct AttnArgs {
     float* side_sum;                     // [n_q][Hq][HD] of the prefix (BESIDE: of a sequence's own keys)
     float2* side_stat;                   // [n_q][Hq] reference and sum of the exponentials
     int2* pieces_of;                     // PREFIX, beside BESIDE: [n_q][Hq] where a row's sums stand
-    int piece_cols;                      // columns of a piece
+    int piece_cols, piece_ctas;          // columns of a piece, CTAs that have pieces
     const unsigned* prefix_voided;       // OWN: PREFIX has computed nothing
 };
 

@@ -639,6 +639,7 @@ cudaError_t launch_shape(const Kv8& c, AttnArgs& p, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     p.QT = S::NC / p.G;
     p.piece_cols = S::NC;
+    p.piece_ctas = p.sms * S::CTAS;
     p.ahead = 2;                         // (64 x 8K decode 102 us with 0, 100 with 1, 98 with 2 and 3)
     p.min_places = 2 + p.ahead;
     if (S::STAGES == 1) {                // items of few tiles: nearly one for each CTA, and whole ones

@@ -72,7 +72,7 @@ __global__ void __launch_bounds__(32 * JOINERS) kv8_both_kernel(const AttnArgs p
     if (none) return;
 #pragma unroll 1
     for (int k = blockIdx.z * JOINERS + warp; k < q.n * p.G; k += gridDim.z * JOINERS) {
-        const int row = q.r0 + div_g(p, k), head = g * p.G + k - div_g(p, k) * p.G;
+        const int row = q.r0 + k / p.G, head = g * p.G + k % p.G;      // (of a sequence: k may pass what div_g divides)
         const int64_t at = prefix_at(p, row, head);
         const float2 own_stat = p.side_stat[at];
         const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -81,8 +81,9 @@ __global__ void __launch_bounds__(32 * JOINERS) kv8_both_kernel(const AttnArgs p
         float4 sum = zero;
         if (prefix) {
             const int2 in = pre.pieces_of[at];
+            const int u0 = in.x >> 7, r = in.x & 127;
             if (in.y > 0) {
-                const int u0 = in.x >> 7, r = in.x & 127;
+                if (u0 < 0 || r >= cols || in.y > pre.piece_ctas - u0) continue;         // (offsets that have changed since)
                 const auto piece_at = [&](int u) { return pre.part + (int64_t)((u0 + u) * 2 + (u == 0 ? 1 : 0)) * (cols * (HD + 2)); };
                 sum = join_pieces<HD, AT_ONCE>(piece_at, in.y, r * HD, cols * HD + 2 * r, before.x, before.y, buf[warp]);
             } else {
@@ -197,7 +198,7 @@ cudaError_t launch_kv8_shared(const Kv8& c, const Kv8Prefix& pre, const Kv8Seqs&
     int beside = 0;
     if (!many) {
         const double round_ns = of_own.tile_ns / of_own.items * of_own.ctas * c.num_sms * (double)(own_tiles + (of_own.ctas == 4 ? 0 : 2));
-        for (int x = 8; x <= c.num_sms - 16; x += 4) {
+        for (int x = 8; x <= std::max(c.num_sms - 16, 8); x += 4) {
             double rounds = of_own.items / (x * of_own.ctas);
             if (short_items) rounds = std::ceil(rounds);
             double t = 19e3 + std::max(rounds * round_ns, of_pre.tile_ns * (double)pre_tiles * c.num_sms / (c.num_sms - x));
@@ -217,9 +218,10 @@ cudaError_t launch_kv8_shared(const Kv8& c, const Kv8Prefix& pre, const Kv8Seqs&
     p.side_stat = reinterpret_cast<float2*>(pre.scratch + 2 * sums);
     p.voided = c.voided + 16;
     const bool rows = many_rows(c, p);
-    if (rows) p.piece_cols = 128;
+    if (rows) p.piece_cols = 128;                                // (the other kernel sets its own)
     if (!many) {
-        p.sms = c.num_sms - beside;
+        p.sms = std::max(c.num_sms - beside, 2);
+        p.piece_ctas = p.sms;
         own.sms = beside;
         own.part += most_part_floats(c.num_sms);
         own.arrived += most_ctas(c.num_sms);

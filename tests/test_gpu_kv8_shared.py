@@ -260,6 +260,37 @@ def test_shared_graph_follows_lengths(cb):
     c.done()
 
 
+@pytest.mark.parametrize("G,dtype,rows", [(7, "f32", [1950, 3]), (5, "f32", [2700, 1]), (1, "f32", [9, 66000]), (7, "bf16", [1900] + [1] * 500)])
+def test_shared_one_sequence_of_many_rows(cb, G, dtype, rows):
+    """A batch of few rows on average in which one sequence has more columns (rows x heads of a group) than small divisions reach: the
+    results are those of attention over joined pages.  Both lie within 2 (hd + 8) 2^-24 sum |q k| scale of the scores (at most 60 here) and
+    170 2^-24 more of the values' spread, 2^-9 in all, and in bf16 calls within another 2^-8 of the value; a row in another's place
+    differs by the values themselves."""
+    P, pre = 64, 128
+    lens = [max(n, 20) for n in rows]
+    L = max(lens)
+    n_q, width = sum(rows), -(-L // P)
+    rng = np.random.default_rng(G)
+    pages = -(-pre // P) + sum(-(-n // P) for n in lens)
+    codes = torch.from_numpy(rng.integers(0, 112, (1, 2, pages, 1, P, 64)).astype(np.uint8) | (rng.integers(0, 2, (1, 2, pages, 1, P, 64)) * 128).astype(np.uint8)).cuda()
+    scales = torch.full((1, 2, pages, 1), 2.0 ** -7, device="cuda")
+    table = np.zeros((len(lens), width), np.int32)
+    at = -(-pre // P)
+    for s, n in enumerate(lens):
+        table[s, :-(-n // P)] = np.arange(at, at - (-n // P))
+        at += -(-n // P)
+    cache = cb.KV8Cache(codes, scales, n_heads=G, dtype=dtype, weight_cells=cb.KV8Cache.shared_cells(n_q, G, 64))
+    q = torch.from_numpy(rng.normal(size=(n_q, G, 64)).astype(np.float32)).cuda().to(cache.dtype)
+    start, own, t = i32(starts_of(rows, 0)), i32(lens), i32(table)
+    head = i32(np.arange(pre // P)[None])
+    a = cache.attention_shared(head, i32([pre]), t, own, q, torch.zeros_like(q), q_start=start)
+    b = cache.attention(torch.cat((head.expand(len(lens), -1), t), dim=1).contiguous(), own + pre, q, torch.zeros_like(q), q_start=start)
+    torch.cuda.synchronize()
+    assert cache.status() == 0
+    assert (a.float() - b.float()).abs().max() <= (2.0 ** -8 if dtype == "f32" else 2.0 ** -6) * b.float().abs().max()
+    cache.close()
+
+
 def test_shared_after_calls_of_other_sizes(cb):
     """What an earlier call of other sizes left in the cache's scratch does not reach a result (here 27 tiles of the prefix, whose items
     span CTAs, after calls with more)."""
