@@ -265,3 +265,33 @@ def test_append_on_a_stream_of_its_own(cb):
     ref, _, spread, _ = m.attention(c.table_np, c.lens, f64(out), [0, 2, 4], 0, hd ** -0.5)
     assert (np.abs(f64(o) - ref) <= 2.0 ** -8 * np.abs(ref) + 2.0 ** -10 * spread).all()
     c.done()
+
+
+def test_append_refusals(cb):
+    """Tensors of another shape, type or layout, and numbers out of range, are refused before anything is enqueued."""
+    c = Case(cb, [40, 20], H=2, G=2, hd=64, P=16)
+    k, v, q = (c.values(2, h, 64)[0] for h in (2, 2, 4))
+    wide = torch.zeros((2, 2, 128), dtype=k.dtype, device="cuda")
+    before = c.codes.clone()
+
+    def refused(what, *args, **kw):
+        with pytest.raises((ValueError, cb.CacheBlendError), match=what):
+            c.cache.append(c.table, c.lens_t, *args, **{"rope_theta": 1e4, **kw})
+    refused("k must", q, k.float(), v)
+    refused("v must", q, k, v.cpu())
+    refused("k must", q, k[:, :1], v)
+    refused("contiguous", q, wide[:, :, ::2], v)
+    refused("contiguous", q, k, wide[:, :, :64])
+    refused("same number of rows", q, k, v[:1])
+    refused("q must", q[:, :3], k, v)
+    refused("rows", q[:1], k, v)
+    refused("rows", q, k, v, out_q=q[:1].clone())
+    refused("out_q without q", None, k, v, out_q=q)
+    refused("positions", q, k, v, positions=i32([1, 2, 3]))
+    refused("row_start", q, k, v, row_start=i32([0, 2]))
+    refused("theta", q, k, v, rope_theta=0.0)
+    refused("theta", q, k, v, rope_theta=float("nan"))
+    refused("layer", q, k, v, layer=1)
+    torch.cuda.synchronize()
+    assert torch.equal(c.codes, before)
+    c.done()
