@@ -7,15 +7,18 @@
 // of any int32 position, exact to the frequency's own rounding: no reduction of a large angle in floating point.  Its upper 32
 // bits less the nearest quarter turn go to fp32 (an angle within pi / 4, off by 2^-25), and the Taylor series of sine and cosine to
 // x^9 and x^10 are off by at most 2e-9 there; quarter turns exchange the two and change their signs.  (The special-function
-// unit's sine and cosine, within 2^-20.5, made 8192 rows 34.0 us instead of 36.4, but moved codes at e4m3's borders.)
+// unit's sine and cosine, within 2^-20.5, made 8192 rows 34.0 us instead of 36.4, but moved codes at e4m3's borders.)  Where even these
+// roundings could decide between two codes, the pair is turned again in 64 bits, so that codes are those of exact rotation (8192 rows: 5 of
+// 8.4 million off by a step, all of them small values, where fp32 alone leaves 10 of any size; 1.6 us).
 //
 // Work, in one launch: the blocks that get rows of K, those of V, then q.  A block's rows stand in one group of 32 .. 512 threads,
 // as 32 values per thread where there are that many, from the load to the largest value to the code; a decoding step's single
 // rows are a warp each.  A thread of q has one vector of a row in several heads, which share its sines and cosines; the first
 // four are under way while the row's sequence is looked up.
 //
-// 32 heads and 8 KV heads of 128, bf16: 8192 rows 36.4 us, 75 % of the measured copy rate (bound by HBM, and by the instructions of K
-// and V, which alone take 17.7 us); one row of each of 64 sequences 3.1 us, one launch.
+// 32 heads and 8 KV heads of 128, bf16: 8192 rows 38.0 us, 71 % of the measured copy rate (bound by HBM, and by the instructions of K
+// and V, which alone take 17.7 us); one row of each of 64 sequences 3.1 us, or 4.1
+// where a pair is turned again, one launch.
 #include <cmath>
 
 #include "cb_kv8_block.cuh"
@@ -26,6 +29,7 @@ namespace {
 
 constexpr int MOST = 512;                // threads of a block's group, at most
 constexpr int QB = 4;                    // heads of q that a thread has under way
+constexpr unsigned NEAR = 5;            // units in the last place of fp32 by which a turned value may be off
 
 struct Turns {
     uint2 of[64];                        // pair i turns by (y 2^32 + x) / 2^64 per position
@@ -122,6 +126,33 @@ __device__ __forceinline__ bool place_of(const Kv8Seqs& q, const Kv8Rows& r, int
     return true;
 }
 
+// The codes of a pair of K turned in 64 bits: for values that fp32 brings so near to the middle between two codes that its roundings
+// decide (one pair of 50000; everything else has the same code either way).
+template <typename T> __device__ __noinline__ uint32_t exact_codes(const T* src, uint2 turn, int position, float inv) {
+    const double x0 = (double)to_f(src[0]), x1 = (double)to_f(src[1]);
+    const unsigned long long phase = (unsigned long long)(long long)position * (((unsigned long long)turn.y << 32) | turn.x);
+    const unsigned long long quarter = (phase + (1ull << 61)) >> 62;
+    const double x = (double)(long long)(phase - (quarter << 62)) * 3.40612158008655e-19, z = x * x;      // 2 pi 2^-64
+    // the series of sine and cosine, to x^11 and x^12: off by at most 1e-11
+    double s = fma(z, -1. / 39916800, 1. / 362880), c = fma(z, 1. / 479001600, -1. / 3628800);
+    s = fma(z, s, -1. / 5040);
+    c = fma(z, c, 1. / 40320);
+    s = fma(z, s, 1. / 120);
+    c = fma(z, c, -1. / 720);
+    s = fma(z, s, -1. / 6);
+    c = fma(z, c, 1. / 24);
+    s = fma(x * z, s, x);
+    c = fma(z, c, -0.5);
+    c = fma(z, c, 1.);
+    const double p = quarter & 1 ? s : c, q = quarter & 1 ? c : s;
+    const double cosine = (quarter + 1) & 2 ? -p : p, sine = quarter & 2 ? -q : q;
+    const auto odd = [](double y) {                    // to odd, so that the rounding to a code is the only one
+        const float f = __double2float_rz(y);
+        return (double)f == y ? f : __uint_as_float(__float_as_uint(f) | 1u);
+    };
+    return kv8_code2(odd((x0 * cosine - x1 * sine) * inv), odd((x0 * sine + x1 * cosine) * inv));
+}
+
 // NV vectors per thread: vector t + i * tpb of the call's rows in the block, tpb / vpr rows apart
 template <typename T, int NV>
 __device__ __forceinline__ void append_kv(const AppendArgs& a, const uint2* turns, int kv, int cta) {
@@ -205,6 +236,8 @@ __device__ __forceinline__ void append_kv(const AppendArgs& a, const uint2* turn
         }
     }
     const float inv = kv8_inverse(sc);
+    unsigned near = 0;                                 // pairs with a value that fp32 does not decide
+    static_assert(NV * VN / 2 <= 32, "a bit for every pair");
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int row = row0 + i * rows;
@@ -215,9 +248,26 @@ __device__ __forceinline__ void append_kv(const AppendArgs& a, const uint2* turn
 #pragma unroll
         for (int k = 0; k < VN / 4; ++k)
             w[k] = kv8_code2(f[i][4 * k], f[i][4 * k + 1]) | (kv8_code2(f[i][4 * k + 2], f[i][4 * k + 3]) << 16);
+        if (kv == 0) {                                 // a code has three bits behind the first: where the rest is near a half
+            unsigned off = ~0u;
+#pragma unroll
+            for (int k = 0; k < VN; ++k) off = min(off, (__float_as_uint(f[i][k]) - (0x80000u - NEAR)) & 0xfffffu);
+            if (off <= 2 * NEAR) {
+#pragma unroll
+                for (int k = 0; k < VN; ++k)
+                    if (((__float_as_uint(f[i][k]) - (0x80000u - NEAR)) & 0xfffffu) <= 2 * NEAR) near |= 1u << (i * (VN / 2) + k / 2);
+            }
+        }
         uint8_t* d = dst + row * a.hd + e;
         if (VN == 8) *reinterpret_cast<uint2*>(d) = make_uint2(w[0], w[VN / 4 - 1]);
         else *reinterpret_cast<uint32_t*>(d) = w[0];
+    }
+#pragma unroll 1
+    for (unsigned left = special ? 0u : near; left; left &= left - 1) {
+        const int at = __ffs(left) - 1, row = row0 + at / (VN / 2) * rows, d = e + at % (VN / 2) * 2, from = b.src_row + row - b.lo;
+        *reinterpret_cast<uint16_t*>(dst + row * a.hd + d) =
+            (uint16_t)exact_codes((const T*)a.src[0] + (int64_t)head * a.hd + d + (int64_t)from * a.kv_stride, turns[d / 2],
+                                  a.positions ? a.positions[from] : b.place + row - b.lo, inv);
     }
     if (b.lo > 0) {                                    // every thread of the group has read the old scale
         if (tpb > 32) asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(tpb) : "memory");

@@ -295,3 +295,30 @@ def test_append_refusals(cb):
     torch.cuda.synchronize()
     assert torch.equal(c.codes, before)
     c.done()
+
+
+def test_append_codes_of_exact_rotation(cb):
+    """Codes are those of the rotation in 64 bits, also next to the middle between two codes.  A value's fp32 error is at most
+    1.7 2^-23 (|a| + |b|) of its pair (sine and cosine within 2^-23.5, a product's and the result's rounding), which is less than the 5
+    units in its last place that are looked at anew where the value is at least 0.8 (|a| + |b|)."""
+    P, H, hd, n = 64, 8, 128, 8192
+    c = Case(cb, [n], H=H, G=1, hd=hd, P=P, seed=31)
+    k = torch.randn((n, H, hd), device="cuda", generator=torch.Generator("cuda").manual_seed(5)).to(c.td)
+    c.cache.append(c.table, c.lens_t, None, k, k, 5e5)
+    torch.cuda.synchronize()
+    i = torch.arange(hd // 2, device="cuda", dtype=torch.float64)
+    angle = torch.arange(n, device="cuda", dtype=torch.float64)[:, None] * 5e5 ** (-2.0 * i / hd)
+    cos, sin = torch.cos(angle)[:, None], torch.sin(angle)[:, None]
+    a, b = k[..., 0::2].double(), k[..., 1::2].double()
+    y = torch.stack((a * cos - b * sin, a * sin + b * cos), dim=-1).flatten(-2)
+    size = (a.abs() + b.abs()).repeat_interleave(2, dim=-1)
+    pages = c.table[0, :n // P].long()
+    scale = c.scales[0, 0, pages].double()                                           # [blocks][H]
+    y = y.view(n // P, P, H, hd) / scale[:, None, :, None]
+    got = c.codes[0, 0, pages].view(torch.float8_e4m3fn).float().double().transpose(1, 2)
+    step = torch.exp2(torch.clamp(torch.floor(torch.log2(y.abs().clamp_min(1e-30))), min=-6) - 3)
+    want = torch.round(y / step) * step                                              # (ties to even)
+    sure = y.abs() >= 0.8 * (size.view_as(y) / scale[:, None, :, None])
+    assert sure.float().mean() > 0.1 and torch.equal(got[sure], want[sure])
+    assert (got != want).sum() < 8.4e6 * 2.0 ** -18                                  # and of the others hardly one
+    c.done()
