@@ -29,7 +29,8 @@ struct Kv8 {
     int* todo;               // attention of many rows: items to be joined, four ints per CTA
     unsigned* arrived;       // attention: pieces finished, one count per CTA (0 between calls)
     unsigned* voided;        // attention: the last call's offsets decrease
-    void* scratch;           // the allocation that holds the seven above
+    unsigned* opened;        // attention over a shared prefix: what its launches read is there (0 between calls)
+    void* scratch;           // the allocation that holds the eight above
     unsigned* also;          // a blend's write and read: the model's status, which gets their bits too (else NULL)
     alignas(64) unsigned char map[128];   // tensor map of the codes
 };

@@ -62,7 +62,22 @@ struct AttnArgs {
     int2* pieces_of;                     // PREFIX, beside BESIDE: [n_q][Hq] where a row's sums stand
     int piece_cols, piece_ctas;          // columns of a piece, CTAs that have pieces
     const unsigned* prefix_voided;       // OWN: PREFIX has computed nothing
+    unsigned* opened;                    // PREFIX, BESIDE: see open_for_beside (NULL: no BESIDE)
 };
+
+// BESIDE starts when all CTAs of PREFIX have let it, and reads what the kernels before PREFIX have written.  That those are complete
+// PREFIX has waited for, which makes their writes visible to PREFIX; a release by one of its threads, before it lets BESIDE start, and an
+// acquire in each CTA of BESIDE, behind which a barrier stands, pass it on.  The launch that joins both sets the word back, so that it is 0
+// when a call's PREFIX starts; a CTA that reads 0 waits for all of PREFIX.
+__device__ __forceinline__ void open_for_beside(const AttnArgs& p) {
+    if (p.opened && blockIdx.x == 0 && threadIdx.x == 0) asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(p.opened), "r"(1u) : "memory");
+}
+__device__ __forceinline__ void wait_beside(const AttnArgs& p) {
+    unsigned open = 1u;
+    if (threadIdx.x == 0) asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(open) : "l"(p.opened) : "memory");
+    if (__syncthreads_or(open != 1u)) grid_dep_wait();
+    asm volatile("fence.proxy.async.global;" ::: "memory");      // codes are read by TMA
+}
 
 // k / G and k % G of a column or row of an item
 __device__ __forceinline__ int div_g(const AttnArgs& p, int k) { return (int)(((unsigned)k * p.inv_g) >> 16); }

@@ -240,6 +240,7 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
     unsigned* status = p.q.status;
     volatile int* abort = &c.abort;
     if (ptx::smem_u32(sm) & 1023) {                     // (the swizzled layouts would not hold)
+        grid_dep_wait();                                // to leave lets the next kernel start too
         if (tid == 0) atomicOr(status, ST_WAIT_TIMEOUT);
         return;
     }
@@ -270,14 +271,11 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS)
     }
 
     // Lengths, tables, queries and the cache are of the kernels before.  BESIDE does not wait for PREFIX, whose CTAs let it start when
-    // they have waited for those kernels and hold their TMEM; the fences keep it from what its SM had read earlier.
+    // they have waited for those kernels and hold their TMEM.
     if (MODE != PREFIX) grid_dep_launch();
-    if constexpr (MODE == BESIDE) {
-        __threadfence();
-        asm volatile("fence.proxy.async.global;" ::: "memory");
-    } else {
-        grid_dep_wait();
-    }
+    if constexpr (MODE == BESIDE) wait_beside(p);
+    else grid_dep_wait();
+    if constexpr (MODE == PREFIX) open_for_beside(p);
     Piece mine;
     Cursor<MODE> cur;
     find_piece<THREADS>(p, c.find, mine, cur, [] { ptx::tc_fence_before(); }, [] { ptx::tc_fence_after(); if (MODE == PREFIX) grid_dep_launch(); });

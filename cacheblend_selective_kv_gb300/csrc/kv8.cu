@@ -203,7 +203,7 @@ cb_status cb_kv8_create(const cb_kv8_config* cfg, void* codes, float* scales, cb
         delete h;
         return fail(CB_ERR_CUDA, "cb_kv8_create: no CUDA device");
     }
-    // one allocation: status, voided, arrival counts (zero between calls), pieces, statistics, what is to be joined, scores (arrival
+    // one allocation: status, opened, voided, arrival counts (zero between calls), pieces, statistics, what is to be joined, scores (arrival
     // counts and pieces twice, for two launches at a time)
     const size_t head = 256 + ((size_t)kv8_most_ctas(h->num_sms) * 4 + 255) / 256 * 256;
     const size_t part = (kv8_part_floats(h->num_sms) * 4 + 255) / 256 * 256;
@@ -217,6 +217,7 @@ cb_status cb_kv8_create(const cb_kv8_config* cfg, void* codes, float* scales, cb
     }
     char* at = (char*)h->scratch;
     h->status = (unsigned*)at;
+    h->opened = (unsigned*)(at + 64);
     h->voided = (unsigned*)(at + 128);
     h->arrived = (unsigned*)(at + 256);
     h->part = (float*)(at + head);

@@ -65,6 +65,7 @@ __global__ void __launch_bounds__(32 * JOINERS) kv8_both_kernel(const AttnArgs p
     __shared__ float4 buf[JOINERS][AT_ONCE * 32];
     grid_dep_launch();
     grid_dep_wait();
+    if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x == 0) *p.opened = 0;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = blockIdx.y, cols = pre.piece_cols;
     const unsigned none = *p.voided | *pre.voided;
     const bool prefix = has_prefix(p, blockIdx.x);
@@ -228,6 +229,7 @@ cudaError_t launch_kv8_shared(const Kv8& c, const Kv8Prefix& pre, const Kv8Seqs&
         own.side_sum = p.side_sum + sums;
         own.side_stat = p.side_stat + heads;
         p.pieces_of = reinterpret_cast<int2*>(own.side_stat + heads);
+        p.opened = own.opened = c.opened;
     }
     cudaError_t e = rows ? launch_kv8_rows(c, &p, PREFIX, s) : launch_kv8_few_prefix(c, &p, s);
     if (e != cudaSuccess) return e;
@@ -238,10 +240,13 @@ cudaError_t launch_kv8_shared(const Kv8& c, const Kv8Prefix& pre, const Kv8Seqs&
         return launch_kv8_rows(c, &own, OWN, s);
     }
     e = launch_kv8_few_own(c, &own, s);
-    if (e != cudaSuccess) return e;
     const bool wide = c.cfg.head_dim == 128;
-    if (c.cfg.dtype == CB_F32) return wide ? launch_both<128, float>(c, own, p, s) : launch_both<64, float>(c, own, p, s);
-    return wide ? launch_both<128, bf16>(c, own, p, s) : launch_both<64, bf16>(c, own, p, s);
+    if (e == cudaSuccess) {
+        if (c.cfg.dtype == CB_F32) e = wide ? launch_both<128, float>(c, own, p, s) : launch_both<64, float>(c, own, p, s);
+        else e = wide ? launch_both<128, bf16>(c, own, p, s) : launch_both<64, bf16>(c, own, p, s);
+    }
+    if (e != cudaSuccess) cudaMemsetAsync(c.opened, 0, sizeof(unsigned), s);      // what a later call must not take for its own
+    return e;
 }
 
 }  // namespace cb

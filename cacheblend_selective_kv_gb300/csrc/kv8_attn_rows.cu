@@ -141,6 +141,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_rows_kernel(const __grid_const
     unsigned* status = p.q.status;
     volatile int* abort = &c.abort;
     if (ptx::smem_u32(sm) & 1023) {
+        grid_dep_wait();                                // to leave lets the next kernel start too
         if (tid == 0) atomicOr(status, ST_WAIT_TIMEOUT);
         return;
     }
@@ -180,6 +181,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_rows_kernel(const __grid_const
     }
     if (MODE != PREFIX) grid_dep_launch();
     grid_dep_wait();
+    if constexpr (MODE == PREFIX) open_for_beside(p);
     Piece mine;
     Cursor<MODE> cur;
     // (BESIDE starts when all CTAs of PREFIX have waited for the kernels before and hold their TMEM)
