@@ -32,6 +32,7 @@ struct Kv8 {
     unsigned* opened;        // attention over a shared prefix: what its launches read is there (0 between calls)
     void* scratch;           // the allocation that holds the eight above
     unsigned* also;          // a blend's write and read: the model's status, which gets their bits too (else NULL)
+    double again_ns;         // attention over a shared prefix in one launch: by how much it may be slower (CB_SHARED_AGAIN)
     alignas(64) unsigned char map[128];   // tensor map of the codes
 };
 

@@ -197,6 +197,8 @@ cb_status cb_kv8_create(const cb_kv8_config* cfg, void* codes, float* scales, cb
     while ((1 << h->shift) < c.page_size) ++h->shift;
     const char* pdl = getenv("CB_PDL");
     h->pdl = !(pdl && pdl[0] == '0');
+    const char* again = getenv("CB_SHARED_AGAIN");
+    h->again_ns = again ? atof(again) : 0.0;
     if (cudaGetDevice(&h->device) != cudaSuccess ||
         cudaDeviceGetAttribute(&h->num_sms, cudaDevAttrMultiProcessorCount, h->device) != cudaSuccess) {
         cudaGetLastError();

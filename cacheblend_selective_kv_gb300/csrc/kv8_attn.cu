@@ -3,7 +3,6 @@
 #include <cudaTypedefs.h>
 
 #include <cmath>
-#include <cstdlib>
 #include <iterator>
 
 #include "cb_kv8_few.cuh"
@@ -210,9 +209,8 @@ cudaError_t launch_kv8_shared(const Kv8& c, const Kv8Prefix& pre, const Kv8Seqs&
             }
         }
     }
-    const char* again = getenv("CB_SHARED_AGAIN");               // by how much one launch may be slower
     const int64_t places = ((int64_t)r.n_rows + q.n) * p.Hkv * (pre_tiles + own_tiles + 9);
-    if (one - two <= (again ? atof(again) : 0.) && places < 0x7fffffff)
+    if (one - two <= c.again_ns && places < 0x7fffffff)
         return many ? launch_kv8_rows(c, &own, JOINT, s) : launch_kv8_few_joint(c, &own, s);
     const int64_t heads = (int64_t)r.n_rows * p.Hq, sums = heads * c.cfg.head_dim;
     p.side_sum = pre.scratch;
