@@ -639,9 +639,9 @@ class KV8Cache:
         if k.dtype is not dt or v.dtype is not dt or k.get_device() != dev or v.get_device() != dev or len(shape) != 3 or \
                 shape[1:] != self._kv_row or stride[2] != 1 or (stride[1] != self.head_dim and self.n_kv_heads > 1) or \
                 v.shape != shape or v.stride() != stride:
-            self._kv(k, "k", 1)
-            self._kv(v, "v", 1)
-            raise ValueError("k and v must be [n_rows][n_kv_heads][head_dim] with the same number of rows and the same strides")
+            # (a single row's stride, and a single head's, say nothing)
+            if self._kv(k, "k", 1)[1:] != self._kv(v, "v", 1)[1:] or len(shape) != 3 or v.dim() != 3:
+                raise ValueError("k and v must be [n_rows][n_kv_heads][head_dim] with the same number of rows and the same strides")
         n = shape[0]
         qp, qs, op, os_ = None, 0, None, 0
         if q is not None:
