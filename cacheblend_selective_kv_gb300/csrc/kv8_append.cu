@@ -3,8 +3,8 @@
 // Pair (2i, 2i + 1) of a head turns by the angle p theta^(-2i / hd) of its row's position p; k and v then go into their
 // blocks as cb_kv8_write puts rows there, q goes to its output.  K meets one rounding, from the rotated fp32 value to its code.
 //
-// The angle.  The host gives every pair's frequency as a 64-bit fraction of a turn, so that p times it modulo 2^64 is the phase
-// of any int32 position, exact to the frequency's own rounding: no reduction of a large angle in floating point.  Its upper 32
+// The angle.  The host gives every pair's float64 frequency as a 64-bit fraction of a turn, so that p times it modulo 2^64 is the phase
+// of any int32 position, within 2^-33 turns: no reduction of a large angle in floating point.  Its upper 32
 // bits less the nearest quarter turn go to fp32 (an angle within pi / 4, off by 2^-25), and the Taylor series of sine and cosine to
 // x^9 and x^10 are off by at most 2e-9 there; quarter turns exchange the two and change their signs.  (The special-function
 // unit's sine and cosine, within 2^-20.5, made 8192 rows 34.0 us instead of 36.4, but moved codes at e4m3's borders.)  Where even these
@@ -333,9 +333,13 @@ const Turns& turns_of(double theta, int hd) {
     static thread_local double of_theta = 0.0;
     static thread_local int of_hd = 0;
     if (of_theta != theta || of_hd != hd) {
+        // A frequency M 2^e times 1 / (2 pi), which is (I1 2^64 + I0) 2^-128 (cut off), in integers: all 64 bits are right.
+        constexpr unsigned long long I1 = 0x28be60db9391054aull, I0 = 0x7f09d5f47d4d3770ull;
         for (int i = 0; i < hd / 2; ++i) {
-            const double turn = std::pow(theta, -2.0 * i / hd) / 6.283185307179586477;
-            const unsigned long long of = (unsigned long long)std::ldexp(turn, 64);
+            int e;
+            const unsigned long long M = (unsigned long long)std::ldexp(std::frexp(std::pow(theta, -2.0 * i / hd), &e), 53);
+            const unsigned __int128 P = (unsigned __int128)M * I1 + ((unsigned __int128)M * I0 >> 64);
+            const unsigned long long of = 53 - e < 128 ? (unsigned long long)(P >> (53 - e)) : 0ull;
             turns.of[i] = make_uint2((unsigned)of, (unsigned)(of >> 32));
         }
         of_theta = theta;
