@@ -21,10 +21,10 @@ def layouts(H, n, k, v):
     """Pairs of tensors with the values of k and v whose strides differ where there is one row or one head."""
     hd = k.shape[2]
     if n == 1:
-        wide = torch.zeros((3, 2 * H * hd), dtype=k.dtype, device="cuda")
-        wide[1, :H * hd] = k.flatten()
-        yield wide[1:2, :H * hd].view(1, H, hd), v      # a slice of a projection's row beside a tensor of its own
-        yield v, wide[1:2, :H * hd].view(1, H, hd)
+        wide = torch.zeros((3, 2 * H, hd), dtype=k.dtype, device="cuda")
+        wide[1, :H] = k[0]
+        yield wide[1:2, :H], v                          # a slice of a projection's row beside a tensor of its own
+        yield v, wide[1:2, :H]
     if H == 1:
         yield k.as_strided((n, 1, hd), (hd, 8, 1)), v
         yield k, v.as_strided((n, 1, hd), (hd, 0, 1))
