@@ -81,7 +81,7 @@ __device__ __forceinline__ bool kv8_block(const Kv8Seqs& q, const Kv8Rows& r, in
     return b.page >= 0;
 }
 
-// maximum over the TPB threads of a group (TPB a power of two from 32 to 256)
+// maximum over the TPB threads of a group (TPB a power of two from 32 to 512)
 __device__ __forceinline__ unsigned group_max(unsigned v, int tpb, unsigned* sm) {
     v = __reduce_max_sync(0xffffffffu, v);
     if (tpb == 32) return v;

@@ -4,21 +4,26 @@
 // blocks as cb_kv8_write puts rows there, q goes to its output.  K meets one rounding, from the rotated fp32 value to its code.
 //
 // The angle.  The host gives every pair's float64 frequency as a 64-bit fraction of a turn, so that p times it modulo 2^64 is the phase
-// of any int32 position, within 2^-33 turns: no reduction of a large angle in floating point.  Its upper 32
-// bits less the nearest quarter turn go to fp32 (an angle within pi / 4, off by 2^-25), and the Taylor series of sine and cosine to
-// x^9 and x^10 are off by at most 2e-9 there; quarter turns exchange the two and change their signs.  (The special-function
-// unit's sine and cosine, within 2^-20.5, made 8192 rows 34.0 us instead of 36.4, but moved codes at e4m3's borders.)  Where even these
-// roundings could decide between two codes, the pair is turned again in 64 bits, so that codes are those of exact rotation (8192 rows: 5 of
-// 8.4 million off by a step, all of them small values, where fp32 alone leaves 10 of any size; 1.6 us).
+// of any int32 position, within 2^-33 turns: no reduction of a large angle in floating point.  Its upper 32 bits less the nearest quarter
+// turn go to fp32, an angle within pi / 4, and from there the Taylor series of sine and cosine to x^9 and x^10; quarter turns exchange the
+// two and change their signs.  (The special-function unit's sine and cosine, within 2^-20.5, made 8192 rows 34.0 us instead of 36.4, but
+// moved codes at e4m3's borders.)
+//
+// Codes and scales are those of exact rotation.  Over all 2^32 phases the vector (cosine, sine) is off by at most 1.266e-7, to which the
+// cut to 32 bits adds 1.5e-9 and the farthest positions 0.7e-9; product and sum round by 2^-24 of the pair's length each.  A turned value is
+// then off by less than 2.5e-7 of that length, and the length is at most the sum of the pair's two magnitudes.  Where the values less and
+// plus that much do not have the same code (a pair of about 10 000), or the scales of maxima less and plus it differ, the pairs in question
+// are turned again in 64 bits.  Left out are blocks with NaN, infinities or numbers from 248 * 2^120 on, and with none above 2^-100, whose
+// codes are those of the fp32 values.
 //
 // Work, in one launch: the blocks that get rows of K, those of V, then q.  A block's rows stand in one group of 32 .. 512 threads,
 // as 32 values per thread where there are that many, from the load to the largest value to the code; a decoding step's single
 // rows are a warp each.  A thread of q has one vector of a row in several heads, which share its sines and cosines; the first
 // four are under way while the row's sequence is looked up.
 //
-// 32 heads and 8 KV heads of 128, bf16: 8192 rows 38.0 us, 71 % of the measured copy rate (bound by HBM, and by the instructions of K
-// and V, which alone take 17.7 us); one row of each of 64 sequences 3.1 us, or 4.1
-// where a pair is turned again, one launch.
+// 32 heads and 8 KV heads of 128, bf16: 8192 rows 38.6 us, 70 % of the measured copy rate (bound by HBM, and by the instructions of K
+// and V, which alone take about half of it; in fp32 78.8 us, 66 %); one row of each of 64 sequences 4.3 us, one launch, of whose 33 thousand
+// pairs some are nearly always turned again (3.1 us where none is).
 #include <cmath>
 
 #include "cb_kv8_block.cuh"
@@ -29,7 +34,8 @@ namespace {
 
 constexpr int MOST = 512;                // threads of a block's group, at most
 constexpr int QB = 4;                    // heads of q that a thread has under way
-constexpr unsigned NEAR = 5;            // units in the last place of fp32 by which a turned value may be off
+// How far a turned value may be off, of the sum of its pair's magnitudes: 2.5e-7, and the rounding of value less and plus that.
+constexpr float OFF = 3.2e-7f;
 
 struct Turns {
     uint2 of[64];                        // pair i turns by (y 2^32 + x) / 2^64 per position
@@ -126,15 +132,16 @@ __device__ __forceinline__ bool place_of(const Kv8Seqs& q, const Kv8Rows& r, int
     return true;
 }
 
-// The codes of a pair of K turned in 64 bits: for values that fp32 brings so near to the middle between two codes that its roundings
-// decide (one pair of 50000; everything else has the same code either way).
-template <typename T> __device__ __noinline__ uint32_t exact_codes(const T* src, uint2 turn, int position, float inv) {
+// A pair turned in 64 bits, within 1e-13 of its length (and 2 pi 2^-64 for every position).
+template <typename T> __device__ __noinline__ double2 exact_pair(const T* src, uint2 turn, int position) {
     const double x0 = (double)to_f(src[0]), x1 = (double)to_f(src[1]);
     const unsigned long long phase = (unsigned long long)(long long)position * (((unsigned long long)turn.y << 32) | turn.x);
     const unsigned long long quarter = (phase + (1ull << 61)) >> 62;
     const double x = (double)(long long)(phase - (quarter << 62)) * 3.40612158008655e-19, z = x * x;      // 2 pi 2^-64
-    // the series of sine and cosine, to x^11 and x^12: off by at most 1e-11
-    double s = fma(z, -1. / 39916800, 1. / 362880), c = fma(z, 1. / 479001600, -1. / 3628800);
+    // the series of sine and cosine, to x^13 and x^14: off by at most 3e-14
+    double s = fma(z, 1. / 6227020800, -1. / 39916800), c = fma(z, -1. / 87178291200, 1. / 479001600);
+    s = fma(z, s, 1. / 362880);
+    c = fma(z, c, -1. / 3628800);
     s = fma(z, s, -1. / 5040);
     c = fma(z, c, 1. / 40320);
     s = fma(z, s, 1. / 120);
@@ -146,16 +153,18 @@ template <typename T> __device__ __noinline__ uint32_t exact_codes(const T* src,
     c = fma(z, c, 1.);
     const double p = quarter & 1 ? s : c, q = quarter & 1 ? c : s;
     const double cosine = (quarter + 1) & 2 ? -p : p, sine = quarter & 2 ? -q : q;
-    const auto odd = [](double y) {                    // to odd, so that the rounding to a code is the only one
-        const float f = __double2float_rz(y);
-        return (double)f == y ? f : __uint_as_float(__float_as_uint(f) | 1u);
-    };
-    return kv8_code2(odd((x0 * cosine - x1 * sine) * inv), odd((x0 * sine + x1 * cosine) * inv));
+    return make_double2(x0 * cosine - x1 * sine, x0 * sine + x1 * cosine);
+}
+// rounded to odd, so that the rounding to a code is the only one
+__device__ __forceinline__ float to_odd(double y) {
+    const float f = __double2float_rz(y);
+    return (double)f == y ? f : __uint_as_float(__float_as_uint(f) | 1u);
 }
 
-// NV vectors per thread: vector t + i * tpb of the call's rows in the block, tpb / vpr rows apart
-template <typename T, int NV>
-__device__ __forceinline__ void append_kv(const AppendArgs& a, const uint2* turns, int kv, int cta) {
+// NV vectors per thread: vector t + i * tpb of the call's rows in the block, tpb / vpr rows apart.  KV: 0 for K, 1 for V (code of its own for
+// each: 8192 rows 39.5 us a call, 40.8 with one for both)
+template <typename T, int NV, int KV>
+__device__ __forceinline__ void append_kv(const AppendArgs& a, const uint2* turns, int cta) {
     constexpr int VN = Vec<T>::N;
     __shared__ unsigned sm[MOST / 32];
     const int tpb = 1 << a.tpb_shift, group = threadIdx.x >> a.tpb_shift, t = threadIdx.x & (tpb - 1);
@@ -165,12 +174,12 @@ __device__ __forceinline__ void append_kv(const AppendArgs& a, const uint2* turn
     const int slot = unit / a.Hkv, head = unit - slot * a.Hkv;
     const bool live = unit < a.units && kv8_block(a.q, a.r, a.per_seq, slot, nullptr, b);
     const int row0 = b.lo + (t >> a.vpr_shift), rows = tpb >> a.vpr_shift, e = (t & ((1 << a.vpr_shift) - 1)) * VN;
-    const int64_t blk = ((int64_t)(a.layer * 2 + kv) * a.q.n_pages + b.page) * a.Hkv + head;
+    const int64_t blk = ((int64_t)(a.layer * 2 + KV) * a.q.n_pages + b.page) * a.Hkv + head;
     float f[NV][VN];
     unsigned most = 0;                                 // the largest magnitude's bits, those of an infinity or a NaN among them
     float was = 0.f;
     if (live) {
-        const T* src = (const T*)a.src[kv] + (int64_t)head * a.hd + e;
+        const T* src = (const T*)a.src[KV] + (int64_t)head * a.hd + e;
         if (b.lo > 0) was = a.scales[blk];             // earlier rows of the sequence stay in the block
         uint4 x[NV];
         int position[NV];
@@ -181,7 +190,7 @@ __device__ __forceinline__ void append_kv(const AppendArgs& a, const uint2* turn
             position[i] = 0;
             if (row >= b.hi) continue;
             x[i] = __ldcs(reinterpret_cast<const uint4*>(src + (int64_t)from * a.kv_stride));
-            if (kv == 0) position[i] = a.positions ? a.positions[from] : b.place + row - b.lo;
+            if (KV == 0) position[i] = a.positions ? a.positions[from] : b.place + row - b.lo;
         }
         uint2 turn[VN / 2];
 #pragma unroll
@@ -190,7 +199,7 @@ __device__ __forceinline__ void append_kv(const AppendArgs& a, const uint2* turn
         for (int i = 0; i < NV; ++i) {
             Vec<T>::get(x[i], f[i]);
             if (row0 + i * rows >= b.hi) continue;
-            if (kv == 0) {
+            if (KV == 0) {
                 Rotation<T> turned;
                 turned.set(turn, position[i]);
                 turned.apply(f[i]);
@@ -200,26 +209,53 @@ __device__ __forceinline__ void append_kv(const AppendArgs& a, const uint2* turn
         }
     }
     most = group_max(most, tpb, sm);
+    // pair `at` of this thread's (bits of a mask), turned in 64 bits
+    const auto exact_at = [&](int at) {
+        const int d = e + at % (VN / 2) * 2, from = b.src_row + row0 + at / (VN / 2) * rows - b.lo;
+        return exact_pair((const T*)a.src[0] + (int64_t)head * a.hd + d + (int64_t)from * a.kv_stride, turns[d / 2],
+                          a.positions ? a.positions[from] : b.place + from - b.src_row);
+    };
+    static_assert(NV * VN / 2 <= 32, "a bit for every pair");
     // infinities, NaN, and numbers that would round to a code whose value is not finite, are looked at one by one
     const bool special = most >= Vec<float>::LAST;
-    if (__syncthreads_or(special)) {
-        float top = 0.f;
-        if (live) {
+    // a maximum whose scale fp32 does not decide: all of its values are within 2^-21 of the largest
+    float sc = kv8_scale(__uint_as_float(most));
+    const auto scale_with = [&](float off) { return kv8_scale(__uint_as_float(most) * (1.f + off)); };
+    const bool edge = KV == 0 && !special && scale_with(-0x1p-21f) != scale_with(0x1p-21f);
+    if (__syncthreads_or(special || edge)) {
+        unsigned found = 0;                            // special: the largest finite magnitude; edge: whether the larger scale is needed
+        if (live && special) {
+            float top = 0.f;
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
 #pragma unroll
                 for (int k = 0; k < VN; ++k) {
                     if (row0 + i * rows < b.hi) top = fmaxf(top, kv8_mag(f[i][k]));
-                    if (special) f[i][k] = kv8_storable(f[i][k]);
+                    f[i][k] = kv8_storable(f[i][k]);
                 }
             }
+            found = __float_as_uint(top);
+        } else if (live && edge) {
+            const float border = 448.f * scale_with(-0x1p-21f), from = border * (1.f - 0x1p-20f);
+            unsigned left = 0;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+#pragma unroll
+                for (int k = 0; k < VN; k += 2)
+                    if (row0 + i * rows < b.hi && fmaxf(fabsf(f[i][k]), fabsf(f[i][k + 1])) >= from) left |= 1u << (i * (VN / 2) + k / 2);
+            }
+#pragma unroll 1
+            for (; left; left &= left - 1) {
+                const double2 y = exact_at(__ffs(left) - 1);
+                if (fmax(fabs(y.x), fabs(y.y)) > (double)border) found = 1;
+            }
         }
-        const unsigned finite = group_max(__float_as_uint(top), tpb, sm);
-        if (special) most = finite;
+        found = group_max(found, tpb, sm);
+        if (special) sc = kv8_scale(__uint_as_float(found));
+        else if (edge) sc = scale_with(found ? 0x1p-21f : -0x1p-21f);
     }
     if (!live) return;                                 // no barrier of all threads below
     uint8_t* dst = a.codes + blk * P * a.hd;
-    float sc = kv8_scale(__uint_as_float(most));
     if (b.lo > 0) {
         if (was >= sc) {
             sc = was;
@@ -235,39 +271,35 @@ __device__ __forceinline__ void append_kv(const AppendArgs& a, const uint2* turn
             }
         }
     }
-    const float inv = kv8_inverse(sc);
-    unsigned near = 0;                                 // pairs with a value that fp32 does not decide
-    static_assert(NV * VN / 2 <= 32, "a bit for every pair");
+    const float inv = kv8_inverse(sc), off = OFF * inv;
+    unsigned near = 0;                                 // pairs with a value whose code fp32 does not decide
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int row = row0 + i * rows;
         if (row >= b.hi) continue;
-        uint32_t w[VN / 4];
+        uint32_t w[VN / 2];
 #pragma unroll
-        for (int k = 0; k < VN; ++k) f[i][k] *= inv;
-#pragma unroll
-        for (int k = 0; k < VN / 4; ++k)
-            w[k] = kv8_code2(f[i][4 * k], f[i][4 * k + 1]) | (kv8_code2(f[i][4 * k + 2], f[i][4 * k + 3]) << 16);
-        if (kv == 0) {                                 // a code has three bits behind the first: where the rest is near a half
-            unsigned off = ~0u;
-#pragma unroll
-            for (int k = 0; k < VN; ++k) off = min(off, (__float_as_uint(f[i][k]) - (0x80000u - NEAR)) & 0xfffffu);
-            if (off <= 2 * NEAR) {
-#pragma unroll
-                for (int k = 0; k < VN; ++k)
-                    if (((__float_as_uint(f[i][k]) - (0x80000u - NEAR)) & 0xfffffu) <= 2 * NEAR) near |= 1u << (i * (VN / 2) + k / 2);
+        for (int k = 0; k < VN / 2; ++k) {
+            const float x = f[i][2 * k], y = f[i][2 * k + 1];
+            if (KV == 0) {
+                const float by = special ? 0.f : fmaf(fabsf(x), off, fabsf(y) * off);      // (one of the two may be NaN there; |x| + |y| may pass fp32)
+                w[k] = kv8_code2(fmaf(x, inv, -by), fmaf(y, inv, -by));
+                // (the sign of a 0 does not count: 0 turned may be -0; other codes of opposite signs are farther apart than twice `by`, at most 6e-4)
+                if ((w[k] ^ kv8_code2(fmaf(x, inv, by), fmaf(y, inv, by))) & 0x7f7fu) near |= 1u << (i * (VN / 2) + k);
+            } else {
+                w[k] = kv8_code2(x * inv, y * inv);
             }
         }
         uint8_t* d = dst + row * a.hd + e;
-        if (VN == 8) *reinterpret_cast<uint2*>(d) = make_uint2(w[0], w[VN / 4 - 1]);
-        else *reinterpret_cast<uint32_t*>(d) = w[0];
+        if constexpr (VN == 8) *reinterpret_cast<uint2*>(d) = make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
+        else *reinterpret_cast<uint32_t*>(d) = w[0] | w[1] << 16;
     }
 #pragma unroll 1
     for (unsigned left = special ? 0u : near; left; left &= left - 1) {
-        const int at = __ffs(left) - 1, row = row0 + at / (VN / 2) * rows, d = e + at % (VN / 2) * 2, from = b.src_row + row - b.lo;
-        *reinterpret_cast<uint16_t*>(dst + row * a.hd + d) =
-            (uint16_t)exact_codes((const T*)a.src[0] + (int64_t)head * a.hd + d + (int64_t)from * a.kv_stride, turns[d / 2],
-                                  a.positions ? a.positions[from] : b.place + row - b.lo, inv);
+        const int at = __ffs(left) - 1;
+        const double2 y = exact_at(at);
+        *reinterpret_cast<uint16_t*>(dst + (row0 + at / (VN / 2) * rows) * a.hd + e + at % (VN / 2) * 2) =
+            (uint16_t)kv8_code2(to_odd(y.x * inv), to_odd(y.y * inv));
     }
     if (b.lo > 0) {                                    // every thread of the group has read the old scale
         if (tpb > 32) asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(tpb) : "memory");
@@ -314,8 +346,9 @@ template <typename T> __device__ __forceinline__ void append_q(const AppendArgs&
     }
 }
 
+// (four CTAs of 256 threads to an SM: 64 registers: 8192 rows 44.3 us a call with three)
 template <typename T, int NV>
-__global__ void __launch_bounds__(MOST) kv8_append_kernel(const __grid_constant__ AppendArgs a, const __grid_constant__ Turns turns) {
+__global__ void __launch_bounds__(MOST, NV <= 4 ? 2 : 1) kv8_append_kernel(const __grid_constant__ AppendArgs a, const __grid_constant__ Turns turns) {
     __shared__ uint2 turn_of[64];                      // (a thread's own from the parameters would be one word at a time)
     grid_dep_launch();
     if (threadIdx.x < a.hd / 2) turn_of[threadIdx.x] = turns.of[threadIdx.x];
@@ -323,7 +356,8 @@ __global__ void __launch_bounds__(MOST) kv8_append_kernel(const __grid_constant_
     kv8_check_offsets(a.q, a.r);
     __syncthreads();
     const int cta = blockIdx.x;
-    if (cta < 2 * a.kv_ctas) append_kv<T, NV>(a, turn_of, cta >= a.kv_ctas, cta >= a.kv_ctas ? cta - a.kv_ctas : cta);
+    if (cta < a.kv_ctas) append_kv<T, NV, 0>(a, turn_of, cta);
+    else if (cta < 2 * a.kv_ctas) append_kv<T, NV, 1>(a, turn_of, cta - a.kv_ctas);
     else append_q<T>(a, turn_of, cta - 2 * a.kv_ctas);
 }
 
