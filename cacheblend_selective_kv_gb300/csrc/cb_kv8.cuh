@@ -180,7 +180,7 @@ struct Kv8Attn {
 cudaError_t launch_kv8_attention(const Kv8& c, const Kv8Seqs& q, const Kv8Rows& r, const Kv8Attn& a, int layer,
                                  cudaStream_t s);
 
-size_t kv8_part_floats(int num_sms);
+size_t kv8_part_floats(int num_sms, bool shared);
 size_t kv8_rows_part_floats(int num_sms);
 // many query rows per sequence (kv8_attn_rows.cu); attn_args: the AttnArgs of launch_kv8_attention, mode: what it computes
 cudaError_t launch_kv8_rows(const Kv8& c, const void* attn_args, int mode, cudaStream_t s);
@@ -196,7 +196,7 @@ cudaError_t launch_kv8_shared(const Kv8& c, const Kv8Prefix& pre, const Kv8Seqs&
 cudaError_t launch_kv8_few_prefix(const Kv8& c, void* attn_args, cudaStream_t s);
 cudaError_t launch_kv8_few_own(const Kv8& c, const void* attn_args, cudaStream_t s);
 cudaError_t launch_kv8_few_joint(const Kv8& c, const void* attn_args, cudaStream_t s);
-int kv8_most_ctas(int num_sms);
+int kv8_most_ctas(int num_sms, bool shared);
 bool kv8_make_map(const Kv8& c, void* out);
 
 struct Kv8Evict {

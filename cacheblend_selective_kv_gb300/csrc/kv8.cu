@@ -139,6 +139,9 @@ cb_status check_io(const cb_kv8& c, const void* k, const void* v, int64_t layer_
     return CB_OK;
 }
 
+// cells that a query row of attention over a shared prefix needs
+int64_t shared_row(const cb_kv8_config& c) { return (int64_t)c.n_heads * (2 * c.head_dim + 6); }
+
 // query and output rows of an attention call
 cb_status check_q(const cb_kv8& c, const void* q, int64_t q_stride, int32_t n_q, float scale, const void* out, int64_t out_stride,
                   const char* who) {
@@ -205,10 +208,11 @@ cb_status cb_kv8_create(const cb_kv8_config* cfg, void* codes, float* scales, cb
         delete h;
         return fail(CB_ERR_CUDA, "cb_kv8_create: no CUDA device");
     }
-    // one allocation: status, opened, voided, arrival counts (zero between calls), pieces, statistics, what is to be joined, scores (arrival
-    // counts and pieces twice, for two launches at a time)
-    const size_t head = 256 + ((size_t)kv8_most_ctas(h->num_sms) * 4 + 255) / 256 * 256;
-    const size_t part = (kv8_part_floats(h->num_sms) * 4 + 255) / 256 * 256;
+    // one allocation: status, opened, voided, arrival counts (zero between calls), pieces, statistics, what is to be joined, scores; arrival
+    // counts and pieces twice, for two launches at a time, where there are cells for a row of attention over a shared prefix
+    const bool shared = c.weight_cells >= shared_row(c);
+    const size_t head = 256 + ((size_t)kv8_most_ctas(h->num_sms, shared) * 4 + 255) / 256 * 256;
+    const size_t part = (kv8_part_floats(h->num_sms, shared) * 4 + 255) / 256 * 256;
     // a row of a call that returns weights takes at least 129 cells
     const size_t stats = c.weight_cells > 0 ? (((size_t)c.weight_cells / 129 + 1) * sizeof(float2) + 255) / 256 * 256 : 0;
     const size_t todo = ((size_t)h->num_sms * 4 * 4 + 255) / 256 * 256;
@@ -394,7 +398,7 @@ cb_status cb_kv8_attention_shared(cb_kv8* c, const cb_kv8_seqs* prefixes, const 
     if (st == CB_OK) st = check_places(*c, n_q, sq, who);
     if (st != CB_OK) return st;
     const bool shared = pre.n > 0 && pre.max_len > 0;
-    const int64_t row = (int64_t)c->cfg.n_heads * (2 * c->cfg.head_dim + 6);
+    const int64_t row = shared_row(c->cfg);
     if (shared && n_q > c->cfg.weight_cells / row)
         return fail(CB_ERR_INVALID_ARG, "%s: %d query rows need %lld cells of scratch, the cache was created with %lld", who, n_q,
                     (long long)(n_q * row), (long long)c->cfg.weight_cells);

@@ -102,7 +102,7 @@ template <int HD, typename T> cudaError_t launch_both(const Kv8& c, const AttnAr
 
 }  // namespace
 
-// scratch: two pieces for every CTA of the largest launch, and of the largest that runs beside another (BESIDE)
+// scratch: two pieces for every CTA of the largest launch, and where calls may share a prefix of the largest that runs beside another (BESIDE)
 template <typename S> constexpr size_t pieces() { return (size_t)S::CTAS * 2 * S::PIECE; }
 static size_t few_part_floats(int num_sms) {
     const size_t sizes[] = {pieces<C4<128>>(), pieces<C4S<128>>(), pieces<C8<128>>(), pieces<C16<128>>(), pieces<C32<128>>(),
@@ -110,9 +110,9 @@ static size_t few_part_floats(int num_sms) {
     return *std::max_element(std::begin(sizes), std::end(sizes)) * num_sms;
 }
 static size_t most_part_floats(int num_sms) { return std::max(few_part_floats(num_sms), kv8_rows_part_floats(num_sms)); }
-size_t kv8_part_floats(int num_sms) { return few_part_floats(num_sms) + most_part_floats(num_sms); }
+size_t kv8_part_floats(int num_sms, bool shared) { return most_part_floats(num_sms) + (shared ? few_part_floats(num_sms) : 0); }
 static int most_ctas(int num_sms) { return 4 * num_sms; }
-int kv8_most_ctas(int num_sms) { return 2 * most_ctas(num_sms); }
+int kv8_most_ctas(int num_sms, bool shared) { return (shared ? 2 : 1) * most_ctas(num_sms); }
 
 bool kv8_make_map(const Kv8& c, void* out) {
     cudaDriverEntryPointQueryResult q;

@@ -68,3 +68,32 @@ def test_batches_of_single_sequences(monkeypatch, cb):
     """Groups of one sequence, a group for every sequence, and sequences of no group at all, by the handle's own choice."""
     for first, n_pre in (([0, 1, 2, 3, 4], 4), ([0, 0, 0, 0, 0], 4), ([4, 4], 1), ([0, 4], 1)):
         result(monkeypatch, cb, None, ([130 + 7 * g for g in range(n_pre)], [20, 1, 0, 128], first, [1, 1, 1, 1], dict(H=2, G=2, hd=64, P=16)), check=True)
+
+
+def test_scratch_without_shared_calls(monkeypatch, cb):
+    """A cache without cells for a row of attention over a shared prefix holds no pieces for a second launch, and refuses such a call."""
+    def size(cells):
+        codes, scales = torch.zeros((1, 2, 4, 8, 16, 128), dtype=torch.uint8, device="cuda"), torch.zeros((1, 2, 4, 8), device="cuda")
+        torch.cuda.synchronize()
+        before = torch.cuda.mem_get_info()[0]
+        caches = [cb.KV8Cache(codes, scales, n_heads=32, dtype="bf16", weight_cells=cells) for _ in range(8)]
+        used = before - torch.cuda.mem_get_info()[0]
+        for c in caches:
+            c.close()
+        return used / 8
+    row = cb.KV8Cache.shared_cells(1, 32, 128)
+    none, shared = size(0), size(row)
+    assert shared - none >= 4 << 20
+    assert size(row - 1) - none < 2 << 20
+    table, lens, q = torch.zeros((1, 2), dtype=torch.int32, device="cuda"), torch.ones(1, dtype=torch.int32, device="cuda"), torch.zeros((1, 32, 128), device="cuda").bfloat16()
+    for cells in (0, row - 1, row):
+        codes, scales = torch.zeros((1, 2, 4, 8, 16, 128), dtype=torch.uint8, device="cuda"), torch.zeros((1, 2, 4, 8), device="cuda")
+        c = cb.KV8Cache(codes, scales, n_heads=32, dtype="bf16", weight_cells=cells)
+        if cells < row:
+            with pytest.raises(cb.CacheBlendError, match="cells"):
+                c.attention_shared(table, lens, table + 1, lens, q)
+        else:
+            assert not c.attention_shared(table, lens, table + 1, lens, q).any()
+        torch.cuda.synchronize()
+        assert c.status() == 0
+        c.close()
