@@ -990,14 +990,14 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const SampleArgs a) 
             low = row.see(low);
             m = 0.f;
         }
-        const float t = 1.44269502f / T1;              // log2(e) = 1.44269502 + 1.92596299e-8
-        w.t = 256.f * t;
-        w.rest = 256.f * ((fmaf(-t, T1, 1.44269502f) + 1.92596299e-8f) / T1);
+        // log2(e) = 1.44269502 + 1.92596299e-8 (times 256 before it is divided: at the highest temperatures 1 / T1 is below the normal numbers)
+        w.t = 256.f * 1.44269502f / T1;
+        w.rest = (fmaf(-w.t, T1, 256.f * 1.44269502f) + 256.f * 1.92596299e-8f) / T1;
         w.power = s.power;
         w.lowest = -INFINITY;
         const int top8 = (w.bits(m) - MAGIC_BITS) >> 8;
         w.base = 18 + top8 + (MAGIC_BITS >> 8);
-        w.lowest = fmaxf((top8 - 44.5f) / t, -3.402823466e38f);
+        w.lowest = fmaxf((top8 - 44.5f) * 256.f / w.t, -3.402823466e38f);
     }
     Cut cut{-INFINITY, -0x7fffffff - 1};               // (-inf, where there is no token among others, is not kept)
     int phase = 0;

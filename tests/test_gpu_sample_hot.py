@@ -1,0 +1,37 @@
+"""GPU tests of cb_sample where numbers near the end of fp32 meet in it: the highest temperatures and logits of their size.  The
+tolerances are those of tests/test_gpu_sample.py.  At temperatures above 2^120 the remainder of 256 log2(e) / T is below the normal numbers
+and off by up to 2^-150, which 2^128 makes 2^-22 in 256ths: 2^-30.5 of a weight, inside the 2^-29 of a probability and the 2^-30 of
+a border that are allowed there."""
+import numpy as np
+import pytest
+
+from test_gpu_sample import check
+
+pytestmark = pytest.mark.gpu
+torch = pytest.importorskip("torch")
+
+
+@pytest.fixture(scope="module")
+def cb():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import __graft_entry__
+    __graft_entry__.build()
+    import cacheblend_selective_kv_gb300 as cbm
+    return cbm
+
+
+@pytest.mark.parametrize("v", [700, 40000])
+def test_highest_temperatures(cb, v):
+    n = 24
+    rng = np.random.default_rng(v)
+    t = np.concatenate([rng.uniform(1.2e38, 3.4e38, n - 8), [1e34, 1e35, 1e36, 1e37, 2e37, 5e37, 8e37, 1e38]]).astype(np.float32)
+    x = rng.uniform(-3.3e38, 3.3e38, (n, v)).astype(np.float32)
+    x[n - 8:] = np.clip(rng.normal(size=(8, v)) * t[n - 8:, None], -3.4e38, 3.4e38)
+    x = torch.from_numpy(x).cuda()
+    u = rng.random(n)
+    check(cb, x, u, t=t)
+    check(cb, x, u, t=t, p=rng.uniform(0.05, 0.95, n))
+    check(cb, x, u, t=t, k=np.full(n, 300), m=np.full(n, 0.2))
+    check(cb, x, u, t=t, k=np.full(n, 20), p=np.full(n, 0.7))
+    check(cb, -x.abs(), u, t=t, m=np.full(n, 0.3))
