@@ -1062,7 +1062,8 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const SampleArgs a) 
 
     // sums of what is kept, per warp; the warp's part in which they pass u of their sum; the token in it
     const float from = fmaxf(cut.x, from_min);         // nothing below is kept
-    const bool all = from == -INFINITY && w.lowest > -3.4e38f;             // (then -inf has no weight by itself)
+    // (then -inf has no weight by itself; the value below which min-p keeps nothing may have passed fp32)
+    const bool all = from == -INFINITY && w.lowest > -3.4e38f && !(min_p > 0.f);
     const auto kept = [&](const float* x, int place, unsigned long long* y) {  // false: none of the warp's
         if (!all && !any_from(x, from)) return false;
 #pragma unroll

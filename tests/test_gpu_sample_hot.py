@@ -35,3 +35,15 @@ def test_highest_temperatures(cb, v):
     check(cb, x, u, t=t, k=np.full(n, 300), m=np.full(n, 0.2))
     check(cb, x, u, t=t, k=np.full(n, 20), p=np.full(n, 0.7))
     check(cb, -x.abs(), u, t=t, m=np.full(n, 0.3))
+
+
+def test_min_p_whose_value_passes_fp32(cb):
+    """The logit below which min-p keeps nothing lies beyond the lowest fp32 number when it is counted from 0, and still cuts: of tokens with
+    2^-38 of the largest weight, min-p 2^-31 keeps none, and the last uniform number below 1 takes the only one that is left."""
+    v, t, top = 128256, 1.6e37, 3.3e38
+    low = top + t * np.log(2.0 ** -38)
+    x = torch.full((4, v), low, device="cuda")
+    x[:2, 0], x[2:, v - 1] = top, top
+    u, m = np.array([1 - 2.0 ** -24, 0.0, 1 - 2.0 ** -24, 0.0]), np.array([2.0 ** -31, 2.0 ** -31, 2.0 ** -31, 2.0 ** -40])
+    tokens, probs = check(cb, x, u, t=np.full(4, t), m=m, compared=0.75)       # (the last row's border is nearer than float64 sums tell)
+    assert tokens.tolist() == [0, 0, v - 1, 0] and (probs[:3] == 1.0).all()
