@@ -257,9 +257,9 @@ template <typename T> struct Row {
     // or the part's candidates in the tokens' order, when they have been listed: places are those of the list
     const float* values;
     const unsigned short* places;        // from the part's first place on
-    // Rows whose values stand for others.  Infinities share all the weight: they become 0, all others -inf.  At low temperatures
-    // values are taken less the largest (what has weight lies so near to it that the difference is exact), and at the very
-    // lowest times 2^32, so that 1 / T stays within fp32.
+    // Rows whose values stand for others.  Infinities share all the weight: they become 0, all others -inf.  Where the largest is thousands
+    // of temperatures from 0, values are taken less the largest (what has weight lies so near to it that the difference is exact), and at
+    // the very lowest temperatures times 2^32, so that 1 / T stays within fp32.
     bool special, infinite;
     float less, times;
     __device__ __forceinline__ float see(float v) const {
@@ -977,18 +977,19 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const SampleArgs a) 
     Weigh w;
     {
         float T1 = fminf(temperature, 3.4e38f);
+        const bool far = !(fabsf(m) * (1.442695f / T1) < 8192.f);
         if (m == INFINITY) {
             row.special = row.infinite = true;
             m = low = 0.f;
             bound = 0;
-        } else if (!(fabsf(m) * (1.442695f / T1) < 8192.f) || T1 < 0x1p-100f) {
+        } else if (far || T1 < 0x1p-100f) {
             row.special = true;
-            row.less = m;
+            row.less = far ? m : 0.f;                  // (nearer to 0 the difference would be rounded)
             row.times = T1 < 0x1p-100f ? 0x1p32f : 1.f;
             T1 *= row.times;
             own = row.see(own);
             low = row.see(low);
-            m = 0.f;
+            m = row.see(m);
         }
         // log2(e) = 1.44269502 + 1.92596299e-8 (times 256 before it is divided: at the highest temperatures 1 / T1 is below the normal numbers)
         w.t = 256.f * 1.44269502f / T1;

@@ -47,3 +47,23 @@ def test_min_p_whose_value_passes_fp32(cb):
     u, m = np.array([1 - 2.0 ** -24, 0.0, 1 - 2.0 ** -24, 0.0]), np.array([2.0 ** -31, 2.0 ** -31, 2.0 ** -31, 2.0 ** -40])
     tokens, probs = check(cb, x, u, t=np.full(4, t), m=m, compared=0.75)       # (the last row's border is nearer than float64 sums tell)
     assert tokens.tolist() == [0, 0, v - 1, 0] and (probs[:3] == 1.0).all()
+
+
+@pytest.mark.parametrize("v", [600, 30000])
+def test_lowest_temperatures(cb, v):
+    """Temperatures down to the smallest that is not greedy, with logits of their size, below the normal numbers among them, and with logits
+    thousands of temperatures away from 0 or below anything that 2^32 leaves within fp32."""
+    n = 24
+    rng = np.random.default_rng(v)
+    t = np.concatenate([10.0 ** rng.uniform(-37.9, -30, n - 2), [1.1754944e-38, 7.8e-31]]).astype(np.float32)
+    x = (rng.normal(size=(n, v)) * 3 * t[:, None]).astype(np.float32)
+    x[3:6] += np.float32(20000) * t[3:6, None]
+    x[6:9, ::3] = -3e38
+    x[9] -= np.float32(5000) * t[9]
+    u = rng.random(n)
+    x = torch.from_numpy(x).cuda()
+    check(cb, x, u, t=t)
+    check(cb, x, u, t=t, p=rng.uniform(0.05, 0.95, n))
+    check(cb, x, u, t=t, k=np.full(n, 300), m=np.full(n, 0.2))
+    check(cb, x, u, t=t, k=np.full(n, 20), p=np.full(n, 0.7))
+    check(cb, x, u, t=t, k=np.full(n, v - 1), p=np.full(n, 0.99), m=np.full(n, 1e-4))
