@@ -6,8 +6,8 @@
 //
 // The result is a whole number, so sums have to be where the exact ones are: at a vocabulary of 128K a border that is off by
 // 2^-24 of the sum would pick a neighbour in one row of a hundred.  Weights are therefore 64-bit integers, in units of
-// 2^-44 to 2^-45 of the largest, and their sums are exact and independent of the order of adding.  A weight is good to about
-// 2^-32 of itself: x / T as a sum of two fp32 numbers, its integer part in 256ths by rounding, 2^(j / 256) from a table of
+// 2^-44 to 2^-45 of the largest, and their sums are exact and independent of the order of adding.  A weight is good to
+// 2^-31 of itself: x / T as a sum of two fp32 numbers, its integer part in 256ths by rounding, 2^(j / 256) from a table of
 // 32-bit integers, and 2^r - 1 for the rest (|r| <= 2^-9) by three terms of the series, all in fp32 and one wide integer product.
 // A weight below 2^-45 of the largest is 0.
 //

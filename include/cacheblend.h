@@ -562,11 +562,12 @@ cb_status cb_select_hkvd(const float* dev, int32_t n, int32_t k, int32_t* out_ro
  *                top_k <= 0 or >= vocab, top_p >= 1 or NaN, min_p <= 0 or NaN; min_p above 1 counts as 1.  A temperature that is
  *                NaN or below the smallest normal number (0 among them) takes the most likely token, the lowest of equal ones.
  *   uniform      device float32 [n_rows] in [0, 1); below, or NaN: as 0; from 1 on: the last kept token
+ *                whose weight is not 0
  *   out_tokens   device int32 [n_rows]; -1 where no logit is above -infinity
  *   out_probs    device float32 [n_rows] or NULL: the token's weight over the sum of the kept ones (0 where there is no token)
- * A NaN counts as -infinity; infinities, where there are any, share all the weight.  Weights are held to about 2^-32 of
- * themselves, in integers of at least 2^-45 of the largest (below which they count as 0), and summed exactly, so that the token
- * is the formula's but for borders nearer than that; no sum depends on an order.
+ * A NaN counts as -infinity; infinities, where there are any, share all the weight.  Weights are held to 2^-31 of themselves
+ * (2^-30 at temperatures above 2^120), in integers of at least 2^-45 of the largest (below which they count as 0), and summed
+ * exactly, so that the token is the formula's but for borders nearer than that; no sum depends on an order.
  * vocab at most CB_SAMPLE_MAX_VOCAB (else CB_ERR_UNSUPPORTED), n_rows at most 2^24.  Async on `stream`, on the current device;
  * no allocation; concurrent calls are independent. */
 #define CB_SAMPLE_MAX_VOCAB 393216
