@@ -10,7 +10,7 @@
 // moved codes at e4m3's borders.)
 //
 // Codes and scales are those of exact rotation.  Over all 2^32 phases the vector (cosine, sine) is off by at most 1.266e-7, to which the
-// cut to 32 bits adds 1.5e-9 and the farthest positions 0.7e-9; product and sum round by 2^-24 of the pair's length each.  A turned value is
+// cut to 32 bits adds 1.5e-9 and the farthest positions 0.7e-9; the product and the sum are rounded by 2^-24 of the pair's length each.  A turned value is
 // then off by less than 2.5e-7 of that length, and the length is at most the sum of the pair's two magnitudes.  Where the values less and
 // plus that much do not have the same code (a pair of about 10 000), or the scales of maxima less and plus it differ, the pairs in question
 // are turned again in 64 bits.  Left out are blocks with NaN, infinities or numbers from 248 * 2^120 on, and with none above 2^-100, whose

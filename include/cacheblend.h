@@ -366,7 +366,7 @@ cb_status cb_kv8_read(cb_kv8* cache, const cb_kv8_seqs* seqs, int32_t layer, int
  *   row_start, n_rows: as for cb_kv8_write.  Rows that belong to no sequence, or to one whose length is out of range or below
  *                 its number of rows, are neither stored nor rotated; a bad page id skips its rows of k and v only.
  * Angles are those of float64 frequencies for every int32 position.  Rotated values are fp32 with errors below 2.5e-7 of their
- * pair's length, rounded once to out_q's type; k's codes and scales are those of exact rotation (of the fp32 values in blocks with
+ * pair's length (and the roundings of numbers below 2^-126), rounded once to out_q's type; k's codes and scales are those of exact rotation (of the fp32 values in blocks with
  * NaN, infinities or numbers from 248 * 2^120 on, or with none above 2^-100).  A rotated value that passes fp32 is kept as an
  * infinity in out_q, as NaN in the cache.
  * Async on `stream`; no allocation. */
